@@ -7,11 +7,13 @@ binding is imported lazily so that the seeded input generators in
 point without a built library raises immediately (there is no CPU fallback).
 """
 
-__all__ = ["sgemm", "sgemm_host", "sgemm_into", "library_path", "workloads"]
+_LAYERS = ("lora_into", "lora_backward_into", "act8_empty", "act8_store_into", "act8_load_into",
+           "act8_grad_into", "act8_weight_grad_into")
+__all__ = ["sgemm", "sgemm_host", "sgemm_into", *_LAYERS, "library_path", "workloads"]
 
 
 def __getattr__(name):
-    if name in ("sgemm", "sgemm_host", "sgemm_into", "library_path", "lib"):
+    if name in ("sgemm", "sgemm_host", "sgemm_into", "library_path", "lib", *_LAYERS):
         from . import binding
         return getattr(binding, name)
     raise AttributeError(name)

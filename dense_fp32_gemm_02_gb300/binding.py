@@ -41,6 +41,21 @@ lib.sgemm_3xtf32.argtypes = [_i, _i, _i, _f, _p, _i, _p, _i, _f, _p, _i, _p]
 lib.sgemm_3xtf32.restype = _i
 lib.sgemm_host_3xtf32.argtypes = [_i, _i, _i, _f, _p, _i, _p, _i, _f, _p, _i, _p]
 lib.sgemm_host_3xtf32.restype = _i
+lib.sgemm_lora.argtypes = [_i] * 6 + [_p, _i, _p, _i, _p, _i, _ll, _p, _i, _ll, _p, _p, _p, _p,
+                                      _p, _i, _p, _i, _p]
+lib.sgemm_lora.restype = _i
+lib.sgemm_lora_backward.argtypes = [_i] * 6 + [_p, _i, _p, _i, _p, _i, _p, _i, _p, _i, _p, _i, _ll,
+                                               _p, _i, _ll, _p, _p, _p, _p, _i, _p, _i, _p, _i,
+                                               _ll, _p, _i, _ll, _p]
+lib.sgemm_lora_backward.restype = _i
+lib.sgemm_act8_store.argtypes = [_i, _i, _i, _p, _i, _i, _p, _i, _p, _i, _p, _i, _p]
+lib.sgemm_act8_store.restype = _i
+lib.sgemm_act8_load.argtypes = [_i, _i, _i, _p, _i, _p, _i, _p, _i, _p]
+lib.sgemm_act8_load.restype = _i
+lib.sgemm_act8_grad.argtypes = [_i, _i, _i, _p, _i, _p, _i, _i, _p, _i, _p, _i, _p]
+lib.sgemm_act8_grad.restype = _i
+lib.sgemm_act8_weight_grad.argtypes = [_i, _i, _i, _i, _p, _i, _p, _i, _p, _i, _f, _p, _i, _p]
+lib.sgemm_act8_weight_grad.restype = _i
 lib.sgemm_status_string.argtypes = [_i]
 lib.sgemm_status_string.restype = ctypes.c_char_p
 lib.sgemm_version.argtypes = []
@@ -273,6 +288,244 @@ def sgemm_host(A, B, C, alpha: float = 1.0, beta: float = 0.0, stream=None, devi
                 float(beta), C.data_ptr(), _ld(C, N), _stream_handle(stream, device))
     check(st)
     return C
+
+
+# ------------------------------------------------------------------ linear layers
+# (include/sgemm_layers.h: float32 or bfloat16 tensors, all of one type)
+ACT8_BLOCK = 32   # columns of a row that share an exponent of an 8-bit checkpoint
+
+
+def _layer_type(first, *named):
+    """The sgemm_type of the (name, tensor) pairs, None tensors left out: CUDA
+    tensors of one type, float32 or bfloat16, on one device."""
+    import torch
+    named = [(n, t) for n, t in (first, *named) if t is not None]
+    for name, t in named:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or \
+                t.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"{name} must be a CUDA float32 or bfloat16 tensor")
+        if t.dtype != named[0][1].dtype:
+            raise TypeError(f"{name} must have the type of {named[0][0]}, {named[0][1].dtype}")
+    _on_device(named[0][1].device, *named)
+    return 1 if named[0][1].dtype == torch.bfloat16 else 0
+
+
+def _on_device(device, *named):
+    for name, t in named:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}")
+
+
+def _typed(name, t, dtype, shape, device):
+    """TypeError / ValueError unless t is a CUDA tensor of this type, shape and device."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA {str(dtype).replace('torch.', '')} tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    _on_device(device, (name, t))
+
+
+def _vector(name, t, dtype, n, device):
+    """Address of a contiguous vector of n elements, or None."""
+    if t is None:
+        return None
+    _typed(name, t, dtype, (n,), device)
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _matrix(name, t, rows, cols):
+    """(address, row pitch) of a rows x cols row-major view; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} must be {(rows, cols)}, got {tuple(t.shape)}")
+    return t.data_ptr(), _ld(t, cols)
+
+
+def _stack(name, t, count, rows, cols):
+    """(address, row pitch, matrix stride) of count x rows x cols; (None, 0, 0) for None."""
+    if t is None:
+        return None, 0, 0
+    if t.dim() != 3 or tuple(t.shape) != (count, rows, cols):
+        raise ValueError(f"{name} must be {(count, rows, cols)}, got {tuple(t.shape)}")
+    if count == 0:
+        return None, max(cols, 1), 0
+    return t.data_ptr(), _ld(t[0], cols), (t.stride(0) if count > 1 else 0)
+
+
+def _checkpoint(q, e, rows, cols, device):
+    """(address, pitch, address, pitch) of an 8-bit checkpoint of a rows x cols matrix."""
+    import torch
+    blocks = -(-cols // ACT8_BLOCK)
+    _typed("q", q, torch.int8, (rows, cols), device)
+    _typed("e", e, torch.int8, (rows, blocks), device)
+    return (*_matrix("q", q, rows, cols), *_matrix("e", e, rows, blocks))
+
+
+def _adapters(A, B, ids, M, scale, ranks, device):
+    """(L, R, ids, ranks, scale) of a stack A (L, K, R), B (L, R, N): sizes and addresses."""
+    import torch
+    if A.dim() != 3:
+        raise ValueError("A must be 3-D (adapters, K, R)")
+    L, _, R = A.shape
+    if L > 0 and not 1 <= R <= 128:
+        raise ValueError(f"the adapters' rank must be 1 to 128, got {R}")
+    if L > 1024:
+        raise ValueError(f"at most 1024 adapters, got {L}")
+    return (L, R, _vector("ids", ids, torch.int32, M, device),
+            _vector("ranks", ranks, torch.int32, L, device),
+            _vector("scale", scale, torch.float32, L, device))
+
+
+def lora_into(X, W, A, B, ids, Y, scale=None, ranks=None, bias=None, H=None, stream=None):
+    """Y[i] <- X[i]@W + bias + scale[a]*(X[i]@A[a])@B[a] with a = ids[i]: the adapters
+    of many requests beside one projection, for one token up to a long prefill.
+
+    X (M, K), W (K, N), A (L, K, R), B (L, R, N), Y (M, N) and bias (N,) or None: CUDA
+    float32 or bfloat16, one type.  ids (M,) int32; a row whose id is not in [0, L)
+    uses no adapter.  scale (L,) float32 or None (1).  ranks (L,) int32 or None: only
+    the first ranks[a] columns of A[a] and rows of B[a] are used.  H (M, R) float32,
+    where given, receives X[i]@A[a] for lora_backward_into().  Asynchronous on `stream`
+    (default: torch's current stream)."""
+    import torch
+    kind = _layer_type(("X", X), ("W", W), ("A", A), ("B", B), ("Y", Y), ("bias", bias))
+    M, N, K = _shapes(X, W, Y)
+    L, R, ids_p, ranks_p, scale_p = _adapters(A, B, ids, M, scale, ranks, Y.device)
+    a = _stack("A", A, L, K, R)
+    b = _stack("B", B, L, R, N)
+    h = (None, 0)
+    if H is not None:
+        _typed("H", H, torch.float32, (M, R), Y.device)
+        h = _matrix("H", H, M, R)
+    bias_p = _vector("bias", bias, Y.dtype, N, Y.device)
+    with torch.cuda.device(Y.device):
+        st = lib.sgemm_lora(kind, M, N, K, L, R, X.data_ptr(), _ld(X, K), W.data_ptr(), _ld(W, N),
+                            *a, *b, ids_p, ranks_p, scale_p, bias_p, *h, Y.data_ptr(), _ld(Y, N),
+                            _stream_handle(stream, Y.device))
+    check(st)
+    return Y
+
+
+def lora_backward_into(dY, X, W, A, B, ids, H, dX=None, dA=None, dB=None, scale=None, ranks=None,
+                       stream=None):
+    """Gradients of lora_into() for dY (M, N), W being frozen: with
+    G[i] = scale[a]*dY[i]@B[a].T, dX <- dY@W.T + G[i]@A[a].T, dA[a] <- sum_i X[i].T@G[i]
+    and dB[a] <- sum_i scale[a]*H[i].T@dY[i] (zero for adapters without rows).
+
+    X is the forward call's input or the pair (q, e) that act8_store_into() kept of it;
+    H what the forward call wrote.  dX (M, K) may be None, and dA (L, K, R) and
+    dB (L, R, N) may be None together.  Returns (dX, dA, dB)."""
+    import torch
+    kept = isinstance(X, tuple)
+    kind = _layer_type(("dY", dY), ("X", None if kept else X), ("W", W), ("A", A), ("B", B),
+                       ("dX", dX), ("dA", dA), ("dB", dB))
+    if (dA is None) != (dB is None):
+        raise ValueError("dA and dB must be given together")
+    if W.dim() != 2:
+        raise ValueError("W must be 2-D")
+    K, N = W.shape
+    M = dY.shape[0]
+    device = dY.device
+    L, R, ids_p, ranks_p, scale_p = _adapters(A, B, ids, M, scale, ranks, device)
+    dy, w = _matrix("dY", dY, M, N), _matrix("W", W, K, N)
+    if kept:
+        x, c = (None, 0), _checkpoint(*X, M, K, device)
+    else:
+        x, c = _matrix("X", X, M, K), (None, 0, None, 0)
+    a, b = _stack("A", A, L, K, R), _stack("B", B, L, R, N)
+    _typed("H", H, torch.float32, (M, R), device)
+    h = _matrix("H", H, M, R)
+    dx = _matrix("dX", dX, M, K)
+    da, db = _stack("dA", dA, L, K, R), _stack("dB", dB, L, R, N)
+    with torch.cuda.device(device):
+        st = lib.sgemm_lora_backward(kind, M, N, K, L, R, *dy, *x, *c, *w, *a, *b, ids_p, ranks_p,
+                                     scale_p, *h, *dx, *da, *db, _stream_handle(stream, device))
+    check(st)
+    return dX, dA, dB
+
+
+def act8_empty(M: int, K: int, device=None):
+    """A checkpoint's two tensors for an M x K matrix: q (M, K) and e (M, ceil(K/32)), int8."""
+    import torch
+    device = device or torch.device("cuda", torch.cuda.current_device())
+    return (torch.empty((M, K), dtype=torch.int8, device=device),
+            torch.empty((M, -(-K // ACT8_BLOCK)), dtype=torch.int8, device=device))
+
+
+def act8_store_into(Z, q, e, act: str = "none", Y=None, stream=None):
+    """(q, e) <- the 8-bit checkpoint of Z (M, K): for each block of 32 columns of a row
+    an exponent e and q = rint(z / 2^e) in int8.  With Y, also Y <- act(Z) in the same
+    pass (Y may be Z).  Returns (q, e)."""
+    import torch
+    kind = _layer_type(("Z", Z), ("Y", Y))
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    if act != "none" and Y is None:
+        raise ValueError("an activation needs an output Y")
+    if Z.dim() != 2:
+        raise ValueError("Z must be 2-D")
+    M, K = Z.shape
+    c = _checkpoint(q, e, M, K, Z.device)
+    z, y = _matrix("Z", Z, M, K), _matrix("Y", Y, M, K)
+    with torch.cuda.device(Z.device):
+        st = lib.sgemm_act8_store(kind, M, K, *z, ACTIVATIONS[act], *c, *y,
+                                  _stream_handle(stream, Z.device))
+    check(st)
+    return q, e
+
+
+def act8_load_into(q, e, X, stream=None):
+    """X <- the values q * 2^e that a checkpoint stands for."""
+    import torch
+    kind = _layer_type(("X", X))
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D")
+    M, K = X.shape
+    c = _checkpoint(q, e, M, K, X.device)
+    with torch.cuda.device(X.device):
+        st = lib.sgemm_act8_load(kind, M, K, *c, *_matrix("X", X, M, K),
+                                 _stream_handle(stream, X.device))
+    check(st)
+    return X
+
+
+def act8_grad_into(q, e, dY, dZ, act: str = "none", stream=None):
+    """dZ <- dY * act'(z), z the values of the checkpoint (q, e) of the activation's
+    input (dZ may be dY)."""
+    import torch
+    kind = _layer_type(("dY", dY), ("dZ", dZ))
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    if dY.dim() != 2:
+        raise ValueError("dY must be 2-D")
+    M, K = dY.shape
+    c = _checkpoint(q, e, M, K, dY.device)
+    dy, dz = _matrix("dY", dY, M, K), _matrix("dZ", dZ, M, K)
+    with torch.cuda.device(dY.device):
+        st = lib.sgemm_act8_grad(kind, M, K, *c, ACTIVATIONS[act], *dy, *dz,
+                                 _stream_handle(stream, dY.device))
+    check(st)
+    return dZ
+
+
+def act8_weight_grad_into(q, e, dY, dW, beta: float = 0.0, stream=None):
+    """dW <- x.T@dY + beta*dW, x (M, K) the values of the checkpoint (q, e) of a layer's
+    input, dY (M, N), dW (K, N)."""
+    import torch
+    kind = _layer_type(("dY", dY), ("dW", dW))
+    if dY.dim() != 2 or dW.dim() != 2:
+        raise ValueError("dY and dW must be 2-D")
+    (M, N), K = dY.shape, dW.shape[0]
+    c = _checkpoint(q, e, M, K, dY.device)
+    dy, dw = _matrix("dY", dY, M, N), _matrix("dW", dW, K, N)
+    with torch.cuda.device(dY.device):
+        st = lib.sgemm_act8_weight_grad(kind, M, N, K, *c, *dy, float(beta), *dw,
+                                        _stream_handle(stream, dY.device))
+    check(st)
+    return dW
 
 
 # ------------------------------------------------------------------ control

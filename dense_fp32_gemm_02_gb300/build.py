@@ -21,7 +21,7 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libsgemm.so")
 # the range-checked build (-DSGEMM_DEBUG_BOUNDS): a test library, never the default
 LIB_DEBUG_BOUNDS_PATH = os.path.join(BUILD_DIR, "libsgemm_debug_bounds.so")
-HEADER = os.path.join(ROOT, "include", "sgemm.h")
+HEADERS = sorted(glob.glob(os.path.join(ROOT, "include", "*.h")))
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMPILE_FLAGS = [
@@ -46,7 +46,8 @@ def units():
 
 
 def sources():
-    return sorted(units() + glob.glob(os.path.join(CSRC, "*.cuh")) + [HEADER])
+    return sorted(units() + glob.glob(os.path.join(CSRC, "*.cuh"))
+                  + glob.glob(os.path.join(CSRC, "*.h")) + HEADERS)
 
 
 def is_stale(path: str = LIB_PATH) -> bool:

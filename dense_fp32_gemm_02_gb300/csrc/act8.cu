@@ -1,0 +1,379 @@
+// act8.cu -- checkpoints of activations in 8 bits: the entry points that store
+// them, read them back and take an activation's gradient from them.
+//
+// Each kernel makes one pass: every input and output byte moves once, and the
+// arithmetic in between (a maximum over 32 columns, an exact scaling, for GELU
+// one exponential and one reciprocal per element) runs in its shadow.
+#include <algorithm>
+
+#include "../../include/sgemm_layers.h"
+#include "act8.cuh"
+#include "host_state.h"
+
+#define SGEMM_API extern "C" __attribute__((visibility("default")))
+
+namespace {
+
+using namespace sgl;
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------------ activations
+// Phi(z) = (1 + erf(z / sqrt 2)) / 2 and exp(-z^2/2), by formula 7.1.26 of
+// Abramowitz and Stegun, Handbook of Mathematical Functions:
+//   erf x = 1 - (a1 t + ... + a5 t^5) exp(-x^2),  t = 1 / (1 + p x),  x >= 0,
+// whose error is at most 1.5e-7, i.e. that of fp32 itself at this size.  The
+// exponential is the one that the derivative needs anyway, and the negative side
+// comes without cancellation.
+__device__ __forceinline__ void normal_cdf(float z, float &cdf, float &bell) {
+    const float x = fabsf(z) * 0.70710678f;
+    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+    bell = __expf(-x * x);
+    float p = fmaf(t, 1.061405429f, -1.453152027f);
+    p = fmaf(t, p, 1.421413741f);
+    p = fmaf(t, p, -0.284496736f);
+    p = fmaf(t, p, 0.254829592f);
+    const float tail = 0.5f * p * t * bell;
+    cdf = z < 0.0f ? tail : 1.0f - tail;
+}
+
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+    if constexpr (ACT == SGEMM_ACT_RELU) return z < 0.0f ? 0.0f : z;   // a NaN stays one
+    if constexpr (ACT == SGEMM_ACT_GELU) {
+        float cdf, bell;
+        normal_cdf(z, cdf, bell);
+        return z * cdf;
+    }
+    return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float slope(float z) {
+    if constexpr (ACT == SGEMM_ACT_RELU) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+    if constexpr (ACT == SGEMM_ACT_GELU) {
+        float cdf, bell;
+        normal_cdf(z, cdf, bell);
+        return fmaf(z * 0.39894228f, bell, cdf);
+    }
+    return z == z ? 1.0f : z;
+}
+
+// ------------------------------------------------------------------ kernels
+// What a kernel works on: `units` blocks of 32 columns, `per_row` to a row.
+struct Blocks {
+    unsigned units, per_row;
+    int K;
+};
+struct Checkpoint {
+    signed char *q, *e;
+    long long ldq, lde;
+};
+
+// Wide form, for rows that are 16-byte aligned and of a multiple of 8 columns:
+// a quarter of a block to a thread, its maximum over four lanes.  Four blocks
+// in flight per thread for bfloat16, two for float32: 64 bytes of loads.
+template <class T>
+constexpr int kDepth = sizeof(T) == 2 ? 4 : 2;
+
+template <class T, int ACT, bool WITH_Y>
+__global__ void __launch_bounds__(kThreads)
+    store_wide_kernel(Blocks b, const T *Z, long long ldz, Checkpoint c, T *Y, long long ldy) {
+    constexpr int D = kDepth<T>;
+    const int sub = threadIdx.x & 3;
+    const unsigned first = (blockIdx.x * D) * (kThreads / 4) + (threadIdx.x >> 2);
+    float z[D][8];
+    unsigned row[D];
+    int col[D];
+    bool in[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        const unsigned u = first + d * (kThreads / 4);
+        row[d] = u / b.per_row;
+        col[d] = int(u - row[d] * b.per_row) * ACT8_BLOCK + sub * 8;
+        in[d] = u < b.units && col[d] < b.K;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[d][i] = 0.0f;
+        if (in[d]) load8(Z + (long long)row[d] * ldz + col[d], z[d]);
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, magnitude_bits(z[d][i]));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = act8_exponent(top);
+        if (!in[d]) continue;
+        const float inverse = act8_inverse_step(e);
+        uint32_t w[2] = {0, 0};
+        if (e != ACT8_NAN) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w[i / 4] |= (uint32_t(act8_quantise(z[d][i], inverse)) & 0xffu) << (8 * (i % 4));
+        }
+        *reinterpret_cast<uint2 *>(c.q + row[d] * c.ldq + col[d]) = make_uint2(w[0], w[1]);
+        if (sub == 0) c.e[row[d] * c.lde + col[d] / ACT8_BLOCK] = static_cast<signed char>(e);
+        if constexpr (WITH_Y) {
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = activate<ACT>(z[d][i]);
+            store8(Y + (long long)row[d] * ldy + col[d], y);
+        }
+    }
+}
+
+// Any alignment and width: a block to a warp, a column to a lane, so that each
+// access covers consecutive elements of a row wherever it starts.
+constexpr int kAnyDepth = 4;
+
+template <class T, int ACT, bool WITH_Y>
+__global__ void __launch_bounds__(kThreads)
+    store_any_kernel(Blocks b, const T *Z, long long ldz, Checkpoint c, T *Y, long long ldy) {
+    constexpr int D = kAnyDepth;
+    const int lane = threadIdx.x & 31;
+    const unsigned first = (blockIdx.x * D) * (kThreads / 32) + (threadIdx.x >> 5);
+    float z[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        const unsigned u = first + d * (kThreads / 32), row = u / b.per_row;
+        const int col = int(u - row * b.per_row) * ACT8_BLOCK + lane;
+        z[d] = (u < b.units && col < b.K) ? to_f32(Z[(long long)row * ldz + col]) : 0.0f;
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        const unsigned u = first + d * (kThreads / 32), row = u / b.per_row;
+        const int block = int(u - row * b.per_row), col = block * ACT8_BLOCK + lane;
+        const int e = act8_exponent(__reduce_max_sync(0xffffffffu, magnitude_bits(z[d])));
+        if (u >= b.units) continue;
+        if (lane == 0) c.e[row * c.lde + block] = static_cast<signed char>(e);
+        if (col >= b.K) continue;
+        const int q = e == ACT8_NAN ? 0 : act8_quantise(z[d], act8_inverse_step(e));
+        c.q[row * c.ldq + col] = static_cast<signed char>(q);
+        if constexpr (WITH_Y) Y[(long long)row * ldy + col] = from_f32<T>(activate<ACT>(z[d]));
+    }
+}
+
+// out = dY * act'(z), or out = z where GRAD is false (dY is not read).
+template <class T, int ACT, bool GRAD>
+__global__ void __launch_bounds__(kThreads)
+    read_wide_kernel(Blocks b, Checkpoint c, const T *dY, long long lddy, T *out, long long ldo) {
+    constexpr int D = kDepth<T>;
+    const int sub = threadIdx.x & 3;
+    const unsigned first = (blockIdx.x * D) * (kThreads / 4) + (threadIdx.x >> 2);
+    uint2 w[D];
+    int e[D];
+    float dy[D][8];
+    unsigned row[D];
+    int col[D];
+    bool in[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        const unsigned u = first + d * (kThreads / 4);
+        row[d] = u / b.per_row;
+        col[d] = int(u - row[d] * b.per_row) * ACT8_BLOCK + sub * 8;
+        in[d] = u < b.units && col[d] < b.K;
+        if (!in[d]) continue;
+        w[d] = *reinterpret_cast<const uint2 *>(c.q + row[d] * c.ldq + col[d]);
+        e[d] = c.e[row[d] * c.lde + col[d] / ACT8_BLOCK];
+        if constexpr (GRAD) load8(dY + (long long)row[d] * lddy + col[d], dy[d]);
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        if (!in[d]) continue;
+        const float step = act8_step(e[d]);
+        float z[8];
+        unpack_s8(w[d].x, z);
+        unpack_s8(w[d].y, z + 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            z[i] *= step;
+            if constexpr (GRAD) z[i] = dy[d][i] * slope<ACT>(z[i]);
+        }
+        store8(out + (long long)row[d] * ldo + col[d], z);
+    }
+}
+
+template <class T, int ACT, bool GRAD>
+__global__ void __launch_bounds__(kThreads)
+    read_any_kernel(Blocks b, Checkpoint c, const T *dY, long long lddy, T *out, long long ldo) {
+    constexpr int D = kAnyDepth;
+    const int lane = threadIdx.x & 31;
+    const unsigned first = (blockIdx.x * D) * (kThreads / 32) + (threadIdx.x >> 5);
+    float z[D], dy[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        const unsigned u = first + d * (kThreads / 32), row = u / b.per_row;
+        const int block = int(u - row * b.per_row), col = block * ACT8_BLOCK + lane;
+        if (u >= b.units || col >= b.K) continue;
+        z[d] = float(c.q[row * c.ldq + col]) * act8_step(c.e[row * c.lde + block]);
+        if constexpr (GRAD) dy[d] = to_f32(dY[(long long)row * lddy + col]);
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        const unsigned u = first + d * (kThreads / 32), row = u / b.per_row;
+        const int col = int(u - row * b.per_row) * ACT8_BLOCK + lane;
+        if (u >= b.units || col >= b.K) continue;
+        float v = z[d];
+        if constexpr (GRAD) v = dy[d] * slope<ACT>(v);
+        out[(long long)row * ldo + col] = from_f32<T>(v);
+    }
+}
+
+// ------------------------------------------------------------------ host
+bool aligned(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+// A matrix whose rows of K elements can be read eight at a time.
+template <class T>
+bool wide(const T *p, int ld) {
+    return !p || (aligned(p, sizeof(T) == 1 ? 8 : 16) && ld % 8 == 0);
+}
+
+int check_sizes(int type, int M, int K) {
+    if (type != SGEMM_F32 && type != SGEMM_BF16) return SGEMM_ERR_INVALID_ARG;
+    if (M < 0 || K < 0) return SGEMM_ERR_INVALID_ARG;
+    if (M > sgh::kMaxDim || K > sgh::kMaxDim) return SGEMM_ERR_TOO_LARGE;
+    return SGEMM_OK;
+}
+bool bad_matrix(const void *p, int ld, int columns, size_t element) {
+    return !p || !aligned(p, element) || ld < std::max(1, columns);
+}
+size_t element_bytes(int type) { return type == SGEMM_BF16 ? 2 : 4; }
+int blocks_of(int K) { return (K + ACT8_BLOCK - 1) / ACT8_BLOCK; }
+
+// Calls launch(first row, rows) for row ranges of fewer than 2^31 blocks, so that
+// the kernels number them in 32 bits.
+template <class F>
+int over_rows(int M, int K, F &&launch) {
+    int sms;
+    cudaMemPool_t pool;
+    const int st = sgh::current_device(&sms, &pool);
+    if (st != SGEMM_OK) return st;
+    const long long most = std::max<long long>(1, 0x7ff00000LL / blocks_of(K));
+    for (long long r = 0; r < M; r += most) {
+        launch(r, int(std::min<long long>(most, M - r)));
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return sgh::cuda_fail(e);
+    }
+    return SGEMM_OK;
+}
+
+unsigned grid_of(unsigned units, unsigned per_block) { return (units + per_block - 1) / per_block; }
+
+template <class T, int ACT, bool WITH_Y>
+int store(int M, int K, const T *Z, int ldz, Checkpoint c, T *Y, int ldy, cudaStream_t stream) {
+    const bool w = K % 8 == 0 && wide(Z, ldz) && wide(Y, ldy) && wide(c.q, int(c.ldq));
+    return over_rows(M, K, [&](long long r, int rows) {
+        const Blocks b{unsigned(rows) * unsigned(blocks_of(K)), unsigned(blocks_of(K)), K};
+        const Checkpoint at{c.q + r * c.ldq, c.e + r * c.lde, c.ldq, c.lde};
+        T *y = WITH_Y ? Y + r * ldy : nullptr;
+        if (w)
+            store_wide_kernel<T, ACT, WITH_Y>
+                <<<grid_of(b.units, kDepth<T> * kThreads / 4), kThreads, 0, stream>>>(
+                    b, Z + r * ldz, ldz, at, y, ldy);
+        else
+            store_any_kernel<T, ACT, WITH_Y>
+                <<<grid_of(b.units, kAnyDepth * kThreads / 32), kThreads, 0, stream>>>(
+                    b, Z + r * ldz, ldz, at, y, ldy);
+        sgh::count_launch(w ? "act8 store, rows read 16 bytes at a time"
+                            : "act8 store, any alignment");
+    });
+}
+
+template <class T, int ACT, bool GRAD>
+int read(int M, int K, Checkpoint c, const T *dY, int lddy, T *out, int ldo, cudaStream_t stream) {
+    const bool w = K % 8 == 0 && wide(dY, lddy) && wide(out, ldo) && wide(c.q, int(c.ldq));
+    return over_rows(M, K, [&](long long r, int rows) {
+        const Blocks b{unsigned(rows) * unsigned(blocks_of(K)), unsigned(blocks_of(K)), K};
+        const Checkpoint at{c.q + r * c.ldq, c.e + r * c.lde, c.ldq, c.lde};
+        const T *dy = GRAD ? dY + r * lddy : nullptr;
+        if (w)
+            read_wide_kernel<T, ACT, GRAD>
+                <<<grid_of(b.units, kDepth<T> * kThreads / 4), kThreads, 0, stream>>>(
+                    b, at, dy, lddy, out + r * ldo, ldo);
+        else
+            read_any_kernel<T, ACT, GRAD>
+                <<<grid_of(b.units, kAnyDepth * kThreads / 32), kThreads, 0, stream>>>(
+                    b, at, dy, lddy, out + r * ldo, ldo);
+        sgh::count_launch(w ? "act8 read, rows read 16 bytes at a time"
+                            : "act8 read, any alignment");
+    });
+}
+
+template <class T>
+int store_typed(int M, int K, const void *Z, int ldz, int act, Checkpoint c, void *Y, int ldy,
+                cudaStream_t s) {
+    const T *z = static_cast<const T *>(Z);
+    T *y = static_cast<T *>(Y);
+    if (!y) return store<T, SGEMM_ACT_NONE, false>(M, K, z, ldz, c, y, 0, s);
+    if (act == SGEMM_ACT_RELU) return store<T, SGEMM_ACT_RELU, true>(M, K, z, ldz, c, y, ldy, s);
+    if (act == SGEMM_ACT_GELU) return store<T, SGEMM_ACT_GELU, true>(M, K, z, ldz, c, y, ldy, s);
+    return store<T, SGEMM_ACT_NONE, true>(M, K, z, ldz, c, y, ldy, s);
+}
+
+template <class T>
+int grad_typed(int M, int K, Checkpoint c, int act, const void *dY, int lddy, void *dZ, int lddz,
+               cudaStream_t s) {
+    const T *dy = static_cast<const T *>(dY);
+    T *dz = static_cast<T *>(dZ);
+    if (act == SGEMM_ACT_RELU) return read<T, SGEMM_ACT_RELU, true>(M, K, c, dy, lddy, dz, lddz, s);
+    if (act == SGEMM_ACT_GELU) return read<T, SGEMM_ACT_GELU, true>(M, K, c, dy, lddy, dz, lddz, s);
+    return read<T, SGEMM_ACT_NONE, true>(M, K, c, dy, lddy, dz, lddz, s);
+}
+
+bool bad_act(int act) { return act < SGEMM_ACT_NONE || act > SGEMM_ACT_GELU; }
+
+// A checkpoint that only is read.
+Checkpoint readable(const signed char *q, int ldq, const signed char *e, int lde) {
+    return Checkpoint{const_cast<signed char *>(q), const_cast<signed char *>(e), ldq, lde};
+}
+
+}  // namespace
+
+SGEMM_API int sgemm_act8_store(int type, int M, int K, const void *Z, int ldz, int act,
+                               signed char *q, int ldq, signed char *e, int lde, void *Y, int ldy,
+                               sgemm_stream_t stream) {
+    const int st = check_sizes(type, M, K);
+    if (st != SGEMM_OK) return st;
+    if (bad_act(act)) return SGEMM_ERR_INVALID_ARG;
+    if (M == 0 || K == 0) return SGEMM_OK;
+    if (bad_matrix(Z, ldz, K, element_bytes(type)) || bad_matrix(q, ldq, K, 1) ||
+        bad_matrix(e, lde, blocks_of(K), 1) || (Y && bad_matrix(Y, ldy, K, element_bytes(type))))
+        return SGEMM_ERR_INVALID_ARG;
+    const Checkpoint c{q, e, ldq, lde};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return type == SGEMM_BF16 ? store_typed<bf16>(M, K, Z, ldz, act, c, Y, ldy, s)
+                              : store_typed<float>(M, K, Z, ldz, act, c, Y, ldy, s);
+}
+
+SGEMM_API int sgemm_act8_load(int type, int M, int K, const signed char *q, int ldq,
+                              const signed char *e, int lde, void *X, int ldx,
+                              sgemm_stream_t stream) {
+    const int st = check_sizes(type, M, K);
+    if (st != SGEMM_OK) return st;
+    if (M == 0 || K == 0) return SGEMM_OK;
+    if (bad_matrix(X, ldx, K, element_bytes(type)) || bad_matrix(q, ldq, K, 1) ||
+        bad_matrix(e, lde, blocks_of(K), 1))
+        return SGEMM_ERR_INVALID_ARG;
+    const Checkpoint c = readable(q, ldq, e, lde);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return type == SGEMM_BF16
+               ? read<bf16, SGEMM_ACT_NONE, false>(M, K, c, nullptr, 0, static_cast<bf16 *>(X), ldx, s)
+               : read<float, SGEMM_ACT_NONE, false>(M, K, c, nullptr, 0, static_cast<float *>(X), ldx, s);
+}
+
+SGEMM_API int sgemm_act8_grad(int type, int M, int K, const signed char *q, int ldq,
+                              const signed char *e, int lde, int act, const void *dY, int lddy,
+                              void *dZ, int lddz, sgemm_stream_t stream) {
+    const int st = check_sizes(type, M, K);
+    if (st != SGEMM_OK) return st;
+    if (bad_act(act)) return SGEMM_ERR_INVALID_ARG;
+    if (M == 0 || K == 0) return SGEMM_OK;
+    if (bad_matrix(dY, lddy, K, element_bytes(type)) || bad_matrix(dZ, lddz, K, element_bytes(type)) ||
+        bad_matrix(q, ldq, K, 1) || bad_matrix(e, lde, blocks_of(K), 1))
+        return SGEMM_ERR_INVALID_ARG;
+    const Checkpoint c = readable(q, ldq, e, lde);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return type == SGEMM_BF16 ? grad_typed<bf16>(M, K, c, act, dY, lddy, dZ, lddz, s)
+                              : grad_typed<float>(M, K, c, act, dY, lddy, dZ, lddz, s);
+}

@@ -1,0 +1,57 @@
+// host_state.h -- the library's per-process and per-device state as the
+// translation units beside sgemm.cu use it (sgemm.cu holds and defines it).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace sgh {
+
+// SM count and workspace pool of the current device, or a status other than
+// SGEMM_OK (first use sets the device's state up).
+int current_device(int *sm_count, cudaMemPool_t *pool);
+
+// Records a failed CUDA call (sgemm_last_cuda_error) and returns its status.
+int cuda_fail(cudaError_t e);
+
+// A launch for sgemm_kernel_launch_count(); `main_kernel`, where it is not
+// null, becomes the calling thread's sgemm_last_kernel().
+void count_launch(const char *main_kernel = nullptr);
+
+// The limit of in-kernel waits (sgemm_set_wait_timeout_ns).
+unsigned long long wait_timeout_ns();
+
+// Largest size that an entry point accepts.
+constexpr int kMaxDim = 0x7fffffff - 0xffff;
+
+// Workspace of one call: `bytes` from the device's pool, handed out in
+// 256-byte aligned pieces, given back to it on `stream` at the end of the call.
+class Workspace {
+public:
+    Workspace(cudaMemPool_t pool, cudaStream_t stream) : pool_(pool), stream_(stream) {}
+    ~Workspace() { release(); }
+    Workspace(const Workspace &) = delete;
+    Workspace &operator=(const Workspace &) = delete;
+
+    static constexpr size_t piece(size_t bytes) { return (bytes + 255) & ~size_t(255); }
+
+    int allocate(size_t bytes);
+    template <class T>
+    T *take(size_t count) {
+        T *p = reinterpret_cast<T *>(base_ + used_);
+        used_ += piece(count * sizeof(T));
+        return p;
+    }
+    int release();
+
+private:
+    cudaMemPool_t pool_;
+    cudaStream_t stream_;
+    char *base_ = nullptr;
+    size_t used_ = 0;
+};
+
+}  // namespace sgh

@@ -25,6 +25,7 @@
 
 #include "../../include/sgemm.h"
 #include "aux_kernels.cuh"
+#include "host_state.h"
 #include "kernels.cuh"
 #include "tf32x3.cuh"
 #include "tf32x3_pair.cuh"
@@ -1407,6 +1408,41 @@ int sgemm_device_noalloc(int M, int N, int K, float alpha, const float *A, int l
 }
 
 }  // namespace
+
+// ------------------------------------------------------------------ for the other units
+int sgh::current_device(int *sm_count, cudaMemPool_t *pool) {
+    DeviceState *dev = nullptr;
+    const int st = device_state(&dev);
+    if (st != SGEMM_OK) return st;
+    *sm_count = dev->sm_count;
+    *pool = dev->pool;
+    return SGEMM_OK;
+}
+
+int sgh::cuda_fail(cudaError_t e) { return ::cuda_fail(e); }
+
+void sgh::count_launch(const char *main_kernel) {
+    g_launches.fetch_add(1);
+    if (main_kernel) t_last_kernel = main_kernel;
+}
+
+unsigned long long sgh::wait_timeout_ns() { return g_timeout_ns.load(); }
+
+int sgh::Workspace::allocate(size_t bytes) {
+    if (bytes == 0) return SGEMM_OK;
+    void *p = nullptr;
+    const cudaError_t e = cudaMallocFromPoolAsync(&p, bytes, pool_, stream_);
+    if (e != cudaSuccess) return ::cuda_fail(e);
+    base_ = static_cast<char *>(p);
+    return SGEMM_OK;
+}
+
+int sgh::Workspace::release() {
+    if (!base_) return SGEMM_OK;
+    const cudaError_t e = cudaFreeAsync(base_, stream_);
+    base_ = nullptr;
+    return e == cudaSuccess ? SGEMM_OK : ::cuda_fail(e);
+}
 
 // ==================================================================== C ABI
 SGEMM_API int sgemm(int M, int N, int K, float alpha, const float *A, int lda, const float *B,
