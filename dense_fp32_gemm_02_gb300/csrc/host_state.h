@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <cstddef>
 #include <cstdint>
@@ -17,12 +18,23 @@ int current_device(int *sm_count, cudaMemPool_t *pool);
 // Records a failed CUDA call (sgemm_last_cuda_error) and returns its status.
 int cuda_fail(cudaError_t e);
 
+// The same for a driver call's result.
+int driver_fail(int result);
+
+// cuTensorMapEncodeTiled, after current_device().
+PFN_cuTensorMapEncodeTiled_v12000 encode_tiled();
+
 // A launch for sgemm_kernel_launch_count(); `main_kernel`, where it is not
 // null, becomes the calling thread's sgemm_last_kernel().
 void count_launch(const char *main_kernel = nullptr);
 
 // The limit of in-kernel waits (sgemm_set_wait_timeout_ns).
 unsigned long long wait_timeout_ns();
+
+// Reads, and clears where asked, the copies of the device error word of lora.cu and
+// parts_gemm.cu.
+cudaError_t lora_error_word(unsigned *v, bool clear);
+cudaError_t parts_gemm_error_word(unsigned *v, bool clear);
 
 // Largest size that an entry point accepts.
 constexpr int kMaxDim = 0x7fffffff - 0xffff;

@@ -5,6 +5,8 @@
 #include "../../include/sgemm_layers.h"
 #include "host_state.h"
 #include "lora.cuh"
+#include "parts_gemm.h"
+#include "variant.cuh"
 
 #define SGEMM_API extern "C" __attribute__((visibility("default")))
 
@@ -92,39 +94,139 @@ bool bad_stack(const void *p, int ld, long long stride, int L, int rows, int col
            (L > 1 && stride < (long long)(rows - 1) * ld + columns);
 }
 
+// ------------------------------------------------------------------ operands
+long long pitch8(long long cols) { return (cols + 7) / 8 * 8; }
+
+// A matrix that the TMA reads where it lies: bfloat16, 16-byte aligned rows.
 template <class T>
-int forward(const Call &c) {
+bool in_place(const T *p, int ld) {
+    return sizeof(T) == 2 && aligned(p, 16) && ld % 8 == 0;
+}
+
+// The parts of a rows x cols matrix as an operand: the matrix itself, or planes in the
+// workspace that pack() fills.
+template <class T>
+struct Packed {
+    static constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
+    long long rows, cols, pitch;
+    bool direct;
+    const T *src;
+    int ld;
+    Parts parts{};
+
+    Packed(long long rows_, long long cols_, const void *p, int ld_)
+        : rows(rows_), cols(cols_), pitch(pitch8(cols_)), direct(in_place(static_cast<const T *>(p), ld_)),
+          src(static_cast<const T *>(p)), ld(ld_) {}
+
+    size_t elements() const { return direct ? 0 : size_t(PARTS) * rows * pitch; }
+    size_t bytes() const { return sgh::Workspace::piece(elements() * 2); }
+    void place(sgh::Workspace &ws) {
+        if (!direct) parts = Parts{ws.take<bf16>(elements()), pitch, rows * pitch};
+    }
+    int pack(int sms, cudaStream_t stream) const {
+        if (direct) return SGEMM_OK;
+        const bool wide = aligned(src, 16) && ld % (16 / sizeof(T)) == 0;
+        const long long threads = rows * (pitch / 8);
+        const unsigned grid = unsigned(std::min<long long>((threads + 255) / 256, sms * 16LL));
+        parts_kernel<PARTS><<<grid, 256, 0, stream>>>(int(rows), int(cols), Rows<T>{src, ld}, wide, parts);
+        return launched();
+    }
+    sgp::Operand operand() const {
+        if (direct)
+            return {reinterpret_cast<const bf16 *>(src), cols, rows, 1, ld, rows * (long long)ld};
+        return {parts.p, cols, rows, PARTS, pitch, rows * pitch};
+    }
+};
+
+template <class T>
+Stack<const T> stack_of(const void *p, int ld, long long stride) {
+    return {static_cast<const T *>(p), ld, stride};
+}
+
+// out (M x N) = P * Q + rank-side term of X's (forward) or dY's (backward) rows.
+//   forward:  P = X (M x K), Q = W (K x N), S = scale X A, V = B
+//   backward: P = dY, Q = W^T (N x K stored), S = G, V = A^T
+// `S`, where given, receives the rank-side sums for the caller.
+template <class T, bool BACK>
+int projection(const Call &c, float *S, float *H, int ldh, void *out, int ldo, bool want_out) {
     int sms, st;
     cudaMemPool_t pool;
     if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
     const Adapters ad = c.adapters();
-    const Rows<T> X{static_cast<const T *>(c.X), c.ldx};
-    const Stack<const T> A{static_cast<const T *>(c.A), c.lda, c.stride_a};
-    const Stack<const T> B{static_cast<const T *>(c.B), c.ldb, c.stride_b};
+    const int M = c.M, N = BACK ? c.K : c.N, K = BACK ? c.N : c.K;
+    const bool ranked = c.L > 0, product = want_out && K > 0 && N > 0;
+    constexpr auto LAYOUT = BACK ? sgp::INPUT_GRAD : sgp::FORWARD;
+    constexpr int PRODUCTS = sizeof(T) == 4 ? 6 : 1, S_PARTS = sizeof(T) == 4 ? 3 : 2;
+    Packed<T> P(M, K, BACK ? c.dY : c.X, BACK ? c.lddy : c.ldx), Q(c.K, c.N, c.W, c.ldw);
+    const sgp::Split split = product ? sgp::plan_split(M, N, K, PRODUCTS, sms) : sgp::Split{0, 0};
+    const bool slabs = ranked && product && split.splits == 1;   // the rank side in the MMA loop
+    const int tiles = (M + 255) / 256, slots = std::min(c.L, tiles);
+    const long long rpitch = pitch8(c.R);
+    const long long vrows = BACK ? N : c.R, vcols = BACK ? c.R : N, vpitch = pitch8(vcols);
+
     sgh::Workspace ws(pool, c.stream);
-    float *S = c.H;
-    long long lds = c.ldh;
-    if (!S && c.L > 0) {
-        if ((st = ws.allocate(sgh::Workspace::piece(size_t(c.M) * c.R * 4))) != SGEMM_OK) return st;
-        S = ws.take<float>(size_t(c.M) * c.R);
-        lds = c.R;
+    const auto piece = [](size_t n) { return sgh::Workspace::piece(n); };
+    const size_t s_floats = ranked && !S ? size_t(M) * c.R : 0;
+    const size_t h_elems = slabs ? size_t(S_PARTS) * M * rpitch : 0;
+    const size_t v_elems = slabs ? size_t(Packed<T>::PARTS) * slots * vrows * vpitch : 0;
+    st = ws.allocate(piece(s_floats * 4) + piece(h_elems * 2) + piece(v_elems * 2) +
+                     (slabs ? piece(tiles * 4) + piece(slots * 4) : 0) +
+                     (product ? P.bytes() + Q.bytes() + piece(split.partial_floats * 4) : 0));
+    if (st != SGEMM_OK) return st;
+    RankSide side{S, c.R, H, ldh, Parts{}};
+    if (s_floats) side.S = ws.take<float>(s_floats);
+    int *tile_adapter = nullptr, *slot_adapter = nullptr;
+    Parts v{};
+    if (slabs) {
+        side.parts = Parts{ws.take<bf16>(h_elems), rpitch, M * rpitch};
+        v = Parts{ws.take<bf16>(v_elems), vpitch, vrows * vpitch};
+        tile_adapter = ws.take<int>(tiles);
+        slot_adapter = ws.take<int>(slots);
     }
-    if (c.L > 0) {
-        const long long pairs = (long long)c.M * c.R;
-        rank_side_kernel<T, false><<<unsigned((pairs + 7) / 8), 256, 0, c.stream>>>(
-            c.M, c.K, X, A, ad, false, S, lds);
+    const Stack<const T> A = stack_of<T>(c.A, c.lda, c.stride_a), B = stack_of<T>(c.B, c.ldb, c.stride_b);
+    if (ranked) {
+        const long long pairs = (long long)M * c.R;
+        const Rows<T> X{P.src, P.ld};
+        rank_side_kernel<T, BACK><<<unsigned((pairs + 7) / 8), 256, 0, c.stream>>>(M, K, X, BACK ? B : A, ad, side);
         if ((st = launched()) != SGEMM_OK) return st;
     }
-    if (c.N > 0) {
-        const dim3 grid(unsigned((c.N + 63) / 64), unsigned((c.M + 63) / 64));
-        const Expand<T, false> expand{ad, S, lds, B, true};
-        product_kernel<<<grid, 256, 0, c.stream>>>(c.M, c.N, c.K, X,
-                                                   Rows<T>{static_cast<const T *>(c.W), c.ldw},
-                                                   expand, static_cast<const T *>(c.bias), 0.0f,
-                                                   static_cast<T *>(c.Y), c.ldy);
-        if ((st = launched("lora forward")) != SGEMM_OK) return st;
+    if (!want_out || N == 0) return ws.release();
+    sgp::Epilogue<T, BACK> epi{ad, side.S, side.lds, BACK ? A : B, BACK ? nullptr : static_cast<const T *>(c.bias),
+                               0.0f, static_cast<T *>(out), ldo};
+    if (!product) {   // K == 0: the epilogue of a zero sum
+        if ((st = sgp::finish<T, BACK>(M, N, 0, nullptr, epi, c.stream)) != SGEMM_OK) return st;
+        return ws.release();
     }
+    if (slabs) {
+        tile_adapters_kernel<<<1, 1024, 0, c.stream>>>(M, tiles, slots, ad, tile_adapter, slot_adapter);
+        if ((st = launched()) != SGEMM_OK) return st;
+        const long long threads = vrows * (vpitch / 8);
+        const dim3 grid(unsigned(std::min<long long>((threads + 255) / 256, sms * 4LL)), unsigned(slots));
+        pack_stack_kernel<T, !BACK><<<grid, 256, 0, c.stream>>>(int(vrows), int(vcols), BACK ? A : B, ad,
+                                                               slot_adapter, slots, v);
+        if ((st = launched()) != SGEMM_OK) return st;
+    }
+    P.place(ws);
+    Q.place(ws);
+    float *partial = split.partial_floats ? ws.take<float>(split.partial_floats) : nullptr;
+    if ((st = P.pack(sms, c.stream)) != SGEMM_OK || (st = Q.pack(sms, c.stream)) != SGEMM_OK) return st;
+    sgp::Product g;
+    g.M = M, g.N = N, g.K = K;
+    g.a = P.operand();
+    g.b = Q.operand();
+    if (slabs) {
+        g.h = {side.parts.p, c.R, M, S_PARTS, rpitch, M * rpitch};
+        g.v = {v.p, vcols, vrows, (long long)Packed<T>::PARTS * slots, vpitch, vrows * vpitch};
+        g.slots = slots;
+        g.tile_adapter = tile_adapter;
+    }
+    if ((st = sgp::run<T, LAYOUT>(g, epi, split, partial, sms, c.stream)) != SGEMM_OK) return st;
     return ws.release();
+}
+
+template <class T>
+int forward(const Call &c) {
+    return projection<T, false>(c, nullptr, c.H, c.ldh, c.Y, c.ldy, true);
 }
 
 template <class T>
@@ -133,29 +235,15 @@ int backward(const Call &c) {
     cudaMemPool_t pool;
     if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
     const Adapters ad = c.adapters();
-    const Rows<T> dY{static_cast<const T *>(c.dY), c.lddy};
-    const Stack<const T> A{static_cast<const T *>(c.A), c.lda, c.stride_a};
-    const Stack<const T> B{static_cast<const T *>(c.B), c.ldb, c.stride_b};
+    const bool want_dx = c.dX && c.M > 0 && c.K > 0, want_stack = (c.dA || c.dB) && c.L > 0;
     sgh::Workspace ws(pool, c.stream);
     float *G = nullptr;
     if (c.L > 0 && c.M > 0) {
         if ((st = ws.allocate(sgh::Workspace::piece(size_t(c.M) * c.R * 4))) != SGEMM_OK) return st;
         G = ws.take<float>(size_t(c.M) * c.R);
-        const long long pairs = (long long)c.M * c.R;
-        rank_side_kernel<T, true><<<unsigned((pairs + 7) / 8), 256, 0, c.stream>>>(
-            c.M, c.N, dY, B, ad, true, G, c.R);
-        if ((st = launched()) != SGEMM_OK) return st;
     }
-    if (c.dX && c.M > 0 && c.K > 0) {
-        const dim3 grid(unsigned((c.K + 63) / 64), unsigned((c.M + 63) / 64));
-        const Expand<T, true> expand{ad, G, c.R, A, false};
-        product_kernel<<<grid, 256, 0, c.stream>>>(c.M, c.K, c.N, dY,
-                                                   Transposed<T>{static_cast<const T *>(c.W), c.ldw},
-                                                   expand, static_cast<const T *>(nullptr), 0.0f,
-                                                   static_cast<T *>(c.dX), c.lddx);
-        if ((st = launched("lora backward")) != SGEMM_OK) return st;
-    }
-    if ((c.dA || c.dB) && c.L > 0) {
+    if (c.M > 0 && (st = projection<T, true>(c, G, nullptr, 0, c.dX, c.lddx, want_dx)) != SGEMM_OK) return st;
+    if (want_stack) {
         if (c.K > 0) {
             const dim3 grid(unsigned((c.K + 255) / 256), unsigned(c.R), unsigned(c.L));
             const Stack<T> out{static_cast<T *>(c.dA), c.ldda, c.stride_da};
@@ -170,7 +258,7 @@ int backward(const Call &c) {
         if (c.N > 0) {
             const dim3 grid(unsigned((c.N + 255) / 256), unsigned(c.R), unsigned(c.L));
             stack_grad_kernel<T, true><<<grid, 256, 0, c.stream>>>(
-                c.M, c.N, dY, c.H, c.ldh, ad, true,
+                c.M, c.N, Rows<T>{static_cast<const T *>(c.dY), c.lddy}, c.H, c.ldh, ad, true,
                 Stack<T>{static_cast<T *>(c.dB), c.lddb, c.stride_db});
             if ((st = launched("lora backward")) != SGEMM_OK) return st;
         }
@@ -184,15 +272,34 @@ int weight_grad(int M, int N, int K, Act8Rows x, const void *dY, int lddy, float
     int sms, st;
     cudaMemPool_t pool;
     if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
-    const dim3 grid(unsigned((N + 63) / 64), unsigned((K + 63) / 64));
-    product_kernel<<<grid, 256, 0, stream>>>(K, N, M, Act8Transposed{x},
-                                             Rows<T>{static_cast<const T *>(dY), lddy}, NoExpand{},
-                                             static_cast<const T *>(nullptr), beta,
-                                             static_cast<T *>(dW), lddw);
-    return launched("act8 weight gradient");
+    const sgp::Epilogue<T, false> epi{Adapters{}, nullptr, 0, {}, nullptr, beta, static_cast<T *>(dW), lddw};
+    if (M == 0) return sgp::finish<T, false>(K, N, 0, nullptr, epi, stream);
+    Packed<T> D(M, N, dY, lddy);
+    const sgp::Split split = sgp::plan_split(K, N, M, sizeof(T) == 4 ? 3 : 1, sms);
+    const long long xpitch = pitch8(K);
+    const size_t x_elems = size_t(M) * xpitch;
+    sgh::Workspace ws(pool, stream);
+    st = ws.allocate(sgh::Workspace::piece(x_elems * 2) + D.bytes() +
+                     sgh::Workspace::piece(split.partial_floats * 4));
+    if (st != SGEMM_OK) return st;
+    const Parts xp{ws.take<bf16>(x_elems), xpitch, M * xpitch};
+    D.place(ws);
+    float *partial = split.partial_floats ? ws.take<float>(split.partial_floats) : nullptr;
+    const bool wide = aligned(x.q, 8) && x.ldq % 8 == 0;
+    const unsigned grid = unsigned(std::min<long long>((M * (xpitch / 8) + 255) / 256, sms * 16LL));
+    parts_kernel<1><<<grid, 256, 0, stream>>>(M, K, x, wide, xp);
+    if ((st = launched()) != SGEMM_OK || (st = D.pack(sms, stream)) != SGEMM_OK) return st;
+    sgp::Product g;
+    g.M = K, g.N = N, g.K = M;
+    g.a = {xp.p, K, M, 1, xpitch, M * xpitch};
+    g.b = D.operand();
+    if ((st = sgp::run<T, sgp::WEIGHT_GRAD>(g, epi, split, partial, sms, stream)) != SGEMM_OK) return st;
+    return ws.release();
 }
 
 }  // namespace
+
+cudaError_t sgh::lora_error_word(unsigned *v, bool clear) { return sgv::unit_error_word(v, clear); }
 
 SGEMM_API int sgemm_lora(int type, int M, int N, int K, int L, int R, const void *X, int ldx,
                          const void *W, int ldw, const void *A, int lda, long long stride_a,

@@ -1,0 +1,164 @@
+// parts_gemm.cu -- launches of parts_gemm.cuh: tensor maps, the split of the
+// contraction, and the kernels of the three layouts in both types.
+#include "../../include/sgemm_layers.h"
+
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "host_state.h"
+#include "parts_gemm.cuh"
+#include "variant.cuh"
+
+namespace {
+
+using namespace sgp;
+
+int encode(CUtensorMap *map, const Operand &o, uint32_t box_inner, uint32_t box_outer) {
+    const cuuint64_t dims[3] = {cuuint64_t(o.inner), cuuint64_t(o.outer), cuuint64_t(o.planes)};
+    const cuuint64_t strides[2] = {cuuint64_t(o.pitch) * 2, cuuint64_t(o.plane_pitch) * 2};
+    const cuuint32_t box[3] = {box_inner, box_outer, 1}, steps[3] = {1, 1, 1};
+    const CUresult r = sgh::encode_tiled()(
+        map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16 *>(o.p), dims, strides, box, steps,
+        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SGEMM_OK : sgh::driver_fail(int(r));
+}
+
+template <class T, Layout LAYOUT>
+struct Kernel {
+    static constexpr bool F32 = sizeof(T) == 4, A_MN = LAYOUT == WEIGHT_GRAD, B_MN = LAYOUT != INPUT_GRAD;
+    static constexpr int PA = F32 && LAYOUT != WEIGHT_GRAD ? 3 : 1, PB = F32 ? 3 : 1;
+    static constexpr auto *main = &parts_gemm_kernel<T, PA, PB, A_MN, B_MN, LAYOUT == INPUT_GRAD>;
+    static cudaError_t set_attr() {
+        return cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM_BYTES));
+    }
+};
+
+}  // namespace
+
+cudaError_t sgh::parts_gemm_error_word(unsigned *v, bool clear) { return sgv::unit_error_word(v, clear); }
+
+int sgp::set_up() {
+    static std::atomic<unsigned long long> done{0};   // a bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return sgh::cuda_fail(e);
+    if (done.load() >> dev & 1) return SGEMM_OK;
+    cudaError_t (*const all[])() = {
+        &Kernel<float, FORWARD>::set_attr, &Kernel<bf16, FORWARD>::set_attr,
+        &Kernel<float, INPUT_GRAD>::set_attr, &Kernel<bf16, INPUT_GRAD>::set_attr,
+        &Kernel<float, WEIGHT_GRAD>::set_attr, &Kernel<bf16, WEIGHT_GRAD>::set_attr};
+    for (auto set : all)
+        if ((e = set()) != cudaSuccess) return sgh::cuda_fail(e);
+    done.fetch_or(1ull << dev);
+    return SGEMM_OK;
+}
+
+// In units of one part pair's slab (64 k of a 256 x 256 tile, 0.27 us on a pair): a
+// wave takes its slabs, about 8 units of pipeline fill and epilogue; partial sums
+// are written and read once at about 5 TB/s.  The least estimate of up to 64 ranges.
+Split sgp::plan_split(int M, int N, int K, int products, int sms) {
+    const long long pairs = std::max(1, sms / 2);
+    const long long tiles = ((M + 255LL) / 256) * ((N + 255LL) / 256);
+    const long long slabs = (K + BK - 1LL) / BK;
+    Split best{1, 0};
+    double least = 0;
+    for (long long s = 1; s <= std::min(64LL, std::max(1LL, slabs)); ++s) {
+        const long long per = (slabs + s - 1) / s;
+        if ((slabs + per - 1) / per != s) continue;      // a range would be empty
+        const long long items = tiles * s, waves = items / pairs, rest = items % pairs;
+        const double last = rest == 0 ? 0.0 : (s == 1 && 2 * rest <= pairs ? 0.5 : 1.0);
+        const double cost = (double(waves) + last) * (double(per) * products + 8.0) +
+                            (s > 1 ? 12.0 + double(s) * M * N * 8.0 / 5.0e6 / 0.27 : 0.0);
+        if (s == 1 || cost < least) {
+            least = cost;
+            best = Split{int(s), s > 1 ? size_t(s) * M * N : 0};
+        }
+    }
+    return best;
+}
+
+template <class T, bool TRANS>
+int sgp::finish(int M, int N, int splits, const float *partial, const Epilogue<T, TRANS> &epi,
+                cudaStream_t stream) {
+    // grid rows are at most 65535 to a launch
+    for (long long r = 0; r < M; r += 65535) {
+        const int rows = int(std::min<long long>(65535, M - r));
+        Epilogue<T, TRANS> at = epi;
+        at.ad.ids += at.ad.L > 0 ? r : 0;
+        at.S += r * at.lds;
+        at.out += r * at.ldo;
+        finish_kernel<<<dim3(unsigned((N + 255) / 256), unsigned(rows)), 256, 0, stream>>>(
+            M, N, splits, partial + r * N, at);
+        sgh::count_launch();
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return sgh::cuda_fail(e);
+    }
+    return SGEMM_OK;
+}
+
+template <class T, Layout LAYOUT>
+int sgp::run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Split split,
+             float *partial, int sms, cudaStream_t stream) {
+    using K = Kernel<T, LAYOUT>;
+    int st = set_up();
+    if (st != SGEMM_OK) return st;
+    const long long tiles_m = (p.M + TILE - 1LL) / TILE, tiles_n = (p.N + TILE - 1LL) / TILE;
+    if (tiles_m * tiles_n * split.splits > (1LL << 30)) return SGEMM_ERR_TOO_LARGE;
+    KernelParams kp{};
+    kp.M = p.M;
+    kp.N = p.N;
+    kp.tiles_m = int(tiles_m);
+    kp.tiles_n = int(tiles_n);
+    kp.group_m = 8;
+    kp.slabs = int((p.K + BK - 1LL) / BK);
+    kp.splits = split.splits;
+    kp.per_split = (kp.slabs + split.splits - 1) / split.splits;
+    kp.slots = p.slots;
+    kp.partial = partial;
+    kp.timeout_ns = sgh::wait_timeout_ns();
+    CUtensorMap mA, mB, mH, mV;
+    if ((st = encode(&mA, p.a, BK, K::A_MN ? BK : ROWS)) != SGEMM_OK ||
+        (st = encode(&mB, p.b, BK, K::B_MN ? BK : ROWS)) != SGEMM_OK)
+        return st;
+    mH = mA;
+    mV = mB;
+    if (p.h.p && split.splits == 1) {
+        kp.tile_adapter = p.tile_adapter;
+        kp.rank_slabs = (epi.ad.R + BK - 1) / BK;
+        if ((st = encode(&mH, p.h, BK, ROWS)) != SGEMM_OK ||
+            (st = encode(&mV, p.v, BK, K::B_MN ? BK : ROWS)) != SGEMM_OK)
+            return st;
+    }
+    const long long pairs = std::min<long long>(tiles_m * tiles_n * split.splits * (split.splits == 1 ? 2 : 1),
+                                                std::max(1, sms / 2));
+    K::main<<<unsigned(2 * pairs), THREADS, SMEM_BYTES, stream>>>(mA, mB, mH, mV, kp, epi);
+    sgh::count_launch(K::F32 ? "bf16 parts of float32, tcgen05 cta_group::2, 256x256 pair tiles"
+                             : "bf16, tcgen05 cta_group::2, 256x256 pair tiles");
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return sgh::cuda_fail(e);
+    if (split.splits > 1) return finish<T, LAYOUT == INPUT_GRAD>(p.M, p.N, split.splits, partial, epi, stream);
+    return SGEMM_OK;
+}
+
+namespace sgp {
+#define LAYER_PRODUCT(T, LAYOUT)                                                                  \
+    template int run<T, LAYOUT>(const Product &, const Epilogue<T, LAYOUT == INPUT_GRAD> &, Split, \
+                                float *, int, cudaStream_t)
+LAYER_PRODUCT(float, FORWARD);
+LAYER_PRODUCT(bf16, FORWARD);
+LAYER_PRODUCT(float, INPUT_GRAD);
+LAYER_PRODUCT(bf16, INPUT_GRAD);
+LAYER_PRODUCT(float, WEIGHT_GRAD);
+LAYER_PRODUCT(bf16, WEIGHT_GRAD);
+#undef LAYER_PRODUCT
+#define LAYER_FINISH(T, TRANS) \
+    template int finish<T, TRANS>(int, int, int, const float *, const Epilogue<T, TRANS> &, cudaStream_t)
+LAYER_FINISH(float, false);
+LAYER_FINISH(bf16, false);
+LAYER_FINISH(float, true);
+LAYER_FINISH(bf16, true);
+#undef LAYER_FINISH
+}  // namespace sgp

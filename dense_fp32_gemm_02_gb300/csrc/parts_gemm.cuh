@@ -1,0 +1,511 @@
+// parts_gemm.cuh -- out = A * B on pairs of SMs (tcgen05 `cta_group::2`) where each
+// operand is a sum of bfloat16 parts.
+//
+// A bfloat16 matrix is one part, and so is an 8-bit checkpoint (act8.cuh).  A
+// float32 matrix is three: x = x0 + x1 + x2 exactly, each part the leading 8 bits
+// of what the ones before leave.  A product of float32 matrices takes the six pairs
+// whose parts' ranks add up to at most 2 (what is left out is below 2^-22 of
+// |a||b|); with one part on one side it takes three.  Six bfloat16 MMAs cost what
+// three TF32 ones do and keep three more bits.
+//
+// The MMA's additions to its fp32 accumulator truncate: sums of n steps come out
+// smaller by up to n * 2^-23 (measured: 4.4e-6 of the result at K = 4096 for one
+// MMA per 16 k, 2.9e-5 for three per 8).  Under a bfloat16 rounding this does not
+// show.  For float32 the five small pairs have an accumulator of their own, which
+// leaves one addition per 16 k in the main one, and every CHUNK slabs the main one
+// is added to fp32 registers, round to nearest, and starts over.
+//
+// A 256 x 256 tile to a pair of SMs, 64 k to a slab, persistent; 320 threads:
+//   warp 0     copies: each CTA its 128 rows of A and its half of B's columns, by
+//              TMA with 128-byte swizzle in either major order, into a ring;
+//   warp 1     allocates TMEM; in CTA 0 one thread issues the MMAs;
+//   warps 2-9  take the accumulators to registers and write the output.
+// One part: two accumulators of 256 columns, the next tile's MMAs run under this
+// tile's epilogue.  Several: main and small, the next chunk's small pairs run while
+// the main accumulator is read.
+// A tile whose rows share an adapter gets the rank-side term as more slabs of the
+// same loop; one of mixed rows by FMAs in the epilogue, row by row: in an MMA a row
+// would meet another row's adapter times zero, which is NaN where that holds an
+// infinity or a NaN.
+// Waits are bounded as in tf32x3_pair.cuh, whose abort protocol this is.
+#pragma once
+
+#include "kernels.cuh"
+#include "parts_gemm.h"
+#include "tcgen05.cuh"
+
+namespace sgp {
+
+using namespace sg;
+using namespace sg::t3;
+using sgl::bf16;
+
+constexpr int TILE = 256, ROWS = 128, BK = 64;
+constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
+constexpr uint32_t PART_BYTES = ROWS * BK * 2;              // 16 KB: 128 rows or columns x 64 k
+constexpr uint32_t GROUP_BYTES = 64 * BK * 2;               // 8 KB: 64 of them, MN-major
+constexpr int EPI_FLOATS = EPI_WARPS * 32 * 33;
+constexpr uint32_t TMEM_COLUMNS = 512, ACC_COLUMNS = 256;
+constexpr size_t SMEM_RING = 192 * 1024;
+constexpr size_t SMEM_BYTES = SMEM_RING + EPI_FLOATS * 4 + 1024 + 256;
+static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+
+struct KernelParams {
+    int M, N;
+    int tiles_m, tiles_n, group_m;
+    int slabs;              // of 64 k
+    int splits, per_split;  // slabs of each range but the last
+    int rank_slabs;         // 64-deep slabs of the rank
+    int slots;              // adapters of the packed stack
+    const int *tile_adapter;
+    float *partial;         // splits x M x N, or null
+    unsigned long long timeout_ns;
+};
+
+// 3-D tile copy into this CTA's shared memory, counted on a barrier of either CTA.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                                 int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// D (both CTAs' TMEM) = A * B (+ D), bfloat16 operands from both CTAs' shared memory.
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                              bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
+        : "memory");
+}
+
+// Shared-memory descriptor of a part at k step kk (16 k) of its slab, 128-byte
+// swizzle.  K-major: rows of 64 k, 8-row groups 1024 bytes apart, a step is 32
+// bytes along the row.  MN-major: rows of 64 rows/columns, one per k, 8-k groups
+// 1024 bytes apart and 64-wide groups GROUP_BYTES apart; a step is 16 such rows.
+template <bool MN_MAJOR>
+__device__ __forceinline__ uint64_t part_desc(uint32_t saddr, int kk) {
+    const uint32_t at = saddr + uint32_t(kk) * (MN_MAJOR ? 2048u : 32u);
+    return uint64_t((at & 0x3FFFFu) >> 4) | uint64_t(MN_MAJOR ? (GROUP_BYTES >> 4) : 1) << 16 |
+           uint64_t(1024 >> 4) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
+}
+
+// The work of pair q of Q: items q, q + Q, ... of `items`: whole tiles, or, with
+// `splits` > 1, (tile, range) pairs; without splits a last wave of at most Q / 2
+// tiles is cut into half-width tiles.
+struct Items {
+    int full, mine_full, mine;
+
+    __device__ void init(const KernelParams &p) {
+        const int Q = gridDim.x / 2, q = blockIdx.x / 2;
+        const int items = p.tiles_m * p.tiles_n * p.splits, tail = items % Q;
+        full = (p.splits == 1 && tail != 0 && 2 * tail <= Q) ? items - tail : items;
+        const int halves = 2 * (items - full);
+        mine_full = q < full ? (full - 1 - q) / Q + 1 : 0;
+        mine = mine_full + (q < halves ? (halves - 1 - q) / Q + 1 : 0);
+    }
+    struct Item {
+        int tm, col0, ncols, split, slab0, slabs, adapter;
+    };
+    __device__ Item item(const KernelParams &p, int j) const {
+        const int Q = gridDim.x / 2, q = blockIdx.x / 2;
+        Item it;
+        it.split = 0;
+        int tn;
+        if (j < mine_full) {
+            int t = q + j * Q;
+            if (p.splits > 1) {
+                it.split = t % p.splits;
+                t /= p.splits;
+            }
+            tile_coords(t, p.tiles_m, p.tiles_n, p.group_m, it.tm, tn);
+            it.col0 = tn * TILE;
+            it.ncols = p.N - it.col0 <= TILE / 2 ? TILE / 2 : TILE;
+        } else {
+            const int h = q + (j - mine_full) * Q;
+            tile_coords(full + h / 2, p.tiles_m, p.tiles_n, p.group_m, it.tm, tn);
+            it.col0 = tn * TILE + (h & 1) * (TILE / 2);
+            it.ncols = TILE / 2;
+        }
+        it.slab0 = it.split * p.per_split;
+        it.slabs = min(p.per_split, p.slabs - it.slab0);
+        it.adapter = p.tile_adapter ? p.tile_adapter[it.tm] : -1;
+        return it;
+    }
+};
+
+// Slabs between two visits to the main accumulator of a product of several parts:
+// 512 k, 32 truncating additions, 4e-6 at most and a third of that on average.
+constexpr int CHUNK = 8;
+
+template <class T, int PA, int PB, bool A_MN, bool B_MN, bool TRANS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    parts_gemm_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
+                      const __grid_constant__ CUtensorMap mH, const __grid_constant__ CUtensorMap mV,
+                      const KernelParams p, const Epilogue<T, TRANS> epi) {
+    constexpr bool SEVERAL = PA * PB > 1;
+    constexpr uint32_t STAGE = (PA + PB) * PART_BYTES;
+    constexpr int STAGES = int(SMEM_RING / STAGE);
+    constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(A_MN) << 15) |
+                               (uint32_t(B_MN) << 16) | (uint32_t(TILE >> 4) << 24);
+
+    extern __shared__ unsigned char smem_raw[];
+    const uintptr_t base = (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023);
+    float *stage_out = reinterpret_cast<float *>(base + SMEM_RING);
+    uint64_t *full = reinterpret_cast<uint64_t *>(stage_out + EPI_FLOATS);
+    uint64_t *empty = full + STAGES;
+    uint64_t *acc_full = empty + STAGES;   // [2] MMA -> epilogue (both CTAs)
+    uint64_t *acc_empty = acc_full + 2;    // [2] epilogue -> MMA (CTA 0's)
+    uint64_t *drain = acc_empty + 2;
+    uint32_t *tmem_base = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_base + 1);
+    volatile int *issued_slot = abort_flag + 1;
+
+    const uint32_t rank = cluster_ctarank();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 2);    // CTA 0's counts one arrival, with bytes, per CTA
+            mbar_init(&empty[s], 1);   // the MMA commit, multicast to both CTAs
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&acc_full[a], 1);
+            mbar_init(&acc_empty[a], 2 * EPI_WARPS);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        *issued_slot = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) tmem_alloc_pair(tmem_base, TMEM_COLUMNS);
+    tc_fence_before();
+    cluster_barrier();
+    tc_fence_after();
+    const uint32_t taddr = *tmem_base;
+    const uint32_t peer_abort = dsmem_map(smem_addr((const void *)abort_flag), rank ^ 1u);
+    auto set_abort = [&] {
+        *abort_flag = 1;
+        st_cluster_flag(peer_abort, 1);
+    };
+
+    Items items;
+    items.init(p);
+    const uint32_t ring = smem_addr(reinterpret_cast<void *>(base));
+    // rank-side slabs: with one part a side, the two parts of S one after the other
+    const int extra = SEVERAL ? p.rank_slabs : 2 * p.rank_slabs;
+
+    if (warp == 0) {
+        // ================================================================ copies (both CTAs)
+        if (lane == 0) {
+            tma_prefetch_desc(&mA);
+            tma_prefetch_desc(&mB);
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            for (int j = 0; j < items.mine && !*abort_flag; ++j) {
+                const Items::Item it = items.item(p, j);
+                const int arow = it.tm * TILE + int(rank) * ROWS;
+                const int bcol = it.col0 + int(rank) * (it.ncols / 2);
+                const int slabs = it.slabs + (it.adapter >= 0 ? extra : 0);
+                for (int s = 0; s < slabs; ++s) {
+                    if (*abort_flag) break;
+                    // first use of a stage: parity 1 counts as complete
+                    if (!mbar_wait(&empty[stage], phase ^ 1u, p.timeout_ns)) {
+                        atomicOr(&g_error_word, ERR_EMPTY_WAIT);
+                        set_abort();
+                        break;
+                    }
+                    const uint32_t st = ring + uint32_t(stage) * STAGE;
+                    const uint32_t fb = dsmem_map(smem_addr(&full[stage]), 0u);
+                    mbar_arrive_expect_tx_cluster(fb, STAGE);
+                    if (s < it.slabs) {
+                        const int k = (it.slab0 + s) * BK;
+#pragma unroll
+                        for (int q = 0; q < PA; ++q) {
+                            const uint32_t at = st + uint32_t(q) * PART_BYTES;
+                            if constexpr (A_MN) {
+                                tma_load_3d_pair(at, &mA, fb, arow, k, q);
+                                tma_load_3d_pair(at + GROUP_BYTES, &mA, fb, arow + 64, k, q);
+                            } else {
+                                tma_load_3d_pair(at, &mA, fb, k, arow, q);
+                            }
+                        }
+#pragma unroll
+                        for (int q = 0; q < PB; ++q) {
+                            const uint32_t at = st + uint32_t(PA + q) * PART_BYTES;
+                            if constexpr (B_MN) {
+                                tma_load_3d_pair(at, &mB, fb, bcol, k, q);
+                                tma_load_3d_pair(at + GROUP_BYTES, &mB, fb, bcol + 64, k, q);
+                            } else {
+                                tma_load_3d_pair(at, &mB, fb, k, bcol, q);
+                            }
+                        }
+                    } else if constexpr (!A_MN) {
+                        const int e = s - it.slabs;
+                        const int r = (SEVERAL ? e : e % p.rank_slabs) * BK;
+#pragma unroll
+                        for (int q = 0; q < PA; ++q)
+                            tma_load_3d_pair(st + uint32_t(q) * PART_BYTES, &mH, fb, r, arow,
+                                             SEVERAL ? q : e / p.rank_slabs);
+#pragma unroll
+                        for (int q = 0; q < PB; ++q) {
+                            const uint32_t at = st + uint32_t(PA + q) * PART_BYTES;
+                            const int plane = q * p.slots + it.adapter;
+                            if constexpr (B_MN) {
+                                tma_load_3d_pair(at, &mV, fb, bcol, r, plane);
+                                tma_load_3d_pair(at + GROUP_BYTES, &mV, fb, bcol + 64, r, plane);
+                            } else {
+                                tma_load_3d_pair(at, &mV, fb, r, bcol, plane);
+                            }
+                        }
+                    }
+                    ++issued;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            *issued_slot = issued;
+        }
+    } else if (warp == 1) {
+        // ================================================================ MMA issuer (CTA 0)
+        if (lane == 0 && rank == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int chunk = 0;   // accumulator hand-overs so far
+            bool ok = true;
+            auto wait_acc = [&](int a, int use) {   // the epilogues are through with its use - 1
+                if (mbar_wait_cluster(&acc_empty[a], (uint32_t(use) & 1u) ^ 1u, p.timeout_ns)) {
+                    tc_fence_after();
+                    return true;
+                }
+                atomicOr(&g_error_word, ERR_EMPTY_WAIT);
+                set_abort();
+                return false;
+            };
+            for (int j = 0; j < items.mine && ok; ++j) {
+                const Items::Item it = items.item(p, j);
+                const uint32_t idesc = IDESC | (uint32_t(it.ncols >> 3) << 17);
+                const int slabs = it.slabs + (it.adapter >= 0 ? extra : 0);
+                const int a = SEVERAL ? 0 : j & 1;
+                const uint32_t main_acc = taddr + uint32_t(a) * ACC_COLUMNS;
+                // one part: this tile's accumulator; several: the small pairs'
+                if (!(ok = SEVERAL ? wait_acc(1, j) : wait_acc(a, j >> 1))) break;
+                for (int s = 0; s < slabs; ++s) {
+                    if (*abort_flag || !mbar_wait_cluster(&full[stage], phase, p.timeout_ns)) {
+                        if (!*abort_flag) atomicOr(&g_error_word, ERR_FULL_WAIT);
+                        set_abort();
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = ring + uint32_t(stage) * STAGE;
+                    const uint32_t sb = sa + uint32_t(PA) * PART_BYTES;
+                    auto mma = [&](uint32_t d, int qa, int qb, int kk, bool accumulate) {
+                        mma_bf16_pair(d, part_desc<A_MN>(sa + uint32_t(qa) * PART_BYTES, kk),
+                                      part_desc<B_MN>(sb + uint32_t(qb) * PART_BYTES, kk), idesc,
+                                      accumulate);
+                    };
+                    if constexpr (SEVERAL) {
+                        const uint32_t small = taddr + ACC_COLUMNS;
+#pragma unroll
+                        for (int kk = 0; kk < BK / 16; ++kk) {
+                            bool first = s == 0 && kk == 0;
+#pragma unroll
+                            for (int qa = PA - 1; qa >= 0; --qa)
+#pragma unroll
+                                for (int qb = PB - 1; qb >= 0; --qb)
+                                    if (qa + qb > 0 && qa + qb <= 2) {
+                                        mma(small, qa, qb, kk, !first);
+                                        first = false;
+                                    }
+                        }
+                        if (s % CHUNK == 0) {
+                            if (!(ok = wait_acc(0, chunk))) break;
+                            ++chunk;
+                        }
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk)
+                        mma(main_acc, 0, 0, kk, SEVERAL ? (s % CHUNK != 0 || kk > 0) : (s > 0 || kk > 0));
+                    mma_commit_pair(&empty[stage]);   // both CTAs' stage free once read
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (SEVERAL && (s % CHUNK == CHUNK - 1 || s == slabs - 1))
+                        mma_commit_pair(&acc_full[0]);
+                }
+                if (!SEVERAL && ok) mma_commit_pair(&acc_full[a]);
+            }
+            if (!ok) {
+                // no MMA may still run when either CTA frees its TMEM or exits
+                mma_commit_pair(drain);
+                if (!mbar_wait(drain, 0u, drain_limit_ns(p.timeout_ns)))
+                    atomicOr(&g_error_word, ERR_DRAIN_WAIT);
+            }
+        }
+    } else {
+        // ================================================================ epilogue (both CTAs)
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        float *buf = stage_out + (warp - 2) * (32 * 33);
+        const uint32_t lanes = uint32_t(quarter * 32) << 16;
+        int chunk = 0;
+        bool ok = true;
+        auto wait_full = [&](int a, int use) {
+            if (__any_sync(0xffffffffu, *abort_flag)) return false;
+            const bool ready =
+                __all_sync(0xffffffffu, mbar_wait(&acc_full[a], uint32_t(use) & 1u, p.timeout_ns));
+            if (!ready && lane == 0) {
+                atomicOr(&g_error_word, ERR_FULL_WAIT);
+                set_abort();
+            }
+            tc_fence_after();
+            return ready;
+        };
+        auto hand_back = [&](int a) {   // what this warp reads of it is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(dsmem_map(smem_addr(&acc_empty[a]), 0u));
+        };
+        for (int j = 0; j < items.mine && ok; ++j) {
+            const Items::Item it = items.item(p, j);
+            const int width = it.ncols / 2;               // this warp's columns: 128 or 64
+            const int row0 = it.tm * TILE + int(rank) * ROWS + quarter * 32;
+            const int col0 = it.col0 + half * width;
+            const bool fma_expand = it.adapter == -2 && p.partial == nullptr;
+
+            auto write = [&](int c, const float (&v)[32]) {   // columns col0 + 32 c ..
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) buf[lane * 33 + i] = v[i];
+                __syncwarp();
+                const int col = col0 + c * 32 + lane;
+                if (col >= p.N) return;
+                const int rows = min(32, p.M - row0);
+                if (!SG_IN_RANGE(col < it.col0 + it.ncols && row0 + rows <= (it.tm + 1) * TILE)) return;
+                if (p.partial) {
+                    float *out = p.partial + ((long long)it.split * p.M + row0) * p.N + col;
+                    for (int r = 0; r < rows; ++r) out[(long long)r * p.N] = buf[r * 33 + lane];
+                    return;
+                }
+                const float bias = epi.bias ? sgl::to_f32(epi.bias[col]) : 0.0f;
+                T *out = epi.out + (long long)row0 * epi.ldo + col;
+                if (!fma_expand && epi.beta == 0.0f) {
+#pragma unroll 8
+                    for (int r = 0; r < rows; ++r)
+                        out[(long long)r * epi.ldo] = sgl::from_f32<T>(buf[r * 33 + lane] + bias);
+                    return;
+                }
+                for (int r = 0; r < rows; ++r) {
+                    float x = buf[r * 33 + lane] + bias;
+                    const int a = fma_expand ? epi.ad.of_row(row0 + r) : -1;
+                    if (a >= 0) {
+                        const int n = epi.ad.rank(a);
+                        const float *S = epi.S + (row0 + r) * epi.lds;
+                        const T *V = epi.V.matrix(a) + (TRANS ? col * epi.V.ld : col);
+#pragma unroll 4
+                        for (int k = 0; k < n; ++k)
+                            x = fmaf(S[k], sgl::to_f32(V[TRANS ? k : k * epi.V.ld]), x);
+                    }
+                    if (epi.beta != 0.0f) x = fmaf(epi.beta, sgl::to_f32(out[(long long)r * epi.ldo]), x);
+                    out[(long long)r * epi.ldo] = sgl::from_f32<T>(x);
+                }
+            };
+
+            if constexpr (SEVERAL) {
+                const int slabs = it.slabs + (it.adapter >= 0 ? extra : 0);
+                float sum[4][32];
+                for (int s = 0; s < slabs && ok; s += CHUNK, ++chunk) {
+                    if (!(ok = wait_full(0, chunk))) break;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (c * 32 >= width) break;
+#pragma unroll
+                        for (int h = 0; h < 32; h += 16)
+                            tmem_add16(taddr + lanes + uint32_t(half * width + c * 32 + h), &sum[c][h], s > 0);
+                    }
+                    hand_back(0);
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c * 32 >= width) break;
+#pragma unroll
+                    for (int h = 0; h < 32; h += 16)
+                        tmem_add16(taddr + ACC_COLUMNS + lanes + uint32_t(half * width + c * 32 + h), &sum[c][h],
+                                   true);
+                }
+                hand_back(1);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c * 32 < width) write(c, sum[c]);
+            } else {
+                const int a = j & 1;
+                if (!(ok = wait_full(a, j >> 1))) break;
+#pragma unroll 1
+                for (int c = 0; c * 32 < width; ++c) {
+                    float v[32];
+                    tmem_load32(taddr + uint32_t(a) * ACC_COLUMNS + lanes + uint32_t(half * width + c * 32), v);
+                    if ((c + 1) * 32 >= width) hand_back(a);
+                    write(c, v);
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_barrier();   // CTA 0's MMAs and both CTAs' remote arrivals are done
+    // After an abort (set in both CTAs before the barrier above), copies may still be
+    // landing; only CTA 0 can wait for them: it completes the arrivals of stages that
+    // one producer alone filled and waits for the last STAGES fillings.
+    if (*abort_flag) {
+        if (rank == 0 && threadIdx.x == 0) {
+            const int mine = *issued_slot;
+            const int peer = ld_cluster_u32(dsmem_map(smem_addr((const void *)issued_slot), 1u));
+            const int lo = mine < peer ? mine : peer, hi = mine < peer ? peer : mine;
+            for (int q = lo; q < hi; ++q) mbar_arrive(&full[q % STAGES]);
+            for (int q = hi > STAGES ? hi - STAGES : 0; q < hi; ++q)
+                if (!mbar_wait_cluster(&full[q % STAGES], uint32_t((q / STAGES) & 1),
+                                       drain_limit_ns(p.timeout_ns))) {
+                    atomicOr(&g_error_word, ERR_DRAIN_WAIT);
+                    break;
+                }
+        }
+        cluster_barrier();
+    }
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(taddr, TMEM_COLUMNS);
+}
+
+// The ranges' partial sums added in order, and the epilogue; a thread to an element.
+template <class T, bool TRANS>
+__global__ void __launch_bounds__(256)
+    finish_kernel(int M, int N, int splits, const float *__restrict__ partial, Epilogue<T, TRANS> epi) {
+    const long long i = blockIdx.y;
+    const int j = blockIdx.x * 256 + threadIdx.x;
+    if (j >= N) return;
+    float x = epi.bias ? sgl::to_f32(epi.bias[j]) : 0.0f;
+    const long long plane = (long long)M * N;
+    float sum = 0.0f;
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) sum += partial[s * plane + i * N + j];
+    x += sum;
+    const int a = epi.ad.of_row(i);
+    if (a >= 0) {
+        const int n = epi.ad.rank(a);
+        const float *S = epi.S + i * epi.lds;
+        const T *V = epi.V.matrix(a) + (TRANS ? j * epi.V.ld : j);
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) x = fmaf(S[k], sgl::to_f32(V[TRANS ? k : k * epi.V.ld]), x);
+    }
+    T *out = epi.out + i * epi.ldo + j;
+    if (epi.beta != 0.0f) x = fmaf(epi.beta, sgl::to_f32(*out), x);
+    *out = sgl::from_f32<T>(x);
+}
+
+}  // namespace sgp

@@ -1,0 +1,68 @@
+// parts_gemm.h -- products of matrices given as sums of bfloat16 parts, on the
+// tensor cores (parts_gemm.cu), as the layer entry points call them.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "adapters.cuh"
+
+namespace sgp {
+
+// One operand: `parts` planes of bfloat16 that add up to the matrix, row-major
+// (inner: the contiguous dimension), the pitch and the plane pitch multiples of 8
+// elements and the address of 16 bytes.
+struct Operand {
+    const sgl::bf16 *p = nullptr;
+    long long inner = 0, outer = 0, planes = 0, pitch = 0, plane_pitch = 0;
+};
+
+// What becomes of an output element, fp32 up to its one rounding:
+//   out = sum + sum_r S[i][r] * V_a(i)[r][j] + bias[j] + beta * out
+// S is M x R (its scale in it), V the caller's own stack (TRANS: stored N x R).
+template <class T, bool TRANS>
+struct Epilogue {
+    sgl::Adapters ad;
+    const float *S;
+    long long lds;
+    sgl::Stack<const T> V;
+    const T *bias;
+    float beta;
+    T *out;
+    long long ldo;
+};
+
+// out (M x N) = a * b over a contraction K.  a is M x K stored K-major (inner = K) or
+// M-major (inner = M), b likewise.  The rank-side term of tiles whose rows share one
+// adapter is taken by the tensor cores: `h` the parts of S (inner R), `v` the parts
+// of `slots` adapters as planes part * slots + slot, stored like b; `tile_adapter` has
+// for each 256 rows the slot of their common adapter, -1 (none) or -2 (several).
+struct Product {
+    int M, N, K;
+    Operand a, b, h, v;
+    int slots = 0;
+    const int *tile_adapter = nullptr;
+};
+
+enum Layout { FORWARD, INPUT_GRAD, WEIGHT_GRAD };   // (a, b): (K, N)-major, (K, K), (M, N)
+
+// How the contraction is split over the SMs: `splits` ranges whose fp32 partial sums
+// (partial_floats of them) a second kernel adds in order, or one.
+struct Split {
+    int splits;
+    size_t partial_floats;
+};
+Split plan_split(int M, int N, int K, int products, int sms);
+
+// float: a of 3 parts (1 in WEIGHT_GRAD) and b of 3; bfloat16: one part each.
+template <class T, Layout LAYOUT>
+int run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Split split, float *partial,
+        int sms, cudaStream_t stream);
+
+// The second kernel alone: out from `splits` partial sums (none: the epilogue of zero).
+template <class T, bool TRANS>
+int finish(int M, int N, int splits, const float *partial, const Epilogue<T, TRANS> &epi,
+           cudaStream_t stream);
+
+int set_up();   // the kernels' attributes on the current device (its first call)
+
+}  // namespace sgp

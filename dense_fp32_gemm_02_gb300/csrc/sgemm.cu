@@ -1266,7 +1266,7 @@ int read_and_clear_error_word(cudaStream_t stream) {
         &sgv::unit_error_word, sgv::extra_variants().error_word,
         sgv::staged_variants().error_word, sgv::sweep_variants_a().error_word,
         sgv::sweep_variants_b().error_word, sgv::sweep_variants_c().error_word,
-        sgv::tall_variants().error_word};
+        sgv::tall_variants().error_word, &sgh::parts_gemm_error_word, &sgh::lora_error_word};
     unsigned any = 0;
     for (auto word : units) {
         unsigned v = 0;
@@ -1420,6 +1420,13 @@ int sgh::current_device(int *sm_count, cudaMemPool_t *pool) {
 }
 
 int sgh::cuda_fail(cudaError_t e) { return ::cuda_fail(e); }
+
+int sgh::driver_fail(int result) {
+    t_last_cuda_error = result;
+    return SGEMM_ERR_CUDA;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 sgh::encode_tiled() { return g_encode_tiled; }
 
 void sgh::count_launch(const char *main_kernel) {
     g_launches.fetch_add(1);

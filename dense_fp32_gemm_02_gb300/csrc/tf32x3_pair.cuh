@@ -48,72 +48,6 @@ constexpr uint32_t P_IDESC = (1u << 4) | (2u << 7) | (2u << 10) | (uint32_t(P_BN
                              (uint32_t(P_BM >> 4) << 24);
 constexpr uint32_t P_IDESC_HALF = (P_IDESC & ~(0x3Fu << 17)) | (uint32_t((P_BN / 2) >> 3) << 17);
 
-// Arrive (with an expected byte count) on a barrier of either CTA of the pair.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
-                     bar),
-                 "r"(bytes)
-                 : "memory");
-}
-// 2-D tile copy into this CTA's shared memory whose completion (bytes) is
-// counted on a barrier of either CTA of the pair (`cta_group::2`: here CTA 0's).
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t smem_dst, const CUtensorMap *map,
-                                                 uint32_t bar, int x, int y) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-        : "memory");
-}
-// Bounded wait on a barrier of this CTA with cluster-scope acquire: what the
-// other CTA (or its copies) did before arriving is visible afterwards.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity,
-                                                  uint64_t timeout_ns) {
-    const uint32_t a = smem_addr(bar);
-    auto try_once = [&] {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(a), "r"(parity)
-            : "memory");
-        return done != 0;
-    };
-    if (try_once()) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-#pragma unroll 1
-        for (int i = 0; i < 64; ++i)
-            if (try_once()) return true;
-        if (global_timer_ns() - t0 > timeout_ns) return false;
-    }
-}
-__device__ __forceinline__ void st_cluster_flag(uint32_t addr, int v) {
-    asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ int ld_cluster_u32(uint32_t addr) {
-    int v;
-    asm volatile("ld.relaxed.cluster.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t *dst, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(dst)),
-                 "r"(ncols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
-                 : "memory");
-}
 // D (both CTAs' TMEM) = A * B (+ D): A and B halves from both CTAs' shared memory
 __device__ __forceinline__ void mma_tf32_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                               uint32_t idesc, uint32_t accumulate) {
@@ -123,16 +57,6 @@ __device__ __forceinline__ void mma_tf32_pair(uint32_t d_tmem, uint64_t a_desc, 
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// Arrive once on the barrier at this shared offset in both CTAs when every MMA
-// this thread issued so far has completed.
-__device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_addr(bar)),
-        "h"((unsigned short)3)
-        : "memory");
-}
-
 // Work of pair q (of Q pairs): its whole 256 x 256 tiles t = q, q + Q, ...
 // below `full`, then, when the last partial wave holds at most Q/2 tiles, that
 // wave cut into 256 x 128 tiles h = q, q + Q, ... below 2 * (tiles - full).
