@@ -1,11 +1,12 @@
 // lora.cu -- entry points of the adapter layer and of the weight gradient from an
 // 8-bit checkpoint: argument checks, workspaces and launches.
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/sgemm_layers.h"
 #include "host_state.h"
-#include "lora.cuh"
 #include "parts_gemm.h"
+#include "rank_products.cuh"
 #include "variant.cuh"
 
 #define SGEMM_API extern "C" __attribute__((visibility("default")))
@@ -142,55 +143,170 @@ template <class T>
 Stack<const T> stack_of(const void *p, int ld, long long stride) {
     return {static_cast<const T *>(p), ld, stride};
 }
+template <class T>
+bool wide_rows(const T *p, long long ld) {
+    return aligned(p, 16) && ld % (16 / (long long)sizeof(T)) == 0;
+}
+template <class T>
+bool wide_stack(const Stack<T> &v, int L) {
+    return wide_rows(v.p, v.ld) && (L <= 1 || v.stride % (16 / (long long)sizeof(T)) == 0);
+}
 
-// out (M x N) = P * Q + rank-side term of X's (forward) or dY's (backward) rows.
+// Raises a kernel's shared memory limit; on every launch, as it costs less than
+// remembering the devices it was done on.
+template <class K>
+int shared_limit(K kernel, size_t bytes) {
+    if (bytes <= 48 * 1024) return SGEMM_OK;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    return e == cudaSuccess ? SGEMM_OK : sgh::cuda_fail(e);
+}
+
+// ------------------------------------------------------------------ rows by adapter
+// The grouping of a call's rows: sizes, workspace and the launch that makes it.
+struct Grouping {
+    int M, L, chunk, max_tiles, max_chunks, tiles256, slots;
+    Groups g{};
+
+    // chunk: rows of a partial sum of the stack's gradients, 512 where that makes
+    // blocks for every SM twice, else down to 128 (`columns`: of the wider gradient).
+    Grouping(const Call &c, int columns, int sms) : M(c.M), L(c.L), chunk(512) {
+        const long long across = (columns + 127) / 128;
+        while (chunk > 128 && (M / chunk) * across < 2LL * sms) chunk /= 2;
+        while (M / chunk + L > 65535) chunk *= 2;   // the grid's limit
+        max_tiles = M / ROW_TILE + L + 1;
+        max_chunks = M / chunk + L;
+        tiles256 = (M + 255) / 256;
+        slots = std::min(L, tiles256);
+    }
+    size_t bytes() const {
+        const auto piece = [](size_t n) { return sgh::Workspace::piece(n); };
+        return piece(size_t(M) * 4) + piece(8) + piece(size_t(max_tiles) * 16) + piece(size_t(max_chunks) * 16) +
+               piece(size_t(L + 1) * 4) + piece(size_t(tiles256) * 4) + piece(size_t(slots) * 4);
+    }
+    int make(sgh::Workspace &ws, const Adapters &ad, cudaStream_t stream) {
+        g = Groups{ws.take<int>(M), ws.take<int>(2), ws.take<int4>(max_tiles), ws.take<int4>(max_chunks),
+                   ws.take<int>(L + 1), chunk, ws.take<int>(tiles256), ws.take<int>(slots), slots};
+        const int st = shared_limit(group_rows_kernel, sort_smem(L));
+        if (st != SGEMM_OK) return st;
+        group_rows_kernel<<<1, SORT_THREADS, sort_smem(L), stream>>>(M, ad, g);
+        return launched();
+    }
+};
+
+// Ranges of the rank side's contraction: blocks for every SM twice over, none of them
+// below 256 deep.
+struct RankSplit {
+    int range, ranges;
+    RankSplit(int M, int C, int sms) {
+        const long long tiles = (M + ROW_TILE - 1) / ROW_TILE;
+        long long n = std::max(1LL, std::min<long long>((2LL * sms + tiles - 1) / tiles, C / 256));
+        range = int(((C + n - 1) / n + SLAB - 1) / SLAB * SLAB);
+        ranges = range > 0 ? (C + range - 1) / range : 1;
+    }
+};
+
+template <class T, bool TRANS, int NT>
+int rank_side_nt(const Grouping &gr, int C, const RankSplit &split, Rows<T> X, Stack<const T> V, const Adapters &ad,
+                 float *partial, const RankSide &to, cudaStream_t stream) {
+    auto kernel = rank_tile_kernel<T, TRANS, NT>;
+    constexpr size_t smem = RankTile<T, TRANS, NT>::SMEM;
+    const int st = shared_limit(kernel, smem);
+    if (st != SGEMM_OK) return st;
+    kernel<<<dim3(unsigned(gr.max_tiles), unsigned(split.ranges)), RANK_THREADS, smem, stream>>>(
+        C, split.range, X, wide_rows(X.p, X.ld), V, wide_stack(V, ad.L), ad, gr.g, partial,
+        (long long)gr.M * ad.R, to);
+    return launched();
+}
+
+// S (and H, and S's parts) of a call: C is the contraction.
+template <class T, bool TRANS>
+int rank_side(const Grouping &gr, int C, const RankSplit &split, Rows<T> X, Stack<const T> V, const Adapters &ad,
+              float *partial, const RankSide &to, int sms, cudaStream_t stream) {
+    auto run = ad.R <= 16 ? rank_side_nt<T, TRANS, 2> : ad.R <= 32 ? rank_side_nt<T, TRANS, 4>
+               : ad.R <= 64 ? rank_side_nt<T, TRANS, 8> : rank_side_nt<T, TRANS, 16>;
+    int st = run(gr, C, split, X, V, ad, partial, to, stream);
+    if (st != SGEMM_OK || split.ranges == 1) return st;
+    const long long total = (long long)gr.M * ad.R;
+    rank_finish_kernel<T><<<unsigned(std::min<long long>((total + 255) / 256, sms * 8LL)), 256, 0, stream>>>(
+        gr.M, split.ranges, partial, total, ad, to);
+    return launched();
+}
+
+template <class T, class X, int PA, int PB, int NT, bool RANK_ROWS>
+int stack_grad_nt(const Grouping &gr, int C, X x, bool x_wide, const float *S, long long lds, bool scaled,
+                  const Adapters &ad, float *partial, cudaStream_t stream) {
+    auto kernel = stack_tile_kernel<X, PA, PB, NT, RANK_ROWS>;
+    using Z = StackTile<X, PA, PB, NT>;
+    const int st = shared_limit(kernel, Z::SMEM);
+    if (st != SGEMM_OK) return st;
+    const unsigned across = unsigned((C + Z::COLS - 1) / Z::COLS);
+    kernel<<<dim3(across, unsigned(gr.max_chunks)), RANK_THREADS, Z::SMEM, stream>>>(C, x, x_wide, S, lds, scaled, ad,
+                                                                                    gr.g, partial);
+    return launched("lora backward, rows grouped by adapter");
+}
+
+// The gradient of a stack, C x R for each adapter (R x C where RANK_ROWS), from X's rows
+// and S.  partial: max_chunks x C x R.
+template <class T, bool RANK_ROWS, class X>
+int stack_grad(const Grouping &gr, int C, X x, bool x_wide, const float *S, long long lds, bool scaled,
+               const Adapters &ad, float *partial, Stack<T> out, int sms, cudaStream_t stream) {
+    constexpr int PA = sizeof(T) == 4 && !std::is_same<X, Act8Rows>::value ? 3 : 1, PB = sizeof(T) == 4 ? 3 : 2;
+    if (gr.M > 0) {
+        auto run = ad.R <= 16   ? stack_grad_nt<T, X, PA, PB, 2, RANK_ROWS>
+                   : ad.R <= 32 ? stack_grad_nt<T, X, PA, PB, 4, RANK_ROWS>
+                   : ad.R <= 64 ? stack_grad_nt<T, X, PA, PB, 8, RANK_ROWS>
+                                : stack_grad_nt<T, X, PA, PB, 16, RANK_ROWS>;
+        const int st = run(gr, C, x, x_wide, S, lds, scaled, ad, partial, stream);
+        if (st != SGEMM_OK) return st;
+    }
+    const long long plane = (long long)C * ad.R;
+    const dim3 grid(unsigned(std::min<long long>((plane + 255) / 256, sms * 8LL)), unsigned(ad.L));
+    stack_finish_kernel<T><<<grid, 256, 0, stream>>>(RANK_ROWS ? ad.R : C, RANK_ROWS ? C : ad.R, partial, gr.g, out);
+    return launched();
+}
+
+// out (M x N) = P * Q + rank-side term of P's rows.
 //   forward:  P = X (M x K), Q = W (K x N), S = scale X A, V = B
 //   backward: P = dY, Q = W^T (N x K stored), S = G, V = A^T
 // `S`, where given, receives the rank-side sums for the caller.
 template <class T, bool BACK>
-int projection(const Call &c, float *S, float *H, int ldh, void *out, int ldo, bool want_out) {
-    int sms, st;
-    cudaMemPool_t pool;
-    if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
+int projection(const Call &c, const Grouping &gr, float *S, float *H, int ldh, void *out, int ldo, int sms,
+               cudaMemPool_t pool) {
+    int st;
     const Adapters ad = c.adapters();
     const int M = c.M, N = BACK ? c.K : c.N, K = BACK ? c.N : c.K;
-    const bool ranked = c.L > 0, product = want_out && K > 0 && N > 0;
+    const bool ranked = c.L > 0, want_out = out && N > 0, product = want_out && K > 0;
     constexpr auto LAYOUT = BACK ? sgp::INPUT_GRAD : sgp::FORWARD;
     constexpr int PRODUCTS = sizeof(T) == 4 ? 6 : 1, S_PARTS = sizeof(T) == 4 ? 3 : 2;
     Packed<T> P(M, K, BACK ? c.dY : c.X, BACK ? c.lddy : c.ldx), Q(c.K, c.N, c.W, c.ldw);
     const sgp::Split split = product ? sgp::plan_split(M, N, K, PRODUCTS, sms) : sgp::Split{0, 0};
     const bool slabs = ranked && product && split.splits == 1;   // the rank side in the MMA loop
-    const int tiles = (M + 255) / 256, slots = std::min(c.L, tiles);
     const long long rpitch = pitch8(c.R);
     const long long vrows = BACK ? N : c.R, vcols = BACK ? c.R : N, vpitch = pitch8(vcols);
+    const RankSplit ranges(M, K, sms);
 
     sgh::Workspace ws(pool, c.stream);
     const auto piece = [](size_t n) { return sgh::Workspace::piece(n); };
     const size_t s_floats = ranked && !S ? size_t(M) * c.R : 0;
+    const size_t r_floats = ranked && ranges.ranges > 1 ? size_t(ranges.ranges) * M * c.R : 0;
     const size_t h_elems = slabs ? size_t(S_PARTS) * M * rpitch : 0;
-    const size_t v_elems = slabs ? size_t(Packed<T>::PARTS) * slots * vrows * vpitch : 0;
-    st = ws.allocate(piece(s_floats * 4) + piece(h_elems * 2) + piece(v_elems * 2) +
-                     (slabs ? piece(tiles * 4) + piece(slots * 4) : 0) +
+    const size_t v_elems = slabs ? size_t(Packed<T>::PARTS) * gr.slots * vrows * vpitch : 0;
+    st = ws.allocate(piece(s_floats * 4) + piece(r_floats * 4) + piece(h_elems * 2) + piece(v_elems * 2) +
                      (product ? P.bytes() + Q.bytes() + piece(split.partial_floats * 4) : 0));
     if (st != SGEMM_OK) return st;
     RankSide side{S, c.R, H, ldh, Parts{}};
     if (s_floats) side.S = ws.take<float>(s_floats);
-    int *tile_adapter = nullptr, *slot_adapter = nullptr;
+    float *r_partial = r_floats ? ws.take<float>(r_floats) : nullptr;
     Parts v{};
     if (slabs) {
         side.parts = Parts{ws.take<bf16>(h_elems), rpitch, M * rpitch};
         v = Parts{ws.take<bf16>(v_elems), vpitch, vrows * vpitch};
-        tile_adapter = ws.take<int>(tiles);
-        slot_adapter = ws.take<int>(slots);
     }
     const Stack<const T> A = stack_of<T>(c.A, c.lda, c.stride_a), B = stack_of<T>(c.B, c.ldb, c.stride_b);
-    if (ranked) {
-        const long long pairs = (long long)M * c.R;
-        const Rows<T> X{P.src, P.ld};
-        rank_side_kernel<T, BACK><<<unsigned((pairs + 7) / 8), 256, 0, c.stream>>>(M, K, X, BACK ? B : A, ad, side);
-        if ((st = launched()) != SGEMM_OK) return st;
-    }
-    if (!want_out || N == 0) return ws.release();
+    if (ranked && (st = rank_side<T, BACK>(gr, K, ranges, Rows<T>{P.src, P.ld}, BACK ? B : A, ad, r_partial, side, sms,
+                                           c.stream)) != SGEMM_OK)
+        return st;
+    if (!want_out) return ws.release();
     sgp::Epilogue<T, BACK> epi{ad, side.S, side.lds, BACK ? A : B, BACK ? nullptr : static_cast<const T *>(c.bias),
                                0.0f, static_cast<T *>(out), ldo};
     if (!product) {   // K == 0: the epilogue of a zero sum
@@ -198,12 +314,10 @@ int projection(const Call &c, float *S, float *H, int ldh, void *out, int ldo, b
         return ws.release();
     }
     if (slabs) {
-        tile_adapters_kernel<<<1, 1024, 0, c.stream>>>(M, tiles, slots, ad, tile_adapter, slot_adapter);
-        if ((st = launched()) != SGEMM_OK) return st;
         const long long threads = vrows * (vpitch / 8);
-        const dim3 grid(unsigned(std::min<long long>((threads + 255) / 256, sms * 4LL)), unsigned(slots));
+        const dim3 grid(unsigned(std::min<long long>((threads + 255) / 256, sms * 4LL)), unsigned(gr.slots));
         pack_stack_kernel<T, !BACK><<<grid, 256, 0, c.stream>>>(int(vrows), int(vcols), BACK ? A : B, ad,
-                                                               slot_adapter, slots, v);
+                                                               gr.g.slot_adapter, gr.slots, v);
         if ((st = launched()) != SGEMM_OK) return st;
     }
     P.place(ws);
@@ -216,9 +330,9 @@ int projection(const Call &c, float *S, float *H, int ldh, void *out, int ldo, b
     g.b = Q.operand();
     if (slabs) {
         g.h = {side.parts.p, c.R, M, S_PARTS, rpitch, M * rpitch};
-        g.v = {v.p, vcols, vrows, (long long)Packed<T>::PARTS * slots, vpitch, vrows * vpitch};
-        g.slots = slots;
-        g.tile_adapter = tile_adapter;
+        g.v = {v.p, vcols, vrows, (long long)Packed<T>::PARTS * gr.slots, vpitch, vrows * vpitch};
+        g.slots = gr.slots;
+        g.tile_adapter = gr.g.tile_adapter;
     }
     if ((st = sgp::run<T, LAYOUT>(g, epi, split, partial, sms, c.stream)) != SGEMM_OK) return st;
     return ws.release();
@@ -226,7 +340,15 @@ int projection(const Call &c, float *S, float *H, int ldh, void *out, int ldo, b
 
 template <class T>
 int forward(const Call &c) {
-    return projection<T, false>(c, nullptr, c.H, c.ldh, c.Y, c.ldy, true);
+    int sms, st;
+    cudaMemPool_t pool;
+    if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
+    sgh::Workspace ws(pool, c.stream);
+    Grouping gr(c, 0, sms);
+    if (c.L > 0 && ((st = ws.allocate(gr.bytes())) != SGEMM_OK || (st = gr.make(ws, c.adapters(), c.stream)) != SGEMM_OK))
+        return st;
+    if ((st = projection<T, false>(c, gr, nullptr, c.H, c.ldh, c.Y, c.ldy, sms, pool)) != SGEMM_OK) return st;
+    return ws.release();
 }
 
 template <class T>
@@ -235,33 +357,33 @@ int backward(const Call &c) {
     cudaMemPool_t pool;
     if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
     const Adapters ad = c.adapters();
-    const bool want_dx = c.dX && c.M > 0 && c.K > 0, want_stack = (c.dA || c.dB) && c.L > 0;
+    const bool want_stack = (c.dA || c.dB) && c.L > 0;
+    Grouping gr(c, std::max(c.K, c.N), sms);
     sgh::Workspace ws(pool, c.stream);
-    float *G = nullptr;
-    if (c.L > 0 && c.M > 0) {
-        if ((st = ws.allocate(sgh::Workspace::piece(size_t(c.M) * c.R * 4))) != SGEMM_OK) return st;
-        G = ws.take<float>(size_t(c.M) * c.R);
+    const auto piece = [](size_t n) { return sgh::Workspace::piece(n); };
+    const size_t g_floats = size_t(c.M) * c.R, p_floats = size_t(gr.max_chunks) * c.R * std::max(c.K, c.N);
+    float *G = nullptr, *partial = nullptr;
+    if (c.L > 0) {
+        if ((st = ws.allocate(gr.bytes() + piece(g_floats * 4) + (want_stack ? piece(p_floats * 4) : 0))) != SGEMM_OK ||
+            (st = gr.make(ws, ad, c.stream)) != SGEMM_OK)
+            return st;
+        G = ws.take<float>(g_floats);
+        if (want_stack) partial = ws.take<float>(p_floats);
     }
-    if (c.M > 0 && (st = projection<T, true>(c, G, nullptr, 0, c.dX, c.lddx, want_dx)) != SGEMM_OK) return st;
-    if (want_stack) {
-        if (c.K > 0) {
-            const dim3 grid(unsigned((c.K + 255) / 256), unsigned(c.R), unsigned(c.L));
-            const Stack<T> out{static_cast<T *>(c.dA), c.ldda, c.stride_da};
-            if (c.X)
-                stack_grad_kernel<T, false><<<grid, 256, 0, c.stream>>>(
-                    c.M, c.K, Rows<T>{static_cast<const T *>(c.X), c.ldx}, G, c.R, ad, false, out);
-            else
-                stack_grad_kernel<T, false><<<grid, 256, 0, c.stream>>>(
-                    c.M, c.K, Act8Rows{c.q, c.e, c.ldq, c.lde}, G, c.R, ad, false, out);
-            if ((st = launched("lora backward")) != SGEMM_OK) return st;
-        }
-        if (c.N > 0) {
-            const dim3 grid(unsigned((c.N + 255) / 256), unsigned(c.R), unsigned(c.L));
-            stack_grad_kernel<T, true><<<grid, 256, 0, c.stream>>>(
-                c.M, c.N, Rows<T>{static_cast<const T *>(c.dY), c.lddy}, c.H, c.ldh, ad, true,
-                Stack<T>{static_cast<T *>(c.dB), c.lddb, c.stride_db});
-            if ((st = launched("lora backward")) != SGEMM_OK) return st;
-        }
+    if (c.M > 0 && (st = projection<T, true>(c, gr, G, nullptr, 0, c.dX, c.lddx, sms, pool)) != SGEMM_OK) return st;
+    if (want_stack && c.K > 0) {
+        const Stack<T> out{static_cast<T *>(c.dA), c.ldda, c.stride_da};
+        const Rows<T> x{static_cast<const T *>(c.X), c.ldx};
+        st = c.X ? stack_grad<T, false>(gr, c.K, x, wide_rows(x.p, x.ld), G, c.R, true, ad, partial, out, sms, c.stream)
+                 : stack_grad<T, false>(gr, c.K, Act8Rows{c.q, c.e, c.ldq, c.lde}, aligned(c.q, 8) && c.ldq % 8 == 0, G,
+                                        c.R, true, ad, partial, out, sms, c.stream);
+        if (st != SGEMM_OK) return st;
+    }
+    if (want_stack && c.N > 0) {
+        const Rows<T> dy{static_cast<const T *>(c.dY), c.lddy};
+        st = stack_grad<T, true>(gr, c.N, dy, wide_rows(dy.p, dy.ld), c.H, c.ldh, false, ad, partial,
+                                 Stack<T>{static_cast<T *>(c.dB), c.lddb, c.stride_db}, sms, c.stream);
+        if (st != SGEMM_OK) return st;
     }
     return ws.release();
 }

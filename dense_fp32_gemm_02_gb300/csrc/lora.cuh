@@ -98,58 +98,162 @@ __global__ void __launch_bounds__(256) parts_kernel(int M, int K, X x, bool wide
     }
 }
 
-// ------------------------------------------------------------------ adapters of tiles
-// For each 256 rows: the slot of the one adapter that all of them use, -1 where none
-// of them uses any (or one of rank 0), -2 otherwise; slot_adapter lists the adapters of
-// the slots in ascending order, -1 after them.  One block.
-constexpr int MAX_ADAPTERS = 1024;
+// ------------------------------------------------------------------ rows by adapter
+// Rows grouped by their adapter, in the order of the rows within a group (a stable
+// counting sort), and the work lists of the kernels that walk the groups.  Rows
+// without an adapter, or with one of rank 0, come last, as group L.
+struct Groups {
+    int *perm;           // M: row numbers, group after group
+    int *totals;         // {tiles, chunks}
+    int4 *tiles;         // of up to ROW_TILE rows: {adapter or -1, first place in perm, rows, 0}
+    int4 *chunks;        // of up to `chunk` rows of an adapter: the same
+    int *chunk_begin;    // L + 1: the chunks of adapter a are [a], .. [a + 1]
+    int chunk;
+    int *tile_adapter;   // for each 256 rows of the call: see Product (may be null)
+    int *slot_adapter;   // `slots` of them, in ascending order, -1 after the last
+    int slots;
+};
+constexpr int MAX_ADAPTERS = 1024, ROW_TILE = 64, SORT_THREADS = 1024;
 
-__global__ void __launch_bounds__(1024)
-    tile_adapters_kernel(int M, int tiles, int slots, Adapters ad, int *tile_adapter, int *slot_adapter) {
-    __shared__ int slot_of[MAX_ADAPTERS];
-    __shared__ int warp_sum[32];
+// Exclusive prefix sum over one value per thread of a 1024-thread block; `all` their sum.
+__device__ __forceinline__ int block_prefix(int v, int *warp_sum, int &all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    slot_of[threadIdx.x] = 0;
-    __syncthreads();
-    for (int t = warp; t < tiles; t += 32) {
-        const long long r0 = (long long)t * 256;
-        int a = ad.of_row(r0);
-        bool same = true;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const long long r = r0 + i * 32 + lane;
-            if (r < M) same = same && ad.of_row(r) == a;
-        }
-        same = __all_sync(0xffffffffu, same);
-        if (lane == 0) {
-            if (same && a >= 0 && ad.rank(a) == 0) a = -1;
-            tile_adapter[t] = same ? a : -2;
-            if (same && a >= 0) slot_of[a] = 1;
-        }
-    }
-    __syncthreads();
-    // slots in ascending order of the adapters: a prefix sum over the flags
-    const int flag = slot_of[threadIdx.x];
-    int sum = flag;
+    int sum = v;
     for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
+        const int u = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += u;
     }
+    __syncthreads();
     if (lane == 31) warp_sum[warp] = sum;
     __syncthreads();
-    int before = 0, all = 0;
+    int before = 0;
+    all = 0;
     for (int w = 0; w < 32; ++w) {
         before += w < warp ? warp_sum[w] : 0;
         all += warp_sum[w];
     }
-    const int slot = before + sum - flag;
-    slot_of[threadIdx.x] = slot;
-    if (flag && SG_IN_RANGE(slot < slots)) slot_adapter[slot] = threadIdx.x;
-    for (int s = all + threadIdx.x; s < slots; s += 1024) slot_adapter[s] = -1;
+    return before + sum - v;
+}
+
+// The group of place `t` given the groups' first places (n + 1 of them, ascending).
+__device__ __forceinline__ int group_at(const int *first, int n, int t) {
+    int lo = 0, hi = n;   // first[lo] <= t < first[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        (first[mid] <= t ? lo : hi) = mid;
+    }
+    return lo;
+}
+
+constexpr size_t sort_smem(int L) { return (size_t(32) * (L + 1) + 3 * (L + 2)) * 4; }
+
+// One block: M is tens of thousands of rows at most in practice, and each warp walks
+// its share of them twice.
+__global__ void __launch_bounds__(SORT_THREADS, 1)
+    group_rows_kernel(int M, Adapters ad, Groups g) {
+    extern __shared__ int sm[];
+    __shared__ int warp_sum[32];
+    const int L = ad.L, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int *count = sm;                       // [warp][group], then the next place of each
+    int *first = count + 32 * (L + 1);     // L + 2: first place of a group
+    int *tile0 = first + (L + 2), *chunk0 = tile0 + (L + 2);
+    for (int i = threadIdx.x; i < 32 * (L + 1); i += SORT_THREADS) count[i] = 0;
     __syncthreads();
-    for (int t = threadIdx.x; t < tiles; t += 1024) {
-        const int a = tile_adapter[t];
-        if (a >= 0) tile_adapter[t] = slot_of[a];
+    const long long per = ((M + 31LL) / 32 + 31) / 32 * 32;
+    const long long r0 = warp * per, r1 = min(r0 + per, (long long)M);
+    auto group_of = [&](long long r) {
+        const int a = ad.of_row(r);
+        return a < 0 || ad.rank(a) == 0 ? L : a;
+    };
+    int *mine = count + warp * (L + 1);
+    for (long long r = r0; r < r1; r += 32) {
+        const bool in = r + lane < r1;
+        const int a = in ? group_of(r + lane) : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, a);
+        if (in && (same & ((1u << lane) - 1)) == 0) mine[a] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    // first places of the groups (up to 1025 of them: group L by the last thread alone)
+    int rows = 0, all;
+    const int a = threadIdx.x;
+    if (a < L)
+        for (int w = 0; w < 32; ++w) rows += count[w * (L + 1) + a];
+    const int at = block_prefix(rows, warp_sum, all);
+    const int tile_at = block_prefix((rows + ROW_TILE - 1) / ROW_TILE, warp_sum, all);
+    if (a < L) first[a] = at, tile0[a] = tile_at;
+    if (a == SORT_THREADS - 1) {
+        first[L] = at + rows;
+        tile0[L] = all;
+        first[L + 1] = M;
+        tile0[L + 1] = all + (M - first[L] + ROW_TILE - 1) / ROW_TILE;
+    }
+    const int chunk_at = block_prefix((rows + g.chunk - 1) / g.chunk, warp_sum, all);
+    if (a < L) chunk0[a] = chunk_at;
+    if (a == SORT_THREADS - 1) chunk0[L] = all;
+    __syncthreads();
+    for (int b = threadIdx.x; b <= L; b += SORT_THREADS) {
+        g.chunk_begin[b] = chunk0[b];
+        int place = first[b];
+        for (int w = 0; w < 32; ++w) {
+            const int n = count[w * (L + 1) + b];
+            count[w * (L + 1) + b] = place;
+            place += n;
+        }
+    }
+    if (threadIdx.x == 0) g.totals[0] = tile0[L + 1], g.totals[1] = chunk0[L];
+    __syncthreads();
+    for (long long r = r0; r < r1; r += 32) {
+        const bool in = r + lane < r1;
+        const int b = in ? group_of(r + lane) : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, b);
+        const int before = __popc(same & ((1u << lane) - 1));
+        const int place = in ? mine[b] + before : 0;
+        __syncwarp();
+        if (in && SG_IN_RANGE(place >= 0 && place < M)) g.perm[place] = int(r + lane);
+        if (in && before == 0) mine[b] += __popc(same);
+        __syncwarp();
+    }
+    for (int t = threadIdx.x; t < tile0[L + 1]; t += SORT_THREADS) {
+        const int b = group_at(tile0, L + 1, t), p = first[b] + (t - tile0[b]) * ROW_TILE;
+        g.tiles[t] = make_int4(b < L ? b : -1, p, min(ROW_TILE, first[b + 1] - p), 0);
+    }
+    for (int t = threadIdx.x; t < chunk0[L]; t += SORT_THREADS) {
+        const int b = group_at(chunk0, L, t), p = first[b] + (t - chunk0[b]) * g.chunk;
+        g.chunks[t] = make_int4(b, p, min(g.chunk, first[b + 1] - p), 0);
+    }
+    if (!g.tile_adapter) return;
+    // tiles of 256 rows with one adapter, and the slots of those adapters
+    int *flag = count;
+    __syncthreads();
+    flag[min(int(threadIdx.x), 32 * (L + 1) - 1)] = 0;
+    __syncthreads();
+    const int tiles = (M + 255) / 256;
+    for (int t = warp; t < tiles; t += 32) {
+        const long long q0 = (long long)t * 256;
+        const int b = group_of(q0);
+        bool same = true;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const long long r = q0 + i * 32 + lane;
+            if (r < M) same = same && group_of(r) == b;
+        }
+        same = __all_sync(0xffffffffu, same);
+        if (lane == 0) {
+            g.tile_adapter[t] = !same ? -2 : (b < L ? b : -1);
+            if (same && b < L) flag[b] = 1;
+        }
+    }
+    __syncthreads();
+    const int used = a < L ? flag[a] : 0;
+    const int slot = block_prefix(used, warp_sum, all);
+    if (used && SG_IN_RANGE(slot < g.slots)) g.slot_adapter[slot] = a;
+    if (a < L) flag[a] = slot;
+    for (int s = all + threadIdx.x; s < g.slots; s += SORT_THREADS) g.slot_adapter[s] = -1;
+    __syncthreads();
+    for (int t = threadIdx.x; t < tiles; t += SORT_THREADS) {
+        const int b = g.tile_adapter[t];
+        if (b >= 0) g.tile_adapter[t] = flag[b];
     }
 }
 
@@ -178,64 +282,6 @@ __global__ void __launch_bounds__(256)
             x[d] = (c + d < cols && (RANK_ROWS ? i : c + d) < rank) ? to_f32(v[i * V.ld + c + d]) : 0.0f;
         store_parts<PARTS>(at, i, c, x);
     }
-}
-
-// ------------------------------------------------------------------ rank side
-// What the rank-side product of a direction leaves behind: S (M x R, scaled), the same
-// as parts where `parts.p` is not null, and unscaled for the caller in H.
-struct RankSide {
-    float *S;
-    long long lds;
-    float *H;
-    long long ldh;
-    Parts parts;
-};
-
-// S[i][r] = scale * sum_c X[i][c] * V_a[c][r] for the rows that use an adapter, 0
-// elsewhere: a warp to an (i, r) pair.  TRANS: V_a is stored R x C.
-template <class T, bool TRANS>
-__global__ void __launch_bounds__(256)
-    rank_side_kernel(int M, int C, Rows<T> X, Stack<const T> V, Adapters ad, RankSide to) {
-    const int lane = threadIdx.x & 31;
-    const long long pair = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const long long i = pair / ad.R;
-    const int r = int(pair - i * ad.R);
-    if (i >= M) return;
-    const int a = ad.of_row(i);
-    float sum = 0.0f, scaled = 0.0f;
-    if (a >= 0 && r < ad.rank(a)) {
-        const T *v = V.matrix(a);
-        for (int c = lane; c < C; c += 32)
-            sum = fmaf(X.at(i, c), to_f32(TRANS ? v[r * V.ld + c] : v[c * V.ld + r]), sum);
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        scaled = sum * ad.scale(a);
-    }
-    if (lane != 0) return;
-    if (to.H) to.H[i * to.ldh + r] = sum;
-    to.S[i * to.lds + r] = scaled;
-    if (to.parts.p) {
-        float part[3];
-        split_parts(scaled, part);
-        for (int q = 0; q < (sizeof(T) == 4 ? 3 : 2); ++q)
-            to.parts.p[q * to.parts.plane + i * to.parts.pitch + r] = __float2bfloat16_rn(part[q]);
-    }
-}
-
-// The gradients of a stack: out_a[c][r] = sum over the rows i of a of
-// factor * X[i][c] * S[i][r] (TRANS: stored R x C): a thread to an element.
-template <class T, bool TRANS, class XR>
-__global__ void __launch_bounds__(256)
-    stack_grad_kernel(int M, int C, XR X, const float *S, long long lds, Adapters ad, bool scaled,
-                      Stack<T> out) {
-    const int c = blockIdx.x * 256 + threadIdx.x, r = blockIdx.y, a = blockIdx.z;
-    if (c >= C) return;
-    float sum = 0.0f;
-    if (r < ad.rank(a)) {
-        for (int i = 0; i < M; ++i)
-            if (ad.of_row(i) == a) sum = fmaf(X.at(i, c), S[i * lds + r], sum);
-        if (scaled) sum *= ad.scale(a);
-    }
-    out.matrix(a)[TRANS ? r * out.ld + c : c * out.ld + r] = from_f32<T>(sum);
 }
 
 }  // namespace sgl
