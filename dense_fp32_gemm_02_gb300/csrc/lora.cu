@@ -1,7 +1,6 @@
 // lora.cu -- entry points of the adapter layer and of the weight gradient from an
 // 8-bit checkpoint: argument checks, workspaces and launches.
 #include <algorithm>
-#include <type_traits>
 
 #include "../../include/sgemm_layers.h"
 #include "host_state.h"
@@ -156,7 +155,7 @@ bool wide_stack(const Stack<T> &v, int L) {
 // remembering the devices it was done on.
 template <class K>
 int shared_limit(K kernel, size_t bytes) {
-    if (bytes <= 48 * 1024) return SGEMM_OK;
+    if (bytes <= 40 * 1024) return SGEMM_OK;   // (48 KB less what a kernel declares itself)
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     return e == cudaSuccess ? SGEMM_OK : sgh::cuda_fail(e);
 }
@@ -164,7 +163,7 @@ int shared_limit(K kernel, size_t bytes) {
 // ------------------------------------------------------------------ rows by adapter
 // The grouping of a call's rows: sizes, workspace and the launch that makes it.
 struct Grouping {
-    int M, L, chunk, max_tiles, max_chunks, tiles256, slots;
+    int M, L, chunk, max_tiles, max_chunks, tiles256, width, capacity;
     Groups g{};
 
     // chunk: rows of a partial sum of the stack's gradients, 512 where that makes
@@ -176,16 +175,21 @@ struct Grouping {
         max_tiles = M / ROW_TILE + L + 1;
         max_chunks = M / chunk + L;
         tiles256 = (M + 255) / 256;
-        slots = std::min(L, tiles256);
+        // planes: for every adapter in every tile, but at most 512 MB a part
+        width = c.R <= 16 ? 16 : c.R <= 32 ? 32 : c.R <= 64 ? 64 : 128;
+        const long long kinds = std::min<long long>(L, std::min(M, 256));
+        capacity = int(std::min<long long>(16384, tiles256 * ((kinds * width + 63) / 64)));
     }
     size_t bytes() const {
         const auto piece = [](size_t n) { return sgh::Workspace::piece(n); };
         return piece(size_t(M) * 4) + piece(8) + piece(size_t(max_tiles) * 16) + piece(size_t(max_chunks) * 16) +
-               piece(size_t(L + 1) * 4) + piece(size_t(tiles256) * 4) + piece(size_t(slots) * 4);
+               piece(size_t(L + 1) * 4) + piece(size_t(L) * 4) + piece(size_t(tiles256) * 8) +
+               piece(size_t(capacity) * 16) + piece(size_t(M) * 4);
     }
     int make(sgh::Workspace &ws, const Adapters &ad, cudaStream_t stream) {
         g = Groups{ws.take<int>(M), ws.take<int>(2), ws.take<int4>(max_tiles), ws.take<int4>(max_chunks),
-                   ws.take<int>(L + 1), chunk, ws.take<int>(tiles256), ws.take<int>(slots), slots};
+                   ws.take<int>(L + 1), chunk, ws.take<int>(L), ws.take<int2>(tiles256), ws.take<int4>(capacity),
+                   ws.take<int>(M), capacity, width};
         const int st = shared_limit(group_rows_kernel, sort_smem(L));
         if (st != SGEMM_OK) return st;
         group_rows_kernel<<<1, SORT_THREADS, sort_smem(L), stream>>>(M, ad, g);
@@ -207,36 +211,35 @@ struct RankSplit {
 
 template <class T, bool TRANS, int NT>
 int rank_side_nt(const Grouping &gr, int C, const RankSplit &split, Rows<T> X, Stack<const T> V, const Adapters &ad,
-                 float *partial, const RankSide &to, cudaStream_t stream) {
+                 float *partial, cudaStream_t stream) {
     auto kernel = rank_tile_kernel<T, TRANS, NT>;
     constexpr size_t smem = RankTile<T, TRANS, NT>::SMEM;
     const int st = shared_limit(kernel, smem);
     if (st != SGEMM_OK) return st;
     kernel<<<dim3(unsigned(gr.max_tiles), unsigned(split.ranges)), RANK_THREADS, smem, stream>>>(
         C, split.range, X, wide_rows(X.p, X.ld), V, wide_stack(V, ad.L), ad, gr.g, partial,
-        (long long)gr.M * ad.R, to);
+        (long long)gr.M * ad.R);
     return launched();
 }
 
-// S (and H, and S's parts) of a call: C is the contraction.
+// S (and H, and the planes) of a call: C is the contraction.
 template <class T, bool TRANS>
 int rank_side(const Grouping &gr, int C, const RankSplit &split, Rows<T> X, Stack<const T> V, const Adapters &ad,
-              float *partial, const RankSide &to, int sms, cudaStream_t stream) {
+              float *partial, const int *unclean, const RankSide &to, cudaStream_t stream) {
     auto run = ad.R <= 16 ? rank_side_nt<T, TRANS, 2> : ad.R <= 32 ? rank_side_nt<T, TRANS, 4>
                : ad.R <= 64 ? rank_side_nt<T, TRANS, 8> : rank_side_nt<T, TRANS, 16>;
-    int st = run(gr, C, split, X, V, ad, partial, to, stream);
-    if (st != SGEMM_OK || split.ranges == 1) return st;
-    const long long total = (long long)gr.M * ad.R;
-    rank_finish_kernel<T><<<unsigned(std::min<long long>((total + 255) / 256, sms * 8LL)), 256, 0, stream>>>(
-        gr.M, split.ranges, partial, total, ad, to);
+    const int st = run(gr, C, split, X, V, ad, partial, stream);
+    if (st != SGEMM_OK) return st;
+    rank_finish_kernel<T><<<unsigned((gr.M + 7) / 8), 256, 0, stream>>>(gr.M, split.ranges, partial,
+                                                                      (long long)gr.M * ad.R, ad, gr.g, unclean, to);
     return launched();
 }
 
-template <class T, class X, int PA, int PB, int NT, bool RANK_ROWS>
+template <class X, int PB, int NT, bool RANK_ROWS>
 int stack_grad_nt(const Grouping &gr, int C, X x, bool x_wide, const float *S, long long lds, bool scaled,
                   const Adapters &ad, float *partial, cudaStream_t stream) {
-    auto kernel = stack_tile_kernel<X, PA, PB, NT, RANK_ROWS>;
-    using Z = StackTile<X, PA, PB, NT>;
+    auto kernel = stack_tile_kernel<X, PB, NT, RANK_ROWS>;
+    using Z = StackTile<X, PB, NT>;
     const int st = shared_limit(kernel, Z::SMEM);
     if (st != SGEMM_OK) return st;
     const unsigned across = unsigned((C + Z::COLS - 1) / Z::COLS);
@@ -250,12 +253,12 @@ int stack_grad_nt(const Grouping &gr, int C, X x, bool x_wide, const float *S, l
 template <class T, bool RANK_ROWS, class X>
 int stack_grad(const Grouping &gr, int C, X x, bool x_wide, const float *S, long long lds, bool scaled,
                const Adapters &ad, float *partial, Stack<T> out, int sms, cudaStream_t stream) {
-    constexpr int PA = sizeof(T) == 4 && !std::is_same<X, Act8Rows>::value ? 3 : 1, PB = sizeof(T) == 4 ? 3 : 2;
+    constexpr int PB = sizeof(T) == 4 ? 3 : 2;
     if (gr.M > 0) {
-        auto run = ad.R <= 16   ? stack_grad_nt<T, X, PA, PB, 2, RANK_ROWS>
-                   : ad.R <= 32 ? stack_grad_nt<T, X, PA, PB, 4, RANK_ROWS>
-                   : ad.R <= 64 ? stack_grad_nt<T, X, PA, PB, 8, RANK_ROWS>
-                                : stack_grad_nt<T, X, PA, PB, 16, RANK_ROWS>;
+        auto run = ad.R <= 16   ? stack_grad_nt<X, PB, 2, RANK_ROWS>
+                   : ad.R <= 32 ? stack_grad_nt<X, PB, 4, RANK_ROWS>
+                   : ad.R <= 64 ? stack_grad_nt<X, PB, 8, RANK_ROWS>
+                                : stack_grad_nt<X, PB, 16, RANK_ROWS>;
         const int st = run(gr, C, x, x_wide, S, lds, scaled, ad, partial, stream);
         if (st != SGEMM_OK) return st;
     }
@@ -280,45 +283,45 @@ int projection(const Call &c, const Grouping &gr, float *S, float *H, int ldh, v
     constexpr int PRODUCTS = sizeof(T) == 4 ? 6 : 1, S_PARTS = sizeof(T) == 4 ? 3 : 2;
     Packed<T> P(M, K, BACK ? c.dY : c.X, BACK ? c.lddy : c.ldx), Q(c.K, c.N, c.W, c.ldw);
     const sgp::Split split = product ? sgp::plan_split(M, N, K, PRODUCTS, sms) : sgp::Split{0, 0};
-    const bool slabs = ranked && product && split.splits == 1;   // the rank side in the MMA loop
-    const long long rpitch = pitch8(c.R);
-    const long long vrows = BACK ? N : c.R, vcols = BACK ? c.R : N, vpitch = pitch8(vcols);
+    const bool planes = ranked && product;   // the rank side in the MMA loop
+    const long long vpitch = pitch8(N), vplane = gr.width * vpitch;
     const RankSplit ranges(M, K, sms);
 
     sgh::Workspace ws(pool, c.stream);
     const auto piece = [](size_t n) { return sgh::Workspace::piece(n); };
     const size_t s_floats = ranked && !S ? size_t(M) * c.R : 0;
-    const size_t r_floats = ranked && ranges.ranges > 1 ? size_t(ranges.ranges) * M * c.R : 0;
-    const size_t h_elems = slabs ? size_t(S_PARTS) * M * rpitch : 0;
-    const size_t v_elems = slabs ? size_t(Packed<T>::PARTS) * gr.slots * vrows * vpitch : 0;
+    const size_t r_floats = ranked ? size_t(ranges.ranges) * M * c.R : 0;
+    const size_t h_elems = planes ? size_t(S_PARTS) * gr.capacity * 256 * 64 : 0;
+    const size_t v_elems = planes ? size_t(Packed<T>::PARTS) * c.L * vplane : 0;
     st = ws.allocate(piece(s_floats * 4) + piece(r_floats * 4) + piece(h_elems * 2) + piece(v_elems * 2) +
+                     (planes ? piece(size_t(c.L) * 4) : 0) +
                      (product ? P.bytes() + Q.bytes() + piece(split.partial_floats * 4) : 0));
     if (st != SGEMM_OK) return st;
-    RankSide side{S, c.R, H, ldh, Parts{}};
+    RankSide side{S, H, ldh, nullptr};
     if (s_floats) side.S = ws.take<float>(s_floats);
     float *r_partial = r_floats ? ws.take<float>(r_floats) : nullptr;
-    Parts v{};
-    if (slabs) {
-        side.parts = Parts{ws.take<bf16>(h_elems), rpitch, M * rpitch};
-        v = Parts{ws.take<bf16>(v_elems), vpitch, vrows * vpitch};
-    }
     const Stack<const T> A = stack_of<T>(c.A, c.lda, c.stride_a), B = stack_of<T>(c.B, c.ldb, c.stride_b);
-    if (ranked && (st = rank_side<T, BACK>(gr, K, ranges, Rows<T>{P.src, P.ld}, BACK ? B : A, ad, r_partial, side, sms,
-                                           c.stream)) != SGEMM_OK)
+    Parts v{};
+    int *unclean = nullptr;
+    if (planes) {
+        side.planes = ws.take<bf16>(h_elems);
+        v = Parts{ws.take<bf16>(v_elems), vpitch, vplane};
+        unclean = ws.take<int>(c.L);
+        const cudaError_t e = cudaMemsetAsync(unclean, 0, size_t(c.L) * 4, c.stream);
+        if (e != cudaSuccess) return sgh::cuda_fail(e);
+        pack_stack_kernel<T, BACK><<<dim3(unsigned((N + 63) / 64), unsigned(c.L)), 256, 0, c.stream>>>(
+            N, BACK ? A : B, ad, gr.g.used, gr.width, unclean, v);
+        if ((st = launched()) != SGEMM_OK) return st;
+    }
+    if (ranked && (st = rank_side<T, BACK>(gr, K, ranges, Rows<T>{P.src, P.ld}, BACK ? B : A, ad, r_partial, unclean,
+                                           side, c.stream)) != SGEMM_OK)
         return st;
     if (!want_out) return ws.release();
-    sgp::Epilogue<T, BACK> epi{ad, side.S, side.lds, BACK ? A : B, BACK ? nullptr : static_cast<const T *>(c.bias),
+    sgp::Epilogue<T, BACK> epi{ad, side.S, c.R, BACK ? A : B, BACK ? nullptr : static_cast<const T *>(c.bias),
                                0.0f, static_cast<T *>(out), ldo};
     if (!product) {   // K == 0: the epilogue of a zero sum
-        if ((st = sgp::finish<T, BACK>(M, N, 0, nullptr, epi, c.stream)) != SGEMM_OK) return st;
+        if ((st = sgp::finish<T, BACK>(M, N, 0, nullptr, nullptr, epi, c.stream)) != SGEMM_OK) return st;
         return ws.release();
-    }
-    if (slabs) {
-        const long long threads = vrows * (vpitch / 8);
-        const dim3 grid(unsigned(std::min<long long>((threads + 255) / 256, sms * 4LL)), unsigned(gr.slots));
-        pack_stack_kernel<T, !BACK><<<grid, 256, 0, c.stream>>>(int(vrows), int(vcols), BACK ? A : B, ad,
-                                                               gr.g.slot_adapter, gr.slots, v);
-        if ((st = launched()) != SGEMM_OK) return st;
     }
     P.place(ws);
     Q.place(ws);
@@ -328,11 +331,13 @@ int projection(const Call &c, const Grouping &gr, float *S, float *H, int ldh, v
     g.M = M, g.N = N, g.K = K;
     g.a = P.operand();
     g.b = Q.operand();
-    if (slabs) {
-        g.h = {side.parts.p, c.R, M, S_PARTS, rpitch, M * rpitch};
-        g.v = {v.p, vcols, vrows, (long long)Packed<T>::PARTS * gr.slots, vpitch, vrows * vpitch};
-        g.slots = gr.slots;
-        g.tile_adapter = gr.g.tile_adapter;
+    if (planes) {
+        g.h = {side.planes, 64, 256, (long long)S_PARTS * gr.capacity, 64, 256 * 64};
+        g.v = {v.p, N, gr.width, (long long)Packed<T>::PARTS * c.L, vpitch, vplane};
+        g.planes = gr.g.planes;
+        g.plane_adapter = gr.g.plane_adapter;
+        g.capacity = gr.capacity;
+        g.width = gr.width;
     }
     if ((st = sgp::run<T, LAYOUT>(g, epi, split, partial, sms, c.stream)) != SGEMM_OK) return st;
     return ws.release();
@@ -375,7 +380,7 @@ int backward(const Call &c) {
         const Stack<T> out{static_cast<T *>(c.dA), c.ldda, c.stride_da};
         const Rows<T> x{static_cast<const T *>(c.X), c.ldx};
         st = c.X ? stack_grad<T, false>(gr, c.K, x, wide_rows(x.p, x.ld), G, c.R, true, ad, partial, out, sms, c.stream)
-                 : stack_grad<T, false>(gr, c.K, Act8Rows{c.q, c.e, c.ldq, c.lde}, aligned(c.q, 8) && c.ldq % 8 == 0, G,
+                 : stack_grad<T, false>(gr, c.K, Act8Rows{c.q, c.e, c.ldq, c.lde}, aligned(c.q, 16) && c.ldq % 16 == 0, G,
                                         c.R, true, ad, partial, out, sms, c.stream);
         if (st != SGEMM_OK) return st;
     }
@@ -395,7 +400,7 @@ int weight_grad(int M, int N, int K, Act8Rows x, const void *dY, int lddy, float
     cudaMemPool_t pool;
     if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
     const sgp::Epilogue<T, false> epi{Adapters{}, nullptr, 0, {}, nullptr, beta, static_cast<T *>(dW), lddw};
-    if (M == 0) return sgp::finish<T, false>(K, N, 0, nullptr, epi, stream);
+    if (M == 0) return sgp::finish<T, false>(K, N, 0, nullptr, nullptr, epi, stream);
     Packed<T> D(M, N, dY, lddy);
     const sgp::Split split = sgp::plan_split(K, N, M, sizeof(T) == 4 ? 3 : 1, sms);
     const long long xpitch = pitch8(K);

@@ -102,6 +102,11 @@ __global__ void __launch_bounds__(256) parts_kernel(int M, int K, X x, bool wide
 // Rows grouped by their adapter, in the order of the rows within a group (a stable
 // counting sort), and the work lists of the kernels that walk the groups.  Rows
 // without an adapter, or with one of rank 0, come last, as group L.
+//
+// For the tensor cores, each 256 rows (a tile of the product) also get their rank-side
+// operand laid out: the adapters that occur in the tile, in ascending order, take `width`
+// columns each, and 64 columns make a plane of 256 x 64, in which a row has its own sums
+// in its own adapter's columns and zeros elsewhere.
 struct Groups {
     int *perm;           // M: row numbers, group after group
     int *totals;         // {tiles, chunks}
@@ -109,16 +114,21 @@ struct Groups {
     int4 *chunks;        // of up to `chunk` rows of an adapter: the same
     int *chunk_begin;    // L + 1: the chunks of adapter a are [a], .. [a + 1]
     int chunk;
-    int *tile_adapter;   // for each 256 rows of the call: see Product (may be null)
-    int *slot_adapter;   // `slots` of them, in ascending order, -1 after the last
-    int slots;
+    int *used;           // L: whether a row uses the adapter
+    int2 *planes;        // for each 256 rows {first plane, planes}: NO_PLANES past the capacity
+    int4 *plane_adapter; // of a plane's 64 / width adapters (the last one repeated), or
+                         // {adapter, first rank column} where width >= 64
+    int *position;       // M: which of its tile's adapters a row uses
+    int capacity;        // planes
+    int width;           // 16, 32, 64 or 128
 };
-constexpr int MAX_ADAPTERS = 1024, ROW_TILE = 64, SORT_THREADS = 1024;
+constexpr int MAX_ADAPTERS = 1024, ROW_TILE = 64, SORT_THREADS = 1024, NO_PLANES = -1;
 
 // Exclusive prefix sum over one value per thread of a 1024-thread block; `all` their sum.
 __device__ __forceinline__ int block_prefix(int v, int *warp_sum, int &all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int sum = v;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += u;
@@ -126,12 +136,9 @@ __device__ __forceinline__ int block_prefix(int v, int *warp_sum, int &all) {
     __syncthreads();
     if (lane == 31) warp_sum[warp] = sum;
     __syncthreads();
-    int before = 0;
-    all = 0;
-    for (int w = 0; w < 32; ++w) {
-        before += w < warp ? warp_sum[w] : 0;
-        all += warp_sum[w];
-    }
+    const int w = warp_sum[lane];
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+    all = __reduce_add_sync(0xffffffffu, w);
     return before + sum - v;
 }
 
@@ -145,40 +152,59 @@ __device__ __forceinline__ int group_at(const int *first, int n, int t) {
     return lo;
 }
 
-constexpr size_t sort_smem(int L) { return (size_t(32) * (L + 1) + 3 * (L + 2)) * 4; }
+constexpr size_t sort_smem(int L) { return (size_t(32) * (L + 1) + 3 * (L + 2) + 32 * 32) * 4; }
 
-// One block: M is tens of thousands of rows at most in practice, and each warp walks
-// its share of them twice.
+// One block; each warp walks its share of the rows, 256 at a time, in three passes of
+// eight independent loads.  Bound by their latency: about 8 us up to 8192 rows.
 __global__ void __launch_bounds__(SORT_THREADS, 1)
     group_rows_kernel(int M, Adapters ad, Groups g) {
     extern __shared__ int sm[];
     __shared__ int warp_sum[32];
+    __shared__ unsigned char no_rank[MAX_ADAPTERS];
     const int L = ad.L, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int *count = sm;                       // [warp][group], then the next place of each
     int *first = count + 32 * (L + 1);     // L + 2: first place of a group
     int *tile0 = first + (L + 2), *chunk0 = tile0 + (L + 2);
+    int *bits = chunk0 + (L + 2) + warp * 32;   // the adapters of this warp's current 256 rows
+    const int a = threadIdx.x;
+    if (a < L) no_rank[a] = ad.rank(a) == 0;
     for (int i = threadIdx.x; i < 32 * (L + 1); i += SORT_THREADS) count[i] = 0;
     __syncthreads();
-    const long long per = ((M + 31LL) / 32 + 31) / 32 * 32;
-    const long long r0 = warp * per, r1 = min(r0 + per, (long long)M);
-    auto group_of = [&](long long r) {
-        const int a = ad.of_row(r);
-        return a < 0 || ad.rank(a) == 0 ? L : a;
-    };
+    const int tiles = (M + 255) / 256, per = (tiles + 31) / 32;
+    const int t0 = min(warp * per, tiles), t1 = min(t0 + per, tiles);
     int *mine = count + warp * (L + 1);
-    for (long long r = r0; r < r1; r += 32) {
-        const bool in = r + lane < r1;
-        const int a = in ? group_of(r + lane) : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, a);
-        if (in && (same & ((1u << lane) - 1)) == 0) mine[a] += __popc(same);
+    // groups of rows 256 t + 32 i + lane; -1 past the end
+    auto load = [&](int t, int (&b)[8]) {
+        const long long r0 = (long long)t * 256 + lane;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = r0 + 32 * i < M ? ad.of_row(r0 + 32 * i) : -2;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = b[i] == -2 ? -1 : (b[i] < 0 || no_rank[b[i]] ? L : b[i]);
+    };
+    for (int t = t0; t < t1; ++t) {
+        int b[8];
+        load(t, b);
+        bits[lane] = 0;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const unsigned same = __match_any_sync(0xffffffffu, b[i]);
+            if (b[i] >= 0 && (same & ((1u << lane) - 1)) == 0) {
+                mine[b[i]] += __popc(same);
+                if (b[i] < L) atomicOr(&bits[b[i] >> 5], 1 << (b[i] & 31));
+            }
+            __syncwarp();
+        }
+        const int kinds = __reduce_add_sync(0xffffffffu, __popc(bits[lane]));
+        if (lane == 0) g.planes[t] = make_int2(0, (kinds * g.width + 63) / 64);
         __syncwarp();
     }
     __syncthreads();
     // first places of the groups (up to 1025 of them: group L by the last thread alone)
     int rows = 0, all;
-    const int a = threadIdx.x;
     if (a < L)
         for (int w = 0; w < 32; ++w) rows += count[w * (L + 1) + a];
+    if (a < L) g.used[a] = rows > 0;
     const int at = block_prefix(rows, warp_sum, all);
     const int tile_at = block_prefix((rows + ROW_TILE - 1) / ROW_TILE, warp_sum, all);
     if (a < L) first[a] = at, tile0[a] = tile_at;
@@ -191,6 +217,13 @@ __global__ void __launch_bounds__(SORT_THREADS, 1)
     const int chunk_at = block_prefix((rows + g.chunk - 1) / g.chunk, warp_sum, all);
     if (a < L) chunk0[a] = chunk_at;
     if (a == SORT_THREADS - 1) chunk0[L] = all;
+    // first planes of the tiles
+    for (int base = 0, t = 0; t < tiles; t += SORT_THREADS) {
+        const int n = t + a < tiles ? g.planes[t + a].y : 0;
+        const int p = base + block_prefix(n, warp_sum, all);
+        if (t + a < tiles) g.planes[t + a] = p + n <= g.capacity ? make_int2(p, n) : make_int2(0, NO_PLANES);
+        base = min(base + all, 1 << 29);
+    }
     __syncthreads();
     for (int b = threadIdx.x; b <= L; b += SORT_THREADS) {
         g.chunk_begin[b] = chunk0[b];
@@ -203,16 +236,60 @@ __global__ void __launch_bounds__(SORT_THREADS, 1)
     }
     if (threadIdx.x == 0) g.totals[0] = tile0[L + 1], g.totals[1] = chunk0[L];
     __syncthreads();
-    for (long long r = r0; r < r1; r += 32) {
-        const bool in = r + lane < r1;
-        const int b = in ? group_of(r + lane) : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, b);
-        const int before = __popc(same & ((1u << lane) - 1));
-        const int place = in ? mine[b] + before : 0;
+    for (int t = t0; t < t1; ++t) {
+        int b[8];
+        load(t, b);
+        bits[lane] = 0;
         __syncwarp();
-        if (in && SG_IN_RANGE(place >= 0 && place < M)) g.perm[place] = int(r + lane);
-        if (in && before == 0) mine[b] += __popc(same);
-        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const unsigned same = __match_any_sync(0xffffffffu, b[i]);
+            const int before = __popc(same & ((1u << lane) - 1));
+            const int place = b[i] >= 0 ? mine[b[i]] + before : 0;
+            __syncwarp();
+            if (b[i] >= 0) {
+                if (SG_IN_RANGE(place >= 0 && place < M)) g.perm[place] = t * 256 + i * 32 + lane;
+                if (before == 0) {
+                    mine[b[i]] += __popc(same);
+                    if (b[i] < L) atomicOr(&bits[b[i] >> 5], 1 << (b[i] & 31));
+                }
+            }
+            __syncwarp();
+        }
+        // the tile's adapters in ascending order: word w of the bits is lane w's
+        const unsigned word = unsigned(bits[lane]);
+        int below = __popc(word);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, below, o);
+            if (lane >= o) below += u;
+        }
+        const int kinds = __shfl_sync(0xffffffffu, below, 31);
+        below -= __popc(word);
+        const int2 planes = g.planes[t];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int w = max(b[i], 0) >> 5 & 31;
+            const unsigned of_w = __shfl_sync(0xffffffffu, word, w);
+            const int position = __shfl_sync(0xffffffffu, below, w) + __popc(of_w & ((1u << (b[i] & 31)) - 1));
+            if (b[i] >= 0) g.position[t * 256 + i * 32 + lane] = b[i] < L ? position : 0;
+        }
+        if (planes.y == NO_PLANES) continue;
+        const int per_plane = g.width >= 64 ? 1 : 64 / g.width, halves = g.width > 64 ? g.width / 64 : 1;
+        unsigned left = word;
+        for (int k = below; left != 0; ++k, left &= left - 1) {
+            const int id = lane * 32 + __ffs(left) - 1;
+            if (g.width >= 64) {
+                for (int h = 0; h < halves; ++h)
+                    if (SG_IN_RANGE(planes.x + k * halves + h < g.capacity))
+                        g.plane_adapter[planes.x + k * halves + h] = make_int4(id, h * 64, 0, 0);
+            } else if (SG_IN_RANGE(planes.x + k / per_plane < g.capacity)) {
+                int *to = reinterpret_cast<int *>(&g.plane_adapter[planes.x + k / per_plane]);
+                to[k % per_plane] = id;
+                if (k == kinds - 1)
+                    for (int d = k % per_plane + 1; d < per_plane; ++d) to[d] = id;
+            }
+        }
     }
     for (int t = threadIdx.x; t < tile0[L + 1]; t += SORT_THREADS) {
         const int b = group_at(tile0, L + 1, t), p = first[b] + (t - tile0[b]) * ROW_TILE;
@@ -222,65 +299,48 @@ __global__ void __launch_bounds__(SORT_THREADS, 1)
         const int b = group_at(chunk0, L, t), p = first[b] + (t - chunk0[b]) * g.chunk;
         g.chunks[t] = make_int4(b, p, min(g.chunk, first[b + 1] - p), 0);
     }
-    if (!g.tile_adapter) return;
-    // tiles of 256 rows with one adapter, and the slots of those adapters
-    int *flag = count;
-    __syncthreads();
-    flag[min(int(threadIdx.x), 32 * (L + 1) - 1)] = 0;
-    __syncthreads();
-    const int tiles = (M + 255) / 256;
-    for (int t = warp; t < tiles; t += 32) {
-        const long long q0 = (long long)t * 256;
-        const int b = group_of(q0);
-        bool same = true;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const long long r = q0 + i * 32 + lane;
-            if (r < M) same = same && group_of(r) == b;
-        }
-        same = __all_sync(0xffffffffu, same);
-        if (lane == 0) {
-            g.tile_adapter[t] = !same ? -2 : (b < L ? b : -1);
-            if (same && b < L) flag[b] = 1;
-        }
-    }
-    __syncthreads();
-    const int used = a < L ? flag[a] : 0;
-    const int slot = block_prefix(used, warp_sum, all);
-    if (used && SG_IN_RANGE(slot < g.slots)) g.slot_adapter[slot] = a;
-    if (a < L) flag[a] = slot;
-    for (int s = all + threadIdx.x; s < g.slots; s += SORT_THREADS) g.slot_adapter[s] = -1;
-    __syncthreads();
-    for (int t = threadIdx.x; t < tiles; t += SORT_THREADS) {
-        const int b = g.tile_adapter[t];
-        if (b >= 0) g.tile_adapter[t] = flag[b];
-    }
 }
 
-// The parts of the slots' adapters, planes part * slots + slot of rows x cols, zero
-// past the adapter's rank (RANK_ROWS: the rank runs down the rows, else along them).
-template <class T, bool RANK_ROWS>
+// The parts of the used adapters for the rank-side planes: plane part * L + a of width x
+// cols, zero past the adapter's rank, and in unclean[a] whether one of its values is not
+// finite.  TRANS: V_a is stored cols x R.  A block to 64 columns of an adapter.
+template <class T, bool TRANS>
 __global__ void __launch_bounds__(256)
-    pack_stack_kernel(int rows, int cols, Stack<const T> V, Adapters ad, const int *slot_adapter,
-                      int slots, Parts to) {
+    pack_stack_kernel(int cols, Stack<const T> V, Adapters ad, const int *used, int width, int *unclean, Parts to) {
     constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
-    const int slot = blockIdx.y, a = slot_adapter[slot];
-    if (a < 0) return;
-    const int rank = ad.rank(a), per_row = (cols + 7) / 8;
+    __shared__ float tile[128][65];
+    const int a = blockIdx.y, c0 = blockIdx.x * 64;
+    if (!used[a]) return;
+    const int rank = ad.rank(a), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const T *v = V.matrix(a);
+    bool finite = true;
+    if (TRANS) {   // lanes along the rank
+        for (int c = warp; c < 64; c += 8)
+            for (int r = lane; r < width; r += 32) {
+                const float x = c0 + c < cols && r < rank ? to_f32(v[(c0 + c) * V.ld + r]) : 0.0f;
+                finite = finite && isfinite(x);
+                tile[r][c] = x;
+            }
+    } else {
+        for (int r = warp; r < width; r += 8)
+            for (int c = lane; c < 64; c += 32) {
+                const float x = c0 + c < cols && r < rank ? to_f32(v[r * V.ld + c0 + c]) : 0.0f;
+                finite = finite && isfinite(x);
+                tile[r][c] = x;
+            }
+    }
+    if (!finite) unclean[a] = 1;
+    __syncthreads();
     Parts at = to;
-    at.p += slot * to.plane;
-    at.plane = to.plane * slots;
-    const long long total = (long long)rows * per_row;
-    for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < total;
-         t += (long long)gridDim.x * 256) {
-        const long long i = t / per_row;
-        const int c = int(t - i * per_row) * 8;
+    at.p += a * to.plane;
+    at.plane = to.plane * ad.L;
+    for (int o = threadIdx.x; o < width * 8; o += 256) {
+        const int r = o / 8, c = (o % 8) * 8;
+        if (c0 + c >= cols) continue;
         float x[8];
 #pragma unroll
-        for (int d = 0; d < 8; ++d)
-            x[d] = (c + d < cols && (RANK_ROWS ? i : c + d) < rank) ? to_f32(v[i * V.ld + c + d]) : 0.0f;
-        store_parts<PARTS>(at, i, c, x);
+        for (int d = 0; d < 8; ++d) x[d] = tile[r][c + d];
+        store_parts<PARTS>(at, r, c0 + c, x);
     }
 }
 

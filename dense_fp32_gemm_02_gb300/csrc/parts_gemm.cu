@@ -81,8 +81,8 @@ Split sgp::plan_split(int M, int N, int K, int products, int sms) {
 }
 
 template <class T, bool TRANS>
-int sgp::finish(int M, int N, int splits, const float *partial, const Epilogue<T, TRANS> &epi,
-                cudaStream_t stream) {
+int sgp::finish(int M, int N, int splits, const float *partial, const int2 *planes,
+                const Epilogue<T, TRANS> &epi, cudaStream_t stream) {
     // grid rows are at most 65535 to a launch
     for (long long r = 0; r < M; r += 65535) {
         const int rows = int(std::min<long long>(65535, M - r));
@@ -91,7 +91,7 @@ int sgp::finish(int M, int N, int splits, const float *partial, const Epilogue<T
         at.S += r * at.lds;
         at.out += r * at.ldo;
         finish_kernel<<<dim3(unsigned((N + 255) / 256), unsigned(rows)), 256, 0, stream>>>(
-            M, N, splits, partial + r * N, at);
+            M, N, splits, partial + r * N, planes, int(r), at);
         sgh::count_launch();
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return sgh::cuda_fail(e);
@@ -116,7 +116,6 @@ int sgp::run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Spl
     kp.slabs = int((p.K + BK - 1LL) / BK);
     kp.splits = split.splits;
     kp.per_split = (kp.slabs + split.splits - 1) / split.splits;
-    kp.slots = p.slots;
     kp.partial = partial;
     kp.timeout_ns = sgh::wait_timeout_ns();
     CUtensorMap mA, mB, mH, mV;
@@ -125,11 +124,14 @@ int sgp::run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Spl
         return st;
     mH = mA;
     mV = mB;
-    if (p.h.p && split.splits == 1) {
-        kp.tile_adapter = p.tile_adapter;
-        kp.rank_slabs = (epi.ad.R + BK - 1) / BK;
+    if (p.planes) {
+        kp.planes = p.planes;
+        kp.plane_adapter = p.plane_adapter;
+        kp.capacity = p.capacity;
+        kp.width = p.width;
+        kp.L = epi.ad.L;
         if ((st = encode(&mH, p.h, BK, ROWS)) != SGEMM_OK ||
-            (st = encode(&mV, p.v, BK, K::B_MN ? BK : ROWS)) != SGEMM_OK)
+            (st = encode(&mV, p.v, BK, uint32_t(std::min(p.width, BK)))) != SGEMM_OK)
             return st;
     }
     const long long pairs = std::min<long long>(tiles_m * tiles_n * split.splits * (split.splits == 1 ? 2 : 1),
@@ -139,7 +141,8 @@ int sgp::run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Spl
                              : "bf16, tcgen05 cta_group::2, 256x256 pair tiles");
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return sgh::cuda_fail(e);
-    if (split.splits > 1) return finish<T, LAYOUT == INPUT_GRAD>(p.M, p.N, split.splits, partial, epi, stream);
+    if (split.splits > 1) 
+        return finish<T, LAYOUT == INPUT_GRAD>(p.M, p.N, split.splits, partial, p.planes, epi, stream);
     return SGEMM_OK;
 }
 
@@ -155,7 +158,8 @@ LAYER_PRODUCT(float, WEIGHT_GRAD);
 LAYER_PRODUCT(bf16, WEIGHT_GRAD);
 #undef LAYER_PRODUCT
 #define LAYER_FINISH(T, TRANS) \
-    template int finish<T, TRANS>(int, int, int, const float *, const Epilogue<T, TRANS> &, cudaStream_t)
+    template int finish<T, TRANS>(int, int, int, const float *, const int2 *,                    \
+                                  const Epilogue<T, TRANS> &, cudaStream_t)
 LAYER_FINISH(float, false);
 LAYER_FINISH(bf16, false);
 LAYER_FINISH(float, true);

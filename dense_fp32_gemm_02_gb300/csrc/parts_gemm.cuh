@@ -23,10 +23,10 @@
 // One part: two accumulators of 256 columns, the next tile's MMAs run under this
 // tile's epilogue.  Several: main and small, the next chunk's small pairs run while
 // the main accumulator is read.
-// A tile whose rows share an adapter gets the rank-side term as more slabs of the
-// same loop; one of mixed rows by FMAs in the epilogue, row by row: in an MMA a row
-// would meet another row's adapter times zero, which is NaN where that holds an
-// infinity or a NaN.
+// The rank-side term is more slabs of the same loop: a row's sums stand in the columns
+// of its own adapter and zeros in those of the tile's others.  Zero times an adapter's
+// value is nothing, unless that is an infinity or a NaN: a tile with such an adapter
+// takes the term by FMAs in the epilogue, each row from its own adapter alone.
 // Waits are bounded as in tf32x3_pair.cuh, whose abort protocol this is.
 #pragma once
 
@@ -55,9 +55,9 @@ struct KernelParams {
     int tiles_m, tiles_n, group_m;
     int slabs;              // of 64 k
     int splits, per_split;  // slabs of each range but the last
-    int rank_slabs;         // 64-deep slabs of the rank
-    int slots;              // adapters of the packed stack
-    const int *tile_adapter;
+    const int2 *planes;     // of the rank side, see Product (null: none)
+    const int4 *plane_adapter;
+    int capacity, width, L;
     float *partial;         // splits x M x N, or null
     unsigned long long timeout_ns;
 };
@@ -108,7 +108,8 @@ struct Items {
         mine = mine_full + (q < halves ? (halves - 1 - q) / Q + 1 : 0);
     }
     struct Item {
-        int tm, col0, ncols, split, slab0, slabs, adapter;
+        int tm, col0, ncols, split, slab0, slabs;
+        int2 planes;   // the rank side's, of the first range only
     };
     __device__ Item item(const KernelParams &p, int j) const {
         const int Q = gridDim.x / 2, q = blockIdx.x / 2;
@@ -132,7 +133,7 @@ struct Items {
         }
         it.slab0 = it.split * p.per_split;
         it.slabs = min(p.per_split, p.slabs - it.slab0);
-        it.adapter = p.tile_adapter ? p.tile_adapter[it.tm] : -1;
+        it.planes = p.planes && it.split == 0 ? p.planes[it.tm] : make_int2(0, 0);
         return it;
     }
 };
@@ -150,7 +151,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     constexpr uint32_t STAGE = (PA + PB) * PART_BYTES;
     constexpr int STAGES = int(SMEM_RING / STAGE);
     constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(A_MN) << 15) |
-                               (uint32_t(B_MN) << 16) | (uint32_t(TILE >> 4) << 24);
+                               (uint32_t(TILE >> 4) << 24);
 
     extern __shared__ unsigned char smem_raw[];
     const uintptr_t base = (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023);
@@ -194,8 +195,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     Items items;
     items.init(p);
     const uint32_t ring = smem_addr(reinterpret_cast<void *>(base));
-    // rank-side slabs: with one part a side, the two parts of S one after the other
-    const int extra = SEVERAL ? p.rank_slabs : 2 * p.rank_slabs;
+    // slabs of an item, the rank side's after the product's: with one part a side, the two
+    // parts of S are planes one after the other
+    auto slabs_of = [](const Items::Item &it) {
+        return it.slabs + max(it.planes.y, 0) * (SEVERAL ? 1 : 2);
+    };
 
     if (warp == 0) {
         // ================================================================ copies (both CTAs)
@@ -208,7 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const Items::Item it = items.item(p, j);
                 const int arow = it.tm * TILE + int(rank) * ROWS;
                 const int bcol = it.col0 + int(rank) * (it.ncols / 2);
-                const int slabs = it.slabs + (it.adapter >= 0 ? extra : 0);
+                const int slabs = slabs_of(it);
                 for (int s = 0; s < slabs; ++s) {
                     if (*abort_flag) break;
                     // first use of a stage: parity 1 counts as complete
@@ -243,23 +247,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                             }
                         }
                     } else if constexpr (!A_MN) {
-                        const int e = s - it.slabs;
-                        const int r = (SEVERAL ? e : e % p.rank_slabs) * BK;
+                        const int e = s - it.slabs, part = SEVERAL ? 0 : e / it.planes.y;
+                        const int plane = it.planes.x + (SEVERAL ? e : e % it.planes.y);
 #pragma unroll
                         for (int q = 0; q < PA; ++q)
-                            tma_load_3d_pair(st + uint32_t(q) * PART_BYTES, &mH, fb, r, arow,
-                                             SEVERAL ? q : e / p.rank_slabs);
+                            tma_load_3d_pair(st + uint32_t(q) * PART_BYTES, &mH, fb, 0, int(rank) * ROWS,
+                                             (part + q) * p.capacity + plane);
+                        const int4 of = p.plane_adapter[plane];
+                        const int deep = min(p.width, BK);   // rank columns of an adapter in this plane
 #pragma unroll
-                        for (int q = 0; q < PB; ++q) {
-                            const uint32_t at = st + uint32_t(PA + q) * PART_BYTES;
-                            const int plane = q * p.slots + it.adapter;
-                            if constexpr (B_MN) {
-                                tma_load_3d_pair(at, &mV, fb, bcol, r, plane);
-                                tma_load_3d_pair(at + GROUP_BYTES, &mV, fb, bcol + 64, r, plane);
-                            } else {
-                                tma_load_3d_pair(at, &mV, fb, r, bcol, plane);
+                        for (int q = 0; q < PB; ++q)
+                            for (int u = 0; u * deep < BK; ++u) {
+                                const uint32_t at =
+                                    st + uint32_t(PA + q) * PART_BYTES + uint32_t(u * deep) * 128u;
+                                const int a = u == 0 ? of.x : u == 1 ? of.y : u == 2 ? of.z : of.w;
+                                const int r = deep == BK ? of.y : 0;
+                                tma_load_3d_pair(at, &mV, fb, bcol, r, q * p.L + a);
+                                tma_load_3d_pair(at + GROUP_BYTES, &mV, fb, bcol + 64, r, q * p.L + a);
                             }
-                        }
                     }
                     ++issued;
                     if (++stage == STAGES) {
@@ -289,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             for (int j = 0; j < items.mine && ok; ++j) {
                 const Items::Item it = items.item(p, j);
                 const uint32_t idesc = IDESC | (uint32_t(it.ncols >> 3) << 17);
-                const int slabs = it.slabs + (it.adapter >= 0 ? extra : 0);
+                const int slabs = slabs_of(it);
                 const int a = SEVERAL ? 0 : j & 1;
                 const uint32_t main_acc = taddr + uint32_t(a) * ACC_COLUMNS;
                 // one part: this tile's accumulator; several: the small pairs'
@@ -304,10 +309,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     tc_fence_after();
                     const uint32_t sa = ring + uint32_t(stage) * STAGE;
                     const uint32_t sb = sa + uint32_t(PA) * PART_BYTES;
+                    const bool rank_side = s >= it.slabs;   // (its stack is MN-major)
                     auto mma = [&](uint32_t d, int qa, int qb, int kk, bool accumulate) {
+                        const uint32_t b = sb + uint32_t(qb) * PART_BYTES;
+                        const bool mn = B_MN || rank_side;
                         mma_bf16_pair(d, part_desc<A_MN>(sa + uint32_t(qa) * PART_BYTES, kk),
-                                      part_desc<B_MN>(sb + uint32_t(qb) * PART_BYTES, kk), idesc,
-                                      accumulate);
+                                      mn ? part_desc<true>(b, kk) : part_desc<false>(b, kk),
+                                      idesc | (uint32_t(mn) << 16), accumulate);
                     };
                     if constexpr (SEVERAL) {
                         const uint32_t small = taddr + ACC_COLUMNS;
@@ -376,7 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const int width = it.ncols / 2;               // this warp's columns: 128 or 64
             const int row0 = it.tm * TILE + int(rank) * ROWS + quarter * 32;
             const int col0 = it.col0 + half * width;
-            const bool fma_expand = it.adapter == -2 && p.partial == nullptr;
+            const bool fma_expand = it.planes.y < 0 && p.partial == nullptr;
 
             auto write = [&](int c, const float (&v)[32]) {   // columns col0 + 32 c ..
                 __syncwarp();
@@ -417,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             };
 
             if constexpr (SEVERAL) {
-                const int slabs = it.slabs + (it.adapter >= 0 ? extra : 0);
+                const int slabs = slabs_of(it);
                 float sum[4][32];
                 for (int s = 0; s < slabs && ok; s += CHUNK, ++chunk) {
                     if (!(ok = wait_full(0, chunk))) break;
@@ -485,7 +493,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 // The ranges' partial sums added in order, and the epilogue; a thread to an element.
 template <class T, bool TRANS>
 __global__ void __launch_bounds__(256)
-    finish_kernel(int M, int N, int splits, const float *__restrict__ partial, Epilogue<T, TRANS> epi) {
+    finish_kernel(int M, int N, int splits, const float *__restrict__ partial, const int2 *planes, int row0,
+                  Epilogue<T, TRANS> epi) {
     const long long i = blockIdx.y;
     const int j = blockIdx.x * 256 + threadIdx.x;
     if (j >= N) return;
@@ -495,7 +504,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll 8
     for (int s = 0; s < splits; ++s) sum += partial[s * plane + i * N + j];
     x += sum;
-    const int a = epi.ad.of_row(i);
+    const int a = planes && planes[(row0 + i) / TILE].y >= 0 ? -1 : epi.ad.of_row(i);
     if (a >= 0) {
         const int n = epi.ad.rank(a);
         const float *S = epi.S + i * epi.lds;

@@ -32,15 +32,16 @@ struct Epilogue {
 };
 
 // out (M x N) = a * b over a contraction K.  a is M x K stored K-major (inner = K) or
-// M-major (inner = M), b likewise.  The rank-side term of tiles whose rows share one
-// adapter is taken by the tensor cores: `h` the parts of S (inner R), `v` the parts
-// of `slots` adapters as planes part * slots + slot, stored like b; `tile_adapter` has
-// for each 256 rows the slot of their common adapter, -1 (none) or -2 (several).
+// M-major (inner = M), b likewise.  The rank-side term joins the product as more of its
+// contraction, 64 columns at a time: `h` the planes of 256 x 64 that sgl::Groups
+// describes (part * capacity + plane), `v` the adapters' parts (part * L + a, `width` x
+// N).  A tile that has no planes gets the term by FMAs from S and the caller's stack.
 struct Product {
     int M, N, K;
     Operand a, b, h, v;
-    int slots = 0;
-    const int *tile_adapter = nullptr;
+    const int2 *planes = nullptr;
+    const int4 *plane_adapter = nullptr;
+    int capacity = 0, width = 64;
 };
 
 enum Layout { FORWARD, INPUT_GRAD, WEIGHT_GRAD };   // (a, b): (K, N)-major, (K, K), (M, N)
@@ -59,8 +60,9 @@ int run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Split sp
         int sms, cudaStream_t stream);
 
 // The second kernel alone: out from `splits` partial sums (none: the epilogue of zero).
+// Rows of tiles that have planes already have their rank-side term (planes null: none).
 template <class T, bool TRANS>
-int finish(int M, int N, int splits, const float *partial, const Epilogue<T, TRANS> &epi,
+int finish(int M, int N, int splits, const float *partial, const int2 *planes, const Epilogue<T, TRANS> &epi,
            cudaStream_t stream);
 
 int set_up();   // the kernels' attributes on the current device (its first call)

@@ -135,6 +135,12 @@ __device__ __forceinline__ void cp_async4(uint32_t smem_dst, const void *src, ui
                  "r"(src_bytes)
                  : "memory");
 }
+// The 16-byte form (both addresses 16-byte aligned): src_bytes are read, the rest zero-filled.
+__device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void *src, uint32_t src_bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(src),
+                 "r"(src_bytes)
+                 : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
     asm volatile("cp.async.commit_group;" ::: "memory");
 }

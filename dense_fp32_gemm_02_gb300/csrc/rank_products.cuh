@@ -5,15 +5,15 @@
 // One side of each is at most 128 wide, so both are bound by reading X once (R = 16:
 // 16 flop per byte of bfloat16), and their rows lie anywhere in X.  So the warp-level
 // MMA (m16n8k16, bfloat16, fp32 accumulators) is fast enough: its operands come from
-// shared memory that plain loads fill row by row, from any alignment, converting on
-// the way: a float32 element as three bfloat16 parts, a checkpoint's as one (see
-// parts_gemm.cuh for the parts).
+// shared memory that asynchronous copies fill row by row, from any alignment, several
+// slabs ahead.  A float32 element becomes three bfloat16 parts on its way into the MMA's
+// registers, a checkpoint's element one (see parts_gemm.cuh for the parts).
 //
 // A block only ever holds rows of one adapter, and of its stack the columns below its
 // rank: nothing of another adapter is multiplied, not even by zero.
 //
-// The MMA's additions truncate, so a slab's products (64 of the contraction; the small
-// pairs of parts first) add up from zero and then go to fp32 sums, round to nearest:
+// The MMA's additions truncate, so a slab's products (64 of the contraction) add up from
+// zero, the small pairs of parts apart, and then go to fp32 sums, round to nearest:
 // four additions of full size to a slab truncate, 5e-7 at most.
 #pragma once
 
@@ -23,13 +23,13 @@ namespace sgl {
 
 constexpr int SLAB = 64;              // of the contraction
 constexpr int RANK_THREADS = 256;
-constexpr int PITCH64 = SLAB + 8;     // elements: rows 16 bytes past a multiple of 128
 
 __device__ __forceinline__ uint32_t shared_address(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 template <bool TRANSPOSE>
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const bf16 *p) {
+    const uint32_t at = shared_address(p);
     if constexpr (TRANSPOSE)
         asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
@@ -45,245 +45,326 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Eight elements as PARTS planes of shared memory, `plane` elements apart.
-template <int PARTS>
-__device__ __forceinline__ void stage8(bf16 *to, int plane, const float (&x)[8]) {
-    store_parts<PARTS>(Parts{to, 0, plane}, 0, 0, x);
+// Two elements as a packed pair of each of three parts.
+__device__ __forceinline__ void pair_parts(float x, float y, uint32_t (&part)[3]) {
+    float px[3], py[3];
+    split_parts(x, px);
+    split_parts(y, py);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) part[q] = pack_bf16(px[q], py[q]);
 }
 
-// What the rank side leaves behind: S (M x R, scaled), the same as parts where
-// `parts.p` is not null, and unscaled for the caller in H.
-struct RankSide {
-    float *S;
-    long long lds;
-    float *H;
-    long long ldh;
-    Parts parts;
-
-    template <class T>
-    __device__ void put(long long i, int r, float sum, float scale) const {
-        if (H) H[i * ldh + r] = sum;
-        const float s = sum * scale;
-        S[i * lds + r] = s;
-        if (parts.p) {
-            float part[3];
-            split_parts(s, part);
-            // (bfloat16: two parts, 2^-16, under the output's rounding)
-            for (int q = 0; q < (sizeof(T) == 4 ? 3 : 2); ++q)
-                parts.p[q * parts.plane + i * parts.pitch + r] = __float2bfloat16_rn(part[q]);
-        }
+// 16 bytes of shared memory from `n` elements at p (the rest zero): an asynchronous copy
+// where p is 16-byte aligned, four of them for float32, else (bfloat16) loads and a store.
+template <class T>
+__device__ __forceinline__ void fill16(T *to, const T *p, int n, bool wide) {
+    constexpr int PER = 16 / int(sizeof(T));
+    n = max(0, min(PER, n));
+    if (wide) {
+        sg::cp_async16(shared_address(to), p, uint32_t(n) * sizeof(T));
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int d = 0; d < PER; ++d) sg::cp_async4(shared_address(to + d), d < n ? p + d : p, d < n ? 4u : 0u);
+    } else {
+        T x[PER];
+#pragma unroll
+        for (int d = 0; d < PER; ++d) x[d] = d < n ? p[d] : T(0.0f);
+        *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(x);
     }
-};
+}
 
-// S of one tile of up to 64 rows of a group (blockIdx.x) over one range of the
-// contraction (blockIdx.y): 8 warps, 16 rows x half of the rank each.  NT: the rank in
-// units of 8, rounded up to 2, 4, 8 or 16.  TRANS: V_a is stored R x C.  With one
-// range the results go to `to`, otherwise to partial[range][row][R].
+// ------------------------------------------------------------------ rank side
+// Sums of one tile of up to 64 rows of a group (blockIdx.x) over one range of the
+// contraction (blockIdx.y), to partial[range][row][R]: 8 warps, 16 rows x half of the
+// rank each.  NT: the rank in units of 8, rounded up to 2, 4, 8 or 16.  TRANS: V_a is
+// stored R x C.  Pitches are such that no fragment load meets a bank conflict.
 template <class T, bool TRANS, int NT>
 struct RankTile {
-    static constexpr int PARTS = sizeof(T) == 4 ? 3 : 1, WN = NT / 2, RP = NT * 8;
-    static constexpr int X_PLANE = ROW_TILE * PITCH64;
-    static constexpr int V_ROWS = TRANS ? RP : SLAB, V_PITCH = TRANS ? PITCH64 : RP + 8;
-    static constexpr int V_PLANE = V_ROWS * V_PITCH;
-    static constexpr size_t SMEM = size_t(PARTS) * (X_PLANE + V_PLANE) * 2;
+    static constexpr bool F32 = sizeof(T) == 4;
+    static constexpr int WN = NT / 2, RP = NT * 8, STAGES = F32 ? 3 : 4;
+    static constexpr int X_PITCH = SLAB + 8, X_ELEMS = ROW_TILE * X_PITCH;
+    static constexpr int V_PITCH = TRANS ? SLAB + 8 : (F32 ? RP + 4 : RP + 8);
+    static constexpr int V_ELEMS = (TRANS ? RP : SLAB) * V_PITCH;
+    static constexpr size_t SMEM = size_t(STAGES) * (X_ELEMS + V_ELEMS) * sizeof(T);
 };
 
 template <class T, bool TRANS, int NT>
 __global__ void __launch_bounds__(RANK_THREADS)
     rank_tile_kernel(int C, int range, Rows<T> X, bool x_wide, Stack<const T> V, bool v_wide, Adapters ad,
-                     Groups g, float *partial, long long partial_plane, RankSide to) {
+                     Groups g, float *partial, long long partial_plane) {
     using Z = RankTile<T, TRANS, NT>;
-    constexpr int PARTS = Z::PARTS, WN = Z::WN;
-    constexpr int VO = Z::V_ROWS * (TRANS ? SLAB : Z::RP) / 8;            // octets of the V slab
-    constexpr int VN = (VO + RANK_THREADS - 1) / RANK_THREADS;
+    constexpr int WN = Z::WN, PER = 16 / int(sizeof(T)), STAGES = Z::STAGES;
     extern __shared__ __align__(16) unsigned char smem_rank[];
-    bf16 *xs = reinterpret_cast<bf16 *>(smem_rank), *vs = xs + PARTS * Z::X_PLANE;
+    T *ring = reinterpret_cast<T *>(smem_rank);
     __shared__ int rows[ROW_TILE];
     if (int(blockIdx.x) >= g.totals[0]) return;
     const int4 tile = g.tiles[blockIdx.x];
     const int a = tile.x, n = tile.z;
+    if (a < 0) return;
     if (threadIdx.x < ROW_TILE) rows[threadIdx.x] = int(threadIdx.x) < n ? g.perm[tile.y + threadIdx.x] : -1;
     __syncthreads();
-    if (a < 0) {   // rows without an adapter: only the caller's H shows them
-        if (to.H && blockIdx.y == 0)
-            for (int t = threadIdx.x; t < n * ad.R; t += RANK_THREADS)
-                to.H[(long long)rows[t / ad.R] * to.ldh + t % ad.R] = 0.0f;
-        return;
-    }
     const int rank = ad.rank(a);
     const T *v = V.matrix(a);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wm = warp & 3, wn = warp >> 2;
     const int c_begin = blockIdx.y * range, c_end = min(C, c_begin + range);
 
-    float xv[2][8], vv[VN][8];
-    auto load = [&](int c0) {
+    auto fill = [&](int stage, int c0) {
+        T *xs = ring + stage * (Z::X_ELEMS + Z::V_ELEMS), *vs = xs + Z::X_ELEMS;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {   // 64 rows x 8 octets
-            const int o = threadIdx.x + h * RANK_THREADS, i = rows[o / 8], c = c0 + (o % 8) * 8;
-            if (i >= 0 && x_wide && c + 8 <= c_end) {
-                X.at8(i, c, xv[h]);
-            } else {
-#pragma unroll
-                for (int d = 0; d < 8; ++d) xv[h][d] = (i >= 0 && c + d < c_end) ? X.at(i, c + d) : 0.0f;
-            }
+        for (int o = threadIdx.x; o < ROW_TILE * SLAB / PER; o += RANK_THREADS) {
+            const int m = o / (SLAB / PER), c = (o % (SLAB / PER)) * PER, i = rows[m];
+            fill16(xs + m * Z::X_PITCH + c, i < 0 ? X.p : X.p + i * X.ld + c0 + c, i < 0 ? 0 : c_end - c0 - c, x_wide);
         }
-#pragma unroll
-        for (int h = 0; h < VN; ++h) {
-            const int o = threadIdx.x + h * RANK_THREADS;
-            if (VO % RANK_THREADS != 0 && o >= VO) break;
-            constexpr int PER = (TRANS ? SLAB : Z::RP) / 8;
-            const int row = o / PER, col = (o % PER) * 8;
-            // (TRANS: row is r and col c - c0; else row is c - c0 and col r)
-            const int cs = TRANS ? c0 + col : c0 + row, r = TRANS ? row : col;
-            const T *p = v + (TRANS ? (long long)r * V.ld + cs : (long long)cs * V.ld + r);
-            const bool whole = TRANS ? r < rank && cs + 8 <= c_end : r + 8 <= rank && cs < c_end;
-            if (whole && v_wide) {
-                load8(p, vv[h]);
-            } else {
-#pragma unroll
-                for (int d = 0; d < 8; ++d)
-                    vv[h][d] = (TRANS ? r < rank && cs + d < c_end : r + d < rank && cs < c_end) ? to_f32(p[d]) : 0.0f;
-            }
+        constexpr int ALONG = (TRANS ? SLAB : Z::RP) / PER;
+        for (int o = threadIdx.x; o < (TRANS ? Z::RP : SLAB) * ALONG; o += RANK_THREADS) {
+            const int row = o / ALONG, col = (o % ALONG) * PER;
+            if (TRANS)
+                fill16(vs + row * Z::V_PITCH + col, row < rank ? v + row * V.ld + c0 + col : v,
+                       row < rank ? c_end - c0 - col : 0, v_wide);
+            else
+                fill16(vs + row * Z::V_PITCH + col, c0 + row < c_end && col < rank ? v + (c0 + row) * V.ld + col : v,
+                       c0 + row < c_end ? rank - col : 0, v_wide);
         }
     };
 
     float sum[WN][4] = {};
-    load(c_begin);
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) {
+        if (c_begin + s * SLAB < c_end) fill(s, c_begin + s * SLAB);
+        sg::cp_async_commit();
+    }
+    int stage = 0;
     for (int c0 = c_begin; c0 < c_end; c0 += SLAB) {
-        __syncthreads();
+        sg::cp_async_wait<STAGES - 2>();
+        __syncthreads();   // this slab has landed, and the stage filled next has been read
+        if (c0 + (STAGES - 1) * SLAB < c_end) fill((stage + STAGES - 1) % STAGES, c0 + (STAGES - 1) * SLAB);
+        sg::cp_async_commit();
+        const T *xs = ring + stage * (Z::X_ELEMS + Z::V_ELEMS), *vs = xs + Z::X_ELEMS;
+        float big[WN][4] = {}, small[WN][4] = {};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int o = threadIdx.x + h * RANK_THREADS;
-            stage8<PARTS>(xs + (o / 8) * PITCH64 + (o % 8) * 8, Z::X_PLANE, xv[h]);
-        }
-#pragma unroll
-        for (int h = 0; h < VN; ++h) {
-            const int o = threadIdx.x + h * RANK_THREADS;
-            if (VO % RANK_THREADS != 0 && o >= VO) break;
-            constexpr int PER = (TRANS ? SLAB : Z::RP) / 8;
-            stage8<PARTS>(vs + (o / PER) * Z::V_PITCH + (o % PER) * 8, Z::V_PLANE, vv[h]);
-        }
-        __syncthreads();
-        if (c0 + SLAB < c_end) load(c0 + SLAB);
-        float acc[WN][4] = {};
-        auto products = [&](int qa, int qb) {
-#pragma unroll
-            for (int kk = 0; kk < SLAB; kk += 16) {
-                uint32_t fa[4];
-                ldmatrix4<false>(fa, shared_address(xs + qa * Z::X_PLANE + (wm * 16 + (lane & 15)) * PITCH64 + kk +
-                                                    (lane >> 4) * 8));
+        for (int kk = 0; kk < SLAB; kk += 16) {
+            if constexpr (!Z::F32) {
+                uint32_t fa[4], fb[4];
+                ldmatrix4<false>(fa, xs + (wm * 16 + (lane & 15)) * Z::X_PITCH + kk + (lane >> 4) * 8);
 #pragma unroll
                 for (int t = 0; t < WN; t += 2) {
-                    const int n0 = (wn * WN + t) * 8;
-                    uint32_t fb[4];
-                    const bf16 *at = vs + qb * Z::V_PLANE;
+                    const int n0 = (wn * WN + t) * 8, second = WN > 1 ? ((lane >> 4) & 1) * 8 : 0;
                     if constexpr (TRANS)
-                        at += (n0 + (lane & 7) + (WN > 1 ? ((lane >> 4) & 1) * 8 : 0)) * PITCH64 + kk + ((lane >> 3) & 1) * 8;
+                        ldmatrix4<false>(fb, vs + (n0 + (lane & 7) + second) * Z::V_PITCH + kk + ((lane >> 3) & 1) * 8);
                     else
-                        at += (kk + (lane & 15)) * Z::V_PITCH + n0 + (WN > 1 ? ((lane >> 4) & 1) * 8 : 0);
-                    ldmatrix4<!TRANS>(fb, shared_address(at));
-                    mma16816(acc[t], fa, fb[0], fb[1]);
-                    if constexpr (WN > 1) mma16816(acc[t + 1], fa, fb[2], fb[3]);
+                        ldmatrix4<true>(fb, vs + (kk + (lane & 15)) * Z::V_PITCH + n0 + second);
+                    mma16816(big[t], fa, fb[0], fb[1]);
+                    if constexpr (WN > 1) mma16816(big[t + 1], fa, fb[2], fb[3]);
+                }
+            } else {
+                const int gr = lane >> 2, t2 = (lane & 3) * 2;
+                uint32_t fa[3][4];
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    const float2 x = *reinterpret_cast<const float2 *>(
+                        xs + (wm * 16 + gr + (d & 1) * 8) * Z::X_PITCH + kk + t2 + (d >> 1) * 8);
+                    uint32_t part[3];
+                    pair_parts(x.x, x.y, part);
+                    fa[0][d] = part[0], fa[1][d] = part[1], fa[2][d] = part[2];
+                }
+#pragma unroll
+                for (int t = 0; t < WN; ++t) {
+                    const int nn = (wn * WN + t) * 8 + gr;
+                    uint32_t fb[2][3];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int k = kk + t2 + h * 8;
+                        float x, y;
+                        if constexpr (TRANS) {
+                            const float2 w = *reinterpret_cast<const float2 *>(vs + nn * Z::V_PITCH + k);
+                            x = w.x, y = w.y;
+                        } else {
+                            x = vs[k * Z::V_PITCH + nn], y = vs[(k + 1) * Z::V_PITCH + nn];
+                        }
+                        pair_parts(x, y, fb[h]);
+                    }
+                    mma16816(small[t], fa[0], fb[0][2], fb[1][2]);
+                    mma16816(small[t], fa[2], fb[0][0], fb[1][0]);
+                    mma16816(small[t], fa[1], fb[0][1], fb[1][1]);
+                    mma16816(small[t], fa[0], fb[0][1], fb[1][1]);
+                    mma16816(small[t], fa[1], fb[0][0], fb[1][0]);
+                    mma16816(big[t], fa[0], fb[0][0], fb[1][0]);
                 }
             }
-        };
-        if constexpr (PARTS == 3) {
-            products(0, 2), products(2, 0), products(1, 1), products(0, 1), products(1, 0);
         }
-        products(0, 0);
 #pragma unroll
         for (int t = 0; t < WN; ++t)
 #pragma unroll
-            for (int d = 0; d < 4; ++d) sum[t][d] += acc[t][d];
+            for (int d = 0; d < 4; ++d) sum[t][d] += Z::F32 ? big[t][d] + small[t][d] : big[t][d];
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
-    const float scale = ad.scale(a);
+    float *out = partial + blockIdx.y * partial_plane;
 #pragma unroll
     for (int t = 0; t < WN; ++t)
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
             const int m = wm * 16 + (lane >> 2) + (d / 2) * 8, r = (wn * WN + t) * 8 + (lane & 3) * 2 + (d & 1);
-            if (m >= n || r >= ad.R) continue;
-            const long long i = rows[m];
-            if (gridDim.y > 1)
-                partial[blockIdx.y * partial_plane + i * ad.R + r] = sum[t][d];
-            else
-                to.put<T>(i, r, sum[t][d], scale);
+            if (m < n && r < ad.R) out[(long long)rows[m] * ad.R + r] = sum[t][d];
         }
 }
 
-// The ranges' partial sums of the rank side, added in order.
+// What the rank side leaves behind: S (M x R, scaled), unscaled for the caller in H, and
+// S's parts in the planes of Groups (float32: three, bfloat16: two, 2^-16, which is under
+// the output's rounding).  H and planes may be null.
+struct RankSide {
+    float *S, *H;
+    long long ldh;
+    bf16 *planes;
+};
+
+// The ranges' partial sums of the rank side added in order, a warp to a row.  A row whose
+// adapter holds something that is not finite takes its tile's planes away.
 template <class T>
 __global__ void __launch_bounds__(256)
-    rank_finish_kernel(int M, int ranges, const float *__restrict__ partial, long long plane, Adapters ad,
-                       RankSide to) {
-    const long long total = (long long)M * ad.R;
-    for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < total; t += (long long)gridDim.x * 256) {
-        const long long i = t / ad.R;
-        const int a = ad.of_row(i);
-        if (a < 0 || ad.rank(a) == 0) continue;
+    rank_finish_kernel(int M, int ranges, const float *__restrict__ partial, long long partial_plane, Adapters ad,
+                       Groups g, const int *unclean, RankSide to) {
+    constexpr int PARTS = sizeof(T) == 4 ? 3 : 2;
+    __shared__ float own[8][128];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long i = (long long)blockIdx.x * 8 + warp;
+    if (i >= M) return;
+    const int a = ad.of_row(i), rank = a < 0 ? 0 : ad.rank(a);
+    const float scale = a < 0 ? 0.0f : ad.scale(a);
+    for (int r = lane; r < ad.R; r += 32) {
         float sum = 0.0f;
+        if (r < rank) {
 #pragma unroll 8
-        for (int s = 0; s < ranges; ++s) sum += partial[s * plane + t];
-        to.put<T>(i, int(t - i * ad.R), sum, ad.scale(a));
+            for (int s = 0; s < ranges; ++s) sum += partial[s * partial_plane + i * ad.R + r];
+        }
+        if (to.H) to.H[i * to.ldh + r] = sum;
+        const float scaled = r < rank ? sum * scale : 0.0f;
+        to.S[i * ad.R + r] = scaled;
+        own[warp][r] = scaled;
+    }
+    if (!to.planes) return;
+    const int2 planes = g.planes[i / 256];
+    if (rank > 0 && unclean[a]) {
+        if (lane == 0) atomicExch(&g.planes[i / 256].y, NO_PLANES);
+        return;
+    }
+    __syncwarp();
+    const int first = g.position[i] * g.width;
+    for (int s = 0; s < planes.y; ++s) {
+        const int r = s * 64 + 2 * lane - first;
+        const float x = r >= 0 && r < rank ? own[warp][r] : 0.0f;
+        const float y = r + 1 >= 0 && r + 1 < rank ? own[warp][r + 1] : 0.0f;
+        uint32_t part[3];
+        pair_parts(x, y, part);
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q)
+            *reinterpret_cast<uint32_t *>(
+                to.planes + (((long long)q * g.capacity + planes.x + s) * 256 + i % 256) * 64 + 2 * lane) = part[q];
     }
 }
 
+// ------------------------------------------------------------------ stack gradients
 // X^T * S over a chunk of rows of a group (blockIdx.y), 128 columns of X (blockIdx.x):
 // 8 warps, 16 columns x the whole rank each.  partial[chunk] is C x R, or R x C where
-// RANK_ROWS.  S (and whether it still is to be scaled) as the rank side left it.
-template <class X, int PA, int PB, int NT>
-struct StackTile {
-    static constexpr int COLS = 128, X_PITCH = COLS + 8, S_PITCH = NT * 8 + 8;
-    static constexpr int X_PLANE = SLAB * X_PITCH, S_PLANE = SLAB * S_PITCH;
-    static constexpr size_t SMEM = size_t(PA * X_PLANE + PB * S_PLANE) * 2;
+// RANK_ROWS.  S (and whether it still is to be scaled) as the rank side left it; its
+// parts are made once per block, on the way through registers.
+template <class X>
+struct ElementOf;
+template <class T>
+struct ElementOf<Rows<T>> {
+    using type = T;
+    static constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
+};
+template <>
+struct ElementOf<Act8Rows> {
+    using type = signed char;
+    static constexpr int PARTS = 1;
 };
 
-template <class X, int PA, int PB, int NT, bool RANK_ROWS>
+template <class X, int PB, int NT>
+struct StackTile {
+    using E = typename ElementOf<X>::type;
+    static constexpr int PA = ElementOf<X>::PARTS;
+    static constexpr int COLS = 128, STAGES = sizeof(E) == 4 ? 3 : 4;
+    // float32: rows 4 banks apart; bfloat16 and q: 16 bytes past a multiple of 128
+    static constexpr int X_PITCH = COLS + (sizeof(E) == 4 ? 4 : 16 / int(sizeof(E)));
+    static constexpr int X_ELEMS = SLAB * X_PITCH, S_PITCH = NT * 8 + 8, S_PLANE = SLAB * S_PITCH;
+    static constexpr size_t SMEM = size_t(STAGES) * X_ELEMS * sizeof(E) + size_t(PB) * S_PLANE * 2 +
+                                   (sizeof(E) == 1 ? size_t(STAGES) * SLAB * 4 : 0);
+};
+
+template <class X, int PB, int NT, bool RANK_ROWS>
 __global__ void __launch_bounds__(RANK_THREADS)
     stack_tile_kernel(int C, X x, bool x_wide, const float *S, long long lds, bool scaled, Adapters ad, Groups g,
                       float *partial) {
-    using Z = StackTile<X, PA, PB, NT>;
+    using Z = StackTile<X, PB, NT>;
+    using E = typename Z::E;
+    constexpr int PA = Z::PA, PER = 16 / int(sizeof(E)), STAGES = Z::STAGES;
     constexpr int SN = (SLAB * NT + RANK_THREADS - 1) / RANK_THREADS;
     extern __shared__ __align__(16) unsigned char smem_rank[];
-    bf16 *xs = reinterpret_cast<bf16 *>(smem_rank), *ss = xs + PA * Z::X_PLANE;
+    E *ring = reinterpret_cast<E *>(smem_rank);
+    bf16 *ss = reinterpret_cast<bf16 *>(ring + STAGES * Z::X_ELEMS);
+    signed char *es = reinterpret_cast<signed char *>(ss + PB * Z::S_PLANE);   // checkpoints: 4 exponents a row
     if (int(blockIdx.y) >= g.totals[1]) return;
     const int4 chunk = g.chunks[blockIdx.y];
     const int a = chunk.x, n = chunk.z, c0 = blockIdx.x * Z::COLS, rank = ad.rank(a);
+    const int *perm = g.perm + chunk.y;
     const float scale = scaled ? 1.0f : ad.scale(a);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
-    float xv[4][8], sv[SN][8];
-    auto load = [&](int i0) {
+    auto fill = [&](int stage, int i0) {
+        E *xs = ring + stage * Z::X_ELEMS;
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {   // 64 rows x 16 octets
-            const int o = threadIdx.x + h * RANK_THREADS, m = i0 + o / 16, c = c0 + (o % 16) * 8;
-            const int i = m < n ? g.perm[chunk.y + m] : -1;
-            if (i >= 0 && x_wide && c + 8 <= C) {
-                x.at8(i, c, xv[h]);
+        for (int o = threadIdx.x; o < SLAB * Z::COLS / PER; o += RANK_THREADS) {
+            const int m = o / (Z::COLS / PER), c = (o % (Z::COLS / PER)) * PER;
+            const bool in = i0 + m < n && c0 + c < C;
+            const long long i = in ? perm[i0 + m] : 0;
+            if constexpr (sizeof(E) == 1) {
+                E *to = xs + m * Z::X_PITCH + c;
+                const E *p = x.q + i * x.ldq + c0 + c;
+                const int count = in ? min(PER, C - c0 - c) : 0;
+                if (x_wide) {
+                    sg::cp_async16(shared_address(to), in ? p : x.q, uint32_t(count));
+                } else {
+                    E b[PER];
+#pragma unroll
+                    for (int d = 0; d < PER; ++d) b[d] = d < count ? p[d] : E(0);
+                    *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(b);
+                }
             } else {
-#pragma unroll
-                for (int d = 0; d < 8; ++d) xv[h][d] = (i >= 0 && c + d < C) ? x.at(i, c + d) : 0.0f;
+                fill16(xs + m * Z::X_PITCH + c, in ? x.p + i * x.ld + c0 + c : x.p, in ? C - c0 - c : 0, x_wide);
             }
         }
+        if constexpr (sizeof(E) == 1) {
+            const int m = threadIdx.x / 4, block = c0 / ACT8_BLOCK + threadIdx.x % 4;
+            const bool in = i0 + m < n && block * ACT8_BLOCK < C;
+            es[stage * SLAB * 4 + threadIdx.x] = in ? x.e[perm[i0 + m] * x.lde + block] : E(0);
+        }
+    };
+    float sv[SN][8];
+    auto load_s = [&](int i0) {
 #pragma unroll
         for (int h = 0; h < SN; ++h) {   // 64 rows x NT octets
             const int o = threadIdx.x + h * RANK_THREADS, m = i0 + o / NT, r = (o % NT) * 8;
             const bool in = o < SLAB * NT && m < n;
-            const long long at = in ? g.perm[chunk.y + m] * lds : 0;
+            const float *p = S + (in ? perm[m] * lds : 0) + r;
 #pragma unroll
-            for (int d = 0; d < 8; ++d) sv[h][d] = in && r + d < rank ? S[at + r + d] * scale : 0.0f;
+            for (int d = 0; d < 8; ++d) sv[h][d] = in && r + d < rank ? p[d] * scale : 0.0f;
         }
     };
 
     float sum[NT][4] = {};
-    load(0);
-    for (int i0 = 0; i0 < n; i0 += SLAB) {
-        __syncthreads();
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            const int o = threadIdx.x + h * RANK_THREADS;
-            stage8<PA>(xs + (o / 16) * Z::X_PITCH + (o % 16) * 8, Z::X_PLANE, xv[h]);
-        }
+    for (int s = 0; s < STAGES - 1; ++s) {
+        if (s * SLAB < n) fill(s, s * SLAB);
+        sg::cp_async_commit();
+    }
+    load_s(0);
+    int stage = 0;
+    for (int i0 = 0; i0 < n; i0 += SLAB) {
+        sg::cp_async_wait<STAGES - 2>();
+        __syncthreads();   // this slab has landed; the last one's fragments have been read
+        if (i0 + (STAGES - 1) * SLAB < n) fill((stage + STAGES - 1) % STAGES, i0 + (STAGES - 1) * SLAB);
+        sg::cp_async_commit();
 #pragma unroll
         for (int h = 0; h < SN; ++h) {
             const int o = threadIdx.x + h * RANK_THREADS;
@@ -299,36 +380,60 @@ __global__ void __launch_bounds__(RANK_THREADS)
                                    pack_bf16(part[4][q], part[5][q]), pack_bf16(part[6][q], part[7][q]));
             }
         }
+        if (i0 + SLAB < n) load_s(i0 + SLAB);
         __syncthreads();
-        if (i0 + SLAB < n) load(i0 + SLAB);
+        const E *xs = ring + stage * Z::X_ELEMS;
         float acc[NT][4] = {};
-        auto products = [&](int qa, int qb) {
+        // the columns' fragment of part qa at rows kk .. kk + 15: element (column, row)
+        auto columns = [&](uint32_t (&fa)[PA][4], int kk) {
+            if constexpr (sizeof(E) == 2) {
+                ldmatrix4<true>(fa[0], reinterpret_cast<const bf16 *>(xs) +
+                                           (kk + (lane & 7) + ((lane >> 4) & 1) * 8) * Z::X_PITCH + warp * 16 +
+                                           ((lane >> 3) & 1) * 8);
+            } else {
 #pragma unroll
-            for (int kk = 0; kk < SLAB; kk += 16) {
-                uint32_t fa[4];
-                ldmatrix4<true>(fa, shared_address(xs + qa * Z::X_PLANE +
-                                                   (kk + (lane & 7) + ((lane >> 4) & 1) * 8) * Z::X_PITCH +
-                                                   warp * 16 + ((lane >> 3) & 1) * 8));
-#pragma unroll
-                for (int t = 0; t < NT; t += 2) {
-                    uint32_t fb[4];
-                    ldmatrix4<true>(fb, shared_address(ss + qb * Z::S_PLANE + (kk + (lane & 15)) * Z::S_PITCH + t * 8 +
-                                                       ((lane >> 4) & 1) * 8));
-                    mma16816(acc[t], fa, fb[0], fb[1]);
-                    mma16816(acc[t + 1], fa, fb[2], fb[3]);
+                for (int d = 0; d < 4; ++d) {
+                    const int k = kk + (lane & 3) * 2 + (d >> 1) * 8, c = warp * 16 + (lane >> 2) + (d & 1) * 8;
+                    if constexpr (sizeof(E) == 4) {
+                        uint32_t part[3];
+                        pair_parts(xs[k * Z::X_PITCH + c], xs[(k + 1) * Z::X_PITCH + c], part);
+                        fa[0][d] = part[0], fa[1][d] = part[1], fa[2][d] = part[2];
+                    } else {
+                        const signed char *e = es + stage * SLAB * 4 + k * 4 + warp / 2;
+                        fa[0][d] = pack_bf16(float(xs[k * Z::X_PITCH + c]) * act8_step(e[0]),
+                                             float(xs[(k + 1) * Z::X_PITCH + c]) * act8_step(e[4]));
+                    }
                 }
             }
         };
+        // small pairs of parts first, so that what truncates at full size is the last pair's
 #pragma unroll
-        for (int rest = 2; rest > 0; --rest)
+        for (int pass = PB > 1 ? 0 : 1; pass < 2; ++pass) {
 #pragma unroll
-            for (int qa = 0; qa <= rest; ++qa)
-                if (qa < PA && rest - qa < PB) products(qa, rest - qa);
-        products(0, 0);
+            for (int kk = 0; kk < SLAB; kk += 16) {
+                uint32_t fa[PA][4];
+                columns(fa, kk);
+#pragma unroll
+                for (int qb = pass == 0 ? PB - 1 : 0; qb >= 0; --qb)
+#pragma unroll
+                    for (int t = 0; t < NT; t += 2) {
+                        uint32_t fb[4];
+                        ldmatrix4<true>(fb, ss + qb * Z::S_PLANE + (kk + (lane & 15)) * Z::S_PITCH + t * 8 +
+                                                ((lane >> 4) & 1) * 8);
+#pragma unroll
+                        for (int qa = PA - 1; qa >= 0; --qa)
+                            if (pass == 0 ? (qa + qb > 0 && qa + qb <= 2) : qa == 0) {
+                                mma16816(acc[t], fa[qa], fb[0], fb[1]);
+                                mma16816(acc[t + 1], fa[qa], fb[2], fb[3]);
+                            }
+                    }
+            }
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int d = 0; d < 4; ++d) sum[t][d] += acc[t][d];
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
     float *out = partial + (long long)blockIdx.y * C * ad.R;
 #pragma unroll
