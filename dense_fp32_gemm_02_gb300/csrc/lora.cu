@@ -6,6 +6,7 @@
 #include "host_state.h"
 #include "parts_gemm.h"
 #include "rank_products.cuh"
+#include "rows.cuh"
 #include "variant.cuh"
 
 #define SGEMM_API extern "C" __attribute__((visibility("default")))
@@ -343,11 +344,60 @@ int projection(const Call &c, const Grouping &gr, float *S, float *H, int ldh, v
     return ws.release();
 }
 
+// ------------------------------------------------------------------ few rows
+template <class T, int MT>
+int few_rows_mt(const RowsWork &w, unsigned blocks, Rows<T> X, const T *W, int ldw, Stack<const T> A, const Adapters &ad,
+                cudaStream_t stream) {
+    auto kernel = few_rows_kernel<T, MT>;
+    constexpr size_t smem = FewRows<T, MT>::SMEM;
+    const int st = shared_limit(kernel, smem);
+    if (st != SGEMM_OK) return st;
+    kernel<<<blocks, RANK_THREADS, smem, stream>>>(w, X, W, ldw, wide_rows(W, ldw), A, ad);
+    return launched("few rows, W read once, k split over the grid");
+}
+
+// A forward call of at most FEW_ROWS rows.
+template <class T>
+int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
+    RowsWork w{};
+    w.M = c.M, w.N = c.N, w.K = c.K;
+    w.across = (c.N + ROWS_COLS - 1) / ROWS_COLS;
+    // two blocks per SM; ranges of whole slabs, their partial sums (8 bytes of traffic per
+    // row and column) at most half of what W takes
+    const long long most = std::max(1LL, (long long)c.K * (long long)sizeof(T) / (16LL * c.M));
+    const long long want = std::min<long long>({(2LL * sms + w.across - 1) / w.across, most, (c.K + 127LL) / 128});
+    w.range = int(((c.K + want - 1) / want + SLAB - 1) / SLAB * SLAB);
+    w.ranges = (c.K + w.range - 1) / w.range;
+    const bool ranked = c.L > 0;
+    w.rank_ranges = ranked ? std::max(1, (c.K + 511) / 512) : 0;
+    w.rank_range = ranked ? (c.K + w.rank_ranges - 1) / w.rank_ranges : 0;
+    w.rank_ranges = ranked ? (c.K + w.rank_range - 1) / w.rank_range : 0;
+    const size_t p_floats = size_t(w.ranges) * c.M * c.N, r_floats = size_t(w.rank_ranges) * c.M * c.R;
+    sgh::Workspace ws(pool, c.stream);
+    int st = ws.allocate(sgh::Workspace::piece(p_floats * 4) + sgh::Workspace::piece(r_floats * 4));
+    if (st != SGEMM_OK) return st;
+    w.partial = ws.take<float>(p_floats);
+    w.rank_partial = ws.take<float>(r_floats);
+    const Adapters ad = c.adapters();
+    const Rows<T> X{static_cast<const T *>(c.X), c.ldx};
+    auto run = c.M <= 16 ? few_rows_mt<T, 1> : c.M <= 32 ? few_rows_mt<T, 2> : few_rows_mt<T, 4>;
+    const long long blocks = (long long)w.across * w.ranges + (long long)c.M * w.rank_ranges;
+    if (blocks > 0x7fffffffLL) return SGEMM_ERR_TOO_LARGE;
+    st = run(w, unsigned(blocks), X, static_cast<const T *>(c.W), c.ldw, stack_of<T>(c.A, c.lda, c.stride_a), ad, c.stream);
+    if (st != SGEMM_OK) return st;
+    few_rows_finish_kernel<T><<<dim3(unsigned((c.N + 255) / 256), unsigned(c.M)), 256, 0, c.stream>>>(
+        w, stack_of<T>(c.B, c.ldb, c.stride_b), ad, static_cast<const T *>(c.bias), c.H, c.ldh,
+        static_cast<T *>(c.Y), c.ldy);
+    if ((st = launched()) != SGEMM_OK) return st;
+    return ws.release();
+}
+
 template <class T>
 int forward(const Call &c) {
     int sms, st;
     cudaMemPool_t pool;
     if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
+    if (c.M <= FEW_ROWS && c.K > 0 && c.N > 0) return forward_few_rows<T>(c, sms, pool);
     sgh::Workspace ws(pool, c.stream);
     Grouping gr(c, 0, sms);
     if (c.L > 0 && ((st = ws.allocate(gr.bytes())) != SGEMM_OK || (st = gr.make(ws, c.adapters(), c.stream)) != SGEMM_OK))
