@@ -295,74 +295,95 @@ def sgemm_host(A, B, C, alpha: float = 1.0, beta: float = 0.0, stream=None, devi
 ACT8_BLOCK = 32   # columns of a row that share an exponent of an 8-bit checkpoint
 
 
-def _layer_type(first, *named):
-    """The sgemm_type of the (name, tensor) pairs, None tensors left out: CUDA
-    tensors of one type, float32 or bfloat16, on one device."""
+# A decode step makes one such call per projection, so the checks below are written for
+# the calls that pass them: what is wrong is worked out only once something is.
+def _layer_type(names, *tensors):
+    """(sgemm_type, device number) of CUDA tensors (or None, past the first) of one type,
+    float32 or bfloat16, on one device."""
     import torch
-    named = [(n, t) for n, t in (first, *named) if t is not None]
-    for name, t in named:
+    first = tensors[0]
+    try:
+        dtype, device = first.dtype, first.get_device()
+        for t in tensors:
+            if t is not None and (t.dtype is not dtype or t.get_device() != device):
+                break
+        else:
+            if device >= 0:
+                if dtype is torch.float32:
+                    return 0, device
+                if dtype is torch.bfloat16:
+                    return 1, device
+    except AttributeError:
+        pass
+    for name, t in zip(names, tensors):
+        if t is None and t is not first:
+            continue
         if not isinstance(t, torch.Tensor) or not t.is_cuda or \
                 t.dtype not in (torch.float32, torch.bfloat16):
             raise TypeError(f"{name} must be a CUDA float32 or bfloat16 tensor")
-        if t.dtype != named[0][1].dtype:
-            raise TypeError(f"{name} must have the type of {named[0][0]}, {named[0][1].dtype}")
-    _on_device(named[0][1].device, *named)
-    return 1 if named[0][1].dtype == torch.bfloat16 else 0
+        if t.dtype != first.dtype:
+            raise TypeError(f"{name} must have the type of {names[0]}, {first.dtype}")
+    raise ValueError(", ".join(names) + " must be on one device")
 
 
-def _on_device(device, *named):
-    for name, t in named:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}")
-
-
-def _typed(name, t, dtype, shape, device):
-    """TypeError / ValueError unless t is a CUDA tensor of this type, shape and device."""
+def _typed(name, t, dtype, device):
+    """TypeError / ValueError unless t is a tensor of this type on CUDA device number `device`."""
+    try:
+        if t.dtype is dtype and t.get_device() == device:
+            return
+    except AttributeError:
+        pass
     import torch
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA {str(dtype).replace('torch.', '')} tensor")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    _on_device(device, (name, t))
+    raise ValueError(f"{name} must be on cuda:{device}")
 
 
 def _vector(name, t, dtype, n, device):
     """Address of a contiguous vector of n elements, or None."""
     if t is None:
         return None
-    _typed(name, t, dtype, (n,), device)
+    _typed(name, t, dtype, device)
+    if t.shape != (n,):
+        raise ValueError(f"{name} must be {(n,)}, got {tuple(t.shape)}")
     if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _pitch(rows, cols, row_stride, col_stride):
+    if cols > 1 and col_stride != 1 and rows > 0:
+        raise ValueError("rows must be contiguous (stride(-1) == 1)")
+    return max(row_stride if rows > 1 else 0, cols, 1)
 
 
 def _matrix(name, t, rows, cols):
     """(address, row pitch) of a rows x cols row-major view; (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be {(rows, cols)}, got {tuple(t.shape)}")
-    return t.data_ptr(), _ld(t, cols)
+    return t.data_ptr(), _pitch(rows, cols, *t.stride())
 
 
 def _stack(name, t, count, rows, cols):
     """(address, row pitch, matrix stride) of count x rows x cols; (None, 0, 0) for None."""
     if t is None:
         return None, 0, 0
-    if t.dim() != 3 or tuple(t.shape) != (count, rows, cols):
+    if t.shape != (count, rows, cols):
         raise ValueError(f"{name} must be {(count, rows, cols)}, got {tuple(t.shape)}")
     if count == 0:
         return None, max(cols, 1), 0
-    return t.data_ptr(), _ld(t[0], cols), (t.stride(0) if count > 1 else 0)
+    stride, row_stride, col_stride = t.stride()
+    return t.data_ptr(), _pitch(rows, cols, row_stride, col_stride), stride if count > 1 else 0
 
 
 def _checkpoint(q, e, rows, cols, device):
     """(address, pitch, address, pitch) of an 8-bit checkpoint of a rows x cols matrix."""
     import torch
-    blocks = -(-cols // ACT8_BLOCK)
-    _typed("q", q, torch.int8, (rows, cols), device)
-    _typed("e", e, torch.int8, (rows, blocks), device)
-    return (*_matrix("q", q, rows, cols), *_matrix("e", e, rows, blocks))
+    _typed("q", q, torch.int8, device)
+    _typed("e", e, torch.int8, device)
+    return (*_matrix("q", q, rows, cols), *_matrix("e", e, rows, -(-cols // ACT8_BLOCK)))
 
 
 def _adapters(A, B, ids, M, scale, ranks, device):
@@ -380,6 +401,17 @@ def _adapters(A, B, ids, M, scale, ranks, device):
             _vector("scale", scale, torch.float32, L, device))
 
 
+def _call(device, stream, fn, *args):
+    """fn(*args, stream) with CUDA device number `device` current, on `stream` or torch's
+    current stream of that device."""
+    import torch
+    handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == device:
+        return check(fn(*args, handle))
+    with torch.cuda.device(device):
+        return check(fn(*args, handle))
+
+
 def lora_into(X, W, A, B, ids, Y, scale=None, ranks=None, bias=None, H=None, stream=None):
     """Y[i] <- X[i]@W + bias + scale[a]*(X[i]@A[a])@B[a] with a = ids[i]: the adapters
     of many requests beside one projection, for one token up to a long prefill.
@@ -391,21 +423,17 @@ def lora_into(X, W, A, B, ids, Y, scale=None, ranks=None, bias=None, H=None, str
     where given, receives X[i]@A[a] for lora_backward_into().  Asynchronous on `stream`
     (default: torch's current stream)."""
     import torch
-    kind = _layer_type(("X", X), ("W", W), ("A", A), ("B", B), ("Y", Y), ("bias", bias))
-    M, N, K = _shapes(X, W, Y)
-    L, R, ids_p, ranks_p, scale_p = _adapters(A, B, ids, M, scale, ranks, Y.device)
-    a = _stack("A", A, L, K, R)
-    b = _stack("B", B, L, R, N)
-    h = (None, 0)
+    kind, device = _layer_type(("X", "W", "A", "B", "Y", "bias"), X, W, A, B, Y, bias)
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError("X and W must be 2-D")
+    (M, K), N = X.shape, W.shape[1]
+    L, R, ids_p, ranks_p, scale_p = _adapters(A, B, ids, M, scale, ranks, device)
     if H is not None:
-        _typed("H", H, torch.float32, (M, R), Y.device)
-        h = _matrix("H", H, M, R)
-    bias_p = _vector("bias", bias, Y.dtype, N, Y.device)
-    with torch.cuda.device(Y.device):
-        st = lib.sgemm_lora(kind, M, N, K, L, R, X.data_ptr(), _ld(X, K), W.data_ptr(), _ld(W, N),
-                            *a, *b, ids_p, ranks_p, scale_p, bias_p, *h, Y.data_ptr(), _ld(Y, N),
-                            _stream_handle(stream, Y.device))
-    check(st)
+        _typed("H", H, torch.float32, device)
+    _call(device, stream, lib.sgemm_lora, kind, M, N, K, L, R, *_matrix("X", X, M, K),
+          *_matrix("W", W, K, N), *_stack("A", A, L, K, R), *_stack("B", B, L, R, N), ids_p, ranks_p,
+          scale_p, _vector("bias", bias, Y.dtype, N, device), *_matrix("H", H, M, R),
+          *_matrix("Y", Y, M, N))
     return Y
 
 
@@ -420,30 +448,20 @@ def lora_backward_into(dY, X, W, A, B, ids, H, dX=None, dA=None, dB=None, scale=
     dB (L, R, N) may be None together.  Returns (dX, dA, dB)."""
     import torch
     kept = isinstance(X, tuple)
-    kind = _layer_type(("dY", dY), ("X", None if kept else X), ("W", W), ("A", A), ("B", B),
-                       ("dX", dX), ("dA", dA), ("dB", dB))
+    kind, device = _layer_type(("dY", "X", "W", "A", "B", "dX", "dA", "dB"), dY, None if kept else X,
+                               W, A, B, dX, dA, dB)
     if (dA is None) != (dB is None):
         raise ValueError("dA and dB must be given together")
-    if W.dim() != 2:
-        raise ValueError("W must be 2-D")
-    K, N = W.shape
-    M = dY.shape[0]
-    device = dY.device
+    if dY.dim() != 2 or W.dim() != 2:
+        raise ValueError("dY and W must be 2-D")
+    M, (K, N) = dY.shape[0], W.shape
     L, R, ids_p, ranks_p, scale_p = _adapters(A, B, ids, M, scale, ranks, device)
-    dy, w = _matrix("dY", dY, M, N), _matrix("W", W, K, N)
-    if kept:
-        x, c = (None, 0), _checkpoint(*X, M, K, device)
-    else:
-        x, c = _matrix("X", X, M, K), (None, 0, None, 0)
-    a, b = _stack("A", A, L, K, R), _stack("B", B, L, R, N)
-    _typed("H", H, torch.float32, (M, R), device)
-    h = _matrix("H", H, M, R)
-    dx = _matrix("dX", dX, M, K)
-    da, db = _stack("dA", dA, L, K, R), _stack("dB", dB, L, R, N)
-    with torch.cuda.device(device):
-        st = lib.sgemm_lora_backward(kind, M, N, K, L, R, *dy, *x, *c, *w, *a, *b, ids_p, ranks_p,
-                                     scale_p, *h, *dx, *da, *db, _stream_handle(stream, device))
-    check(st)
+    _typed("H", H, torch.float32, device)
+    x = (None, 0, *_checkpoint(*X, M, K, device)) if kept else (*_matrix("X", X, M, K), None, 0, None, 0)
+    _call(device, stream, lib.sgemm_lora_backward, kind, M, N, K, L, R, *_matrix("dY", dY, M, N), *x,
+          *_matrix("W", W, K, N), *_stack("A", A, L, K, R), *_stack("B", B, L, R, N), ids_p, ranks_p,
+          scale_p, *_matrix("H", H, M, R), *_matrix("dX", dX, M, K), *_stack("dA", dA, L, K, R),
+          *_stack("dB", dB, L, R, N))
     return dX, dA, dB
 
 
@@ -455,76 +473,60 @@ def act8_empty(M: int, K: int, device=None):
             torch.empty((M, -(-K // ACT8_BLOCK)), dtype=torch.int8, device=device))
 
 
+def _act_number(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def _sizes(name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return t.shape
+
+
 def act8_store_into(Z, q, e, act: str = "none", Y=None, stream=None):
     """(q, e) <- the 8-bit checkpoint of Z (M, K): for each block of 32 columns of a row
     an exponent e and q = rint(z / 2^e) in int8.  With Y, also Y <- act(Z) in the same
     pass (Y may be Z).  Returns (q, e)."""
-    import torch
-    kind = _layer_type(("Z", Z), ("Y", Y))
-    if act not in ACTIVATIONS:
-        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
-    if act != "none" and Y is None:
+    kind, device = _layer_type(("Z", "Y"), Z, Y)
+    number = _act_number(act)
+    if number and Y is None:
         raise ValueError("an activation needs an output Y")
-    if Z.dim() != 2:
-        raise ValueError("Z must be 2-D")
-    M, K = Z.shape
-    c = _checkpoint(q, e, M, K, Z.device)
-    z, y = _matrix("Z", Z, M, K), _matrix("Y", Y, M, K)
-    with torch.cuda.device(Z.device):
-        st = lib.sgemm_act8_store(kind, M, K, *z, ACTIVATIONS[act], *c, *y,
-                                  _stream_handle(stream, Z.device))
-    check(st)
+    M, K = _sizes("Z", Z)
+    _call(device, stream, lib.sgemm_act8_store, kind, M, K, *_matrix("Z", Z, M, K), number,
+          *_checkpoint(q, e, M, K, device), *_matrix("Y", Y, M, K))
     return q, e
 
 
 def act8_load_into(q, e, X, stream=None):
     """X <- the values q * 2^e that a checkpoint stands for."""
-    import torch
-    kind = _layer_type(("X", X))
-    if X.dim() != 2:
-        raise ValueError("X must be 2-D")
-    M, K = X.shape
-    c = _checkpoint(q, e, M, K, X.device)
-    with torch.cuda.device(X.device):
-        st = lib.sgemm_act8_load(kind, M, K, *c, *_matrix("X", X, M, K),
-                                 _stream_handle(stream, X.device))
-    check(st)
+    kind, device = _layer_type(("X",), X)
+    M, K = _sizes("X", X)
+    _call(device, stream, lib.sgemm_act8_load, kind, M, K, *_checkpoint(q, e, M, K, device),
+          *_matrix("X", X, M, K))
     return X
 
 
 def act8_grad_into(q, e, dY, dZ, act: str = "none", stream=None):
     """dZ <- dY * act'(z), z the values of the checkpoint (q, e) of the activation's
     input (dZ may be dY)."""
-    import torch
-    kind = _layer_type(("dY", dY), ("dZ", dZ))
-    if act not in ACTIVATIONS:
-        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
-    if dY.dim() != 2:
-        raise ValueError("dY must be 2-D")
-    M, K = dY.shape
-    c = _checkpoint(q, e, M, K, dY.device)
-    dy, dz = _matrix("dY", dY, M, K), _matrix("dZ", dZ, M, K)
-    with torch.cuda.device(dY.device):
-        st = lib.sgemm_act8_grad(kind, M, K, *c, ACTIVATIONS[act], *dy, *dz,
-                                 _stream_handle(stream, dY.device))
-    check(st)
+    kind, device = _layer_type(("dY", "dZ"), dY, dZ)
+    number = _act_number(act)
+    M, K = _sizes("dY", dY)
+    _call(device, stream, lib.sgemm_act8_grad, kind, M, K, *_checkpoint(q, e, M, K, device), number,
+          *_matrix("dY", dY, M, K), *_matrix("dZ", dZ, M, K))
     return dZ
 
 
 def act8_weight_grad_into(q, e, dY, dW, beta: float = 0.0, stream=None):
     """dW <- x.T@dY + beta*dW, x (M, K) the values of the checkpoint (q, e) of a layer's
     input, dY (M, N), dW (K, N)."""
-    import torch
-    kind = _layer_type(("dY", dY), ("dW", dW))
-    if dY.dim() != 2 or dW.dim() != 2:
-        raise ValueError("dY and dW must be 2-D")
-    (M, N), K = dY.shape, dW.shape[0]
-    c = _checkpoint(q, e, M, K, dY.device)
-    dy, dw = _matrix("dY", dY, M, N), _matrix("dW", dW, K, N)
-    with torch.cuda.device(dY.device):
-        st = lib.sgemm_act8_weight_grad(kind, M, N, K, *c, *dy, float(beta), *dw,
-                                        _stream_handle(stream, dY.device))
-    check(st)
+    kind, device = _layer_type(("dY", "dW"), dY, dW)
+    (M, N), K = _sizes("dY", dY), _sizes("dW", dW)[0]
+    _call(device, stream, lib.sgemm_act8_weight_grad, kind, M, N, K,
+          *_checkpoint(q, e, M, K, device), *_matrix("dY", dY, M, N), float(beta),
+          *_matrix("dW", dW, K, N))
     return dW
 
 
