@@ -33,6 +33,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// Four consecutive elements, aligned to their size together.
+__device__ __forceinline__ void load4(const float *p, float (&v)[4]) {
+    const float4 a = *reinterpret_cast<const float4 *>(p);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+}
+__device__ __forceinline__ void load4(const bf16 *p, float (&v)[4]) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
+}
+
 // Eight consecutive elements at a 16-byte aligned address.
 __device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
     const float4 a = *reinterpret_cast<const float4 *>(p);

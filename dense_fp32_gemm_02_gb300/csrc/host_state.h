@@ -39,6 +39,24 @@ cudaError_t parts_gemm_error_word(unsigned *v, bool clear);
 // Largest size that an entry point accepts.
 constexpr int kMaxDim = 0x7fffffff - 0xffff;
 
+// A launch that need not wait for the kernel before it on the stream (programmatic stream
+// serialization): the kernel itself waits where it has to.
+template <class... P, class... Args>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+                         const Args &...args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // Workspace of one call: `bytes` from the device's pool, handed out in
 // 256-byte aligned pieces, given back to it on `stream` at the end of the call.
 class Workspace {

@@ -345,51 +345,143 @@ int projection(const Call &c, const Grouping &gr, float *S, float *H, int ldh, v
 }
 
 // ------------------------------------------------------------------ few rows
-template <class T, int MT>
-int few_rows_mt(const RowsWork &w, unsigned blocks, Rows<T> X, const T *W, int ldw, Stack<const T> A, const Adapters &ad,
-                cudaStream_t stream) {
-    auto kernel = few_rows_kernel<T, MT>;
-    constexpr size_t smem = FewRows<T, MT>::SMEM;
-    const int st = shared_limit(kernel, smem);
-    if (st != SGEMM_OK) return st;
-    kernel<<<blocks, RANK_THREADS, smem, stream>>>(w, X, W, ldw, wide_rows(W, ldw), A, ad);
-    return launched("few rows, W read once, k split over the grid");
+constexpr const char *kFewRows = "few rows, W read once, k split over the grid";
+
+template <class T>
+using StreamKernel = void (*)(RowsWork, Rows<T>, const T *, long long, Stack<const T>, Adapters);
+
+template <class T, bool WIDE>
+StreamKernel<T> stream_kernel(int M) {
+    return M <= 1   ? stream_rows_kernel<T, 1, WIDE>
+           : M <= 2 ? stream_rows_kernel<T, 2, WIDE>
+           : M <= 4 ? stream_rows_kernel<T, 4, WIDE>
+           : M <= 8 ? stream_rows_kernel<T, 8, WIDE>
+                    : stream_rows_kernel<T, 16, WIDE>;
 }
 
-// A forward call of at most FEW_ROWS rows.
+// The split of K over the grid: the count of ranges (whole `step`s, none above `longest`)
+// whose waves of blocks take the fewest steps, with two for filling and emptying; partial
+// sums (8 bytes of traffic per row and column) of at most half of what W takes.
+void split_rows(RowsWork &w, int cols, int step, int longest, long long slots, size_t element) {
+    w.across = (w.N + cols - 1) / cols;
+    const long long steps = (w.K + step - 1LL) / step;
+    const long long fewest = (w.K + (long long)longest - 1) / longest;
+    const long long most = std::max(fewest, std::min(steps, (long long)w.K * (long long)element / (16LL * w.M)));
+    long long least = 0;
+    for (long long n = fewest; n <= std::min(most, fewest + 64); ++n) {
+        const long long per = (steps + n - 1) / n;
+        const long long cost = ((w.across * n + slots - 1) / slots) * (per + 2);
+        if (n == fewest || cost < least) least = cost, w.range = int(per * step);
+    }
+    w.ranges = int((w.K + (long long)w.range - 1) / w.range);
+}
+
+// A forward call of few rows: see rows.cuh.
 template <class T>
 int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
+    constexpr bool F32 = sizeof(T) == 4;
+    const bool stream_rows = c.M <= STREAM_ROWS, mma_rows = F32 && !stream_rows, ranked = c.L > 0;
+    const T *W = static_cast<const T *>(c.W);
+    const bool w_wide = wide_rows(W, c.ldw);
+    const Adapters ad = c.adapters();
+    const Rows<T> X{static_cast<const T *>(c.X), c.ldx};
+    const Stack<const T> A = stack_of<T>(c.A, c.lda, c.stride_a), B = stack_of<T>(c.B, c.ldb, c.stride_b);
+    int st;
     RowsWork w{};
     w.M = c.M, w.N = c.N, w.K = c.K;
-    w.across = (c.N + ROWS_COLS - 1) / ROWS_COLS;
-    // two blocks per SM; ranges of whole slabs, their partial sums (8 bytes of traffic per
-    // row and column) at most half of what W takes
-    const long long most = std::max(1LL, (long long)c.K * (long long)sizeof(T) / (16LL * c.M));
-    const long long want = std::min<long long>({(2LL * sms + w.across - 1) / w.across, most, (c.K + 127LL) / 128});
-    w.range = int(((c.K + want - 1) / want + SLAB - 1) / SLAB * SLAB);
-    w.ranges = (c.K + w.range - 1) / w.range;
-    const bool ranked = c.L > 0;
-    w.rank_ranges = ranked ? std::max(1, (c.K + 511) / 512) : 0;
-    w.rank_range = ranked ? (c.K + w.rank_ranges - 1) / w.rank_ranges : 0;
-    w.rank_ranges = ranked ? (c.K + w.rank_range - 1) / w.rank_range : 0;
+    w.x_wide = aligned(c.X, 4 * sizeof(T)) && c.ldx % 4 == 0;
+    w.v_wide = wide_stack(A, c.L);
+    Packed<T> P(c.M, c.K, c.X, c.ldx), Q(c.K, c.N, c.W, c.ldw);   // (of the third kernel)
+    sgp::Split split{1, 0};
+    auto stream = w_wide ? stream_kernel<T, true>(c.M) : stream_kernel<T, false>(c.M);
+    long long slots = sms;
+    if (stream_rows) {
+        int per_sm = 1;
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stream, RANK_THREADS, 0);
+        if (e != cudaSuccess) return sgh::cuda_fail(e);
+        slots *= std::max(1, std::min(per_sm, 4));
+        split_rows(w, 32 * 16 / int(sizeof(T)), RANK_THREADS / 32 * STREAM_DEPTH, STREAM_RANGE, slots, sizeof(T));
+    } else if (mma_rows) {
+        slots *= c.M <= 32 ? 2 : 1;
+        split_rows(w, ROWS_COLS, SLAB, sgh::kMaxDim, slots, sizeof(T));
+    } else {
+        split = sgp::plan_split(c.M, c.N, c.K, 1, sms);
+        w.ranges = split.splits;
+    }
+    if (ranked) {
+        const int n = std::max(1, (c.K + 511) / 512);
+        w.rank_range = (c.K + n - 1) / n;
+        w.rank_ranges = (c.K + w.rank_range - 1) / w.rank_range;
+    }
     const size_t p_floats = size_t(w.ranges) * c.M * c.N, r_floats = size_t(w.rank_ranges) * c.M * c.R;
+    const bool third = !stream_rows && !mma_rows;
     sgh::Workspace ws(pool, c.stream);
-    int st = ws.allocate(sgh::Workspace::piece(p_floats * 4) + sgh::Workspace::piece(r_floats * 4));
+    st = ws.allocate(sgh::Workspace::piece(p_floats * 4) + sgh::Workspace::piece(r_floats * 4) +
+                     (third ? P.bytes() + Q.bytes() : 0));
     if (st != SGEMM_OK) return st;
     w.partial = ws.take<float>(p_floats);
     w.rank_partial = ws.take<float>(r_floats);
-    const Adapters ad = c.adapters();
-    const Rows<T> X{static_cast<const T *>(c.X), c.ldx};
-    auto run = c.M <= 16 ? few_rows_mt<T, 1> : c.M <= 32 ? few_rows_mt<T, 2> : few_rows_mt<T, 4>;
-    const long long blocks = (long long)w.across * w.ranges + (long long)c.M * w.rank_ranges;
-    if (blocks > 0x7fffffffLL) return SGEMM_ERR_TOO_LARGE;
-    st = run(w, unsigned(blocks), X, static_cast<const T *>(c.W), c.ldw, stack_of<T>(c.A, c.lda, c.stride_a), ad, c.stream);
+    const long long product = (long long)w.across * w.ranges, rank = (long long)c.M * w.rank_ranges;
+    if (product + rank > 0x7fffffffLL) return SGEMM_ERR_TOO_LARGE;
+    const bool together = stream_rows && product + rank <= slots;
+    if (third) {   // what the product reads has to be there before the kernel that it overtakes
+        P.place(ws);
+        Q.place(ws);
+        if ((st = P.pack(sms, c.stream)) != SGEMM_OK || (st = Q.pack(sms, c.stream)) != SGEMM_OK) return st;
+    }
+    const bool alone = !ranked || together;   // the product's is the first kernel of the call
+    if (!alone) {
+        few_rows_rank_kernel<T><<<unsigned(rank), RANK_THREADS, 0, c.stream>>>(w, X, A, ad);
+        if ((st = launched()) != SGEMM_OK) return st;
+    }
+    if (stream_rows) {
+        const dim3 grid(unsigned(product + (together ? rank : 0)));
+        if (alone) {
+            stream<<<grid, RANK_THREADS, 0, c.stream>>>(w, X, W, c.ldw, A, ad);
+        } else {
+            const cudaError_t e = sgh::launch_early(stream, grid, RANK_THREADS, 0, c.stream, w, X, W, c.ldw, A, ad);
+            if (e != cudaSuccess) return sgh::cuda_fail(e);
+        }
+        st = launched(kFewRows);
+    } else if constexpr (F32) {
+        auto kernel = c.M <= 32 ? few_rows_kernel<2> : few_rows_kernel<4>;
+        const size_t smem = c.M <= 32 ? FewRows<2>::SMEM : FewRows<4>::SMEM;
+        if ((st = shared_limit(kernel, smem)) != SGEMM_OK) return st;
+        if (alone) {
+            kernel<<<unsigned(product), RANK_THREADS, smem, c.stream>>>(w, X, W, c.ldw, w_wide);
+        } else {
+            const cudaError_t e = sgh::launch_early(kernel, dim3(unsigned(product)), RANK_THREADS, smem, c.stream, w, X, W,
+                                                    c.ldw, w_wide);
+            if (e != cudaSuccess) return sgh::cuda_fail(e);
+        }
+        st = launched(kFewRows);
+    } else {
+        sgp::Product g;
+        g.M = c.M, g.N = c.N, g.K = c.K;
+        g.a = P.operand();
+        g.b = Q.operand();
+        st = sgp::run<T, sgp::FORWARD>(g, sgp::Epilogue<T, false>{}, split, w.partial, sms, c.stream,
+                                       alone ? sgp::PARTIALS : sgp::PARTIALS_EARLY);
+    }
     if (st != SGEMM_OK) return st;
-    few_rows_finish_kernel<T><<<dim3(unsigned((c.N + 255) / 256), unsigned(c.M)), 256, 0, c.stream>>>(
-        w, stack_of<T>(c.B, c.ldb, c.stride_b), ad, static_cast<const T *>(c.bias), c.H, c.ldh,
-        static_cast<T *>(c.Y), c.ldy);
+    const T *bias = static_cast<const T *>(c.bias);
+    const bool wide = (!bias || aligned(bias, 16)) && wide_stack(B, c.L);
+    const dim3 grid(unsigned((c.N + 255) / 256), unsigned(c.M));
+    const cudaError_t e = sgh::launch_early(wide ? few_rows_finish_kernel<T, true> : few_rows_finish_kernel<T, false>,
+                                            grid, 256, 0, c.stream, w, B, ad, bias, c.N % 4 == 0, c.H, (long long)c.ldh,
+                                            static_cast<T *>(c.Y), (long long)c.ldy);
+    if (e != cudaSuccess) return sgh::cuda_fail(e);
     if ((st = launched()) != SGEMM_OK) return st;
     return ws.release();
+}
+
+// Few rows: their sums of the rank side are cheaper taken one by one than grouped by
+// adapter (five launches, 40 us) up to about 4096 of them.
+bool few_rows(const Call &c) {
+    if (c.K == 0 || c.N == 0) return false;
+    if (c.M <= STREAM_ROWS) return true;
+    const int most = c.type == SGEMM_F32 ? MMA_ROWS : FEW_ROWS;
+    return c.M <= most && (c.L == 0 || (long long)c.M * c.R <= 4096);
 }
 
 template <class T>
@@ -397,7 +489,7 @@ int forward(const Call &c) {
     int sms, st;
     cudaMemPool_t pool;
     if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
-    if (c.M <= FEW_ROWS && c.K > 0 && c.N > 0) return forward_few_rows<T>(c, sms, pool);
+    if (few_rows(c)) return forward_few_rows<T>(c, sms, pool);
     sgh::Workspace ws(pool, c.stream);
     Grouping gr(c, 0, sms);
     if (c.L > 0 && ((st = ws.allocate(gr.bytes())) != SGEMM_OK || (st = gr.make(ws, c.adapters(), c.stream)) != SGEMM_OK))

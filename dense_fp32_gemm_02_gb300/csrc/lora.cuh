@@ -37,15 +37,18 @@ struct Act8Rows {
 // leave (cut, not rounded: x = x0 + x1 + x2 exactly, and no part overflows).  What is
 // not finite stays in the first.
 __device__ __forceinline__ void split_parts(float x, float (&part)[3]) {
-    part[0] = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-    if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) {
-        if (x != x) part[0] = __uint_as_float(0x7fc00000u);
-        part[1] = part[2] = 0.0f;
-        return;
-    }
-    const float rest = x - part[0];
+    const float head = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+    float rest = x - head;
+    const bool finite = fabsf(rest) < 3.0e38f;   // not for an infinity or a NaN
+    rest = finite ? rest : 0.0f;
+    part[0] = finite ? head : x + x;             // (x + x: a NaN whose leading bits say so)
     part[1] = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
     part[2] = rest - part[1];
+}
+
+// Two floats that are bfloat16 already as a word (the first in the low half).
+__device__ __forceinline__ uint32_t pack_exact(float lo, float hi) {
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
 
 // Where the parts of a matrix go: `planes` apart, rows `pitch` apart (both multiples
@@ -72,8 +75,8 @@ __device__ __forceinline__ void store_parts(const Parts &to, long long row, long
 #pragma unroll
     for (int q = 0; q < PARTS; ++q)
         *reinterpret_cast<uint4 *>(at + q * to.plane) =
-            make_uint4(pack_bf16(part[0][q], part[1][q]), pack_bf16(part[2][q], part[3][q]),
-                       pack_bf16(part[4][q], part[5][q]), pack_bf16(part[6][q], part[7][q]));
+            make_uint4(pack_exact(part[0][q], part[1][q]), pack_exact(part[2][q], part[3][q]),
+                       pack_exact(part[4][q], part[5][q]), pack_exact(part[6][q], part[7][q]));
 }
 
 // The parts of a matrix: its values, a thread to eight columns.  One part suffices

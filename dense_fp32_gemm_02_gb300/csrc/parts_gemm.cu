@@ -58,7 +58,10 @@ int sgp::set_up() {
 
 // In units of one part pair's slab (64 k of a 256 x 256 tile, 0.27 us on a pair): a
 // wave takes its slabs, about 8 units of pipeline fill and epilogue; partial sums
-// are written and read once at about 5 TB/s.  The least estimate of up to 64 ranges.
+// are written and read once at about 5 TB/s, by a second launch (12 units).  A last wave
+// of half-width tiles counts half after others, whole where it is the only one (it then
+// waits for its loads).  The least estimate of up to 64 ranges: 64 x 4096 x 4096 bfloat16
+// takes 4 (18 us; 1: 26, 2: 21, 8: 22), 512 rows 1 (27; 2: 29, 4: 34).
 Split sgp::plan_split(int M, int N, int K, int products, int sms) {
     const long long pairs = std::max(1, sms / 2);
     const long long tiles = ((M + 255LL) / 256) * ((N + 255LL) / 256);
@@ -69,7 +72,7 @@ Split sgp::plan_split(int M, int N, int K, int products, int sms) {
         const long long per = (slabs + s - 1) / s;
         if ((slabs + per - 1) / per != s) continue;      // a range would be empty
         const long long items = tiles * s, waves = items / pairs, rest = items % pairs;
-        const double last = rest == 0 ? 0.0 : (s == 1 && 2 * rest <= pairs ? 0.5 : 1.0);
+        const double last = rest == 0 ? 0.0 : (s == 1 && waves > 0 && 2 * rest <= pairs ? 0.5 : 1.0);
         const double cost = (double(waves) + last) * (double(per) * products + 8.0) +
                             (s > 1 ? 12.0 + double(s) * M * N * 8.0 / 5.0e6 / 0.27 : 0.0);
         if (s == 1 || cost < least) {
@@ -101,7 +104,7 @@ int sgp::finish(int M, int N, int splits, const float *partial, const int2 *plan
 
 template <class T, Layout LAYOUT>
 int sgp::run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Split split,
-             float *partial, int sms, cudaStream_t stream) {
+             float *partial, int sms, cudaStream_t stream, Mode mode) {
     using K = Kernel<T, LAYOUT>;
     int st = set_up();
     if (st != SGEMM_OK) return st;
@@ -136,12 +139,17 @@ int sgp::run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Spl
     }
     const long long pairs = std::min<long long>(tiles_m * tiles_n * split.splits * (split.splits == 1 ? 2 : 1),
                                                 std::max(1, sms / 2));
-    K::main<<<unsigned(2 * pairs), THREADS, SMEM_BYTES, stream>>>(mA, mB, mH, mV, kp, epi);
+    cudaError_t e = cudaSuccess;
+    if (mode == PARTIALS_EARLY)
+        e = sgh::launch_early(K::main, dim3(unsigned(2 * pairs)), THREADS, SMEM_BYTES, stream, mA, mB, mH, mV, kp, epi);
+    else
+        K::main<<<unsigned(2 * pairs), THREADS, SMEM_BYTES, stream>>>(mA, mB, mH, mV, kp, epi);
+    if (e != cudaSuccess) return sgh::cuda_fail(e);
     sgh::count_launch(K::F32 ? "bf16 parts of float32, tcgen05 cta_group::2, 256x256 pair tiles"
                              : "bf16, tcgen05 cta_group::2, 256x256 pair tiles");
-    cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess) return sgh::cuda_fail(e);
-    if (split.splits > 1) 
+    if (split.splits > 1 && mode == WHOLE)
         return finish<T, LAYOUT == INPUT_GRAD>(p.M, p.N, split.splits, partial, p.planes, epi, stream);
     return SGEMM_OK;
 }
@@ -149,7 +157,7 @@ int sgp::run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Spl
 namespace sgp {
 #define LAYER_PRODUCT(T, LAYOUT)                                                                  \
     template int run<T, LAYOUT>(const Product &, const Epilogue<T, LAYOUT == INPUT_GRAD> &, Split, \
-                                float *, int, cudaStream_t)
+                                float *, int, cudaStream_t, Mode)
 LAYER_PRODUCT(float, FORWARD);
 LAYER_PRODUCT(bf16, FORWARD);
 LAYER_PRODUCT(float, INPUT_GRAD);

@@ -153,6 +153,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(A_MN) << 15) |
                                (uint32_t(TILE >> 4) << 24);
 
+    launch_dependents();   // (a dependent launched early waits for this kernel's end itself)
     extern __shared__ unsigned char smem_raw[];
     const uintptr_t base = (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023);
     float *stage_out = reinterpret_cast<float *>(base + SMEM_RING);
@@ -488,6 +489,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     tc_fence_after();
     if (warp == 1) tmem_dealloc_pair(taddr, TMEM_COLUMNS);
+    wait_prerequisites();   // launched early, its end is also that of the kernels before it
 }
 
 // The ranges' partial sums added in order, and the epilogue; a thread to an element.

@@ -55,9 +55,13 @@ struct Split {
 Split plan_split(int M, int N, int K, int products, int sms);
 
 // float: a of 3 parts (1 in WEIGHT_GRAD) and b of 3; bfloat16: one part each.
+// PARTIALS leaves the partial sums (of one range too) to the caller; PARTIALS_EARLY also
+// lets the kernel start while the one before it on the stream runs, of which it then
+// may read nothing.
+enum Mode { WHOLE, PARTIALS, PARTIALS_EARLY };
 template <class T, Layout LAYOUT>
 int run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Split split, float *partial,
-        int sms, cudaStream_t stream);
+        int sms, cudaStream_t stream, Mode mode = WHOLE);
 
 // The second kernel alone: out from `splits` partial sums (none: the epilogue of zero).
 // Rows of tiles that have planes already have their rank-side term (planes null: none).

@@ -183,6 +183,17 @@ __device__ __forceinline__ void tma_load_2d(void *smem_dst, const CUtensorMap *m
     tma_load_2d_at(smem_addr(smem_dst), map, smem_addr(bar), x, y);
 }
 
+// ---------------------------------------------------------------- dependent launches
+// For kernels launched with programmatic stream serialization: let the next kernel on the
+// stream start (it may not yet read what this one writes); wait until the kernels before
+// this one have completed and their writes are visible.
+__device__ __forceinline__ void launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_prerequisites() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- FP32x2
 // d = a * b + c on both lanes, round to nearest even (one instruction on sm_100+).
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {

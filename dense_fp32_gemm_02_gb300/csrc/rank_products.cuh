@@ -51,7 +51,7 @@ __device__ __forceinline__ void pair_parts(float x, float y, uint32_t (&part)[3]
     split_parts(x, px);
     split_parts(y, py);
 #pragma unroll
-    for (int q = 0; q < 3; ++q) part[q] = pack_bf16(px[q], py[q]);
+    for (int q = 0; q < 3; ++q) part[q] = pack_exact(px[q], py[q]);
 }
 
 // 16 bytes of shared memory from `n` elements at p (the rest zero): an asynchronous copy
@@ -376,8 +376,8 @@ __global__ void __launch_bounds__(RANK_THREADS)
 #pragma unroll
                 for (int q = 0; q < PB; ++q)
                     *reinterpret_cast<uint4 *>(to + q * Z::S_PLANE) =
-                        make_uint4(pack_bf16(part[0][q], part[1][q]), pack_bf16(part[2][q], part[3][q]),
-                                   pack_bf16(part[4][q], part[5][q]), pack_bf16(part[6][q], part[7][q]));
+                        make_uint4(pack_exact(part[0][q], part[1][q]), pack_exact(part[2][q], part[3][q]),
+                                   pack_exact(part[4][q], part[5][q]), pack_exact(part[6][q], part[7][q]));
             }
         }
         if (i0 + SLAB < n) load_s(i0 + SLAB);

@@ -1,74 +1,199 @@
 // rows.cuh -- the adapter layer for few rows (a decode step): Y = X W + bias + rank side.
 //
-// Bound by reading W once (and of the stack what the rows use).  W goes through shared
-// memory by asynchronous copies, 128 columns of a range of K to a block, three slabs
-// ahead; the warp-level MMA takes the rows 16 at a time, so that 1 row and 16 cost the
-// same.  In the same launch, blocks of their own take the rank side row by row, each row
-// with its own adapter.  A second kernel adds the ranges in order and applies the rest.
+// Bound by reading W once (and of the stack what the rows use).  The contraction is
+// split over the grid, each range's sums go to memory, and a last kernel adds the ranges
+// in order and applies the rest.  The product itself, by the count of rows:
+//   up to 16            stream_rows_kernel: W to registers 16 bytes at a time, fp32 FMAs
+//                       (16 rows of bfloat16 are 7 us of them at 4096 x 4096, W 5 us);
+//   float32 up to 64    few_rows_kernel: W through shared memory, the warp-level MMA on
+//                       three bfloat16 parts, split in registers;
+//   bfloat16 above 16   parts_gemm.cuh (18 us at 64 x 4096 x 4096, where the warp-level
+//                       MMA took 32: its operands pass through shared memory five times).
+// The rank side is taken row by row, each with its own adapter, by blocks of their own:
+// in the product's launch where all blocks fit the GPU at once, else in one just before,
+// which the product does not wait for.
 #pragma once
 
 #include "rank_products.cuh"
 
 namespace sgl {
 
-constexpr int FEW_ROWS = 64, ROWS_COLS = 128;
+constexpr int FEW_ROWS = 256, STREAM_ROWS = 16, MMA_ROWS = 64, ROWS_COLS = 128;
 
-template <class T, int MT>
-struct FewRows {
-    static constexpr bool F32 = sizeof(T) == 4;
-    static constexpr int PARTS = F32 ? 3 : 1, STAGES = 4;
-    static constexpr int W_PITCH = ROWS_COLS + (F32 ? 4 : 8), W_ELEMS = SLAB * W_PITCH;
-    static constexpr int X_PITCH = SLAB + 8, X_PLANE = MT * 16 * X_PITCH;
-    static constexpr size_t SMEM = size_t(STAGES) * W_ELEMS * sizeof(T) + size_t(2) * PARTS * X_PLANE * 2;
-};
-
-// The work of a launch: `across` x `ranges` blocks of the product, then M x `rank_ranges`
-// blocks of the rank side.
+// The work: `across` x `ranges` blocks of the product, then M x `rank_ranges` blocks of
+// the rank side.
 struct RowsWork {
     int M, N, K;
     int across, ranges, range;
     int rank_ranges, rank_range;
+    bool x_wide, v_wide;
     float *partial;        // ranges x M x N
     float *rank_partial;   // rank_ranges x M x R
 };
 
-// The rank side of one row over one range: threads along the rank and, in groups, along
-// the range, whose sums are added in order.
+// The rank side of one row over one range.  Lanes along the rank, 16 bytes each, and in
+// groups along the range; a thread's sums, then its warp's groups, then the warps.
 template <class T>
 __device__ __forceinline__ void rank_of_row(const RowsWork &w, int b, const Rows<T> &X, const Stack<const T> &V,
                                             const Adapters &ad, float *sums) {
+    constexpr int PER = 16 / int(sizeof(T));
     const int i = b / w.rank_ranges, q = b - i * w.rank_ranges;
     const int a = ad.of_row(i);
     const int rank = a < 0 ? 0 : ad.rank(a);
     if (rank == 0) return;   // nothing reads this row's sums
-    const int width = ad.R <= 8 ? 8 : ad.R <= 16 ? 16 : ad.R <= 32 ? 32 : ad.R <= 64 ? 64 : 128;
-    const int groups = RANK_THREADS / width, r = threadIdx.x & (width - 1), group = threadIdx.x / width;
-    const int c1 = min(w.K, (q + 1) * w.rank_range);
-    const T *x = X.p + i * X.ld, *v = V.matrix(a) + r;
-    float sum = 0.0f;
-    if (r < rank) {
-#pragma unroll 8
-        for (int c = q * w.rank_range + group; c < c1; c += groups)
-            sum = fmaf(to_f32(x[c]), to_f32(v[c * V.ld]), sum);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int along = 1;           // lanes along the rank: a power of two, up to 16 (32 for float32)
+    while (along * PER < ad.R) along *= 2;
+    const int groups = RANK_THREADS / along, r0 = (threadIdx.x & (along - 1)) * PER, group = threadIdx.x / along;
+    const int c0 = q * w.rank_range, c1 = min(w.K, c0 + w.rank_range);
+    const T *x = X.p + i * X.ld, *v = V.matrix(a) + r0;
+    float sum[PER] = {};
+    if (r0 < rank) {
+        if (w.v_wide && r0 + PER <= ad.R) {
+#pragma unroll 4
+            for (int c = c0 + group; c < c1; c += groups) {
+                const float xc = to_f32(x[c]);
+                float y[PER];
+                if constexpr (PER == 8) load8(v + c * V.ld, y); else load4(v + c * V.ld, y);
+#pragma unroll
+                for (int d = 0; d < PER; ++d) sum[d] = fmaf(xc, r0 + d < rank ? y[d] : 0.0f, sum[d]);
+            }
+        } else {
+#pragma unroll 2
+            for (int c = c0 + group; c < c1; c += groups) {
+                const float xc = to_f32(x[c]);
+#pragma unroll
+                for (int d = 0; d < PER; ++d) sum[d] = fmaf(xc, r0 + d < rank ? to_f32(v[c * V.ld + d]) : 0.0f, sum[d]);
+            }
+        }
     }
-    sums[threadIdx.x] = sum;
+#pragma unroll
+    for (int d = 0; d < PER; ++d)
+        for (int o = 16; o >= along; o >>= 1) sum[d] += __shfl_xor_sync(0xffffffffu, sum[d], o);
+    if (lane < along) {
+#pragma unroll
+        for (int d = 0; d < PER; ++d) sums[warp * 128 + r0 + d] = sum[d];
+    }
     __syncthreads();
-    if (group == 0 && r < rank) {
-        for (int g = 1; g < groups; ++g) sum += sums[g * width + r];
-        w.rank_partial[((long long)q * w.M + i) * ad.R + r] = sum;
+    const int r = threadIdx.x;
+    if (r < rank) {
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < RANK_THREADS / 32; ++k) s += sums[k * 128 + r];
+        w.rank_partial[((long long)q * w.M + i) * ad.R + r] = s;
     }
 }
+constexpr int RANK_SUMS = RANK_THREADS / 32 * 128;
 
-template <class T, int MT>
+template <class T>
 __global__ void __launch_bounds__(RANK_THREADS)
-    few_rows_kernel(RowsWork w, Rows<T> X, const T *W, long long ldw, bool w_wide, Stack<const T> V, Adapters ad) {
-    using Z = FewRows<T, MT>;
-    constexpr int PARTS = Z::PARTS, STAGES = Z::STAGES;
-    extern __shared__ __align__(16) unsigned char smem_rows[];
+    few_rows_rank_kernel(RowsWork w, Rows<T> X, Stack<const T> V, Adapters ad) {
+    __shared__ float sums[RANK_SUMS];
+    sg::launch_dependents();
+    rank_of_row(w, int(blockIdx.x), X, V, ad, sums);
+}
+
+// ------------------------------------------------------------------ up to 16 rows
+// A block to 32 x 16 bytes of columns and a range of at most STREAM_RANGE of K: its warps
+// take 8 rows of W at a time, all loads before the first use.  X's range stands in shared
+// memory as fp32, MR rows next to each other.  WIDE: 16-byte loads, a lane's columns
+// together; else single elements, 32 lanes next to each other.
+constexpr int STREAM_RANGE = 512, STREAM_DEPTH = 8;
+
+template <class T, int MR, bool WIDE>
+__global__ void __launch_bounds__(RANK_THREADS)
+    stream_rows_kernel(RowsWork w, Rows<T> X, const T *W, long long ldw, Stack<const T> V, Adapters ad) {
+    constexpr int PER = 16 / int(sizeof(T)), COLS = 32 * PER, WARPS = RANK_THREADS / 32;
+    constexpr int XS = STREAM_RANGE * MR, RED = WARPS * COLS * (MR < 4 ? MR : 4);
+    __shared__ __align__(16) float sm[XS > RED ? (XS > RANK_SUMS ? XS : RANK_SUMS) : (RED > RANK_SUMS ? RED : RANK_SUMS)];
+    sg::launch_dependents();
     if (int(blockIdx.x) >= w.across * w.ranges) {
-        rank_of_row(w, int(blockIdx.x) - w.across * w.ranges, X, V, ad, reinterpret_cast<float *>(smem_rows));
+        rank_of_row(w, int(blockIdx.x) - w.across * w.ranges, X, V, ad, sm);
+        sg::wait_prerequisites();
         return;
     }
+    const int n0 = (int(blockIdx.x) % w.across) * COLS, q = int(blockIdx.x) / w.across;
+    const int k0 = q * w.range, kn = min(w.range, w.K - k0);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto column = [&](int e) { return n0 + (WIDE ? lane * PER + e : e * 32 + lane); };
+    auto load = [&](int k) {   // 16 bytes of row k0 + k of W, zero past its end
+        const T *p = W + (k0 + k) * ldw;
+        if (WIDE && column(PER - 1) < w.N) return *reinterpret_cast<const uint4 *>(p + column(0));
+        T v[PER];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) v[e] = column(e) < w.N ? p[column(e)] : T(0.0f);
+        return *reinterpret_cast<const uint4 *>(v);
+    };
+    for (int t = threadIdx.x; t < kn * MR; t += RANK_THREADS) {
+        const int m = t / kn, k = t - m * kn;
+        sm[k * MR + m] = m < w.M ? X.at(m, k0 + k) : 0.0f;
+    }
+    __syncthreads();
+    float2 acc[MR][PER / 2] = {};
+    for (int k = warp * STREAM_DEPTH; k < kn; k += WARPS * STREAM_DEPTH) {
+        uint4 v[STREAM_DEPTH];
+#pragma unroll
+        for (int u = 0; u < STREAM_DEPTH; ++u) v[u] = k + u < kn ? load(k + u) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < STREAM_DEPTH; ++u) {
+            const float *x = sm + min(k + u, kn - 1) * MR;
+            const bool in = k + u < kn;   // (a row past the range is 0 * x: x may be NaN)
+            float2 y[PER / 2];
+            if constexpr (PER == 8) {
+                y[0] = make_float2(bf16_lo(v[u].x), bf16_hi(v[u].x)), y[1] = make_float2(bf16_lo(v[u].y), bf16_hi(v[u].y));
+                y[2] = make_float2(bf16_lo(v[u].z), bf16_hi(v[u].z)), y[3] = make_float2(bf16_lo(v[u].w), bf16_hi(v[u].w));
+            } else {
+                y[0] = make_float2(__uint_as_float(v[u].x), __uint_as_float(v[u].y));
+                y[1] = make_float2(__uint_as_float(v[u].z), __uint_as_float(v[u].w));
+            }
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+                const float xm = in ? x[m] : 0.0f;
+#pragma unroll
+                for (int e = 0; e < PER / 2; ++e) acc[m][e] = sg::ffma2(make_float2(xm, xm), y[e], acc[m][e]);
+            }
+        }
+    }
+    float *out = w.partial + (long long)q * w.M * w.N;
+#pragma unroll
+    for (int m0 = 0; m0 < MR; m0 += 4) {
+        __syncthreads();
+#pragma unroll
+        for (int m = m0; m < m0 + 4 && m < MR; ++m)
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                const float s = e & 1 ? acc[m][e / 2].y : acc[m][e / 2].x;
+                sm[((m - m0) * WARPS + warp) * COLS + (WIDE ? lane * PER + e : e * 32 + lane)] = s;
+            }
+        __syncthreads();
+        for (int t = threadIdx.x; t < min(4, MR) * COLS; t += RANK_THREADS) {
+            const int m = m0 + t / COLS, c = t % COLS;
+            float s = 0.0f;
+#pragma unroll
+            for (int k = 0; k < WARPS; ++k) s += sm[((m - m0) * WARPS + k) * COLS + c];
+            if (m < w.M && n0 + c < w.N) out[(long long)m * w.N + n0 + c] = s;
+        }
+    }
+    sg::wait_prerequisites();   // this kernel's end is also that of the rank side's
+}
+
+// ------------------------------------------------------------------ float32, up to 64 rows
+template <int MT>
+struct FewRows {
+    static constexpr int PARTS = 3, STAGES = MT <= 2 ? 2 : 4;   // two blocks to an SM, or one
+    static constexpr int W_PITCH = ROWS_COLS + 4, W_ELEMS = SLAB * W_PITCH;
+    static constexpr int X_PITCH = SLAB + 8, X_PLANE = MT * 16 * X_PITCH;
+    static constexpr size_t SMEM = size_t(STAGES) * W_ELEMS * 4 + size_t(2) * PARTS * X_PLANE * 2;
+};
+
+template <int MT>
+__global__ void __launch_bounds__(RANK_THREADS)
+    few_rows_kernel(RowsWork w, Rows<float> X, const float *W, long long ldw, bool w_wide) {
+    using T = float;
+    using Z = FewRows<MT>;
+    constexpr int PARTS = Z::PARTS, STAGES = Z::STAGES;
+    extern __shared__ __align__(16) unsigned char smem_rows[];
+    sg::launch_dependents();
     T *ring = reinterpret_cast<T *>(smem_rows);
     bf16 *xs = reinterpret_cast<bf16 *>(ring + STAGES * Z::W_ELEMS);   // [2][PARTS][16 MT rows]
     const int n0 = (int(blockIdx.x) % w.across) * ROWS_COLS, q = int(blockIdx.x) / w.across;
@@ -91,8 +216,12 @@ __global__ void __launch_bounds__(RANK_THREADS)
 #pragma unroll
         for (int h = 0; h < MT; ++h) {
             const int o = threadIdx.x + h * RANK_THREADS, m = o / 16, k = k0 + (o % 16) * 4;
+            if (m < w.M && w.x_wide && k + 4 <= k_end) {
+                load4(X.p + m * X.ld + k, xv[h]);
+            } else {
 #pragma unroll
-            for (int d = 0; d < 4; ++d) xv[h][d] = m < w.M && k + d < k_end ? X.at(m, k + d) : 0.0f;
+                for (int d = 0; d < 4; ++d) xv[h][d] = m < w.M && k + d < k_end ? X.at(m, k + d) : 0.0f;
+            }
         }
     };
     auto stage_x = [&](bf16 *to) {
@@ -104,9 +233,7 @@ __global__ void __launch_bounds__(RANK_THREADS)
             pair_parts(xv[h][2], xv[h][3], hi);
 #pragma unroll
             for (int p = 0; p < PARTS; ++p)
-                *reinterpret_cast<uint2 *>(to + p * Z::X_PLANE + m * Z::X_PITCH + k) =
-                    PARTS == 1 ? make_uint2(pack_bf16(xv[h][0], xv[h][1]), pack_bf16(xv[h][2], xv[h][3]))
-                               : make_uint2(lo[p], hi[p]);
+                *reinterpret_cast<uint2 *>(to + p * Z::X_PLANE + m * Z::X_PITCH + k) = make_uint2(lo[p], hi[p]);
         }
     };
 
@@ -131,16 +258,12 @@ __global__ void __launch_bounds__(RANK_THREADS)
 #pragma unroll
         for (int kk = 0; kk < SLAB; kk += 16) {
             uint32_t fb[PARTS][4];   // two 8-column tiles of 16 k
-            if constexpr (!Z::F32) {
-                ldmatrix4<true>(fb[0], ws + (kk + (lane & 15)) * Z::W_PITCH + warp * 16 + ((lane >> 4) & 1) * 8);
-            } else {
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const T *p = ws + (kk + (lane & 3) * 2 + (d & 1) * 8) * Z::W_PITCH + warp * 16 + (lane >> 2) + (d >> 1) * 8;
-                    uint32_t part[3];
-                    pair_parts(p[0], p[Z::W_PITCH], part);
-                    fb[0][d] = part[0], fb[1][d] = part[1], fb[2][d] = part[2];
-                }
+            for (int d = 0; d < 4; ++d) {
+                const float *p = ws + (kk + (lane & 3) * 2 + (d & 1) * 8) * Z::W_PITCH + warp * 16 + (lane >> 2) + (d >> 1) * 8;
+                uint32_t part[3];
+                pair_parts(p[0], p[Z::W_PITCH], part);
+                fb[0][d] = part[0], fb[1][d] = part[1], fb[2][d] = part[2];
             }
 #pragma unroll
             for (int m = 0; m < MT; ++m)
@@ -161,7 +284,7 @@ __global__ void __launch_bounds__(RANK_THREADS)
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int d = 0; d < 4; ++d)
-                    sum[m][t][d] += Z::F32 ? big[m][t][d] + small[m][t][d] : big[m][t][d];
+                    sum[m][t][d] += big[m][t][d] + small[m][t][d];
         stage = (stage + 1) % STAGES;
     }
     float *out = w.partial + (long long)q * w.M * w.N;
@@ -174,39 +297,75 @@ __global__ void __launch_bounds__(RANK_THREADS)
                 const int i = m * 16 + (lane >> 2) + (d / 2) * 8, j = n0 + warp * 16 + t * 8 + (lane & 3) * 2 + (d & 1);
                 if (i < w.M && j < w.N) out[(long long)i * w.N + j] = sum[m][t][d];
             }
+    sg::wait_prerequisites();   // this kernel's end is also that of the rank side's
 }
 
-// Y from the partial sums: a block to 256 columns of a row.  The first one of a row also
-// writes H.
-template <class T>
+// ------------------------------------------------------------------ the rest
+// Y from the partial sums: a block to 256 columns of a row (8 to a lane), its 8 warps to
+// the ranges and the rank, whose terms they share out; the warps' sums are added in
+// order.  The first block of a row also writes H.  WIDE: rows of everything but the
+// partial sums can be read eight elements at a time; `p_wide` the same of those.
+template <class T, bool WIDE>
 __global__ void __launch_bounds__(256)
-    few_rows_finish_kernel(RowsWork w, Stack<const T> V, Adapters ad, const T *bias, float *H, long long ldh, T *Y,
-                           long long ldy) {
+    few_rows_finish_kernel(RowsWork w, Stack<const T> V, Adapters ad, const T *bias, bool p_wide, float *H, long long ldh,
+                           T *Y, long long ldy) {
     __shared__ float S[128];
-    const int i = blockIdx.y, j = blockIdx.x * 256 + threadIdx.x;
+    __shared__ __align__(16) float sums[8][256];
+    const int i = blockIdx.y, n0 = blockIdx.x * 256, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int j = n0 + lane * 8;
     const int a = ad.of_row(i), rank = a < 0 ? 0 : ad.rank(a);
+    const float scale = a < 0 ? 0.0f : ad.scale(a);
+    sg::wait_prerequisites();
     if (int(threadIdx.x) < ad.R && ad.L > 0) {
         const int r = threadIdx.x;
         float sum = 0.0f;
-        if (r < rank)
-            for (int q = 0; q < w.rank_ranges; ++q) sum += w.rank_partial[((long long)q * w.M + i) * ad.R + r];
+        if (r < rank) {
+            const float *p = w.rank_partial + (long long)i * ad.R + r;
+#pragma unroll 8
+            for (int q = 0; q < w.rank_ranges; ++q) sum += p[(long long)q * w.M * ad.R];
+        }
         if (H && blockIdx.x == 0) H[i * ldh + r] = sum;
-        S[r] = r < rank ? sum * ad.scale(a) : 0.0f;
+        S[r] = r < rank ? sum * scale : 0.0f;
+    }
+    float x[8] = {}, v[8];
+    auto read = [&](auto *p, bool eight) {   // columns j .. j + 7
+        if (eight && j + 8 <= w.N) {
+            load8(p + j, v);
+        } else {
+#pragma unroll
+            for (int d = 0; d < 8; ++d) v[d] = j + d < w.N ? to_f32(p[j + d]) : 0.0f;
+        }
+    };
+    const float *p = w.partial + (long long)i * w.N;
+    const long long plane = (long long)w.M * w.N;
+#pragma unroll 2
+    for (int q = warp; q < w.ranges; q += 8) {
+        read(p + q * plane, p_wide);
+#pragma unroll
+        for (int d = 0; d < 8; ++d) x[d] += v[d];
+    }
+    if (bias && warp == 7) {
+        read(bias, WIDE);
+#pragma unroll
+        for (int d = 0; d < 8; ++d) x[d] += v[d];
     }
     __syncthreads();
-    if (j >= w.N) return;
-    float x = 0.0f;
-    const float *p = w.partial + (long long)i * w.N + j;
-    const long long plane = (long long)w.M * w.N;
-#pragma unroll 8
-    for (int q = 0; q < w.ranges; ++q) x += p[q * plane];
-    if (bias) x += to_f32(bias[j]);
     if (rank > 0) {
-        const T *v = V.matrix(a) + j;
-#pragma unroll 8
-        for (int r = 0; r < rank; ++r) x = fmaf(S[r], to_f32(v[r * V.ld]), x);
+        const T *m = V.matrix(a);
+#pragma unroll 4
+        for (int r = warp; r < rank; r += 8) {
+            read(m + r * V.ld, WIDE);
+#pragma unroll
+            for (int d = 0; d < 8; ++d) x[d] = fmaf(S[r], v[d], x[d]);
+        }
     }
-    Y[(long long)i * ldy + j] = from_f32<T>(x);
+    *reinterpret_cast<float4 *>(&sums[warp][lane * 8]) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4 *>(&sums[warp][lane * 8 + 4]) = make_float4(x[4], x[5], x[6], x[7]);
+    __syncthreads();
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += sums[k][threadIdx.x];
+    if (n0 + int(threadIdx.x) < w.N) Y[(long long)i * ldy + n0 + threadIdx.x] = from_f32<T>(s);
 }
 
 }  // namespace sgl

@@ -86,7 +86,8 @@ FORWARD = [  # (M, K, N, L, R, ids, padding, offset)
     (400, 520, 264, 3, 16, "none", 0, 0), (513, 128, 513, 2, 128, "runs", 0, 1),
     (700, 264, 300, 6, 40, "mixed", 0, 0), (1100, 520, 776, 3, 16, "runs", 0, 0),
     (1025, 2056, 264, 2, 65, "runs", 0, 0), (64, 64, 4100, 4, 8, "mixed", 0, 0),
-    (300, 64, 64, 0, 1, "none", 0, 0), (7, 96, 40, 0, 1, "none", 0, 0), (600, 32, 8, 500, 4, "mixed", 0, 0)]
+    (64, 4100, 520, 0, 1, "none", 0, 0), (40, 4100, 1032, 3, 8, "mixed", 4, 4), (200, 3000, 264, 2, 20, "runs", 0, 0),
+    (16, 5000, 264, 5, 24, "mixed", 0, 0), (3, 9000, 72, 3, 128, "mixed", 0, 0), (300, 64, 64, 0, 1, "none", 0, 0), (7, 96, 40, 0, 1, "none", 0, 0), (600, 32, 8, 500, 4, "mixed", 0, 0)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
