@@ -355,8 +355,7 @@ StreamKernel<T> stream_kernel(int M) {
     return M <= 1   ? stream_rows_kernel<T, 1, WIDE>
            : M <= 2 ? stream_rows_kernel<T, 2, WIDE>
            : M <= 4 ? stream_rows_kernel<T, 4, WIDE>
-           : M <= 8 ? stream_rows_kernel<T, 8, WIDE>
-                    : stream_rows_kernel<T, 16, WIDE>;
+                    : stream_rows_kernel<T, 8, WIDE>;
 }
 
 // The split of K over the grid: the count of ranges (whole `step`s, none above `longest`)
@@ -402,7 +401,7 @@ int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
         slots *= std::max(1, std::min(per_sm, 4));
         split_rows(w, 32 * 16 / int(sizeof(T)), RANK_THREADS / 32 * STREAM_DEPTH, STREAM_RANGE, slots, sizeof(T));
     } else if (mma_rows) {
-        slots *= c.M <= 32 ? 2 : 1;
+        slots *= 2;
         split_rows(w, ROWS_COLS, SLAB, sgh::kMaxDim, slots, sizeof(T));
     } else {
         split = sgp::plan_split(c.M, c.N, c.K, 1, sms);

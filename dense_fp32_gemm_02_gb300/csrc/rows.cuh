@@ -3,12 +3,15 @@
 // Bound by reading W once (and of the stack what the rows use).  The contraction is
 // split over the grid, each range's sums go to memory, and a last kernel adds the ranges
 // in order and applies the rest.  The product itself, by the count of rows:
-//   up to 16            stream_rows_kernel: W to registers 16 bytes at a time, fp32 FMAs
-//                       (16 rows of bfloat16 are 7 us of them at 4096 x 4096, W 5 us);
+//   up to 8             stream_rows_kernel: W to registers 16 bytes at a time, fp32 FMAs;
 //   float32 up to 64    few_rows_kernel: W through shared memory, the warp-level MMA on
 //                       three bfloat16 parts, split in registers;
-//   bfloat16 above 16   parts_gemm.cuh (18 us at 64 x 4096 x 4096, where the warp-level
-//                       MMA took 32: its operands pass through shared memory five times).
+//   bfloat16 above 8    parts_gemm.cuh.
+// At 4096 x 4096 without adapters, us: bfloat16 (W is 5.0 of them) 1 row 9.6, 4 rows 12.5,
+// 8 rows 20.5 and by parts_gemm 9 rows 15.4 (by FMAs 16 rows 34), 64 rows 17.6 (the
+// warp-level MMA took 32: its operands pass through shared memory five times); float32 (W
+// 9.9) 1 row 14.3, 8 rows 21.3, 16 rows 32.3 (by FMAs 43).  At 1024 x 1024 8 rows of
+// bfloat16 take 5.7 by FMAs, 9 rows 8.4 by parts_gemm: hence 8 for both.
 // The rank side is taken row by row, each with its own adapter, by blocks of their own:
 // in the product's launch where all blocks fit the GPU at once, else in one just before,
 // which the product does not wait for.
@@ -18,7 +21,7 @@
 
 namespace sgl {
 
-constexpr int FEW_ROWS = 256, STREAM_ROWS = 16, MMA_ROWS = 64, ROWS_COLS = 128;
+constexpr int FEW_ROWS = 256, STREAM_ROWS = 8, MMA_ROWS = 64, ROWS_COLS = 128;
 
 // The work: `across` x `ranges` blocks of the product, then M x `rank_ranges` blocks of
 // the rank side.
@@ -93,7 +96,7 @@ __global__ void __launch_bounds__(RANK_THREADS)
     rank_of_row(w, int(blockIdx.x), X, V, ad, sums);
 }
 
-// ------------------------------------------------------------------ up to 16 rows
+// ------------------------------------------------------------------ up to 8 rows
 // A block to 32 x 16 bytes of columns and a range of at most STREAM_RANGE of K: its warps
 // take 8 rows of W at a time, all loads before the first use.  X's range stands in shared
 // memory as fp32, MR rows next to each other.  WIDE: 16-byte loads, a lane's columns
@@ -180,10 +183,12 @@ __global__ void __launch_bounds__(RANK_THREADS)
 // ------------------------------------------------------------------ float32, up to 64 rows
 template <int MT>
 struct FewRows {
-    static constexpr int PARTS = 3, STAGES = MT <= 2 ? 2 : 4;   // two blocks to an SM, or one
+    // two blocks to an SM (one of deeper rings took 56 us at 64 x 4096 x 4096): with 64
+    // rows, X has one buffer
+    static constexpr int PARTS = 3, STAGES = 2, X_BUFFERS = MT <= 2 ? 2 : 1;
     static constexpr int W_PITCH = ROWS_COLS + 4, W_ELEMS = SLAB * W_PITCH;
     static constexpr int X_PITCH = SLAB + 8, X_PLANE = MT * 16 * X_PITCH;
-    static constexpr size_t SMEM = size_t(STAGES) * W_ELEMS * 4 + size_t(2) * PARTS * X_PLANE * 2;
+    static constexpr size_t SMEM = size_t(STAGES) * W_ELEMS * 4 + size_t(X_BUFFERS) * PARTS * X_PLANE * 2;
 };
 
 template <int MT>
@@ -195,7 +200,7 @@ __global__ void __launch_bounds__(RANK_THREADS)
     extern __shared__ __align__(16) unsigned char smem_rows[];
     sg::launch_dependents();
     T *ring = reinterpret_cast<T *>(smem_rows);
-    bf16 *xs = reinterpret_cast<bf16 *>(ring + STAGES * Z::W_ELEMS);   // [2][PARTS][16 MT rows]
+    bf16 *xs = reinterpret_cast<bf16 *>(ring + STAGES * Z::W_ELEMS);   // [X_BUFFERS][PARTS][16 MT rows]
     const int n0 = (int(blockIdx.x) % w.across) * ROWS_COLS, q = int(blockIdx.x) / w.across;
     const int k_begin = q * w.range, k_end = min(w.K, k_begin + w.range);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -246,7 +251,8 @@ __global__ void __launch_bounds__(RANK_THREADS)
     load_x(k_begin);
     int stage = 0;
     for (int k0 = k_begin; k0 < k_end; k0 += SLAB) {
-        bf16 *x = xs + (stage & 1) * PARTS * Z::X_PLANE;
+        bf16 *x = xs + (Z::X_BUFFERS == 2 ? stage & 1 : 0) * PARTS * Z::X_PLANE;
+        if (Z::X_BUFFERS == 1 && k0 > k_begin) __syncthreads();   // the last slab's has been read
         stage_x(x);
         sg::cp_async_wait<STAGES - 2>();
         __syncthreads();   // this slab has landed, and the stage filled next has been read
