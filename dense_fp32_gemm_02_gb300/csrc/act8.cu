@@ -19,48 +19,62 @@ using namespace sgl;
 constexpr int kThreads = 256;
 
 // ------------------------------------------------------------------ activations
-// Phi(z) = (1 + erf(z / sqrt 2)) / 2 and exp(-z^2/2), by formula 7.1.26 of
-// Abramowitz and Stegun, Handbook of Mathematical Functions:
+// With Phi(z) = (1 + erf(z / sqrt 2)) / 2: tail = 1 - Phi(|z|) and bell = exp(-z^2/2), by
+// formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical Functions:
 //   erf x = 1 - (a1 t + ... + a5 t^5) exp(-x^2),  t = 1 / (1 + p x),  x >= 0,
-// whose error is at most 1.5e-7, i.e. that of fp32 itself at this size.  The
-// exponential is the one that the derivative needs anyway, and the negative side
-// comes without cancellation.
-__device__ __forceinline__ void normal_cdf(float z, float &cdf, float &bell) {
-    const float x = fabsf(z) * 0.70710678f;
-    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
-    bell = __expf(-x * x);
-    float p = fmaf(t, 1.061405429f, -1.453152027f);
-    p = fmaf(t, p, 1.421413741f);
-    p = fmaf(t, p, -0.284496736f);
-    p = fmaf(t, p, 0.254829592f);
-    const float tail = 0.5f * p * t * bell;
-    cdf = z < 0.0f ? tail : 1.0f - tail;
+// whose error is at most 1.5e-7, i.e. that of fp32 itself at this size.  The exponential is
+// the one that the derivative needs anyway, and both come without cancellation.  (x = |z| /
+// sqrt 2 is folded into p, the half of Phi into the a's.)  Two elements at a time: with
+// single-precision instructions for one, GELU over 8192 x 16384 bfloat16 took 175 us.
+__device__ __forceinline__ float exp2f_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ void normal_tail(float2 z, float2 &tail, float2 &bell) {
+    const float2 e = __fmul2_rn(__fmul2_rn(z, z), both(-0.72134752f));   // -z^2/2 log2 e
+    bell = make_float2(exp2f_fast(e.x), exp2f_fast(e.y));
+    const float2 t = make_float2(__fdividef(1.0f, fmaf(0.23164190f, fabsf(z.x), 1.0f)),
+                                 __fdividef(1.0f, fmaf(0.23164190f, fabsf(z.y), 1.0f)));
+    float2 p = __ffma2_rn(t, both(0.5307027145f), both(-0.7265760135f));
+    p = __ffma2_rn(t, p, both(0.7107068705f));
+    p = __ffma2_rn(t, p, both(-0.142248368f));
+    p = __ffma2_rn(t, p, both(0.127414796f));
+    tail = __fmul2_rn(__fmul2_rn(p, t), bell);
 }
 
 template <int ACT>
-__device__ __forceinline__ float activate(float z) {
-    if constexpr (ACT == SGEMM_ACT_RELU) return z < 0.0f ? 0.0f : z;   // a NaN stays one
-    if constexpr (ACT == SGEMM_ACT_GELU) {
-        float cdf, bell;
-        normal_cdf(z, cdf, bell);
-        return z * cdf;
+__device__ __forceinline__ float2 activate(float2 z) {
+    if constexpr (ACT == SGEMM_ACT_RELU)   // (a NaN stays one)
+        return make_float2(z.x < 0.0f ? 0.0f : z.x, z.y < 0.0f ? 0.0f : z.y);
+    if constexpr (ACT == SGEMM_ACT_GELU) {   // z Phi(z) = max(z, 0) - |z| tail
+        float2 tail, bell;
+        normal_tail(z, tail, bell);
+        return make_float2(fmaf(-fabsf(z.x), tail.x, fmaxf(z.x, 0.0f)),
+                           fmaf(-fabsf(z.y), tail.y, fmaxf(z.y, 0.0f)));
     }
     return z;
 }
 
 template <int ACT>
-__device__ __forceinline__ float slope(float z) {
-    if constexpr (ACT == SGEMM_ACT_RELU) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
-    if constexpr (ACT == SGEMM_ACT_GELU) {
-        float cdf, bell;
-        normal_cdf(z, cdf, bell);
-        return fmaf(z * 0.39894228f, bell, cdf);
+__device__ __forceinline__ float2 slope(float2 z) {
+    if constexpr (ACT == SGEMM_ACT_RELU)
+        return make_float2(z.x > 0.0f ? 1.0f : (z.x <= 0.0f ? 0.0f : z.x),
+                           z.y > 0.0f ? 1.0f : (z.y <= 0.0f ? 0.0f : z.y));
+    if constexpr (ACT == SGEMM_ACT_GELU) {   // Phi(z) = 1/2 + sign(z) (1/2 - tail)
+        float2 tail, bell;
+        normal_tail(z, tail, bell);
+        const float2 h = __fadd2_rn(both(0.5f), make_float2(-tail.x, -tail.y));
+        const float2 cdf = __fadd2_rn(both(0.5f), make_float2(copysignf(h.x, z.x), copysignf(h.y, z.y)));
+        return __ffma2_rn(__fmul2_rn(z, both(0.39894228f)), bell, cdf);
     }
-    return z == z ? 1.0f : z;
+    return make_float2(z.x == z.x ? 1.0f : z.x, z.y == z.y ? 1.0f : z.y);
 }
 
 // ------------------------------------------------------------------ kernels
-// What a kernel works on: `units` blocks of 32 columns, `per_row` to a row.
+// What a kernel works on: `units` of 32 columns (wide forms) or 256, `per_row` to a row.
 struct Blocks {
     unsigned units, per_row;
     int K;
@@ -70,16 +84,20 @@ struct Checkpoint {
     long long ldq, lde;
 };
 
-// Wide form, for rows that are 16-byte aligned and of a multiple of 8 columns:
-// a quarter of a block to a thread, its maximum over four lanes.  Four blocks
-// in flight per thread for bfloat16, two for float32: 64 bytes of loads.
+// Wide form, for rows that are 16-byte aligned and of a multiple of 8 columns: a quarter
+// of a block to a thread, its maximum over four lanes.  Storing keeps 64 bytes of loads in
+// flight per thread, reading back 32 of bfloat16.  At 8192 x 16384, us (GB/s over the bytes
+// of either side): bfloat16 store 70, with GELU 125 (5400), GELU gradient 132 (5100), load
+// 68; float32 with GELU 174 (6940).  Half or twice the depth: store 133 or 158 with GELU,
+// gradient (twice, four times) 151 or 231.
 template <class T>
-constexpr int kDepth = sizeof(T) == 2 ? 4 : 2;
+constexpr int kStoreDepth = sizeof(T) == 2 ? 4 : 2;
+constexpr int kReadDepth = 2;
 
 template <class T, int ACT, bool WITH_Y>
 __global__ void __launch_bounds__(kThreads)
     store_wide_kernel(Blocks b, const T *Z, long long ldz, Checkpoint c, T *Y, long long ldy) {
-    constexpr int D = kDepth<T>;
+    constexpr int D = kStoreDepth<T>;
     const int sub = threadIdx.x & 3;
     const unsigned first = (blockIdx.x * D) * (kThreads / 4) + (threadIdx.x >> 2);
     float z[D][8];
@@ -106,51 +124,70 @@ __global__ void __launch_bounds__(kThreads)
         const int e = act8_exponent(top);
         if (!in[d]) continue;
         const float inverse = act8_inverse_step(e);
-        uint32_t w[2] = {0, 0};
-        if (e != ACT8_NAN) {
+        uint32_t w[2] = {pack_s8(z[d], inverse), pack_s8(z[d] + 4, inverse)};
+        if (e == ACT8_NAN || e == 121) {   // rare: nothing to keep, or 127 is exceeded
+            w[0] = w[1] = 0;
+            if (e == 121)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                w[i / 4] |= (uint32_t(act8_quantise(z[d][i], inverse)) & 0xffu) << (8 * (i % 4));
+                for (int i = 0; i < 8; ++i)
+                    w[i / 4] |= (uint32_t(act8_quantise(z[d][i], inverse)) & 0xffu) << (8 * (i % 4));
         }
         *reinterpret_cast<uint2 *>(c.q + row[d] * c.ldq + col[d]) = make_uint2(w[0], w[1]);
         if (sub == 0) c.e[row[d] * c.lde + col[d] / ACT8_BLOCK] = static_cast<signed char>(e);
         if constexpr (WITH_Y) {
             float y[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = activate<ACT>(z[d][i]);
+            for (int i = 0; i < 8; i += 2) {
+                const float2 v = activate<ACT>(make_float2(z[d][i], z[d][i + 1]));
+                y[i] = v.x, y[i + 1] = v.y;
+            }
             store8(Y + (long long)row[d] * ldy + col[d], y);
         }
     }
 }
 
-// Any alignment and width: a block to a warp, a column to a lane, so that each
-// access covers consecutive elements of a row wherever it starts.
-constexpr int kAnyDepth = 4;
+// Any alignment and width: eight blocks of a row to a warp, a column of each to a lane, so
+// that every access covers consecutive elements wherever the row starts.  GELU over 4097 x
+// 3001 float32: 23 us stored, its gradient 21 (5400 GB/s); one block to a warp took 41 and
+// 39, most of it finding rows.
+constexpr int kAnyDepth = 8;
 
 template <class T, int ACT, bool WITH_Y>
 __global__ void __launch_bounds__(kThreads)
     store_any_kernel(Blocks b, const T *Z, long long ldz, Checkpoint c, T *Y, long long ldy) {
     constexpr int D = kAnyDepth;
     const int lane = threadIdx.x & 31;
-    const unsigned first = (blockIdx.x * D) * (kThreads / 32) + (threadIdx.x >> 5);
+    const unsigned u = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), row = u / b.per_row;
+    if (u >= b.units) return;
+    const int c0 = int(u - row * b.per_row) * (D * ACT8_BLOCK) + lane;
+    const T *zr = Z + (long long)row * ldz + c0;
+    signed char *q = c.q + row * c.ldq + c0, *e = c.e + row * c.lde + (c0 - lane) / ACT8_BLOCK;
+    T *y = WITH_Y ? Y + (long long)row * ldy + c0 : nullptr;
     float z[D];
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-        const unsigned u = first + d * (kThreads / 32), row = u / b.per_row;
-        const int col = int(u - row * b.per_row) * ACT8_BLOCK + lane;
-        z[d] = (u < b.units && col < b.K) ? to_f32(Z[(long long)row * ldz + col]) : 0.0f;
+    for (int d = 0; d < D; ++d) z[d] = c0 + d * ACT8_BLOCK < b.K ? to_f32(zr[d * ACT8_BLOCK]) : 0.0f;
+    if constexpr (WITH_Y) {
+#pragma unroll
+        for (int d = 0; d < D; d += 2) {
+            const float2 v = activate<ACT>(make_float2(z[d], z[d + 1]));
+            if (c0 + d * ACT8_BLOCK < b.K) y[d * ACT8_BLOCK] = from_f32<T>(v.x);
+            if (c0 + (d + 1) * ACT8_BLOCK < b.K) y[(d + 1) * ACT8_BLOCK] = from_f32<T>(v.y);
+        }
     }
+    // lane d works out the exponent of block d
+    uint32_t top = 0;
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-        const unsigned u = first + d * (kThreads / 32), row = u / b.per_row;
-        const int block = int(u - row * b.per_row), col = block * ACT8_BLOCK + lane;
-        const int e = act8_exponent(__reduce_max_sync(0xffffffffu, magnitude_bits(z[d])));
-        if (u >= b.units) continue;
-        if (lane == 0) c.e[row * c.lde + block] = static_cast<signed char>(e);
-        if (col >= b.K) continue;
-        const int q = e == ACT8_NAN ? 0 : act8_quantise(z[d], act8_inverse_step(e));
-        c.q[row * c.ldq + col] = static_cast<signed char>(q);
-        if constexpr (WITH_Y) Y[(long long)row * ldy + col] = from_f32<T>(activate<ACT>(z[d]));
+        const uint32_t t = __reduce_max_sync(0xffffffffu, magnitude_bits(z[d]));
+        if (lane == d) top = t;
+    }
+    const int ex = act8_exponent(top);
+    if (lane < D && c0 - lane + lane * ACT8_BLOCK < b.K) e[lane] = static_cast<signed char>(ex);
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        const int of = __shfl_sync(0xffffffffu, ex, d);
+        const int v = of == ACT8_NAN ? 0 : act8_quantise(z[d], act8_inverse_step(of));
+        if (c0 + d * ACT8_BLOCK < b.K) q[d * ACT8_BLOCK] = static_cast<signed char>(v);
     }
 }
 
@@ -158,7 +195,7 @@ __global__ void __launch_bounds__(kThreads)
 template <class T, int ACT, bool GRAD>
 __global__ void __launch_bounds__(kThreads)
     read_wide_kernel(Blocks b, Checkpoint c, const T *dY, long long lddy, T *out, long long ldo) {
-    constexpr int D = kDepth<T>;
+    constexpr int D = kReadDepth;
     const int sub = threadIdx.x & 3;
     const unsigned first = (blockIdx.x * D) * (kThreads / 4) + (threadIdx.x >> 2);
     uint2 w[D];
@@ -186,9 +223,10 @@ __global__ void __launch_bounds__(kThreads)
         unpack_s8(w[d].x, z);
         unpack_s8(w[d].y, z + 4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            z[i] *= step;
-            if constexpr (GRAD) z[i] = dy[d][i] * slope<ACT>(z[i]);
+        for (int i = 0; i < 8; i += 2) {
+            float2 v = __fmul2_rn(make_float2(z[i], z[i + 1]), both(step));
+            if constexpr (GRAD) v = __fmul2_rn(make_float2(dy[d][i], dy[d][i + 1]), slope<ACT>(v));
+            z[i] = v.x, z[i + 1] = v.y;
         }
         store8(out + (long long)row[d] * ldo + col[d], z);
     }
@@ -199,24 +237,28 @@ __global__ void __launch_bounds__(kThreads)
     read_any_kernel(Blocks b, Checkpoint c, const T *dY, long long lddy, T *out, long long ldo) {
     constexpr int D = kAnyDepth;
     const int lane = threadIdx.x & 31;
-    const unsigned first = (blockIdx.x * D) * (kThreads / 32) + (threadIdx.x >> 5);
-    float z[D], dy[D];
+    const unsigned u = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), row = u / b.per_row;
+    if (u >= b.units) return;
+    const int c0 = int(u - row * b.per_row) * (D * ACT8_BLOCK) + lane;
+    const signed char *q = c.q + row * c.ldq + c0, *e = c.e + row * c.lde + (c0 - lane) / ACT8_BLOCK;
+    const T *dyr = GRAD ? dY + (long long)row * lddy + c0 : nullptr;
+    T *to = out + (long long)row * ldo + c0;
+    signed char w[D];
+    float dy[D];
+    const int mine = lane < D && c0 - lane + lane * ACT8_BLOCK < b.K ? e[lane] : 0;
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-        const unsigned u = first + d * (kThreads / 32), row = u / b.per_row;
-        const int block = int(u - row * b.per_row), col = block * ACT8_BLOCK + lane;
-        if (u >= b.units || col >= b.K) continue;
-        z[d] = float(c.q[row * c.ldq + col]) * act8_step(c.e[row * c.lde + block]);
-        if constexpr (GRAD) dy[d] = to_f32(dY[(long long)row * lddy + col]);
+        const bool in = c0 + d * ACT8_BLOCK < b.K;
+        w[d] = in ? q[d * ACT8_BLOCK] : 0;
+        if constexpr (GRAD) dy[d] = in ? to_f32(dyr[d * ACT8_BLOCK]) : 0.0f;
     }
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-        const unsigned u = first + d * (kThreads / 32), row = u / b.per_row;
-        const int col = int(u - row * b.per_row) * ACT8_BLOCK + lane;
-        if (u >= b.units || col >= b.K) continue;
-        float v = z[d];
-        if constexpr (GRAD) v = dy[d] * slope<ACT>(v);
-        out[(long long)row * ldo + col] = from_f32<T>(v);
+    for (int d = 0; d < D; d += 2) {
+        float2 v = make_float2(float(w[d]) * act8_step(__shfl_sync(0xffffffffu, mine, d)),
+                               float(w[d + 1]) * act8_step(__shfl_sync(0xffffffffu, mine, d + 1)));
+        if constexpr (GRAD) v = __fmul2_rn(make_float2(dy[d], dy[d + 1]), slope<ACT>(v));
+        if (c0 + d * ACT8_BLOCK < b.K) to[d * ACT8_BLOCK] = from_f32<T>(v.x);
+        if (c0 + (d + 1) * ACT8_BLOCK < b.K) to[(d + 1) * ACT8_BLOCK] = from_f32<T>(v.y);
     }
 }
 
@@ -258,22 +300,26 @@ int over_rows(int M, int K, F &&launch) {
     return SGEMM_OK;
 }
 
+Blocks blocks_in(int rows, int K, bool wide_form) {
+    const unsigned per_row = unsigned(wide_form ? blocks_of(K) : (blocks_of(K) + kAnyDepth - 1) / kAnyDepth);
+    return Blocks{unsigned(rows) * per_row, per_row, K};
+}
 unsigned grid_of(unsigned units, unsigned per_block) { return (units + per_block - 1) / per_block; }
 
 template <class T, int ACT, bool WITH_Y>
 int store(int M, int K, const T *Z, int ldz, Checkpoint c, T *Y, int ldy, cudaStream_t stream) {
     const bool w = K % 8 == 0 && wide(Z, ldz) && wide(Y, ldy) && wide(c.q, int(c.ldq));
     return over_rows(M, K, [&](long long r, int rows) {
-        const Blocks b{unsigned(rows) * unsigned(blocks_of(K)), unsigned(blocks_of(K)), K};
+        const Blocks b = blocks_in(rows, K, w);
         const Checkpoint at{c.q + r * c.ldq, c.e + r * c.lde, c.ldq, c.lde};
         T *y = WITH_Y ? Y + r * ldy : nullptr;
         if (w)
             store_wide_kernel<T, ACT, WITH_Y>
-                <<<grid_of(b.units, kDepth<T> * kThreads / 4), kThreads, 0, stream>>>(
+                <<<grid_of(b.units, kStoreDepth<T> * kThreads / 4), kThreads, 0, stream>>>(
                     b, Z + r * ldz, ldz, at, y, ldy);
         else
             store_any_kernel<T, ACT, WITH_Y>
-                <<<grid_of(b.units, kAnyDepth * kThreads / 32), kThreads, 0, stream>>>(
+                <<<grid_of(b.units, kThreads / 32), kThreads, 0, stream>>>(
                     b, Z + r * ldz, ldz, at, y, ldy);
         sgh::count_launch(w ? "act8 store, rows read 16 bytes at a time"
                             : "act8 store, any alignment");
@@ -284,16 +330,16 @@ template <class T, int ACT, bool GRAD>
 int read(int M, int K, Checkpoint c, const T *dY, int lddy, T *out, int ldo, cudaStream_t stream) {
     const bool w = K % 8 == 0 && wide(dY, lddy) && wide(out, ldo) && wide(c.q, int(c.ldq));
     return over_rows(M, K, [&](long long r, int rows) {
-        const Blocks b{unsigned(rows) * unsigned(blocks_of(K)), unsigned(blocks_of(K)), K};
+        const Blocks b = blocks_in(rows, K, w);
         const Checkpoint at{c.q + r * c.ldq, c.e + r * c.lde, c.ldq, c.lde};
         const T *dy = GRAD ? dY + r * lddy : nullptr;
         if (w)
             read_wide_kernel<T, ACT, GRAD>
-                <<<grid_of(b.units, kDepth<T> * kThreads / 4), kThreads, 0, stream>>>(
+                <<<grid_of(b.units, kReadDepth * kThreads / 4), kThreads, 0, stream>>>(
                     b, at, dy, lddy, out + r * ldo, ldo);
         else
             read_any_kernel<T, ACT, GRAD>
-                <<<grid_of(b.units, kAnyDepth * kThreads / 32), kThreads, 0, stream>>>(
+                <<<grid_of(b.units, kThreads / 32), kThreads, 0, stream>>>(
                     b, at, dy, lddy, out + r * ldo, ldo);
         sgh::count_launch(w ? "act8 read, rows read 16 bytes at a time"
                             : "act8 read, any alignment");

@@ -42,12 +42,24 @@ __device__ __forceinline__ float act8_step(int e) {
     return e == ACT8_NAN ? __uint_as_float(0x7fc00000u) : __uint_as_float(uint32_t(e + 127) << 23);
 }
 
-// Four int8 of a word as floats.
+// Conversions between int8 and float by way of the low bits of a float of known exponent:
+// the converting instructions run at a quarter of the rate of these.
+//
+// Four int8 of a word as floats: 2^23 + (q + 128) by its bytes, less 2^23 + 128.
 __device__ __forceinline__ void unpack_s8(uint32_t w, float *v) {
-    v[0] = float(int(w << 24) >> 24);
-    v[1] = float(int(w << 16) >> 24);
-    v[2] = float(int(w << 8) >> 24);
-    v[3] = float(int(w) >> 24);
+    w ^= 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540u + i)) - 8388736.0f;
+}
+// Four values of at most 127 in magnitude after scaling, rounded to nearest even, as the
+// bytes of a word: 1.5 * 2^23 + x keeps the integer in its low bits.
+__device__ __forceinline__ uint32_t pack_s8(const float *x, float scale) {
+    const float2 s = make_float2(scale, scale), magic = make_float2(12582912.0f, 12582912.0f);
+    const float2 a = __ffma2_rn(make_float2(x[0], x[1]), s, magic);
+    const float2 b = __ffma2_rn(make_float2(x[2], x[3]), s, magic);
+    return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                       __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
 }
 
 }  // namespace sgl
