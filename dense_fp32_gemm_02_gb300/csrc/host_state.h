@@ -40,7 +40,9 @@ cudaError_t parts_gemm_error_word(unsigned *v, bool clear);
 constexpr int kMaxDim = 0x7fffffff - 0xffff;
 
 // A launch that need not wait for the kernel before it on the stream (programmatic stream
-// serialization): the kernel itself waits where it has to.
+// serialization): its blocks start when that one's have all begun and made way, and the
+// kernel itself waits for that one's end (sg::wait_prerequisites) before it reads or
+// writes memory.  It saves the launch's latency between two kernels.
 template <class... P, class... Args>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
                          const Args &...args) {

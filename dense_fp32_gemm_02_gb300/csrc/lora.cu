@@ -104,8 +104,21 @@ bool in_place(const T *p, int ld) {
     return sizeof(T) == 2 && aligned(p, 16) && ld % 8 == 0;
 }
 
+template <class T>
+Stack<const T> stack_of(const void *p, int ld, long long stride) {
+    return {static_cast<const T *>(p), ld, stride};
+}
+template <class T>
+bool wide_rows(const T *p, long long ld) {
+    return aligned(p, 16) && ld % (16 / (long long)sizeof(T)) == 0;
+}
+template <class T>
+bool wide_stack(const Stack<T> &v, int L) {
+    return wide_rows(v.p, v.ld) && (L <= 1 || v.stride % (16 / (long long)sizeof(T)) == 0);
+}
+
 // The parts of a rows x cols matrix as an operand: the matrix itself, or planes in the
-// workspace that pack() fills.
+// workspace that prepare_kernel fills.
 template <class T>
 struct Packed {
     static constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
@@ -124,13 +137,8 @@ struct Packed {
     void place(sgh::Workspace &ws) {
         if (!direct) parts = Parts{ws.take<bf16>(elements()), pitch, rows * pitch};
     }
-    int pack(int sms, cudaStream_t stream) const {
-        if (direct) return SGEMM_OK;
-        const bool wide = aligned(src, 16) && ld % (16 / sizeof(T)) == 0;
-        const long long threads = rows * (pitch / 8);
-        const unsigned grid = unsigned(std::min<long long>((threads + 255) / 256, sms * 16LL));
-        parts_kernel<PARTS><<<grid, 256, 0, stream>>>(int(rows), int(cols), Rows<T>{src, ld}, wide, parts);
-        return launched();
+    PartsJob<Rows<T>> job() const {   // (no rows where the TMA reads the matrix itself)
+        return {Rows<T>{src, ld}, direct ? 0 : int(rows), int(cols), wide_rows(src, ld), parts};
     }
     sgp::Operand operand() const {
         if (direct)
@@ -138,19 +146,6 @@ struct Packed {
         return {parts.p, cols, rows, PARTS, pitch, rows * pitch};
     }
 };
-
-template <class T>
-Stack<const T> stack_of(const void *p, int ld, long long stride) {
-    return {static_cast<const T *>(p), ld, stride};
-}
-template <class T>
-bool wide_rows(const T *p, long long ld) {
-    return aligned(p, 16) && ld % (16 / (long long)sizeof(T)) == 0;
-}
-template <class T>
-bool wide_stack(const Stack<T> &v, int L) {
-    return wide_rows(v.p, v.ld) && (L <= 1 || v.stride % (16 / (long long)sizeof(T)) == 0);
-}
 
 // Raises a kernel's shared memory limit; on every launch, as it costs less than
 // remembering the devices it was done on.
@@ -161,18 +156,41 @@ int shared_limit(K kernel, size_t bytes) {
     return e == cudaSuccess ? SGEMM_OK : sgh::cuda_fail(e);
 }
 
-// ------------------------------------------------------------------ rows by adapter
-// The grouping of a call's rows: sizes, workspace and the launch that makes it.
+// A launch after current_device(): early (host_state.h), counted, its errors returned.
+template <class... P, class... Args>
+int launch(const char *text, void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+           const Args &...args) {
+    const cudaError_t e = sgh::launch_early(kernel, grid, threads, smem, stream, args...);
+    return e == cudaSuccess ? launched(text) : sgh::cuda_fail(e);
+}
+
+// ------------------------------------------------------------------ the first kernel
+// Groups the rows (g.perm not null) and takes the operands' parts; nothing where there is
+// neither.
+template <int P_PARTS, int Q_PARTS, class XP, class XQ>
+int prepare(int M, const Adapters &ad, const Groups &g, const PartsJob<XP> &p, const PartsJob<XQ> &q, int sms,
+            cudaStream_t stream) {
+    const long long octets = p.octets() + q.octets();
+    const long long blocks = std::min<long long>((octets + SORT_THREADS - 1) / SORT_THREADS, 8LL * sms);
+    const size_t smem = g.perm ? sort_smem(ad.L) : 0;
+    if (blocks == 0 && !g.perm) return SGEMM_OK;
+    auto kernel = prepare_kernel<P_PARTS, Q_PARTS, XP, XQ>;
+    const int st = shared_limit(kernel, smem);
+    if (st != SGEMM_OK) return st;
+    // (no block but the grouping one: that one's own step is then never used)
+    return launch(nullptr, kernel, dim3(unsigned(blocks + (g.perm ? 1 : 0))), SORT_THREADS, smem, stream, M, ad, g, p, q);
+}
+
+// Sizes and workspace of the grouping of a call's rows.
 struct Grouping {
     int M, L, chunk, max_tiles, max_chunks, tiles256, width, capacity;
     Groups g{};
 
     // chunk: rows of a partial sum of the stack's gradients, 512 where that makes
-    // blocks for every SM twice, else down to 128 (`columns`: of the wider gradient).
-    Grouping(const Call &c, int columns, int sms) : M(c.M), L(c.L), chunk(512) {
+    // blocks for every SM twice, else down to 128 (`columns`: of both gradients).
+    Grouping(const Call &c, long long columns, int sms) : M(c.M), L(c.L), chunk(CHUNK_ROWS) {
         const long long across = (columns + 127) / 128;
         while (chunk > 128 && (M / chunk) * across < 2LL * sms) chunk /= 2;
-        while (M / chunk + L > 65535) chunk *= 2;   // the grid's limit
         max_tiles = M / ROW_TILE + L + 1;
         max_chunks = M / chunk + L;
         tiles256 = (M + 255) / 256;
@@ -183,164 +201,209 @@ struct Grouping {
     }
     size_t bytes() const {
         const auto piece = [](size_t n) { return sgh::Workspace::piece(n); };
-        return piece(size_t(M) * 4) + piece(8) + piece(size_t(max_tiles) * 16) + piece(size_t(max_chunks) * 16) +
-               piece(size_t(L + 1) * 4) + piece(size_t(L) * 4) + piece(size_t(tiles256) * 8) +
-               piece(size_t(capacity) * 16) + piece(size_t(M) * 4);
+        return L == 0 ? 0
+                      : 2 * piece(size_t(M) * 4) + piece(size_t(max_tiles) * 16) + piece(size_t(max_chunks) * 16) +
+                            piece(size_t(L + 1) * 4) + 2 * piece(size_t(L) * 4) + piece(size_t(tiles256) * 8) +
+                            piece(size_t(capacity) * 16);
     }
-    int make(sgh::Workspace &ws, const Adapters &ad, cudaStream_t stream) {
-        g = Groups{ws.take<int>(M), ws.take<int>(2), ws.take<int4>(max_tiles), ws.take<int4>(max_chunks),
-                   ws.take<int>(L + 1), chunk, ws.take<int>(L), ws.take<int2>(tiles256), ws.take<int4>(capacity),
-                   ws.take<int>(M), capacity, width};
-        const int st = shared_limit(group_rows_kernel, sort_smem(L));
-        if (st != SGEMM_OK) return st;
-        group_rows_kernel<<<1, SORT_THREADS, sort_smem(L), stream>>>(M, ad, g);
-        return launched();
+    void place(sgh::Workspace &ws) {
+        if (L == 0) return;
+        g.perm = ws.take<int>(M);
+        g.tiles = ws.take<int4>(max_tiles);
+        g.chunks = ws.take<int4>(max_chunks);
+        g.chunk_begin = ws.take<int>(L + 1);
+        g.max_tiles = max_tiles, g.max_chunks = max_chunks, g.chunk = chunk;
+        g.used = ws.take<int>(L);
+        g.unclean = ws.take<int>(L);
+        g.planes = ws.take<int2>(tiles256);
+        g.plane_adapter = ws.take<int4>(capacity);
+        g.position = ws.take<int>(M);
+        g.capacity = capacity, g.width = width;
     }
 };
 
-// Ranges of the rank side's contraction: blocks for every SM twice over, none of them
-// below 256 deep.
+// ------------------------------------------------------------------ rank side
+template <class T>
+struct RankKernel {
+    void (*kernel)(RankWork<T>, Adapters, Groups);
+    size_t smem;
+
+    template <bool TRANS, int NT>
+    static constexpr RankKernel of() {
+        return {&rank_tile_kernel<T, TRANS, NT>, RankTile<T, TRANS, NT>::SMEM};
+    }
+    template <bool TRANS>
+    static constexpr RankKernel pick(int R) {
+        return R <= 16 ? of<TRANS, 2>() : R <= 32 ? of<TRANS, 4>() : R <= 64 ? of<TRANS, 8>() : of<TRANS, 16>();
+    }
+};
+
+// Ranges of the rank side's contraction, C deep: the count whose waves of blocks (of about
+// one tile more for each adapter than M has) take the fewest slabs, with three for filling
+// and emptying; a range is at least 256 deep.
 struct RankSplit {
     int range, ranges;
-    RankSplit(int M, int C, int sms) {
-        const long long tiles = (M + ROW_TILE - 1) / ROW_TILE;
-        long long n = std::max(1LL, std::min<long long>((2LL * sms + tiles - 1) / tiles, C / 256));
-        range = int(((C + n - 1) / n + SLAB - 1) / SLAB * SLAB);
-        ranges = range > 0 ? (C + range - 1) / range : 1;
+    RankSplit(int M, int L, int C, size_t smem, int sms) {
+        const long long slots = (long long)sms * std::max<size_t>(1, std::min<size_t>(2, (227 * 1024) / (smem + 1280)));
+        const long long tiles = (M + ROW_TILE - 1) / ROW_TILE, all = tiles + std::min<long long>(L, tiles) / 2;
+        const long long slabs = (C + SLAB - 1LL) / SLAB;
+        long long least = 0;
+        range = SLAB;
+        for (long long n = 1; n <= std::max(1LL, std::min(slabs / 4, 32LL)); ++n) {
+            const long long per = std::max(1LL, (slabs + n - 1) / n);
+            const long long cost = ((all * n + slots - 1) / slots) * (per + 3);
+            if (n == 1 || cost < least) least = cost, range = int(per * SLAB);
+        }
+        ranges = std::max(1, int((C + (long long)range - 1) / range));
     }
 };
 
-template <class T, bool TRANS, int NT>
-int rank_side_nt(const Grouping &gr, int C, const RankSplit &split, Rows<T> X, Stack<const T> V, const Adapters &ad,
-                 float *partial, cudaStream_t stream) {
-    auto kernel = rank_tile_kernel<T, TRANS, NT>;
-    constexpr size_t smem = RankTile<T, TRANS, NT>::SMEM;
-    const int st = shared_limit(kernel, smem);
-    if (st != SGEMM_OK) return st;
-    kernel<<<dim3(unsigned(gr.max_tiles), unsigned(split.ranges)), RANK_THREADS, smem, stream>>>(
-        C, split.range, X, wide_rows(X.p, X.ld), V, wide_stack(V, ad.L), ad, gr.g, partial,
-        (long long)gr.M * ad.R);
-    return launched();
-}
+// ------------------------------------------------------------------ stack gradients
+template <class XA, class T>
+struct StackKernel {
+    void (*kernel)(StackWork<XA>, StackWork<Rows<T>>, int, int, Adapters, Groups);
+    size_t smem;
 
-// S (and H, and the planes) of a call: C is the contraction.
-template <class T, bool TRANS>
-int rank_side(const Grouping &gr, int C, const RankSplit &split, Rows<T> X, Stack<const T> V, const Adapters &ad,
-              float *partial, const int *unclean, const RankSide &to, cudaStream_t stream) {
-    auto run = ad.R <= 16 ? rank_side_nt<T, TRANS, 2> : ad.R <= 32 ? rank_side_nt<T, TRANS, 4>
-               : ad.R <= 64 ? rank_side_nt<T, TRANS, 8> : rank_side_nt<T, TRANS, 16>;
-    const int st = run(gr, C, split, X, V, ad, partial, stream);
-    if (st != SGEMM_OK) return st;
-    rank_finish_kernel<T><<<unsigned((gr.M + 7) / 8), 256, 0, stream>>>(gr.M, split.ranges, partial,
-                                                                      (long long)gr.M * ad.R, ad, gr.g, unclean, to);
-    return launched();
-}
+    template <int NT>
+    static constexpr StackKernel of() {
+        constexpr int PB = sizeof(T) == 4 ? 3 : 2;
+        constexpr size_t a = StackTile<XA, PB, NT>::SMEM, b = StackTile<Rows<T>, PB, NT>::SMEM;
+        return {&stack_tile_kernel<XA, T, NT>, a > b ? a : b};
+    }
+    static constexpr StackKernel pick(int R) {
+        return R <= 16 ? of<2>() : R <= 32 ? of<4>() : R <= 64 ? of<8>() : of<16>();
+    }
+};
 
-template <class X, int PB, int NT, bool RANK_ROWS>
-int stack_grad_nt(const Grouping &gr, int C, X x, bool x_wide, const float *S, long long lds, bool scaled,
-                  const Adapters &ad, float *partial, cudaStream_t stream) {
-    auto kernel = stack_tile_kernel<X, PB, NT, RANK_ROWS>;
-    using Z = StackTile<X, PB, NT>;
-    const int st = shared_limit(kernel, Z::SMEM);
-    if (st != SGEMM_OK) return st;
-    const unsigned across = unsigned((C + Z::COLS - 1) / Z::COLS);
-    kernel<<<dim3(across, unsigned(gr.max_chunks)), RANK_THREADS, Z::SMEM, stream>>>(C, x, x_wide, S, lds, scaled, ad,
-                                                                                    gr.g, partial);
-    return launched("lora backward, rows grouped by adapter");
-}
-
-// The gradient of a stack, C x R for each adapter (R x C where RANK_ROWS), from X's rows
-// and S.  partial: max_chunks x C x R.
-template <class T, bool RANK_ROWS, class X>
-int stack_grad(const Grouping &gr, int C, X x, bool x_wide, const float *S, long long lds, bool scaled,
-               const Adapters &ad, float *partial, Stack<T> out, int sms, cudaStream_t stream) {
-    constexpr int PB = sizeof(T) == 4 ? 3 : 2;
-    if (gr.M > 0) {
-        auto run = ad.R <= 16   ? stack_grad_nt<X, PB, 2, RANK_ROWS>
-                   : ad.R <= 32 ? stack_grad_nt<X, PB, 4, RANK_ROWS>
-                   : ad.R <= 64 ? stack_grad_nt<X, PB, 8, RANK_ROWS>
-                                : stack_grad_nt<X, PB, 16, RANK_ROWS>;
-        const int st = run(gr, C, x, x_wide, S, lds, scaled, ad, partial, stream);
+// dA and dB from X's rows (or their checkpoint's) and dY's, and the parts of G and H.
+template <class T, class XA>
+int stack_gradients(const Call &c, const Grouping &gr, XA x, bool x_wide, const bf16 *s_rows, const bf16 *h_rows,
+                    int pitch, float *partial_a, float *partial_b, int sms) {
+    const Adapters ad = c.adapters();
+    const Rows<T> dy{static_cast<const T *>(c.dY), c.lddy};
+    int st;
+    if (c.M > 0) {
+        const auto k = StackKernel<XA, T>::pick(c.R);
+        if ((st = shared_limit(k.kernel, k.smem)) != SGEMM_OK) return st;
+        const StackWork<XA> wa{c.K, x, x_wide, s_rows, partial_a};
+        const StackWork<Rows<T>> wb{c.N, dy, wide_rows(dy.p, dy.ld), h_rows, partial_b};
+        const long long blocks = ((c.K + 127LL) / 128 + (c.N + 127LL) / 128) * gr.max_chunks;
+        if (blocks > 0x7fffffffLL) return SGEMM_ERR_TOO_LARGE;
+        st = launch("lora backward, rows grouped by adapter", k.kernel, dim3(unsigned(blocks)), RANK_THREADS, k.smem,
+                    c.stream, wa, wb, c.M, pitch, ad, gr.g);
         if (st != SGEMM_OK) return st;
     }
-    const long long plane = (long long)C * ad.R;
-    const dim3 grid(unsigned(std::min<long long>((plane + 255) / 256, sms * 8LL)), unsigned(ad.L));
-    stack_finish_kernel<T><<<grid, 256, 0, stream>>>(RANK_ROWS ? ad.R : C, RANK_ROWS ? C : ad.R, partial, gr.g, out);
-    return launched();
+    const long long plane = ((long long)c.K + c.N) * c.R;
+    const dim3 grid(unsigned(std::min<long long>((plane + 255) / 256, sms * 8LL)), unsigned(c.L));
+    return launch(nullptr, stack_finish_kernel<T>, grid, 256, 0, c.stream, c.K, c.N, c.R, (const float *)partial_a,
+                  (const float *)partial_b, gr.g, Stack<T>{static_cast<T *>(c.dA), c.ldda, c.stride_da},
+                  Stack<T>{static_cast<T *>(c.dB), c.lddb, c.stride_db});
 }
 
-// out (M x N) = P * Q + rank-side term of P's rows.
-//   forward:  P = X (M x K), Q = W (K x N), S = scale X A, V = B
-//   backward: P = dY, Q = W^T (N x K stored), S = G, V = A^T
-// `S`, where given, receives the rank-side sums for the caller.
+// ------------------------------------------------------------------ many rows
+// Forward: Y = X W + bias + rank side, S = scale X A.  Backward: dX = dY W^T + G A^T with
+// G = scale dY B^T, and the stack's gradients.  In either, with P (X or dY), V1 (A or B^T)
+// and V2 (B or A^T): group the rows and take P's and W's parts; S = P V1 and V2's layout;
+// S into its planes; P W + S V2 on the tensor cores.
 template <class T, bool BACK>
-int projection(const Call &c, const Grouping &gr, float *S, float *H, int ldh, void *out, int ldo, int sms,
-               cudaMemPool_t pool) {
+int many_rows(const Call &c, int sms, cudaMemPool_t pool) {
     int st;
     const Adapters ad = c.adapters();
     const int M = c.M, N = BACK ? c.K : c.N, K = BACK ? c.N : c.K;
-    const bool ranked = c.L > 0, want_out = out && N > 0, product = want_out && K > 0;
+    void *out = BACK ? c.dX : c.Y;
+    const bool ranked = c.L > 0, want_out = out && N > 0 && M > 0, product = want_out && K > 0;
+    const bool planes = ranked && product, want_stack = BACK && ranked && (c.dA || c.dB);
     constexpr auto LAYOUT = BACK ? sgp::INPUT_GRAD : sgp::FORWARD;
-    constexpr int PRODUCTS = sizeof(T) == 4 ? 6 : 1, S_PARTS = sizeof(T) == 4 ? 3 : 2;
+    constexpr int PRODUCTS = sizeof(T) == 4 ? 6 : 1, S_PARTS = sizeof(T) == 4 ? 3 : 2, PARTS = Packed<T>::PARTS;
     Packed<T> P(M, K, BACK ? c.dY : c.X, BACK ? c.lddy : c.ldx), Q(c.K, c.N, c.W, c.ldw);
+    if (!product) P.direct = Q.direct = true;   // no parts are needed
     const sgp::Split split = product ? sgp::plan_split(M, N, K, PRODUCTS, sms) : sgp::Split{0, 0};
-    const bool planes = ranked && product;   // the rank side in the MMA loop
+    Grouping gr(c, want_stack ? (long long)c.K + c.N : 0, sms);
+    const RankKernel<T> rank = RankKernel<T>::template pick<BACK>(c.R);
+    const RankSplit ranges(M, c.L, K, rank.smem, sms);
+    const int pitch = c.R <= 16 ? 16 : c.R <= 32 ? 32 : c.R <= 64 ? 64 : 128;
     const long long vpitch = pitch8(N), vplane = gr.width * vpitch;
-    const RankSplit ranges(M, K, sms);
 
     sgh::Workspace ws(pool, c.stream);
     const auto piece = [](size_t n) { return sgh::Workspace::piece(n); };
-    const size_t s_floats = ranked && !S ? size_t(M) * c.R : 0;
-    const size_t r_floats = ranked ? size_t(ranges.ranges) * M * c.R : 0;
+    const size_t s_floats = ranked ? size_t(M) * c.R : 0, r_floats = s_floats * ranges.ranges;
     const size_t h_elems = planes ? size_t(S_PARTS) * gr.capacity * 256 * 64 : 0;
-    const size_t v_elems = planes ? size_t(Packed<T>::PARTS) * c.L * vplane : 0;
-    st = ws.allocate(piece(s_floats * 4) + piece(r_floats * 4) + piece(h_elems * 2) + piece(v_elems * 2) +
-                     (planes ? piece(size_t(c.L) * 4) : 0) +
-                     (product ? P.bytes() + Q.bytes() + piece(split.partial_floats * 4) : 0));
+    const size_t v_elems = planes ? size_t(PARTS) * c.L * vplane : 0;
+    const size_t row_elems = want_stack ? size_t(S_PARTS) * M * pitch : 0;
+    const size_t pa_floats = want_stack ? size_t(gr.max_chunks) * c.R * c.K : 0;
+    const size_t pb_floats = want_stack ? size_t(gr.max_chunks) * c.R * c.N : 0;
+    st = ws.allocate(gr.bytes() + piece(s_floats * 4) + piece(r_floats * 4) + piece(h_elems * 2) + piece(v_elems * 2) +
+                     2 * piece(row_elems * 2) + piece(pa_floats * 4) + piece(pb_floats * 4) + P.bytes() + Q.bytes() +
+                     piece(split.partial_floats * 4));
     if (st != SGEMM_OK) return st;
-    RankSide side{S, H, ldh, nullptr};
-    if (s_floats) side.S = ws.take<float>(s_floats);
-    float *r_partial = r_floats ? ws.take<float>(r_floats) : nullptr;
+    gr.place(ws);
+    RankSide side{ws.take<float>(s_floats), c.H, c.ldh, nullptr, nullptr, nullptr, pitch};
+    float *r_partial = ws.take<float>(r_floats);
     const Stack<const T> A = stack_of<T>(c.A, c.lda, c.stride_a), B = stack_of<T>(c.B, c.ldb, c.stride_b);
     Parts v{};
-    int *unclean = nullptr;
     if (planes) {
         side.planes = ws.take<bf16>(h_elems);
         v = Parts{ws.take<bf16>(v_elems), vpitch, vplane};
-        unclean = ws.take<int>(c.L);
-        const cudaError_t e = cudaMemsetAsync(unclean, 0, size_t(c.L) * 4, c.stream);
-        if (e != cudaSuccess) return sgh::cuda_fail(e);
-        pack_stack_kernel<T, BACK><<<dim3(unsigned((N + 63) / 64), unsigned(c.L)), 256, 0, c.stream>>>(
-            N, BACK ? A : B, ad, gr.g.used, gr.width, unclean, v);
-        if ((st = launched()) != SGEMM_OK) return st;
     }
-    if (ranked && (st = rank_side<T, BACK>(gr, K, ranges, Rows<T>{P.src, P.ld}, BACK ? B : A, ad, r_partial, unclean,
-                                           side, c.stream)) != SGEMM_OK)
-        return st;
-    if (!want_out) return ws.release();
-    sgp::Epilogue<T, BACK> epi{ad, side.S, c.R, BACK ? A : B, BACK ? nullptr : static_cast<const T *>(c.bias),
-                               0.0f, static_cast<T *>(out), ldo};
-    if (!product) {   // K == 0: the epilogue of a zero sum
-        if ((st = sgp::finish<T, BACK>(M, N, 0, nullptr, nullptr, epi, c.stream)) != SGEMM_OK) return st;
-        return ws.release();
+    if (want_stack) {
+        side.s_rows = ws.take<bf16>(row_elems);
+        side.h_rows = ws.take<bf16>(row_elems);
+    } else if (BACK) {
+        side.H = nullptr;
     }
+    float *pa = ws.take<float>(pa_floats), *pb = ws.take<float>(pb_floats);
     P.place(ws);
     Q.place(ws);
     float *partial = split.partial_floats ? ws.take<float>(split.partial_floats) : nullptr;
-    if ((st = P.pack(sms, c.stream)) != SGEMM_OK || (st = Q.pack(sms, c.stream)) != SGEMM_OK) return st;
-    sgp::Product g;
-    g.M = M, g.N = N, g.K = K;
-    g.a = P.operand();
-    g.b = Q.operand();
-    if (planes) {
-        g.h = {side.planes, 64, 256, (long long)S_PARTS * gr.capacity, 64, 256 * 64};
-        g.v = {v.p, N, gr.width, (long long)Packed<T>::PARTS * c.L, vpitch, vplane};
-        g.planes = gr.g.planes;
-        g.plane_adapter = gr.g.plane_adapter;
-        g.capacity = gr.capacity;
-        g.width = gr.width;
+
+    st = prepare<PARTS, PARTS>(M, ad, gr.g, P.job(), Q.job(), sms, c.stream);
+    if (st != SGEMM_OK) return st;
+    if (ranked && M > 0) {
+        const long long tiles = (long long)gr.max_tiles * ranges.ranges;
+        const long long blocks = tiles + (planes ? (N + 63LL) / 64 * c.L : 0);
+        if (blocks > 0x7fffffffLL) return SGEMM_ERR_TOO_LARGE;
+        const Stack<const T> &V = BACK ? B : A, &other = BACK ? A : B;
+        const RankWork<T> w{K, ranges.range, int(tiles), Rows<T>{P.src, P.ld}, V, wide_rows(P.src, P.ld),
+                            wide_stack(V, c.L), r_partial, (long long)M * c.R, planes ? N : 0, other, v};
+        if ((st = shared_limit(rank.kernel, rank.smem)) != SGEMM_OK) return st;
+        st = launch(nullptr, rank.kernel, dim3(unsigned(blocks)), RANK_THREADS, rank.smem, c.stream, w, ad, gr.g);
+        if (st != SGEMM_OK) return st;
+        st = launch(nullptr, rank_finish_kernel<T>, dim3(unsigned((M + 7LL) / 8)), 256, 0, c.stream, M, ranges.ranges,
+                    (const float *)r_partial, (long long)M * c.R, ad, gr.g, side);
+        if (st != SGEMM_OK) return st;
     }
-    if ((st = sgp::run<T, LAYOUT>(g, epi, split, partial, sms, c.stream)) != SGEMM_OK) return st;
+    if (want_out) {
+        const sgp::Epilogue<T, BACK> epi{ad, side.S, c.R, BACK ? A : B, BACK ? nullptr : static_cast<const T *>(c.bias),
+                                         0.0f, static_cast<T *>(out), BACK ? c.lddx : c.ldy};
+        if (product) {
+            sgp::Product g;
+            g.M = M, g.N = N, g.K = K;
+            g.a = P.operand();
+            g.b = Q.operand();
+            if (planes) {
+                g.h = {side.planes, 64, 256, (long long)S_PARTS * gr.capacity, 64, 256 * 64};
+                g.v = {v.p, N, gr.width, (long long)PARTS * c.L, vpitch, vplane};
+                g.planes = gr.g.planes;
+                g.plane_adapter = gr.g.plane_adapter;
+                g.capacity = gr.capacity;
+                g.width = gr.width;
+            }
+            st = sgp::run<T, LAYOUT>(g, epi, split, partial, sms, c.stream);
+        } else {   // K == 0: the epilogue of a zero sum
+            st = sgp::finish<T, BACK>(M, N, 0, nullptr, nullptr, epi, c.stream);
+        }
+        if (st != SGEMM_OK) return st;
+    }
+    if constexpr (BACK) {
+        if (want_stack) {
+            const Rows<T> x{static_cast<const T *>(c.X), c.ldx};
+            const Act8Rows kept{c.q, c.e, c.ldq, c.lde};
+            st = c.X ? stack_gradients<T>(c, gr, x, wide_rows(x.p, x.ld), side.s_rows, side.h_rows, pitch, pa, pb, sms)
+                     : stack_gradients<T>(c, gr, kept, aligned(c.q, 16) && c.ldq % 16 == 0, side.s_rows, side.h_rows,
+                                          pitch, pa, pb, sms);
+            if (st != SGEMM_OK) return st;
+        }
+    }
     return ws.release();
 }
 
@@ -426,7 +489,8 @@ int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
     if (third) {   // what the product reads has to be there before the kernel that it overtakes
         P.place(ws);
         Q.place(ws);
-        if ((st = P.pack(sms, c.stream)) != SGEMM_OK || (st = Q.pack(sms, c.stream)) != SGEMM_OK) return st;
+        st = prepare<Packed<T>::PARTS, Packed<T>::PARTS>(c.M, ad, Groups{}, P.job(), Q.job(), sms, c.stream);
+        if (st != SGEMM_OK) return st;
     }
     const bool alone = !ranked || together;   // the product's is the first kernel of the call
     if (!alone) {
@@ -460,7 +524,7 @@ int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
         g.a = P.operand();
         g.b = Q.operand();
         st = sgp::run<T, sgp::FORWARD>(g, sgp::Epilogue<T, false>{}, split, w.partial, sms, c.stream,
-                                       alone ? sgp::PARTIALS : sgp::PARTIALS_EARLY);
+                                       alone ? sgp::PARTIALS : sgp::PARTIALS_OVERTAKING);
     }
     if (st != SGEMM_OK) return st;
     const T *bias = static_cast<const T *>(c.bias);
@@ -488,13 +552,7 @@ int forward(const Call &c) {
     int sms, st;
     cudaMemPool_t pool;
     if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
-    if (few_rows(c)) return forward_few_rows<T>(c, sms, pool);
-    sgh::Workspace ws(pool, c.stream);
-    Grouping gr(c, 0, sms);
-    if (c.L > 0 && ((st = ws.allocate(gr.bytes())) != SGEMM_OK || (st = gr.make(ws, c.adapters(), c.stream)) != SGEMM_OK))
-        return st;
-    if ((st = projection<T, false>(c, gr, nullptr, c.H, c.ldh, c.Y, c.ldy, sms, pool)) != SGEMM_OK) return st;
-    return ws.release();
+    return few_rows(c) ? forward_few_rows<T>(c, sms, pool) : many_rows<T, false>(c, sms, pool);
 }
 
 template <class T>
@@ -502,36 +560,7 @@ int backward(const Call &c) {
     int sms, st;
     cudaMemPool_t pool;
     if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
-    const Adapters ad = c.adapters();
-    const bool want_stack = (c.dA || c.dB) && c.L > 0;
-    Grouping gr(c, std::max(c.K, c.N), sms);
-    sgh::Workspace ws(pool, c.stream);
-    const auto piece = [](size_t n) { return sgh::Workspace::piece(n); };
-    const size_t g_floats = size_t(c.M) * c.R, p_floats = size_t(gr.max_chunks) * c.R * std::max(c.K, c.N);
-    float *G = nullptr, *partial = nullptr;
-    if (c.L > 0) {
-        if ((st = ws.allocate(gr.bytes() + piece(g_floats * 4) + (want_stack ? piece(p_floats * 4) : 0))) != SGEMM_OK ||
-            (st = gr.make(ws, ad, c.stream)) != SGEMM_OK)
-            return st;
-        G = ws.take<float>(g_floats);
-        if (want_stack) partial = ws.take<float>(p_floats);
-    }
-    if (c.M > 0 && (st = projection<T, true>(c, gr, G, nullptr, 0, c.dX, c.lddx, sms, pool)) != SGEMM_OK) return st;
-    if (want_stack && c.K > 0) {
-        const Stack<T> out{static_cast<T *>(c.dA), c.ldda, c.stride_da};
-        const Rows<T> x{static_cast<const T *>(c.X), c.ldx};
-        st = c.X ? stack_grad<T, false>(gr, c.K, x, wide_rows(x.p, x.ld), G, c.R, true, ad, partial, out, sms, c.stream)
-                 : stack_grad<T, false>(gr, c.K, Act8Rows{c.q, c.e, c.ldq, c.lde}, aligned(c.q, 16) && c.ldq % 16 == 0, G,
-                                        c.R, true, ad, partial, out, sms, c.stream);
-        if (st != SGEMM_OK) return st;
-    }
-    if (want_stack && c.N > 0) {
-        const Rows<T> dy{static_cast<const T *>(c.dY), c.lddy};
-        st = stack_grad<T, true>(gr, c.N, dy, wide_rows(dy.p, dy.ld), c.H, c.ldh, false, ad, partial,
-                                 Stack<T>{static_cast<T *>(c.dB), c.lddb, c.stride_db}, sms, c.stream);
-        if (st != SGEMM_OK) return st;
-    }
-    return ws.release();
+    return many_rows<T, true>(c, sms, pool);
 }
 
 template <class T>
@@ -553,10 +582,9 @@ int weight_grad(int M, int N, int K, Act8Rows x, const void *dY, int lddy, float
     const Parts xp{ws.take<bf16>(x_elems), xpitch, M * xpitch};
     D.place(ws);
     float *partial = split.partial_floats ? ws.take<float>(split.partial_floats) : nullptr;
-    const bool wide = aligned(x.q, 8) && x.ldq % 8 == 0;
-    const unsigned grid = unsigned(std::min<long long>((M * (xpitch / 8) + 255) / 256, sms * 16LL));
-    parts_kernel<1><<<grid, 256, 0, stream>>>(M, K, x, wide, xp);
-    if ((st = launched()) != SGEMM_OK || (st = D.pack(sms, stream)) != SGEMM_OK) return st;
+    const PartsJob<Act8Rows> xjob{x, M, K, aligned(x.q, 8) && x.ldq % 8 == 0, xp};
+    st = prepare<1, Packed<T>::PARTS>(M, Adapters{}, Groups{}, xjob, D.job(), sms, stream);
+    if (st != SGEMM_OK) return st;
     sgp::Product g;
     g.M = K, g.N = N, g.K = M;
     g.a = {xp.p, K, M, 1, xpitch, M * xpitch};

@@ -79,25 +79,33 @@ __device__ __forceinline__ void store_parts(const Parts &to, long long row, long
                        pack_exact(part[4][q], part[5][q]), pack_exact(part[6][q], part[7][q]));
 }
 
-// The parts of a matrix: its values, a thread to eight columns.  One part suffices
-// for bfloat16 (re-pitched for the TMA) and for a checkpoint.  `wide`: rows of X are
-// 16-byte aligned (8-byte for a checkpoint's q).
+// A matrix and where its parts go.  `wide`: its rows are 16-byte aligned (8-byte for a
+// checkpoint's q).  No rows: nothing to do.
+template <class X>
+struct PartsJob {
+    X x;
+    int rows, cols;
+    bool wide;
+    Parts to;
+
+    __host__ __device__ long long octets() const { return (long long)rows * ((cols + 7) / 8); }
+};
+
+// Octets t, t + step, ... of a job: a thread to eight columns of a row.
 template <int PARTS, class X>
-__global__ void __launch_bounds__(256) parts_kernel(int M, int K, X x, bool wide, Parts to) {
-    const int per_row = (K + 7) / 8;
-    const long long total = (long long)M * per_row;
-    for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < total;
-         t += (long long)gridDim.x * 256) {
+__device__ __forceinline__ void take_parts(const PartsJob<X> &job, long long t, long long step) {
+    const int per_row = (job.cols + 7) / 8;
+    for (const long long total = job.octets(); t < total; t += step) {
         const long long i = t / per_row;
         const int c = int(t - i * per_row) * 8;
         float v[8];
-        if (wide && c + 8 <= K) {
-            x.at8(i, c, v);
+        if (job.wide && c + 8 <= job.cols) {
+            job.x.at8(i, c, v);
         } else {
 #pragma unroll
-            for (int d = 0; d < 8; ++d) v[d] = c + d < K ? x.at(i, c + d) : 0.0f;
+            for (int d = 0; d < 8; ++d) v[d] = c + d < job.cols ? job.x.at(i, c + d) : 0.0f;
         }
-        store_parts<PARTS>(to, i, c, v);
+        store_parts<PARTS>(job.to, i, c, v);
     }
 }
 
@@ -112,12 +120,13 @@ __global__ void __launch_bounds__(256) parts_kernel(int M, int K, X x, bool wide
 // in its own adapter's columns and zeros elsewhere.
 struct Groups {
     int *perm;           // M: row numbers, group after group
-    int *totals;         // {tiles, chunks}
-    int4 *tiles;         // of up to ROW_TILE rows: {adapter or -1, first place in perm, rows, 0}
-    int4 *chunks;        // of up to `chunk` rows of an adapter: the same
+    int4 *tiles;         // of up to ROW_TILE rows: {adapter or -1, first place in perm, rows, 0},
+                         // max_tiles of them, the last without rows
+    int4 *chunks;        // of up to `chunk` rows of an adapter: the same, max_chunks of them
     int *chunk_begin;    // L + 1: the chunks of adapter a are [a], .. [a + 1]
-    int chunk;
+    int max_tiles, max_chunks, chunk;
     int *used;           // L: whether a row uses the adapter
+    int *unclean;        // L: whether it holds something that is not finite (pack_stack)
     int2 *planes;        // for each 256 rows {first plane, planes}: NO_PLANES past the capacity
     int4 *plane_adapter; // of a plane's 64 / width adapters (the last one repeated), or
                          // {adapter, first rank column} where width >= 64
@@ -157,11 +166,10 @@ __device__ __forceinline__ int group_at(const int *first, int n, int t) {
 
 constexpr size_t sort_smem(int L) { return (size_t(32) * (L + 1) + 3 * (L + 2) + 32 * 32) * 4; }
 
-// One block; each warp walks its share of the rows, 256 at a time, in three passes of
-// eight independent loads.  Bound by their latency: about 8 us up to 8192 rows.
-__global__ void __launch_bounds__(SORT_THREADS, 1)
-    group_rows_kernel(int M, Adapters ad, Groups g) {
-    extern __shared__ int sm[];
+// One block of 1024 threads; each warp walks its share of the rows, 256 at a time, in two
+// passes of eight independent loads.  Bound by their latency and the counters': 6 us up to
+// 8192 rows.
+__device__ __forceinline__ void group_rows(int M, const Adapters &ad, const Groups &g, int *sm) {
     __shared__ int warp_sum[32];
     __shared__ unsigned char no_rank[MAX_ADAPTERS];
     const int L = ad.L, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -170,7 +178,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1)
     int *tile0 = first + (L + 2), *chunk0 = tile0 + (L + 2);
     int *bits = chunk0 + (L + 2) + warp * 32;   // the adapters of this warp's current 256 rows
     const int a = threadIdx.x;
-    if (a < L) no_rank[a] = ad.rank(a) == 0;
+    if (a < L) no_rank[a] = ad.rank(a) == 0, g.unclean[a] = 0;
     for (int i = threadIdx.x; i < 32 * (L + 1); i += SORT_THREADS) count[i] = 0;
     __syncthreads();
     const int tiles = (M + 255) / 256, per = (tiles + 31) / 32;
@@ -237,7 +245,6 @@ __global__ void __launch_bounds__(SORT_THREADS, 1)
             place += n;
         }
     }
-    if (threadIdx.x == 0) g.totals[0] = tile0[L + 1], g.totals[1] = chunk0[L];
     __syncthreads();
     for (int t = t0; t < t1; ++t) {
         int b[8];
@@ -294,30 +301,58 @@ __global__ void __launch_bounds__(SORT_THREADS, 1)
             }
         }
     }
-    for (int t = threadIdx.x; t < tile0[L + 1]; t += SORT_THREADS) {
+    for (int t = threadIdx.x; t < g.max_tiles; t += SORT_THREADS) {
+        if (t >= tile0[L + 1]) {
+            g.tiles[t] = make_int4(-1, 0, 0, 0);
+            continue;
+        }
         const int b = group_at(tile0, L + 1, t), p = first[b] + (t - tile0[b]) * ROW_TILE;
         g.tiles[t] = make_int4(b < L ? b : -1, p, min(ROW_TILE, first[b + 1] - p), 0);
     }
-    for (int t = threadIdx.x; t < chunk0[L]; t += SORT_THREADS) {
+    for (int t = threadIdx.x; t < g.max_chunks; t += SORT_THREADS) {
+        if (t >= chunk0[L]) {
+            g.chunks[t] = make_int4(-1, 0, 0, 0);
+            continue;
+        }
         const int b = group_at(chunk0, L, t), p = first[b] + (t - chunk0[b]) * g.chunk;
         g.chunks[t] = make_int4(b, p, min(g.chunk, first[b + 1] - p), 0);
     }
 }
 
+// The first kernel of a call: block 0 groups the rows (where g.perm is not null), the
+// others take the parts of the product's operands that the TMA cannot read in place.
+template <int P_PARTS, int Q_PARTS, class XP, class XQ>
+__global__ void __launch_bounds__(SORT_THREADS, 1)
+    prepare_kernel(int M, Adapters ad, Groups g, PartsJob<XP> p, PartsJob<XQ> q) {
+    extern __shared__ int sm[];
+    const int groups = g.perm != nullptr;
+    sg::wait_prerequisites();
+    sg::launch_dependents();
+    if (groups && blockIdx.x == 0) {
+        group_rows(M, ad, g, sm);
+        return;
+    }
+    const long long t = (long long)(blockIdx.x - groups) * SORT_THREADS + threadIdx.x;
+    const long long step = (long long)(gridDim.x - groups) * SORT_THREADS;
+    take_parts<P_PARTS>(p, t, step);
+    take_parts<Q_PARTS>(q, t, step);
+}
+
 // The parts of the used adapters for the rank-side planes: plane part * L + a of width x
 // cols, zero past the adapter's rank, and in unclean[a] whether one of its values is not
-// finite.  TRANS: V_a is stored cols x R.  A block to 64 columns of an adapter.
+// finite.  TRANS: V_a is stored cols x R.  A block of 256 threads to 64 columns (from
+// block `bx`) of an adapter, through a 128 x 65 tile of shared memory.
 template <class T, bool TRANS>
-__global__ void __launch_bounds__(256)
-    pack_stack_kernel(int cols, Stack<const T> V, Adapters ad, const int *used, int width, int *unclean, Parts to) {
+__device__ __forceinline__ void pack_stack(int bx, int a, int cols, const Stack<const T> &V, const Adapters &ad,
+                                           const Groups &g, const Parts &to, float (*tile)[65]) {
     constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
-    __shared__ float tile[128][65];
-    const int a = blockIdx.y, c0 = blockIdx.x * 64;
-    if (!used[a]) return;
+    const int c0 = bx * 64, width = g.width;
+    if (!g.used[a]) return;
     const int rank = ad.rank(a), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const T *v = V.matrix(a);
     bool finite = true;
     if (TRANS) {   // lanes along the rank
+#pragma unroll 8
         for (int c = warp; c < 64; c += 8)
             for (int r = lane; r < width; r += 32) {
                 const float x = c0 + c < cols && r < rank ? to_f32(v[(c0 + c) * V.ld + r]) : 0.0f;
@@ -325,6 +360,7 @@ __global__ void __launch_bounds__(256)
                 tile[r][c] = x;
             }
     } else {
+#pragma unroll 4
         for (int r = warp; r < width; r += 8)
             for (int c = lane; c < 64; c += 32) {
                 const float x = c0 + c < cols && r < rank ? to_f32(v[r * V.ld + c0 + c]) : 0.0f;
@@ -332,7 +368,7 @@ __global__ void __launch_bounds__(256)
                 tile[r][c] = x;
             }
     }
-    if (!finite) unclean[a] = 1;
+    if (!finite) g.unclean[a] = 1;
     __syncthreads();
     Parts at = to;
     at.p += a * to.plane;

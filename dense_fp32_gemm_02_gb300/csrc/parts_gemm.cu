@@ -93,10 +93,11 @@ int sgp::finish(int M, int N, int splits, const float *partial, const int2 *plan
         at.ad.ids += at.ad.L > 0 ? r : 0;
         at.S += r * at.lds;
         at.out += r * at.ldo;
-        finish_kernel<<<dim3(unsigned((N + 255) / 256), unsigned(rows)), 256, 0, stream>>>(
-            M, N, splits, partial + r * N, planes, int(r), at);
+        cudaError_t e = sgh::launch_early(finish_kernel<T, TRANS>, dim3(unsigned((N + 255) / 256), unsigned(rows)), 256, 0,
+                                          stream, M, N, splits, partial + r * N, planes, int(r), at);
+        if (e != cudaSuccess) return sgh::cuda_fail(e);
         sgh::count_launch();
-        const cudaError_t e = cudaGetLastError();
+        e = cudaGetLastError();
         if (e != cudaSuccess) return sgh::cuda_fail(e);
     }
     return SGEMM_OK;
@@ -139,11 +140,9 @@ int sgp::run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Spl
     }
     const long long pairs = std::min<long long>(tiles_m * tiles_n * split.splits * (split.splits == 1 ? 2 : 1),
                                                 std::max(1, sms / 2));
-    cudaError_t e = cudaSuccess;
-    if (mode == PARTIALS_EARLY)
-        e = sgh::launch_early(K::main, dim3(unsigned(2 * pairs)), THREADS, SMEM_BYTES, stream, mA, mB, mH, mV, kp, epi);
-    else
-        K::main<<<unsigned(2 * pairs), THREADS, SMEM_BYTES, stream>>>(mA, mB, mH, mV, kp, epi);
+    kp.wait_last = mode == PARTIALS_OVERTAKING;
+    cudaError_t e =
+        sgh::launch_early(K::main, dim3(unsigned(2 * pairs)), THREADS, SMEM_BYTES, stream, mA, mB, mH, mV, kp, epi);
     if (e != cudaSuccess) return sgh::cuda_fail(e);
     sgh::count_launch(K::F32 ? "bf16 parts of float32, tcgen05 cta_group::2, 256x256 pair tiles"
                              : "bf16, tcgen05 cta_group::2, 256x256 pair tiles");

@@ -60,6 +60,7 @@ struct KernelParams {
     int capacity, width, L;
     float *partial;         // splits x M x N, or null
     unsigned long long timeout_ns;
+    bool wait_last;         // launched early: it reads nothing of the kernel before it
 };
 
 // 3-D tile copy into this CTA's shared memory, counted on a barrier of either CTA.
@@ -153,7 +154,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(A_MN) << 15) |
                                (uint32_t(TILE >> 4) << 24);
 
-    launch_dependents();   // (a dependent launched early waits for this kernel's end itself)
     extern __shared__ unsigned char smem_raw[];
     const uintptr_t base = (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023);
     float *stage_out = reinterpret_cast<float *>(base + SMEM_RING);
@@ -186,6 +186,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tc_fence_before();
     cluster_barrier();
     tc_fence_after();
+    if (!p.wait_last) wait_prerequisites();
+    launch_dependents();
     const uint32_t taddr = *tmem_base;
     const uint32_t peer_abort = dsmem_map(smem_addr((const void *)abort_flag), rank ^ 1u);
     auto set_abort = [&] {
@@ -489,7 +491,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     tc_fence_after();
     if (warp == 1) tmem_dealloc_pair(taddr, TMEM_COLUMNS);
-    wait_prerequisites();   // launched early, its end is also that of the kernels before it
+    if (p.wait_last) wait_prerequisites();   // its end is also that of the kernels before it
 }
 
 // The ranges' partial sums added in order, and the epilogue; a thread to an element.
@@ -500,6 +502,8 @@ __global__ void __launch_bounds__(256)
     const long long i = blockIdx.y;
     const int j = blockIdx.x * 256 + threadIdx.x;
     if (j >= N) return;
+    wait_prerequisites();
+    launch_dependents();
     float x = epi.bias ? sgl::to_f32(epi.bias[j]) : 0.0f;
     const long long plane = (long long)M * N;
     float sum = 0.0f;

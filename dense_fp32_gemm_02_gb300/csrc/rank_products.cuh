@@ -74,8 +74,8 @@ __device__ __forceinline__ void fill16(T *to, const T *p, int n, bool wide) {
 }
 
 // ------------------------------------------------------------------ rank side
-// Sums of one tile of up to 64 rows of a group (blockIdx.x) over one range of the
-// contraction (blockIdx.y), to partial[range][row][R]: 8 warps, 16 rows x half of the
+// Sums of one tile of up to 64 rows of a group over one range of the contraction, to
+// partial[range][row][R]: 8 warps, 16 rows x half of the
 // rank each.  NT: the rank in units of 8, rounded up to 2, 4, 8 or 16.  TRANS: V_a is
 // stored R x C.  Pitches are such that no fragment load meets a bank conflict.
 template <class T, bool TRANS, int NT>
@@ -88,25 +88,51 @@ struct RankTile {
     static constexpr size_t SMEM = size_t(STAGES) * (X_ELEMS + V_ELEMS) * sizeof(T);
 };
 
+// A call's two uses of the stack that only wait for the grouping: `rank_blocks` blocks of
+// the rank side (max_tiles for each range), then ceil(cols / 64) x L that lay the other
+// half of the stack out for the product.
+template <class T>
+struct RankWork {
+    int C, range, rank_blocks;
+    Rows<T> X;
+    Stack<const T> V;
+    bool x_wide, v_wide;
+    float *partial;
+    long long partial_plane;
+    int cols;            // of the half to lay out (0: none)
+    Stack<const T> other;
+    Parts to;
+};
+
 template <class T, bool TRANS, int NT>
-__global__ void __launch_bounds__(RANK_THREADS)
-    rank_tile_kernel(int C, int range, Rows<T> X, bool x_wide, Stack<const T> V, bool v_wide, Adapters ad,
-                     Groups g, float *partial, long long partial_plane) {
+__global__ void __launch_bounds__(RANK_THREADS) rank_tile_kernel(RankWork<T> w, Adapters ad, Groups g) {
     using Z = RankTile<T, TRANS, NT>;
     constexpr int WN = Z::WN, PER = 16 / int(sizeof(T)), STAGES = Z::STAGES;
     extern __shared__ __align__(16) unsigned char smem_rank[];
+    static_assert(Z::SMEM >= 128 * 65 * 4, "the tile of pack_stack");
+    sg::wait_prerequisites();
+    sg::launch_dependents();
+    if (int(blockIdx.x) >= w.rank_blocks) {
+        const int b = int(blockIdx.x) - w.rank_blocks, across = (w.cols + 63) / 64;
+        pack_stack<T, TRANS>(b % across, b / across, w.cols, w.other, ad, g, w.to,
+                             reinterpret_cast<float (*)[65]>(smem_rank));
+        return;
+    }
     T *ring = reinterpret_cast<T *>(smem_rank);
     __shared__ int rows[ROW_TILE];
-    if (int(blockIdx.x) >= g.totals[0]) return;
-    const int4 tile = g.tiles[blockIdx.x];
-    const int a = tile.x, n = tile.z;
+    const int4 tile = g.tiles[blockIdx.x % g.max_tiles];
+    const int a = tile.x, n = tile.z, range = blockIdx.x / g.max_tiles;
     if (a < 0) return;
+    const int C = w.C;
+    const Rows<T> &X = w.X;
+    const Stack<const T> &V = w.V;
+    const bool x_wide = w.x_wide, v_wide = w.v_wide;
     if (threadIdx.x < ROW_TILE) rows[threadIdx.x] = int(threadIdx.x) < n ? g.perm[tile.y + threadIdx.x] : -1;
     __syncthreads();
     const int rank = ad.rank(a);
     const T *v = V.matrix(a);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wm = warp & 3, wn = warp >> 2;
-    const int c_begin = blockIdx.y * range, c_end = min(C, c_begin + range);
+    const int c_begin = range * w.range, c_end = min(C, c_begin + w.range);
 
     auto fill = [&](int stage, int c0) {
         T *xs = ring + stage * (Z::X_ELEMS + Z::V_ELEMS), *vs = xs + Z::X_ELEMS;
@@ -198,7 +224,7 @@ __global__ void __launch_bounds__(RANK_THREADS)
             for (int d = 0; d < 4; ++d) sum[t][d] += Z::F32 ? big[t][d] + small[t][d] : big[t][d];
         stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
-    float *out = partial + blockIdx.y * partial_plane;
+    float *out = w.partial + range * w.partial_plane;
 #pragma unroll
     for (int t = 0; t < WN; ++t)
 #pragma unroll
@@ -209,12 +235,15 @@ __global__ void __launch_bounds__(RANK_THREADS)
 }
 
 // What the rank side leaves behind: S (M x R, scaled), unscaled for the caller in H, and
-// S's parts in the planes of Groups (float32: three, bfloat16: two, 2^-16, which is under
-// the output's rounding).  H and planes may be null.
+// S's parts (float32: three, bfloat16: two, 2^-16, which is under the output's rounding)
+// in the planes of Groups and, for the stack's gradients, as rows of `pitch` columns, zero
+// past the rank: `s_rows` of S and `h_rows` of the scaled H that the caller gave.  What is
+// null is left out.
 struct RankSide {
     float *S, *H;
     long long ldh;
-    bf16 *planes;
+    bf16 *planes, *s_rows, *h_rows;
+    int pitch;
 };
 
 // The ranges' partial sums of the rank side added in order, a warp to a row.  A row whose
@@ -222,7 +251,7 @@ struct RankSide {
 template <class T>
 __global__ void __launch_bounds__(256)
     rank_finish_kernel(int M, int ranges, const float *__restrict__ partial, long long partial_plane, Adapters ad,
-                       Groups g, const int *unclean, RankSide to) {
+                       Groups g, RankSide to) {
     constexpr int PARTS = sizeof(T) == 4 ? 3 : 2;
     __shared__ float own[8][128];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -230,20 +259,38 @@ __global__ void __launch_bounds__(256)
     if (i >= M) return;
     const int a = ad.of_row(i), rank = a < 0 ? 0 : ad.rank(a);
     const float scale = a < 0 ? 0.0f : ad.scale(a);
+    sg::wait_prerequisites();
+    sg::launch_dependents();
+    auto rows_of = [&](bf16 *rows) {   // own[warp] as parts
+        __syncwarp();
+        for (int r = 2 * lane; r < to.pitch; r += 64) {
+            uint32_t part[3];
+            pair_parts(r < rank ? own[warp][r] : 0.0f, r + 1 < rank ? own[warp][r + 1] : 0.0f, part);
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q)
+                *reinterpret_cast<uint32_t *>(rows + ((long long)q * M + i) * to.pitch + r) = part[q];
+        }
+        __syncwarp();
+    };
+    if (to.h_rows) {
+        for (int r = lane; r < rank; r += 32) own[warp][r] = to.H[i * to.ldh + r] * scale;
+        rows_of(to.h_rows);
+    }
     for (int r = lane; r < ad.R; r += 32) {
         float sum = 0.0f;
         if (r < rank) {
 #pragma unroll 8
             for (int s = 0; s < ranges; ++s) sum += partial[s * partial_plane + i * ad.R + r];
         }
-        if (to.H) to.H[i * to.ldh + r] = sum;
+        if (to.H && !to.h_rows) to.H[i * to.ldh + r] = sum;
         const float scaled = r < rank ? sum * scale : 0.0f;
         to.S[i * ad.R + r] = scaled;
         own[warp][r] = scaled;
     }
+    if (to.s_rows) rows_of(to.s_rows);
     if (!to.planes) return;
     const int2 planes = g.planes[i / 256];
-    if (rank > 0 && unclean[a]) {
+    if (rank > 0 && g.unclean[a]) {
         if (lane == 0) atomicExch(&g.planes[i / 256].y, NO_PLANES);
         return;
     }
@@ -263,10 +310,8 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------------ stack gradients
-// X^T * S over a chunk of rows of a group (blockIdx.y), 128 columns of X (blockIdx.x):
-// 8 warps, 16 columns x the whole rank each.  partial[chunk] is C x R, or R x C where
-// RANK_ROWS.  S (and whether it still is to be scaled) as the rank side left it; its
-// parts are made once per block, on the way through registers.
+// X^T * S over a chunk of rows of a group, 128 columns of X: 8 warps, 16 columns x the
+// whole rank each.  partial[chunk] is C x R, or R x C where RANK_ROWS.
 template <class X>
 struct ElementOf;
 template <class T>
@@ -283,46 +328,54 @@ struct ElementOf<Act8Rows> {
 template <class X, int PB, int NT>
 struct StackTile {
     using E = typename ElementOf<X>::type;
-    static constexpr int PA = ElementOf<X>::PARTS;
-    static constexpr int COLS = 128, STAGES = sizeof(E) == 4 ? 3 : 4;
+    static constexpr int PA = ElementOf<X>::PARTS, COLS = 128;
     // float32: rows 4 banks apart; bfloat16 and q: 16 bytes past a multiple of 128
     static constexpr int X_PITCH = COLS + (sizeof(E) == 4 ? 4 : 16 / int(sizeof(E)));
-    static constexpr int X_ELEMS = SLAB * X_PITCH, S_PITCH = NT * 8 + 8, S_PLANE = SLAB * S_PITCH;
-    static constexpr size_t SMEM = size_t(STAGES) * X_ELEMS * sizeof(E) + size_t(PB) * S_PLANE * 2 +
-                                   (sizeof(E) == 1 ? size_t(STAGES) * SLAB * 4 : 0);
+    static constexpr int X_BYTES = SLAB * X_PITCH * int(sizeof(E));
+    static constexpr int S_PITCH = NT * 8 + 8, S_PLANE = SLAB * S_PITCH, S_BYTES = PB * S_PLANE * 2;
+    static constexpr int E_BYTES = sizeof(E) == 1 ? SLAB * 4 : 0;   // a row's four exponents
+    static constexpr int STAGE = X_BYTES + S_BYTES + E_BYTES;
+    static constexpr int STAGES = 4 * STAGE <= 110 * 1024 ? 4 : 3 * STAGE <= 220 * 1024 ? 3 : 2;
+    static constexpr size_t SMEM = size_t(STAGES) * STAGE;
+};
+constexpr int CHUNK_ROWS = 512;   // of a chunk at most
+
+template <class X>
+struct StackWork {
+    int C;
+    X x;
+    bool wide;
+    const bf16 *s;   // parts of S: PB x M rows of `pitch` columns
+    float *partial;
 };
 
 template <class X, int PB, int NT, bool RANK_ROWS>
-__global__ void __launch_bounds__(RANK_THREADS)
-    stack_tile_kernel(int C, X x, bool x_wide, const float *S, long long lds, bool scaled, Adapters ad, Groups g,
-                      float *partial) {
+__device__ __forceinline__ void stack_tile(const StackWork<X> &w, int bx, int by, int M, int pitch, const Adapters &ad,
+                                           const Groups &g, unsigned char *smem, int *rows) {
     using Z = StackTile<X, PB, NT>;
     using E = typename Z::E;
     constexpr int PA = Z::PA, PER = 16 / int(sizeof(E)), STAGES = Z::STAGES;
-    constexpr int SN = (SLAB * NT + RANK_THREADS - 1) / RANK_THREADS;
-    extern __shared__ __align__(16) unsigned char smem_rank[];
-    E *ring = reinterpret_cast<E *>(smem_rank);
-    bf16 *ss = reinterpret_cast<bf16 *>(ring + STAGES * Z::X_ELEMS);
-    signed char *es = reinterpret_cast<signed char *>(ss + PB * Z::S_PLANE);   // checkpoints: 4 exponents a row
-    if (int(blockIdx.y) >= g.totals[1]) return;
-    const int4 chunk = g.chunks[blockIdx.y];
-    const int a = chunk.x, n = chunk.z, c0 = blockIdx.x * Z::COLS, rank = ad.rank(a);
-    const int *perm = g.perm + chunk.y;
-    const float scale = scaled ? 1.0f : ad.scale(a);
+    const int4 chunk = g.chunks[by];
+    const int n = chunk.z, c0 = bx * Z::COLS, C = w.C;
+    if (n == 0) return;
+    const X &x = w.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int m = threadIdx.x; m < n; m += RANK_THREADS) rows[m] = g.perm[chunk.y + m];
+    __syncthreads();
 
     auto fill = [&](int stage, int i0) {
-        E *xs = ring + stage * Z::X_ELEMS;
+        E *xs = reinterpret_cast<E *>(smem + stage * Z::STAGE);
+        bf16 *ss = reinterpret_cast<bf16 *>(smem + stage * Z::STAGE + Z::X_BYTES);
 #pragma unroll
         for (int o = threadIdx.x; o < SLAB * Z::COLS / PER; o += RANK_THREADS) {
             const int m = o / (Z::COLS / PER), c = (o % (Z::COLS / PER)) * PER;
             const bool in = i0 + m < n && c0 + c < C;
-            const long long i = in ? perm[i0 + m] : 0;
+            const long long i = in ? rows[i0 + m] : 0;
             if constexpr (sizeof(E) == 1) {
                 E *to = xs + m * Z::X_PITCH + c;
                 const E *p = x.q + i * x.ldq + c0 + c;
                 const int count = in ? min(PER, C - c0 - c) : 0;
-                if (x_wide) {
+                if (w.wide) {
                     sg::cp_async16(shared_address(to), in ? p : x.q, uint32_t(count));
                 } else {
                     E b[PER];
@@ -331,24 +384,24 @@ __global__ void __launch_bounds__(RANK_THREADS)
                     *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(b);
                 }
             } else {
-                fill16(xs + m * Z::X_PITCH + c, in ? x.p + i * x.ld + c0 + c : x.p, in ? C - c0 - c : 0, x_wide);
+                fill16(xs + m * Z::X_PITCH + c, in ? x.p + i * x.ld + c0 + c : x.p, in ? C - c0 - c : 0, w.wide);
             }
         }
+#pragma unroll
+        for (int q = 0; q < PB; ++q)
+#pragma unroll
+            for (int o = threadIdx.x; o < SLAB * NT; o += RANK_THREADS) {
+                const int m = o / NT, r = (o % NT) * 8;
+                const bool in = i0 + m < n;
+                const long long i = in ? rows[i0 + m] : 0;
+                sg::cp_async16(shared_address(ss + q * Z::S_PLANE + m * Z::S_PITCH + r),
+                               w.s + ((long long)q * M + i) * pitch + r, in ? 16u : 0u);
+            }
         if constexpr (sizeof(E) == 1) {
+            signed char *es = reinterpret_cast<signed char *>(ss) + Z::S_BYTES;
             const int m = threadIdx.x / 4, block = c0 / ACT8_BLOCK + threadIdx.x % 4;
             const bool in = i0 + m < n && block * ACT8_BLOCK < C;
-            es[stage * SLAB * 4 + threadIdx.x] = in ? x.e[perm[i0 + m] * x.lde + block] : E(0);
-        }
-    };
-    float sv[SN][8];
-    auto load_s = [&](int i0) {
-#pragma unroll
-        for (int h = 0; h < SN; ++h) {   // 64 rows x NT octets
-            const int o = threadIdx.x + h * RANK_THREADS, m = i0 + o / NT, r = (o % NT) * 8;
-            const bool in = o < SLAB * NT && m < n;
-            const float *p = S + (in ? perm[m] * lds : 0) + r;
-#pragma unroll
-            for (int d = 0; d < 8; ++d) sv[h][d] = in && r + d < rank ? p[d] * scale : 0.0f;
+            es[threadIdx.x] = in ? x.e[rows[i0 + m] * x.lde + block] : E(0);
         }
     };
 
@@ -358,31 +411,15 @@ __global__ void __launch_bounds__(RANK_THREADS)
         if (s * SLAB < n) fill(s, s * SLAB);
         sg::cp_async_commit();
     }
-    load_s(0);
     int stage = 0;
     for (int i0 = 0; i0 < n; i0 += SLAB) {
         sg::cp_async_wait<STAGES - 2>();
-        __syncthreads();   // this slab has landed; the last one's fragments have been read
+        __syncthreads();   // this slab has landed, and the stage filled next has been read
         if (i0 + (STAGES - 1) * SLAB < n) fill((stage + STAGES - 1) % STAGES, i0 + (STAGES - 1) * SLAB);
         sg::cp_async_commit();
-#pragma unroll
-        for (int h = 0; h < SN; ++h) {
-            const int o = threadIdx.x + h * RANK_THREADS;
-            if (o < SLAB * NT) {
-                float part[8][3];
-#pragma unroll
-                for (int d = 0; d < 8; ++d) split_parts(sv[h][d], part[d]);
-                bf16 *to = ss + (o / NT) * Z::S_PITCH + (o % NT) * 8;
-#pragma unroll
-                for (int q = 0; q < PB; ++q)
-                    *reinterpret_cast<uint4 *>(to + q * Z::S_PLANE) =
-                        make_uint4(pack_exact(part[0][q], part[1][q]), pack_exact(part[2][q], part[3][q]),
-                                   pack_exact(part[4][q], part[5][q]), pack_exact(part[6][q], part[7][q]));
-            }
-        }
-        if (i0 + SLAB < n) load_s(i0 + SLAB);
-        __syncthreads();
-        const E *xs = ring + stage * Z::X_ELEMS;
+        const E *xs = reinterpret_cast<const E *>(smem + stage * Z::STAGE);
+        const bf16 *ss = reinterpret_cast<const bf16 *>(smem + stage * Z::STAGE + Z::X_BYTES);
+        const signed char *es = reinterpret_cast<const signed char *>(ss) + Z::S_BYTES;
         float acc[NT][4] = {};
         // the columns' fragment of part qa at rows kk .. kk + 15: element (column, row)
         auto columns = [&](uint32_t (&fa)[PA][4], int kk) {
@@ -399,7 +436,7 @@ __global__ void __launch_bounds__(RANK_THREADS)
                         pair_parts(xs[k * Z::X_PITCH + c], xs[(k + 1) * Z::X_PITCH + c], part);
                         fa[0][d] = part[0], fa[1][d] = part[1], fa[2][d] = part[2];
                     } else {
-                        const signed char *e = es + stage * SLAB * 4 + k * 4 + warp / 2;
+                        const signed char *e = es + k * 4 + warp / 2;
                         fa[0][d] = pack_bf16(float(xs[k * Z::X_PITCH + c]) * act8_step(e[0]),
                                              float(xs[(k + 1) * Z::X_PITCH + c]) * act8_step(e[4]));
                     }
@@ -408,7 +445,7 @@ __global__ void __launch_bounds__(RANK_THREADS)
         };
         // small pairs of parts first, so that what truncates at full size is the last pair's
 #pragma unroll
-        for (int pass = PB > 1 ? 0 : 1; pass < 2; ++pass) {
+        for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll
             for (int kk = 0; kk < SLAB; kk += 16) {
                 uint32_t fa[PA][4];
@@ -435,7 +472,7 @@ __global__ void __launch_bounds__(RANK_THREADS)
             for (int d = 0; d < 4; ++d) sum[t][d] += acc[t][d];
         stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
-    float *out = partial + (long long)blockIdx.y * C * ad.R;
+    float *out = w.partial + (long long)by * C * ad.R;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -445,20 +482,45 @@ __global__ void __launch_bounds__(RANK_THREADS)
         }
 }
 
-// The chunks' partial sums of an adapter (blockIdx.y) added in order; rows x cols is the
-// shape of its gradient (the rank down the rows where RANK_ROWS).
+// Both gradients: X^T G (C = K columns of X, 128 to a block) and H^T dY (N columns of dY),
+// each for max_chunks chunks.
+template <class XA, class T, int NT>
+__global__ void __launch_bounds__(RANK_THREADS)
+    stack_tile_kernel(StackWork<XA> wa, StackWork<Rows<T>> wb, int M, int pitch, Adapters ad, Groups g) {
+    constexpr int PB = sizeof(T) == 4 ? 3 : 2;
+    extern __shared__ __align__(16) unsigned char smem_stack[];
+    __shared__ int rows[CHUNK_ROWS];
+    sg::wait_prerequisites();
+    sg::launch_dependents();
+    const int across = (wa.C + 127) / 128 + (wb.C + 127) / 128, bx = blockIdx.x % across, by = blockIdx.x / across;
+    if (bx < (wa.C + 127) / 128)
+        stack_tile<XA, PB, NT, false>(wa, bx, by, M, pitch, ad, g, smem_stack, rows);
+    else
+        stack_tile<Rows<T>, PB, NT, true>(wb, bx - (wa.C + 127) / 128, by, M, pitch, ad, g, smem_stack, rows);
+}
+
+// The chunks' partial sums of an adapter (blockIdx.y) added in order: K x R to dA, then
+// R x N to dB.
 template <class T>
 __global__ void __launch_bounds__(256)
-    stack_finish_kernel(int rows, int cols, const float *__restrict__ partial, Groups g, Stack<T> out) {
+    stack_finish_kernel(int K, int N, int R, const float *__restrict__ pa, const float *__restrict__ pb, Groups g,
+                        Stack<T> dA, Stack<T> dB) {
+    sg::wait_prerequisites();
+    sg::launch_dependents();
     const int a = blockIdx.y, q0 = g.chunk_begin[a], q1 = g.chunk_begin[a + 1];
-    const long long plane = (long long)rows * cols;
-    T *to = out.matrix(a);
-    for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < plane; t += (long long)gridDim.x * 256) {
+    const long long plane_a = (long long)K * R, plane_b = (long long)R * N;
+    for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < plane_a + plane_b;
+         t += (long long)gridDim.x * 256) {
+        const bool first = t < plane_a;
+        const long long u = first ? t : t - plane_a, plane = first ? plane_a : plane_b;
+        const float *p = (first ? pa : pb) + u;
         float sum = 0.0f;
 #pragma unroll 4
-        for (int q = q0; q < q1; ++q) sum += partial[q * plane + t];
-        const long long i = t / cols;
-        to[i * out.ld + (t - i * cols)] = from_f32<T>(sum);
+        for (int q = q0; q < q1; ++q) sum += p[q * plane];
+        const int cols = first ? R : N;
+        const long long i = u / cols;
+        const Stack<T> &out = first ? dA : dB;
+        out.matrix(a)[i * out.ld + (u - i * cols)] = from_f32<T>(sum);
     }
 }
 
