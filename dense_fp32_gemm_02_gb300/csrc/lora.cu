@@ -164,21 +164,21 @@ int launch(const char *text, void (*kernel)(P...), dim3 grid, unsigned threads, 
     return e == cudaSuccess ? launched(text) : sgh::cuda_fail(e);
 }
 
-// ------------------------------------------------------------------ the first kernel
-// Groups the rows (g.perm not null) and takes the operands' parts; nothing where there is
-// neither.
+// ------------------------------------------------------------------ the first kernels
+// Groups the rows (g.perm not null) and takes the operands' parts.
 template <int P_PARTS, int Q_PARTS, class XP, class XQ>
 int prepare(int M, const Adapters &ad, const Groups &g, const PartsJob<XP> &p, const PartsJob<XQ> &q, int sms,
             cudaStream_t stream) {
+    int st = SGEMM_OK;
+    if (g.perm) {
+        if ((st = shared_limit(group_rows_kernel, sort_smem(ad.L))) != SGEMM_OK) return st;
+        st = launch(nullptr, group_rows_kernel, dim3(1), SORT_THREADS, sort_smem(ad.L), stream, M, ad, g);
+        if (st != SGEMM_OK) return st;
+    }
     const long long octets = p.octets() + q.octets();
-    const long long blocks = std::min<long long>((octets + SORT_THREADS - 1) / SORT_THREADS, 8LL * sms);
-    const size_t smem = g.perm ? sort_smem(ad.L) : 0;
-    if (blocks == 0 && !g.perm) return SGEMM_OK;
-    auto kernel = prepare_kernel<P_PARTS, Q_PARTS, XP, XQ>;
-    const int st = shared_limit(kernel, smem);
-    if (st != SGEMM_OK) return st;
-    // (no block but the grouping one: that one's own step is then never used)
-    return launch(nullptr, kernel, dim3(unsigned(blocks + (g.perm ? 1 : 0))), SORT_THREADS, smem, stream, M, ad, g, p, q);
+    if (octets == 0) return SGEMM_OK;
+    const unsigned blocks = unsigned(std::min<long long>((octets + 255) / 256, 32LL * sms));
+    return launch(nullptr, parts_kernel<P_PARTS, Q_PARTS, XP, XQ>, dim3(blocks), 256, 0, stream, p, q, g.perm != nullptr);
 }
 
 // Sizes and workspace of the grouping of a call's rows.
@@ -259,16 +259,15 @@ struct RankSplit {
 };
 
 // ------------------------------------------------------------------ stack gradients
-template <class XA, class T>
+template <class XA, class XB, int PB>
 struct StackKernel {
-    void (*kernel)(StackWork<XA>, StackWork<Rows<T>>, int, int, Adapters, Groups);
+    void (*kernel)(StackWork<XA>, StackWork<XB>, int, int, Adapters, Groups);
     size_t smem;
 
     template <int NT>
     static constexpr StackKernel of() {
-        constexpr int PB = sizeof(T) == 4 ? 3 : 2;
-        constexpr size_t a = StackTile<XA, PB, NT>::SMEM, b = StackTile<Rows<T>, PB, NT>::SMEM;
-        return {&stack_tile_kernel<XA, T, NT>, a > b ? a : b};
+        constexpr size_t a = StackTile<XA, PB, NT>::SMEM, b = StackTile<XB, PB, NT>::SMEM;
+        return {&stack_tile_kernel<XA, XB, PB, NT>, a > b ? a : b};
     }
     static constexpr StackKernel pick(int R) {
         return R <= 16 ? of<2>() : R <= 32 ? of<4>() : R <= 64 ? of<8>() : of<16>();
@@ -276,17 +275,16 @@ struct StackKernel {
 };
 
 // dA and dB from X's rows (or their checkpoint's) and dY's, and the parts of G and H.
-template <class T, class XA>
-int stack_gradients(const Call &c, const Grouping &gr, XA x, bool x_wide, const bf16 *s_rows, const bf16 *h_rows,
-                    int pitch, float *partial_a, float *partial_b, int sms) {
+template <class T, class XA, class XB>
+int stack_gradients(const Call &c, const Grouping &gr, XA x, bool x_wide, XB dy, bool dy_wide, const bf16 *s_rows,
+                    const bf16 *h_rows, int pitch, float *partial_a, float *partial_b, int sms) {
     const Adapters ad = c.adapters();
-    const Rows<T> dy{static_cast<const T *>(c.dY), c.lddy};
     int st;
     if (c.M > 0) {
-        const auto k = StackKernel<XA, T>::pick(c.R);
+        const auto k = StackKernel<XA, XB, sizeof(T) == 4 ? 3 : 2>::pick(c.R);
         if ((st = shared_limit(k.kernel, k.smem)) != SGEMM_OK) return st;
         const StackWork<XA> wa{c.K, x, x_wide, s_rows, partial_a};
-        const StackWork<Rows<T>> wb{c.N, dy, wide_rows(dy.p, dy.ld), h_rows, partial_b};
+        const StackWork<XB> wb{c.N, dy, dy_wide, h_rows, partial_b};
         const long long blocks = ((c.K + 127LL) / 128 + (c.N + 127LL) / 128) * gr.max_chunks;
         if (blocks > 0x7fffffffLL) return SGEMM_ERR_TOO_LARGE;
         st = launch("lora backward, rows grouped by adapter", k.kernel, dim3(unsigned(blocks)), RANK_THREADS, k.smem,
@@ -316,7 +314,9 @@ int many_rows(const Call &c, int sms, cudaMemPool_t pool) {
     constexpr auto LAYOUT = BACK ? sgp::INPUT_GRAD : sgp::FORWARD;
     constexpr int PRODUCTS = sizeof(T) == 4 ? 6 : 1, S_PARTS = sizeof(T) == 4 ? 3 : 2, PARTS = Packed<T>::PARTS;
     Packed<T> P(M, K, BACK ? c.dY : c.X, BACK ? c.lddy : c.ldx), Q(c.K, c.N, c.W, c.ldw);
-    if (!product) P.direct = Q.direct = true;   // no parts are needed
+    if (!product) Q.direct = true;               // no parts of W are needed,
+    if (!product && !ranked) P.direct = true;    // nor of P
+    if (M == 0 || K == 0) P.direct = true;
     const sgp::Split split = product ? sgp::plan_split(M, N, K, PRODUCTS, sms) : sgp::Split{0, 0};
     Grouping gr(c, want_stack ? (long long)c.K + c.N : 0, sms);
     const RankKernel<T> rank = RankKernel<T>::template pick<BACK>(c.R);
@@ -363,8 +363,12 @@ int many_rows(const Call &c, int sms, cudaMemPool_t pool) {
         const long long blocks = tiles + (planes ? (N + 63LL) / 64 * c.L : 0);
         if (blocks > 0x7fffffffLL) return SGEMM_ERR_TOO_LARGE;
         const Stack<const T> &V = BACK ? B : A, &other = BACK ? A : B;
-        const RankWork<T> w{K, ranges.range, int(tiles), Rows<T>{P.src, P.ld}, V, wide_rows(P.src, P.ld),
-                            wide_stack(V, c.L), r_partial, (long long)M * c.R, planes ? N : 0, other, v};
+        // X: the parts, or a bfloat16 matrix as it is
+        const bool as_is = sizeof(T) == 2 || P.direct;
+        const bf16 *x = as_is ? reinterpret_cast<const bf16 *>(P.src) : P.parts.p;
+        const RankWork<T> w{K, ranges.range, int(tiles), x, as_is ? P.ld : P.pitch, P.parts.plane, V,
+                            !as_is || wide_rows(x, P.ld), wide_stack(V, c.L), r_partial, (long long)M * c.R,
+                            planes ? N : 0, other, v};
         if ((st = shared_limit(rank.kernel, rank.smem)) != SGEMM_OK) return st;
         st = launch(nullptr, rank.kernel, dim3(unsigned(blocks)), RANK_THREADS, rank.smem, c.stream, w, ad, gr.g);
         if (st != SGEMM_OK) return st;
@@ -398,9 +402,15 @@ int many_rows(const Call &c, int sms, cudaMemPool_t pool) {
         if (want_stack) {
             const Rows<T> x{static_cast<const T *>(c.X), c.ldx};
             const Act8Rows kept{c.q, c.e, c.ldq, c.lde};
-            st = c.X ? stack_gradients<T>(c, gr, x, wide_rows(x.p, x.ld), side.s_rows, side.h_rows, pitch, pa, pb, sms)
-                     : stack_gradients<T>(c, gr, kept, aligned(c.q, 16) && c.ldq % 16 == 0, side.s_rows, side.h_rows,
-                                          pitch, pa, pb, sms);
+            const bool q_wide = aligned(c.q, 16) && c.ldq % 16 == 0, x_wide = wide_rows(x.p, x.ld);
+            auto gradients = [&](auto dy, bool dy_wide) {
+                return c.X ? stack_gradients<T>(c, gr, x, x_wide, dy, dy_wide, side.s_rows, side.h_rows, pitch, pa, pb, sms)
+                           : stack_gradients<T>(c, gr, kept, q_wide, dy, dy_wide, side.s_rows, side.h_rows, pitch, pa, pb, sms);
+            };
+            if constexpr (sizeof(T) == 4)
+                st = gradients(PartRows{P.parts.p, P.pitch, P.parts.plane}, true);
+            else
+                st = gradients(Rows<T>{P.src, P.ld}, wide_rows(P.src, P.ld));
             if (st != SGEMM_OK) return st;
         }
     }

@@ -109,6 +109,18 @@ __device__ __forceinline__ void take_parts(const PartsJob<X> &job, long long t, 
     }
 }
 
+// The parts of the product's operands that the TMA cannot read in place.  `beside`: the
+// kernel before it groups the rows, and need only have ended when this one ends.
+template <int P_PARTS, int Q_PARTS, class XP, class XQ>
+__global__ void __launch_bounds__(256) parts_kernel(PartsJob<XP> p, PartsJob<XQ> q, bool beside) {
+    if (!beside) sg::wait_prerequisites();
+    sg::launch_dependents();
+    const long long t = (long long)blockIdx.x * 256 + threadIdx.x, step = (long long)gridDim.x * 256;
+    take_parts<P_PARTS>(p, t, step);
+    take_parts<Q_PARTS>(q, t, step);
+    if (beside) sg::wait_prerequisites();
+}
+
 // ------------------------------------------------------------------ rows by adapter
 // Rows grouped by their adapter, in the order of the rows within a group (a stable
 // counting sort), and the work lists of the kernels that walk the groups.  Rows
@@ -169,9 +181,12 @@ constexpr size_t sort_smem(int L) { return (size_t(32) * (L + 1) + 3 * (L + 2) +
 // One block of 1024 threads; each warp walks its share of the rows, 256 at a time, in two
 // passes of eight independent loads.  Bound by their latency and the counters': 6 us up to
 // 8192 rows.
-__device__ __forceinline__ void group_rows(int M, const Adapters &ad, const Groups &g, int *sm) {
+__global__ void __launch_bounds__(SORT_THREADS, 1) group_rows_kernel(int M, Adapters ad, Groups g) {
+    extern __shared__ int sm[];
     __shared__ int warp_sum[32];
     __shared__ unsigned char no_rank[MAX_ADAPTERS];
+    sg::wait_prerequisites();
+    sg::launch_dependents();
     const int L = ad.L, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int *count = sm;                       // [warp][group], then the next place of each
     int *first = count + 32 * (L + 1);     // L + 2: first place of a group
@@ -317,25 +332,6 @@ __device__ __forceinline__ void group_rows(int M, const Adapters &ad, const Grou
         const int b = group_at(chunk0, L, t), p = first[b] + (t - chunk0[b]) * g.chunk;
         g.chunks[t] = make_int4(b, p, min(g.chunk, first[b + 1] - p), 0);
     }
-}
-
-// The first kernel of a call: block 0 groups the rows (where g.perm is not null), the
-// others take the parts of the product's operands that the TMA cannot read in place.
-template <int P_PARTS, int Q_PARTS, class XP, class XQ>
-__global__ void __launch_bounds__(SORT_THREADS, 1)
-    prepare_kernel(int M, Adapters ad, Groups g, PartsJob<XP> p, PartsJob<XQ> q) {
-    extern __shared__ int sm[];
-    const int groups = g.perm != nullptr;
-    sg::wait_prerequisites();
-    sg::launch_dependents();
-    if (groups && blockIdx.x == 0) {
-        group_rows(M, ad, g, sm);
-        return;
-    }
-    const long long t = (long long)(blockIdx.x - groups) * SORT_THREADS + threadIdx.x;
-    const long long step = (long long)(gridDim.x - groups) * SORT_THREADS;
-    take_parts<P_PARTS>(p, t, step);
-    take_parts<Q_PARTS>(q, t, step);
 }
 
 // The parts of the used adapters for the rank-side planes: plane part * L + a of width x

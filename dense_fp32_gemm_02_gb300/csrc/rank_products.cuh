@@ -6,8 +6,8 @@
 // 16 flop per byte of bfloat16), and their rows lie anywhere in X.  So the warp-level
 // MMA (m16n8k16, bfloat16, fp32 accumulators) is fast enough: its operands come from
 // shared memory that asynchronous copies fill row by row, from any alignment, several
-// slabs ahead.  A float32 element becomes three bfloat16 parts on its way into the MMA's
-// registers, a checkpoint's element one (see parts_gemm.cuh for the parts).
+// slabs ahead.  A float32 element is three bfloat16 parts (see parts_gemm.cuh), which the
+// call has in memory for its product, or makes on the way; a checkpoint's is one.
 //
 // A block only ever holds rows of one adapter, and of its stack the columns below its
 // rank: nothing of another adapter is multiplied, not even by zero.
@@ -16,6 +16,8 @@
 // zero, the small pairs of parts apart, and then go to fp32 sums, round to nearest:
 // four additions of full size to a slab truncate, 5e-7 at most.
 #pragma once
+
+#include <type_traits>
 
 #include "lora.cuh"
 
@@ -75,17 +77,21 @@ __device__ __forceinline__ void fill16(T *to, const T *p, int n, bool wide) {
 
 // ------------------------------------------------------------------ rank side
 // Sums of one tile of up to 64 rows of a group over one range of the contraction, to
-// partial[range][row][R]: 8 warps, 16 rows x half of the
-// rank each.  NT: the rank in units of 8, rounded up to 2, 4, 8 or 16.  TRANS: V_a is
-// stored R x C.  Pitches are such that no fragment load meets a bank conflict.
+// partial[range][row][R]: 8 warps, 16 rows x half of the rank each.  NT: the rank in
+// units of 8, rounded up to 2, 4, 8 or 16.  TRANS: V_a is stored R x C.  X comes as
+// bfloat16, of a float32 matrix the three parts that the product needs anyway; V_a as it
+// is, a float32 slab of it is split once per block on its way from the ring to `planes`.
+// Pitches are such that no fragment load meets a bank conflict.
 template <class T, bool TRANS, int NT>
 struct RankTile {
     static constexpr bool F32 = sizeof(T) == 4;
-    static constexpr int WN = NT / 2, RP = NT * 8, STAGES = F32 ? 3 : 4;
-    static constexpr int X_PITCH = SLAB + 8, X_ELEMS = ROW_TILE * X_PITCH;
-    static constexpr int V_PITCH = TRANS ? SLAB + 8 : (F32 ? RP + 4 : RP + 8);
-    static constexpr int V_ELEMS = (TRANS ? RP : SLAB) * V_PITCH;
-    static constexpr size_t SMEM = size_t(STAGES) * (X_ELEMS + V_ELEMS) * sizeof(T);
+    static constexpr int PARTS = F32 ? 3 : 1, WN = NT / 2, RP = NT * 8;
+    static constexpr int X_PITCH = SLAB + 8, X_PLANE = ROW_TILE * X_PITCH;
+    static constexpr int V_ROWS = TRANS ? RP : SLAB, V_COLS = TRANS ? SLAB : RP, V_PITCH = V_COLS + 8;
+    static constexpr int X_BYTES = PARTS * X_PLANE * 2, V_BYTES = V_ROWS * V_PITCH * int(sizeof(T));
+    static constexpr int PLANES_BYTES = F32 ? PARTS * V_ROWS * V_PITCH * 2 : 0;
+    static constexpr int STAGES = F32 ? (3 * (X_BYTES + V_BYTES) + PLANES_BYTES <= 226 * 1024 ? 3 : 2) : 4;
+    static constexpr size_t SMEM = size_t(STAGES) * (X_BYTES + V_BYTES) + PLANES_BYTES;
 };
 
 // A call's two uses of the stack that only wait for the grouping: `rank_blocks` blocks of
@@ -94,7 +100,8 @@ struct RankTile {
 template <class T>
 struct RankWork {
     int C, range, rank_blocks;
-    Rows<T> X;
+    const bf16 *x;       // X's parts, x_plane apart
+    long long ldx, x_plane;
     Stack<const T> V;
     bool x_wide, v_wide;
     float *partial;
@@ -105,9 +112,10 @@ struct RankWork {
 };
 
 template <class T, bool TRANS, int NT>
-__global__ void __launch_bounds__(RANK_THREADS) rank_tile_kernel(RankWork<T> w, Adapters ad, Groups g) {
+__global__ void __launch_bounds__(RANK_THREADS, sizeof(T) == 2 && NT <= 8 ? 2 : 1)
+    rank_tile_kernel(RankWork<T> w, Adapters ad, Groups g) {
     using Z = RankTile<T, TRANS, NT>;
-    constexpr int WN = Z::WN, PER = 16 / int(sizeof(T)), STAGES = Z::STAGES;
+    constexpr int WN = Z::WN, PARTS = Z::PARTS, STAGES = Z::STAGES, STAGE = Z::X_BYTES + Z::V_BYTES;
     extern __shared__ __align__(16) unsigned char smem_rank[];
     static_assert(Z::SMEM >= 128 * 65 * 4, "the tile of pack_stack");
     sg::wait_prerequisites();
@@ -118,38 +126,34 @@ __global__ void __launch_bounds__(RANK_THREADS) rank_tile_kernel(RankWork<T> w, 
                              reinterpret_cast<float (*)[65]>(smem_rank));
         return;
     }
-    T *ring = reinterpret_cast<T *>(smem_rank);
     __shared__ int rows[ROW_TILE];
     const int4 tile = g.tiles[blockIdx.x % g.max_tiles];
     const int a = tile.x, n = tile.z, range = blockIdx.x / g.max_tiles;
     if (a < 0) return;
-    const int C = w.C;
-    const Rows<T> &X = w.X;
-    const Stack<const T> &V = w.V;
-    const bool x_wide = w.x_wide, v_wide = w.v_wide;
     if (threadIdx.x < ROW_TILE) rows[threadIdx.x] = int(threadIdx.x) < n ? g.perm[tile.y + threadIdx.x] : -1;
     __syncthreads();
     const int rank = ad.rank(a);
-    const T *v = V.matrix(a);
+    const T *v = w.V.matrix(a);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wm = warp & 3, wn = warp >> 2;
-    const int c_begin = range * w.range, c_end = min(C, c_begin + w.range);
+    const int c_begin = range * w.range, c_end = min(w.C, c_begin + w.range);
 
     auto fill = [&](int stage, int c0) {
-        T *xs = ring + stage * (Z::X_ELEMS + Z::V_ELEMS), *vs = xs + Z::X_ELEMS;
+        bf16 *xs = reinterpret_cast<bf16 *>(smem_rank + stage * STAGE);
+        T *vs = reinterpret_cast<T *>(smem_rank + stage * STAGE + Z::X_BYTES);
 #pragma unroll
-        for (int o = threadIdx.x; o < ROW_TILE * SLAB / PER; o += RANK_THREADS) {
-            const int m = o / (SLAB / PER), c = (o % (SLAB / PER)) * PER, i = rows[m];
-            fill16(xs + m * Z::X_PITCH + c, i < 0 ? X.p : X.p + i * X.ld + c0 + c, i < 0 ? 0 : c_end - c0 - c, x_wide);
-        }
-        constexpr int ALONG = (TRANS ? SLAB : Z::RP) / PER;
-        for (int o = threadIdx.x; o < (TRANS ? Z::RP : SLAB) * ALONG; o += RANK_THREADS) {
+        for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+            for (int o = threadIdx.x; o < ROW_TILE * SLAB / 8; o += RANK_THREADS) {
+                const int m = o / (SLAB / 8), c = (o % (SLAB / 8)) * 8, i = rows[m];
+                fill16(xs + q * Z::X_PLANE + m * Z::X_PITCH + c, i < 0 ? w.x : w.x + q * w.x_plane + i * w.ldx + c0 + c,
+                       i < 0 ? 0 : c_end - c0 - c, w.x_wide);
+            }
+        constexpr int PER = 16 / int(sizeof(T)), ALONG = Z::V_COLS / PER;
+        for (int o = threadIdx.x; o < Z::V_ROWS * ALONG; o += RANK_THREADS) {
             const int row = o / ALONG, col = (o % ALONG) * PER;
-            if (TRANS)
-                fill16(vs + row * Z::V_PITCH + col, row < rank ? v + row * V.ld + c0 + col : v,
-                       row < rank ? c_end - c0 - col : 0, v_wide);
-            else
-                fill16(vs + row * Z::V_PITCH + col, c0 + row < c_end && col < rank ? v + (c0 + row) * V.ld + col : v,
-                       c0 + row < c_end ? rank - col : 0, v_wide);
+            const bool in = TRANS ? row < rank : c0 + row < c_end && col < rank;
+            const T *p = TRANS ? v + row * w.V.ld + c0 + col : v + (c0 + row) * w.V.ld + col;
+            fill16(vs + row * Z::V_PITCH + col, in ? p : v, in ? (TRANS ? c_end - c0 - col : rank - col) : 0, w.v_wide);
         }
     };
 
@@ -165,56 +169,50 @@ __global__ void __launch_bounds__(RANK_THREADS) rank_tile_kernel(RankWork<T> w, 
         __syncthreads();   // this slab has landed, and the stage filled next has been read
         if (c0 + (STAGES - 1) * SLAB < c_end) fill((stage + STAGES - 1) % STAGES, c0 + (STAGES - 1) * SLAB);
         sg::cp_async_commit();
-        const T *xs = ring + stage * (Z::X_ELEMS + Z::V_ELEMS), *vs = xs + Z::X_ELEMS;
+        const bf16 *xs = reinterpret_cast<const bf16 *>(smem_rank + stage * STAGE);
+        const T *raw = reinterpret_cast<const T *>(smem_rank + stage * STAGE + Z::X_BYTES);
+        const bf16 *vs = reinterpret_cast<const bf16 *>(raw);
+        constexpr int V_PLANE = Z::V_ROWS * Z::V_PITCH;
+        if constexpr (Z::F32) {
+            bf16 *planes = reinterpret_cast<bf16 *>(smem_rank + STAGES * STAGE);
+            vs = planes;
+#pragma unroll
+            for (int o = threadIdx.x; o < Z::V_ROWS * Z::V_COLS / 4; o += RANK_THREADS) {
+                const int at = o / (Z::V_COLS / 4) * Z::V_PITCH + (o % (Z::V_COLS / 4)) * 4;
+                float x[4];
+                load4(raw + at, x);
+                uint32_t lo[3], hi[3];
+                pair_parts(x[0], x[1], lo);
+                pair_parts(x[2], x[3], hi);
+#pragma unroll
+                for (int q = 0; q < 3; ++q)
+                    *reinterpret_cast<uint2 *>(planes + q * V_PLANE + at) = make_uint2(lo[q], hi[q]);
+            }
+            __syncthreads();
+        }
         float big[WN][4] = {}, small[WN][4] = {};
 #pragma unroll
         for (int kk = 0; kk < SLAB; kk += 16) {
-            if constexpr (!Z::F32) {
-                uint32_t fa[4], fb[4];
-                ldmatrix4<false>(fa, xs + (wm * 16 + (lane & 15)) * Z::X_PITCH + kk + (lane >> 4) * 8);
+            uint32_t fa[PARTS][4];
 #pragma unroll
-                for (int t = 0; t < WN; t += 2) {
-                    const int n0 = (wn * WN + t) * 8, second = WN > 1 ? ((lane >> 4) & 1) * 8 : 0;
+            for (int q = 0; q < PARTS; ++q)
+                ldmatrix4<false>(fa[q], xs + q * Z::X_PLANE + (wm * 16 + (lane & 15)) * Z::X_PITCH + kk + (lane >> 4) * 8);
+#pragma unroll
+            for (int t = 0; t < WN; t += 2) {
+                const int n0 = (wn * WN + t) * 8, second = WN > 1 ? ((lane >> 4) & 1) * 8 : 0;
+#pragma unroll
+                for (int qb = PARTS - 1; qb >= 0; --qb) {
+                    uint32_t fb[4];
                     if constexpr (TRANS)
-                        ldmatrix4<false>(fb, vs + (n0 + (lane & 7) + second) * Z::V_PITCH + kk + ((lane >> 3) & 1) * 8);
+                        ldmatrix4<false>(fb, vs + qb * V_PLANE + (n0 + (lane & 7) + second) * Z::V_PITCH + kk +
+                                                 ((lane >> 3) & 1) * 8);
                     else
-                        ldmatrix4<true>(fb, vs + (kk + (lane & 15)) * Z::V_PITCH + n0 + second);
-                    mma16816(big[t], fa, fb[0], fb[1]);
-                    if constexpr (WN > 1) mma16816(big[t + 1], fa, fb[2], fb[3]);
-                }
-            } else {
-                const int gr = lane >> 2, t2 = (lane & 3) * 2;
-                uint32_t fa[3][4];
+                        ldmatrix4<true>(fb, vs + qb * V_PLANE + (kk + (lane & 15)) * Z::V_PITCH + n0 + second);
 #pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    const float2 x = *reinterpret_cast<const float2 *>(
-                        xs + (wm * 16 + gr + (d & 1) * 8) * Z::X_PITCH + kk + t2 + (d >> 1) * 8);
-                    uint32_t part[3];
-                    pair_parts(x.x, x.y, part);
-                    fa[0][d] = part[0], fa[1][d] = part[1], fa[2][d] = part[2];
-                }
-#pragma unroll
-                for (int t = 0; t < WN; ++t) {
-                    const int nn = (wn * WN + t) * 8 + gr;
-                    uint32_t fb[2][3];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int k = kk + t2 + h * 8;
-                        float x, y;
-                        if constexpr (TRANS) {
-                            const float2 w = *reinterpret_cast<const float2 *>(vs + nn * Z::V_PITCH + k);
-                            x = w.x, y = w.y;
-                        } else {
-                            x = vs[k * Z::V_PITCH + nn], y = vs[(k + 1) * Z::V_PITCH + nn];
-                        }
-                        pair_parts(x, y, fb[h]);
+                    for (int qa = PARTS - 1 - qb; qa >= 0; --qa) {
+                        mma16816(qa + qb > 0 ? small[t] : big[t], fa[qa], fb[0], fb[1]);
+                        if constexpr (WN > 1) mma16816(qa + qb > 0 ? small[t + 1] : big[t + 1], fa[qa], fb[2], fb[3]);
                     }
-                    mma16816(small[t], fa[0], fb[0][2], fb[1][2]);
-                    mma16816(small[t], fa[2], fb[0][0], fb[1][0]);
-                    mma16816(small[t], fa[1], fb[0][1], fb[1][1]);
-                    mma16816(small[t], fa[0], fb[0][1], fb[1][1]);
-                    mma16816(small[t], fa[1], fb[0][0], fb[1][0]);
-                    mma16816(big[t], fa[0], fb[0][0], fb[1][0]);
                 }
             }
         }
@@ -324,6 +322,16 @@ struct ElementOf<Act8Rows> {
     using type = signed char;
     static constexpr int PARTS = 1;
 };
+// A float32 matrix whose parts are there already, `plane` apart, 16-byte aligned rows.
+struct PartRows {
+    const bf16 *p;
+    long long ld, plane;
+};
+template <>
+struct ElementOf<PartRows> {
+    using type = bf16;
+    static constexpr int PARTS = 3;
+};
 
 template <class X, int PB, int NT>
 struct StackTile {
@@ -331,7 +339,8 @@ struct StackTile {
     static constexpr int PA = ElementOf<X>::PARTS, COLS = 128;
     // float32: rows 4 banks apart; bfloat16 and q: 16 bytes past a multiple of 128
     static constexpr int X_PITCH = COLS + (sizeof(E) == 4 ? 4 : 16 / int(sizeof(E)));
-    static constexpr int X_BYTES = SLAB * X_PITCH * int(sizeof(E));
+    static constexpr int X_PLANES = sizeof(E) == 2 ? PA : 1, X_PLANE = SLAB * X_PITCH;
+    static constexpr int X_BYTES = X_PLANES * X_PLANE * int(sizeof(E));
     static constexpr int S_PITCH = NT * 8 + 8, S_PLANE = SLAB * S_PITCH, S_BYTES = PB * S_PLANE * 2;
     static constexpr int E_BYTES = sizeof(E) == 1 ? SLAB * 4 : 0;   // a row's four exponents
     static constexpr int STAGE = X_BYTES + S_BYTES + E_BYTES;
@@ -383,6 +392,11 @@ __device__ __forceinline__ void stack_tile(const StackWork<X> &w, int bx, int by
                     for (int d = 0; d < PER; ++d) b[d] = d < count ? p[d] : E(0);
                     *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(b);
                 }
+            } else if constexpr (std::is_same<X, PartRows>::value) {
+#pragma unroll
+                for (int q = 0; q < 3; ++q)
+                    fill16(xs + q * Z::X_PLANE + m * Z::X_PITCH + c, in ? x.p + q * x.plane + i * x.ld + c0 + c : x.p,
+                           in ? C - c0 - c : 0, true);
             } else {
                 fill16(xs + m * Z::X_PITCH + c, in ? x.p + i * x.ld + c0 + c : x.p, in ? C - c0 - c : 0, w.wide);
             }
@@ -424,9 +438,11 @@ __device__ __forceinline__ void stack_tile(const StackWork<X> &w, int bx, int by
         // the columns' fragment of part qa at rows kk .. kk + 15: element (column, row)
         auto columns = [&](uint32_t (&fa)[PA][4], int kk) {
             if constexpr (sizeof(E) == 2) {
-                ldmatrix4<true>(fa[0], reinterpret_cast<const bf16 *>(xs) +
-                                           (kk + (lane & 7) + ((lane >> 4) & 1) * 8) * Z::X_PITCH + warp * 16 +
-                                           ((lane >> 3) & 1) * 8);
+#pragma unroll
+                for (int q = 0; q < PA; ++q)
+                    ldmatrix4<true>(fa[q], reinterpret_cast<const bf16 *>(xs) + q * Z::X_PLANE +
+                                               (kk + (lane & 7) + ((lane >> 4) & 1) * 8) * Z::X_PITCH + warp * 16 +
+                                               ((lane >> 3) & 1) * 8);
             } else {
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
@@ -443,33 +459,37 @@ __device__ __forceinline__ void stack_tile(const StackWork<X> &w, int bx, int by
                 }
             }
         };
-        // small pairs of parts first, so that what truncates at full size is the last pair's
+        // The small pairs of parts have sums of their own; at the widest rank, for which that
+        // takes too many registers, they come first instead, in a pass of their own.
+        constexpr bool APART = NT <= 8;
+        float small[APART ? NT : 1][4] = {};
 #pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
+        for (int pass = APART ? 1 : 0; pass < 2; ++pass) {
 #pragma unroll
             for (int kk = 0; kk < SLAB; kk += 16) {
                 uint32_t fa[PA][4];
                 columns(fa, kk);
 #pragma unroll
-                for (int qb = pass == 0 ? PB - 1 : 0; qb >= 0; --qb)
+                for (int qb = APART || pass == 0 ? PB - 1 : 0; qb >= 0; --qb)
 #pragma unroll
                     for (int t = 0; t < NT; t += 2) {
                         uint32_t fb[4];
                         ldmatrix4<true>(fb, ss + qb * Z::S_PLANE + (kk + (lane & 15)) * Z::S_PITCH + t * 8 +
                                                 ((lane >> 4) & 1) * 8);
 #pragma unroll
-                        for (int qa = PA - 1; qa >= 0; --qa)
-                            if (pass == 0 ? (qa + qb > 0 && qa + qb <= 2) : qa == 0) {
-                                mma16816(acc[t], fa[qa], fb[0], fb[1]);
-                                mma16816(acc[t + 1], fa[qa], fb[2], fb[3]);
-                            }
+                        for (int qa = PA - 1; qa >= 0; --qa) {
+                            const bool minor = qa + qb > 0;
+                            if (qa + qb > 2 || (!APART && minor != (pass == 0))) continue;
+                            mma16816(APART && minor ? small[APART ? t : 0] : acc[t], fa[qa], fb[0], fb[1]);
+                            mma16816(APART && minor ? small[APART ? t + 1 : 0] : acc[t + 1], fa[qa], fb[2], fb[3]);
+                        }
                     }
             }
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int d = 0; d < 4; ++d) sum[t][d] += acc[t][d];
+            for (int d = 0; d < 4; ++d) sum[t][d] += APART ? acc[t][d] + small[APART ? t : 0][d] : acc[t][d];
         stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
     float *out = w.partial + (long long)by * C * ad.R;
@@ -484,10 +504,9 @@ __device__ __forceinline__ void stack_tile(const StackWork<X> &w, int bx, int by
 
 // Both gradients: X^T G (C = K columns of X, 128 to a block) and H^T dY (N columns of dY),
 // each for max_chunks chunks.
-template <class XA, class T, int NT>
+template <class XA, class XB, int PB, int NT>
 __global__ void __launch_bounds__(RANK_THREADS)
-    stack_tile_kernel(StackWork<XA> wa, StackWork<Rows<T>> wb, int M, int pitch, Adapters ad, Groups g) {
-    constexpr int PB = sizeof(T) == 4 ? 3 : 2;
+    stack_tile_kernel(StackWork<XA> wa, StackWork<XB> wb, int M, int pitch, Adapters ad, Groups g) {
     extern __shared__ __align__(16) unsigned char smem_stack[];
     __shared__ int rows[CHUNK_ROWS];
     sg::wait_prerequisites();
@@ -496,7 +515,7 @@ __global__ void __launch_bounds__(RANK_THREADS)
     if (bx < (wa.C + 127) / 128)
         stack_tile<XA, PB, NT, false>(wa, bx, by, M, pitch, ad, g, smem_stack, rows);
     else
-        stack_tile<Rows<T>, PB, NT, true>(wb, bx - (wa.C + 127) / 128, by, M, pitch, ad, g, smem_stack, rows);
+        stack_tile<XB, PB, NT, true>(wb, bx - (wa.C + 127) / 128, by, M, pitch, ad, g, smem_stack, rows);
 }
 
 // The chunks' partial sums of an adapter (blockIdx.y) added in order: K x R to dA, then
