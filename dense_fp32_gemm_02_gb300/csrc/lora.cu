@@ -183,7 +183,7 @@ int prepare(int M, const Adapters &ad, const Groups &g, const PartsJob<XP> &p, c
 
 // Sizes and workspace of the grouping of a call's rows.
 struct Grouping {
-    int M, L, chunk, max_tiles, max_chunks, tiles256, width, capacity;
+    int M, L, chunk, max_chunks, tiles256, width, most_planes, capacity;
     Groups g{};
 
     // chunk: rows of a partial sum of the stack's gradients, 512 where that makes
@@ -191,70 +191,32 @@ struct Grouping {
     Grouping(const Call &c, long long columns, int sms) : M(c.M), L(c.L), chunk(CHUNK_ROWS) {
         const long long across = (columns + 127) / 128;
         while (chunk > 128 && (M / chunk) * across < 2LL * sms) chunk /= 2;
-        max_tiles = M / ROW_TILE + L + 1;
         max_chunks = M / chunk + L;
         tiles256 = (M + 255) / 256;
         // planes: for every adapter in every tile, but at most 512 MB a part
         width = c.R <= 16 ? 16 : c.R <= 32 ? 32 : c.R <= 64 ? 64 : 128;
-        const long long kinds = std::min<long long>(L, std::min(M, 256));
-        capacity = int(std::min<long long>(16384, tiles256 * ((kinds * width + 63) / 64)));
+        most_planes = (std::min(L, std::min(M, 256)) * width + 63) / 64;
+        capacity = int(std::min<long long>(16384, (long long)tiles256 * most_planes));
     }
     size_t bytes() const {
         const auto piece = [](size_t n) { return sgh::Workspace::piece(n); };
         return L == 0 ? 0
-                      : 2 * piece(size_t(M) * 4) + piece(size_t(max_tiles) * 16) + piece(size_t(max_chunks) * 16) +
-                            piece(size_t(L + 1) * 4) + 2 * piece(size_t(L) * 4) + piece(size_t(tiles256) * 8) +
-                            piece(size_t(capacity) * 16);
+                      : 2 * piece(size_t(M) * 4) + piece(size_t(max_chunks) * 16) + piece(size_t(L + 1) * 4) +
+                            2 * piece(size_t(L) * 4) + piece(size_t(tiles256) * 16) +
+                            piece(size_t(tiles256) * most_planes * 16);
     }
     void place(sgh::Workspace &ws) {
         if (L == 0) return;
         g.perm = ws.take<int>(M);
-        g.tiles = ws.take<int4>(max_tiles);
         g.chunks = ws.take<int4>(max_chunks);
         g.chunk_begin = ws.take<int>(L + 1);
-        g.max_tiles = max_tiles, g.max_chunks = max_chunks, g.chunk = chunk;
+        g.max_chunks = max_chunks, g.chunk = chunk;
         g.used = ws.take<int>(L);
         g.unclean = ws.take<int>(L);
-        g.planes = ws.take<int2>(tiles256);
-        g.plane_adapter = ws.take<int4>(capacity);
+        g.planes = ws.take<int4>(tiles256);
+        g.plane_adapter = ws.take<int4>(size_t(tiles256) * most_planes);
         g.position = ws.take<int>(M);
         g.capacity = capacity, g.width = width;
-    }
-};
-
-// ------------------------------------------------------------------ rank side
-template <class T>
-struct RankKernel {
-    void (*kernel)(RankWork<T>, Adapters, Groups);
-    size_t smem;
-
-    template <bool TRANS, int NT>
-    static constexpr RankKernel of() {
-        return {&rank_tile_kernel<T, TRANS, NT>, RankTile<T, TRANS, NT>::SMEM};
-    }
-    template <bool TRANS>
-    static constexpr RankKernel pick(int R) {
-        return R <= 16 ? of<TRANS, 2>() : R <= 32 ? of<TRANS, 4>() : R <= 64 ? of<TRANS, 8>() : of<TRANS, 16>();
-    }
-};
-
-// Ranges of the rank side's contraction, C deep: the count whose waves of blocks (of about
-// one tile more for each adapter than M has) take the fewest slabs, with three for filling
-// and emptying; a range is at least 256 deep.
-struct RankSplit {
-    int range, ranges;
-    RankSplit(int M, int L, int C, size_t smem, int sms) {
-        const long long slots = (long long)sms * std::max<size_t>(1, std::min<size_t>(2, (227 * 1024) / (smem + 1280)));
-        const long long tiles = (M + ROW_TILE - 1) / ROW_TILE, all = tiles + std::min<long long>(L, tiles) / 2;
-        const long long slabs = (C + SLAB - 1LL) / SLAB;
-        long long least = 0;
-        range = SLAB;
-        for (long long n = 1; n <= std::max(1LL, std::min(slabs / 4, 32LL)); ++n) {
-            const long long per = std::max(1LL, (slabs + n - 1) / n);
-            const long long cost = ((all * n + slots - 1) / slots) * (per + 3);
-            if (n == 1 || cost < least) least = cost, range = int(per * SLAB);
-        }
-        ranges = std::max(1, int((C + (long long)range - 1) / range));
     }
 };
 
@@ -316,35 +278,32 @@ int many_rows(const Call &c, int sms, cudaMemPool_t pool) {
     Packed<T> P(M, K, BACK ? c.dY : c.X, BACK ? c.lddy : c.ldx), Q(c.K, c.N, c.W, c.ldw);
     if (!product) Q.direct = true;               // no parts of W are needed,
     if (!product && !ranked) P.direct = true;    // nor of P
-    if (M == 0 || K == 0) P.direct = true;
+    if (M == 0 || K == 0) P.direct = true;       // (nothing of P is read)
     const sgp::Split split = product ? sgp::plan_split(M, N, K, PRODUCTS, sms) : sgp::Split{0, 0};
     Grouping gr(c, want_stack ? (long long)c.K + c.N : 0, sms);
-    const RankKernel<T> rank = RankKernel<T>::template pick<BACK>(c.R);
-    const RankSplit ranges(M, c.L, K, rank.smem, sms);
+    const int ranges = K > 0 ? sgp::rank_splits(M, K, sms) : 0;   // (no contraction: no sums)
     const int pitch = c.R <= 16 ? 16 : c.R <= 32 ? 32 : c.R <= 64 ? 64 : 128;
-    const long long vpitch = pitch8(N), vplane = gr.width * vpitch;
+    const long long vpitch = pitch8(N), vplane = gr.width * vpitch, upitch = pitch8(K), uplane = gr.width * upitch;
 
     sgh::Workspace ws(pool, c.stream);
     const auto piece = [](size_t n) { return sgh::Workspace::piece(n); };
-    const size_t s_floats = ranked ? size_t(M) * c.R : 0, r_floats = s_floats * ranges.ranges;
+    const size_t s_floats = ranked ? size_t(M) * c.R : 0, r_floats = s_floats * ranges;
     const size_t h_elems = planes ? size_t(S_PARTS) * gr.capacity * 256 * 64 : 0;
     const size_t v_elems = planes ? size_t(PARTS) * c.L * vplane : 0;
+    const size_t u_elems = ranked && K > 0 ? size_t(PARTS) * c.L * uplane : 0;
     const size_t row_elems = want_stack ? size_t(S_PARTS) * M * pitch : 0;
     const size_t pa_floats = want_stack ? size_t(gr.max_chunks) * c.R * c.K : 0;
     const size_t pb_floats = want_stack ? size_t(gr.max_chunks) * c.R * c.N : 0;
     st = ws.allocate(gr.bytes() + piece(s_floats * 4) + piece(r_floats * 4) + piece(h_elems * 2) + piece(v_elems * 2) +
-                     2 * piece(row_elems * 2) + piece(pa_floats * 4) + piece(pb_floats * 4) + P.bytes() + Q.bytes() +
+                     piece(u_elems * 2) + 2 * piece(row_elems * 2) + piece(pa_floats * 4) + piece(pb_floats * 4) + P.bytes() + Q.bytes() +
                      piece(split.partial_floats * 4));
     if (st != SGEMM_OK) return st;
     gr.place(ws);
     RankSide side{ws.take<float>(s_floats), c.H, c.ldh, nullptr, nullptr, nullptr, pitch};
     float *r_partial = ws.take<float>(r_floats);
     const Stack<const T> A = stack_of<T>(c.A, c.lda, c.stride_a), B = stack_of<T>(c.B, c.ldb, c.stride_b);
-    Parts v{};
-    if (planes) {
-        side.planes = ws.take<bf16>(h_elems);
-        v = Parts{ws.take<bf16>(v_elems), vpitch, vplane};
-    }
+    const Parts u{ws.take<bf16>(u_elems), upitch, uplane}, v{ws.take<bf16>(v_elems), vpitch, vplane};
+    if (planes) side.planes = ws.take<bf16>(h_elems);
     if (want_stack) {
         side.s_rows = ws.take<bf16>(row_elems);
         side.h_rows = ws.take<bf16>(row_elems);
@@ -359,20 +318,25 @@ int many_rows(const Call &c, int sms, cudaMemPool_t pool) {
     st = prepare<PARTS, PARTS>(M, ad, gr.g, P.job(), Q.job(), sms, c.stream);
     if (st != SGEMM_OK) return st;
     if (ranked && M > 0) {
-        const long long tiles = (long long)gr.max_tiles * ranges.ranges;
-        const long long blocks = tiles + (planes ? (N + 63LL) / 64 * c.L : 0);
-        if (blocks > 0x7fffffffLL) return SGEMM_ERR_TOO_LARGE;
-        const Stack<const T> &V = BACK ? B : A, &other = BACK ? A : B;
-        // X: the parts, or a bfloat16 matrix as it is
-        const bool as_is = sizeof(T) == 2 || P.direct;
-        const bf16 *x = as_is ? reinterpret_cast<const bf16 *>(P.src) : P.parts.p;
-        const RankWork<T> w{K, ranges.range, int(tiles), x, as_is ? P.ld : P.pitch, P.parts.plane, V,
-                            !as_is || wide_rows(x, P.ld), wide_stack(V, c.L), r_partial, (long long)M * c.R,
-                            planes ? N : 0, other, v};
-        if ((st = shared_limit(rank.kernel, rank.smem)) != SGEMM_OK) return st;
-        st = launch(nullptr, rank.kernel, dim3(unsigned(blocks)), RANK_THREADS, rank.smem, c.stream, w, ad, gr.g);
-        if (st != SGEMM_OK) return st;
-        st = launch(nullptr, rank_finish_kernel<T>, dim3(unsigned((M + 7LL) / 8)), 256, 0, c.stream, M, ranges.ranges,
+        // V1 with the contraction along its rows, V2 as the product reads it
+        const StackSide<T> v1{BACK ? B : A, K, !BACK, false, u}, v2{BACK ? A : B, planes ? N : 0, BACK, true, v};
+        const int across = (K + 255) / 256;
+        const dim3 grid(unsigned(across + (v2.cols + 255) / 256), unsigned(c.L), unsigned(gr.width / 8));
+        if (grid.x > 0) {
+            st = launch(nullptr, pack_stack_kernel<T>, grid, 256, 0, c.stream, v1, v2, across, ad, gr.g);
+            if (st != SGEMM_OK) return st;
+        }
+        if (K > 0) {
+            const sgp::RankProduct r{M, K, gr.width, gr.most_planes, P.operand(),
+                                     {u.p, K, gr.width, (long long)PARTS * c.L, upitch, uplane},
+                                     ad, gr.g.planes, gr.g.plane_adapter, gr.g.position};
+            if ((st = sgp::run_rank<T>(r, ranges, r_partial, sms, c.stream)) != SGEMM_OK) return st;
+        }
+        // four warps to a row where there are few (154 rows of rank 122: 18 -> 6 us), one
+        // else (8192 of rank 64: 7 us, four 15)
+        const bool four = c.R > 32 && M <= 1024;
+        st = launch(nullptr, four ? rank_finish_kernel<T, 4> : rank_finish_kernel<T, 1>,
+                    dim3(unsigned(four ? (M + 1LL) / 2 : (M + 7LL) / 8)), 256, 0, c.stream, M, ranges,
                     (const float *)r_partial, (long long)M * c.R, ad, gr.g, side);
         if (st != SGEMM_OK) return st;
     }

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(256) parts_kernel(PartsJob<XP> p, PartsJob<XQ>
 
 // ------------------------------------------------------------------ rows by adapter
 // Rows grouped by their adapter, in the order of the rows within a group (a stable
-// counting sort), and the work lists of the kernels that walk the groups.  Rows
+// counting sort), and the work list of the kernel that walks the groups.  Rows
 // without an adapter, or with one of rank 0, come last, as group L.
 //
 // For the tensor cores, each 256 rows (a tile of the product) also get their rank-side
@@ -132,21 +132,21 @@ __global__ void __launch_bounds__(256) parts_kernel(PartsJob<XP> p, PartsJob<XQ>
 // in its own adapter's columns and zeros elsewhere.
 struct Groups {
     int *perm;           // M: row numbers, group after group
-    int4 *tiles;         // of up to ROW_TILE rows: {adapter or -1, first place in perm, rows, 0},
-                         // max_tiles of them, the last without rows
-    int4 *chunks;        // of up to `chunk` rows of an adapter: the same, max_chunks of them
+    int4 *chunks;        // of up to `chunk` rows of an adapter: {adapter, first place in perm,
+                         // rows, 0}, max_chunks of them, the last without rows
     int *chunk_begin;    // L + 1: the chunks of adapter a are [a], .. [a + 1]
-    int max_tiles, max_chunks, chunk;
+    int max_chunks, chunk;
     int *used;           // L: whether a row uses the adapter
     int *unclean;        // L: whether it holds something that is not finite (pack_stack)
-    int2 *planes;        // for each 256 rows {first plane, planes}: NO_PLANES past the capacity
+    int4 *planes;        // for each 256 rows {first plane, planes, 1 if the product may use them
+                         // (not past the capacity, nor with an unclean adapter), 0}
     int4 *plane_adapter; // of a plane's 64 / width adapters (the last one repeated), or
                          // {adapter, first rank column} where width >= 64
     int *position;       // M: which of its tile's adapters a row uses
-    int capacity;        // planes
+    int capacity;        // planes that have memory
     int width;           // 16, 32, 64 or 128
 };
-constexpr int MAX_ADAPTERS = 1024, ROW_TILE = 64, SORT_THREADS = 1024, NO_PLANES = -1;
+constexpr int MAX_ADAPTERS = 1024, SORT_THREADS = 1024;
 
 // Exclusive prefix sum over one value per thread of a 1024-thread block; `all` their sum.
 __device__ __forceinline__ int block_prefix(int v, int *warp_sum, int &all) {
@@ -176,7 +176,7 @@ __device__ __forceinline__ int group_at(const int *first, int n, int t) {
     return lo;
 }
 
-constexpr size_t sort_smem(int L) { return (size_t(32) * (L + 1) + 3 * (L + 2) + 32 * 32) * 4; }
+constexpr size_t sort_smem(int L) { return (size_t(32) * (L + 1) + 2 * (L + 2) + 32 * 32) * 4; }
 
 // One block of 1024 threads; each warp walks its share of the rows, 256 at a time, in two
 // passes of eight independent loads.  Bound by their latency and the counters': 6 us up to
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) group_rows_kernel(int M, Adap
     const int L = ad.L, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int *count = sm;                       // [warp][group], then the next place of each
     int *first = count + 32 * (L + 1);     // L + 2: first place of a group
-    int *tile0 = first + (L + 2), *chunk0 = tile0 + (L + 2);
+    int *chunk0 = first + (L + 2);
     int *bits = chunk0 + (L + 2) + warp * 32;   // the adapters of this warp's current 256 rows
     const int a = threadIdx.x;
     if (a < L) no_rank[a] = ad.rank(a) == 0, g.unclean[a] = 0;
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) group_rows_kernel(int M, Adap
             __syncwarp();
         }
         const int kinds = __reduce_add_sync(0xffffffffu, __popc(bits[lane]));
-        if (lane == 0) g.planes[t] = make_int2(0, (kinds * g.width + 63) / 64);
+        if (lane == 0) g.planes[t] = make_int4(0, (kinds * g.width + 63) / 64, 0, 0);
         __syncwarp();
     }
     __syncthreads();
@@ -232,14 +232,8 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) group_rows_kernel(int M, Adap
         for (int w = 0; w < 32; ++w) rows += count[w * (L + 1) + a];
     if (a < L) g.used[a] = rows > 0;
     const int at = block_prefix(rows, warp_sum, all);
-    const int tile_at = block_prefix((rows + ROW_TILE - 1) / ROW_TILE, warp_sum, all);
-    if (a < L) first[a] = at, tile0[a] = tile_at;
-    if (a == SORT_THREADS - 1) {
-        first[L] = at + rows;
-        tile0[L] = all;
-        first[L + 1] = M;
-        tile0[L + 1] = all + (M - first[L] + ROW_TILE - 1) / ROW_TILE;
-    }
+    if (a < L) first[a] = at;
+    if (a == SORT_THREADS - 1) first[L] = at + rows, first[L + 1] = M;
     const int chunk_at = block_prefix((rows + g.chunk - 1) / g.chunk, warp_sum, all);
     if (a < L) chunk0[a] = chunk_at;
     if (a == SORT_THREADS - 1) chunk0[L] = all;
@@ -247,8 +241,8 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) group_rows_kernel(int M, Adap
     for (int base = 0, t = 0; t < tiles; t += SORT_THREADS) {
         const int n = t + a < tiles ? g.planes[t + a].y : 0;
         const int p = base + block_prefix(n, warp_sum, all);
-        if (t + a < tiles) g.planes[t + a] = p + n <= g.capacity ? make_int2(p, n) : make_int2(0, NO_PLANES);
-        base = min(base + all, 1 << 29);
+        if (t + a < tiles) g.planes[t + a] = make_int4(p, n, p + n <= g.capacity, 0);
+        base += all;
     }
     __syncthreads();
     for (int b = threadIdx.x; b <= L; b += SORT_THREADS) {
@@ -291,7 +285,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) group_rows_kernel(int M, Adap
         }
         const int kinds = __shfl_sync(0xffffffffu, below, 31);
         below -= __popc(word);
-        const int2 planes = g.planes[t];
+        const int4 planes = g.planes[t];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int w = max(b[i], 0) >> 5 & 31;
@@ -299,30 +293,21 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) group_rows_kernel(int M, Adap
             const int position = __shfl_sync(0xffffffffu, below, w) + __popc(of_w & ((1u << (b[i] & 31)) - 1));
             if (b[i] >= 0) g.position[t * 256 + i * 32 + lane] = b[i] < L ? position : 0;
         }
-        if (planes.y == NO_PLANES) continue;
         const int per_plane = g.width >= 64 ? 1 : 64 / g.width, halves = g.width > 64 ? g.width / 64 : 1;
         unsigned left = word;
         for (int k = below; left != 0; ++k, left &= left - 1) {
             const int id = lane * 32 + __ffs(left) - 1;
             if (g.width >= 64) {
                 for (int h = 0; h < halves; ++h)
-                    if (SG_IN_RANGE(planes.x + k * halves + h < g.capacity))
+                    if (SG_IN_RANGE(k * halves + h < planes.y))
                         g.plane_adapter[planes.x + k * halves + h] = make_int4(id, h * 64, 0, 0);
-            } else if (SG_IN_RANGE(planes.x + k / per_plane < g.capacity)) {
+            } else if (SG_IN_RANGE(k / per_plane < planes.y)) {
                 int *to = reinterpret_cast<int *>(&g.plane_adapter[planes.x + k / per_plane]);
                 to[k % per_plane] = id;
                 if (k == kinds - 1)
                     for (int d = k % per_plane + 1; d < per_plane; ++d) to[d] = id;
             }
         }
-    }
-    for (int t = threadIdx.x; t < g.max_tiles; t += SORT_THREADS) {
-        if (t >= tile0[L + 1]) {
-            g.tiles[t] = make_int4(-1, 0, 0, 0);
-            continue;
-        }
-        const int b = group_at(tile0, L + 1, t), p = first[b] + (t - tile0[b]) * ROW_TILE;
-        g.tiles[t] = make_int4(b < L ? b : -1, p, min(ROW_TILE, first[b + 1] - p), 0);
     }
     for (int t = threadIdx.x; t < g.max_chunks; t += SORT_THREADS) {
         if (t >= chunk0[L]) {
@@ -334,49 +319,50 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) group_rows_kernel(int M, Adap
     }
 }
 
-// The parts of the used adapters for the rank-side planes: plane part * L + a of width x
-// cols, zero past the adapter's rank, and in unclean[a] whether one of its values is not
-// finite.  TRANS: V_a is stored cols x R.  A block of 256 threads to 64 columns (from
-// block `bx`) of an adapter, through a 128 x 65 tile of shared memory.
-template <class T, bool TRANS>
-__device__ __forceinline__ void pack_stack(int bx, int a, int cols, const Stack<const T> &V, const Adapters &ad,
-                                           const Groups &g, const Parts &to, float (*tile)[65]) {
+// One side of the stack laid out for the tensor cores: the parts of the used adapters as
+// planes part * L + a of width x cols, zero past the adapter's rank.  `trans`: V_a is
+// stored cols x R, else R x cols.  `watch`: it enters the rank-side planes, where what is
+// not finite would reach other adapters' rows: unclean[a] says that there is some.
+template <class T>
+struct StackSide {
+    Stack<const T> V;
+    int cols;
+    bool trans, watch;
+    Parts to;
+};
+
+// A block to 8 rank columns (blockIdx.z) x 256 columns of an adapter of either side (`across`
+// blocks of the first, the rest of the second): a warp to 8 x 32, a thread to eight columns
+// of one, so that loads and stores cover 16 bytes and 64 without shared memory.
+template <class T>
+__global__ void __launch_bounds__(256)
+    pack_stack_kernel(StackSide<T> first, StackSide<T> second, int across, Adapters ad, Groups g) {
     constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
-    const int c0 = bx * 64, width = g.width;
-    if (!g.used[a]) return;
-    const int rank = ad.rank(a), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const T *v = V.matrix(a);
+    sg::wait_prerequisites();
+    sg::launch_dependents();
+    const int a = blockIdx.y;
+    const bool is_first = int(blockIdx.x) < across;
+    const StackSide<T> &side = is_first ? first : second;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cols = side.cols;
+    const int c = (int(blockIdx.x) - (is_first ? 0 : across)) * 256 + warp * 32 + (lane >> 3) * 8;
+    const int rank = ad.rank(a);
+    if (!g.used[a] || c >= cols) return;
+    const T *v = side.V.matrix(a);
+    const long long ld = side.V.ld, step = side.trans ? ld : 1;   // from column to column
+    Parts at = side.to;
+    at.p += a * at.plane;
+    at.plane *= ad.L;
+    const int r = blockIdx.z * 8 + (lane & 7);
+    const T *p = v + (side.trans ? c * ld + r : r * ld + c);
     bool finite = true;
-    if (TRANS) {   // lanes along the rank
-#pragma unroll 8
-        for (int c = warp; c < 64; c += 8)
-            for (int r = lane; r < width; r += 32) {
-                const float x = c0 + c < cols && r < rank ? to_f32(v[(c0 + c) * V.ld + r]) : 0.0f;
-                finite = finite && isfinite(x);
-                tile[r][c] = x;
-            }
-    } else {
-#pragma unroll 4
-        for (int r = warp; r < width; r += 8)
-            for (int c = lane; c < 64; c += 32) {
-                const float x = c0 + c < cols && r < rank ? to_f32(v[r * V.ld + c0 + c]) : 0.0f;
-                finite = finite && isfinite(x);
-                tile[r][c] = x;
-            }
-    }
-    if (!finite) g.unclean[a] = 1;
-    __syncthreads();
-    Parts at = to;
-    at.p += a * to.plane;
-    at.plane = to.plane * ad.L;
-    for (int o = threadIdx.x; o < width * 8; o += 256) {
-        const int r = o / 8, c = (o % 8) * 8;
-        if (c0 + c >= cols) continue;
-        float x[8];
+    float x[8];
 #pragma unroll
-        for (int d = 0; d < 8; ++d) x[d] = tile[r][c + d];
-        store_parts<PARTS>(at, r, c0 + c, x);
+    for (int d = 0; d < 8; ++d) {
+        x[d] = c + d < cols && r < rank ? to_f32(p[d * step]) : 0.0f;
+        finite = finite && isfinite(x[d]);
     }
+    store_parts<PARTS>(at, r, c, x);
+    if (side.watch && !finite) g.unclean[a] = 1;
 }
 
 }  // namespace sgl

@@ -30,7 +30,16 @@ template <class T, Layout LAYOUT>
 struct Kernel {
     static constexpr bool F32 = sizeof(T) == 4, A_MN = LAYOUT == WEIGHT_GRAD, B_MN = LAYOUT != INPUT_GRAD;
     static constexpr int PA = F32 && LAYOUT != WEIGHT_GRAD ? 3 : 1, PB = F32 ? 3 : 1;
-    static constexpr auto *main = &parts_gemm_kernel<T, PA, PB, A_MN, B_MN, LAYOUT == INPUT_GRAD>;
+    static constexpr auto *main = &parts_gemm_kernel<T, PA, PB, A_MN, B_MN, LAYOUT == INPUT_GRAD, false>;
+    static cudaError_t set_attr() {
+        return cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM_BYTES));
+    }
+};
+
+template <class T>
+struct RankKernel {
+    static constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
+    static constexpr auto *main = &parts_gemm_kernel<T, PARTS, PARTS, false, false, false, true>;
     static cudaError_t set_attr() {
         return cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM_BYTES));
     }
@@ -49,7 +58,8 @@ int sgp::set_up() {
     cudaError_t (*const all[])() = {
         &Kernel<float, FORWARD>::set_attr, &Kernel<bf16, FORWARD>::set_attr,
         &Kernel<float, INPUT_GRAD>::set_attr, &Kernel<bf16, INPUT_GRAD>::set_attr,
-        &Kernel<float, WEIGHT_GRAD>::set_attr, &Kernel<bf16, WEIGHT_GRAD>::set_attr};
+        &Kernel<float, WEIGHT_GRAD>::set_attr, &Kernel<bf16, WEIGHT_GRAD>::set_attr,
+        &RankKernel<float>::set_attr, &RankKernel<bf16>::set_attr};
     for (auto set : all)
         if ((e = set()) != cudaSuccess) return sgh::cuda_fail(e);
     done.fetch_or(1ull << dev);
@@ -84,7 +94,7 @@ Split sgp::plan_split(int M, int N, int K, int products, int sms) {
 }
 
 template <class T, bool TRANS>
-int sgp::finish(int M, int N, int splits, const float *partial, const int2 *planes,
+int sgp::finish(int M, int N, int splits, const float *partial, const int4 *planes,
                 const Epilogue<T, TRANS> &epi, cudaStream_t stream) {
     // grid rows are at most 65535 to a launch
     for (long long r = 0; r < M; r += 65535) {
@@ -153,6 +163,60 @@ int sgp::run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Spl
     return SGEMM_OK;
 }
 
+// Ranges of the rank side's contraction: the count whose waves of (256 rows, range) items
+// over the pairs take the fewest slabs, with six for filling and emptying.
+int sgp::rank_splits(int M, int K, int sms) {
+    const long long pairs = std::max(1, sms / 2), tiles = (M + 255LL) / 256, slabs = (K + BK - 1LL) / BK;
+    int best = 1;
+    long long least = 0;
+    for (long long n = 1; n <= std::min(64LL, slabs); ++n) {
+        const long long per = (slabs + n - 1) / n;
+        if ((slabs + per - 1) / per != n) continue;   // a range would be empty
+        const long long cost = ((tiles * n + pairs - 1) / pairs) * (per + 6);
+        if (n == 1 || cost < least) least = cost, best = int(n);
+    }
+    return best;
+}
+
+template <class T>
+int sgp::run_rank(const RankProduct &p, int splits, float *partial, int sms, cudaStream_t stream) {
+    using K = RankKernel<T>;
+    int st = set_up();
+    if (st != SGEMM_OK) return st;
+    const long long tiles_m = (p.M + TILE - 1LL) / TILE, groups = (p.most_planes + 3LL) / 4;
+    const long long items = tiles_m * groups * splits;
+    if (items > (1LL << 30)) return SGEMM_ERR_TOO_LARGE;
+    KernelParams kp{};
+    kp.M = p.M;
+    kp.N = int(groups * TILE);
+    kp.tiles_m = int(tiles_m);
+    kp.tiles_n = int(groups);
+    kp.group_m = 8;
+    kp.slabs = int((p.K + BK - 1LL) / BK);
+    kp.splits = splits;
+    kp.per_split = (kp.slabs + splits - 1) / splits;
+    kp.planes = p.planes;
+    kp.plane_adapter = p.plane_adapter;
+    kp.position = p.position;
+    kp.width = p.width;
+    kp.L = p.ad.L;
+    kp.partial = partial;
+    kp.timeout_ns = sgh::wait_timeout_ns();
+    CUtensorMap mA, mB;
+    if ((st = encode(&mA, p.x, BK, ROWS)) != SGEMM_OK ||
+        (st = encode(&mB, p.v, BK, uint32_t(std::min(p.width, 32)))) != SGEMM_OK)
+        return st;
+    Epilogue<T, false> epi{};
+    epi.ad = p.ad;
+    const long long pairs = std::min<long long>(items, std::max(1, sms / 2));
+    const cudaError_t e = sgh::launch_early(K::main, dim3(unsigned(2 * pairs)), THREADS, SMEM_BYTES, stream, mA, mB, mA, mB,
+                                            kp, epi);
+    if (e != cudaSuccess) return sgh::cuda_fail(e);
+    sgh::count_launch();
+    const cudaError_t after = cudaGetLastError();
+    return after == cudaSuccess ? SGEMM_OK : sgh::cuda_fail(after);
+}
+
 namespace sgp {
 #define LAYER_PRODUCT(T, LAYOUT)                                                                  \
     template int run<T, LAYOUT>(const Product &, const Epilogue<T, LAYOUT == INPUT_GRAD> &, Split, \
@@ -165,11 +229,13 @@ LAYER_PRODUCT(float, WEIGHT_GRAD);
 LAYER_PRODUCT(bf16, WEIGHT_GRAD);
 #undef LAYER_PRODUCT
 #define LAYER_FINISH(T, TRANS) \
-    template int finish<T, TRANS>(int, int, int, const float *, const int2 *,                    \
+    template int finish<T, TRANS>(int, int, int, const float *, const int4 *,                    \
                                   const Epilogue<T, TRANS> &, cudaStream_t)
 LAYER_FINISH(float, false);
 LAYER_FINISH(bf16, false);
 LAYER_FINISH(float, true);
 LAYER_FINISH(bf16, true);
 #undef LAYER_FINISH
+template int run_rank<float>(const RankProduct &, int, float *, int, cudaStream_t);
+template int run_rank<bf16>(const RankProduct &, int, float *, int, cudaStream_t);
 }  // namespace sgp

@@ -55,8 +55,9 @@ struct KernelParams {
     int tiles_m, tiles_n, group_m;
     int slabs;              // of 64 k
     int splits, per_split;  // slabs of each range but the last
-    const int2 *planes;     // of the rank side, see Product (null: none)
+    const int4 *planes;     // of the rank side, see Product (null: none)
     const int4 *plane_adapter;
+    const int *position;
     int capacity, width, L;
     float *partial;         // splits x M x N, or null
     unsigned long long timeout_ns;
@@ -96,21 +97,23 @@ __device__ __forceinline__ uint64_t part_desc(uint32_t saddr, int kk) {
 
 // The work of pair q of Q: items q, q + Q, ... of `items`: whole tiles, or, with
 // `splits` > 1, (tile, range) pairs; without splits a last wave of at most Q / 2
-// tiles is cut into half-width tiles.
+// tiles is cut into half-width tiles.  RANK: (256 rows, four of their planes, range)
+// triples, the planes slowest, so that those that hold nothing come last.
+template <bool RANK>
 struct Items {
     int full, mine_full, mine;
 
     __device__ void init(const KernelParams &p) {
         const int Q = gridDim.x / 2, q = blockIdx.x / 2;
         const int items = p.tiles_m * p.tiles_n * p.splits, tail = items % Q;
-        full = (p.splits == 1 && tail != 0 && 2 * tail <= Q) ? items - tail : items;
+        full = (!RANK && p.splits == 1 && tail != 0 && 2 * tail <= Q) ? items - tail : items;
         const int halves = 2 * (items - full);
         mine_full = q < full ? (full - 1 - q) / Q + 1 : 0;
         mine = mine_full + (q < halves ? (halves - 1 - q) / Q + 1 : 0);
     }
     struct Item {
         int tm, col0, ncols, split, slab0, slabs;
-        int2 planes;   // the rank side's, of the first range only
+        int2 planes;   // the rank side's, of the first range only (RANK: the item's own)
     };
     __device__ Item item(const KernelParams &p, int j) const {
         const int Q = gridDim.x / 2, q = blockIdx.x / 2;
@@ -123,7 +126,10 @@ struct Items {
                 it.split = t % p.splits;
                 t /= p.splits;
             }
-            tile_coords(t, p.tiles_m, p.tiles_n, p.group_m, it.tm, tn);
+            if (RANK)
+                it.tm = t % p.tiles_m, tn = t / p.tiles_m;
+            else
+                tile_coords(t, p.tiles_m, p.tiles_n, p.group_m, it.tm, tn);
             it.col0 = tn * TILE;
             it.ncols = p.N - it.col0 <= TILE / 2 ? TILE / 2 : TILE;
         } else {
@@ -134,7 +140,15 @@ struct Items {
         }
         it.slab0 = it.split * p.per_split;
         it.slabs = min(p.per_split, p.slabs - it.slab0);
-        it.planes = p.planes && it.split == 0 ? p.planes[it.tm] : make_int2(0, 0);
+        if (RANK) {
+            const int4 all = p.planes[it.tm];
+            it.planes = make_int2(all.x + 4 * tn, min(4, all.y - 4 * tn));
+            it.ncols = 64 * it.planes.y;
+            if (it.planes.y <= 0) it.slabs = 0;   // nothing here: every role passes it over
+        } else {
+            const int4 all = p.planes && it.split == 0 ? p.planes[it.tm] : make_int4(0, 0, 1, 0);
+            it.planes = make_int2(all.x, all.z ? all.y : -1);
+        }
         return it;
     }
 };
@@ -143,12 +157,16 @@ struct Items {
 // 512 k, 32 truncating additions, 4e-6 at most and a third of that on average.
 constexpr int CHUNK = 8;
 
-template <class T, int PA, int PB, bool A_MN, bool B_MN, bool TRANS>
+// RANK: the rank side's own product, X (256 rows) * [columns of the adapters that the rows
+// use, as their planes lie], of which a row keeps its own adapter's columns: sums to
+// partial[range][row][R].
+template <class T, int PA, int PB, bool A_MN, bool B_MN, bool TRANS, bool RANK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     parts_gemm_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
                       const __grid_constant__ CUtensorMap mH, const __grid_constant__ CUtensorMap mV,
                       const KernelParams p, const Epilogue<T, TRANS> epi) {
     constexpr bool SEVERAL = PA * PB > 1;
+    constexpr bool CHUNKED = SEVERAL || RANK;   // the main accumulator goes to registers by chunks
     constexpr uint32_t STAGE = (PA + PB) * PART_BYTES;
     constexpr int STAGES = int(SMEM_RING / STAGE);
     constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(A_MN) << 15) |
@@ -195,13 +213,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         st_cluster_flag(peer_abort, 1);
     };
 
-    Items items;
+    Items<RANK> items;
+    using Item = typename Items<RANK>::Item;
     items.init(p);
     const uint32_t ring = smem_addr(reinterpret_cast<void *>(base));
     // slabs of an item, the rank side's after the product's: with one part a side, the two
     // parts of S are planes one after the other
-    auto slabs_of = [](const Items::Item &it) {
-        return it.slabs + max(it.planes.y, 0) * (SEVERAL ? 1 : 2);
+    auto slabs_of = [](const Item &it) {
+        return it.slabs + (RANK ? 0 : max(it.planes.y, 0) * (SEVERAL ? 1 : 2));
     };
 
     if (warp == 0) {
@@ -212,7 +231,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             int stage = 0, issued = 0;
             uint32_t phase = 0;
             for (int j = 0; j < items.mine && !*abort_flag; ++j) {
-                const Items::Item it = items.item(p, j);
+                const Item it = items.item(p, j);
                 const int arow = it.tm * TILE + int(rank) * ROWS;
                 const int bcol = it.col0 + int(rank) * (it.ncols / 2);
                 const int slabs = slabs_of(it);
@@ -226,7 +245,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     }
                     const uint32_t st = ring + uint32_t(stage) * STAGE;
                     const uint32_t fb = dsmem_map(smem_addr(&full[stage]), 0u);
-                    mbar_arrive_expect_tx_cluster(fb, STAGE);
+                    mbar_arrive_expect_tx_cluster(
+                        fb, RANK ? PA * PART_BYTES + PB * uint32_t(it.ncols / 2) * 128u : STAGE);
                     if (s < it.slabs) {
                         const int k = (it.slab0 + s) * BK;
 #pragma unroll
@@ -239,8 +259,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                                 tma_load_3d_pair(at, &mA, fb, k, arow, q);
                             }
                         }
+                        if constexpr (RANK) {
+                            // this CTA's half of the columns, from each adapter at most 32 at a time
+                            const int deep = min(p.width, 32);
+                            for (int u = 0; u < it.ncols / 2; u += deep) {
+                                const int c = int(rank) * (it.ncols / 2) + u, in_plane = c % 64;
+                                const int4 of = p.plane_adapter[it.planes.x + c / 64];
+                                const int slot = p.width < 64 ? in_plane / p.width : 0;
+                                const int a = slot == 0 ? of.x : slot == 1 ? of.y : slot == 2 ? of.z : of.w;
+                                const int r = p.width < 64 ? in_plane % p.width : of.y + in_plane;
 #pragma unroll
-                        for (int q = 0; q < PB; ++q) {
+                                for (int q = 0; q < PB; ++q)
+                                    tma_load_3d_pair(st + uint32_t(PA + q) * PART_BYTES + uint32_t(u) * 128u, &mB, fb, k,
+                                                     r, q * p.L + a);
+                            }
+                        }
+#pragma unroll
+                        for (int q = 0; !RANK && q < PB; ++q) {
                             const uint32_t at = st + uint32_t(PA + q) * PART_BYTES;
                             if constexpr (B_MN) {
                                 tma_load_3d_pair(at, &mB, fb, bcol, k, q);
@@ -249,7 +284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                                 tma_load_3d_pair(at, &mB, fb, k, bcol, q);
                             }
                         }
-                    } else if constexpr (!A_MN) {
+                    } else if constexpr (!A_MN && !RANK) {
                         const int e = s - it.slabs, part = SEVERAL ? 0 : e / it.planes.y;
                         const int plane = it.planes.x + (SEVERAL ? e : e % it.planes.y);
 #pragma unroll
@@ -283,7 +318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (lane == 0 && rank == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            int chunk = 0;   // accumulator hand-overs so far
+            int chunk = 0, tile = 0;   // accumulator hand-overs, tiles so far
             bool ok = true;
             auto wait_acc = [&](int a, int use) {   // the epilogues are through with its use - 1
                 if (mbar_wait_cluster(&acc_empty[a], (uint32_t(use) & 1u) ^ 1u, p.timeout_ns)) {
@@ -295,13 +330,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 return false;
             };
             for (int j = 0; j < items.mine && ok; ++j) {
-                const Items::Item it = items.item(p, j);
+                const Item it = items.item(p, j);
                 const uint32_t idesc = IDESC | (uint32_t(it.ncols >> 3) << 17);
                 const int slabs = slabs_of(it);
-                const int a = SEVERAL ? 0 : j & 1;
+                if (RANK && slabs == 0) continue;
+                const int a = CHUNKED ? 0 : tile & 1;
                 const uint32_t main_acc = taddr + uint32_t(a) * ACC_COLUMNS;
                 // one part: this tile's accumulator; several: the small pairs'
-                if (!(ok = SEVERAL ? wait_acc(1, j) : wait_acc(a, j >> 1))) break;
+                if (SEVERAL && !(ok = wait_acc(1, tile))) break;
+                if (!CHUNKED && !(ok = wait_acc(a, tile >> 1))) break;
+                ++tile;
                 for (int s = 0; s < slabs; ++s) {
                     if (*abort_flag || !mbar_wait_cluster(&full[stage], phase, p.timeout_ns)) {
                         if (!*abort_flag) atomicOr(&g_error_word, ERR_FULL_WAIT);
@@ -334,23 +372,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                                         first = false;
                                     }
                         }
-                        if (s % CHUNK == 0) {
-                            if (!(ok = wait_acc(0, chunk))) break;
-                            ++chunk;
-                        }
+                    }
+                    if (CHUNKED && s % CHUNK == 0) {
+                        if (!(ok = wait_acc(0, chunk))) break;
+                        ++chunk;
                     }
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk)
-                        mma(main_acc, 0, 0, kk, SEVERAL ? (s % CHUNK != 0 || kk > 0) : (s > 0 || kk > 0));
+                        mma(main_acc, 0, 0, kk, CHUNKED ? (s % CHUNK != 0 || kk > 0) : (s > 0 || kk > 0));
                     mma_commit_pair(&empty[stage]);   // both CTAs' stage free once read
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
-                    if (SEVERAL && (s % CHUNK == CHUNK - 1 || s == slabs - 1))
+                    if (CHUNKED && (s % CHUNK == CHUNK - 1 || s == slabs - 1))
                         mma_commit_pair(&acc_full[0]);
                 }
-                if (!SEVERAL && ok) mma_commit_pair(&acc_full[a]);
+                if (!CHUNKED && ok) mma_commit_pair(&acc_full[a]);
             }
             if (!ok) {
                 // no MMA may still run when either CTA frees its TMEM or exits
@@ -364,7 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         float *buf = stage_out + (warp - 2) * (32 * 33);
         const uint32_t lanes = uint32_t(quarter * 32) << 16;
-        int chunk = 0;
+        int chunk = 0, done = 0;
         bool ok = true;
         auto wait_full = [&](int a, int use) {
             if (__any_sync(0xffffffffu, *abort_flag)) return false;
@@ -383,8 +421,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (lane == 0) mbar_arrive_cluster(dsmem_map(smem_addr(&acc_empty[a]), 0u));
         };
         for (int j = 0; j < items.mine && ok; ++j) {
-            const Items::Item it = items.item(p, j);
-            const int width = it.ncols / 2;               // this warp's columns: 128 or 64
+            const Item it = items.item(p, j);
+            if (RANK && it.slabs == 0) continue;
+            const int width = it.ncols / 2;               // this warp's columns: 128, 96 (RANK), 64 or 32
             const int row0 = it.tm * TILE + int(rank) * ROWS + quarter * 32;
             const int col0 = it.col0 + half * width;
             const bool fma_expand = it.planes.y < 0 && p.partial == nullptr;
@@ -427,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 }
             };
 
-            if constexpr (SEVERAL) {
+            if constexpr (CHUNKED) {
                 const int slabs = slabs_of(it);
                 float sum[4][32];
                 for (int s = 0; s < slabs && ok; s += CHUNK, ++chunk) {
@@ -443,20 +482,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 }
                 if (!ok) break;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; SEVERAL && c < 4; ++c) {
                     if (c * 32 >= width) break;
 #pragma unroll
                     for (int h = 0; h < 32; h += 16)
                         tmem_add16(taddr + ACC_COLUMNS + lanes + uint32_t(half * width + c * 32 + h), &sum[c][h],
                                    true);
                 }
-                hand_back(1);
+                if (SEVERAL) hand_back(1);
+                if constexpr (RANK) {   // a lane has a row's columns: it keeps its adapter's
+                    const int row = row0 + lane, of = row < p.M ? epi.ad.of_row(row) : -1;
+                    const int n = of < 0 ? 0 : epi.ad.rank(of);
+                    const int first = n > 0 ? p.position[row] * p.width : 0;
+                    float *out = p.partial + ((long long)it.split * p.M + row) * epi.ad.R;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (c * 32 < width) write(c, sum[c]);
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int r = col0 + c * 32 + i - first;
+                            if (c * 32 < width && r >= 0 && r < n && SG_IN_RANGE(it.split < p.splits)) out[r] = sum[c][i];
+                        }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (c * 32 < width) write(c, sum[c]);
+                }
             } else {
-                const int a = j & 1;
-                if (!(ok = wait_full(a, j >> 1))) break;
+                const int a = done & 1;
+                if (!(ok = wait_full(a, done >> 1))) break;
+                ++done;
 #pragma unroll 1
                 for (int c = 0; c * 32 < width; ++c) {
                     float v[32];
@@ -497,7 +551,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 // The ranges' partial sums added in order, and the epilogue; a thread to an element.
 template <class T, bool TRANS>
 __global__ void __launch_bounds__(256)
-    finish_kernel(int M, int N, int splits, const float *__restrict__ partial, const int2 *planes, int row0,
+    finish_kernel(int M, int N, int splits, const float *__restrict__ partial, const int4 *planes, int row0,
                   Epilogue<T, TRANS> epi) {
     const long long i = blockIdx.y;
     const int j = blockIdx.x * 256 + threadIdx.x;
@@ -510,7 +564,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll 8
     for (int s = 0; s < splits; ++s) sum += partial[s * plane + i * N + j];
     x += sum;
-    const int a = planes && planes[(row0 + i) / TILE].y >= 0 ? -1 : epi.ad.of_row(i);
+    const int a = planes && planes[(row0 + i) / TILE].z ? -1 : epi.ad.of_row(i);
     if (a >= 0) {
         const int n = epi.ad.rank(a);
         const float *S = epi.S + i * epi.lds;

@@ -35,14 +35,30 @@ struct Epilogue {
 // M-major (inner = M), b likewise.  The rank-side term joins the product as more of its
 // contraction, 64 columns at a time: `h` the planes of 256 x 64 that sgl::Groups
 // describes (part * capacity + plane), `v` the adapters' parts (part * L + a, `width` x
-// N).  A tile that has no planes gets the term by FMAs from S and the caller's stack.
+// N).  A tile whose planes may not be used gets the term by FMAs from S and the caller's
+// stack.
 struct Product {
     int M, N, K;
     Operand a, b, h, v;
-    const int2 *planes = nullptr;
+    const int4 *planes = nullptr;
     const int4 *plane_adapter = nullptr;
     int capacity = 0, width = 64;
 };
+
+// The rank side's own product: S before its scale.  `x` the parts of X (M x K, K-major),
+// `v` those of the stack with K along its rows (plane part * L + a, width x K).  A row's
+// sums over each range go to partial[range][row][R].
+struct RankProduct {
+    int M, K, width, most_planes;   // planes of a tile at most
+    Operand x, v;
+    sgl::Adapters ad;
+    const int4 *planes;
+    const int4 *plane_adapter;
+    const int *position;
+};
+int rank_splits(int M, int K, int sms);
+template <class T>
+int run_rank(const RankProduct &p, int splits, float *partial, int sms, cudaStream_t stream);
 
 enum Layout { FORWARD, INPUT_GRAD, WEIGHT_GRAD };   // (a, b): (K, N)-major, (K, K), (M, N)
 
@@ -66,7 +82,7 @@ int run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Split sp
 // The second kernel alone: out from `splits` partial sums (none: the epilogue of zero).
 // Rows of tiles that have planes already have their rank-side term (planes null: none).
 template <class T, bool TRANS>
-int finish(int M, int N, int splits, const float *partial, const int2 *planes, const Epilogue<T, TRANS> &epi,
+int finish(int M, int N, int splits, const float *partial, const int4 *planes, const Epilogue<T, TRANS> &epi,
            cudaStream_t stream);
 
 int set_up();   // the kernels' attributes on the current device (its first call)

@@ -1,16 +1,15 @@
-// rank_products.cuh -- the two skinny products of the adapter layer, over rows grouped
-// by adapter: the rank side, S = X * V_a (rows of a group x R), and the gradients of
-// the stack, X^T * S over the rows of a group (C x R).
+// rank_products.cuh -- what the adapter layer computes from the rank side's sums: their
+// scaled forms, and the gradients of the stack, X^T * S over the rows of a group (C x R).
 //
-// One side of each is at most 128 wide, so both are bound by reading X once (R = 16:
-// 16 flop per byte of bfloat16), and their rows lie anywhere in X.  So the warp-level
-// MMA (m16n8k16, bfloat16, fp32 accumulators) is fast enough: its operands come from
-// shared memory that asynchronous copies fill row by row, from any alignment, several
-// slabs ahead.  A float32 element is three bfloat16 parts (see parts_gemm.cuh), which the
-// call has in memory for its product, or makes on the way; a checkpoint's is one.
+// The gradients are skinny (at most 128 wide), so they are bound by reading X once, and
+// the rows of a group lie anywhere in X.  So the warp-level MMA (m16n8k16, bfloat16, fp32
+// accumulators) is fast enough: its operands come from shared memory that asynchronous
+// copies fill row by row, from any alignment, several slabs ahead.  A float32 element is
+// three bfloat16 parts (see parts_gemm.cuh), which the call has in memory for its product,
+// or makes on the way; a checkpoint's is one.
 //
-// A block only ever holds rows of one adapter, and of its stack the columns below its
-// rank: nothing of another adapter is multiplied, not even by zero.
+// A block only ever holds rows of one adapter: nothing of another one's is multiplied,
+// not even by zero.
 //
 // The MMA's additions truncate, so a slab's products (64 of the contraction) add up from
 // zero, the small pairs of parts apart, and then go to fp32 sums, round to nearest:
@@ -76,162 +75,6 @@ __device__ __forceinline__ void fill16(T *to, const T *p, int n, bool wide) {
 }
 
 // ------------------------------------------------------------------ rank side
-// Sums of one tile of up to 64 rows of a group over one range of the contraction, to
-// partial[range][row][R]: 8 warps, 16 rows x half of the rank each.  NT: the rank in
-// units of 8, rounded up to 2, 4, 8 or 16.  TRANS: V_a is stored R x C.  X comes as
-// bfloat16, of a float32 matrix the three parts that the product needs anyway; V_a as it
-// is, a float32 slab of it is split once per block on its way from the ring to `planes`.
-// Pitches are such that no fragment load meets a bank conflict.
-template <class T, bool TRANS, int NT>
-struct RankTile {
-    static constexpr bool F32 = sizeof(T) == 4;
-    static constexpr int PARTS = F32 ? 3 : 1, WN = NT / 2, RP = NT * 8;
-    static constexpr int X_PITCH = SLAB + 8, X_PLANE = ROW_TILE * X_PITCH;
-    static constexpr int V_ROWS = TRANS ? RP : SLAB, V_COLS = TRANS ? SLAB : RP, V_PITCH = V_COLS + 8;
-    static constexpr int X_BYTES = PARTS * X_PLANE * 2, V_BYTES = V_ROWS * V_PITCH * int(sizeof(T));
-    static constexpr int PLANES_BYTES = F32 ? PARTS * V_ROWS * V_PITCH * 2 : 0;
-    static constexpr int STAGES = F32 ? (3 * (X_BYTES + V_BYTES) + PLANES_BYTES <= 226 * 1024 ? 3 : 2) : 4;
-    static constexpr size_t SMEM = size_t(STAGES) * (X_BYTES + V_BYTES) + PLANES_BYTES;
-};
-
-// A call's two uses of the stack that only wait for the grouping: `rank_blocks` blocks of
-// the rank side (max_tiles for each range), then ceil(cols / 64) x L that lay the other
-// half of the stack out for the product.
-template <class T>
-struct RankWork {
-    int C, range, rank_blocks;
-    const bf16 *x;       // X's parts, x_plane apart
-    long long ldx, x_plane;
-    Stack<const T> V;
-    bool x_wide, v_wide;
-    float *partial;
-    long long partial_plane;
-    int cols;            // of the half to lay out (0: none)
-    Stack<const T> other;
-    Parts to;
-};
-
-template <class T, bool TRANS, int NT>
-__global__ void __launch_bounds__(RANK_THREADS, sizeof(T) == 2 && NT <= 8 ? 2 : 1)
-    rank_tile_kernel(RankWork<T> w, Adapters ad, Groups g) {
-    using Z = RankTile<T, TRANS, NT>;
-    constexpr int WN = Z::WN, PARTS = Z::PARTS, STAGES = Z::STAGES, STAGE = Z::X_BYTES + Z::V_BYTES;
-    extern __shared__ __align__(16) unsigned char smem_rank[];
-    static_assert(Z::SMEM >= 128 * 65 * 4, "the tile of pack_stack");
-    sg::wait_prerequisites();
-    sg::launch_dependents();
-    if (int(blockIdx.x) >= w.rank_blocks) {
-        const int b = int(blockIdx.x) - w.rank_blocks, across = (w.cols + 63) / 64;
-        pack_stack<T, TRANS>(b % across, b / across, w.cols, w.other, ad, g, w.to,
-                             reinterpret_cast<float (*)[65]>(smem_rank));
-        return;
-    }
-    __shared__ int rows[ROW_TILE];
-    const int4 tile = g.tiles[blockIdx.x % g.max_tiles];
-    const int a = tile.x, n = tile.z, range = blockIdx.x / g.max_tiles;
-    if (a < 0) return;
-    if (threadIdx.x < ROW_TILE) rows[threadIdx.x] = int(threadIdx.x) < n ? g.perm[tile.y + threadIdx.x] : -1;
-    __syncthreads();
-    const int rank = ad.rank(a);
-    const T *v = w.V.matrix(a);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wm = warp & 3, wn = warp >> 2;
-    const int c_begin = range * w.range, c_end = min(w.C, c_begin + w.range);
-
-    auto fill = [&](int stage, int c0) {
-        bf16 *xs = reinterpret_cast<bf16 *>(smem_rank + stage * STAGE);
-        T *vs = reinterpret_cast<T *>(smem_rank + stage * STAGE + Z::X_BYTES);
-#pragma unroll
-        for (int q = 0; q < PARTS; ++q)
-#pragma unroll
-            for (int o = threadIdx.x; o < ROW_TILE * SLAB / 8; o += RANK_THREADS) {
-                const int m = o / (SLAB / 8), c = (o % (SLAB / 8)) * 8, i = rows[m];
-                fill16(xs + q * Z::X_PLANE + m * Z::X_PITCH + c, i < 0 ? w.x : w.x + q * w.x_plane + i * w.ldx + c0 + c,
-                       i < 0 ? 0 : c_end - c0 - c, w.x_wide);
-            }
-        constexpr int PER = 16 / int(sizeof(T)), ALONG = Z::V_COLS / PER;
-        for (int o = threadIdx.x; o < Z::V_ROWS * ALONG; o += RANK_THREADS) {
-            const int row = o / ALONG, col = (o % ALONG) * PER;
-            const bool in = TRANS ? row < rank : c0 + row < c_end && col < rank;
-            const T *p = TRANS ? v + row * w.V.ld + c0 + col : v + (c0 + row) * w.V.ld + col;
-            fill16(vs + row * Z::V_PITCH + col, in ? p : v, in ? (TRANS ? c_end - c0 - col : rank - col) : 0, w.v_wide);
-        }
-    };
-
-    float sum[WN][4] = {};
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) {
-        if (c_begin + s * SLAB < c_end) fill(s, c_begin + s * SLAB);
-        sg::cp_async_commit();
-    }
-    int stage = 0;
-    for (int c0 = c_begin; c0 < c_end; c0 += SLAB) {
-        sg::cp_async_wait<STAGES - 2>();
-        __syncthreads();   // this slab has landed, and the stage filled next has been read
-        if (c0 + (STAGES - 1) * SLAB < c_end) fill((stage + STAGES - 1) % STAGES, c0 + (STAGES - 1) * SLAB);
-        sg::cp_async_commit();
-        const bf16 *xs = reinterpret_cast<const bf16 *>(smem_rank + stage * STAGE);
-        const T *raw = reinterpret_cast<const T *>(smem_rank + stage * STAGE + Z::X_BYTES);
-        const bf16 *vs = reinterpret_cast<const bf16 *>(raw);
-        constexpr int V_PLANE = Z::V_ROWS * Z::V_PITCH;
-        if constexpr (Z::F32) {
-            bf16 *planes = reinterpret_cast<bf16 *>(smem_rank + STAGES * STAGE);
-            vs = planes;
-#pragma unroll
-            for (int o = threadIdx.x; o < Z::V_ROWS * Z::V_COLS / 4; o += RANK_THREADS) {
-                const int at = o / (Z::V_COLS / 4) * Z::V_PITCH + (o % (Z::V_COLS / 4)) * 4;
-                float x[4];
-                load4(raw + at, x);
-                uint32_t lo[3], hi[3];
-                pair_parts(x[0], x[1], lo);
-                pair_parts(x[2], x[3], hi);
-#pragma unroll
-                for (int q = 0; q < 3; ++q)
-                    *reinterpret_cast<uint2 *>(planes + q * V_PLANE + at) = make_uint2(lo[q], hi[q]);
-            }
-            __syncthreads();
-        }
-        float big[WN][4] = {}, small[WN][4] = {};
-#pragma unroll
-        for (int kk = 0; kk < SLAB; kk += 16) {
-            uint32_t fa[PARTS][4];
-#pragma unroll
-            for (int q = 0; q < PARTS; ++q)
-                ldmatrix4<false>(fa[q], xs + q * Z::X_PLANE + (wm * 16 + (lane & 15)) * Z::X_PITCH + kk + (lane >> 4) * 8);
-#pragma unroll
-            for (int t = 0; t < WN; t += 2) {
-                const int n0 = (wn * WN + t) * 8, second = WN > 1 ? ((lane >> 4) & 1) * 8 : 0;
-#pragma unroll
-                for (int qb = PARTS - 1; qb >= 0; --qb) {
-                    uint32_t fb[4];
-                    if constexpr (TRANS)
-                        ldmatrix4<false>(fb, vs + qb * V_PLANE + (n0 + (lane & 7) + second) * Z::V_PITCH + kk +
-                                                 ((lane >> 3) & 1) * 8);
-                    else
-                        ldmatrix4<true>(fb, vs + qb * V_PLANE + (kk + (lane & 15)) * Z::V_PITCH + n0 + second);
-#pragma unroll
-                    for (int qa = PARTS - 1 - qb; qa >= 0; --qa) {
-                        mma16816(qa + qb > 0 ? small[t] : big[t], fa[qa], fb[0], fb[1]);
-                        if constexpr (WN > 1) mma16816(qa + qb > 0 ? small[t + 1] : big[t + 1], fa[qa], fb[2], fb[3]);
-                    }
-                }
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < WN; ++t)
-#pragma unroll
-            for (int d = 0; d < 4; ++d) sum[t][d] += Z::F32 ? big[t][d] + small[t][d] : big[t][d];
-        stage = stage + 1 == STAGES ? 0 : stage + 1;
-    }
-    float *out = w.partial + range * w.partial_plane;
-#pragma unroll
-    for (int t = 0; t < WN; ++t)
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            const int m = wm * 16 + (lane >> 2) + (d / 2) * 8, r = (wn * WN + t) * 8 + (lane & 3) * 2 + (d & 1);
-            if (m < n && r < ad.R) out[(long long)rows[m] * ad.R + r] = sum[t][d];
-        }
-}
-
 // What the rank side leaves behind: S (M x R, scaled), unscaled for the caller in H, and
 // S's parts (float32: three, bfloat16: two, 2^-16, which is under the output's rounding)
 // in the planes of Groups and, for the stack's gradients, as rows of `pitch` columns, zero
@@ -244,60 +87,58 @@ struct RankSide {
     int pitch;
 };
 
-// The ranges' partial sums of the rank side added in order, a warp to a row.  A row whose
-// adapter holds something that is not finite takes its tile's planes away.
-template <class T>
+// The ranges' partial sums of the rank side added in order, WARPS warps to a row.  A row
+// whose adapter holds something that is not finite keeps the product from its tile's planes.
+template <class T, int WARPS>
 __global__ void __launch_bounds__(256)
     rank_finish_kernel(int M, int ranges, const float *__restrict__ partial, long long partial_plane, Adapters ad,
                        Groups g, RankSide to) {
-    constexpr int PARTS = sizeof(T) == 4 ? 3 : 2;
-    __shared__ float own[8][128];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long i = (long long)blockIdx.x * 8 + warp;
-    if (i >= M) return;
+    constexpr int PARTS = sizeof(T) == 4 ? 3 : 2, ROWS = 8 / WARPS, THREADS = 32 * WARPS;
+    __shared__ float own_s[ROWS][128], own_h[ROWS][128];
+    const int t = threadIdx.x % THREADS, lane = t & 31, warp = t >> 5, in_block = threadIdx.x / THREADS;
+    const long long row = (long long)blockIdx.x * ROWS + in_block, i = row < M ? row : M - 1;
     const int a = ad.of_row(i), rank = a < 0 ? 0 : ad.rank(a);
     const float scale = a < 0 ? 0.0f : ad.scale(a);
+    float *S = own_s[in_block], *H = own_h[in_block];
     sg::wait_prerequisites();
     sg::launch_dependents();
-    auto rows_of = [&](bf16 *rows) {   // own[warp] as parts
-        __syncwarp();
-        for (int r = 2 * lane; r < to.pitch; r += 64) {
+    const int4 planes = to.planes ? g.planes[i / 256] : make_int4(0, 0, 0, 0);
+    const int first = to.planes ? g.position[i] * g.width : 0;
+    const bool unclean = to.planes && rank > 0 && g.unclean[a];
+    for (int r = t; r < ad.R; r += THREADS) {
+        float sum = 0.0f, h = 0.0f;
+        if (r < rank) {
+            if (to.h_rows) h = to.H[i * to.ldh + r];
+#pragma unroll 8
+            for (int s = 0; s < ranges; ++s) sum += partial[s * partial_plane + i * ad.R + r];
+        }
+        const float scaled = r < rank ? sum * scale : 0.0f;
+        S[r] = scaled;
+        H[r] = r < rank ? h * scale : 0.0f;
+        if (row < M) {
+            to.S[i * ad.R + r] = scaled;
+            if (to.H && !to.h_rows) to.H[i * to.ldh + r] = sum;
+        }
+    }
+    __syncthreads();
+    if (row >= M) return;
+    auto rows_of = [&](bf16 *rows, const float *x) {   // a row as parts
+        for (int r = 2 * t; r < to.pitch; r += 2 * THREADS) {
             uint32_t part[3];
-            pair_parts(r < rank ? own[warp][r] : 0.0f, r + 1 < rank ? own[warp][r + 1] : 0.0f, part);
+            pair_parts(r < rank ? x[r] : 0.0f, r + 1 < rank ? x[r + 1] : 0.0f, part);
 #pragma unroll
             for (int q = 0; q < PARTS; ++q)
                 *reinterpret_cast<uint32_t *>(rows + ((long long)q * M + i) * to.pitch + r) = part[q];
         }
-        __syncwarp();
     };
-    if (to.h_rows) {
-        for (int r = lane; r < rank; r += 32) own[warp][r] = to.H[i * to.ldh + r] * scale;
-        rows_of(to.h_rows);
-    }
-    for (int r = lane; r < ad.R; r += 32) {
-        float sum = 0.0f;
-        if (r < rank) {
-#pragma unroll 8
-            for (int s = 0; s < ranges; ++s) sum += partial[s * partial_plane + i * ad.R + r];
-        }
-        if (to.H && !to.h_rows) to.H[i * to.ldh + r] = sum;
-        const float scaled = r < rank ? sum * scale : 0.0f;
-        to.S[i * ad.R + r] = scaled;
-        own[warp][r] = scaled;
-    }
-    if (to.s_rows) rows_of(to.s_rows);
-    if (!to.planes) return;
-    const int2 planes = g.planes[i / 256];
-    if (rank > 0 && g.unclean[a]) {
-        if (lane == 0) atomicExch(&g.planes[i / 256].y, NO_PLANES);
-        return;
-    }
-    __syncwarp();
-    const int first = g.position[i] * g.width;
-    for (int s = 0; s < planes.y; ++s) {
+    if (to.h_rows) rows_of(to.h_rows, H);
+    if (to.s_rows) rows_of(to.s_rows, S);
+    if (unclean && t == 0) atomicExch(&g.planes[i / 256].z, 0);
+    if (!planes.z) return;
+    for (int s = warp; s < planes.y; s += WARPS) {
         const int r = s * 64 + 2 * lane - first;
-        const float x = r >= 0 && r < rank ? own[warp][r] : 0.0f;
-        const float y = r + 1 >= 0 && r + 1 < rank ? own[warp][r + 1] : 0.0f;
+        const float x = r >= 0 && r < rank ? S[r] : 0.0f;
+        const float y = r + 1 >= 0 && r + 1 < rank ? S[r + 1] : 0.0f;
         uint32_t part[3];
         pair_parts(x, y, part);
 #pragma unroll
