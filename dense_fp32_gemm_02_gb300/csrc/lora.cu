@@ -416,7 +416,7 @@ void split_rows(RowsWork &w, int cols, int step, int longest, long long slots, s
 template <class T>
 int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
     constexpr bool F32 = sizeof(T) == 4;
-    const bool stream_rows = c.M <= STREAM_ROWS, mma_rows = F32 && !stream_rows, ranked = c.L > 0;
+    const bool stream_rows = c.M <= STREAM_ROWS, mma_rows = F32 && !stream_rows && c.M <= MMA_ROWS, ranked = c.L > 0;
     const T *W = static_cast<const T *>(c.W);
     const bool w_wide = wide_rows(W, c.ldw);
     const Adapters ad = c.adapters();
@@ -441,7 +441,7 @@ int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
         slots *= 2;
         split_rows(w, ROWS_COLS, SLAB, sgh::kMaxDim, slots, sizeof(T));
     } else {
-        split = sgp::plan_split(c.M, c.N, c.K, 1, sms);
+        split = sgp::plan_split(c.M, c.N, c.K, F32 ? 6 : 1, sms);
         w.ranges = split.splits;
     }
     if (ranked) {
@@ -480,18 +480,20 @@ int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
             if (e != cudaSuccess) return sgh::cuda_fail(e);
         }
         st = launched(kFewRows);
-    } else if constexpr (F32) {
-        auto kernel = c.M <= 32 ? few_rows_kernel<2> : few_rows_kernel<4>;
-        const size_t smem = c.M <= 32 ? FewRows<2>::SMEM : FewRows<4>::SMEM;
-        if ((st = shared_limit(kernel, smem)) != SGEMM_OK) return st;
-        if (alone) {
-            kernel<<<unsigned(product), RANK_THREADS, smem, c.stream>>>(w, X, W, c.ldw, w_wide);
-        } else {
-            const cudaError_t e = sgh::launch_early(kernel, dim3(unsigned(product)), RANK_THREADS, smem, c.stream, w, X, W,
-                                                    c.ldw, w_wide);
-            if (e != cudaSuccess) return sgh::cuda_fail(e);
+    } else if (mma_rows) {
+        if constexpr (F32) {
+            auto kernel = c.M <= 32 ? few_rows_kernel<2> : few_rows_kernel<4>;
+            const size_t smem = c.M <= 32 ? FewRows<2>::SMEM : FewRows<4>::SMEM;
+            if ((st = shared_limit(kernel, smem)) != SGEMM_OK) return st;
+            if (alone) {
+                kernel<<<unsigned(product), RANK_THREADS, smem, c.stream>>>(w, X, W, c.ldw, w_wide);
+            } else {
+                const cudaError_t e = sgh::launch_early(kernel, dim3(unsigned(product)), RANK_THREADS, smem, c.stream, w, X,
+                                                        W, c.ldw, w_wide);
+                if (e != cudaSuccess) return sgh::cuda_fail(e);
+            }
+            st = launched(kFewRows);
         }
-        st = launched(kFewRows);
     } else {
         sgp::Product g;
         g.M = c.M, g.N = c.N, g.K = c.K;
@@ -517,8 +519,7 @@ int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
 bool few_rows(const Call &c) {
     if (c.K == 0 || c.N == 0) return false;
     if (c.M <= STREAM_ROWS) return true;
-    const int most = c.type == SGEMM_F32 ? MMA_ROWS : FEW_ROWS;
-    return c.M <= most && (c.L == 0 || (long long)c.M * c.R <= 4096);
+    return c.M <= FEW_ROWS && (c.L == 0 || (long long)c.M * c.R <= 4096);
 }
 
 template <class T>
