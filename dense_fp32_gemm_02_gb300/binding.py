@@ -297,10 +297,20 @@ ACT8_BLOCK = 32   # columns of a row that share an exponent of an 8-bit checkpoi
 
 # A decode step makes one such call per projection, so the checks below are written for
 # the calls that pass them: what is wrong is worked out only once something is.
+torch = None   # imported by the first call (this module loads without it)
+
+
+def _import_torch():
+    global torch
+    import torch as module
+    torch = module
+
+
 def _layer_type(names, *tensors):
     """(sgemm_type, device number) of CUDA tensors (or None, past the first) of one type,
     float32 or bfloat16, on one device."""
-    import torch
+    if torch is None:
+        _import_torch()
     first = tensors[0]
     try:
         dtype, device = first.dtype, first.get_device()
@@ -333,7 +343,8 @@ def _typed(name, t, dtype, device):
             return
     except AttributeError:
         pass
-    import torch
+    if torch is None:
+        _import_torch()
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA {str(dtype).replace('torch.', '')} tensor")
     raise ValueError(f"{name} must be on cuda:{device}")
@@ -380,7 +391,6 @@ def _stack(name, t, count, rows, cols):
 
 def _checkpoint(q, e, rows, cols, device):
     """(address, pitch, address, pitch) of an 8-bit checkpoint of a rows x cols matrix."""
-    import torch
     _typed("q", q, torch.int8, device)
     _typed("e", e, torch.int8, device)
     return (*_matrix("q", q, rows, cols), *_matrix("e", e, rows, -(-cols // ACT8_BLOCK)))
@@ -388,7 +398,8 @@ def _checkpoint(q, e, rows, cols, device):
 
 def _adapters(A, B, ids, M, scale, ranks, device):
     """(L, R, ids, ranks, scale) of a stack A (L, K, R), B (L, R, N): sizes and addresses."""
-    import torch
+    if torch is None:
+        _import_torch()
     if A.dim() != 3:
         raise ValueError("A must be 3-D (adapters, K, R)")
     L, _, R = A.shape
@@ -404,9 +415,8 @@ def _adapters(A, B, ids, M, scale, ranks, device):
 def _call(device, stream, fn, *args):
     """fn(*args, stream) with CUDA device number `device` current, on `stream` or torch's
     current stream of that device."""
-    import torch
     handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == device:
+    if torch._C._cuda_getDevice() == device:
         return check(fn(*args, handle))
     with torch.cuda.device(device):
         return check(fn(*args, handle))
@@ -422,7 +432,6 @@ def lora_into(X, W, A, B, ids, Y, scale=None, ranks=None, bias=None, H=None, str
     the first ranks[a] columns of A[a] and rows of B[a] are used.  H (M, R) float32,
     where given, receives X[i]@A[a] for lora_backward_into().  Asynchronous on `stream`
     (default: torch's current stream)."""
-    import torch
     kind, device = _layer_type(("X", "W", "A", "B", "Y", "bias"), X, W, A, B, Y, bias)
     if X.dim() != 2 or W.dim() != 2:
         raise ValueError("X and W must be 2-D")
@@ -446,7 +455,6 @@ def lora_backward_into(dY, X, W, A, B, ids, H, dX=None, dA=None, dB=None, scale=
     X is the forward call's input or the pair (q, e) that act8_store_into() kept of it;
     H what the forward call wrote.  dX (M, K) may be None, and dA (L, K, R) and
     dB (L, R, N) may be None together.  Returns (dX, dA, dB)."""
-    import torch
     kept = isinstance(X, tuple)
     kind, device = _layer_type(("dY", "X", "W", "A", "B", "dX", "dA", "dB"), dY, None if kept else X,
                                W, A, B, dX, dA, dB)
@@ -467,7 +475,8 @@ def lora_backward_into(dY, X, W, A, B, ids, H, dX=None, dA=None, dB=None, scale=
 
 def act8_empty(M: int, K: int, device=None):
     """A checkpoint's two tensors for an M x K matrix: q (M, K) and e (M, ceil(K/32)), int8."""
-    import torch
+    if torch is None:
+        _import_torch()
     device = device or torch.device("cuda", torch.cuda.current_device())
     return (torch.empty((M, K), dtype=torch.int8, device=device),
             torch.empty((M, -(-K // ACT8_BLOCK)), dtype=torch.int8, device=device))

@@ -432,10 +432,7 @@ int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
     auto stream = w_wide ? stream_kernel<T, true>(c.M) : stream_kernel<T, false>(c.M);
     long long slots = sms;
     if (stream_rows) {
-        int per_sm = 1;
-        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, stream, RANK_THREADS, 0);
-        if (e != cudaSuccess) return sgh::cuda_fail(e);
-        slots *= std::max(1, std::min(per_sm, 4));
+        slots *= stream_blocks(c.M);
         split_rows(w, 32 * 16 / int(sizeof(T)), RANK_THREADS / 32 * STREAM_DEPTH, STREAM_RANGE, slots, sizeof(T));
     } else if (mma_rows) {
         slots *= 2;

@@ -103,8 +103,10 @@ __global__ void __launch_bounds__(RANK_THREADS)
 // together; else single elements, 32 lanes next to each other.
 constexpr int STREAM_RANGE = 512, STREAM_DEPTH = 8;
 
+constexpr int stream_blocks(int rows) { return rows <= 4 ? 3 : 2; }   // to an SM
+
 template <class T, int MR, bool WIDE>
-__global__ void __launch_bounds__(RANK_THREADS)
+__global__ void __launch_bounds__(RANK_THREADS, stream_blocks(MR))
     stream_rows_kernel(RowsWork w, Rows<T> X, const T *W, long long ldw, Stack<const T> V, Adapters ad) {
     constexpr int PER = 16 / int(sizeof(T)), COLS = 32 * PER, WARPS = RANK_THREADS / 32;
     constexpr int XS = STREAM_RANGE * MR, RED = WARPS * COLS * (MR < 4 ? MR : 4);
