@@ -233,3 +233,46 @@ def test_weight_gradient_against_differences_and_repeats():
         quotient = float(loss[0] - loss[1]) / 2
         have = float((dw.cpu().double() * D).sum())
         assert abs(have - quotient) <= 4e-6 * float(dw.double().norm() * D.norm())
+
+
+def test_past_two_to_the_31_elements():
+    """70000 x 32800 (2.3e9 elements, in both forms): the rows past the 2^31-th element are
+    those of a call on them alone, bit for bit."""
+    b = binding()
+    for K, pad in ((32800, 0), (32801, 0)):
+        M, tail = 70000, 300
+        z = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+        g = torch.Generator(device="cuda")
+        g.manual_seed(3)
+        for r in range(0, M, 10000):
+            z[r:r + 10000].normal_(generator=g)
+        q, e = b.act8_empty(M, K)
+        y = torch.empty_like(z)
+        b.act8_store_into(z, q, e, act="gelu", Y=y)
+        q2, e2 = b.act8_empty(tail, K)
+        y2 = torch.empty(tail, K, dtype=torch.bfloat16, device="cuda")
+        b.act8_store_into(z[-tail:], q2, e2, act="gelu", Y=y2)
+        assert torch.equal(q[-tail:], q2) and torch.equal(e[-tail:], e2) and torch.equal(y[-tail:], y2)
+        b.act8_grad_into(q, e, z, y, act="gelu")
+        b.act8_grad_into(q2, e2, z[-tail:], y2, act="gelu")
+        assert torch.equal(y[-tail:], y2)
+        del z, q, e, y
+    torch.cuda.empty_cache()
+
+
+def test_weight_gradient_past_two_to_the_31_elements():
+    """The columns of a 70000 x 32800 checkpoint one at a time would be the same sums: the
+    last 64 against a call on a copy of them."""
+    b = binding()
+    M, K = 70000, 32800
+    q = torch.randint(-127, 128, (M, K), dtype=torch.int8, device="cuda")
+    e = torch.randint(-9, -5, (M, K // 32), dtype=torch.int8, device="cuda")
+    dy = torch.randn(M, 40, device="cuda").to(torch.bfloat16)
+    dw = b.act8_weight_grad_into(q, e, dy, torch.empty(K, 40, dtype=torch.bfloat16, device="cuda"))
+    some = b.act8_weight_grad_into(q[:, -64:].contiguous(), e[:, -2:].contiguous(), dy,
+                                   torch.empty(64, 40, dtype=torch.bfloat16, device="cuda"))
+    # other splits of the contraction: equal up to fp32 sums, i.e. one rounding to bfloat16
+    far = (dw[-64:].float() - some.float()).abs().max() / some.float().abs().max()
+    assert float(far) <= 2.0 ** -7
+    del q, e, dy
+    torch.cuda.empty_cache()

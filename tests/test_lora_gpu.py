@@ -265,3 +265,57 @@ def test_capture_in_a_graph(M):
     graph.replay()
     torch.cuda.synchronize()
     check_forward(p, Y, None, "replayed")
+
+
+def test_host_threads_on_their_own_streams():
+    """Calls of every path from four threads at once give what they give alone."""
+    import threading
+    problems = [Problem(M, 264, 520, 3, 16, dtype, "mixed", seed=M)
+                for M, dtype in ((3, torch.float32), (40, torch.float32), (100, torch.bfloat16), (700, torch.bfloat16))]
+    want = []
+    for p in problems:
+        Y, h = run_forward(p)
+        want.append((Y, h, *run_backward(p, h)))
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(10):
+                    Y, h = run_forward(problems[i])
+                    got = (Y, h, *run_backward(problems[i], h))
+                    torch.cuda.current_stream().synchronize()
+                    assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
+        except Exception as e:   # noqa: BLE001  (reported by the main thread)
+            errors.append(f"problem {i}: {e!r}")
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(problems))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+
+
+def test_long_stacks_and_strides():
+    """X, Y and the stack as slices of wider tensors whose strides pass 2^31 elements."""
+    b = binding()
+    K, N, R, M = 64, 72, 8, 300
+    wide = torch.zeros(M * 8_000_000, dtype=torch.bfloat16, device="cuda")   # 4.8 GB
+    X = torch.as_strided(wide, (M, K), (8_000_000, 1))
+    X.copy_(torch.randn(M, K))
+    stack = torch.zeros(3 * 1_500_000_000, dtype=torch.bfloat16, device="cuda")   # 9 GB
+    A = torch.as_strided(stack, (3, K, R), (1_500_000_000, R, 1))
+    B = torch.as_strided(stack, (3, R, N), (1_500_000_000, N, 1), storage_offset=4096)
+    A.copy_(torch.randn(3, K, R))
+    B.copy_(torch.randn(3, R, N))
+    W = torch.randn(K, N).to(torch.bfloat16).cuda()
+    ids = row_ids(M, 3, "mixed", 4).cuda()
+    got = b.lora_into(X, W, A, B, ids, torch.empty(M, N, dtype=torch.bfloat16, device="cuda"))
+    few = b.lora_into(X[-5:], W, A, B, ids[-5:], torch.empty(5, N, dtype=torch.bfloat16, device="cuda"))
+    ref, _, mag, _ = lora_reference(X.cpu(), W.cpu(), A.cpu(), B.cpu(), ids.cpu(), None, None, None)
+    assert_close(got, ref, mag, K + R, "wide strides")
+    assert_close(few, ref[-5:], mag[-5:], K + R, "wide strides, few rows")
+    del wide, stack
+    torch.cuda.empty_cache()
