@@ -287,7 +287,7 @@ int many_rows(const Call &c, int sms, cudaMemPool_t pool) {
 
     sgh::Workspace ws(pool, c.stream);
     const auto piece = [](size_t n) { return sgh::Workspace::piece(n); };
-    const size_t s_floats = ranked ? size_t(M) * c.R : 0, r_floats = s_floats * ranges;
+    const size_t s_floats = ranked ? size_t(M) * c.R : 0, r_floats = ranked ? size_t(ranges) * M * gr.width : 0;
     const size_t h_elems = planes ? size_t(S_PARTS) * gr.capacity * 256 * 64 : 0;
     const size_t v_elems = planes ? size_t(PARTS) * c.L * vplane : 0;
     const size_t u_elems = ranked && K > 0 ? size_t(PARTS) * c.L * uplane : 0;
@@ -332,12 +332,13 @@ int many_rows(const Call &c, int sms, cudaMemPool_t pool) {
                                      ad, gr.g.planes, gr.g.plane_adapter, gr.g.position};
             if ((st = sgp::run_rank<T>(r, ranges, r_partial, sms, c.stream)) != SGEMM_OK) return st;
         }
-        // four warps to a row where there are few (154 rows of rank 122: 18 -> 6 us), one
+        // four warps to a row where there are few (154 rows of rank 122: 18 -> 6 us; 512 rows of
+        // 32 adapters of rank 16: 17 -> 9), one
         // else (8192 of rank 64: 7 us, four 15)
-        const bool four = c.R > 32 && M <= 1024;
+        const bool four = M <= 2048;
         st = launch(nullptr, four ? rank_finish_kernel<T, 4> : rank_finish_kernel<T, 1>,
                     dim3(unsigned(four ? (M + 1LL) / 2 : (M + 7LL) / 8)), 256, 0, c.stream, M, ranges,
-                    (const float *)r_partial, (long long)M * c.R, ad, gr.g, side);
+                    (const float *)r_partial, (long long)M * gr.width, ad, gr.g, side);
         if (st != SGEMM_OK) return st;
     }
     if (want_out) {

@@ -95,8 +95,10 @@ struct PartsJob {
 template <int PARTS, class X>
 __device__ __forceinline__ void take_parts(const PartsJob<X> &job, long long t, long long step) {
     const int per_row = (job.cols + 7) / 8;
-    for (const long long total = job.octets(); t < total; t += step) {
-        const long long i = t / per_row;
+    const long long total = job.octets();
+    const bool small = total <= 0xffffffffll;   // 32-bit division: a third of the time
+    for (; t < total; t += step) {
+        const long long i = small ? (long long)(unsigned(t) / unsigned(per_row)) : t / per_row;
         const int c = int(t - i * per_row) * 8;
         float v[8];
         if (job.wide && c + 8 <= job.cols) {

@@ -159,7 +159,7 @@ constexpr int CHUNK = 8;
 
 // RANK: the rank side's own product, X (256 rows) * [columns of the adapters that the rows
 // use, as their planes lie], of which a row keeps its own adapter's columns: sums to
-// partial[range][row][R].
+// partial[range][row][width].
 template <class T, int PA, int PB, bool A_MN, bool B_MN, bool TRANS, bool RANK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     parts_gemm_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
@@ -335,7 +335,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const int slabs = slabs_of(it);
                 if (RANK && slabs == 0) continue;
                 const int a = CHUNKED ? 0 : tile & 1;
-                const uint32_t main_acc = taddr + uint32_t(a) * ACC_COLUMNS;
+                int main_buf = a;
                 // one part: this tile's accumulator; several: the small pairs'
                 if (SEVERAL && !(ok = wait_acc(1, tile))) break;
                 if (!CHUNKED && !(ok = wait_acc(a, tile >> 1))) break;
@@ -373,10 +373,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                                     }
                         }
                     }
+                    // (one part leaves TMEM for two main accumulators, taken in turn)
                     if (CHUNKED && s % CHUNK == 0) {
-                        if (!(ok = wait_acc(0, chunk))) break;
+                        main_buf = SEVERAL ? 0 : chunk & 1;
+                        if (!(ok = wait_acc(main_buf, SEVERAL ? chunk : chunk >> 1))) break;
                         ++chunk;
                     }
+                    const uint32_t main_acc = taddr + uint32_t(main_buf) * ACC_COLUMNS;
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk)
                         mma(main_acc, 0, 0, kk, CHUNKED ? (s % CHUNK != 0 || kk > 0) : (s > 0 || kk > 0));
@@ -386,7 +389,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         phase ^= 1u;
                     }
                     if (CHUNKED && (s % CHUNK == CHUNK - 1 || s == slabs - 1))
-                        mma_commit_pair(&acc_full[0]);
+                        mma_commit_pair(&acc_full[main_buf]);
                 }
                 if (!CHUNKED && ok) mma_commit_pair(&acc_full[a]);
             }
@@ -470,15 +473,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const int slabs = slabs_of(it);
                 float sum[4][32];
                 for (int s = 0; s < slabs && ok; s += CHUNK, ++chunk) {
-                    if (!(ok = wait_full(0, chunk))) break;
+                    const int buf = SEVERAL ? 0 : chunk & 1;
+                    if (!(ok = wait_full(buf, SEVERAL ? chunk : chunk >> 1))) break;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         if (c * 32 >= width) break;
 #pragma unroll
                         for (int h = 0; h < 32; h += 16)
-                            tmem_add16(taddr + lanes + uint32_t(half * width + c * 32 + h), &sum[c][h], s > 0);
+                            tmem_add16(taddr + uint32_t(buf) * ACC_COLUMNS + lanes + uint32_t(half * width + c * 32 + h),
+                                       &sum[c][h], s > 0);
                     }
-                    hand_back(0);
+                    hand_back(buf);
                 }
                 if (!ok) break;
 #pragma unroll
@@ -492,15 +497,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 if (SEVERAL) hand_back(1);
                 if constexpr (RANK) {   // a lane has a row's columns: it keeps its adapter's
                     const int row = row0 + lane, of = row < p.M ? epi.ad.of_row(row) : -1;
-                    const int n = of < 0 ? 0 : epi.ad.rank(of);
-                    const int first = n > 0 ? p.position[row] * p.width : 0;
-                    float *out = p.partial + ((long long)it.split * p.M + row) * epi.ad.R;
+                    const bool any = of >= 0 && epi.ad.rank(of) > 0;
+                    const int first = any ? p.position[row] * p.width : 0;
+                    float *out = p.partial + ((long long)it.split * p.M + row) * p.width;
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int r = col0 + c * 32 + i - first;
-                            if (c * 32 < width && r >= 0 && r < n && SG_IN_RANGE(it.split < p.splits)) out[r] = sum[c][i];
+                        for (int i = 0; i < 32; i += 4) {
+                            const int r = col0 + c * 32 + i - first;   // a multiple of 4, as all of these are
+                            if (any && c * 32 < width && r >= 0 && r < p.width && SG_IN_RANGE(it.split < p.splits))
+                                *reinterpret_cast<float4 *>(out + r) =
+                                    make_float4(sum[c][i], sum[c][i + 1], sum[c][i + 2], sum[c][i + 3]);
                         }
                 } else {
 #pragma unroll

@@ -47,7 +47,7 @@ struct Product {
 
 // The rank side's own product: S before its scale.  `x` the parts of X (M x K, K-major),
 // `v` those of the stack with K along its rows (plane part * L + a, width x K).  A row's
-// sums over each range go to partial[range][row][R].
+// sums over each range go to partial[range][row][width].
 struct RankProduct {
     int M, K, width, most_planes;   // planes of a tile at most
     Operand x, v;

@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(256)
         if (r < rank) {
             if (to.h_rows) h = to.H[i * to.ldh + r];
 #pragma unroll 8
-            for (int s = 0; s < ranges; ++s) sum += partial[s * partial_plane + i * ad.R + r];
+            for (int s = 0; s < ranges; ++s) sum += partial[s * partial_plane + i * g.width + r];
         }
         const float scaled = r < rank ? sum * scale : 0.0f;
         S[r] = scaled;
