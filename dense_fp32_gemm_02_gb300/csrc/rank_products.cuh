@@ -11,7 +11,7 @@
 // A block only ever holds rows of one adapter: nothing of another one's is multiplied,
 // not even by zero.
 //
-// The MMA's additions truncate, so a slab's products (64 of the contraction) add up from
+// The MMA's additions truncate, so a slab's products (at most 64 of the contraction) add up from
 // zero, the small pairs of parts apart, and then go to fp32 sums, round to nearest:
 // four additions of full size to a slab truncate, 5e-7 at most.
 #pragma once
@@ -180,12 +180,17 @@ struct StackTile {
     static constexpr int PA = ElementOf<X>::PARTS, COLS = 128;
     // float32: rows 4 banks apart; bfloat16 and q: 16 bytes past a multiple of 128
     static constexpr int X_PITCH = COLS + (sizeof(E) == 4 ? 4 : 16 / int(sizeof(E)));
-    static constexpr int X_PLANES = sizeof(E) == 2 ? PA : 1, X_PLANE = SLAB * X_PITCH;
-    static constexpr int X_BYTES = X_PLANES * X_PLANE * int(sizeof(E));
-    static constexpr int S_PITCH = NT * 8 + 8, S_PLANE = SLAB * S_PITCH, S_BYTES = PB * S_PLANE * 2;
-    static constexpr int E_BYTES = sizeof(E) == 1 ? SLAB * 4 : 0;   // a row's four exponents
+    static constexpr int X_PLANES = sizeof(E) == 2 ? PA : 1, S_PITCH = NT * 8 + 8;
+    static constexpr int ROW_BYTES = X_PLANES * X_PITCH * int(sizeof(E)) + PB * S_PITCH * 2 + (sizeof(E) == 1 ? 4 : 0);
+    // Rows to a slab, and slabs in the ring: several blocks to an SM hide more than a
+    // deeper ring does (4096 x 4096 bfloat16, rank 32: 28 us with two of 4 slabs, 22 with
+    // four of 2).
+    static constexpr int DEPTH = SLAB * ROW_BYTES <= 56 * 1024 ? SLAB : SLAB / 2;
+    static constexpr int X_PLANE = DEPTH * X_PITCH, X_BYTES = X_PLANES * X_PLANE * int(sizeof(E));
+    static constexpr int S_PLANE = DEPTH * S_PITCH, S_BYTES = PB * S_PLANE * 2;
+    static constexpr int E_BYTES = sizeof(E) == 1 ? DEPTH * 4 : 0;   // a row's four exponents
     static constexpr int STAGE = X_BYTES + S_BYTES + E_BYTES;
-    static constexpr int STAGES = 4 * STAGE <= 110 * 1024 ? 4 : 3 * STAGE <= 220 * 1024 ? 3 : 2;
+    static constexpr int STAGES = 3 * STAGE <= 74 * 1024 ? 3 : 2;
     static constexpr size_t SMEM = size_t(STAGES) * STAGE;
 };
 constexpr int CHUNK_ROWS = 512;   // of a chunk at most
@@ -204,7 +209,7 @@ __device__ __forceinline__ void stack_tile(const StackWork<X> &w, int bx, int by
                                            const Groups &g, unsigned char *smem, int *rows) {
     using Z = StackTile<X, PB, NT>;
     using E = typename Z::E;
-    constexpr int PA = Z::PA, PER = 16 / int(sizeof(E)), STAGES = Z::STAGES;
+    constexpr int PA = Z::PA, PER = 16 / int(sizeof(E)), STAGES = Z::STAGES, DEPTH = Z::DEPTH;
     const int4 chunk = g.chunks[by];
     const int n = chunk.z, c0 = bx * Z::COLS, C = w.C;
     if (n == 0) return;
@@ -217,7 +222,7 @@ __device__ __forceinline__ void stack_tile(const StackWork<X> &w, int bx, int by
         E *xs = reinterpret_cast<E *>(smem + stage * Z::STAGE);
         bf16 *ss = reinterpret_cast<bf16 *>(smem + stage * Z::STAGE + Z::X_BYTES);
 #pragma unroll
-        for (int o = threadIdx.x; o < SLAB * Z::COLS / PER; o += RANK_THREADS) {
+        for (int o = threadIdx.x; o < DEPTH * Z::COLS / PER; o += RANK_THREADS) {
             const int m = o / (Z::COLS / PER), c = (o % (Z::COLS / PER)) * PER;
             const bool in = i0 + m < n && c0 + c < C;
             const long long i = in ? rows[i0 + m] : 0;
@@ -245,7 +250,7 @@ __device__ __forceinline__ void stack_tile(const StackWork<X> &w, int bx, int by
 #pragma unroll
         for (int q = 0; q < PB; ++q)
 #pragma unroll
-            for (int o = threadIdx.x; o < SLAB * NT; o += RANK_THREADS) {
+            for (int o = threadIdx.x; o < DEPTH * NT; o += RANK_THREADS) {
                 const int m = o / NT, r = (o % NT) * 8;
                 const bool in = i0 + m < n;
                 const long long i = in ? rows[i0 + m] : 0;
@@ -256,21 +261,21 @@ __device__ __forceinline__ void stack_tile(const StackWork<X> &w, int bx, int by
             signed char *es = reinterpret_cast<signed char *>(ss) + Z::S_BYTES;
             const int m = threadIdx.x / 4, block = c0 / ACT8_BLOCK + threadIdx.x % 4;
             const bool in = i0 + m < n && block * ACT8_BLOCK < C;
-            es[threadIdx.x] = in ? x.e[rows[i0 + m] * x.lde + block] : E(0);
+            if (m < DEPTH) es[threadIdx.x] = in ? x.e[rows[i0 + m] * x.lde + block] : E(0);
         }
     };
 
     float sum[NT][4] = {};
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) {
-        if (s * SLAB < n) fill(s, s * SLAB);
+        if (s * DEPTH < n) fill(s, s * DEPTH);
         sg::cp_async_commit();
     }
     int stage = 0;
-    for (int i0 = 0; i0 < n; i0 += SLAB) {
+    for (int i0 = 0; i0 < n; i0 += DEPTH) {
         sg::cp_async_wait<STAGES - 2>();
         __syncthreads();   // this slab has landed, and the stage filled next has been read
-        if (i0 + (STAGES - 1) * SLAB < n) fill((stage + STAGES - 1) % STAGES, i0 + (STAGES - 1) * SLAB);
+        if (i0 + (STAGES - 1) * DEPTH < n) fill((stage + STAGES - 1) % STAGES, i0 + (STAGES - 1) * DEPTH);
         sg::cp_async_commit();
         const E *xs = reinterpret_cast<const E *>(smem + stage * Z::STAGE);
         const bf16 *ss = reinterpret_cast<const bf16 *>(smem + stage * Z::STAGE + Z::X_BYTES);
@@ -307,7 +312,7 @@ __device__ __forceinline__ void stack_tile(const StackWork<X> &w, int bx, int by
 #pragma unroll
         for (int pass = APART ? 1 : 0; pass < 2; ++pass) {
 #pragma unroll
-            for (int kk = 0; kk < SLAB; kk += 16) {
+            for (int kk = 0; kk < DEPTH; kk += 16) {
                 uint32_t fa[PA][4];
                 columns(fa, kk);
 #pragma unroll
@@ -343,10 +348,14 @@ __device__ __forceinline__ void stack_tile(const StackWork<X> &w, int bx, int by
         }
 }
 
+// Blocks to an SM that the registers are limited for.  (float32 of rank 64, 4483 x 5120 x
+// 5760: 158 us at one, 125 at two.)
+constexpr int stack_blocks(int parts, int nt) { return nt <= 4 ? (parts == 2 ? 4 : 2) : nt == 8 ? 2 : 1; }
+
 // Both gradients: X^T G (C = K columns of X, 128 to a block) and H^T dY (N columns of dY),
 // each for max_chunks chunks.
 template <class XA, class XB, int PB, int NT>
-__global__ void __launch_bounds__(RANK_THREADS)
+__global__ void __launch_bounds__(RANK_THREADS, stack_blocks(PB, NT))
     stack_tile_kernel(StackWork<XA> wa, StackWork<XB> wb, int M, int pitch, Adapters ad, Groups g) {
     extern __shared__ __align__(16) unsigned char smem_stack[];
     __shared__ int rows[CHUNK_ROWS];
