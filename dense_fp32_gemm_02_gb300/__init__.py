@@ -1,4 +1,5 @@
-"""GB300-native FP32 SGEMM: C = alpha*A*B + beta*C, row-major, behind a C ABI.
+"""GB300-native FP32 SGEMM: C = alpha*A*B + beta*C, row-major, behind a C ABI; and around it the
+linear layer of a language model (low-rank adapters, 8-bit activation checkpoints).
 
 The compute path is ``libsgemm`` (hand-written CUDA for sm_103a, built from
 ``csrc/``); ``binding`` marshals torch tensors to it and nothing else.  The
