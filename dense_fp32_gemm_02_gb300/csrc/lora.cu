@@ -512,12 +512,17 @@ int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
     return ws.release();
 }
 
-// Few rows: their sums of the rank side are cheaper taken one by one than grouped by
-// adapter (five launches, 40 us) up to about 4096 of them.
+// Few rows: the rank side row by row (M rank (K + N) elements of the stack from L2, and
+// partial sums of all of Y) against grouping it by adapter (five launches more, about 25
+// us).  us, row by row / grouped, bfloat16: 256 x 4096 x 4096 of rank 16 44 / 69, 512 rows
+// 78 / 70; 512 x 1024 x 1024 of rank 64 33 / 37, 1024 rows 49 / 35; 1118 x 64 x 192 of
+// rank 78 17 / 27; 4096 x 256 x 256 of rank 16 32 / 28.
 bool few_rows(const Call &c) {
     if (c.K == 0 || c.N == 0) return false;
     if (c.M <= STREAM_ROWS) return true;
-    return c.M <= FEW_ROWS && (c.L == 0 || (long long)c.M * c.R <= 4096);
+    if (c.L == 0) return c.M <= 256;
+    const long long stack = (long long)c.M * c.R * ((long long)c.K + c.N);
+    return c.M <= FEW_ROWS && stack <= 68000000 && (long long)c.M * c.N <= 1500000;
 }
 
 template <class T>

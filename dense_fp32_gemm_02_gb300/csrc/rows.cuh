@@ -6,7 +6,7 @@
 //   up to 8             stream_rows_kernel: W to registers 16 bytes at a time, fp32 FMAs;
 //   float32 up to 64    few_rows_kernel: W through shared memory, the warp-level MMA on
 //                       three bfloat16 parts, split in registers;
-//   else, up to 256     parts_gemm.cuh.
+//   else                parts_gemm.cuh.
 // At 4096 x 4096 without adapters, us: bfloat16 (W is 5.0 of them) 1 row 9.6, 4 rows 12.5,
 // 8 rows 20.5 and by parts_gemm 9 rows 15.4 (by FMAs 16 rows 34), 64 rows 17.6 (the
 // warp-level MMA took 32: its operands pass through shared memory five times); float32 (W
@@ -21,7 +21,7 @@
 
 namespace sgl {
 
-constexpr int FEW_ROWS = 256, STREAM_ROWS = 8, MMA_ROWS = 64, ROWS_COLS = 128;
+constexpr int FEW_ROWS = 1280, STREAM_ROWS = 8, MMA_ROWS = 64, ROWS_COLS = 128;
 
 // The work: `across` x `ranges` blocks of the product, then M x `rank_ranges` blocks of
 // the rank side.

@@ -98,7 +98,7 @@ def test_forward(case, dtype):
     check_forward(p, *run_forward(p, pad, offset, H=L > 0), case)
 
 
-@pytest.mark.parametrize("M", [3, 40, 600])
+@pytest.mark.parametrize("M", [3, 40, 600, 1400])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_forward_defaults(M, dtype):
     """No scale, no ranks, no bias, no H."""
@@ -106,7 +106,7 @@ def test_forward_defaults(M, dtype):
     check_forward(p, *run_forward(p, H=False), "defaults")
 
 
-@pytest.mark.parametrize("M", [6, 70, 900])
+@pytest.mark.parametrize("M", [6, 70, 900, 1700])
 @pytest.mark.parametrize("ids", ["mixed", "runs"])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_an_adapters_infinities_and_nans_stay_in_its_rows(M, ids, dtype):
@@ -206,7 +206,7 @@ def test_gradients_against_differences():
     """loss = sum(V * Y) is linear in X, in A and in B one at a time, so (loss(+D) -
     loss(-D)) / 2 along D is the gradient's inner product with D, up to the fp32 rounding
     of Y (4e-6 of its norm, times V's) and of the gradient (the same, times D's)."""
-    p = Problem(500, 136, 264, 3, 16, torch.float32, ranks=False, bias=False)
+    p = Problem(1500, 136, 264, 3, 16, torch.float32, ranks=False, bias=False)
     p.A, p.B = torch.nan_to_num(p.A), torch.nan_to_num(p.B)
     _, h = run_forward(p)
     grads = dict(zip("XAB", run_backward(p, h)))
@@ -228,7 +228,7 @@ def test_gradients_against_differences():
         assert abs(have - quotient) <= 4e-6 * (size + float(grads[name].double().norm() * D.norm())), name
 
 
-@pytest.mark.parametrize("M", [4, 48, 700])
+@pytest.mark.parametrize("M", [4, 48, 700, 1500])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_repeats_are_bitwise_equal_on_any_stream(M, dtype):
     p = Problem(M, 264, 520, 4, 24, dtype, "mixed")
@@ -245,7 +245,7 @@ def test_repeats_are_bitwise_equal_on_any_stream(M, dtype):
     assert all(torch.equal(a, b) for a, b in zip(grads, grads2))
 
 
-@pytest.mark.parametrize("M", [4, 48, 700])
+@pytest.mark.parametrize("M", [4, 48, 700, 1500])
 def test_capture_in_a_graph(M):
     """A forward call captured once and replayed on new inputs."""
     b = binding()
