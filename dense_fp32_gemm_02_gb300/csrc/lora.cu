@@ -118,7 +118,7 @@ bool wide_stack(const Stack<T> &v, int L) {
 }
 
 // The parts of a rows x cols matrix as an operand: the matrix itself, or planes in the
-// workspace that prepare_kernel fills.
+// workspace that parts_kernel fills.
 template <class T>
 struct Packed {
     static constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
@@ -282,7 +282,7 @@ int many_rows(const Call &c, int sms, cudaMemPool_t pool) {
     const sgp::Split split = product ? sgp::plan_split(M, N, K, PRODUCTS, sms) : sgp::Split{0, 0};
     Grouping gr(c, want_stack ? (long long)c.K + c.N : 0, sms);
     const int ranges = K > 0 ? sgp::rank_splits(M, K, sms) : 0;   // (no contraction: no sums)
-    const int pitch = c.R <= 16 ? 16 : c.R <= 32 ? 32 : c.R <= 64 ? 64 : 128;
+    const int pitch = gr.width;   // of the rows of S and H, as parts
     const long long vpitch = pitch8(N), vplane = gr.width * vpitch, upitch = pitch8(K), uplane = gr.width * upitch;
 
     sgh::Workspace ws(pool, c.stream);
@@ -295,8 +295,8 @@ int many_rows(const Call &c, int sms, cudaMemPool_t pool) {
     const size_t pa_floats = want_stack ? size_t(gr.max_chunks) * c.R * c.K : 0;
     const size_t pb_floats = want_stack ? size_t(gr.max_chunks) * c.R * c.N : 0;
     st = ws.allocate(gr.bytes() + piece(s_floats * 4) + piece(r_floats * 4) + piece(h_elems * 2) + piece(v_elems * 2) +
-                     piece(u_elems * 2) + 2 * piece(row_elems * 2) + piece(pa_floats * 4) + piece(pb_floats * 4) + P.bytes() + Q.bytes() +
-                     piece(split.partial_floats * 4));
+                     piece(u_elems * 2) + 2 * piece(row_elems * 2) + piece(pa_floats * 4) + piece(pb_floats * 4) +
+                     P.bytes() + Q.bytes() + piece(split.partial_floats * 4));
     if (st != SGEMM_OK) return st;
     gr.place(ws);
     RankSide side{ws.take<float>(s_floats), c.H, c.ldh, nullptr, nullptr, nullptr, pitch};
@@ -332,9 +332,8 @@ int many_rows(const Call &c, int sms, cudaMemPool_t pool) {
                                      ad, gr.g.planes, gr.g.plane_adapter, gr.g.position};
             if ((st = sgp::run_rank<T>(r, ranges, r_partial, sms, c.stream)) != SGEMM_OK) return st;
         }
-        // four warps to a row where there are few (154 rows of rank 122: 18 -> 6 us; 512 rows of
-        // 32 adapters of rank 16: 17 -> 9), one
-        // else (8192 of rank 64: 7 us, four 15)
+        // Four warps to a row where there are few (154 rows of rank 122: 18 -> 6 us; 512 rows
+        // of 32 adapters of rank 16: 17 -> 9), else one (8192 rows of rank 64: 7 us, four 15).
         const bool four = M <= 2048;
         st = launch(nullptr, four ? rank_finish_kernel<T, 4> : rank_finish_kernel<T, 1>,
                     dim3(unsigned(four ? (M + 1LL) / 2 : (M + 7LL) / 8)), 256, 0, c.stream, M, ranges,

@@ -4,9 +4,9 @@
 // A bfloat16 matrix is one part, and so is an 8-bit checkpoint (act8.cuh).  A
 // float32 matrix is three: x = x0 + x1 + x2 exactly, each part the leading 8 bits
 // of what the ones before leave.  A product of float32 matrices takes the six pairs
-// whose parts' ranks add up to at most 2 (what is left out is below 2^-22 of
-// |a||b|); with one part on one side it takes three.  Six bfloat16 MMAs cost what
-// three TF32 ones do and keep three more bits.
+// whose parts' ranks add up to at most 2 (what is left out is at most 2^-21 of
+// |a||b|, 2^-24 on average); with one part on one side it takes three, and nothing is
+// left out.  Six bfloat16 MMAs cost what three TF32 ones do.
 //
 // The MMA's additions to its fp32 accumulator truncate: sums of n steps come out
 // smaller by up to n * 2^-23 (measured: 4.4e-6 of the result at K = 4096 for one
@@ -28,6 +28,12 @@
 // value is nothing, unless that is an infinity or a NaN: a tile with such an adapter
 // takes the term by FMAs in the epilogue, each row from its own adapter alone.
 // Waits are bounded as in tf32x3_pair.cuh, whose abort protocol this is.
+//
+// Bound by the tensor pipe where the tiles fill whole waves: 8192 x 4096 x 4096 bfloat16 166
+// us (1.66 PFLOP/s; the pipe 76 % busy), 4096^3 float32 428 us (1.93 PFLOP/s of bfloat16
+// MMAs); at few rows by W's bytes and latency (64 x 4096 x 4096: about 11 us, 3 TB/s).
+// 256-column tiles on pairs because a single SM's 128 x 256 would take 96 bytes of operands
+// per cycle from L2, a pair's SM takes 64.
 #pragma once
 
 #include "kernels.cuh"

@@ -15,7 +15,9 @@
  *  - Sizes are at most 2^31 - 65536 (SGEMM_ERR_TOO_LARGE above that).
  *  - Elements of an output outside its rows x columns block are not written.
  *  - Results are bitwise reproducible from call to call on a GPU model.
- *  - The work is enqueued on `stream`; nothing synchronises the host.
+ *  - The work is enqueued on `stream`; nothing synchronises the host.  Workspaces come
+ *    from the library's stream-ordered pool and go back to it behind the last kernel.
+ *    Every call may be captured in a graph after a first call on the device.
  */
 #ifndef DENSE_FP32_GEMM_02_GB300_SGEMM_LAYERS_H
 #define DENSE_FP32_GEMM_02_GB300_SGEMM_LAYERS_H
@@ -85,7 +87,7 @@ int sgemm_lora(int type, int M, int N, int K, int L, int R,
  * NULL, and dA may be NULL together with dB: those are not computed, and the
  * inputs that only they need (W and dX; X and H) are not read.  dA and dB are
  * written whole: zero past an adapter's rank and for adapters without rows.
- * They must not overlap an input or each other.
+ * The outputs must not overlap an input or each other.
  */
 int sgemm_lora_backward(int type, int M, int N, int K, int L, int R,
                         const void *dY, int lddy,
