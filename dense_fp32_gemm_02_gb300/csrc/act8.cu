@@ -24,11 +24,17 @@ constexpr int kThreads = 256;
 //   erf x = 1 - (a1 t + ... + a5 t^5) exp(-x^2),  t = 1 / (1 + p x),  x >= 0,
 // whose error is at most 1.5e-7, i.e. that of fp32 itself at this size.  The exponential is
 // the one that the derivative needs anyway, and both come without cancellation.  (x = |z| /
-// sqrt 2 is folded into p, the half of Phi into the a's.)  Two elements at a time: with
-// single-precision instructions for one, GELU over 8192 x 16384 bfloat16 took 175 us.
+// sqrt 2 is folded into p, the half of Phi into the a's.)  Two elements at a time, and the
+// approximate reciprocal alone for a division: GELU over 8192 x 16384 bfloat16 took 175 us
+// one at a time, 126 with __fdividef.
 __device__ __forceinline__ float exp2f_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float reciprocal_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
@@ -36,8 +42,8 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ void normal_tail(float2 z, float2 &tail, float2 &bell) {
     const float2 e = __fmul2_rn(__fmul2_rn(z, z), both(-0.72134752f));   // -z^2/2 log2 e
     bell = make_float2(exp2f_fast(e.x), exp2f_fast(e.y));
-    const float2 t = make_float2(__fdividef(1.0f, fmaf(0.23164190f, fabsf(z.x), 1.0f)),
-                                 __fdividef(1.0f, fmaf(0.23164190f, fabsf(z.y), 1.0f)));
+    const float2 t = make_float2(reciprocal_fast(fmaf(0.23164190f, fabsf(z.x), 1.0f)),
+                                 reciprocal_fast(fmaf(0.23164190f, fabsf(z.y), 1.0f)));
     float2 p = __ffma2_rn(t, both(0.5307027145f), both(-0.7265760135f));
     p = __ffma2_rn(t, p, both(0.7107068705f));
     p = __ffma2_rn(t, p, both(-0.142248368f));
@@ -75,9 +81,17 @@ __device__ __forceinline__ float2 slope(float2 z) {
 
 // ------------------------------------------------------------------ kernels
 // What a kernel works on: `units` of 32 columns (wide forms) or 256, `per_row` to a row.
+// Rows are found by multiplication (Granlund and Montgomery, Division by Invariant
+// Integers using Multiplication, 1994): three instructions for about twenty, of the 150 that
+// eight elements take.
 struct Blocks {
     unsigned units, per_row;
     int K;
+    unsigned factor, shift;
+
+    __device__ unsigned row_of(unsigned u) const {   // u / per_row, for u < 2^31
+        return (__umulhi(u, factor) + u) >> shift;
+    }
 };
 struct Checkpoint {
     signed char *q, *e;
@@ -85,14 +99,16 @@ struct Checkpoint {
 };
 
 // Wide form, for rows that are 16-byte aligned and of a multiple of 8 columns: a quarter
-// of a block to a thread, its maximum over four lanes.  Storing keeps 64 bytes of loads in
-// flight per thread, reading back 32 of bfloat16.  At 8192 x 16384, us (GB/s over the bytes
-// of either side): bfloat16 store 70, with GELU 125 (5400), GELU gradient 132 (5100), load
-// 68; float32 with GELU 174 (6940).  Half or twice the depth: store 133 or 158 with GELU,
-// gradient (twice, four times) 151 or 231.
+// of a block to a thread, its maximum over four lanes; so many blocks to a thread, all
+// loaded before the first is used.  At 8192 x 16384, us (GB/s over the bytes of either
+// side): bfloat16 store 68, with GELU 113 (5980), GELU gradient 112 (6030), load 67
+// (6080); float32 with GELU 174 (6940), gradient 173.  What is left is issue slots: storing
+// with half the depth 119, the gradient with two blocks to a thread 129, with four 151;
+// reading back with one 72.
 template <class T>
 constexpr int kStoreDepth = sizeof(T) == 2 ? 4 : 2;
-constexpr int kReadDepth = 2;
+template <bool GRAD>
+constexpr int kReadDepth = GRAD ? 1 : 2;
 
 template <class T, int ACT, bool WITH_Y>
 __global__ void __launch_bounds__(kThreads)
@@ -107,7 +123,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int d = 0; d < D; ++d) {
         const unsigned u = first + d * (kThreads / 4);
-        row[d] = u / b.per_row;
+        row[d] = b.row_of(u);
         col[d] = int(u - row[d] * b.per_row) * ACT8_BLOCK + sub * 8;
         in[d] = u < b.units && col[d] < b.K;
 #pragma unroll
@@ -157,7 +173,7 @@ __global__ void __launch_bounds__(kThreads)
     store_any_kernel(Blocks b, const T *Z, long long ldz, Checkpoint c, T *Y, long long ldy) {
     constexpr int D = kAnyDepth;
     const int lane = threadIdx.x & 31;
-    const unsigned u = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), row = u / b.per_row;
+    const unsigned u = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), row = b.row_of(u);
     if (u >= b.units) return;
     const int c0 = int(u - row * b.per_row) * (D * ACT8_BLOCK) + lane;
     const T *zr = Z + (long long)row * ldz + c0;
@@ -195,7 +211,7 @@ __global__ void __launch_bounds__(kThreads)
 template <class T, int ACT, bool GRAD>
 __global__ void __launch_bounds__(kThreads)
     read_wide_kernel(Blocks b, Checkpoint c, const T *dY, long long lddy, T *out, long long ldo) {
-    constexpr int D = kReadDepth;
+    constexpr int D = kReadDepth<GRAD>;
     const int sub = threadIdx.x & 3;
     const unsigned first = (blockIdx.x * D) * (kThreads / 4) + (threadIdx.x >> 2);
     uint2 w[D];
@@ -207,7 +223,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int d = 0; d < D; ++d) {
         const unsigned u = first + d * (kThreads / 4);
-        row[d] = u / b.per_row;
+        row[d] = b.row_of(u);
         col[d] = int(u - row[d] * b.per_row) * ACT8_BLOCK + sub * 8;
         in[d] = u < b.units && col[d] < b.K;
         if (!in[d]) continue;
@@ -237,7 +253,7 @@ __global__ void __launch_bounds__(kThreads)
     read_any_kernel(Blocks b, Checkpoint c, const T *dY, long long lddy, T *out, long long ldo) {
     constexpr int D = kAnyDepth;
     const int lane = threadIdx.x & 31;
-    const unsigned u = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), row = u / b.per_row;
+    const unsigned u = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), row = b.row_of(u);
     if (u >= b.units) return;
     const int c0 = int(u - row * b.per_row) * (D * ACT8_BLOCK) + lane;
     const signed char *q = c.q + row * c.ldq + c0, *e = c.e + row * c.lde + (c0 - lane) / ACT8_BLOCK;
@@ -302,7 +318,10 @@ int over_rows(int M, int K, F &&launch) {
 
 Blocks blocks_in(int rows, int K, bool wide_form) {
     const unsigned per_row = unsigned(wide_form ? blocks_of(K) : (blocks_of(K) + kAnyDepth - 1) / kAnyDepth);
-    return Blocks{unsigned(rows) * per_row, per_row, K};
+    unsigned shift = 0;
+    while ((1u << shift) < per_row) ++shift;
+    const unsigned long long gap = (1ull << shift) - per_row;
+    return Blocks{unsigned(rows) * per_row, per_row, K, unsigned((gap << 32) / per_row + 1), shift};
 }
 unsigned grid_of(unsigned units, unsigned per_block) { return (units + per_block - 1) / per_block; }
 
@@ -335,7 +354,7 @@ int read(int M, int K, Checkpoint c, const T *dY, int lddy, T *out, int ldo, cud
         const T *dy = GRAD ? dY + r * lddy : nullptr;
         if (w)
             read_wide_kernel<T, ACT, GRAD>
-                <<<grid_of(b.units, kReadDepth * kThreads / 4), kThreads, 0, stream>>>(
+                <<<grid_of(b.units, kReadDepth<GRAD> * kThreads / 4), kThreads, 0, stream>>>(
                     b, at, dy, lddy, out + r * ldo, ldo);
         else
             read_any_kernel<T, ACT, GRAD>
