@@ -25,6 +25,20 @@ __device__ __forceinline__ bf16 from_f32<bf16>(float x) {
     return __float2bfloat16_rn(x);
 }
 
+// Division of u < 2^31 by an invariant d, in three instructions instead of about twenty
+// (Granlund and Montgomery, Division by Invariant Integers using Multiplication, 1994).
+struct Divisor {
+    unsigned d, factor, shift;
+
+    static Divisor of(unsigned d) {
+        unsigned shift = 0;
+        while ((1u << shift) < d) ++shift;
+        const unsigned long long gap = (1ull << shift) - d;
+        return Divisor{d, unsigned((gap << 32) / d + 1), shift};
+    }
+    __device__ unsigned quotient(unsigned u) const { return (__umulhi(u, factor) + u) >> shift; }
+};
+
 // The two bfloat16 of a 32-bit word (the lower address in the low half).
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }

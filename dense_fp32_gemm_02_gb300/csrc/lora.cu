@@ -138,7 +138,7 @@ struct Packed {
         if (!direct) parts = Parts{ws.take<bf16>(elements()), pitch, rows * pitch};
     }
     PartsJob<Rows<T>> job() const {   // (no rows where the TMA reads the matrix itself)
-        return {Rows<T>{src, ld}, direct ? 0 : int(rows), int(cols), wide_rows(src, ld), parts};
+        return PartsJob<Rows<T>>(Rows<T>{src, ld}, direct ? 0 : int(rows), int(cols), wide_rows(src, ld), parts);
     }
     sgp::Operand operand() const {
         if (direct)
@@ -559,7 +559,7 @@ int weight_grad(int M, int N, int K, Act8Rows x, const void *dY, int lddy, float
     const Parts xp{ws.take<bf16>(x_elems), xpitch, M * xpitch};
     D.place(ws);
     float *partial = split.partial_floats ? ws.take<float>(split.partial_floats) : nullptr;
-    const PartsJob<Act8Rows> xjob{x, M, K, aligned(x.q, 8) && x.ldq % 8 == 0, xp};
+    const PartsJob<Act8Rows> xjob(x, M, K, aligned(x.q, 8) && x.ldq % 8 == 0, xp);
     st = prepare<1, Packed<T>::PARTS>(M, Adapters{}, Groups{}, xjob, D.job(), sms, stream);
     if (st != SGEMM_OK) return st;
     sgp::Product g;

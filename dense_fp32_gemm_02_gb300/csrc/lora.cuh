@@ -87,19 +87,22 @@ struct PartsJob {
     int rows, cols;
     bool wide;
     Parts to;
+    Divisor per_row;     // octets
 
-    __host__ __device__ long long octets() const { return (long long)rows * ((cols + 7) / 8); }
+    PartsJob(X x_, int rows_, int cols_, bool wide_, Parts to_)
+        : x(x_), rows(rows_), cols(cols_), wide(wide_), to(to_),
+          per_row(Divisor::of(cols > 0 ? unsigned((cols + 7LL) / 8) : 1u)) {}
+    __host__ __device__ long long octets() const { return (long long)rows * ((cols + 7LL) / 8); }
 };
 
 // Octets t, t + step, ... of a job: a thread to eight columns of a row.
 template <int PARTS, class X>
 __device__ __forceinline__ void take_parts(const PartsJob<X> &job, long long t, long long step) {
-    const int per_row = (job.cols + 7) / 8;
     const long long total = job.octets();
-    const bool small = total <= 0xffffffffll;   // 32-bit division: a third of the time
+    const bool small = total <= 0x7fffffffll;
     for (; t < total; t += step) {
-        const long long i = small ? (long long)(unsigned(t) / unsigned(per_row)) : t / per_row;
-        const int c = int(t - i * per_row) * 8;
+        const long long i = small ? (long long)job.per_row.quotient(unsigned(t)) : t / job.per_row.d;
+        const int c = int(t - i * job.per_row.d) * 8;
         float v[8];
         if (job.wide && c + 8 <= job.cols) {
             job.x.at8(i, c, v);
