@@ -165,30 +165,32 @@ int launch(const char *text, void (*kernel)(P...), dim3 grid, unsigned threads, 
 }
 
 // ------------------------------------------------------------------ the first kernels
-// Groups the rows (g.perm not null) and takes the operands' parts.
+// Lays the planes out (g.planes not null), sorts the rows by adapter (g.perm not null) and
+// takes the operands' parts.
 template <int P_PARTS, int Q_PARTS, class XP, class XQ>
 int prepare(int M, const Adapters &ad, const Groups &g, const PartsJob<XP> &p, const PartsJob<XQ> &q, int sms,
             cudaStream_t stream) {
     int st = SGEMM_OK;
-    if (g.perm) {
+    if (g.planes) {
         if ((st = shared_limit(group_rows_kernel, sort_smem(ad.L))) != SGEMM_OK) return st;
-        st = launch(nullptr, group_rows_kernel, dim3(1), SORT_THREADS, sort_smem(ad.L), stream, M, ad, g);
+        st = launch(nullptr, group_rows_kernel, dim3(g.perm ? 2 : 1), SORT_THREADS, sort_smem(ad.L), stream, M, ad, g);
         if (st != SGEMM_OK) return st;
     }
     const long long octets = p.octets() + q.octets();
     if (octets == 0) return SGEMM_OK;
     const unsigned blocks = unsigned(std::min<long long>((octets + 255) / 256, 32LL * sms));
-    return launch(nullptr, parts_kernel<P_PARTS, Q_PARTS, XP, XQ>, dim3(blocks), 256, 0, stream, p, q, g.perm != nullptr);
+    return launch(nullptr, parts_kernel<P_PARTS, Q_PARTS, XP, XQ>, dim3(blocks), 256, 0, stream, p, q, g.planes != nullptr);
 }
 
 // Sizes and workspace of the grouping of a call's rows.
 struct Grouping {
     int M, L, chunk, max_chunks, tiles256, width, most_planes, capacity;
+    bool sorted;   // for the stack's gradients
     Groups g{};
 
     // chunk: rows of a partial sum of the stack's gradients, 512 where that makes
-    // blocks for every SM twice, else down to 128 (`columns`: of both gradients).
-    Grouping(const Call &c, long long columns, int sms) : M(c.M), L(c.L), chunk(CHUNK_ROWS) {
+    // blocks for every SM twice, else down to 128 (`columns`: of both gradients, 0: none).
+    Grouping(const Call &c, long long columns, int sms) : M(c.M), L(c.L), chunk(CHUNK_ROWS), sorted(columns > 0) {
         const long long across = (columns + 127) / 128;
         while (chunk > 128 && (M / chunk) * across < 2LL * sms) chunk /= 2;
         max_chunks = M / chunk + L;
@@ -201,22 +203,24 @@ struct Grouping {
     size_t bytes() const {
         const auto piece = [](size_t n) { return sgh::Workspace::piece(n); };
         return L == 0 ? 0
-                      : 2 * piece(size_t(M) * 4) + piece(size_t(max_chunks) * 16) + piece(size_t(L + 1) * 4) +
-                            2 * piece(size_t(L) * 4) + piece(size_t(tiles256) * 16) +
+                      : (sorted ? piece(size_t(M) * 4) + piece(size_t(max_chunks) * 16) + piece(size_t(L + 1) * 4) : 0) +
+                            piece(size_t(M) * 4) + 2 * piece(size_t(L) * 4) + piece(size_t(tiles256) * 16) +
                             piece(size_t(tiles256) * most_planes * 16);
     }
     void place(sgh::Workspace &ws) {
         if (L == 0) return;
-        g.perm = ws.take<int>(M);
-        g.chunks = ws.take<int4>(max_chunks);
-        g.chunk_begin = ws.take<int>(L + 1);
-        g.max_chunks = max_chunks, g.chunk = chunk;
+        if (sorted) {
+            g.perm = ws.take<int>(M);
+            g.chunks = ws.take<int4>(max_chunks);
+            g.chunk_begin = ws.take<int>(L + 1);
+            g.max_chunks = max_chunks, g.chunk = chunk;
+        }
         g.used = ws.take<int>(L);
         g.unclean = ws.take<int>(L);
         g.planes = ws.take<int4>(tiles256);
         g.plane_adapter = ws.take<int4>(size_t(tiles256) * most_planes);
         g.position = ws.take<int>(M);
-        g.capacity = capacity, g.width = width;
+        g.most_planes = most_planes, g.capacity = capacity, g.width = width;
     }
 };
 
@@ -353,6 +357,7 @@ int many_rows(const Call &c, int sms, cudaMemPool_t pool) {
                 g.v = {v.p, N, gr.width, (long long)PARTS * c.L, vpitch, vplane};
                 g.planes = gr.g.planes;
                 g.plane_adapter = gr.g.plane_adapter;
+                g.most_planes = gr.most_planes;
                 g.capacity = gr.capacity;
                 g.width = gr.width;
             }

@@ -145,9 +145,10 @@ struct Groups {
     int *unclean;        // L: whether it holds something that is not finite (pack_stack)
     int4 *planes;        // for each 256 rows {first plane, planes, 1 if the product may use them
                          // (not past the capacity, nor with an unclean adapter), 0}
-    int4 *plane_adapter; // of a plane's 64 / width adapters (the last one repeated), or
-                         // {adapter, first rank column} where width >= 64
+    int4 *plane_adapter; // most_planes for each 256 rows: a plane's 64 / width adapters (the
+                         // last one repeated), or {adapter, first rank column} where width >= 64
     int *position;       // M: which of its tile's adapters a row uses
+    int most_planes;     // of 256 rows
     int capacity;        // planes that have memory
     int width;           // 16, 32, 64 or 128
 };
@@ -181,74 +182,117 @@ __device__ __forceinline__ int group_at(const int *first, int n, int t) {
     return lo;
 }
 
-constexpr size_t sort_smem(int L) { return (size_t(32) * (L + 1) + 2 * (L + 2) + 32 * 32) * 4; }
+// Groups (or -1: none) of rows 256 t + 32 i + lane; -2 past the end.
+__device__ __forceinline__ void load_groups(int M, const Adapters &ad, const unsigned char *no_rank, int t, int (&b)[8]) {
+    const long long r0 = (long long)t * 256 + (threadIdx.x & 31);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = r0 + 32 * i < M ? ad.of_row(r0 + 32 * i) : -2;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (b[i] >= 0 && no_rank[b[i]]) b[i] = -1;
+}
 
-// One block of 1024 threads; each warp walks its share of the rows, 256 at a time, in two
-// passes of eight independent loads.  Bound by their latency and the counters': 6 us up to
-// 8192 rows.
-__global__ void __launch_bounds__(SORT_THREADS, 1) group_rows_kernel(int M, Adapters ad, Groups g) {
-    extern __shared__ int sm[];
-    __shared__ int warp_sum[32];
-    __shared__ unsigned char no_rank[MAX_ADAPTERS];
-    sg::wait_prerequisites();
-    sg::launch_dependents();
-    const int L = ad.L, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int *count = sm;                       // [warp][group], then the next place of each
-    int *first = count + 32 * (L + 1);     // L + 2: first place of a group
-    int *chunk0 = first + (L + 2);
-    int *bits = chunk0 + (L + 2) + warp * 32;   // the adapters of this warp's current 256 rows
-    const int a = threadIdx.x;
-    if (a < L) no_rank[a] = ad.rank(a) == 0, g.unclean[a] = 0;
-    for (int i = threadIdx.x; i < 32 * (L + 1); i += SORT_THREADS) count[i] = 0;
+// For each 256 rows the adapters that they use, in ascending order, their planes, and
+// which of them each row uses.  A warp to 256 rows, by a bit for each adapter.
+__device__ __forceinline__ void lay_out_planes(int M, const Adapters &ad, const Groups &g, const unsigned char *no_rank,
+                                               int *sm, int *warp_sum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, a = threadIdx.x, tiles = (M + 255) / 256;
+    int *bits = sm + warp * 32, *used = sm + 32 * 32;
+    used[a] = 0;
     __syncthreads();
-    const int tiles = (M + 255) / 256, per = (tiles + 31) / 32;
-    const int t0 = min(warp * per, tiles), t1 = min(t0 + per, tiles);
-    int *mine = count + warp * (L + 1);
-    // groups of rows 256 t + 32 i + lane; -1 past the end
-    auto load = [&](int t, int (&b)[8]) {
-        const long long r0 = (long long)t * 256 + lane;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = r0 + 32 * i < M ? ad.of_row(r0 + 32 * i) : -2;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = b[i] == -2 ? -1 : (b[i] < 0 || no_rank[b[i]] ? L : b[i]);
-    };
-    for (int t = t0; t < t1; ++t) {
+    const int per_plane = g.width >= 64 ? 1 : 64 / g.width, halves = g.width > 64 ? g.width / 64 : 1;
+    for (int t = warp; t < tiles; t += 32) {
         int b[8];
-        load(t, b);
+        load_groups(M, ad, no_rank, t, b);
         bits[lane] = 0;
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const unsigned same = __match_any_sync(0xffffffffu, b[i]);
             if (b[i] >= 0 && (same & ((1u << lane) - 1)) == 0) {
-                mine[b[i]] += __popc(same);
-                if (b[i] < L) atomicOr(&bits[b[i] >> 5], 1 << (b[i] & 31));
+                atomicOr(&bits[b[i] >> 5], 1 << (b[i] & 31));
+                used[b[i]] = 1;
             }
+        }
+        __syncwarp();
+        // word w of the bits is lane w's; below: adapters in the words before it
+        const unsigned word = unsigned(bits[lane]);
+        int below = __popc(word);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, below, o);
+            if (lane >= o) below += u;
+        }
+        const int kinds = __shfl_sync(0xffffffffu, below, 31), planes = (kinds * g.width + 63) / 64;
+        below -= __popc(word);
+        if (lane == 0) g.planes[t] = make_int4(0, planes, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int w = max(b[i], 0) >> 5 & 31;
+            const unsigned of_w = __shfl_sync(0xffffffffu, word, w);
+            const int position = __shfl_sync(0xffffffffu, below, w) + __popc(of_w & ((1u << (b[i] & 31)) - 1));
+            if (b[i] > -2) g.position[t * 256 + i * 32 + lane] = b[i] >= 0 ? position : 0;
+        }
+        int4 *list = g.plane_adapter + (long long)t * g.most_planes;
+        unsigned left = word;
+        for (int k = below; left != 0; ++k, left &= left - 1) {
+            const int id = lane * 32 + __ffs(left) - 1;
+            if (!SG_IN_RANGE(k * g.width / 64 < min(planes, g.most_planes))) break;
+            if (g.width >= 64) {
+                for (int h = 0; h < halves; ++h) list[k * halves + h] = make_int4(id, h * 64, 0, 0);
+            } else {
+                int *to = reinterpret_cast<int *>(&list[k / per_plane]);
+                to[k % per_plane] = id;
+                if (k == kinds - 1)
+                    for (int d = k % per_plane + 1; d < per_plane; ++d) to[d] = id;
+            }
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    if (a < ad.L) g.used[a] = used[a], g.unclean[a] = 0;
+    int all;
+    for (int base = 0, t = 0; t < tiles; t += SORT_THREADS, base += all) {   // first planes of the tiles
+        const int n = t + a < tiles ? g.planes[t + a].y : 0;
+        const int p = base + block_prefix(n, warp_sum, all);
+        if (t + a < tiles) g.planes[t + a] = make_int4(p, n, p + n <= g.capacity, 0);
+    }
+}
+
+// The counting sort: each warp walks its share of the rows twice, 256 at a time.
+__device__ __forceinline__ void sort_rows(int M, const Adapters &ad, const Groups &g, const unsigned char *no_rank, int *sm,
+                                          int *warp_sum) {
+    const int L = ad.L, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, a = threadIdx.x;
+    int *count = sm;                       // [warp][group], then the next place of each
+    int *first = count + 32 * (L + 1);     // L + 2: first place of a group
+    int *chunk0 = first + (L + 2);
+    for (int i = threadIdx.x; i < 32 * (L + 1); i += SORT_THREADS) count[i] = 0;
+    __syncthreads();
+    const int tiles = (M + 255) / 256, per = (tiles + 31) / 32;
+    const int t0 = min(warp * per, tiles), t1 = min(t0 + per, tiles);
+    int *mine = count + warp * (L + 1);
+    for (int t = t0; t < t1; ++t) {
+        int b[8];
+        load_groups(M, ad, no_rank, t, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int group = b[i] == -1 ? L : b[i];
+            const unsigned same = __match_any_sync(0xffffffffu, group);
+            if (group >= 0 && (same & ((1u << lane) - 1)) == 0) mine[group] += __popc(same);
             __syncwarp();
         }
-        const int kinds = __reduce_add_sync(0xffffffffu, __popc(bits[lane]));
-        if (lane == 0) g.planes[t] = make_int4(0, (kinds * g.width + 63) / 64, 0, 0);
-        __syncwarp();
     }
     __syncthreads();
     // first places of the groups (up to 1025 of them: group L by the last thread alone)
     int rows = 0, all;
     if (a < L)
         for (int w = 0; w < 32; ++w) rows += count[w * (L + 1) + a];
-    if (a < L) g.used[a] = rows > 0;
     const int at = block_prefix(rows, warp_sum, all);
     if (a < L) first[a] = at;
     if (a == SORT_THREADS - 1) first[L] = at + rows, first[L + 1] = M;
     const int chunk_at = block_prefix((rows + g.chunk - 1) / g.chunk, warp_sum, all);
     if (a < L) chunk0[a] = chunk_at;
     if (a == SORT_THREADS - 1) chunk0[L] = all;
-    // first planes of the tiles
-    for (int base = 0, t = 0; t < tiles; t += SORT_THREADS) {
-        const int n = t + a < tiles ? g.planes[t + a].y : 0;
-        const int p = base + block_prefix(n, warp_sum, all);
-        if (t + a < tiles) g.planes[t + a] = make_int4(p, n, p + n <= g.capacity, 0);
-        base += all;
-    }
     __syncthreads();
     for (int b = threadIdx.x; b <= L; b += SORT_THREADS) {
         g.chunk_begin[b] = chunk0[b];
@@ -262,56 +306,19 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) group_rows_kernel(int M, Adap
     __syncthreads();
     for (int t = t0; t < t1; ++t) {
         int b[8];
-        load(t, b);
-        bits[lane] = 0;
-        __syncwarp();
+        load_groups(M, ad, no_rank, t, b);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const unsigned same = __match_any_sync(0xffffffffu, b[i]);
+            const int group = b[i] == -1 ? L : b[i];
+            const unsigned same = __match_any_sync(0xffffffffu, group);
             const int before = __popc(same & ((1u << lane) - 1));
-            const int place = b[i] >= 0 ? mine[b[i]] + before : 0;
+            const int place = group >= 0 ? mine[group] + before : 0;
             __syncwarp();
-            if (b[i] >= 0) {
+            if (group >= 0) {
                 if (SG_IN_RANGE(place >= 0 && place < M)) g.perm[place] = t * 256 + i * 32 + lane;
-                if (before == 0) {
-                    mine[b[i]] += __popc(same);
-                    if (b[i] < L) atomicOr(&bits[b[i] >> 5], 1 << (b[i] & 31));
-                }
+                if (before == 0) mine[group] += __popc(same);
             }
             __syncwarp();
-        }
-        // the tile's adapters in ascending order: word w of the bits is lane w's
-        const unsigned word = unsigned(bits[lane]);
-        int below = __popc(word);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, below, o);
-            if (lane >= o) below += u;
-        }
-        const int kinds = __shfl_sync(0xffffffffu, below, 31);
-        below -= __popc(word);
-        const int4 planes = g.planes[t];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int w = max(b[i], 0) >> 5 & 31;
-            const unsigned of_w = __shfl_sync(0xffffffffu, word, w);
-            const int position = __shfl_sync(0xffffffffu, below, w) + __popc(of_w & ((1u << (b[i] & 31)) - 1));
-            if (b[i] >= 0) g.position[t * 256 + i * 32 + lane] = b[i] < L ? position : 0;
-        }
-        const int per_plane = g.width >= 64 ? 1 : 64 / g.width, halves = g.width > 64 ? g.width / 64 : 1;
-        unsigned left = word;
-        for (int k = below; left != 0; ++k, left &= left - 1) {
-            const int id = lane * 32 + __ffs(left) - 1;
-            if (g.width >= 64) {
-                for (int h = 0; h < halves; ++h)
-                    if (SG_IN_RANGE(k * halves + h < planes.y))
-                        g.plane_adapter[planes.x + k * halves + h] = make_int4(id, h * 64, 0, 0);
-            } else if (SG_IN_RANGE(k / per_plane < planes.y)) {
-                int *to = reinterpret_cast<int *>(&g.plane_adapter[planes.x + k / per_plane]);
-                to[k % per_plane] = id;
-                if (k == kinds - 1)
-                    for (int d = k % per_plane + 1; d < per_plane; ++d) to[d] = id;
-            }
         }
     }
     for (int t = threadIdx.x; t < g.max_chunks; t += SORT_THREADS) {
@@ -322,6 +329,27 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) group_rows_kernel(int M, Adap
         const int b = group_at(chunk0, L, t), p = first[b] + (t - chunk0[b]) * g.chunk;
         g.chunks[t] = make_int4(b, p, min(g.chunk, first[b + 1] - p), 0);
     }
+}
+
+constexpr size_t sort_smem(int L) {
+    const size_t sort = size_t(32) * (L + 1) + 2 * (L + 2), planes = 32 * 32 + SORT_THREADS;
+    return (sort > planes ? sort : planes) * 4;
+}
+
+// Block 0 lays the planes out; block 1, where there is one, sorts the rows.  Bound by
+// latency: 6 us up to 8192 rows.
+__global__ void __launch_bounds__(SORT_THREADS, 1) group_rows_kernel(int M, Adapters ad, Groups g) {
+    extern __shared__ int sm[];
+    __shared__ int warp_sum[32];
+    __shared__ unsigned char no_rank[MAX_ADAPTERS];
+    sg::wait_prerequisites();
+    sg::launch_dependents();
+    if (int(threadIdx.x) < ad.L) no_rank[threadIdx.x] = ad.rank(threadIdx.x) == 0;
+    __syncthreads();
+    if (blockIdx.x == 0)
+        lay_out_planes(M, ad, g, no_rank, sm, warp_sum);
+    else
+        sort_rows(M, ad, g, no_rank, sm, warp_sum);
 }
 
 // One side of the stack laid out for the tensor cores: the parts of the used adapters as

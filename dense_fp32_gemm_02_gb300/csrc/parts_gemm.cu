@@ -141,6 +141,7 @@ int sgp::run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Spl
     if (p.planes) {
         kp.planes = p.planes;
         kp.plane_adapter = p.plane_adapter;
+        kp.most_planes = p.most_planes;
         kp.capacity = p.capacity;
         kp.width = p.width;
         kp.L = epi.ad.L;
@@ -198,6 +199,7 @@ int sgp::run_rank(const RankProduct &p, int splits, float *partial, int sms, cud
     kp.planes = p.planes;
     kp.plane_adapter = p.plane_adapter;
     kp.position = p.position;
+    kp.most_planes = p.most_planes;
     kp.width = p.width;
     kp.L = p.ad.L;
     kp.partial = partial;

@@ -31,7 +31,8 @@
 //
 // Bound by the tensor pipe where the tiles fill whole waves: 8192 x 4096 x 4096 bfloat16 166
 // us (1.66 PFLOP/s; the pipe 76 % busy), 4096^3 float32 428 us (1.93 PFLOP/s of bfloat16
-// MMAs); at few rows by W's bytes and latency (64 x 4096 x 4096: about 11 us, 3 TB/s).
+// MMAs); at few rows by W's bytes and latency (64 x 4096 x 4096: 18 us with the kernel that
+// adds its four ranges).
 // 256-column tiles on pairs because a single SM's 128 x 256 would take 96 bytes of operands
 // per cycle from L2, a pair's SM takes 64.
 #pragma once
@@ -64,7 +65,7 @@ struct KernelParams {
     const int4 *planes;     // of the rank side, see Product (null: none)
     const int4 *plane_adapter;
     const int *position;
-    int capacity, width, L;
+    int most_planes, capacity, width, L;
     float *partial;         // splits x M x N, or null
     unsigned long long timeout_ns;
     bool wait_last;         // launched early: it reads nothing of the kernel before it
@@ -120,6 +121,7 @@ struct Items {
     struct Item {
         int tm, col0, ncols, split, slab0, slabs;
         int2 planes;   // the rank side's, of the first range only (RANK: the item's own)
+        const int4 *adapters;   // of those planes
     };
     __device__ Item item(const KernelParams &p, int j) const {
         const int Q = gridDim.x / 2, q = blockIdx.x / 2;
@@ -149,11 +151,13 @@ struct Items {
         if (RANK) {
             const int4 all = p.planes[it.tm];
             it.planes = make_int2(all.x + 4 * tn, min(4, all.y - 4 * tn));
+            it.adapters = p.plane_adapter + (long long)it.tm * p.most_planes + 4 * tn;
             it.ncols = 64 * it.planes.y;
             if (it.planes.y <= 0) it.slabs = 0;   // nothing here: every role passes it over
         } else {
             const int4 all = p.planes && it.split == 0 ? p.planes[it.tm] : make_int4(0, 0, 1, 0);
             it.planes = make_int2(all.x, all.z ? all.y : -1);
+            it.adapters = p.plane_adapter + (long long)it.tm * p.most_planes;
         }
         return it;
     }
@@ -270,7 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                             const int deep = min(p.width, 32);
                             for (int u = 0; u < it.ncols / 2; u += deep) {
                                 const int c = int(rank) * (it.ncols / 2) + u, in_plane = c % 64;
-                                const int4 of = p.plane_adapter[it.planes.x + c / 64];
+                                const int4 of = it.adapters[c / 64];
                                 const int slot = p.width < 64 ? in_plane / p.width : 0;
                                 const int a = slot == 0 ? of.x : slot == 1 ? of.y : slot == 2 ? of.z : of.w;
                                 const int r = p.width < 64 ? in_plane % p.width : of.y + in_plane;
@@ -292,12 +296,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         }
                     } else if constexpr (!A_MN && !RANK) {
                         const int e = s - it.slabs, part = SEVERAL ? 0 : e / it.planes.y;
-                        const int plane = it.planes.x + (SEVERAL ? e : e % it.planes.y);
+                        const int in_tile = SEVERAL ? e : e % it.planes.y, plane = it.planes.x + in_tile;
 #pragma unroll
                         for (int q = 0; q < PA; ++q)
                             tma_load_3d_pair(st + uint32_t(q) * PART_BYTES, &mH, fb, 0, int(rank) * ROWS,
                                              (part + q) * p.capacity + plane);
-                        const int4 of = p.plane_adapter[plane];
+                        const int4 of = it.adapters[in_tile];
                         const int deep = min(p.width, BK);   // rank columns of an adapter in this plane
 #pragma unroll
                         for (int q = 0; q < PB; ++q)

@@ -42,7 +42,7 @@ struct Product {
     Operand a, b, h, v;
     const int4 *planes = nullptr;
     const int4 *plane_adapter = nullptr;
-    int capacity = 0, width = 64;
+    int most_planes = 0, capacity = 0, width = 64;
 };
 
 // The rank side's own product: S before its scale.  `x` the parts of X (M x K, K-major),
