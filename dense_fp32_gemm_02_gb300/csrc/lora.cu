@@ -283,7 +283,7 @@ int many_rows(const Call &c, int sms, cudaMemPool_t pool) {
     if (!product) Q.direct = true;               // no parts of W are needed,
     if (!product && !ranked) P.direct = true;    // nor of P
     if (M == 0 || K == 0) P.direct = true;       // (nothing of P is read)
-    const sgp::Split split = product ? sgp::plan_split(M, N, K, PRODUCTS, sms) : sgp::Split{0, 0};
+    const sgp::Split split = product ? sgp::plan_split(M, N, K, PRODUCTS, sms) : sgp::Split{0, 0, 0};
     Grouping gr(c, want_stack ? (long long)c.K + c.N : 0, sms);
     const int ranges = K > 0 ? sgp::rank_splits(M, K, sms) : 0;   // (no contraction: no sums)
     const int pitch = gr.width;   // of the rows of S and H, as parts
@@ -433,7 +433,7 @@ int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
     w.x_wide = aligned(c.X, 4 * sizeof(T)) && c.ldx % 4 == 0;
     w.v_wide = wide_stack(A, c.L);
     Packed<T> P(c.M, c.K, c.X, c.ldx), Q(c.K, c.N, c.W, c.ldw);   // (of the third kernel)
-    sgp::Split split{1, 0};
+    sgp::Split split{1, 256, 0};
     auto stream = w_wide ? stream_kernel<T, true>(c.M) : stream_kernel<T, false>(c.M);
     long long slots = sms;
     if (stream_rows) {

@@ -69,25 +69,45 @@ int sgp::set_up() {
 // In units of one part pair's slab (64 k of a 256 x 256 tile, 0.27 us on a pair): a
 // wave takes its slabs, about 8 units of pipeline fill and epilogue; partial sums
 // are written and read once at about 5 TB/s, by a second launch (12 units).  A last wave
-// of half-width tiles counts half after others, whole where it is the only one (it then
-// waits for its loads).  The least estimate of up to 64 ranges: 64 x 4096 x 4096 bfloat16
-// takes 4 (18 us; 1: 26, 2: 21, 8: 22), 512 rows 1 (27; 2: 29, 4: 34).
+// of half-width tiles counts half after others, as narrow tiles where it is the only one.
+//
+// Tiles of 128 to 224 columns fill the pairs better where there are few.  With several
+// products to a slab one takes 1.1 times its share of a slab's time, and not less than
+// 0.57 units for each part that it loads; bfloat16's one product is bound by its loads,
+// which do not get fewer, so narrow tiles gain nothing there (128 columns: 8192 x 4096 x
+// 4096 in 332 us for 208).
+//
+// The least estimate over the widths and up to 64 ranges: 64 x 4096 x 4096 bfloat16
+// takes 4 ranges (18 us; 1: 26, 2: 21, 8: 22), 512 rows 1 (27; 2: 29, 4: 34); the float32
+// weight gradient 4097 x 1023 x 3001 tiles of 160 columns (the call 82.5 us; 256: 93.3, 224:
+// 89.1, 192: 84.1, 128: 128.8), the input gradient 3001 x 1024 x 1023 of 192 (75.4; 256:
+// 81.8).  120 float32 products of random sizes take 0.966 of the time that 256 columns
+// take, the best width of each 0.954.
 Split sgp::plan_split(int M, int N, int K, int products, int sms) {
     const long long pairs = std::max(1, sms / 2);
-    const long long tiles = ((M + 255LL) / 256) * ((N + 255LL) / 256);
     const long long slabs = (K + BK - 1LL) / BK;
-    Split best{1, 0};
+    const int parts = products == 1 ? 2 : products == 3 ? 4 : 6;   // that a slab loads
+    auto slab_cost = [&](int width) {
+        return width == TILE || products == 1 ? double(products)
+                                              : std::max(1.1 * products * width / TILE, 0.57 * parts);
+    };
+    Split best{1, TILE, 0};
     double least = 0;
-    for (long long s = 1; s <= std::min(64LL, std::max(1LL, slabs)); ++s) {
-        const long long per = (slabs + s - 1) / s;
-        if ((slabs + per - 1) / per != s) continue;      // a range would be empty
-        const long long items = tiles * s, waves = items / pairs, rest = items % pairs;
-        const double last = rest == 0 ? 0.0 : (s == 1 && waves > 0 && 2 * rest <= pairs ? 0.5 : 1.0);
-        const double cost = (double(waves) + last) * (double(per) * products + 8.0) +
-                            (s > 1 ? 12.0 + double(s) * M * N * 8.0 / 5.0e6 / 0.27 : 0.0);
-        if (s == 1 || cost < least) {
-            least = cost;
-            best = Split{int(s), s > 1 ? size_t(s) * M * N : 0};
+    for (int width = TILE; width >= (products == 1 ? TILE : TILE / 2); width -= 32) {
+        const long long tiles = ((M + 255LL) / 256) * ((N + width - 1LL) / width);
+        for (long long s = 1; s <= std::min(64LL, std::max(1LL, slabs)); ++s) {
+            const long long per = (slabs + s - 1) / s;
+            if ((slabs + per - 1) / per != s) continue;      // a range would be empty
+            const long long items = tiles * s, waves = items / pairs, rest = items % pairs;
+            const bool halves = width == TILE && s == 1 && 2 * rest <= pairs;   // the last wave's
+            const double last = rest == 0 ? 0.0 : halves && waves > 0 ? 0.5 : 1.0;
+            const double slab = slab_cost(halves && waves == 0 ? TILE / 2 : width);
+            const double cost = (double(waves) + last) * (double(per) * slab + 8.0) +
+                                (s > 1 ? 12.0 + double(s) * M * N * 8.0 / 5.0e6 / 0.27 : 0.0);
+            if (least == 0 || cost < least) {
+                least = cost;
+                best = Split{int(s), width, s > 1 ? size_t(s) * M * N : 0};
+            }
         }
     }
     return best;
@@ -119,13 +139,14 @@ int sgp::run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Spl
     using K = Kernel<T, LAYOUT>;
     int st = set_up();
     if (st != SGEMM_OK) return st;
-    const long long tiles_m = (p.M + TILE - 1LL) / TILE, tiles_n = (p.N + TILE - 1LL) / TILE;
+    const long long tiles_m = (p.M + TILE - 1LL) / TILE, tiles_n = (p.N + split.tile_n - 1LL) / split.tile_n;
     if (tiles_m * tiles_n * split.splits > (1LL << 30)) return SGEMM_ERR_TOO_LARGE;
     KernelParams kp{};
     kp.M = p.M;
     kp.N = p.N;
     kp.tiles_m = int(tiles_m);
     kp.tiles_n = int(tiles_n);
+    kp.tile_n = split.tile_n;
     kp.group_m = 8;
     kp.slabs = int((p.K + BK - 1LL) / BK);
     kp.splits = split.splits;
@@ -155,7 +176,7 @@ int sgp::run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Spl
     cudaError_t e =
         sgh::launch_early(K::main, dim3(unsigned(2 * pairs)), THREADS, SMEM_BYTES, stream, mA, mB, mH, mV, kp, epi);
     if (e != cudaSuccess) return sgh::cuda_fail(e);
-    sgh::count_launch(K::F32 ? "bf16 parts of float32, tcgen05 cta_group::2, 256x256 pair tiles"
+    sgh::count_launch(K::F32 ? "bf16 parts of float32, tcgen05 cta_group::2, pair tiles of 256 rows"
                              : "bf16, tcgen05 cta_group::2, 256x256 pair tiles");
     e = cudaGetLastError();
     if (e != cudaSuccess) return sgh::cuda_fail(e);
@@ -192,6 +213,7 @@ int sgp::run_rank(const RankProduct &p, int splits, float *partial, int sms, cud
     kp.N = int(groups * TILE);
     kp.tiles_m = int(tiles_m);
     kp.tiles_n = int(groups);
+    kp.tile_n = TILE;
     kp.group_m = 8;
     kp.slabs = int((p.K + BK - 1LL) / BK);
     kp.splits = splits;

@@ -60,6 +60,7 @@ static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 struct KernelParams {
     int M, N;
     int tiles_m, tiles_n, group_m;
+    int tile_n;             // columns of a tile: 128 to 256, a multiple of 32
     int slabs;              // of 64 k
     int splits, per_split;  // slabs of each range but the last
     const int4 *planes;     // of the rank side, see Product (null: none)
@@ -104,7 +105,7 @@ __device__ __forceinline__ uint64_t part_desc(uint32_t saddr, int kk) {
 
 // The work of pair q of Q: items q, q + Q, ... of `items`: whole tiles, or, with
 // `splits` > 1, (tile, range) pairs; without splits a last wave of at most Q / 2
-// tiles is cut into half-width tiles.  RANK: (256 rows, four of their planes, range)
+// tiles of 256 columns is cut into half-width tiles.  RANK: (256 rows, four of their planes, range)
 // triples, the planes slowest, so that those that hold nothing come last.
 template <bool RANK>
 struct Items {
@@ -113,7 +114,7 @@ struct Items {
     __device__ void init(const KernelParams &p) {
         const int Q = gridDim.x / 2, q = blockIdx.x / 2;
         const int items = p.tiles_m * p.tiles_n * p.splits, tail = items % Q;
-        full = (!RANK && p.splits == 1 && tail != 0 && 2 * tail <= Q) ? items - tail : items;
+        full = (!RANK && p.tile_n == TILE && p.splits == 1 && tail != 0 && 2 * tail <= Q) ? items - tail : items;
         const int halves = 2 * (items - full);
         mine_full = q < full ? (full - 1 - q) / Q + 1 : 0;
         mine = mine_full + (q < halves ? (halves - 1 - q) / Q + 1 : 0);
@@ -138,8 +139,8 @@ struct Items {
                 it.tm = t % p.tiles_m, tn = t / p.tiles_m;
             else
                 tile_coords(t, p.tiles_m, p.tiles_n, p.group_m, it.tm, tn);
-            it.col0 = tn * TILE;
-            it.ncols = p.N - it.col0 <= TILE / 2 ? TILE / 2 : TILE;
+            it.col0 = tn * p.tile_n;
+            it.ncols = p.N - it.col0 <= TILE / 2 ? TILE / 2 : p.tile_n;
         } else {
             const int h = q + (j - mine_full) * Q;
             tile_coords(full + h / 2, p.tiles_m, p.tiles_n, p.group_m, it.tm, tn);
@@ -436,9 +437,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int j = 0; j < items.mine && ok; ++j) {
             const Item it = items.item(p, j);
             if (RANK && it.slabs == 0) continue;
-            const int width = it.ncols / 2;               // this warp's columns: 128, 96 (RANK), 64 or 32
+            const int first_half = (it.ncols / 2 + 31) & ~31;   // this warp's columns: 128, 96, 64 or 32
+            const int width = half ? it.ncols - first_half : first_half;
             const int row0 = it.tm * TILE + int(rank) * ROWS + quarter * 32;
-            const int col0 = it.col0 + half * width;
+            const int col0 = it.col0 + half * first_half;
             const bool fma_expand = it.planes.y < 0 && p.partial == nullptr;
 
             auto write = [&](int c, const float (&v)[32]) {   // columns col0 + 32 c ..
@@ -490,7 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         if (c * 32 >= width) break;
 #pragma unroll
                         for (int h = 0; h < 32; h += 16)
-                            tmem_add16(taddr + uint32_t(buf) * ACC_COLUMNS + lanes + uint32_t(half * width + c * 32 + h),
+                            tmem_add16(taddr + uint32_t(buf) * ACC_COLUMNS + lanes + uint32_t(half * first_half + c * 32 + h),
                                        &sum[c][h], s > 0);
                     }
                     hand_back(buf);
@@ -501,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     if (c * 32 >= width) break;
 #pragma unroll
                     for (int h = 0; h < 32; h += 16)
-                        tmem_add16(taddr + ACC_COLUMNS + lanes + uint32_t(half * width + c * 32 + h), &sum[c][h],
+                        tmem_add16(taddr + ACC_COLUMNS + lanes + uint32_t(half * first_half + c * 32 + h), &sum[c][h],
                                    true);
                 }
                 if (SEVERAL) hand_back(1);
@@ -531,7 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll 1
                 for (int c = 0; c * 32 < width; ++c) {
                     float v[32];
-                    tmem_load32(taddr + uint32_t(a) * ACC_COLUMNS + lanes + uint32_t(half * width + c * 32), v);
+                    tmem_load32(taddr + uint32_t(a) * ACC_COLUMNS + lanes + uint32_t(half * first_half + c * 32), v);
                     if ((c + 1) * 32 >= width) hand_back(a);
                     write(c, v);
                 }

@@ -65,7 +65,7 @@ enum Layout { FORWARD, INPUT_GRAD, WEIGHT_GRAD };   // (a, b): (K, N)-major, (K,
 // How the contraction is split over the SMs: `splits` ranges whose fp32 partial sums
 // (partial_floats of them) a second kernel adds in order, or one.
 struct Split {
-    int splits;
+    int splits, tile_n;   // tile_n: columns of a tile
     size_t partial_floats;
 };
 Split plan_split(int M, int N, int K, int products, int sms);

@@ -172,7 +172,9 @@ def test_in_place_and_other_streams():
 WGRAD = [  # (M, K, N, padding, offset)
     (1, 1, 1, 0, 0), (1, 64, 64, 0, 0), (2, 33, 5, 3, 1), (63, 128, 96, 0, 0), (64, 256, 256, 8, 8),
     (65, 257, 127, 1, 0), (500, 96, 520, 0, 0), (513, 320, 8, 0, 3), (1025, 136, 264, 0, 0),
-    (2300, 65, 300, 0, 0), (700, 1030, 700, 2, 2), (4111, 264, 40, 0, 0)]
+    (2300, 65, 300, 0, 0), (700, 1030, 700, 2, 2), (4111, 264, 40, 0, 0),
+    # the float32 product's tiles of 160, 192 and 224 columns
+    (72, 5000, 270, 1, 1), (72, 5000, 490, 0, 0), (72, 5000, 583, 1, 1)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)

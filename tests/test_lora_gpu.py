@@ -98,6 +98,21 @@ def test_forward(case, dtype):
     check_forward(p, *run_forward(p, pad, offset, H=L > 0), case)
 
 
+WIDTHS = [270, 390, 490, 583]   # of 5000 rows: the float32 products' tiles of 128, 160, 192 and 224 columns
+
+
+@pytest.mark.parametrize("ids", ["mixed", "outside"])
+@pytest.mark.parametrize("N", WIDTHS)
+def test_forward_at_each_tile_width(N, ids):
+    p = Problem(5000, 72, N, 3, 24, torch.float32, ids, ranks=False, seed=5)
+    check_forward(p, *run_forward(p, 1, 1), N)
+    p.A[1, 5, 3] = float("inf")     # the rank side of its rows' tiles in the epilogue
+    ref, _, mag, _ = lora_reference(p.X, p.W, torch.where(p.A.isinf(), 0.0, p.A), p.B, p.ids, p.scale, p.ranks, p.bias)
+    Y, _ = run_forward(p)
+    clean = p.ids != 1
+    assert_close(Y[clean.cuda()], ref[clean], mag[clean], p.K + p.R, f"Y {N}")
+
+
 @pytest.mark.parametrize("M", [3, 40, 600, 1400])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_forward_defaults(M, dtype):
@@ -160,6 +175,9 @@ BACKWARD = [  # (M, K, N, L, R, ids, padding, offset, kept in 8 bits)
     (600, 96, 64, 300, 4, "mixed", 0, 0, False), (1025, 2056, 264, 1, 100, "single", 0, 0, False)]
 
 
+WIDE = [(5000, K, 72, 3, 24, "mixed", 1, 1, True) for K in WIDTHS]   # tile widths, as above
+
+
 def run_backward(p, H, pad=0, offset=0, kept=None, stack=True, dx=True):
     b, d = binding(), p.on_gpu(pad, offset)
     dX = p.out(p.M, p.K, pad, offset) if dx else None
@@ -174,7 +192,7 @@ def run_backward(p, H, pad=0, offset=0, kept=None, stack=True, dx=True):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("case", BACKWARD)
+@pytest.mark.parametrize("case", BACKWARD + WIDE)
 def test_backward(case, dtype):
     M, K, N, L, R, ids, pad, offset, x8 = case
     p = Problem(M, K, N, L, R, dtype, ids, seed=8)
