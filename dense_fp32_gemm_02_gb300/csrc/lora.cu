@@ -462,38 +462,22 @@ int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
     const long long product = (long long)w.across * w.ranges, rank = (long long)c.M * w.rank_ranges;
     if (product + rank > 0x7fffffffLL) return SGEMM_ERR_TOO_LARGE;
     const bool together = stream_rows && product + rank <= slots;
-    if (third) {   // what the product reads has to be there before the kernel that it overtakes
+    if (third) {
         P.place(ws);
         Q.place(ws);
         st = prepare<Packed<T>::PARTS, Packed<T>::PARTS>(c.M, ad, Groups{}, P.job(), Q.job(), sms, c.stream);
         if (st != SGEMM_OK) return st;
     }
-    const bool alone = !ranked || together;   // the product's is the first kernel of the call
-    if (!alone) {
-        few_rows_rank_kernel<T><<<unsigned(rank), RANK_THREADS, 0, c.stream>>>(w, X, A, ad);
-        if ((st = launched()) != SGEMM_OK) return st;
-    }
     if (stream_rows) {
         const dim3 grid(unsigned(product + (together ? rank : 0)));
-        if (alone) {
-            stream<<<grid, RANK_THREADS, 0, c.stream>>>(w, X, W, c.ldw, A, ad);
-        } else {
-            const cudaError_t e = sgh::launch_early(stream, grid, RANK_THREADS, 0, c.stream, w, X, W, c.ldw, A, ad);
-            if (e != cudaSuccess) return sgh::cuda_fail(e);
-        }
+        stream<<<grid, RANK_THREADS, 0, c.stream>>>(w, X, W, c.ldw, A, ad);
         st = launched(kFewRows);
     } else if (mma_rows) {
         if constexpr (F32) {
             auto kernel = c.M <= 32 ? few_rows_kernel<2> : few_rows_kernel<4>;
             const size_t smem = c.M <= 32 ? FewRows<2>::SMEM : FewRows<4>::SMEM;
             if ((st = shared_limit(kernel, smem)) != SGEMM_OK) return st;
-            if (alone) {
-                kernel<<<unsigned(product), RANK_THREADS, smem, c.stream>>>(w, X, W, c.ldw, w_wide);
-            } else {
-                const cudaError_t e = sgh::launch_early(kernel, dim3(unsigned(product)), RANK_THREADS, smem, c.stream, w, X,
-                                                        W, c.ldw, w_wide);
-                if (e != cudaSuccess) return sgh::cuda_fail(e);
-            }
+            kernel<<<unsigned(product), RANK_THREADS, smem, c.stream>>>(w, X, W, c.ldw, w_wide);
             st = launched(kFewRows);
         }
     } else {
@@ -501,15 +485,22 @@ int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
         g.M = c.M, g.N = c.N, g.K = c.K;
         g.a = P.operand();
         g.b = Q.operand();
-        st = sgp::run<T, sgp::FORWARD>(g, sgp::Epilogue<T, false>{}, split, w.partial, sms, c.stream,
-                                       alone ? sgp::PARTIALS : sgp::PARTIALS_OVERTAKING);
+        st = sgp::run<T, sgp::FORWARD>(g, sgp::Epilogue<T, false>{}, split, w.partial, sms, c.stream, sgp::PARTIALS);
     }
     if (st != SGEMM_OK) return st;
+    if (ranked && !together) {   // it reads nothing of the product's and runs beside it
+        const cudaError_t e = sgh::launch_early(few_rows_rank_kernel<T>, dim3(unsigned(rank)), RANK_THREADS, 0, c.stream, w,
+                                                X, A, ad);
+        if (e != cudaSuccess) return sgh::cuda_fail(e);
+        if ((st = launched()) != SGEMM_OK) return st;
+    }
     const T *bias = static_cast<const T *>(c.bias);
     const bool wide = (!bias || aligned(bias, 16)) && wide_stack(B, c.L);
     const dim3 grid(unsigned((c.N + 255) / 256), unsigned(c.M));
-    const cudaError_t e = sgh::launch_early(wide ? few_rows_finish_kernel<T, true> : few_rows_finish_kernel<T, false>,
-                                            grid, 256, 0, c.stream, w, B, ad, bias, c.N % 4 == 0, c.H, (long long)c.ldh,
+    const bool early = (long long)grid.x * grid.y <= 2LL * sms;
+    const auto finish = wide ? (early ? few_rows_finish_kernel<T, true, true> : few_rows_finish_kernel<T, true, false>)
+                             : (early ? few_rows_finish_kernel<T, false, true> : few_rows_finish_kernel<T, false, false>);
+    const cudaError_t e = sgh::launch_early(finish, grid, 256, 0, c.stream, w, B, ad, bias, c.N % 4 == 0, c.H, (long long)c.ldh,
                                             static_cast<T *>(c.Y), (long long)c.ldy);
     if (e != cudaSuccess) return sgh::cuda_fail(e);
     if ((st = launched()) != SGEMM_OK) return st;
@@ -517,10 +508,10 @@ int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
 }
 
 // Few rows: the rank side row by row (M rank (K + N) elements of the stack from L2, and
-// partial sums of all of Y) against grouping it by adapter (five launches more, about 25
-// us).  us, row by row / grouped, bfloat16: 256 x 4096 x 4096 of rank 16 44 / 69, 512 rows
-// 78 / 70; 512 x 1024 x 1024 of rank 64 33 / 37, 1024 rows 49 / 35; 1118 x 64 x 192 of
-// rank 78 17 / 27; 4096 x 256 x 256 of rank 16 32 / 28.
+// partial sums of all of Y) against grouping it by adapter (four launches more, about 20
+// us).  us, row by row / grouped, bfloat16: 256 x 4096 x 4096 of rank 16 35 / 49, 512 rows
+// 73 / 48; 512 x 1024 x 1024 of rank 64 23 / 33, 1024 rows 47 / 34; 1280 x 768 x 768 of
+// rank 16 27 / 27; 1000 x 512 x 512 of rank 16 15 / 24.
 bool few_rows(const Call &c) {
     if (c.K == 0 || c.N == 0) return false;
     if (c.M <= STREAM_ROWS) return true;

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(256) parts_kernel(PartsJob<XP> p, PartsJob<XQ>
     const long long t = (long long)blockIdx.x * 256 + threadIdx.x, step = (long long)gridDim.x * 256;
     take_parts<P_PARTS>(p, t, step);
     take_parts<Q_PARTS>(q, t, step);
-    if (beside) sg::wait_prerequisites();
+    if (beside && blockIdx.x == 0) sg::wait_prerequisites();
 }
 
 // ------------------------------------------------------------------ rows by adapter

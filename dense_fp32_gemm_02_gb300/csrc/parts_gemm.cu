@@ -172,7 +172,6 @@ int sgp::run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Spl
     }
     const long long pairs = std::min<long long>(tiles_m * tiles_n * split.splits * (split.splits == 1 ? 2 : 1),
                                                 std::max(1, sms / 2));
-    kp.wait_last = mode == PARTIALS_OVERTAKING;
     cudaError_t e =
         sgh::launch_early(K::main, dim3(unsigned(2 * pairs)), THREADS, SMEM_BYTES, stream, mA, mB, mH, mV, kp, epi);
     if (e != cudaSuccess) return sgh::cuda_fail(e);

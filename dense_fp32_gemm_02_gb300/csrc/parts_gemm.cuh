@@ -69,7 +69,6 @@ struct KernelParams {
     int most_planes, capacity, width, L;
     float *partial;         // splits x M x N, or null
     unsigned long long timeout_ns;
-    bool wait_last;         // launched early: it reads nothing of the kernel before it
 };
 
 // 3-D tile copy into this CTA's shared memory, counted on a barrier of either CTA.
@@ -215,7 +214,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tc_fence_before();
     cluster_barrier();
     tc_fence_after();
-    if (!p.wait_last) wait_prerequisites();
+    wait_prerequisites();
     launch_dependents();
     const uint32_t taddr = *tmem_base;
     const uint32_t peer_abort = dsmem_map(smem_addr((const void *)abort_flag), rank ^ 1u);
@@ -564,7 +563,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     tc_fence_after();
     if (warp == 1) tmem_dealloc_pair(taddr, TMEM_COLUMNS);
-    if (p.wait_last) wait_prerequisites();   // its end is also that of the kernels before it
 }
 
 // The ranges' partial sums added in order, and the epilogue; a thread to an element.

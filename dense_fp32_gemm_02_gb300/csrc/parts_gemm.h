@@ -72,9 +72,8 @@ Split plan_split(int M, int N, int K, int products, int sms);
 
 // float: a of 3 parts (1 in WEIGHT_GRAD) and b of 3; bfloat16: one part each.
 // The kernel is launched early (host_state.h).  PARTIALS leaves the partial sums (of one
-// range too) to the caller; with PARTIALS_OVERTAKING it also runs beside the kernel before
-// it on the stream, of which it then may read nothing, and ends after it.
-enum Mode { WHOLE, PARTIALS, PARTIALS_OVERTAKING };
+// range too) to the caller.
+enum Mode { WHOLE, PARTIALS };
 template <class T, Layout LAYOUT>
 int run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Split split, float *partial,
         int sms, cudaStream_t stream, Mode mode = WHOLE);

@@ -13,8 +13,9 @@
 // 9.9) 1 row 14.3, 8 rows 21.3, 16 rows 32.3 (by FMAs 43).  At 1024 x 1024 8 rows of
 // bfloat16 take 5.7 by FMAs, 9 rows 8.4 by parts_gemm: hence 8 for both.
 // The rank side is taken row by row, each with its own adapter, by blocks of their own:
-// in the product's launch where all blocks fit the GPU at once, else in one just before,
-// which the product does not wait for.
+// in the product's launch where all blocks fit the GPU at once, else in one just after,
+// which runs beside it where it leaves room (64 x 4096 x 4096 bfloat16 with rank 16: 21.5 us;
+// before it 23.6, because the product's blocks then wait for shared memory).
 #pragma once
 
 #include "rank_products.cuh"
@@ -94,6 +95,7 @@ __global__ void __launch_bounds__(RANK_THREADS)
     __shared__ float sums[RANK_SUMS];
     sg::launch_dependents();
     rank_of_row(w, int(blockIdx.x), X, V, ad, sums);
+    if (blockIdx.x == 0) sg::wait_prerequisites();   // this kernel's end is also that of the product's
 }
 
 // ------------------------------------------------------------------ up to 8 rows
@@ -114,7 +116,6 @@ __global__ void __launch_bounds__(RANK_THREADS, stream_blocks(MR))
     sg::launch_dependents();
     if (int(blockIdx.x) >= w.across * w.ranges) {
         rank_of_row(w, int(blockIdx.x) - w.across * w.ranges, X, V, ad, sm);
-        sg::wait_prerequisites();
         return;
     }
     const int n0 = (int(blockIdx.x) % w.across) * COLS, q = int(blockIdx.x) / w.across;
@@ -179,7 +180,6 @@ __global__ void __launch_bounds__(RANK_THREADS, stream_blocks(MR))
             if (m < w.M && n0 + c < w.N) out[(long long)m * w.N + n0 + c] = s;
         }
     }
-    sg::wait_prerequisites();   // this kernel's end is also that of the rank side's
 }
 
 // ------------------------------------------------------------------ float32, up to 64 rows
@@ -305,15 +305,16 @@ __global__ void __launch_bounds__(RANK_THREADS)
                 const int i = m * 16 + (lane >> 2) + (d / 2) * 8, j = n0 + warp * 16 + t * 8 + (lane & 3) * 2 + (d & 1);
                 if (i < w.M && j < w.N) out[(long long)i * w.N + j] = sum[m][t][d];
             }
-    sg::wait_prerequisites();   // this kernel's end is also that of the rank side's
 }
 
 // ------------------------------------------------------------------ the rest
 // Y from the partial sums: a block to 256 columns of a row (8 to a lane), its 8 warps to
 // the ranges and the rank, whose terms they share out; the warps' sums are added in
 // order.  The first block of a row also writes H.  WIDE: rows of everything but the
-// partial sums can be read eight elements at a time; `p_wide` the same of those.
-template <class T, bool WIDE>
+// partial sums can be read eight elements at a time; `p_wide` the same of those.  EARLY, for
+// grids of up to two blocks to an SM: the first terms of the rank are read before the sums
+// are there (4 x 4096 x 4096 bfloat16 15.4 -> 14.4 us; 64 rows, of more blocks, 21.5 -> 23).
+template <class T, bool WIDE, bool EARLY>
 __global__ void __launch_bounds__(256)
     few_rows_finish_kernel(RowsWork w, Stack<const T> V, Adapters ad, const T *bias, bool p_wide, float *H, long long ldh,
                            T *Y, long long ldy) {
@@ -323,6 +324,22 @@ __global__ void __launch_bounds__(256)
     const int j = n0 + lane * 8;
     const int a = ad.of_row(i), rank = a < 0 ? 0 : ad.rank(a);
     const float scale = a < 0 ? 0.0f : ad.scale(a);
+    float x[8] = {}, v[8];
+    auto read = [&](auto *p, bool eight, float (&v)[8]) {   // columns j .. j + 7
+        if (eight && j + 8 <= w.N) {
+            load8(p + j, v);
+        } else {
+#pragma unroll
+            for (int d = 0; d < 8; ++d) v[d] = j + d < w.N ? to_f32(p[j + d]) : 0.0f;
+        }
+    };
+    // the call's inputs, before the sums are there
+    const T *m = rank > 0 ? V.matrix(a) : nullptr;
+    float first[2][8];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+        if (EARLY && warp + 8 * u < rank) read(m + (warp + 8 * u) * V.ld, WIDE, first[u]);
+    if (bias && warp == 7) read(bias, WIDE, x);
     sg::wait_prerequisites();
     if (int(threadIdx.x) < ad.R && ad.L > 0) {
         const int r = threadIdx.x;
@@ -335,37 +352,25 @@ __global__ void __launch_bounds__(256)
         if (H && blockIdx.x == 0) H[i * ldh + r] = sum;
         S[r] = r < rank ? sum * scale : 0.0f;
     }
-    float x[8] = {}, v[8];
-    auto read = [&](auto *p, bool eight) {   // columns j .. j + 7
-        if (eight && j + 8 <= w.N) {
-            load8(p + j, v);
-        } else {
-#pragma unroll
-            for (int d = 0; d < 8; ++d) v[d] = j + d < w.N ? to_f32(p[j + d]) : 0.0f;
-        }
-    };
     const float *p = w.partial + (long long)i * w.N;
     const long long plane = (long long)w.M * w.N;
 #pragma unroll 2
     for (int q = warp; q < w.ranges; q += 8) {
-        read(p + q * plane, p_wide);
-#pragma unroll
-        for (int d = 0; d < 8; ++d) x[d] += v[d];
-    }
-    if (bias && warp == 7) {
-        read(bias, WIDE);
+        read(p + q * plane, p_wide, v);
 #pragma unroll
         for (int d = 0; d < 8; ++d) x[d] += v[d];
     }
     __syncthreads();
-    if (rank > 0) {
-        const T *m = V.matrix(a);
-#pragma unroll 4
-        for (int r = warp; r < rank; r += 8) {
-            read(m + r * V.ld, WIDE);
 #pragma unroll
-            for (int d = 0; d < 8; ++d) x[d] = fmaf(S[r], v[d], x[d]);
-        }
+    for (int u = 0; u < 2; ++u)
+        if (EARLY && warp + 8 * u < rank)
+#pragma unroll
+            for (int d = 0; d < 8; ++d) x[d] = fmaf(S[warp + 8 * u], first[u][d], x[d]);
+#pragma unroll 4
+    for (int r = warp + (EARLY ? 16 : 0); r < rank; r += 8) {
+        read(m + r * V.ld, WIDE, v);
+#pragma unroll
+        for (int d = 0; d < 8; ++d) x[d] = fmaf(S[r], v[d], x[d]);
     }
     *reinterpret_cast<float4 *>(&sums[warp][lane * 8]) = make_float4(x[0], x[1], x[2], x[3]);
     *reinterpret_cast<float4 *>(&sums[warp][lane * 8 + 4]) = make_float4(x[4], x[5], x[6], x[7]);
