@@ -474,8 +474,8 @@ int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
         st = launched(kFewRows);
     } else if (mma_rows) {
         if constexpr (F32) {
-            auto kernel = c.M <= 32 ? few_rows_kernel<2> : few_rows_kernel<4>;
-            const size_t smem = c.M <= 32 ? FewRows<2>::SMEM : FewRows<4>::SMEM;
+            auto kernel = c.M <= 16 ? few_rows_kernel<1> : c.M <= 32 ? few_rows_kernel<2> : few_rows_kernel<4>;
+            const size_t smem = c.M <= 16 ? FewRows<1>::SMEM : c.M <= 32 ? FewRows<2>::SMEM : FewRows<4>::SMEM;
             if ((st = shared_limit(kernel, smem)) != SGEMM_OK) return st;
             kernel<<<unsigned(product), RANK_THREADS, smem, c.stream>>>(w, X, W, c.ldw, w_wide);
             st = launched(kFewRows);

@@ -10,7 +10,7 @@
 // At 4096 x 4096 without adapters, us: bfloat16 (W is 5.0 of them) 1 row 9.6, 4 rows 12.5,
 // 8 rows 20.5 and by parts_gemm 9 rows 15.4 (by FMAs 16 rows 34), 64 rows 17.6 (the
 // warp-level MMA took 32: its operands pass through shared memory five times); float32 (W
-// 9.9) 1 row 14.3, 8 rows 21.3, 16 rows 32.3 (by FMAs 43).  At 1024 x 1024 8 rows of
+// 9.9) 1 row 14.3, 8 rows 21.3, 16 rows 22.5 (by FMAs 43), 64 rows 50.  At 1024 x 1024 8 rows of
 // bfloat16 take 5.7 by FMAs, 9 rows 8.4 by parts_gemm: hence 8 for both.
 // The rank side is taken row by row, each with its own adapter, by blocks of their own:
 // in the product's launch where all blocks fit the GPU at once, else in one just after,
@@ -183,128 +183,212 @@ __global__ void __launch_bounds__(RANK_THREADS, stream_blocks(MR))
 }
 
 // ------------------------------------------------------------------ float32, up to 64 rows
+// The warp-level MMA on three bfloat16 parts of each side, six products (parts_gemm.cuh), each
+// 16 k from zero, small products first, and then into fp32 sums.  The warps take 32 columns
+// each, four apart in a tile, so that a lane reads its columns of four tiles at once, and a
+// piece of a slab's k.
+//
+// Bound by the latency of a slab's steps at 16 rows (4096 x 4096: 22.5 us, W's bytes 9.9; three
+// stages of W, or sixteen warps to a block, took 23 and 26) and by the MMAs at 64 (1024
+// products per clock and SM: 21 us of 50).  Two TF32 parts, three products at a quarter of
+// the rate, took 22 and 60.
 template <int MT>
 struct FewRows {
-    // two blocks to an SM (one of deeper rings took 56 us at 64 x 4096 x 4096): with 64
-    // rows, X has one buffer
-    static constexpr int PARTS = 3, STAGES = 2, X_BUFFERS = MT <= 2 ? 2 : 1;
+    static constexpr int STAGES = 2;   // and two blocks to an SM
     static constexpr int W_PITCH = ROWS_COLS + 4, W_ELEMS = SLAB * W_PITCH;
-    static constexpr int X_PITCH = SLAB + 8, X_PLANE = MT * 16 * X_PITCH;
-    static constexpr size_t SMEM = size_t(STAGES) * W_ELEMS * 4 + size_t(X_BUFFERS) * PARTS * X_PLANE * 2;
+    static constexpr int X_ROWS = MT * 16, X_PITCH = SLAB + 8, X_PLANE = X_ROWS * X_PITCH;
+    static constexpr size_t SMEM = size_t(STAGES) * W_ELEMS * 4 + size_t(X_ROWS) * SLAB * 4 + size_t(3) * X_PLANE * 2;
 };
 
+// Four pairs (x[i], y[i]) as packed parts.  Remainders of what is finite need no check.
+__device__ __forceinline__ void parts_of_pairs(const float (&x)[4], const float (&y)[4], uint32_t (&part)[3][4]) {
+    auto head = [](float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); };
+    const float2 one = make_float2(1.0f, 1.0f), minus = make_float2(-1.0f, -1.0f);
+    float2 rest[4], all = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        rest[i] = sg::ffma2(make_float2(head(x[i]), head(y[i])), minus, make_float2(x[i], y[i]));
+        all = sg::ffma2(rest[i], one, all);
+    }
+    if (all.x + all.y != all.x + all.y) {   // an infinity or a NaN among them
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t p[3];
+            pair_parts(x[i], y[i], p);
+            part[0][i] = p[0], part[1][i] = p[1], part[2][i] = p[2];
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 s = sg::ffma2(make_float2(head(rest[i].x), head(rest[i].y)), minus, rest[i]);
+        part[0][i] = pack_exact(x[i], y[i]);
+        part[1][i] = pack_exact(rest[i].x, rest[i].y);
+        part[2][i] = pack_exact(s.x, s.y);
+    }
+}
+
+// d = a * b
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 template <int MT>
-__global__ void __launch_bounds__(RANK_THREADS)
+__global__ void __launch_bounds__(RANK_THREADS, 2)
     few_rows_kernel(RowsWork w, Rows<float> X, const float *W, long long ldw, bool w_wide) {
-    using T = float;
     using Z = FewRows<MT>;
-    constexpr int PARTS = Z::PARTS, STAGES = Z::STAGES;
+    constexpr int STAGES = Z::STAGES, WARPS = RANK_THREADS / 32, PIECES = WARPS / 4;   // of a slab's k
     extern __shared__ __align__(16) unsigned char smem_rows[];
     sg::launch_dependents();
-    T *ring = reinterpret_cast<T *>(smem_rows);
-    bf16 *xs = reinterpret_cast<bf16 *>(ring + STAGES * Z::W_ELEMS);   // [X_BUFFERS][PARTS][16 MT rows]
+    float *ring = reinterpret_cast<float *>(smem_rows);
+    float *raw = ring + STAGES * Z::W_ELEMS;                      // X's next slab
+    bf16 *xs = reinterpret_cast<bf16 *>(raw + Z::X_ROWS * SLAB);   // this one's parts
     const int n0 = (int(blockIdx.x) % w.across) * ROWS_COLS, q = int(blockIdx.x) / w.across;
     const int k_begin = q * w.range, k_end = min(w.K, k_begin + w.range);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp & 3, piece = warp >> 2;
 
+    // every WARPS'th row of the slab to a warp, 16 bytes to a lane or single elements
     auto fill = [&](int stage, int k0) {
-        T *ws = ring + stage * Z::W_ELEMS;
-        constexpr int PER = 16 / int(sizeof(T)), ALONG = ROWS_COLS / PER;
+        float *to = ring + stage * Z::W_ELEMS + warp * Z::W_PITCH;
+        const float *from = W + (k0 + warp) * ldw + n0;
+        if (w_wide && n0 + ROWS_COLS <= w.N) {
 #pragma unroll
-        for (int o = threadIdx.x; o < SLAB * ALONG; o += RANK_THREADS) {
-            const int k = o / ALONG, c = (o % ALONG) * PER;
-            const bool in = k0 + k < k_end && n0 + c < w.N;
-            fill16(ws + k * Z::W_PITCH + c, in ? W + (k0 + k) * ldw + n0 + c : W, in ? w.N - n0 - c : 0, w_wide);
-        }
-    };
-    // a slab of X, 16 MT x 64, as parts: MT * 4 elements to a thread, four at a time
-    float xv[MT][4];
-    auto load_x = [&](int k0) {
-#pragma unroll
-        for (int h = 0; h < MT; ++h) {
-            const int o = threadIdx.x + h * RANK_THREADS, m = o / 16, k = k0 + (o % 16) * 4;
-            if (m < w.M && w.x_wide && k + 4 <= k_end) {
-                load4(X.p + m * X.ld + k, xv[h]);
-            } else {
-#pragma unroll
-                for (int d = 0; d < 4; ++d) xv[h][d] = m < w.M && k + d < k_end ? X.at(m, k + d) : 0.0f;
+            for (int i = 0; i < SLAB / WARPS; ++i, from += WARPS * ldw) {
+                const bool in = k0 + warp + WARPS * i < k_end;
+                sg::cp_async16(shared_address(to + i * WARPS * Z::W_PITCH + lane * 4), in ? from + lane * 4 : W, in ? 16u : 0u);
             }
+            return;
         }
-    };
-    auto stage_x = [&](bf16 *to) {
 #pragma unroll
-        for (int h = 0; h < MT; ++h) {
-            const int o = threadIdx.x + h * RANK_THREADS, m = o / 16, k = (o % 16) * 4;
-            uint32_t lo[3], hi[3];
-            pair_parts(xv[h][0], xv[h][1], lo);
-            pair_parts(xv[h][2], xv[h][3], hi);
-#pragma unroll
-            for (int p = 0; p < PARTS; ++p)
-                *reinterpret_cast<uint2 *>(to + p * Z::X_PLANE + m * Z::X_PITCH + k) = make_uint2(lo[p], hi[p]);
-        }
-    };
-
-    float sum[MT][2][4] = {};
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) {
-        if (k_begin + s * SLAB < k_end) fill(s, k_begin + s * SLAB);
-        sg::cp_async_commit();
-    }
-    load_x(k_begin);
-    int stage = 0;
-    for (int k0 = k_begin; k0 < k_end; k0 += SLAB) {
-        bf16 *x = xs + (Z::X_BUFFERS == 2 ? stage & 1 : 0) * PARTS * Z::X_PLANE;
-        if (Z::X_BUFFERS == 1 && k0 > k_begin) __syncthreads();   // the last slab's has been read
-        stage_x(x);
-        sg::cp_async_wait<STAGES - 2>();
-        __syncthreads();   // this slab has landed, and the stage filled next has been read
-        if (k0 + (STAGES - 1) * SLAB < k_end) fill((stage + STAGES - 1) % STAGES, k0 + (STAGES - 1) * SLAB);
-        sg::cp_async_commit();
-        if (k0 + SLAB < k_end) load_x(k0 + SLAB);
-        const T *ws = ring + stage * Z::W_ELEMS;
-        float big[MT][2][4] = {}, small[MT][2][4] = {};
-#pragma unroll
-        for (int kk = 0; kk < SLAB; kk += 16) {
-            uint32_t fb[PARTS][4];   // two 8-column tiles of 16 k
+        for (int i = 0; i < SLAB / WARPS; ++i, from += WARPS * ldw, to += WARPS * Z::W_PITCH)
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
-                const float *p = ws + (kk + (lane & 3) * 2 + (d & 1) * 8) * Z::W_PITCH + warp * 16 + (lane >> 2) + (d >> 1) * 8;
-                uint32_t part[3];
-                pair_parts(p[0], p[Z::W_PITCH], part);
-                fb[0][d] = part[0], fb[1][d] = part[1], fb[2][d] = part[2];
+                const int c = lane + 32 * d;
+                const bool in = k0 + warp + WARPS * i < k_end && n0 + c < w.N;
+                sg::cp_async4(shared_address(to + c), in ? from + c : W, in ? 4u : 0u);
+            }
+    };
+    constexpr int QUADS = Z::X_ROWS * SLAB / 4;   // of a slab of X
+    auto fill_x = [&](int k0) {
+        if (w.x_wide && k0 + SLAB <= k_end) {
+#pragma unroll
+            for (int o = threadIdx.x; o < QUADS; o += RANK_THREADS) {
+                const int m = o / 16;
+                sg::cp_async16(shared_address(raw + o * 4), m < w.M ? X.p + m * X.ld + k0 + (o % 16) * 4 : X.p,
+                               m < w.M ? 16u : 0u);
+            }
+            return;
+        }
+#pragma unroll
+        for (int o = threadIdx.x; o < QUADS * 4; o += RANK_THREADS) {
+            const int m = o / SLAB, k = k0 + o % SLAB;
+            const bool in = m < w.M && k < k_end;
+            sg::cp_async4(shared_address(raw + o), in ? X.p + m * X.ld + k : X.p, in ? 4u : 0u);
+        }
+    };
+
+    float sum[MT][4][4] = {};   // [16 rows][tile: column 4 c + tile of the warp's 32][fragment]
+    fill(0, k_begin);
+    fill_x(k_begin);
+    sg::cp_async_commit();
+    int stage = 0;
+    for (int k0 = k_begin; k0 < k_end; k0 += SLAB) {
+        sg::cp_async_wait<0>();
+        __syncthreads();   // this slab has landed, and the last one has been read
+        if (k0 + SLAB < k_end) fill(stage ^ 1, k0 + SLAB);
+        for (int o = threadIdx.x; o < QUADS / 2; o += RANK_THREADS) {   // eight elements of a row of X
+            float v[4], t[4];
+            load4(raw + o * 8, v);
+            load4(raw + o * 8 + 4, t);
+            uint32_t part[3][4];
+            const float x[4] = {v[0], v[2], t[0], t[2]}, y[4] = {v[1], v[3], t[1], t[3]};
+            parts_of_pairs(x, y, part);
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+                *reinterpret_cast<uint4 *>(xs + p * Z::X_PLANE + (o / 8) * Z::X_PITCH + (o % 8) * 8) =
+                    make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
+        }
+        __syncthreads();   // X's parts are there, and its slab has been read
+        if (k0 + SLAB < k_end) fill_x(k0 + SLAB);
+        sg::cp_async_commit();
+        const float *ws = ring + stage * Z::W_ELEMS + (lane & 3) * 2 * Z::W_PITCH + group * 32 + (lane >> 2) * 4;
+        const bf16 *xa = xs + (lane & 15) * Z::X_PITCH + (lane >> 4) * 8;
+#pragma unroll
+        for (int kh = 0; kh < SLAB / PIECES; kh += 16) {
+            const int kk = piece * (SLAB / PIECES) + kh;
+            uint32_t fb[2][3][4];   // [k, k + 8][part][tile]
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                float x[4], y[4];
+                load4(ws + (kk + 8 * d) * Z::W_PITCH, x);
+                load4(ws + (kk + 8 * d + 1) * Z::W_PITCH, y);
+                parts_of_pairs(x, y, fb[d]);
             }
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MT; ++m) {
+                float d[4][4];
 #pragma unroll
-                for (int pa = PARTS - 1; pa >= 0; --pa) {
+                for (int pa = 2; pa >= 0; --pa) {
                     uint32_t fa[4];
-                    ldmatrix4<false>(fa, x + pa * Z::X_PLANE + (m * 16 + (lane & 15)) * Z::X_PITCH + kk + (lane >> 4) * 8);
+                    ldmatrix4<false>(fa, xa + pa * Z::X_PLANE + m * 16 * Z::X_PITCH + kk);
 #pragma unroll
-                    for (int pb = 0; pb < PARTS - pa; ++pb)
+                    for (int pb = 2 - pa; pb >= 0; --pb)
 #pragma unroll
-                        for (int t = 0; t < 2; ++t)
-                            mma16816(pa + pb > 0 ? small[m][t] : big[m][t], fa, fb[pb][2 * t], fb[pb][2 * t + 1]);
+                        for (int t = 0; t < 4; ++t)
+                            if (pa == 2)
+                                mma16816_first(d[t], fa, fb[0][pb][t], fb[1][pb][t]);
+                            else
+                                mma16816(d[t], fa, fb[0][pb][t], fb[1][pb][t]);
                 }
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum[m][t][e] += d[t][e];
+            }
         }
+        stage ^= 1;
+    }
+    // the pieces of the slabs' k in order, then out
+    auto place = [&](int p, int m, int t, int e) {
+        return ring + (((p - 1) * MT * 16 + (m * 4 + t) * 4 + e) * 128 + group * 32 + lane);
+    };
+    __syncthreads();
+    if (piece > 0) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int d = 0; d < 4; ++d)
-                    sum[m][t][d] += big[m][t][d] + small[m][t][d];
-        stage = (stage + 1) % STAGES;
+                for (int e = 0; e < 4; ++e) *place(piece, m, t, e) = sum[m][t][e];
     }
+    __syncthreads();
+    if (piece > 0) return;
     float *out = w.partial + (long long)q * w.M * w.N;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int e = 0; e < 4; ++e) {
+            const int i = m * 16 + (lane >> 2) + (e / 2) * 8, j = n0 + group * 32 + 4 * ((lane & 3) * 2 + (e & 1));
+            float v[4];
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                const int i = m * 16 + (lane >> 2) + (d / 2) * 8, j = n0 + warp * 16 + t * 8 + (lane & 3) * 2 + (d & 1);
-                if (i < w.M && j < w.N) out[(long long)i * w.N + j] = sum[m][t][d];
+            for (int t = 0; t < 4; ++t) {
+                v[t] = sum[m][t][e];
+#pragma unroll
+                for (int p = 1; p < PIECES; ++p) v[t] += *place(p, m, t, e);
             }
+            if (i >= w.M) continue;
+            if (w.N % 4 == 0 && j < w.N) {
+                *reinterpret_cast<float4 *>(out + (long long)i * w.N + j) = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    if (j + t < w.N) out[(long long)i * w.N + j + t] = v[t];
+            }
+        }
 }
 
 // ------------------------------------------------------------------ the rest
