@@ -354,7 +354,12 @@ def _vector(name, t, dtype, n, device):
     """Address of a contiguous vector of n elements, or None."""
     if t is None:
         return None
-    _typed(name, t, dtype, device)
+    try:
+        typed = t.dtype is dtype and t.get_device() == device
+    except AttributeError:
+        typed = False
+    if not typed:
+        _typed(name, t, dtype, device)
     if t.shape != (n,):
         raise ValueError(f"{name} must be {(n,)}, got {tuple(t.shape)}")
     if n > 1 and t.stride(0) != 1:
@@ -365,7 +370,8 @@ def _vector(name, t, dtype, n, device):
 def _pitch(rows, cols, row_stride, col_stride):
     if cols > 1 and col_stride != 1 and rows > 0:
         raise ValueError("rows must be contiguous (stride(-1) == 1)")
-    return max(row_stride if rows > 1 else 0, cols, 1)
+    pitch = row_stride if rows > 1 and row_stride > cols else cols
+    return pitch if pitch > 0 else 1
 
 
 def _matrix(name, t, rows, cols):
@@ -374,7 +380,10 @@ def _matrix(name, t, rows, cols):
         return None, 0
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must be {(rows, cols)}, got {tuple(t.shape)}")
-    return t.data_ptr(), _pitch(rows, cols, *t.stride())
+    row_stride, col_stride = t.stride()
+    if col_stride == 1 and row_stride >= cols > 0 and rows > 1:   # (what _pitch would say)
+        return t.data_ptr(), row_stride
+    return t.data_ptr(), _pitch(rows, cols, row_stride, col_stride)
 
 
 def _stack(name, t, count, rows, cols):
@@ -386,6 +395,8 @@ def _stack(name, t, count, rows, cols):
     if count == 0:
         return None, max(cols, 1), 0
     stride, row_stride, col_stride = t.stride()
+    if col_stride == 1 and row_stride >= cols > 0 and rows > 1:
+        return t.data_ptr(), row_stride, stride if count > 1 else 0
     return t.data_ptr(), _pitch(rows, cols, row_stride, col_stride), stride if count > 1 else 0
 
 
@@ -417,7 +428,8 @@ def _call(device, stream, fn, *args):
     current stream of that device."""
     handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
     if torch._C._cuda_getDevice() == device:
-        return check(fn(*args, handle))
+        status = fn(*args, handle)
+        return check(status) if status else status
     with torch.cuda.device(device):
         return check(fn(*args, handle))
 
