@@ -81,7 +81,7 @@ __device__ __forceinline__ float2 slope(float2 z) {
 
 // ------------------------------------------------------------------ kernels
 // What a kernel works on: `units` of 32 columns (wide forms) or 256, `per_row` to a row.
-// (Finding rows by a division took 13 of the 126 us of GELU at 8192 x 16384 bfloat16.)
+// (Rows by a division: GELU at 8192 x 16384 bfloat16 117 us, by multiplication 113.)
 struct Blocks {
     unsigned units;
     Divisor per_row;

@@ -14,7 +14,7 @@
 // bfloat16 take 5.7 by FMAs, 9 rows 8.4 by parts_gemm: hence 8 for both.
 // The rank side is taken row by row, each with its own adapter, by blocks of their own:
 // in the product's launch where all blocks fit the GPU at once, else in one just after,
-// which runs beside it where it leaves room (64 x 4096 x 4096 bfloat16 with rank 16: 21.5 us;
+// which runs beside it where it leaves room (64 x 4096 x 4096 bfloat16 with rank 16: 22 us;
 // before it 23.6, because the product's blocks then wait for shared memory).
 #pragma once
 

@@ -191,6 +191,22 @@ def run_backward(p, H, pad=0, offset=0, kept=None, stack=True, dx=True):
     return dX, dA, dB
 
 
+@pytest.mark.parametrize("M", [5, 13, 30, 60, 200])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_infinities_and_nans_of_x_and_w_stay_in_their_row_and_column(M, dtype):
+    p = Problem(M, 200, 264, 2, 8, dtype, "mixed", ranks=False)
+    p.X[1, 7], p.X[3, 150], p.W[100, 9], p.W[101, 70] = float("inf"), float("nan"), float("-inf"), float("nan")
+    Y, _ = run_forward(p, H=False)
+    rows, cols = torch.ones(M, dtype=torch.bool), torch.ones(264, dtype=torch.bool)
+    rows[[1, 3]], cols[[9, 70]] = False, False
+    X, W = p.X.nan_to_num(0, 0, 0), p.W.nan_to_num(0, 0, 0)
+    A, B = p.clean()
+    ref, _, mag, _ = lora_reference(X, W, A, B, p.ids, p.scale, p.ranks, p.bias)
+    Y = Y.cpu()
+    assert not torch.isfinite(Y[~rows]).any() and not torch.isfinite(Y[:, ~cols]).any()
+    assert_close(Y[rows][:, cols], ref[rows][:, cols], mag[rows][:, cols], p.K + p.R, f"Y {M}")
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("case", BACKWARD + WIDE)
 def test_backward(case, dtype):
