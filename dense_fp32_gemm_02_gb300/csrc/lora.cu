@@ -417,11 +417,23 @@ void split_rows(RowsWork &w, int cols, int step, int longest, long long slots, s
     w.ranges = int((w.K + (long long)w.range - 1) / w.range);
 }
 
+// Whether W goes through registers and FMAs.  Of up to 8 rows all do in float32 (8 x 8192 x
+// 8192 69 us, the warp-level MMA 77), and bfloat16 until the FMAs of several rows take longer
+// than W's bytes: us, by FMAs / by parts_gemm (where W needs no copy), 2 rows 8192 x 8192 30 / 36;
+// 4 rows 4096 x 4096 14.3 / 14.8, 4096 x 8192 24.6 / 23.5, 8192 x 8192 44 / 37; 8 rows 2048 x
+// 2048 10.7 / 11.4, 3000 x 3000 15.3 / 14.4, 4096 x 4096 19.2 / 15.9, 8192 x 8192 76 / 31.
+bool streamed(int M, int K, int N, bool always) {
+    if (M > STREAM_ROWS) return false;
+    return always || M <= 2 || (long long)K * N < (M <= 4 ? 32000000 : 9000000);
+}
+
 // A forward call of few rows: see rows.cuh.
 template <class T>
 int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
     constexpr bool F32 = sizeof(T) == 4;
-    const bool stream_rows = c.M <= STREAM_ROWS, mma_rows = F32 && !stream_rows && c.M <= MMA_ROWS, ranked = c.L > 0;
+    Packed<T> P(c.M, c.K, c.X, c.ldx), Q(c.K, c.N, c.W, c.ldw);   // (of the third kernel)
+    const bool stream_rows = streamed(c.M, c.K, c.N, F32 || !Q.direct);
+    const bool mma_rows = F32 && !stream_rows && c.M <= MMA_ROWS, ranked = c.L > 0;
     const T *W = static_cast<const T *>(c.W);
     const bool w_wide = wide_rows(W, c.ldw);
     const Adapters ad = c.adapters();
@@ -432,7 +444,6 @@ int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
     w.M = c.M, w.N = c.N, w.K = c.K;
     w.x_wide = aligned(c.X, 4 * sizeof(T)) && c.ldx % 4 == 0;
     w.v_wide = wide_stack(A, c.L);
-    Packed<T> P(c.M, c.K, c.X, c.ldx), Q(c.K, c.N, c.W, c.ldw);   // (of the third kernel)
     sgp::Split split{1, 256, 0};
     auto stream = w_wide ? stream_kernel<T, true>(c.M) : stream_kernel<T, false>(c.M);
     long long slots = sms;

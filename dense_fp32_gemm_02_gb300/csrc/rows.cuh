@@ -3,12 +3,13 @@
 // Bound by reading W once (and of the stack what the rows use).  The contraction is
 // split over the grid, each range's sums go to memory, and a last kernel adds the ranges
 // in order and applies the rest.  The product itself, by the count of rows:
-//   up to 8             stream_rows_kernel: W to registers 16 bytes at a time, fp32 FMAs;
+//   up to 8             stream_rows_kernel: W to registers 16 bytes at a time, fp32 FMAs
+//                       (bfloat16 of 3 and more rows: unless W is large);
 //   float32 up to 64    few_rows_kernel: W through shared memory, the warp-level MMA on
 //                       three bfloat16 parts, split in registers;
 //   else                parts_gemm.cuh.
 // At 4096 x 4096 without adapters, us: bfloat16 (W is 5.0 of them) 1 row 9.6, 4 rows 12.5,
-// 8 rows 20.5 and by parts_gemm 9 rows 15.4 (by FMAs 16 rows 34), 64 rows 17.6 (the
+// and by parts_gemm 8 rows 15 (by FMAs 20.5, 16 rows 34), 64 rows 17.6 (the
 // warp-level MMA took 32: its operands pass through shared memory five times); float32 (W
 // 9.9) 1 row 14.3, 8 rows 21.3, 16 rows 22.5 (by FMAs 43), 64 rows 50.  At 1024 x 1024 8 rows of
 // bfloat16 take 5.7 by FMAs, 9 rows 8.4 by parts_gemm: hence 8 for both.

@@ -87,7 +87,9 @@ FORWARD = [  # (M, K, N, L, R, ids, padding, offset)
     (700, 264, 300, 6, 40, "mixed", 0, 0), (1100, 520, 776, 3, 16, "runs", 0, 0),
     (1025, 2056, 264, 2, 65, "runs", 0, 0), (64, 64, 4100, 4, 8, "mixed", 0, 0),
     (64, 4100, 520, 0, 1, "none", 0, 0), (40, 4100, 1032, 3, 8, "mixed", 4, 4), (200, 3000, 264, 2, 20, "runs", 0, 0),
-    (16, 5000, 264, 5, 24, "mixed", 0, 0), (3, 9000, 72, 3, 128, "mixed", 0, 0), (300, 64, 64, 0, 1, "none", 0, 0), (7, 96, 40, 0, 1, "none", 0, 0), (600, 32, 8, 500, 4, "mixed", 0, 0)]
+    (16, 5000, 264, 5, 24, "mixed", 0, 0), (3, 9000, 72, 3, 128, "mixed", 0, 0), (300, 64, 64, 0, 1, "none", 0, 0), (7, 96, 40, 0, 1, "none", 0, 0), (600, 32, 8, 500, 4, "mixed", 0, 0),
+    (8, 3000, 3016, 3, 8, "mixed", 0, 0), (5, 4100, 2300, 2, 16, "outside", 4, 4), (4, 4096, 7816, 2, 4, "runs", 0, 0),
+    (3, 3000, 3017, 2, 8, "mixed", 1, 1)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
