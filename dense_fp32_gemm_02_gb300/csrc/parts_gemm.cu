@@ -30,16 +30,20 @@ template <class T, Layout LAYOUT>
 struct Kernel {
     static constexpr bool F32 = sizeof(T) == 4, A_MN = LAYOUT == WEIGHT_GRAD, B_MN = LAYOUT != INPUT_GRAD;
     static constexpr int PA = F32 && LAYOUT != WEIGHT_GRAD ? 3 : 1, PB = F32 ? 3 : 1;
-    static constexpr auto *main = &parts_gemm_kernel<T, PA, PB, A_MN, B_MN, LAYOUT == INPUT_GRAD, false>;
+    static constexpr auto *main = &parts_gemm_kernel<T, PA, PB, A_MN, B_MN, LAYOUT == INPUT_GRAD, false, false>;
+    // (of several parts the one kernel is for any length)
+    static constexpr auto *main_long = &parts_gemm_kernel<T, PA, PB, A_MN, B_MN, LAYOUT == INPUT_GRAD, false, PA * PB == 1>;
     static cudaError_t set_attr() {
-        return cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM_BYTES));
+        const cudaError_t e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM_BYTES));
+        if (e != cudaSuccess) return e;
+        return cudaFuncSetAttribute(main_long, cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM_BYTES));
     }
 };
 
 template <class T>
 struct RankKernel {
     static constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
-    static constexpr auto *main = &parts_gemm_kernel<T, PARTS, PARTS, false, false, false, true>;
+    static constexpr auto *main = &parts_gemm_kernel<T, PARTS, PARTS, false, false, false, true, false>;
     static cudaError_t set_attr() {
         return cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM_BYTES));
     }
@@ -172,8 +176,8 @@ int sgp::run(const Product &p, const Epilogue<T, LAYOUT == INPUT_GRAD> &epi, Spl
     }
     const long long pairs = std::min<long long>(tiles_m * tiles_n * split.splits * (split.splits == 1 ? 2 : 1),
                                                 std::max(1, sms / 2));
-    cudaError_t e =
-        sgh::launch_early(K::main, dim3(unsigned(2 * pairs)), THREADS, SMEM_BYTES, stream, mA, mB, mH, mV, kp, epi);
+    cudaError_t e = sgh::launch_early(kp.per_split > LONG_CHUNK ? K::main_long : K::main, dim3(unsigned(2 * pairs)), THREADS,
+                                      SMEM_BYTES, stream, mA, mB, mH, mV, kp, epi);
     if (e != cudaSuccess) return sgh::cuda_fail(e);
     sgh::count_launch(K::F32 ? "bf16 parts of float32, tcgen05 cta_group::2, pair tiles of 256 rows"
                              : "bf16, tcgen05 cta_group::2, 256x256 pair tiles");

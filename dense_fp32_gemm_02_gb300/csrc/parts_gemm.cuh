@@ -10,18 +10,18 @@
 //
 // The MMA's additions to its fp32 accumulator truncate: sums of n steps come out
 // smaller by up to n * 2^-23 (measured: 4.4e-6 of the result at K = 4096 for one
-// MMA per 16 k, 2.9e-5 for three per 8).  Under a bfloat16 rounding this does not
-// show.  For float32 the five small pairs have an accumulator of their own, which
-// leaves one addition per 16 k in the main one, and every CHUNK slabs the main one
-// is added to fp32 registers, round to nearest, and starts over.
+// MMA per 16 k, 2.9e-5 for three per 8).  For float32 the five small pairs have an
+// accumulator of their own, which leaves one addition per 16 k in the main one, and every
+// CHUNK slabs the main one is added to fp32 registers, round to nearest, and starts over.
+// For bfloat16 this happens every LONG_CHUNK slabs.
 //
 // A 256 x 256 tile to a pair of SMs, 64 k to a slab, persistent; 320 threads:
 //   warp 0     copies: each CTA its 128 rows of A and its half of B's columns, by
 //              TMA with 128-byte swizzle in either major order, into a ring;
 //   warp 1     allocates TMEM; in CTA 0 one thread issues the MMAs;
 //   warps 2-9  take the accumulators to registers and write the output.
-// One part: two accumulators of 256 columns, the next tile's MMAs run under this
-// tile's epilogue.  Several: main and small, the next chunk's small pairs run while
+// One part: two accumulators of 256 columns, the next tile's (or long chunk's) MMAs run under
+// this one's epilogue.  Several: main and small, the next chunk's small pairs run while
 // the main accumulator is read.
 // The rank-side term is more slabs of the same loop: a row's sums stand in the columns
 // of its own adapter and zeros in those of the tile's others.  Zero times an adapter's
@@ -166,17 +166,24 @@ struct Items {
 // Slabs between two visits to the main accumulator of a product of several parts:
 // 512 k, 32 truncating additions, 4e-6 at most and a third of that on average.
 constexpr int CHUNK = 8;
+// The same of one part: 8192 k, 512 additions, 3e-5 of the terms' magnitudes at most (5e-6
+// measured), under a hundredth of a bfloat16 spacing.  A kernel of its own (LONG), as the chunks'
+// sums in registers cost the shorter products 2 to 3 %: weight gradient of 4096 x 4096 from 16384
+// rows 368 us, in one accumulator, whose error grows with the rows (1.1e-4 at 200000), 358; from
+// 65536 rows 1440 and 1404.  (16384 rows in chunks of 4096 377, of 2048 382, of 1024 394.)
+constexpr int LONG_CHUNK = 128;
 
 // RANK: the rank side's own product, X (256 rows) * [columns of the adapters that the rows
 // use, as their planes lie], of which a row keeps its own adapter's columns: sums to
-// partial[range][row][width].
-template <class T, int PA, int PB, bool A_MN, bool B_MN, bool TRANS, bool RANK>
+// partial[range][row][width].  LONG: one part, ranges of more than LONG_CHUNK slabs.
+template <class T, int PA, int PB, bool A_MN, bool B_MN, bool TRANS, bool RANK, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     parts_gemm_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
                       const __grid_constant__ CUtensorMap mH, const __grid_constant__ CUtensorMap mV,
                       const KernelParams p, const Epilogue<T, TRANS> epi) {
     constexpr bool SEVERAL = PA * PB > 1;
-    constexpr bool CHUNKED = SEVERAL || RANK;   // the main accumulator goes to registers by chunks
+    constexpr bool CHUNKED = SEVERAL || RANK || LONG;   // the main accumulator goes to registers by chunks
+    constexpr int PER_CHUNK = LONG ? LONG_CHUNK : CHUNK;
     constexpr uint32_t STAGE = (PA + PB) * PART_BYTES;
     constexpr int STAGES = int(SMEM_RING / STAGE);
     constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(A_MN) << 15) |
@@ -328,7 +335,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (lane == 0 && rank == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            int chunk = 0, tile = 0;   // accumulator hand-overs, tiles so far
+            int chunk = 0, tile = 0;   // accumulator hand-overs, tiles (LONG: chunks) so far
             bool ok = true;
             auto wait_acc = [&](int a, int use) {   // the epilogues are through with its use - 1
                 if (mbar_wait_cluster(&acc_empty[a], (uint32_t(use) & 1u) ^ 1u, p.timeout_ns)) {
@@ -344,64 +351,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const uint32_t idesc = IDESC | (uint32_t(it.ncols >> 3) << 17);
                 const int slabs = slabs_of(it);
                 if (RANK && slabs == 0) continue;
-                const int a = CHUNKED ? 0 : tile & 1;
-                int main_buf = a;
-                // one part: this tile's accumulator; several: the small pairs'
-                if (SEVERAL && !(ok = wait_acc(1, tile))) break;
-                if (!CHUNKED && !(ok = wait_acc(a, tile >> 1))) break;
-                ++tile;
-                for (int s = 0; s < slabs; ++s) {
-                    if (*abort_flag || !mbar_wait_cluster(&full[stage], phase, p.timeout_ns)) {
-                        if (!*abort_flag) atomicOr(&g_error_word, ERR_FULL_WAIT);
-                        set_abort();
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sa = ring + uint32_t(stage) * STAGE;
-                    const uint32_t sb = sa + uint32_t(PA) * PART_BYTES;
-                    const bool rank_side = s >= it.slabs;   // (its stack is MN-major)
-                    auto mma = [&](uint32_t d, int qa, int qb, int kk, bool accumulate) {
-                        const uint32_t b = sb + uint32_t(qb) * PART_BYTES;
-                        const bool mn = B_MN || rank_side;
-                        mma_bf16_pair(d, part_desc<A_MN>(sa + uint32_t(qa) * PART_BYTES, kk),
-                                      mn ? part_desc<true>(b, kk) : part_desc<false>(b, kk),
-                                      idesc | (uint32_t(mn) << 16), accumulate);
-                    };
-                    if constexpr (SEVERAL) {
-                        const uint32_t small = taddr + ACC_COLUMNS;
-#pragma unroll
-                        for (int kk = 0; kk < BK / 16; ++kk) {
-                            bool first = s == 0 && kk == 0;
-#pragma unroll
-                            for (int qa = PA - 1; qa >= 0; --qa)
-#pragma unroll
-                                for (int qb = PB - 1; qb >= 0; --qb)
-                                    if (qa + qb > 0 && qa + qb <= 2) {
-                                        mma(small, qa, qb, kk, !first);
-                                        first = false;
-                                    }
+                // Several parts and RANK: chunks begin and end inside the loop over slabs.  (So they
+                // could here, but that made a slab of one MMA per 16 k 11 % longer.)
+                constexpr bool INSIDE = SEVERAL || RANK;
+                int begin = 0;
+                do {
+                    const int end = LONG ? min(slabs, begin + LONG_CHUNK) : slabs;
+                    const int a = INSIDE ? 0 : tile & 1;
+                    int main_buf = a;
+                    // one part: this tile's (LONG: chunk's) accumulator; several: the small pairs'
+                    if (SEVERAL && !(ok = wait_acc(1, tile))) break;
+                    if (!INSIDE && !(ok = wait_acc(a, tile >> 1))) break;
+                    ++tile;
+                    for (int s = begin; s < end; ++s) {
+                        if (*abort_flag || !mbar_wait_cluster(&full[stage], phase, p.timeout_ns)) {
+                            if (!*abort_flag) atomicOr(&g_error_word, ERR_FULL_WAIT);
+                            set_abort();
+                            ok = false;
+                            break;
                         }
-                    }
-                    // (one part leaves TMEM for two main accumulators, taken in turn)
-                    if (CHUNKED && s % CHUNK == 0) {
-                        main_buf = SEVERAL ? 0 : chunk & 1;
-                        if (!(ok = wait_acc(main_buf, SEVERAL ? chunk : chunk >> 1))) break;
-                        ++chunk;
-                    }
-                    const uint32_t main_acc = taddr + uint32_t(main_buf) * ACC_COLUMNS;
+                        tc_fence_after();
+                        const uint32_t sa = ring + uint32_t(stage) * STAGE;
+                        const uint32_t sb = sa + uint32_t(PA) * PART_BYTES;
+                        const bool rank_side = s >= it.slabs;   // (its stack is MN-major)
+                        auto mma = [&](uint32_t d, int qa, int qb, int kk, bool accumulate) {
+                            const uint32_t b = sb + uint32_t(qb) * PART_BYTES;
+                            const bool mn = B_MN || rank_side;
+                            mma_bf16_pair(d, part_desc<A_MN>(sa + uint32_t(qa) * PART_BYTES, kk),
+                                          mn ? part_desc<true>(b, kk) : part_desc<false>(b, kk),
+                                          idesc | (uint32_t(mn) << 16), accumulate);
+                        };
+                        if constexpr (SEVERAL) {
+                            const uint32_t small = taddr + ACC_COLUMNS;
 #pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk)
-                        mma(main_acc, 0, 0, kk, CHUNKED ? (s % CHUNK != 0 || kk > 0) : (s > 0 || kk > 0));
-                    mma_commit_pair(&empty[stage]);   // both CTAs' stage free once read
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
+                            for (int kk = 0; kk < BK / 16; ++kk) {
+                                bool first = s == 0 && kk == 0;
+#pragma unroll
+                                for (int qa = PA - 1; qa >= 0; --qa)
+#pragma unroll
+                                    for (int qb = PB - 1; qb >= 0; --qb)
+                                        if (qa + qb > 0 && qa + qb <= 2) {
+                                            mma(small, qa, qb, kk, !first);
+                                            first = false;
+                                        }
+                            }
+                        }
+                        // (one part leaves TMEM for two main accumulators, taken in turn)
+                        if (INSIDE && s % PER_CHUNK == 0) {
+                            main_buf = SEVERAL ? 0 : chunk & 1;
+                            if (!(ok = wait_acc(main_buf, SEVERAL ? chunk : chunk >> 1))) break;
+                            ++chunk;
+                        }
+                        const uint32_t main_acc = taddr + uint32_t(main_buf) * ACC_COLUMNS;
+#pragma unroll
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            mma(main_acc, 0, 0, kk, INSIDE ? (s % PER_CHUNK != 0 || kk > 0) : (s > begin || kk > 0));
+                        mma_commit_pair(&empty[stage]);   // both CTAs' stage free once read
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                        if (INSIDE && (s % PER_CHUNK == PER_CHUNK - 1 || s == slabs - 1))
+                            mma_commit_pair(&acc_full[main_buf]);
                     }
-                    if (CHUNKED && (s % CHUNK == CHUNK - 1 || s == slabs - 1))
-                        mma_commit_pair(&acc_full[main_buf]);
-                }
-                if (!CHUNKED && ok) mma_commit_pair(&acc_full[a]);
+                    if (!INSIDE && ok) mma_commit_pair(&acc_full[a]);
+                    begin = end;
+                } while (LONG && ok && begin < slabs);
             }
             if (!ok) {
                 // no MMA may still run when either CTA frees its TMEM or exits
@@ -483,7 +498,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if constexpr (CHUNKED) {
                 const int slabs = slabs_of(it);
                 float sum[4][32];
-                for (int s = 0; s < slabs && ok; s += CHUNK, ++chunk) {
+                for (int s = 0; s < slabs && ok; s += PER_CHUNK, ++chunk) {
                     const int buf = SEVERAL ? 0 : chunk & 1;
                     if (!(ok = wait_full(buf, SEVERAL ? chunk : chunk >> 1))) break;
 #pragma unroll
