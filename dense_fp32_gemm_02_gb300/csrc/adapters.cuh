@@ -5,6 +5,12 @@
 
 namespace sgl {
 
+// bfloat16 parts of the rank side's fp32 sums: all of their 24 bits, whatever the call's type.
+// (Two, 16 bits, would do for most of a bfloat16 result, but not where the sums cancel.  4096 x
+// 4096 x 4096 bfloat16, rank 32 of 4, us: backward 155 with two and 165 with three, of it the stack's
+// gradients 60 and 67; forward 118 and 120.)
+constexpr int S_PARTS = 3;
+
 // The adapters of a call: which one a row uses, its rank and scale.
 struct Adapters {
     const int *ids, *ranks;

@@ -225,15 +225,15 @@ struct Grouping {
 };
 
 // ------------------------------------------------------------------ stack gradients
-template <class XA, class XB, int PB>
+template <class XA, class XB>
 struct StackKernel {
     void (*kernel)(StackWork<XA>, StackWork<XB>, int, int, Adapters, Groups);
     size_t smem;
 
     template <int NT>
     static constexpr StackKernel of() {
-        constexpr size_t a = StackTile<XA, PB, NT>::SMEM, b = StackTile<XB, PB, NT>::SMEM;
-        return {&stack_tile_kernel<XA, XB, PB, NT>, a > b ? a : b};
+        constexpr size_t a = StackTile<XA, NT>::SMEM, b = StackTile<XB, NT>::SMEM;
+        return {&stack_tile_kernel<XA, XB, NT>, a > b ? a : b};
     }
     static constexpr StackKernel pick(int R) {
         return R <= 16 ? of<2>() : R <= 32 ? of<4>() : R <= 64 ? of<8>() : of<16>();
@@ -247,7 +247,7 @@ int stack_gradients(const Call &c, const Grouping &gr, XA x, bool x_wide, XB dy,
     const Adapters ad = c.adapters();
     int st;
     if (c.M > 0) {
-        const auto k = StackKernel<XA, XB, sizeof(T) == 4 ? 3 : 2>::pick(c.R);
+        const auto k = StackKernel<XA, XB>::pick(c.R);
         if ((st = shared_limit(k.kernel, k.smem)) != SGEMM_OK) return st;
         const StackWork<XA> wa{c.K, x, x_wide, s_rows, partial_a};
         const StackWork<XB> wb{c.N, dy, dy_wide, h_rows, partial_b};
@@ -278,7 +278,7 @@ int many_rows(const Call &c, int sms, cudaMemPool_t pool) {
     const bool ranked = c.L > 0, want_out = out && N > 0 && M > 0, product = want_out && K > 0;
     const bool planes = ranked && product, want_stack = BACK && ranked && (c.dA || c.dB);
     constexpr auto LAYOUT = BACK ? sgp::INPUT_GRAD : sgp::FORWARD;
-    constexpr int PRODUCTS = sizeof(T) == 4 ? 6 : 1, S_PARTS = sizeof(T) == 4 ? 3 : 2, PARTS = Packed<T>::PARTS;
+    constexpr int PRODUCTS = sizeof(T) == 4 ? 6 : 1, PARTS = Packed<T>::PARTS;
     Packed<T> P(M, K, BACK ? c.dY : c.X, BACK ? c.lddy : c.ldx), Q(c.K, c.N, c.W, c.ldw);
     if (!product) Q.direct = true;               // no parts of W are needed,
     if (!product && !ranked) P.direct = true;    // nor of P
@@ -339,7 +339,7 @@ int many_rows(const Call &c, int sms, cudaMemPool_t pool) {
         // Four warps to a row where there are few (154 rows of rank 122: 18 -> 6 us; 512 rows
         // of 32 adapters of rank 16: 17 -> 9), else one (8192 rows of rank 64: 7 us, four 15).
         const bool four = M <= 2048;
-        st = launch(nullptr, four ? rank_finish_kernel<T, 4> : rank_finish_kernel<T, 1>,
+        st = launch(nullptr, four ? rank_finish_kernel<4> : rank_finish_kernel<1>,
                     dim3(unsigned(four ? (M + 1LL) / 2 : (M + 7LL) / 8)), 256, 0, c.stream, M, ranges,
                     (const float *)r_partial, (long long)M * gr.width, ad, gr.g, side);
         if (st != SGEMM_OK) return st;

@@ -234,10 +234,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     using Item = typename Items<RANK>::Item;
     items.init(p);
     const uint32_t ring = smem_addr(reinterpret_cast<void *>(base));
-    // slabs of an item, the rank side's after the product's: with one part a side, the two
-    // parts of S are planes one after the other
+    // slabs of an item, the rank side's after the product's: with one part a side, the parts of S
+    // are planes one after the other
     auto slabs_of = [](const Item &it) {
-        return it.slabs + (RANK ? 0 : max(it.planes.y, 0) * (SEVERAL ? 1 : 2));
+        return it.slabs + (RANK ? 0 : max(it.planes.y, 0) * (SEVERAL ? 1 : sgl::S_PARTS));
     };
 
     if (warp == 0) {

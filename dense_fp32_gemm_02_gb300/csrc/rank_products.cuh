@@ -76,8 +76,7 @@ __device__ __forceinline__ void fill16(T *to, const T *p, int n, bool wide) {
 
 // ------------------------------------------------------------------ rank side
 // What the rank side leaves behind: S (M x R, scaled), unscaled for the caller in H, and
-// S's parts (float32: three, bfloat16: two, 2^-16, which is under the output's rounding)
-// in the planes of Groups and, for the stack's gradients, as rows of `pitch` columns, zero
+// S's parts in the planes of Groups and, for the stack's gradients, as rows of `pitch` columns, zero
 // past the rank: `s_rows` of S and `h_rows` of the scaled H that the caller gave.  What is
 // null is left out.
 struct RankSide {
@@ -89,11 +88,11 @@ struct RankSide {
 
 // The ranges' partial sums of the rank side added in order, WARPS warps to a row.  A row
 // whose adapter holds something that is not finite keeps the product from its tile's planes.
-template <class T, int WARPS>
+template <int WARPS>
 __global__ void __launch_bounds__(256)
     rank_finish_kernel(int M, int ranges, const float *__restrict__ partial, long long partial_plane, Adapters ad,
                        Groups g, RankSide to) {
-    constexpr int PARTS = sizeof(T) == 4 ? 3 : 2, ROWS = 8 / WARPS, THREADS = 32 * WARPS;
+    constexpr int ROWS = 8 / WARPS, THREADS = 32 * WARPS;
     __shared__ float own_s[ROWS][128], own_h[ROWS][128];
     const int t = threadIdx.x % THREADS, lane = t & 31, warp = t >> 5, in_block = threadIdx.x / THREADS;
     const long long row = (long long)blockIdx.x * ROWS + in_block, i = row < M ? row : M - 1;
@@ -127,7 +126,7 @@ __global__ void __launch_bounds__(256)
             uint32_t part[3];
             pair_parts(r < rank ? x[r] : 0.0f, r + 1 < rank ? x[r + 1] : 0.0f, part);
 #pragma unroll
-            for (int q = 0; q < PARTS; ++q)
+            for (int q = 0; q < S_PARTS; ++q)
                 *reinterpret_cast<uint32_t *>(rows + ((long long)q * M + i) * to.pitch + r) = part[q];
         }
     };
@@ -142,7 +141,7 @@ __global__ void __launch_bounds__(256)
         uint32_t part[3];
         pair_parts(x, y, part);
 #pragma unroll
-        for (int q = 0; q < PARTS; ++q)
+        for (int q = 0; q < S_PARTS; ++q)
             *reinterpret_cast<uint32_t *>(
                 to.planes + (((long long)q * g.capacity + planes.x + s) * 256 + i % 256) * 64 + 2 * lane) = part[q];
     }
@@ -174,17 +173,17 @@ struct ElementOf<PartRows> {
     static constexpr int PARTS = 3;
 };
 
-template <class X, int PB, int NT>
+template <class X, int NT>
 struct StackTile {
     using E = typename ElementOf<X>::type;
-    static constexpr int PA = ElementOf<X>::PARTS, COLS = 128;
+    static constexpr int PA = ElementOf<X>::PARTS, PB = S_PARTS, COLS = 128;
     // float32: rows 4 banks apart; bfloat16 and q: 16 bytes past a multiple of 128
     static constexpr int X_PITCH = COLS + (sizeof(E) == 4 ? 4 : 16 / int(sizeof(E)));
     static constexpr int X_PLANES = sizeof(E) == 2 ? PA : 1, S_PITCH = NT * 8 + 8;
     static constexpr int ROW_BYTES = X_PLANES * X_PITCH * int(sizeof(E)) + PB * S_PITCH * 2 + (sizeof(E) == 1 ? 4 : 0);
     // Rows to a slab, and slabs in the ring: several blocks to an SM hide more than a
-    // deeper ring does (4096 x 4096 bfloat16, rank 32: 28 us with two of 4 slabs, 22 with
-    // four of 2).
+    // deeper ring does (4096 x 4096 bfloat16, rank 32, two parts of S: 28 us with two of 4
+    // slabs, 22 with four of 2).
     static constexpr int DEPTH = SLAB * ROW_BYTES <= 56 * 1024 ? SLAB : SLAB / 2;
     static constexpr int X_PLANE = DEPTH * X_PITCH, X_BYTES = X_PLANES * X_PLANE * int(sizeof(E));
     static constexpr int S_PLANE = DEPTH * S_PITCH, S_BYTES = PB * S_PLANE * 2;
@@ -204,12 +203,12 @@ struct StackWork {
     float *partial;
 };
 
-template <class X, int PB, int NT, bool RANK_ROWS>
+template <class X, int NT, bool RANK_ROWS>
 __device__ __forceinline__ void stack_tile(const StackWork<X> &w, int bx, int by, int M, int pitch, const Adapters &ad,
                                            const Groups &g, unsigned char *smem, int *rows) {
-    using Z = StackTile<X, PB, NT>;
+    using Z = StackTile<X, NT>;
     using E = typename Z::E;
-    constexpr int PA = Z::PA, PER = 16 / int(sizeof(E)), STAGES = Z::STAGES, DEPTH = Z::DEPTH;
+    constexpr int PA = Z::PA, PB = Z::PB, PER = 16 / int(sizeof(E)), STAGES = Z::STAGES, DEPTH = Z::DEPTH;
     const int4 chunk = g.chunks[by];
     const int n = chunk.z, c0 = bx * Z::COLS, C = w.C;
     if (n == 0) return;
@@ -350,12 +349,12 @@ __device__ __forceinline__ void stack_tile(const StackWork<X> &w, int bx, int by
 
 // Blocks to an SM that the registers are limited for.  (float32 of rank 64, 4483 x 5120 x
 // 5760: 158 us at one, 125 at two.)
-constexpr int stack_blocks(int parts, int nt) { return nt <= 4 ? (parts == 2 ? 4 : 2) : nt == 8 ? 2 : 1; }
+constexpr int stack_blocks(int parts, int nt) { return nt <= 4 ? (parts == 1 ? 4 : 2) : nt == 8 ? 2 : 1; }
 
 // Both gradients: X^T G (C = K columns of X, 128 to a block) and H^T dY (N columns of dY),
 // each for max_chunks chunks.
-template <class XA, class XB, int PB, int NT>
-__global__ void __launch_bounds__(RANK_THREADS, stack_blocks(PB, NT))
+template <class XA, class XB, int NT>
+__global__ void __launch_bounds__(RANK_THREADS, stack_blocks(ElementOf<XB>::PARTS, NT))
     stack_tile_kernel(StackWork<XA> wa, StackWork<XB> wb, int M, int pitch, Adapters ad, Groups g) {
     extern __shared__ __align__(16) unsigned char smem_stack[];
     __shared__ int rows[CHUNK_ROWS];
@@ -363,9 +362,9 @@ __global__ void __launch_bounds__(RANK_THREADS, stack_blocks(PB, NT))
     sg::launch_dependents();
     const int across = (wa.C + 127) / 128 + (wb.C + 127) / 128, bx = blockIdx.x % across, by = blockIdx.x / across;
     if (bx < (wa.C + 127) / 128)
-        stack_tile<XA, PB, NT, false>(wa, bx, by, M, pitch, ad, g, smem_stack, rows);
+        stack_tile<XA, NT, false>(wa, bx, by, M, pitch, ad, g, smem_stack, rows);
     else
-        stack_tile<XB, PB, NT, true>(wb, bx - (wa.C + 127) / 128, by, M, pitch, ad, g, smem_stack, rows);
+        stack_tile<XB, NT, true>(wb, bx - (wa.C + 127) / 128, by, M, pitch, ad, g, smem_stack, rows);
 }
 
 // The chunks' partial sums of an adapter (blockIdx.y) added in order: K x R to dA, then

@@ -56,3 +56,43 @@ def test_a_long_bfloat16_sum_has_no_bias(op, K):
     magnitudes at most.  What is longer is added up in fp32 to nearest, another 25 * 2^-24."""
     got, mag = cancelling_product(op, K)
     assert float((got.abs() / mag).max()) <= 3.3e-5
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+@pytest.mark.parametrize("M", [3, 40, 300, 1500])
+def test_the_rank_side_keeps_fp32(M, dtype):
+    """X A is 2^20 + 2^10 + 1 and 2^20 + 2^10 (21 bits, with a gap in them after the first 8 and
+    after the next), and B takes one from the other: exactly 1 in fp32."""
+    b, K, N = binding(), 72, 264
+    X, A, B = torch.zeros(M, K), torch.zeros(1, K, 2), torch.zeros(1, 2, N)
+    X[:, 0], X[:, 1], X[:, 2] = 1024, 32, 1
+    A[0, 0], A[0, 1], A[0, 2, 0] = 1024, 32, 1
+    B[0, 0], B[0, 1] = 1, -1
+    X, A, B = (t.to(dtype).cuda() for t in (X, A, B))
+    Y = torch.empty(M, N, dtype=dtype, device="cuda")
+    b.lora_into(X, torch.zeros(K, N, dtype=dtype, device="cuda"), A, B,
+                torch.zeros(M, dtype=torch.int32, device="cuda"), Y)
+    assert bool((Y == 1).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+@pytest.mark.parametrize("M", [2, 700])
+def test_the_rank_sides_gradients_keep_fp32(M, dtype):
+    """The same of the gradients: G in dX and in dA, H in dB."""
+    b, K, N = binding(), 72, 264
+    X, dY, H = torch.zeros(M, K), torch.zeros(M, N), torch.zeros(M, 2)
+    A, B = torch.zeros(1, K, 2), torch.zeros(1, 2, N)
+    X[0], X[1] = 1, -1
+    dY[:2, 0], dY[:2, 1], dY[0, 2] = 1024, 32, 1
+    dY[0, 5], dY[1, 5] = 1, -1
+    B[0, :, 0], B[0, :, 1], B[0, 0, 2] = 1024, 32, 1
+    H[0, 0], H[1, 0] = 2 ** 20 + 2 ** 10 + 1, 2 ** 20 + 2 ** 10
+    A[0, :, 0], A[0, :, 1] = 1, -1
+    X, dY, A, B = (t.to(dtype).cuda() for t in (X, dY, A, B))
+    ids = torch.full((M,), -1, dtype=torch.int32, device="cuda")
+    ids[:2] = 0
+    dX, dA, dB = b.lora_backward_into(dY, X, torch.zeros(K, N, dtype=dtype, device="cuda"), A, B, ids, H.cuda(),
+                                      dX=torch.empty_like(X), dA=torch.empty_like(A), dB=torch.empty_like(B))
+    assert bool((dX[0] == 1).all()) and bool((dX[1] == 0).all())
+    assert bool((dA[0, :, 0] == 1).all()) and bool((dA[0, :, 1] == 0).all())
+    assert bool((dB[0, 0, 5] == 1).all()) and bool((dB[0, 1] == 0).all())
