@@ -291,7 +291,9 @@ def sgemm_host(A, B, C, alpha: float = 1.0, beta: float = 0.0, stream=None, devi
 
 
 # ------------------------------------------------------------------ linear layers
-# (include/sgemm_layers.h: float32 or bfloat16 tensors, all of one type)
+# (include/sgemm_layers.h: float32 or bfloat16 tensors, all of one type.  A matrix's rows are
+# contiguous, any distance apart, and do not overlap: what was expanded, the gradient of a sum
+# over rows for one, needs contiguous() first.)
 ACT8_BLOCK = 32   # columns of a row that share an exponent of an 8-bit checkpoint
 
 
@@ -367,11 +369,22 @@ def _vector(name, t, dtype, n, device):
     return t.data_ptr()
 
 
-def _pitch(rows, cols, row_stride, col_stride):
+_INT_MAX = 2 ** 31 - 1   # sizes and pitches are C ints, which ctypes cuts to 32 bits
+
+
+def _pitch(name, rows, cols, row_stride, col_stride):
+    if rows > _INT_MAX or cols > _INT_MAX:
+        raise SgemmError(SGEMM_ERR_TOO_LARGE)
     if cols > 1 and col_stride != 1 and rows > 0:
-        raise ValueError("rows must be contiguous (stride(-1) == 1)")
-    pitch = row_stride if rows > 1 and row_stride > cols else cols
-    return pitch if pitch > 0 else 1
+        raise ValueError(f"{name}: rows must be contiguous (stride(-1) == 1)")
+    if rows <= 1 or cols == 0:
+        return max(cols, 1)
+    if row_stride < cols:
+        raise ValueError(f"{name}: rows must not overlap (stride(-2) is {row_stride}, below the {cols} "
+                         "columns, as in an expanded tensor)")
+    if row_stride > _INT_MAX:
+        raise ValueError(f"{name}: rows are too far apart (stride(-2) is {row_stride}, past 2^31 - 1)")
+    return row_stride
 
 
 def _matrix(name, t, rows, cols):
@@ -381,9 +394,9 @@ def _matrix(name, t, rows, cols):
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must be {(rows, cols)}, got {tuple(t.shape)}")
     row_stride, col_stride = t.stride()
-    if col_stride == 1 and row_stride >= cols > 0 and rows > 1:   # (what _pitch would say)
+    if col_stride == 1 and 0 < cols <= row_stride <= _INT_MAX and 1 < rows <= _INT_MAX:   # (what _pitch would say)
         return t.data_ptr(), row_stride
-    return t.data_ptr(), _pitch(rows, cols, row_stride, col_stride)
+    return t.data_ptr(), _pitch(name, rows, cols, row_stride, col_stride)
 
 
 def _stack(name, t, count, rows, cols):
@@ -395,9 +408,9 @@ def _stack(name, t, count, rows, cols):
     if count == 0:
         return None, max(cols, 1), 0
     stride, row_stride, col_stride = t.stride()
-    if col_stride == 1 and row_stride >= cols > 0 and rows > 1:
+    if col_stride == 1 and 0 < cols <= row_stride <= _INT_MAX and 1 < rows <= _INT_MAX:
         return t.data_ptr(), row_stride, stride if count > 1 else 0
-    return t.data_ptr(), _pitch(rows, cols, row_stride, col_stride), stride if count > 1 else 0
+    return t.data_ptr(), _pitch(name, rows, cols, row_stride, col_stride), stride if count > 1 else 0
 
 
 def _checkpoint(q, e, rows, cols, device):
