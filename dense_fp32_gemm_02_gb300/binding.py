@@ -126,14 +126,24 @@ def version() -> int:
 
 
 # ------------------------------------------------------------------ tensors
+_INT_MAX = 2 ** 31 - 1   # sizes and pitches are C ints, which ctypes cuts to 32 bits
+
+
 def _ld(t, width: int) -> int:
     """Row pitch (elements) of a 2-D row-major tensor/array view."""
     if t.dim() != 2:
         raise ValueError("expected a 2-D tensor")
     if t.numel() > 0 and t.size(1) > 1 and t.stride(1) != 1:
         raise ValueError("rows must be contiguous (stride(1) == 1)")
-    ld = t.stride(0) if (t.size(0) > 1 and t.numel() > 0) else 0
-    return max(ld, width, 1)
+    if t.size(0) <= 1 or t.numel() == 0:
+        return max(width, 1)
+    ld = t.stride(0)
+    if ld < t.size(1):
+        raise ValueError(f"rows must not overlap (stride(0) is {ld}, below the {t.size(1)} columns, "
+                         "as in an expanded tensor)")
+    if ld > _INT_MAX:
+        raise ValueError(f"rows are too far apart (stride(0) is {ld}, past 2^31 - 1)")
+    return max(ld, width)
 
 
 def _stream_handle(stream, device):
@@ -150,6 +160,8 @@ def _shapes(A, B, C):
         raise ValueError(f"inner dimensions differ: A {tuple(A.shape)}, B {tuple(B.shape)}")
     if tuple(C.shape) != (M, N):
         raise ValueError(f"C must be {(M, N)}, got {tuple(C.shape)}")
+    if max(M, N, K) > _INT_MAX:
+        raise SgemmError(SGEMM_ERR_TOO_LARGE)
     return M, N, K
 
 
@@ -367,9 +379,6 @@ def _vector(name, t, dtype, n, device):
     if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
-
-
-_INT_MAX = 2 ** 31 - 1   # sizes and pitches are C ints, which ctypes cuts to 32 bits
 
 
 def _pitch(name, rows, cols, row_stride, col_stride):
