@@ -55,11 +55,14 @@ template <int ACT>
 __device__ __forceinline__ float2 activate(float2 z) {
     if constexpr (ACT == SGEMM_ACT_RELU)   // (a NaN stays one)
         return make_float2(z.x < 0.0f ? 0.0f : z.x, z.y < 0.0f ? 0.0f : z.y);
-    if constexpr (ACT == SGEMM_ACT_GELU) {   // z Phi(z) = max(z, 0) - |z| tail
+    // z Phi(z) = max(z, 0) - |z| tail, where +inf would be inf - inf * 0: its |z| is taken to be
+    // the largest number.  (2 us of 115 at 8192 x 16384 bfloat16; a check of the result took 6.)
+    if constexpr (ACT == SGEMM_ACT_GELU) {
         float2 tail, bell;
         normal_tail(z, tail, bell);
-        return make_float2(fmaf(-fabsf(z.x), tail.x, fmaxf(z.x, 0.0f)),
-                           fmaf(-fabsf(z.y), tail.y, fmaxf(z.y, 0.0f)));
+        const float most = __uint_as_float(0x7f7fffffu);
+        return make_float2(fmaf(-fabsf(fminf(z.x, most)), tail.x, fmaxf(z.x, 0.0f)),
+                           fmaf(-fabsf(fminf(z.y, most)), tail.y, fmaxf(z.y, 0.0f)));
     }
     return z;
 }

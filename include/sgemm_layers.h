@@ -118,7 +118,9 @@ int sgemm_lora_backward(int type, int M, int N, int K, int L, int R,
 /*
  * sgemm_act8_store -- the checkpoint of Z, and with it Y = act(Z) (sgemm_act of
  * sgemm.h) in the same pass where Y is not NULL.  Y may be Z itself (same
- * pointer and leading dimension).
+ * pointer and leading dimension).  GELU is +inf at +inf and, 0 times infinity, NaN at
+ * -inf, as its formula is; a NaN stays one under either activation (sgemm_ex's RELU
+ * gives 0).
  */
 int sgemm_act8_store(int type, int M, int K, const void *Z, int ldz, int act,
                      signed char *q, int ldq, signed char *e, int lde,
