@@ -259,7 +259,7 @@ int stack_gradients(const Call &c, const Grouping &gr, XA x, bool x_wide, XB dy,
     }
     const long long plane = ((long long)c.K + c.N) * c.R;
     const dim3 grid(unsigned(std::min<long long>((plane + 255) / 256, sms * 8LL)), unsigned(c.L));
-    return launch(nullptr, stack_finish_kernel<T>, grid, 256, 0, c.stream, c.K, c.N, c.R, (const float *)partial_a,
+    return launch(nullptr, stack_finish_kernel<T>, grid, 256, 0, c.stream, c.K, c.N, ad, (const float *)partial_a,
                   (const float *)partial_b, gr.g, Stack<T>{static_cast<T *>(c.dA), c.ldda, c.stride_da},
                   Stack<T>{static_cast<T *>(c.dB), c.lddb, c.stride_db});
 }

@@ -368,25 +368,27 @@ __global__ void __launch_bounds__(RANK_THREADS, stack_blocks(ElementOf<XB>::PART
 }
 
 // The chunks' partial sums of an adapter (blockIdx.y) added in order: K x R to dA, then
-// R x N to dB.
+// R x N to dB.  Past the adapter's rank there is zero: the partial sums hold products of S's zeros
+// there, which are NaN where a row of X or dY holds an infinity or a NaN.
 template <class T>
 __global__ void __launch_bounds__(256)
-    stack_finish_kernel(int K, int N, int R, const float *__restrict__ pa, const float *__restrict__ pb, Groups g,
+    stack_finish_kernel(int K, int N, Adapters ad, const float *__restrict__ pa, const float *__restrict__ pb, Groups g,
                         Stack<T> dA, Stack<T> dB) {
     sg::wait_prerequisites();
     sg::launch_dependents();
-    const int a = blockIdx.y, q0 = g.chunk_begin[a], q1 = g.chunk_begin[a + 1];
+    const int a = blockIdx.y, R = ad.R, rank = ad.rank(a), q0 = g.chunk_begin[a], q1 = g.chunk_begin[a + 1];
     const long long plane_a = (long long)K * R, plane_b = (long long)R * N;
     for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < plane_a + plane_b;
          t += (long long)gridDim.x * 256) {
         const bool first = t < plane_a;
         const long long u = first ? t : t - plane_a, plane = first ? plane_a : plane_b;
         const float *p = (first ? pa : pb) + u;
-        float sum = 0.0f;
-#pragma unroll 4
-        for (int q = q0; q < q1; ++q) sum += p[q * plane];
         const int cols = first ? R : N;
         const long long i = u / cols;
+        const int r = int(first ? u - i * cols : i);
+        float sum = 0.0f;
+#pragma unroll 4
+        for (int q = q0; q < (r < rank ? q1 : q0); ++q) sum += p[q * plane];
         const Stack<T> &out = first ? dA : dB;
         out.matrix(a)[i * out.ld + (u - i * cols)] = from_f32<T>(sum);
     }

@@ -49,3 +49,46 @@ def test_activations_of_infinities(K, dtype, act):
     in_place = z.cuda()
     b.act8_store_into(in_place, q, e, act=act, Y=in_place)
     assert same(in_place, y.cpu())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("where", ["X", "checkpoint", "dY", "H"])
+@pytest.mark.parametrize("R", [5, 24, 64, 100])
+def test_the_stacks_gradients_are_zero_past_the_rank(R, where, dtype):
+    """... whatever the rows hold: an infinity or a NaN in a row of adapter 1 shows in its
+    gradients, in the columns (rows) within its rank, and nowhere else."""
+    b, M, K, N, L = binding(), 700, 136, 200, 3
+    g = torch.Generator().manual_seed(R)
+    X, dY = torch.randn(M, K, generator=g).to(dtype), torch.randn(M, N, generator=g).to(dtype)
+    W, A, B = (torch.randn(*s, generator=g).to(dtype) for s in ((K, N), (L, K, R), (L, R, N)))
+    H = torch.randn(M, R, generator=g)
+    ids, ranks = torch.arange(M, dtype=torch.int32) % L, torch.tensor([R, R // 2, 0], dtype=torch.int32)
+    row = 1                                  # of adapter 1
+    if where in ("X", "checkpoint"):
+        X[row, 40] = INF
+    elif where == "dY":
+        dY[row, 17] = INF
+    else:
+        H[row, 0], H[:, R // 2:] = NAN, NAN   # (past its rank an adapter's H is not read)
+        H[0::3, R // 2:] = 1.0
+    x = X.cuda()
+    if where == "checkpoint":
+        x = b.act8_store_into(x, *b.act8_empty(M, K))
+    dA, dB = (torch.full(t.shape, 7.0, dtype=dtype, device="cuda") for t in (A, B))
+    b.lora_backward_into(dY.cuda(), x, W.cuda(), A.cuda(), B.cuda(), ids.cuda(), H.cuda(), dA=dA, dB=dB,
+                         ranks=ranks.cuda())
+    for a in range(L):
+        assert bool((dA[a, :, int(ranks[a]):] == 0).all()) and bool((dB[a, int(ranks[a]):] == 0).all())
+    assert bool(torch.isfinite(dA[0]).all()) and bool(torch.isfinite(dB[0]).all())
+    assert bool((dA[0] != 0).any()) and bool((dB[0] != 0).any())
+    within_a, within_b = dA[1, :, :R // 2], dB[1, :R // 2]
+    if where == "X":
+        assert not torch.isfinite(within_a[40]).any() and bool(torch.isfinite(within_a[41:]).all())
+    elif where == "checkpoint":               # the block of 32 columns
+        assert not torch.isfinite(within_a[32:64]).any() and bool(torch.isfinite(within_a[64:]).all())
+    elif where == "dY":
+        assert not torch.isfinite(within_a).any() and not torch.isfinite(within_b[:, 17]).any()
+        assert bool(torch.isfinite(within_b[:, 18:]).all())
+    else:
+        assert not torch.isfinite(within_b[0]).any() and bool(torch.isfinite(within_b[1:]).all())
+    assert b.device_status() == b.SGEMM_OK
