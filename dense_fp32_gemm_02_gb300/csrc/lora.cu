@@ -148,10 +148,11 @@ struct Packed {
 };
 
 // Raises a kernel's shared memory limit; on every launch, as it costs less than
-// remembering the devices it was done on.
+// remembering the devices it was done on.  `bytes` is the same in every call for a kernel.
+constexpr size_t DEFAULT_SHARED = 40 * 1024;   // (48 KB less what a kernel declares itself)
 template <class K>
 int shared_limit(K kernel, size_t bytes) {
-    if (bytes <= 40 * 1024) return SGEMM_OK;   // (48 KB less what a kernel declares itself)
+    if (bytes <= DEFAULT_SHARED) return SGEMM_OK;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     return e == cudaSuccess ? SGEMM_OK : sgh::cuda_fail(e);
 }
@@ -172,7 +173,9 @@ int prepare(int M, const Adapters &ad, const Groups &g, const PartsJob<XP> &p, c
             cudaStream_t stream) {
     int st = SGEMM_OK;
     if (g.planes) {
-        if ((st = shared_limit(group_rows_kernel, sort_smem(ad.L))) != SGEMM_OK) return st;
+        // (the limit is the process's: never this call's size, which another thread's may exceed)
+        if (sort_smem(ad.L) > DEFAULT_SHARED && (st = shared_limit(group_rows_kernel, sort_smem(kMaxAdapters))) != SGEMM_OK)
+            return st;
         st = launch(nullptr, group_rows_kernel, dim3(g.perm ? 2 : 1), SORT_THREADS, sort_smem(ad.L), stream, M, ad, g);
         if (st != SGEMM_OK) return st;
     }
