@@ -9,6 +9,7 @@
 #include "../../include/sgemm_layers.h"
 #include "act8.cuh"
 #include "host_state.h"
+#include "variant.cuh"
 
 #define SGEMM_API extern "C" __attribute__((visibility("default")))
 
@@ -89,6 +90,13 @@ struct Blocks {
     unsigned units;
     Divisor per_row;
     int K;
+
+#ifdef SGEMM_DEBUG_BOUNDS
+    // Whether n columns from c of a row are the matrix's.
+    __device__ bool holds(unsigned row, int c, int n) const {
+        return row < units / per_row.d && c >= 0 && (long long)c + n <= K;
+    }
+#endif
 };
 struct Checkpoint {
     signed char *q, *e;
@@ -122,7 +130,7 @@ __global__ void __launch_bounds__(kThreads)
         const unsigned u = first + d * (kThreads / 4);
         row[d] = b.per_row.quotient(u);
         col[d] = int(u - row[d] * b.per_row.d) * ACT8_BLOCK + sub * 8;
-        in[d] = u < b.units && col[d] < b.K;
+        in[d] = u < b.units && col[d] < b.K && SG_IN_RANGE(b.holds(row[d], col[d], 8));
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[d][i] = 0.0f;
         if (in[d]) load8(Z + (long long)row[d] * ldz + col[d], z[d]);
@@ -173,6 +181,7 @@ __global__ void __launch_bounds__(kThreads)
     const unsigned u = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), row = b.per_row.quotient(u);
     if (u >= b.units) return;
     const int c0 = int(u - row * b.per_row.d) * (D * ACT8_BLOCK) + lane;
+    if (!SG_IN_RANGE(b.holds(row, c0 - lane, 1))) return;
     const T *zr = Z + (long long)row * ldz + c0;
     signed char *q = c.q + row * c.ldq + c0, *e = c.e + row * c.lde + (c0 - lane) / ACT8_BLOCK;
     T *y = WITH_Y ? Y + (long long)row * ldy + c0 : nullptr;
@@ -222,7 +231,7 @@ __global__ void __launch_bounds__(kThreads)
         const unsigned u = first + d * (kThreads / 4);
         row[d] = b.per_row.quotient(u);
         col[d] = int(u - row[d] * b.per_row.d) * ACT8_BLOCK + sub * 8;
-        in[d] = u < b.units && col[d] < b.K;
+        in[d] = u < b.units && col[d] < b.K && SG_IN_RANGE(b.holds(row[d], col[d], 8));
         if (!in[d]) continue;
         w[d] = *reinterpret_cast<const uint2 *>(c.q + row[d] * c.ldq + col[d]);
         e[d] = c.e[row[d] * c.lde + col[d] / ACT8_BLOCK];
@@ -253,6 +262,7 @@ __global__ void __launch_bounds__(kThreads)
     const unsigned u = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), row = b.per_row.quotient(u);
     if (u >= b.units) return;
     const int c0 = int(u - row * b.per_row.d) * (D * ACT8_BLOCK) + lane;
+    if (!SG_IN_RANGE(b.holds(row, c0 - lane, 1))) return;
     const signed char *q = c.q + row * c.ldq + c0, *e = c.e + row * c.lde + (c0 - lane) / ACT8_BLOCK;
     const T *dyr = GRAD ? dY + (long long)row * lddy + c0 : nullptr;
     T *to = out + (long long)row * ldo + c0;
@@ -388,6 +398,8 @@ Checkpoint readable(const signed char *q, int ldq, const signed char *e, int lde
 }
 
 }  // namespace
+
+cudaError_t sgh::act8_error_word(unsigned *v, bool clear) { return sgv::unit_error_word(v, clear); }
 
 SGEMM_API int sgemm_act8_store(int type, int M, int K, const void *Z, int ldz, int act,
                                signed char *q, int ldq, signed char *e, int lde, void *Y, int ldy,

@@ -103,6 +103,9 @@ __device__ __forceinline__ void take_parts(const PartsJob<X> &job, long long t, 
     for (; t < total; t += step) {
         const long long i = small ? (long long)job.per_row.quotient(unsigned(t)) : t / job.per_row.d;
         const int c = int(t - i * job.per_row.d) * 8;
+        if (!SG_IN_RANGE(i >= 0 && i < job.rows && c >= 0 && c < job.cols && c + 8 <= job.to.pitch &&
+                         (i + 1) * job.to.pitch <= job.to.plane))
+            continue;
         float v[8];
         if (job.wide && c + 8 <= job.cols) {
             job.x.at8(i, c, v);
@@ -231,13 +234,14 @@ __device__ __forceinline__ void lay_out_planes(int M, const Adapters &ad, const 
             const int w = max(b[i], 0) >> 5 & 31;
             const unsigned of_w = __shfl_sync(0xffffffffu, word, w);
             const int position = __shfl_sync(0xffffffffu, below, w) + __popc(of_w & ((1u << (b[i] & 31)) - 1));
-            if (b[i] > -2) g.position[t * 256 + i * 32 + lane] = b[i] >= 0 ? position : 0;
+            if (b[i] > -2 && SG_IN_RANGE((long long)t * 256 + i * 32 + lane < M && position >= 0 && position <= kinds))
+                g.position[t * 256 + i * 32 + lane] = b[i] >= 0 ? position : 0;
         }
         int4 *list = g.plane_adapter + (long long)t * g.most_planes;
         unsigned left = word;
         for (int k = below; left != 0; ++k, left &= left - 1) {
             const int id = lane * 32 + __ffs(left) - 1;
-            if (!SG_IN_RANGE(k * g.width / 64 < min(planes, g.most_planes))) break;
+            if (!SG_IN_RANGE(k * g.width / 64 < planes && (k + 1) * g.width <= g.most_planes * 64 && id < ad.L)) break;
             if (g.width >= 64) {
                 for (int h = 0; h < halves; ++h) list[k * halves + h] = make_int4(id, h * 64, 0, 0);
             } else {
@@ -327,7 +331,9 @@ __device__ __forceinline__ void sort_rows(int M, const Adapters &ad, const Group
             continue;
         }
         const int b = group_at(chunk0, L, t), p = first[b] + (t - chunk0[b]) * g.chunk;
-        g.chunks[t] = make_int4(b, p, min(g.chunk, first[b + 1] - p), 0);
+        const int n = min(g.chunk, first[b + 1] - p);
+        const bool in = SG_IN_RANGE(chunk0[L] <= g.max_chunks && p >= 0 && n > 0 && (long long)p + n <= M);
+        g.chunks[t] = make_int4(b, p, in ? n : 0, 0);
     }
 }
 
@@ -386,6 +392,7 @@ __global__ void __launch_bounds__(256)
     at.p += a * at.plane;
     at.plane *= ad.L;
     const int r = blockIdx.z * 8 + (lane & 7);
+    if (!SG_IN_RANGE(a < ad.L && c >= 0 && c + 8 <= at.pitch && (r + 1) * at.pitch <= side.to.plane)) return;
     const T *p = v + (side.trans ? c * ld + r : r * ld + c);
     bool finite = true;
     float x[8];

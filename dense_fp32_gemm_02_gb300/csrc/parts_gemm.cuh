@@ -265,7 +265,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     mbar_arrive_expect_tx_cluster(
                         fb, RANK ? PA * PART_BYTES + PB * uint32_t(it.ncols / 2) * 128u : STAGE);
                     if (s < it.slabs) {
-                        const int k = (it.slab0 + s) * BK;
+                        const int k = SG_IN_RANGE(it.slab0 + s < p.slabs && it.tm < p.tiles_m && stage < STAGES)
+                                          ? (it.slab0 + s) * BK : 0;
 #pragma unroll
                         for (int q = 0; q < PA; ++q) {
                             const uint32_t at = st + uint32_t(q) * PART_BYTES;
@@ -281,10 +282,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                             const int deep = min(p.width, 32);
                             for (int u = 0; u < it.ncols / 2; u += deep) {
                                 const int c = int(rank) * (it.ncols / 2) + u, in_plane = c % 64;
-                                const int4 of = it.adapters[c / 64];
+                                const int4 of = it.adapters[SG_IN_RANGE(c / 64 < it.planes.y) ? c / 64 : 0];
                                 const int slot = p.width < 64 ? in_plane / p.width : 0;
-                                const int a = slot == 0 ? of.x : slot == 1 ? of.y : slot == 2 ? of.z : of.w;
+                                const int id = slot == 0 ? of.x : slot == 1 ? of.y : slot == 2 ? of.z : of.w;
                                 const int r = p.width < 64 ? in_plane % p.width : of.y + in_plane;
+                                const int a = SG_IN_RANGE(id >= 0 && id < p.L && r >= 0 && r + deep <= p.width) ? id : 0;
 #pragma unroll
                                 for (int q = 0; q < PB; ++q)
                                     tma_load_3d_pair(st + uint32_t(PA + q) * PART_BYTES + uint32_t(u) * 128u, &mB, fb, k,
@@ -303,7 +305,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         }
                     } else if constexpr (!A_MN && !RANK) {
                         const int e = s - it.slabs, part = SEVERAL ? 0 : e / it.planes.y;
-                        const int in_tile = SEVERAL ? e : e % it.planes.y, plane = it.planes.x + in_tile;
+                        const int in_tile = SEVERAL ? e : e % it.planes.y;
+                        const int plane = SG_IN_RANGE(in_tile < p.most_planes && part < sgl::S_PARTS && it.planes.x >= 0 &&
+                                                      it.planes.x + in_tile < p.capacity) ? it.planes.x + in_tile : 0;
 #pragma unroll
                         for (int q = 0; q < PA; ++q)
                             tma_load_3d_pair(st + uint32_t(q) * PART_BYTES, &mH, fb, 0, int(rank) * ROWS,
@@ -315,8 +319,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                             for (int u = 0; u * deep < BK; ++u) {
                                 const uint32_t at =
                                     st + uint32_t(PA + q) * PART_BYTES + uint32_t(u * deep) * 128u;
-                                const int a = u == 0 ? of.x : u == 1 ? of.y : u == 2 ? of.z : of.w;
+                                const int id = u == 0 ? of.x : u == 1 ? of.y : u == 2 ? of.z : of.w;
                                 const int r = deep == BK ? of.y : 0;
+                                const int a = SG_IN_RANGE(id >= 0 && id < p.L && r >= 0 && r + deep <= p.width) ? id : 0;
                                 tma_load_3d_pair(at, &mV, fb, bcol, r, q * p.L + a);
                                 tma_load_3d_pair(at + GROUP_BYTES, &mV, fb, bcol + 64, r, q * p.L + a);
                             }
@@ -465,7 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const int col = col0 + c * 32 + lane;
                 if (col >= p.N) return;
                 const int rows = min(32, p.M - row0);
-                if (!SG_IN_RANGE(col < it.col0 + it.ncols && row0 + rows <= (it.tm + 1) * TILE)) return;
+                if (!SG_IN_RANGE(col < it.col0 + it.ncols && row0 + rows <= (it.tm + 1) * TILE && it.split < p.splits)) return;
                 if (p.partial) {
                     float *out = p.partial + ((long long)it.split * p.M + row0) * p.N + col;
                     for (int r = 0; r < rows; ++r) out[(long long)r * p.N] = buf[r * 33 + lane];
@@ -531,7 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
                             const int r = col0 + c * 32 + i - first;   // a multiple of 4, as all of these are
-                            if (any && c * 32 < width && r >= 0 && r < p.width && SG_IN_RANGE(it.split < p.splits))
+                            if (any && c * 32 < width && r >= 0 && r < p.width && SG_IN_RANGE(it.split < p.splits && r + 4 <= p.width))
                                 *reinterpret_cast<float4 *>(out + r) =
                                     make_float4(sum[c][i], sum[c][i + 1], sum[c][i + 2], sum[c][i + 3]);
                         }
@@ -587,7 +592,7 @@ __global__ void __launch_bounds__(256)
                   Epilogue<T, TRANS> epi) {
     const long long i = blockIdx.y;
     const int j = blockIdx.x * 256 + threadIdx.x;
-    if (j >= N) return;
+    if (j >= N || !SG_IN_RANGE(row0 + i < M)) return;
     wait_prerequisites();
     launch_dependents();
     float x = epi.bias ? sgl::to_f32(epi.bias[j]) : 0.0f;

@@ -104,6 +104,9 @@ __global__ void __launch_bounds__(256)
     const int4 planes = to.planes ? g.planes[i / 256] : make_int4(0, 0, 0, 0);
     const int first = to.planes ? g.position[i] * g.width : 0;
     const bool unclean = to.planes && rank > 0 && g.unclean[a];
+    const bool fits = SG_IN_RANGE(ad.R <= g.width && ad.R <= 128 && first >= 0 &&
+                                  (!to.planes || rank == 0 || first + g.width <= 64 * planes.y) &&
+                                  (!planes.z || (planes.x >= 0 && planes.x + planes.y <= g.capacity)));
     for (int r = t; r < ad.R; r += THREADS) {
         float sum = 0.0f, h = 0.0f;
         if (r < rank) {
@@ -120,7 +123,7 @@ __global__ void __launch_bounds__(256)
         }
     }
     __syncthreads();
-    if (row >= M) return;
+    if (row >= M || !fits) return;
     auto rows_of = [&](bf16 *rows, const float *x) {   // a row as parts
         for (int r = 2 * t; r < to.pitch; r += 2 * THREADS) {
             uint32_t part[3];
@@ -214,7 +217,11 @@ __device__ __forceinline__ void stack_tile(const StackWork<X> &w, int bx, int by
     if (n == 0) return;
     const X &x = w.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int m = threadIdx.x; m < n; m += RANK_THREADS) rows[m] = g.perm[chunk.y + m];
+    if (!SG_IN_RANGE(by < g.max_chunks && n > 0 && n <= CHUNK_ROWS && chunk.y >= 0 && (long long)chunk.y + n <= M)) return;
+    for (int m = threadIdx.x; m < n; m += RANK_THREADS) {
+        const int row = g.perm[chunk.y + m];
+        rows[m] = SG_IN_RANGE(row >= 0 && row < M) ? row : 0;
+    }
     __syncthreads();
 
     auto fill = [&](int stage, int i0) {
@@ -223,7 +230,7 @@ __device__ __forceinline__ void stack_tile(const StackWork<X> &w, int bx, int by
 #pragma unroll
         for (int o = threadIdx.x; o < DEPTH * Z::COLS / PER; o += RANK_THREADS) {
             const int m = o / (Z::COLS / PER), c = (o % (Z::COLS / PER)) * PER;
-            const bool in = i0 + m < n && c0 + c < C;
+            const bool in = i0 + m < n && c0 + c < C && SG_IN_RANGE(m < DEPTH && c + PER <= Z::X_PITCH);
             const long long i = in ? rows[i0 + m] : 0;
             if constexpr (sizeof(E) == 1) {
                 E *to = xs + m * Z::X_PITCH + c;
@@ -251,7 +258,7 @@ __device__ __forceinline__ void stack_tile(const StackWork<X> &w, int bx, int by
 #pragma unroll
             for (int o = threadIdx.x; o < DEPTH * NT; o += RANK_THREADS) {
                 const int m = o / NT, r = (o % NT) * 8;
-                const bool in = i0 + m < n;
+                const bool in = i0 + m < n && SG_IN_RANGE(m < DEPTH && r + 8 <= Z::S_PITCH && r + 8 <= pitch);
                 const long long i = in ? rows[i0 + m] : 0;
                 sg::cp_async16(shared_address(ss + q * Z::S_PLANE + m * Z::S_PITCH + r),
                                w.s + ((long long)q * M + i) * pitch + r, in ? 16u : 0u);
@@ -377,6 +384,7 @@ __global__ void __launch_bounds__(256)
     sg::wait_prerequisites();
     sg::launch_dependents();
     const int a = blockIdx.y, R = ad.R, rank = ad.rank(a), q0 = g.chunk_begin[a], q1 = g.chunk_begin[a + 1];
+    if (!SG_IN_RANGE(a < ad.L && q0 >= 0 && q0 <= q1 && q1 <= g.max_chunks)) return;
     const long long plane_a = (long long)K * R, plane_b = (long long)R * N;
     for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < plane_a + plane_b;
          t += (long long)gridDim.x * 256) {
@@ -390,7 +398,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll 4
         for (int q = q0; q < (r < rank ? q1 : q0); ++q) sum += p[q * plane];
         const Stack<T> &out = first ? dA : dB;
-        out.matrix(a)[i * out.ld + (u - i * cols)] = from_f32<T>(sum);
+        if (SG_IN_RANGE(i >= 0 && i < (first ? K : R) && r >= 0 && r < R)) out.matrix(a)[i * out.ld + (u - i * cols)] = from_f32<T>(sum);
     }
 }
 

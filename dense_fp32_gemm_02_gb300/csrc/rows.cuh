@@ -46,6 +46,7 @@ __device__ __forceinline__ void rank_of_row(const RowsWork &w, int b, const Rows
     const int a = ad.of_row(i);
     const int rank = a < 0 ? 0 : ad.rank(a);
     if (rank == 0) return;   // nothing reads this row's sums
+    if (!SG_IN_RANGE(b >= 0 && i < w.M && q >= 0 && q < w.rank_ranges && ad.R <= 128)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int along = 1;           // lanes along the rank: a power of two, up to 16 (32 for float32)
     while (along * PER < ad.R) along *= 2;
@@ -75,7 +76,7 @@ __device__ __forceinline__ void rank_of_row(const RowsWork &w, int b, const Rows
 #pragma unroll
     for (int d = 0; d < PER; ++d)
         for (int o = 16; o >= along; o >>= 1) sum[d] += __shfl_xor_sync(0xffffffffu, sum[d], o);
-    if (lane < along) {
+    if (lane < along && SG_IN_RANGE(r0 + PER <= 128)) {
 #pragma unroll
         for (int d = 0; d < PER; ++d) sums[warp * 128 + r0 + d] = sum[d];
     }
@@ -122,6 +123,7 @@ __global__ void __launch_bounds__(RANK_THREADS, stream_blocks(MR))
     const int n0 = (int(blockIdx.x) % w.across) * COLS, q = int(blockIdx.x) / w.across;
     const int k0 = q * w.range, kn = min(w.range, w.K - k0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (!SG_IN_RANGE(kn > 0 && kn <= STREAM_RANGE && k0 + kn <= w.K && n0 < w.N && q < w.ranges && w.M <= MR)) return;
     auto column = [&](int e) { return n0 + (WIDE ? lane * PER + e : e * 32 + lane); };
     auto load = [&](int k) {   // 16 bytes of row k0 + k of W, zero past its end
         const T *p = W + (k0 + k) * ldw;
@@ -178,7 +180,7 @@ __global__ void __launch_bounds__(RANK_THREADS, stream_blocks(MR))
             float s = 0.0f;
 #pragma unroll
             for (int k = 0; k < WARPS; ++k) s += sm[((m - m0) * WARPS + k) * COLS + c];
-            if (m < w.M && n0 + c < w.N) out[(long long)m * w.N + n0 + c] = s;
+            if (m < w.M && n0 + c < w.N && SG_IN_RANGE(((m - m0 + 1) * WARPS - 1) * COLS + c < RED)) out[(long long)m * w.N + n0 + c] = s;
         }
     }
 }
@@ -251,6 +253,7 @@ __global__ void __launch_bounds__(RANK_THREADS, 2)
     const int n0 = (int(blockIdx.x) % w.across) * ROWS_COLS, q = int(blockIdx.x) / w.across;
     const int k_begin = q * w.range, k_end = min(w.K, k_begin + w.range);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp & 3, piece = warp >> 2;
+    if (!SG_IN_RANGE(k_begin < k_end && n0 < w.N && q < w.ranges && w.M <= Z::X_ROWS)) return;
 
     // every WARPS'th row of the slab to a warp, 16 bytes to a lane or single elements
     auto fill = [&](int stage, int k0) {
@@ -355,7 +358,8 @@ __global__ void __launch_bounds__(RANK_THREADS, 2)
     }
     // the pieces of the slabs' k in order, then out
     auto place = [&](int p, int m, int t, int e) {
-        return ring + (((p - 1) * MT * 16 + (m * 4 + t) * 4 + e) * 128 + group * 32 + lane);
+        const int at = ((p - 1) * MT * 16 + (m * 4 + t) * 4 + e) * 128 + group * 32 + lane;
+        return ring + (SG_IN_RANGE(at >= 0 && at < STAGES * Z::W_ELEMS) ? at : 0);
     };
     __syncthreads();
     if (piece > 0) {
@@ -407,6 +411,7 @@ __global__ void __launch_bounds__(256)
     __shared__ __align__(16) float sums[8][256];
     const int i = blockIdx.y, n0 = blockIdx.x * 256, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int j = n0 + lane * 8;
+    if (!SG_IN_RANGE(i < w.M && n0 < w.N && (ad.L == 0 || ad.R <= 128))) return;
     const int a = ad.of_row(i), rank = a < 0 ? 0 : ad.rank(a);
     const float scale = a < 0 ? 0.0f : ad.scale(a);
     float x[8] = {}, v[8];

@@ -1266,7 +1266,7 @@ int read_and_clear_error_word(cudaStream_t stream) {
         &sgv::unit_error_word, sgv::extra_variants().error_word,
         sgv::staged_variants().error_word, sgv::sweep_variants_a().error_word,
         sgv::sweep_variants_b().error_word, sgv::sweep_variants_c().error_word,
-        sgv::tall_variants().error_word, &sgh::parts_gemm_error_word, &sgh::lora_error_word};
+        sgv::tall_variants().error_word, &sgh::parts_gemm_error_word, &sgh::lora_error_word, &sgh::act8_error_word};
     unsigned any = 0;
     for (auto word : units) {
         unsigned v = 0;

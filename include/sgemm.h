@@ -245,10 +245,11 @@ int sgemm_selftest_wait_timeout(unsigned long long ns, sgemm_stream_t stream);
  * sgemm_debug_bounds_checks -- 1 when this library is the range-checked build
  * (compiled with -DSGEMM_DEBUG_BOUNDS: libsgemm_debug_bounds.so), 0 otherwise.
  * In that build every kernel checks the indices of its shared-memory,
- * global-memory, tensor-memory and TMA accesses against the ranges they must
- * lie in (the fragments of a slab inside its ring stage, the outputs of a tile
- * inside the tile, stream-K slots and counters inside their arrays, pre-pass
- * writes inside the row pitch, ...).  An index out of range is not used: the
+ * global-memory, tensor-memory and TMA accesses that are computed from sizes
+ * or read from memory against the ranges they must lie in (the fragments of a
+ * slab inside its ring stage, the outputs of a tile inside the tile, stream-K
+ * slots and counters inside their arrays, pre-pass writes inside the row pitch,
+ * the layers' row numbers, chunks, planes, adapters and parts inside theirs, ...).  An index out of range is not used: the
  * access is skipped and sgemm_device_status() reports SGEMM_ERR_BOUNDS.  It is
  * the library's own stand-in for a memory checker, for tests; it runs slower
  * and is never the library the package loads by default.
