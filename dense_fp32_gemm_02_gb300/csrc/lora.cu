@@ -306,7 +306,7 @@ int many_rows(const Call &c, int sms, cudaMemPool_t pool) {
                      P.bytes() + Q.bytes() + piece(split.partial_floats * 4));
     if (st != SGEMM_OK) return st;
     gr.place(ws);
-    RankSide side{ws.take<float>(s_floats), c.H, c.ldh, nullptr, nullptr, nullptr, pitch};
+    RankSide side{ws.take<float>(s_floats), c.H, c.ldh, nullptr, nullptr, nullptr, pitch, PARTS == 1};
     float *r_partial = ws.take<float>(r_floats);
     const Stack<const T> A = stack_of<T>(c.A, c.lda, c.stride_a), B = stack_of<T>(c.B, c.ldb, c.stride_b);
     const Parts u{ws.take<bf16>(u_elems), upitch, uplane}, v{ws.take<bf16>(v_elems), vpitch, vplane};

@@ -35,15 +35,17 @@ struct Act8Rows {
 // ------------------------------------------------------------------ parts
 // x as a sum of up to three bfloat16, each the leading 8 bits of what the ones before
 // leave (cut, not rounded: x = x0 + x1 + x2 exactly, and no part overflows).  What is
-// not finite stays in the first.
+// not finite stays in the last, which a product of parts takes with the other side's first alone:
+// infinity times a part that is zero only because the number has few bits would be NaN.  (The
+// first is then 1 of its sign, for infinity times infinity.)
 __device__ __forceinline__ void split_parts(float x, float (&part)[3]) {
     const float head = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
     float rest = x - head;
     const bool finite = fabsf(rest) < 3.0e38f;   // not for an infinity or a NaN
     rest = finite ? rest : 0.0f;
-    part[0] = finite ? head : x + x;             // (x + x: a NaN whose leading bits say so)
+    part[0] = finite ? head : copysignf(1.0f, x);
     part[1] = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
-    part[2] = rest - part[1];
+    part[2] = finite ? rest - part[1] : x + x;   // (x + x: a NaN whose leading bits say so)
 }
 
 // Two floats that are bfloat16 already as a word (the first in the low half).

@@ -78,13 +78,23 @@ __device__ __forceinline__ void fill16(T *to, const T *p, int n, bool wide) {
 // What the rank side leaves behind: S (M x R, scaled), unscaled for the caller in H, and
 // S's parts in the planes of Groups and, for the stack's gradients, as rows of `pitch` columns, zero
 // past the rank: `s_rows` of S and `h_rows` of the scaled H that the caller gave.  What is
-// null is left out.
+// null is left out.  `filled`: those rows meet matrices of one part, whose infinities meet all
+// parts of a sum.
 struct RankSide {
     float *S, *H;
     long long ldh;
     bf16 *planes, *s_rows, *h_rows;
     int pitch;
+    bool filled;
 };
+
+// The parts of x with none of them zero: the least normal number, of x's sign, in the place of a
+// zero (under 2^-30 of x; a smaller x keeps its zeros), because infinity times zero is NaN.
+__device__ __forceinline__ void fill_parts(float x, float (&part)[3]) {
+    const float least = fabsf(x) >= 0x1p-96f ? copysignf(0x1p-126f, x) : 0.0f;
+    part[1] = part[1] == 0.0f ? least : part[1];
+    part[2] = part[2] == 0.0f ? least : part[2];
+}
 
 // The ranges' partial sums of the rank side added in order, WARPS warps to a row.  A row
 // whose adapter holds something that is not finite keeps the product from its tile's planes.
@@ -126,11 +136,14 @@ __global__ void __launch_bounds__(256)
     if (row >= M || !fits) return;
     auto rows_of = [&](bf16 *rows, const float *x) {   // a row as parts
         for (int r = 2 * t; r < to.pitch; r += 2 * THREADS) {
-            uint32_t part[3];
-            pair_parts(r < rank ? x[r] : 0.0f, r + 1 < rank ? x[r + 1] : 0.0f, part);
+            const float xr = r < rank ? x[r] : 0.0f, yr = r + 1 < rank ? x[r + 1] : 0.0f;
+            float px[3], py[3];
+            split_parts(xr, px);
+            split_parts(yr, py);
+            if (to.filled) fill_parts(xr, px), fill_parts(yr, py);
 #pragma unroll
             for (int q = 0; q < S_PARTS; ++q)
-                *reinterpret_cast<uint32_t *>(rows + ((long long)q * M + i) * to.pitch + r) = part[q];
+                *reinterpret_cast<uint32_t *>(rows + ((long long)q * M + i) * to.pitch + r) = pack_exact(px[q], py[q]);
         }
     };
     if (to.h_rows) rows_of(to.h_rows, H);

@@ -14,6 +14,8 @@
  *    aligned rows are faster, no more).
  *  - Sizes are at most 2^31 - 65536 (SGEMM_ERR_TOO_LARGE above that).
  *  - Elements of an output outside its rows x columns block are not written.
+ *  - Infinities and NaNs give what the formulas give, however many rows there are
+ *    (bfloat16's and float32's alike; weights under 2^-96 may count as zero next to an infinity).
  *  - Results are bitwise reproducible from call to call on a GPU model.
  *  - The work is enqueued on `stream`; nothing synchronises the host.  Workspaces come
  *    from the library's stream-ordered pool and go back to it behind the last kernel.

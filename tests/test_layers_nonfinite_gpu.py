@@ -92,3 +92,84 @@ def test_the_stacks_gradients_are_zero_past_the_rank(R, where, dtype):
     else:
         assert not torch.isfinite(within_b[0]).any() and bool(torch.isfinite(within_b[1:]).all())
     assert b.device_status() == b.SGEMM_OK
+
+
+def product(x, w):
+    """x w in 64 bits, every product and sum by IEEE 754's rules (infinity times zero among them)."""
+    return torch.stack([(row.double().unsqueeze(1) * w.double()).sum(0) for row in x])
+
+
+def same_kinds(got, ref):
+    got = got.cpu().double()
+    for kind in (torch.isnan, torch.isposinf, torch.isneginf):
+        assert torch.equal(kind(got), kind(ref)), (kind.__name__, int((kind(got) != kind(ref)).sum()))
+
+
+def few_bits(rows, cols, seed):
+    """Values that bfloat16 holds, zeros among them: float32 of these has nothing but zeros
+    past its first bits."""
+    g = torch.Generator().manual_seed(seed)
+    return torch.randint(-4, 5, (rows, cols), generator=g) / 2
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M", [1, 3, 8, 9, 16, 40, 65, 300, 1500])
+def test_infinities_of_x_and_w_are_those_of_the_formula(M, dtype):
+    """However many rows there are: infinity times a number is infinity of its sign, times
+    zero, or with infinity of the other sign in the sum, NaN."""
+    b, K, N = binding(), 72, 136
+    X, W = few_bits(M, K, 1), few_bits(K, N, 2)
+    X[0, 3], W[5, 2], W[7, 4], W[8, 4], W[9, 6] = INF, INF, -INF, INF, NAN
+    if M > 2:
+        X[1, 4], X[2, 5], X[2, 6] = -INF, INF, -INF       # (X[2, 5] meets W[5, 2])
+    W[3, 10:20] = torch.linspace(0.1, 2.3, 10)            # of all bits
+    ids = torch.full((M,), -1, dtype=torch.int32, device="cuda")
+    A, B = torch.zeros(1, K, 4, dtype=dtype, device="cuda"), torch.zeros(1, 4, N, dtype=dtype, device="cuda")
+    X, W = X.to(dtype), W.to(dtype)
+    Y = b.lora_into(X.cuda(), W.cuda(), A, B, ids, torch.empty(M, N, dtype=dtype, device="cuda"))
+    same_kinds(Y, product(X, W))
+    dX = torch.empty(M, N, dtype=dtype, device="cuda")
+    b.lora_backward_into(X.cuda(), dX, W.t().contiguous().cuda(), torch.zeros(1, N, 4, dtype=dtype, device="cuda"),
+                         torch.zeros(1, 4, K, dtype=dtype, device="cuda"), ids, torch.zeros(M, 4, device="cuda"), dX=dX)
+    same_kinds(dX, product(X, W))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M", [3, 16, 70, 1500])
+def test_infinities_of_the_rank_side_are_those_of_the_formula(M, dtype):
+    """An infinity in X reaches H and, through it, Y; one in dY reaches the gradients."""
+    b, K, N, R = binding(), 72, 136, 4
+    X, A, B, dY = few_bits(M, K, 1), few_bits(K, R, 2), few_bits(R, N, 3), few_bits(M, N, 4)
+    W = torch.zeros(K, N)
+    X[1, 3], dY[2, 7] = INF, -INF
+    W[3] = torch.where((product(product(X[1:2], A), B)[0]) > 0, 1.0, -1.0)   # (no inf - inf by W)
+    X, A, B, dY, W = (t.to(dtype) for t in (X, A, B, dY, W))
+    ids = torch.zeros(M, dtype=torch.int32, device="cuda")
+    H = torch.empty(M, R, device="cuda")
+    Y = b.lora_into(X.cuda(), W.cuda(), A[None].cuda(), B[None].cuda(), ids,
+                    torch.empty(M, N, dtype=dtype, device="cuda"), H=H)
+    h = product(X, A)
+    same_kinds(H, h)
+    same_kinds(Y, product(X, W) + product(h, B))
+    dX, dA, dB = (torch.empty(*s, dtype=dtype, device="cuda") for s in ((M, K), (1, K, R), (1, R, N)))
+    H = few_bits(M, R, 5)
+    x = X.nan_to_num(0, 0, 0)
+    b.lora_backward_into(dY.cuda(), x.cuda(), torch.zeros_like(W).cuda(), A[None].cuda(), B[None].cuda(), ids, H.cuda(),
+                         dX=dX, dA=dA, dB=dB)
+    G = product(dY, B.t())
+    ref = product(dY, torch.zeros(N, K)) + product(G, A.t())
+    same_kinds(dX, ref)
+    same_kinds(dA[0], product(x.t(), G))
+    same_kinds(dB[0], product(H.t(), dY))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M", [1, 70, 700])
+def test_infinities_of_a_weight_gradient_are_those_of_the_formula(M, dtype):
+    b, K, N = binding(), 72, 136
+    x, dY = few_bits(M, K, 1), few_bits(M, N, 2)
+    dY[0, 3], dY[M // 2, 5], dY[M - 1, 7] = INF, -INF, NAN
+    dY = dY.to(dtype)
+    q, e = b.act8_store_into(x.cuda(), *b.act8_empty(M, K))
+    dW = b.act8_weight_grad_into(q, e, dY.cuda(), torch.empty(K, N, dtype=dtype, device="cuda"))
+    same_kinds(dW, product(x.t(), dY))
