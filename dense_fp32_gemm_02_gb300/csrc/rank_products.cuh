@@ -67,7 +67,7 @@ __device__ __forceinline__ void fill16(T *to, const T *p, int n, bool wide) {
 #pragma unroll
         for (int d = 0; d < PER; ++d) sg::cp_async4(shared_address(to + d), d < n ? p + d : p, d < n ? 4u : 0u);
     } else {
-        T x[PER];
+        alignas(16) T x[PER];
 #pragma unroll
         for (int d = 0; d < PER; ++d) x[d] = d < n ? p[d] : T(0.0f);
         *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(x);
@@ -252,7 +252,7 @@ __device__ __forceinline__ void stack_tile(const StackWork<X> &w, int bx, int by
                 if (w.wide) {
                     sg::cp_async16(shared_address(to), in ? p : x.q, uint32_t(count));
                 } else {
-                    E b[PER];
+                    alignas(16) E b[PER];
 #pragma unroll
                     for (int d = 0; d < PER; ++d) b[d] = d < count ? p[d] : E(0);
                     *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(b);

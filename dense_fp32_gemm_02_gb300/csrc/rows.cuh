@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(RANK_THREADS, stream_blocks(MR))
     auto load = [&](int k) {   // 16 bytes of row k0 + k of W, zero past its end
         const T *p = W + (k0 + k) * ldw;
         if (WIDE && column(PER - 1) < w.N) return *reinterpret_cast<const uint4 *>(p + column(0));
-        T v[PER];
+        alignas(16) T v[PER];
 #pragma unroll
         for (int e = 0; e < PER; ++e) v[e] = column(e) < w.N ? p[column(e)] : T(0.0f);
         return *reinterpret_cast<const uint4 *>(v);

@@ -54,3 +54,21 @@ def test_the_kernels_are_found():
 @pytest.mark.parametrize("kernel", KERNELS)
 def test_every_kernel_checks_its_indices(kernel):
     assert checks(kernel), f"{kernel} asks SG_IN_RANGE about nothing"
+
+
+def test_local_arrays_read_as_vectors_are_aligned():
+    """A local array that is read or written through a vector pointer has the vector's alignment
+    (in registers it makes no difference, in local memory it would)."""
+    size = {"uint2": 8, "uint4": 16, "float2": 8, "float4": 16}
+    seen = 0
+    for name in FILES:
+        with open(os.path.join(CSRC, name)) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        for m in re.finditer(r"reinterpret_cast<(?:const )?(\w+) \*>\((\w+)\)", text):
+            vector, array = m.group(1), m.group(2)
+            local = list(re.finditer(rf"(alignas\((\d+)\) )?\b(?:T|E|float|bf16|uint32_t|signed char) {array}\[", text[:m.start()]))
+            if vector not in size or not local:
+                continue
+            seen += 1
+            assert int(local[-1].group(2) or 0) >= size[vector], f"{name}: {array} as {vector}"
+    assert seen >= 3
