@@ -350,6 +350,13 @@ def _layer_type(names, *tensors):
     raise ValueError(", ".join(names) + " must be on one device")
 
 
+def _missing(names, *tensors):
+    """TypeError for the first of these that is None."""
+    for name, t in zip(names, tensors):
+        if t is None:
+            raise TypeError(f"{name} must be a CUDA tensor, not None")
+
+
 def _typed(name, t, dtype, device):
     """TypeError / ValueError unless t is a tensor of this type on CUDA device number `device`."""
     try:
@@ -440,6 +447,8 @@ def _adapters(A, B, ids, M, scale, ranks, device):
         raise ValueError(f"the adapters' rank must be 1 to 128, got {R}")
     if L > 1024:
         raise ValueError(f"at most 1024 adapters, got {L}")
+    if ids is None and L > 0:
+        _missing(("ids",), ids)
     return (L, R, _vector("ids", ids, torch.int32, M, device),
             _vector("ranks", ranks, torch.int32, L, device),
             _vector("scale", scale, torch.float32, L, device))
@@ -467,6 +476,8 @@ def lora_into(X, W, A, B, ids, Y, scale=None, ranks=None, bias=None, H=None, str
     where given, receives X[i]@A[a] for lora_backward_into().  Asynchronous on `stream`
     (default: torch's current stream)."""
     kind, device = _layer_type(("X", "W", "A", "B", "Y", "bias"), X, W, A, B, Y, bias)
+    if W is None or A is None or B is None or Y is None:
+        _missing(("W", "A", "B", "Y"), W, A, B, Y)
     if X.dim() != 2 or W.dim() != 2:
         raise ValueError("X and W must be 2-D")
     (M, K), N = X.shape, W.shape[1]
@@ -488,17 +499,22 @@ def lora_backward_into(dY, X, W, A, B, ids, H, dX=None, dA=None, dB=None, scale=
 
     X is the forward call's input or the pair (q, e) that act8_store_into() kept of it;
     H what the forward call wrote.  dX (M, K) may be None, and dA (L, K, R) and
-    dB (L, R, N) may be None together.  Returns (dX, dA, dB)."""
+    dB (L, R, N) may be None together; X and H may then be None too.  Returns (dX, dA, dB)."""
     kept = isinstance(X, tuple)
     kind, device = _layer_type(("dY", "X", "W", "A", "B", "dX", "dA", "dB"), dY, None if kept else X,
                                W, A, B, dX, dA, dB)
+    if W is None or A is None or B is None:
+        _missing(("W", "A", "B"), W, A, B)
     if (dA is None) != (dB is None):
         raise ValueError("dA and dB must be given together")
+    if dA is not None and (X is None or H is None):   # (dX needs neither)
+        _missing(("X", "H"), X, H)
     if dY.dim() != 2 or W.dim() != 2:
         raise ValueError("dY and W must be 2-D")
     M, (K, N) = dY.shape[0], W.shape
     L, R, ids_p, ranks_p, scale_p = _adapters(A, B, ids, M, scale, ranks, device)
-    _typed("H", H, torch.float32, device)
+    if H is not None:
+        _typed("H", H, torch.float32, device)
     x = (None, 0, *_checkpoint(*X, M, K, device)) if kept else (*_matrix("X", X, M, K), None, 0, None, 0)
     _call(device, stream, lib.sgemm_lora_backward, kind, M, N, K, L, R, *_matrix("dY", dY, M, N), *x,
           *_matrix("W", W, K, N), *_stack("A", A, L, K, R), *_stack("B", B, L, R, N), ids_p, ranks_p,
@@ -555,6 +571,8 @@ def act8_grad_into(q, e, dY, dZ, act: str = "none", stream=None):
     """dZ <- dY * act'(z), z the values of the checkpoint (q, e) of the activation's
     input (dZ may be dY)."""
     kind, device = _layer_type(("dY", "dZ"), dY, dZ)
+    if dZ is None:
+        _missing(("dZ",), dZ)
     number = _act_number(act)
     M, K = _sizes("dY", dY)
     _call(device, stream, lib.sgemm_act8_grad, kind, M, K, *_checkpoint(q, e, M, K, device), number,
@@ -566,6 +584,8 @@ def act8_weight_grad_into(q, e, dY, dW, beta: float = 0.0, stream=None):
     """dW <- x.T@dY + beta*dW, x (M, K) the values of the checkpoint (q, e) of a layer's
     input, dY (M, N), dW (K, N)."""
     kind, device = _layer_type(("dY", "dW"), dY, dW)
+    if dW is None:
+        _missing(("dW",), dW)
     (M, N), K = _sizes("dY", dY), _sizes("dW", dW)[0]
     _call(device, stream, lib.sgemm_act8_weight_grad, kind, M, N, K,
           *_checkpoint(q, e, M, K, device), *_matrix("dY", dY, M, N), float(beta),
