@@ -527,7 +527,8 @@ def act8_empty(M: int, K: int, device=None):
     """A checkpoint's two tensors for an M x K matrix: q (M, K) and e (M, ceil(K/32)), int8."""
     if torch is None:
         _import_torch()
-    device = device or torch.device("cuda", torch.cuda.current_device())
+    if device is None:
+        device = torch.device("cuda", torch.cuda.current_device())
     return (torch.empty((M, K), dtype=torch.int8, device=device),
             torch.empty((M, -(-K // ACT8_BLOCK)), dtype=torch.int8, device=device))
 
@@ -597,7 +598,8 @@ def act8_weight_grad_into(q, e, dY, dW, beta: float = 0.0, stream=None):
 def device_status(stream=None, device=None) -> int:
     """Synchronise and read/clear the device error word: 0 or SGEMM_ERR_TIMEOUT."""
     import torch
-    device = device or torch.device("cuda", torch.cuda.current_device())
+    if device is None:
+        device = torch.device("cuda", torch.cuda.current_device())
     with torch.cuda.device(device):
         return lib.sgemm_device_status(_stream_handle(stream, device))
 
@@ -608,7 +610,8 @@ def set_wait_timeout_ns(ns: int) -> None:
 
 def selftest_wait_timeout(ns: int, stream=None, device=None) -> int:
     import torch
-    device = device or torch.device("cuda", torch.cuda.current_device())
+    if device is None:
+        device = torch.device("cuda", torch.cuda.current_device())
     with torch.cuda.device(device):
         return lib.sgemm_selftest_wait_timeout(int(ns), _stream_handle(stream, device))
 
