@@ -345,7 +345,7 @@ def run_oracle_table(args):
             g, rows, secs = time_oracle_rows(w, A, B, C, row_budget_s=args.oracle_budget,
                                              first=max(1, min(16, threads)), threads=threads)
             table.append({"workload": name, "threads": threads, "gflops": round(g, 3),
-                          "rows": rows, "secs": round(secs, 3),
+                          "rows": rows, "secs": round(secs, 6),
                           "full_oracle_s": round(w.flops / (g * 1e9), 1)})
         del A, B, C
     print(json.dumps({"oracle_table": table, "unit": "GFLOP/s", "kind": "oracle",
