@@ -41,9 +41,19 @@ cudaError_t parts_gemm_error_word(unsigned *v, bool clear);
 constexpr int kMaxDim = 0x7fffffff - 0xffff;
 
 // A launch that need not wait for the kernel before it on the stream (programmatic stream
-// serialization): its blocks start when that one's have all begun and made way, and the
-// kernel itself waits for that one's end (sg::wait_prerequisites) before it reads or
-// writes memory.  It saves the launch's latency between two kernels.
+// serialization): its blocks start once every block of that one has called
+// sg::launch_dependents() or ended, and sg::wait_prerequisites() waits for that one's end.  It
+// saves the launch's latency between two kernels.  What makes it safe:
+//  1. The first kernel of a call is launched plainly, or waits before it calls
+//     launch_dependents().  So all work enqueued before the call has ended when its second kernel
+//     starts, and a later kernel may at once read the caller's inputs and write workspace that no
+//     kernel of this call has used yet.  (A call to launch_dependents() above that wait would be a
+//     race with the call before.)
+//  2. What another kernel of the call writes, or still reads, is touched after the wait only.
+//  3. A kernel whose blocks do not all wait has its first block wait at the end: its own end then
+//     says that the kernels before it have ended, which is what the next one's wait relies on.
+// Kernels that make use of 1: parts_kernel beside the grouping, few_rows_rank_kernel beside the
+// product, and few_rows_finish_kernel, which reads ids, B and bias before its wait.
 template <class... P, class... Args>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
                          const Args &...args) {

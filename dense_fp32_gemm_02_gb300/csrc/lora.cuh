@@ -120,7 +120,7 @@ __device__ __forceinline__ void take_parts(const PartsJob<X> &job, long long t, 
 }
 
 // The parts of the product's operands that the TMA cannot read in place.  `beside`: the
-// kernel before it groups the rows, and need only have ended when this one ends.
+// kernel before it groups the rows, and need only have ended when this one ends (host_state.h).
 template <int P_PARTS, int Q_PARTS, class XP, class XQ>
 __global__ void __launch_bounds__(256) parts_kernel(PartsJob<XP> p, PartsJob<XQ> q, bool beside) {
     if (!beside) sg::wait_prerequisites();

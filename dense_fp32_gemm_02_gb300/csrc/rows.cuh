@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(RANK_THREADS)
     few_rows_rank_kernel(RowsWork w, Rows<T> X, Stack<const T> V, Adapters ad) {
     __shared__ float sums[RANK_SUMS];
     sg::launch_dependents();
-    rank_of_row(w, int(blockIdx.x), X, V, ad, sums);
+    rank_of_row(w, int(blockIdx.x), X, V, ad, sums);   // (inputs, and workspace of its own: host_state.h)
     if (blockIdx.x == 0) sg::wait_prerequisites();   // this kernel's end is also that of the product's
 }
 

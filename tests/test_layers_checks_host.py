@@ -72,3 +72,20 @@ def test_local_arrays_read_as_vectors_are_aligned():
             seen += 1
             assert int(local[-1].group(2) or 0) >= size[vector], f"{name}: {array} as {vector}"
     assert seen >= 3
+
+
+def test_early_kernels_wait_before_they_let_the_next_one_start():
+    """A call's first kernel may let the second start only when all earlier work has ended, that
+    is behind its own wait.  The others: launched plainly (so that wait is the launch's), or never
+    first in a call."""
+    plain, never_first = {"stream_rows_kernel", "few_rows_kernel"}, {"few_rows_rank_kernel"}
+    for name in KERNELS:
+        body = FUNCTIONS[name][1]
+        wait, let = body.find("wait_prerequisites()"), body.find("launch_dependents()")
+        if let >= 0 and name not in plain | never_first:
+            assert 0 <= wait < let, name
+    with open(os.path.join(CSRC, "lora.cu")) as f:
+        text = f.read()
+    for name in ("stream", "kernel"):     # what forward_few_rows calls those two
+        assert re.search(rf"\b{name}<<<", text)
+    assert "launch_early(stream" not in text and "launch_early(kernel" not in text.replace("launch_early(kernel, grid", "")
