@@ -523,9 +523,11 @@ int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
 
 // Few rows: the rank side row by row (M rank (K + N) elements of the stack from L2, and
 // partial sums of all of Y) against grouping it by adapter (four launches more, about 20
-// us).  us, row by row / grouped, bfloat16: 256 x 4096 x 4096 of rank 16 35 / 49, 512 rows
-// 73 / 48; 512 x 1024 x 1024 of rank 64 23 / 33, 1024 rows 47 / 34; 1280 x 768 x 768 of
-// rank 16 27 / 27; 1000 x 512 x 512 of rank 16 15 / 24.
+// us).  Both types cross over at the same rows, within what the rule gives away.  us, row by row /
+// grouped, 8 adapters at random, bfloat16 and float32: 4096 x 4096 of rank 16, 128 rows 27 / 44 and
+// 79 / 98, 256 rows 36 / 48 and 92 / 104, 512 rows 68 / 50 and 146 / 142; 1024 x 1024 of rank 64,
+// 512 rows 26 / 40 and 42 / 50, 768 rows 37 / 44 and 53 / 55, 1000 rows 45 / 44 and 63 / 58; 768 x
+// 768 of rank 16, 1280 rows 30 / 32 and 39 / 46; 512 x 512, 1280 rows 19 / 30 and 29 / 38.
 bool few_rows(const Call &c) {
     if (c.K == 0 || c.N == 0) return false;
     if (c.M <= STREAM_ROWS) return true;
