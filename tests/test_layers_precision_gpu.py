@@ -96,3 +96,26 @@ def test_the_rank_sides_gradients_keep_fp32(M, dtype):
     assert bool((dX[0] == 1).all()) and bool((dX[1] == 0).all())
     assert bool((dA[0, :, 0] == 1).all()) and bool((dA[0, :, 1] == 0).all())
     assert bool((dB[0, 0, 5] == 1).all()) and bool((dB[0, 1] == 0).all())
+
+
+@pytest.mark.parametrize("K", [128, 131])     # rows read 16 bytes at a time, and of any alignment
+def test_gelu_keeps_the_relative_accuracy_of_small_values(K):
+    """float32 at z from -8 to 0, where Phi falls to 6e-16.  Relative: exp(-z^2/2) is off by the
+    roundings of its exponent, 2^-23 z^2/2 (6e-8 z^2), and by 2e-7 of its own; the tail over it by
+    6e-7; products and sums by 2^-24 each: under 2e-6 + 6e-8 z^2.  The slope below -3 is a difference
+    of which the smaller part is a ninth at most: a quarter more."""
+    b = binding()
+    z = -(torch.arange(64 * K, device="cuda") % 128).view(64, K).float() / 16      # kept exactly
+    z[:, ::32] = -127 / 16
+    y = torch.empty_like(z)
+    q, e = b.act8_store_into(z, *b.act8_empty(64, K), act="gelu", Y=y)
+    assert torch.equal(b.act8_load_into(q, e, torch.empty_like(z)), z)
+    slope = b.act8_grad_into(q, e, torch.ones_like(z), torch.empty_like(z), act="gelu").double()
+    z = z.double()
+    cdf, bell = 0.5 * torch.erfc(-z / 2 ** 0.5), torch.exp(-z * z / 2) / (2 * torch.pi) ** 0.5
+    limit = 2e-6 + 6e-8 * z * z
+    assert bool(((y.double() - z * cdf).abs() <= limit * (z * cdf).abs()).all())
+    ref = cdf + z * bell
+    low = z < -3
+    assert bool(((slope - ref).abs() <= 1.25 * limit * ref.abs())[low].all())
+    assert float((slope - ref).abs().max()) <= 4e-7
