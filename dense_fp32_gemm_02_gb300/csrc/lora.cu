@@ -600,16 +600,23 @@ SGEMM_API int sgemm_lora(int type, int M, int N, int K, int L, int R, const void
     c.stream = reinterpret_cast<cudaStream_t>(stream);
     const int st = check_common(c);
     if (st != SGEMM_OK) return st;
-    if (M == 0 || (N == 0 && (!H || L == 0))) return SGEMM_OK;
+    if (M == 0 || (N == 0 && !H)) return SGEMM_OK;
     const size_t size = element_bytes(type);
     if ((K > 0 && bad_matrix(X, ldx, K, size)) ||
         (K > 0 && N > 0 && bad_matrix(W, ldw, N, size)) || (N > 0 && bad_matrix(Y, ldy, N, size)) ||
         !aligned(bias, size))
         return SGEMM_ERR_INVALID_ARG;
     if (L > 0 && (bad_stack(A, lda, stride_a, L, K, R, size) ||
-                  bad_stack(B, ldb, stride_b, L, R, N, size) || (H && bad_matrix(H, ldh, R, 4))))
+                  bad_stack(B, ldb, stride_b, L, R, N, size)))
         return SGEMM_ERR_INVALID_ARG;
-    if (L == 0) c.H = nullptr;
+    if (H && R > 0 && bad_matrix(H, ldh, R, 4)) return SGEMM_ERR_INVALID_ARG;
+    if (L == 0 && H) {   // no row has an adapter
+        const cudaError_t e = R <= 0 ? cudaSuccess
+                                     : cudaMemset2DAsync(H, size_t(ldh) * 4, 0, size_t(R) * 4, size_t(M), c.stream);
+        if (e != cudaSuccess) return sgh::cuda_fail(e);
+        c.H = nullptr;
+        if (N == 0) return SGEMM_OK;
+    }
     return type == SGEMM_BF16 ? forward<bf16>(c) : forward<float>(c);
 }
 

@@ -63,7 +63,8 @@ typedef enum {
  * bias: N elements of `type`, or NULL.  H (row pitch ldh >= R), where it is not
  * NULL, receives X * A_a for the backward pass: zero in the columns past an
  * adapter's rank and in rows without one.  Y must not overlap an input.
- * M == 0 or N == 0 leaves Y alone (H is still written where M > 0).
+ * M == 0 or N == 0 leaves Y alone (H is still written where M > 0, by zeros where
+ * L == 0).
  */
 int sgemm_lora(int type, int M, int N, int K, int L, int R,
                const void *X, int ldx,

@@ -74,3 +74,18 @@ def test_the_device_of_an_empty_checkpoint():
     for device in (None, 0, "cuda:0", torch.device("cuda", 0)):
         assert all(t.device == torch.device("cuda", 0) for t in b.act8_empty(3, 40, device))
     assert all(t.device.type == "cpu" for t in b.act8_empty(3, 40, "cpu"))
+
+
+@pytest.mark.parametrize("rows", [1, 5, 40, 300, 1500])
+@pytest.mark.parametrize("cols", [96, 0])
+def test_h_of_an_empty_stack_is_zero(rows, cols):
+    """Every row is one without an adapter; what lies beside H's columns is left alone."""
+    b = binding()
+    X, W = torch.randn(rows, K, device="cuda"), torch.randn(K, cols, device="cuda")
+    Y = torch.empty(rows, cols, device="cuda")
+    H = torch.full((rows, R + 3), 7.0, device="cuda")
+    b.lora_into(X, W, X.new_empty(0, K, R), X.new_empty(0, R, cols), None, Y, H=H[:, :R])
+    assert bool((H[:, :R] == 0).all()) and bool((H[:, R:] == 7).all())
+    plain = torch.empty_like(Y)
+    b.lora_into(X, W, X.new_empty(0, K, R), X.new_empty(0, R, cols), None, plain)
+    assert torch.equal(Y, plain) and b.device_status() == b.SGEMM_OK
