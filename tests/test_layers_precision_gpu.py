@@ -119,3 +119,36 @@ def test_gelu_keeps_the_relative_accuracy_of_small_values(K):
     low = z < -3
     assert bool(((slope - ref).abs() <= 1.25 * limit * ref.abs())[low].all())
     assert float((slope - ref).abs().max()) <= 4e-7
+
+
+@pytest.mark.parametrize("R", [16, 128])
+def test_adapters_beside_a_long_contraction(R):
+    """The rank side's slabs come after those of a contraction that is added up in chunks.  A
+    result is within half a bfloat16 spacing (2^-8) of a sum that is off by at most 3.3e-5 of its
+    terms' magnitudes (the contraction) and 2^-23 of each of the R terms beside it."""
+    b, M, LONG, SHORT, L = binding(), 4096, 8320, 2560, 3
+    g = torch.Generator(device="cuda")
+    g.manual_seed(R)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF16)   # noqa: E731
+    ids = torch.randint(-1, L, (M,), generator=g, device="cuda", dtype=torch.int32)
+    some = slice(0, SHORT, 20)
+
+    def check(got, x, w, v1, v2):     # got = x w + (x v1) v2 of the row's adapter
+        ref, mag = x.double() @ w[:, some].double(), x.double().abs() @ w[:, some].double().abs()
+        for a in range(L):
+            mine = (ids == a).double().unsqueeze(1)
+            s = mine * (x.double() @ v1[a].double())
+            ref += s @ v2[a][:, some].double()
+            mag += (mine * (x.double().abs() @ v1[a].double().abs())) @ v2[a][:, some].double().abs() * R * 2.0 ** -8
+        err = (got[:, some].double() - ref).abs()
+        limit = 3.3e-5 * mag
+        assert bool((err <= 2.0 ** -8 * (ref.abs() + limit) + limit).all())
+
+    X, W, A, B = r(M, LONG), r(LONG, SHORT), r(L, LONG, R), r(L, R, SHORT)
+    Y = b.lora_into(X, W, A, B, ids, torch.empty(M, SHORT, dtype=BF16, device="cuda"))
+    check(Y, X, W, A, B)
+    dX = torch.empty(M, SHORT, dtype=BF16, device="cuda")
+    A, B, W = A.transpose(1, 2).contiguous(), B.transpose(1, 2).contiguous(), W.t().contiguous()
+    b.lora_backward_into(X, dX, W, B, A, ids, torch.zeros(M, R, device="cuda"), dX=dX)
+    check(dX, X, W.t(), A.transpose(1, 2), B.transpose(1, 2))
+    assert b.device_status() == b.SGEMM_OK
