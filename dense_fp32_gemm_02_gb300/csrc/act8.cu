@@ -32,7 +32,7 @@ constexpr int kThreads = 256;
 // float32: tail / bell = (1 - v) Q(v) with v = 0.3 |z| / (1 + 0.3 |z|), Q of degree 9 fitted to the
 // least relative error over |z| <= 14 (3.5e-9; with fp32's roundings 5e-7 of the tail, 4e-8 of 1).
 // In v, not 1 - v, because then no rounding at z = 0 is magnified.  Against 64 bits GELU's
-// gradient is 4.2e-8 off (2-norm; by 7.1.26 9.3e-8, by erff and expf 3.7e-8 but 199 us for 174 at
+// gradient is 3.9e-8 off (2-norm; by 7.1.26 9.3e-8, by erff and expf 3.7e-8 but 199 us for 173 at
 // 8192 x 16384), and small values at negative z keep their relative accuracy.
 //
 // Two elements at a time, and the approximate reciprocal alone for a division: GELU over 8192 x
@@ -136,7 +136,7 @@ struct Checkpoint {
 // Wide form, for rows that are 16-byte aligned and of a multiple of 8 columns: a quarter
 // of a block to a thread, its maximum over four lanes; so many blocks to a thread, all
 // loaded before the first is used.  At 8192 x 16384, us (GB/s over the bytes of either
-// side): bfloat16 store 68, with GELU 113 (5980), GELU gradient 112 (6030), load 67
+// side): bfloat16 store 68, with GELU 115 (5870), GELU gradient 111 (6080), load 67
 // (6080); float32 with GELU 174 (6940), gradient 173.  What is left is issue slots: storing
 // with half the depth 119, the gradient with two blocks to a thread 129, with four 151;
 // reading back with one 72.

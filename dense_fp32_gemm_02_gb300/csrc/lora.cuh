@@ -34,7 +34,8 @@ struct Act8Rows {
 
 // ------------------------------------------------------------------ parts
 // x as a sum of up to three bfloat16, each the leading 8 bits of what the ones before
-// leave (cut, not rounded: x = x0 + x1 + x2 exactly, and no part overflows).  What is
+// leave (cut, not rounded: x = x0 + x1 + x2 exactly, and no part overflows; below 2^-110 what
+// lies under 2^-133, the least bfloat16, is lost).  What is
 // not finite stays in the last, which a product of parts takes with the other side's first alone:
 // infinity times a part that is zero only because the number has few bits would be NaN.  (The
 // first is then 1 of its sign, for infinity times infinity.)

@@ -8,14 +8,18 @@
  * Conventions of every entry point here:
  *  - `type` is the element type of the activations, weights and gradients
  *    (sgemm_type); all of a call's matrices have it unless a parameter says
- *    otherwise.  Sums are fp32 or better and each output is rounded once.
+ *    otherwise.  Sums are fp32 and each output is rounded once.  (The tensor
+ *    cores truncate where they add: bfloat16 sums of up to 8192 terms, which
+ *    stays under 3e-5 of the terms' magnitudes, and float32 sums of up to 512;
+ *    what is longer is added to nearest.)
  *  - Matrices are row-major with a leading dimension in elements, at least
  *    max(1, columns).  Pointers must be aligned to their element (16-byte
  *    aligned rows are faster, no more).
  *  - Sizes are at most 2^31 - 65536 (SGEMM_ERR_TOO_LARGE above that).
  *  - Elements of an output outside its rows x columns block are not written.
- *  - Infinities and NaNs give what the formulas give, however many rows there are
- *    (bfloat16's and float32's alike; weights under 2^-96 may count as zero next to an infinity).
+ *  - Infinities and NaNs give what the formulas give, however many rows there
+ *    are.  float32 magnitudes below 2^-110 may count as the next lower multiple
+ *    of 2^-133, and next to an infinity a value under 2^-96 as zero.
  *  - Results are bitwise reproducible from call to call on a GPU model.
  *  - The work is enqueued on `stream`; nothing synchronises the host.  Workspaces come
  *    from the library's stream-ordered pool and go back to it behind the last kernel.
