@@ -56,6 +56,10 @@ lib.sgemm_act8_grad.argtypes = [_i, _i, _i, _p, _i, _p, _i, _i, _p, _i, _p, _i, 
 lib.sgemm_act8_grad.restype = _i
 lib.sgemm_act8_weight_grad.argtypes = [_i, _i, _i, _i, _p, _i, _p, _i, _p, _i, _f, _p, _i, _p]
 lib.sgemm_act8_weight_grad.restype = _i
+lib.sgemm_rmsnorm.argtypes = [_i] * 3 + [_p, _i, _p, _i, _p, _f, _p, _i, _p, _i, _p, _i, _p, _p]
+lib.sgemm_rmsnorm.restype = _i
+lib.sgemm_rmsnorm_backward.argtypes = [_i] * 3 + [_p, _i, _p, _i, _p, _f, _p, _i, _p, _i, _p, _p]
+lib.sgemm_rmsnorm_backward.restype = _i
 lib.sgemm_status_string.argtypes = [_i]
 lib.sgemm_status_string.restype = ctypes.c_char_p
 lib.sgemm_version.argtypes = []
@@ -592,6 +596,60 @@ def act8_weight_grad_into(q, e, dY, dW, beta: float = 0.0, stream=None):
           *_checkpoint(q, e, M, K, device), *_matrix("dY", dY, M, N), float(beta),
           *_matrix("dW", dW, K, N))
     return dW
+
+
+def _eps(eps):
+    eps = float(eps)
+    if not 0.0 <= eps < 3.0e38:
+        raise ValueError(f"eps must be a number >= 0, got {eps}")
+    return eps
+
+
+def _rows8(q, scale, rows, cols, device):
+    """(address, pitch, address) of rows in 8 bits, each with its scale."""
+    _typed("q", q, torch.int8, device)
+    if scale is None:
+        _missing(("scale",), scale)
+    return (*_matrix("q", q, rows, cols), _vector("scale", scale, torch.float32, rows, device))
+
+
+def rmsnorm_into(X, w, Y=None, q=None, scale=None, R=None, S=None, eps: float = 1e-6, stream=None):
+    """The root-mean-square norm of the rows of V = X + R (X where R is None), V in the tensors'
+    type: y = V * w / sqrt(mean(V^2) + eps).  X, R, Y, S (M, K) and w (K,): CUDA float32 or
+    bfloat16, one type.
+
+    S, where given, receives V (the residual stream); Y receives y; q (M, K) int8 and scale (M,)
+    float32, given together, receive y in 8 bits with a scale for each row, for linear8_into().
+    At least one of them.  S and Y may be X or R, not each other.  Returns (S, Y, q, scale)."""
+    kind, device = _layer_type(("X", "w", "R", "S", "Y"), X, w, R, S, Y)
+    if w is None:
+        _missing(("w",), w)
+    if S is None and Y is None and q is None:
+        raise ValueError("rmsnorm_into needs an output: S, Y or (q, scale)")
+    if (q is None) != (scale is None):
+        raise ValueError("q and scale must be given together")
+    M, K = _sizes("X", X)
+    _call(device, stream, lib.sgemm_rmsnorm, kind, M, K, *_matrix("X", X, M, K), *_matrix("R", R, M, K),
+          _vector("w", w, X.dtype, K, device), _eps(eps), *_matrix("S", S, M, K), *_matrix("Y", Y, M, K),
+          *(_rows8(q, scale, M, K, device) if q is not None else (None, 0, None)))
+    return S, Y, q, scale
+
+
+def rmsnorm_backward_into(dY, V, w, dX, dw=None, dS=None, eps: float = 1e-6, stream=None):
+    """Gradients of rmsnorm_into()'s y for dY (M, K), V being the sum that it took the norm of:
+    with n = V / sqrt(mean(V^2) + eps) and g = dY*w, dX <- dS + (g - n*mean(g*n)) / sqrt(mean(V^2) +
+    eps) and dw <- sum over the rows of dY*n.
+
+    dX (M, K) is the gradient of X and of R alike; dS (M, K) or None (0), the gradient that reaches V
+    along the residual stream.  dX may be dY, dS or V.  dw (K,) may be None.  Returns (dX, dw)."""
+    kind, device = _layer_type(("dY", "V", "w", "dX", "dw", "dS"), dY, V, w, dX, dw, dS)
+    if V is None or w is None or dX is None:
+        _missing(("V", "w", "dX"), V, w, dX)
+    M, K = _sizes("dY", dY)
+    _call(device, stream, lib.sgemm_rmsnorm_backward, kind, M, K, *_matrix("dY", dY, M, K), *_matrix("V", V, M, K),
+          _vector("w", w, dY.dtype, K, device), _eps(eps), *_matrix("dS", dS, M, K), *_matrix("dX", dX, M, K),
+          _vector("dw", dw, dY.dtype, K, device))
+    return dX, dw
 
 
 # ------------------------------------------------------------------ control

@@ -31,11 +31,12 @@ void count_launch(const char *main_kernel = nullptr);
 // The limit of in-kernel waits (sgemm_set_wait_timeout_ns).
 unsigned long long wait_timeout_ns();
 
-// Reads, and clears where asked, the copies of the device error word of act8.cu, lora.cu and
-// parts_gemm.cu.
+// Reads, and clears where asked, the copies of the device error word of act8.cu, lora.cu,
+// parts_gemm.cu and the units beside them.
 cudaError_t act8_error_word(unsigned *v, bool clear);
 cudaError_t lora_error_word(unsigned *v, bool clear);
 cudaError_t parts_gemm_error_word(unsigned *v, bool clear);
+cudaError_t norm_error_word(unsigned *v, bool clear);
 
 // Largest size that an entry point accepts.
 constexpr int kMaxDim = 0x7fffffff - 0xffff;

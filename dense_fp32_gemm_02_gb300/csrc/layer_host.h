@@ -1,0 +1,59 @@
+// layer_host.h -- argument checks and launches that the units of the layer's entry points share.
+#pragma once
+
+#include <algorithm>
+
+#include "../../include/sgemm_layers.h"
+#include "host_state.h"
+
+namespace sgh {
+
+inline bool aligned(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+// A matrix that an entry point refuses: none, not aligned to its elements, or with overlapping rows.
+inline bool bad_matrix(const void *p, int ld, int columns, size_t element) {
+    return !p || !aligned(p, element) || ld < std::max(1, columns);
+}
+// The same of one that may be left out, and of vectors.
+inline bool bad_optional(const void *p, int ld, int columns, size_t element) {
+    return p && bad_matrix(p, ld, columns, element);
+}
+inline bool bad_vector(const void *p, size_t element) { return !p || !aligned(p, element); }
+
+inline size_t element_bytes(int type) { return type == SGEMM_BF16 ? 2 : 4; }
+
+inline int check_sizes(int type, std::initializer_list<int> sizes) {
+    if (type != SGEMM_F32 && type != SGEMM_BF16) return SGEMM_ERR_INVALID_ARG;
+    for (int n : sizes)
+        if (n < 0) return SGEMM_ERR_INVALID_ARG;
+    for (int n : sizes)
+        if (n > kMaxDim) return SGEMM_ERR_TOO_LARGE;
+    return SGEMM_OK;
+}
+
+// Rows that can be read or written 16 bytes at a time (or that there are none of).
+template <class T>
+bool wide_rows(const T *p, long long ld) {
+    return !p || (aligned(p, 16) && ld % (16 / (long long)sizeof(T)) == 0);
+}
+
+// Counts a launch just made and returns its error.
+inline int launched(const char *main_kernel = nullptr) {
+    count_launch(main_kernel);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? SGEMM_OK : cuda_fail(e);
+}
+
+// An early launch (host_state.h), counted.
+template <class... P, class... Args>
+int launch(const char *text, void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+           const Args &...args) {
+    const cudaError_t e = launch_early(kernel, grid, threads, smem, stream, args...);
+    return e == cudaSuccess ? launched(text) : cuda_fail(e);
+}
+
+// Rows in 8 bits, each with a scale (norm.cu): q and scale of the rows of X.
+int rows8(int type, int M, int K, const void *X, int ldx, signed char *q, long long ldq, float *scale, int sms,
+          cudaStream_t stream);
+
+}  // namespace sgh

@@ -1,0 +1,476 @@
+// norm.cuh -- kernels of the root-mean-square norm and of rows in 8 bits.
+//
+//   v = x + r, held in the call's type;   y_j = v_j rstd w_j,  rstd = 1 / sqrt(mean(v^2) + eps)
+//   8 bits: scale = max|y| / 127,  q_j = rint(y_j / scale) = rint(127 p_j / max|p|),  p = v w
+//
+// q does not depend on rstd, so the row's sum of squares and its largest |p| are taken together in
+// one pass, and q is the exactly rounded quotient whatever order the sum is taken in: 127 p / max is
+// worked out in fp32 (at most 4 roundings, 3.1e-5 in q's units), and where that is within NEAR = 2^-14
+// of a tie the products are compared in 64 bits, where p (16 bits from bfloat16, 48 from float32) is
+// exact.  For this the maximum of float32 products is kept as a pair (value, remainder).
+//
+// A row goes to a group of threads (a warp or a block) that keeps it in registers between its
+// two uses, up to 16384 columns; longer rows are read twice (LONG).  Everything is read and
+// written once, and the kernels are bound by that.
+#pragma once
+
+#include "act8.cuh"
+#include "kernels.cuh"
+
+namespace sgl {
+
+constexpr float NEAR = 0x1p-14f;
+// The range of the largest |p| in which fp32 products and 127 / max lose nothing; rows outside it
+// are quantised in 64 bits.
+constexpr float LEAST_TOP = 0x1p-60f, MOST_TOP = 0x1p100f;
+// The range of a row's sum of squares in which no term has overflowed or counts for too little.
+constexpr float LEAST_SQUARES = 0x1p-80f, MOST_SQUARES = 0x1p120f;
+
+__host__ __device__ constexpr int norm_block(int threads) { return threads < 256 ? 256 : threads; }
+
+// Where eight elements `c` of thread `t` lie in a row: together (WIDE, rows that are 16-byte
+// aligned and of a multiple of 8 columns), or a group's width apart, next to the other threads'.
+template <int THREADS, bool WIDE>
+struct Place {
+    int K, base, t;
+
+    __device__ int column(int c, int e) const {
+        return base + (WIDE ? (c * THREADS + t) * 8 + e : (c * 8 + e) * THREADS + t);
+    }
+    template <class T>
+    __device__ void load(const T *row, int c, float (&v)[8]) const {
+        if (WIDE) {
+            if (column(c, 0) < K) {
+                load8(row + column(c, 0), v);
+                return;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = column(c, e) < K ? to_f32(row[column(c, e)]) : 0.0f;
+        }
+    }
+    template <class T>
+    __device__ void store(T *row, int c, const float (&v)[8]) const {
+        if (WIDE) {
+            if (column(c, 0) < K) store8(row + column(c, 0), v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (column(c, e) < K) row[column(c, e)] = from_f32<T>(v[e]);
+        }
+    }
+    // Eight integers of at most 127 in magnitude, given as floats.
+    __device__ void store_q(signed char *row, int c, const float (&r)[8]) const {
+        if (WIDE) {
+            if (column(c, 0) < K)
+                *reinterpret_cast<uint2 *>(row + column(c, 0)) = make_uint2(pack_s8(r, 1.0f), pack_s8(r + 4, 1.0f));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (column(c, e) < K) row[column(c, e)] = static_cast<signed char>(__float2int_rn(r[e]));
+        }
+    }
+};
+
+// ------------------------------------------------------------------ a group's sums and maxima
+// A product's magnitude exactly: `hi` its fp32 value, `lo` what that leaves (bfloat16: nothing).
+struct Top {
+    uint32_t hi;   // bits of a magnitude: they order as it does, an infinity or a NaN above all
+    float lo;
+
+    __device__ bool below(const Top &o) const { return hi < o.hi || (hi == o.hi && lo < o.lo); }
+    __device__ float value() const { return __uint_as_float(hi); }
+};
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+    return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+template <bool WITH_LO>
+__device__ __forceinline__ Top warp_top(Top t) {
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, t.hi);
+    if (WITH_LO) t.lo = from_ordered(__reduce_max_sync(0xffffffffu, t.hi == hi ? ordered(t.lo) : 0u));
+    t.hi = hi;
+    return t;
+}
+
+// Two sums and a maximum over a group, the warps' in order.  `turn` alternates from call to
+// call: a warp writes here again only when all have read what it wrote the time before.
+struct GroupSums {
+    float a[2][32], b[2][32], lo[2][32];
+    uint32_t hi[2][32];
+    double wide[32];
+};
+template <int THREADS, bool B, bool TOP, bool WITH_LO>
+__device__ __forceinline__ void group_reduce(GroupSums &sm, int turn, float &a, float &b, Top &top) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    a = warp_sum(a);
+    if (B) b = warp_sum(b);
+    if (TOP) top = warp_top<WITH_LO>(top);
+    if (THREADS == 32) return;
+    if (lane == 0) {
+        sm.a[turn][warp] = a;
+        if (B) sm.b[turn][warp] = b;
+        if (TOP) sm.hi[turn][warp] = top.hi, sm.lo[turn][warp] = top.lo;
+    }
+    __syncthreads();
+    a = b = 0.0f;
+    top = Top{0, 0.0f};
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        a += sm.a[turn][w];
+        if (B) b += sm.b[turn][w];
+        if (TOP) {
+            const Top o{sm.hi[turn][w], sm.lo[turn][w]};
+            if (top.below(o)) top = o;
+        }
+    }
+}
+template <int THREADS>
+__device__ __forceinline__ double group_sum(GroupSums &sm, double v) {
+    v = warp_sum(v);
+    if (THREADS == 32) return v;
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sm.wide[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) all += sm.wide[w];
+    return all;
+}
+template <int THREADS>
+__device__ __forceinline__ double group_max(GroupSums &sm, double v) {   // of magnitudes, NaN the largest
+    auto larger = [](double a, double b) { return a != a || a > b ? a : b; };
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = larger(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if (THREADS == 32) return v;
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sm.wide[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double all = sm.wide[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 32; ++w) all = larger(all, sm.wide[w]);
+    return all;
+}
+
+// ------------------------------------------------------------------ rows out of fp32's range
+// 1 / sqrt(mean(v^2) + eps) in 64 bits, where squares leave fp32's range.  An infinity in v
+// gives 0, a NaN a NaN.
+template <int THREADS, class V>
+__device__ __noinline__ float rare_rstd(GroupSums &sm, V v, int K, float eps, int t) {
+    double ss = 0;
+    for (int j = t; j < K; j += THREADS) ss += double(v(j)) * v(j);
+    return float(1.0 / sqrt(group_sum<THREADS>(sm, ss) / K + eps));
+}
+
+// A row's q and the largest |p| in 64 bits, where products leave fp32's range.
+template <class T, int THREADS, bool WEIGHED, class V>
+__device__ __noinline__ double rare_rows8(GroupSums &sm, V v, const T *w, signed char *q, int K, int t) {
+    double top = 0;
+    bool any = false;   // rows of zeros, padding, need no more than this pass
+    for (int j = t; j < K; j += THREADS) {
+        const float x = v(j), y = WEIGHED ? to_f32(w[j]) : 1.0f;
+        if (x == 0.0f && y - y == 0.0f) continue;
+        any = true;
+        const double p = fabs(double(x) * y);
+        top = p != p || p > top ? p : top;
+    }
+    any = THREADS == 32 ? __any_sync(0xffffffffu, any) : __syncthreads_or(any);
+    if (any) top = group_max<THREADS>(sm, top);
+    const bool keep = any && top > 0 && top <= 1.7e308;   // not zeros, an infinity or a NaN
+    for (int j = t; j < K; j += THREADS) {
+        const double p = keep ? double(v(j)) * (WEIGHED ? to_f32(w[j]) : 1.0f) : 0.0;
+        q[j] = static_cast<signed char>(keep ? __double2int_rn(127.0 * p / top) : 0);
+    }
+    return top;
+}
+
+// q of |p| near a tie: n or n + 1, n the whole part of the fp32 quotient.
+static __device__ __noinline__ float near_tie(float v, float w, float quotient, float top_hi, float top_lo) {
+    const double p = fabs(double(v) * w), top = double(top_hi) + top_lo;
+    const float n = floorf(fabsf(quotient));
+    const double d = fma(127.0, p, -(n + 0.5) * top);
+    const bool up = d > 0 || (d == 0 && fmodf(n, 2.0f) == 1.0f);
+    return copysignf(up ? n + 1.0f : n, quotient);
+}
+
+// ------------------------------------------------------------------ forward
+enum NormKind { NORM, NORM8, ROWS8 };   // y alone; q and, where Y is given, y; q of x itself
+
+template <class T>
+struct NormCall {
+    int M, K;
+    const T *X, *R, *w;
+    T *S, *Y;
+    signed char *q;
+    float *scale;
+    long long ldx, ldr, lds, ldy, ldq;
+    float eps;
+};
+
+template <class T, int KIND, int THREADS, int CHUNKS, bool WIDE, bool LONG>
+__global__ void __launch_bounds__(norm_block(THREADS))
+    norm_kernel(const NormCall<T> a) {
+    constexpr int GROUPS = norm_block(THREADS) / THREADS, SPAN = THREADS * 8 * CHUNKS;
+    constexpr bool EIGHT = KIND != NORM, WITH_LO = EIGHT && KIND != ROWS8 && sizeof(T) == 4;
+    __shared__ GroupSums sm;
+    const int t = threadIdx.x % THREADS;
+    const long long row = (long long)blockIdx.x * GROUPS + threadIdx.x / THREADS;
+    if (row >= a.M || !SG_IN_RANGE(LONG || a.K <= SPAN)) return;
+    const T *x = a.X + row * a.ldx, *r = a.R ? a.R + row * a.ldr : nullptr;
+    T *s = a.S ? a.S + row * a.lds : nullptr, *y = KIND != ROWS8 && a.Y ? a.Y + row * a.ldy : nullptr;
+    signed char *q = EIGHT ? a.q + row * a.ldq : nullptr;
+
+    float v[CHUNKS][8], w[8];
+    auto read = [&](const Place<THREADS, WIDE> &at, bool again) {
+        const T *from = again && s ? s : x;
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) at.load(from, c, v[c]);
+        if constexpr (KIND != ROWS8) {
+            if (!r || (again && s)) return;
+            float u[CHUNKS][8];
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) at.load(r, c, u[c]);
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[c][e] = to_f32(from_f32<T>(v[c][e] + u[c][e]));
+        }
+    };
+
+    float squares = 0.0f, none = 0.0f;
+    Top top{0, 0.0f};
+    for (int base = 0; base < (LONG ? a.K : 1); base += SPAN) {
+        const Place<THREADS, WIDE> at{a.K, base, t};
+        read(at, false);
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+            if (KIND != ROWS8 && s) at.store(s, c, v[c]);
+            if (EIGHT && KIND != ROWS8) at.load(a.w, c, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (KIND != ROWS8) squares = fmaf(v[c][e], v[c][e], squares);
+                if (EIGHT) {
+                    const float p = KIND == ROWS8 ? v[c][e] : v[c][e] * w[e];
+                    Top o{magnitude_bits(p), 0.0f};
+                    if (WITH_LO) {
+                        o.lo = fmaf(v[c][e], w[e], -p);
+                        o.lo = p < 0.0f ? -o.lo : o.lo;
+                        if (top.below(o)) top = o;
+                    } else {
+                        top.hi = max(top.hi, o.hi);
+                    }
+                }
+            }
+        }
+    }
+    group_reduce<THREADS, false, EIGHT, WITH_LO>(sm, 0, squares, none, top);
+
+    auto held = [&](int j) {   // v, from what any thread may have written of it above
+        if (KIND == ROWS8) return to_f32(x[j]);
+        return s ? to_f32(s[j]) : r ? to_f32(from_f32<T>(to_f32(x[j]) + to_f32(r[j]))) : to_f32(x[j]);
+    };
+    if (THREADS == 32) __syncwarp();
+    float rstd = 1.0f;
+    if (KIND != ROWS8) {
+        rstd = 1.0f / sqrtf(squares / float(a.K) + a.eps);
+        if (!(squares <= MOST_SQUARES) || (squares < LEAST_SQUARES && a.eps < 1e-10f)) {
+            rstd = rare_rstd<THREADS>(sm, held, a.K, a.eps, t);
+            if (THREADS > 32) __syncthreads();   // Y, written below, may be X
+        }
+    }
+    float times = 0.0f;    // 127 / max|p|; 0: q is there already
+    if (EIGHT) {
+        float scale;
+        if (top.value() >= LEAST_TOP && top.value() <= MOST_TOP) {
+            times = 127.0f / top.value();
+            scale = (KIND == ROWS8 ? top.value() : top.value() * rstd) / 127.0f;
+        } else {
+            const double all = rare_rows8<T, THREADS, KIND != ROWS8>(sm, held, a.w, q, a.K, t);
+            scale = all <= 1.7e308 ? float(all * rstd / 127.0) : __uint_as_float(0x7fc00000u);
+            if (THREADS > 32) __syncthreads();   // Y, written below, may be X
+        }
+        if (t == 0) a.scale[row] = scale;
+    }
+
+    for (int base = 0; base < (LONG ? a.K : 1); base += SPAN) {
+        const Place<THREADS, WIDE> at{a.K, base, t};
+        if (LONG) read(at, true);
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+            float out[8];
+            if (KIND != ROWS8) at.load(a.w, c, w);
+            if (EIGHT && times != 0.0f) {
+                float off = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float quotient = (KIND == ROWS8 ? v[c][e] : v[c][e] * w[e]) * times;
+                    out[e] = rintf(quotient);
+                    off = fmaxf(off, fabsf(quotient - out[e]));
+                }
+                if (off > 0.5f - NEAR) {   // one of eight: 1 in 1000
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float u = KIND == ROWS8 ? 1.0f : w[e], quotient = v[c][e] * u * times;
+                        if (fabsf(quotient - out[e]) > 0.5f - NEAR)
+                            out[e] = near_tie(v[c][e], u, quotient, top.value(), top.lo);
+                    }
+                }
+                at.store_q(q, c, out);
+            }
+            if (KIND != ROWS8 && y) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) out[e] = v[c][e] * rstd * w[e];
+                at.store(y, c, out);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ backward
+// With n = v rstd, g = dy w and c = sum(g n) / K:  dx = ds + rstd (g - c n),  dw = sum over rows of dy n.
+// A group keeps the sums of dw's columns over its rows, which are `groups` apart; a second
+// kernel adds the groups' (of a block's warps: the block's) in order.
+template <class T>
+struct NormBackCall {
+    int M, K;
+    const T *dY, *V, *w, *dS;
+    T *dX;
+    float *partial;   // blocks x K, or null: no dw
+    long long lddy, ldv, ldds, lddx;
+    float eps;
+};
+
+template <class T, int THREADS, int CHUNKS, bool WIDE, bool LONG>
+__global__ void __launch_bounds__(norm_block(THREADS))
+    norm_backward_kernel(const NormBackCall<T> a) {
+    constexpr int GROUPS = norm_block(THREADS) / THREADS, SPAN = THREADS * 8 * CHUNKS;
+    __shared__ GroupSums sm;
+    __shared__ float columns[GROUPS > 1 ? SPAN : 1];
+    const int t = threadIdx.x % THREADS, group = threadIdx.x / THREADS;
+    if (!SG_IN_RANGE(LONG || a.K <= SPAN)) return;
+    float *partial = a.partial ? a.partial + (long long)blockIdx.x * a.K : nullptr;
+    float v[CHUNKS][8], dy[CHUNKS][8], dw[LONG ? 1 : CHUNKS][8] = {}, w[8];
+    int turn = 0;
+    bool first = true;
+    for (long long row = (long long)blockIdx.x * GROUPS + group; row < a.M; row += (long long)gridDim.x * GROUPS) {
+        const T *vr = a.V + row * a.ldv, *dyr = a.dY + row * a.lddy, *dsr = a.dS ? a.dS + row * a.ldds : nullptr;
+        T *dxr = a.dX + row * a.lddx;
+        auto read = [&](const Place<THREADS, WIDE> &at) {
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) at.load(vr, c, v[c]), at.load(dyr, c, dy[c]);
+        };
+        float squares = 0.0f, gv = 0.0f;
+        Top none{};
+        for (int base = 0; base < (LONG ? a.K : 1); base += SPAN) {
+            const Place<THREADS, WIDE> at{a.K, base, t};
+            read(at);
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) {
+                at.load(a.w, c, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    squares = fmaf(v[c][e], v[c][e], squares);
+                    gv = fmaf(dy[c][e] * w[e], v[c][e], gv);
+                }
+            }
+            }
+        group_reduce<THREADS, true, false, false>(sm, turn, squares, gv, none);
+        turn ^= 1;
+        float rstd = 1.0f / sqrtf(squares / float(a.K) + a.eps), mean = gv * rstd / float(a.K);
+        if (!(squares <= MOST_SQUARES) || (squares < LEAST_SQUARES && a.eps < 1e-10f)) {
+            double sum = 0;
+            for (int j = t; j < a.K; j += THREADS) sum += double(to_f32(dyr[j])) * to_f32(a.w[j]) * to_f32(vr[j]);
+            rstd = rare_rstd<THREADS>(sm, [&](int j) { return to_f32(vr[j]); }, a.K, a.eps, t);
+            mean = float(group_sum<THREADS>(sm, sum) * rstd / a.K);
+            if (THREADS > 32) __syncthreads();   // dX, written below, may be dY
+        }
+        for (int base = 0; base < (LONG ? a.K : 1); base += SPAN) {
+            const Place<THREADS, WIDE> at{a.K, base, t};
+            if (LONG) read(at);
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) {
+                float out[8];
+                if (dsr) {
+                    at.load(dsr, c, out);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) out[e] = 0.0f;
+                }
+                at.load(a.w, c, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float n = v[c][e] * rstd;
+                    out[e] = fmaf(rstd, fmaf(-mean, n, dy[c][e] * w[e]), out[e]);
+                    if (!LONG) {
+                        dw[c][e] = fmaf(dy[c][e], n, dw[c][e]);
+                    } else if (partial && at.column(c, e) < a.K) {   // (this thread's own column)
+                        float *p = partial + at.column(c, e);
+                        *p = fmaf(dy[c][e], n, first ? 0.0f : *p);
+                    }
+                }
+                at.store(dxr, c, out);
+            }
+            }
+        first = false;
+    }
+    if (LONG || !partial) return;
+    const Place<THREADS, WIDE> at{a.K, 0, t};
+    for (int g = 0; g < GROUPS; ++g) {   // a block's warps in order
+        if (GROUPS > 1) __syncthreads();
+        if (group != g) continue;
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int j = at.column(c, e);
+                if (j >= a.K) continue;
+                if (GROUPS == 1)
+                    partial[j] = dw[c][e];
+                else
+                    columns[j] = g == 0 ? dw[c][e] : columns[j] + dw[c][e];
+            }
+    }
+    if (GROUPS == 1) return;
+    __syncthreads();
+    for (int j = threadIdx.x; j < a.K; j += norm_block(THREADS)) partial[j] = columns[j];
+}
+
+// dw from the blocks' sums: 32 columns to a block, its warps' shares of the sums in order.
+template <class T>
+__global__ void __launch_bounds__(256)
+    norm_weight_kernel(int K, int sums, const float *__restrict__ partial, T *dw) {
+    __shared__ float part[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = blockIdx.x * 32 + lane;
+    const int per = (sums + 7) / 8, last = min(sums, (warp + 1) * per);
+    sg::wait_prerequisites();
+    float s = 0.0f;
+    if (j < K && SG_IN_RANGE(sums > 0)) {
+#pragma unroll 8
+        for (int i = warp * per; i < last; ++i) s += partial[(long long)i * K + j];
+    }
+    part[warp][lane] = s;
+    __syncthreads();
+    if (warp != 0 || j >= K) return;
+    float all = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) all += part[k][lane];
+    dw[j] = from_f32<T>(all);
+}
+
+}  // namespace sgl

@@ -1,8 +1,9 @@
 /*
  * sgemm_layers.h -- the linear layer of a language model around the GEMM of
  * sgemm.h: low-rank adapters of many requests beside a shared projection
- * (forward and backward), and activation checkpoints in 8 bits with their use
- * in the backward pass.  Part of libsgemm.so; statuses, streams, ownership,
+ * (forward and backward), activation checkpoints in 8 bits with their use
+ * in the backward pass, and the root-mean-square norm before such a layer, with an
+ * output in 8 bits.  Part of libsgemm.so; statuses, streams, ownership,
  * workspaces and the device error word are those of sgemm.h.
  *
  * Conventions of every entry point here:
@@ -155,6 +156,55 @@ int sgemm_act8_grad(int type, int M, int K,
 int sgemm_act8_weight_grad(int type, int M, int N, int K,
                            const signed char *q, int ldq, const signed char *e, int lde,
                            const void *dY, int lddy, float beta, void *dW, int lddw,
+                           sgemm_stream_t stream);
+
+/* ------------------------------------------------------------------ norm and rows in 8 bits
+ *
+ * A matrix (M x K) in rows of 8 bits: q, M x K int8, and scale, M floats; row i stands for
+ * scale[i] * q[i].  With t the largest magnitude of a row, scale = t / 127 and q = x / scale rounded to
+ * the nearest integer, ties to even, of the exact quotient.  A row of zeros has scale 0; a row with an
+ * infinity or a NaN is kept as q = 0, scale NaN and stands for NaN throughout.
+ */
+
+/*
+ * sgemm_rmsnorm -- the root-mean-square norm of the rows of V = X + R, and V itself:
+ *
+ *   V = X + R (rounded to `type`: the residual stream as it is held; X where R is NULL)
+ *   y[j] = V[j] * w[j] / sqrt(mean over the row of V^2 + eps)
+ *
+ * w: K elements of `type`.  Outputs, each of which may be NULL but not all: S receives V; Y receives y
+ * in `type`; (q, scale), NULL together, receive y as rows of 8 bits (of the values before they are
+ * rounded to `type`).  S and Y may be X or R (same pointer and leading dimension), not each other.
+ * eps >= 0.  The mean is taken where squares leave fp32's range too; a row with an infinity has y = 0
+ * where V is finite, and NaN at the infinity.
+ */
+int sgemm_rmsnorm(int type, int M, int K,
+                  const void *X, int ldx,
+                  const void *R, int ldr,
+                  const void *w, float eps,
+                  void *S, int lds,
+                  void *Y, int ldy,
+                  signed char *q, int ldq, float *scale,
+                  sgemm_stream_t stream);
+
+/*
+ * sgemm_rmsnorm_backward -- the gradients of sgemm_rmsnorm's y for dY (M x K), given V:
+ * with r = 1 / sqrt(mean(V^2) + eps), n = V r and g = dY w,
+ *
+ *   dX[j] = dS[j] + r * (g[j] - n[j] * mean over the row of g n)
+ *   dw[j] = sum over the rows of dY[j] * n[j]
+ *
+ * dX is the gradient of X and of R alike.  dS, the gradient that reaches V by its other way (the
+ * residual stream), may be NULL (0); dw (K elements) may be NULL.  M == 0 gives dw = 0.  dX may be
+ * dY, dS or V (same pointer and leading dimension).
+ */
+int sgemm_rmsnorm_backward(int type, int M, int K,
+                           const void *dY, int lddy,
+                           const void *V, int ldv,
+                           const void *w, float eps,
+                           const void *dS, int ldds,
+                           void *dX, int lddx,
+                           void *dw,
                            sgemm_stream_t stream);
 
 #ifdef __cplusplus
