@@ -9,7 +9,8 @@ point without a built library raises immediately (there is no CPU fallback).
 """
 
 _LAYERS = ("lora_into", "lora_backward_into", "act8_empty", "act8_store_into", "act8_load_into",
-           "act8_grad_into", "act8_weight_grad_into", "rmsnorm_into", "rmsnorm_backward_into")
+           "act8_grad_into", "act8_weight_grad_into", "rmsnorm_into", "rmsnorm_backward_into",
+           "linear8_into", "gated_into", "gated_backward_into")
 __all__ = ["sgemm", "sgemm_host", "sgemm_into", *_LAYERS, "library_path", "workloads"]
 
 

@@ -60,6 +60,12 @@ lib.sgemm_rmsnorm.argtypes = [_i] * 3 + [_p, _i, _p, _i, _p, _f, _p, _i, _p, _i,
 lib.sgemm_rmsnorm.restype = _i
 lib.sgemm_rmsnorm_backward.argtypes = [_i] * 3 + [_p, _i, _p, _i, _p, _f, _p, _i, _p, _i, _p, _p]
 lib.sgemm_rmsnorm_backward.restype = _i
+lib.sgemm_linear8.argtypes = [_i] * 4 + [_p, _i, _p, _i, _p, _p, _i, _p, _p, _p, _i, _p]
+lib.sgemm_linear8.restype = _i
+lib.sgemm_gated.argtypes = [_i] * 4 + [_p, _i, _p, _i, _p, _i, _i, _p, _i, _p, _i, _p, _i, _p]
+lib.sgemm_gated.restype = _i
+lib.sgemm_gated_backward.argtypes = [_i] * 5 + [_p, _i] * 9 + [_p]
+lib.sgemm_gated_backward.restype = _i
 lib.sgemm_status_string.argtypes = [_i]
 lib.sgemm_status_string.restype = ctypes.c_char_p
 lib.sgemm_version.argtypes = []
@@ -650,6 +656,76 @@ def rmsnorm_backward_into(dY, V, w, dX, dw=None, dS=None, eps: float = 1e-6, str
           _vector("w", w, dY.dtype, K, device), _eps(eps), *_matrix("dS", dS, M, K), *_matrix("dX", dX, M, K),
           _vector("dw", dw, dY.dtype, K, device))
     return dX, dw
+
+
+def linear8_into(X, W, wscale, Y, bias=None, stream=None):
+    """Y[i, j] <- scale[i]*wscale[j]*(sum_k q[i, k]*W[k, j]) + bias[j]: rows in 8 bits times a weight in 8 bits.
+
+    X is the pair (q, scale) that rmsnorm_into() wrote, q (M, K) int8 and scale (M,) float32, or a
+    matrix (M, K) of Y's type, whose rows the call brings to 8 bits itself (scale = max|x| / 127, q
+    = x / scale rounded).  W (K, N) int8, wscale (N,) float32, Y (M, N) and bias (N,) or None: float32 or
+    bfloat16, one type.  The integer sums are exact; K is at most 131071."""
+    pair = isinstance(X, tuple)
+    kind, device = _layer_type(("Y", "bias", "X"), Y, bias, None if pair else X)
+    if X is None or W is None or wscale is None:
+        _missing(("X", "W", "wscale"), X, W, wscale)
+    if pair and len(X) != 2:
+        raise ValueError("X must be a matrix or the pair (q, scale)")
+    _typed("W", W, torch.int8, device)
+    (M, N), K = _sizes("Y", Y), _sizes("W", W)[0]
+    x = (None, 0, *_rows8(*X, M, K, device)) if pair else (*_matrix("X", X, M, K), None, 0, None)
+    _call(device, stream, lib.sgemm_linear8, kind, M, N, K, *x, *_matrix("W", W, K, N),
+          _vector("wscale", wscale, torch.float32, N, device), _vector("bias", bias, Y.dtype, N, device),
+          *_matrix("Y", Y, M, N))
+    return Y
+
+
+GATES = {**ACTIVATIONS, "silu": 3}   # activations of the gated block
+
+
+def _gate_number(act):
+    if act not in GATES:
+        raise ValueError(f"act must be one of {sorted(GATES)}, got {act!r}")
+    return GATES[act]
+
+
+def gated_into(X, Wg, Wu, H, act: str = "silu", G=None, U=None, stream=None):
+    """H <- act(X@Wg) * (X@Wu): the gated feed-forward block up to its last projection, for one token up
+    to a long prefill.
+
+    X (M, K), Wg, Wu (K, N), H (M, N): CUDA float32 or bfloat16, one type.  G and U (M, N),
+    given together, receive X@Wg and X@Wu for gated_backward_into()."""
+    kind, device = _layer_type(("X", "Wg", "Wu", "H", "G", "U"), X, Wg, Wu, H, G, U)
+    if Wg is None or Wu is None or H is None:
+        _missing(("Wg", "Wu", "H"), Wg, Wu, H)
+    if (G is None) != (U is None):
+        raise ValueError("G and U must be given together")
+    number = _gate_number(act)
+    (M, K), N = _sizes("X", X), _sizes("Wg", Wg)[1]
+    _call(device, stream, lib.sgemm_gated, kind, M, N, K, *_matrix("X", X, M, K), *_matrix("Wg", Wg, K, N),
+          *_matrix("Wu", Wu, K, N), number, *_matrix("G", G, M, N), *_matrix("U", U, M, N), *_matrix("H", H, M, N))
+    return H
+
+
+def gated_backward_into(dH, X, Wg, Wu, G, U, dX=None, dWg=None, dWu=None, act: str = "silu", stream=None):
+    """Gradients of gated_into() for dH (M, N): with dG = dH*U*act'(G) and dU = dH*act(G),
+    dX <- dG@Wg.T + dU@Wu.T, dWg <- X.T@dG and dWu <- X.T@dU.
+
+    G and U are what the forward call wrote.  dX (M, K) may be None, and dWg and dWu (K, N) may be
+    None together; X may be None without them.  Returns (dX, dWg, dWu)."""
+    kind, device = _layer_type(("dH", "X", "Wg", "Wu", "G", "U", "dX", "dWg", "dWu"), dH, X, Wg, Wu, G, U, dX, dWg, dWu)
+    if Wg is None or Wu is None or G is None or U is None:
+        _missing(("Wg", "Wu", "G", "U"), Wg, Wu, G, U)
+    if (dWg is None) != (dWu is None):
+        raise ValueError("dWg and dWu must be given together")
+    if dWg is not None and X is None:
+        _missing(("X",), X)
+    number = _gate_number(act)
+    (M, N), K = _sizes("dH", dH), _sizes("Wg", Wg)[0]
+    _call(device, stream, lib.sgemm_gated_backward, kind, M, N, K, number, *_matrix("dH", dH, M, N), *_matrix("X", X, M, K),
+          *_matrix("G", G, M, N), *_matrix("U", U, M, N), *_matrix("Wg", Wg, K, N), *_matrix("Wu", Wu, K, N),
+          *_matrix("dX", dX, M, K), *_matrix("dWg", dWg, K, N), *_matrix("dWu", dWu, K, N))
+    return dX, dWg, dWu
 
 
 # ------------------------------------------------------------------ control

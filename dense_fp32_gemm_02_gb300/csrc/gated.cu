@@ -1,0 +1,262 @@
+// gated.cu -- entry points of the gated block, forward and backward.
+#include "gated.cuh"
+#include "layer_host.h"
+#include "packed.cuh"
+#include "pair_gemm.h"
+#include "variant.cuh"
+
+#define SGEMM_API extern "C" __attribute__((visibility("default")))
+
+namespace {
+
+using namespace sgl;
+
+constexpr const char *kFewRows = "gated, few rows, both matrices read once";
+
+struct Call {
+    int type, M, N, K, act;
+    const void *X;
+    int ldx;
+    const void *Wg;
+    int ldwg;
+    const void *Wu;
+    int ldwu;
+    void *G;
+    int ldg;
+    void *U;
+    int ldu;
+    void *H;   // backward: dH
+    int ldh;
+    void *dX;
+    int lddx;
+    void *dWg;
+    int lddwg;
+    void *dWu;
+    int lddwu;
+    cudaStream_t stream;
+};
+
+int zero(void *p, int ld, int rows, int columns, size_t element, cudaStream_t stream) {
+    if (!p || rows == 0 || columns == 0) return SGEMM_OK;
+    const cudaError_t e = cudaMemset2DAsync(p, size_t(ld) * element, 0, size_t(columns) * element, size_t(rows), stream);
+    return e == cudaSuccess ? SGEMM_OK : sgh::cuda_fail(e);
+}
+
+// Sums of ranges, `pitch` apart in a range and `plane` from one range to the next.
+template <class T, bool GATED>
+int finish(int M, int N, int ranges, const float *x, const float *y, long long pitch, long long plane,
+           const PairOut<T> &to, cudaStream_t stream) {
+    const bool wide = N % 4 == 0 && pitch % 4 == 0 && plane % 4 == 0 && sgh::aligned(x, 16) && sgh::aligned(y, 16);
+    return sgh::launch(nullptr, pair_finish_kernel<T, GATED>, dim3(unsigned((N + 511LL) / 512), unsigned(std::min(M, 65535))),
+                       128, 0, stream, M, N, ranges, x, y, pitch, plane, wide, to);
+}
+
+// The operands that the TMA does not read where they lie, as parts.
+template <class T>
+int pack(const Packed<T> &p, const Packed<T> &q, int sms, cudaStream_t stream) {
+    const auto a = p.job(), b = q.job();
+    const long long octets = a.octets() + b.octets();
+    if (octets == 0) return SGEMM_OK;
+    const unsigned blocks = unsigned(std::min<long long>((octets + 255) / 256, 32LL * sms));
+    constexpr int PARTS = Packed<T>::PARTS;
+    return sgh::launch(nullptr, parts_kernel<PARTS, PARTS, Rows<T>, Rows<T>>, dim3(blocks), 256, 0, stream, a, b, false);
+}
+
+// ------------------------------------------------------------------ forward
+template <class T>
+int forward_few_rows(const Call &c, bool stream_rows, int sms, cudaMemPool_t pool) {
+    const T *Wg = static_cast<const T *>(c.Wg), *Wu = static_cast<const T *>(c.Wu);
+    const bool w_wide = wide_rows(Wg, c.ldwg) && wide_rows(Wu, c.ldwu);
+    const Rows<T> X{static_cast<const T *>(c.X), c.ldx};
+    RowsWork w{};
+    w.M = c.M, w.N = c.N, w.K = c.K;
+    w.x_wide = sgh::aligned(c.X, 4 * sizeof(T)) && c.ldx % 4 == 0;
+    if (stream_rows)
+        split_rows(w, 32 * 16 / int(sizeof(T)), RANK_THREADS / 32 * STREAM_DEPTH, STREAM_RANGE,
+                   (long long)sms * stream_blocks(c.M), sizeof(T), 2);
+    else
+        split_rows(w, ROWS_COLS, SLAB, sgh::kMaxDim, 2LL * sms, sizeof(T), 2);
+    const long long blocks = 2LL * w.across * w.ranges, one = (long long)w.ranges * c.M * c.N;
+    if (blocks > 0x7fffffffLL) return SGEMM_ERR_TOO_LARGE;
+    sgh::Workspace ws(pool, c.stream);
+    int st = ws.allocate(sgh::Workspace::piece(size_t(one) * 8));
+    if (st != SGEMM_OK) return st;
+    w.partial = ws.take<float>(size_t(one) * 2);
+    if (stream_rows) {
+        auto pick = [&](auto wide) {
+            constexpr bool W = decltype(wide)::value;
+            return c.M <= 1   ? gated_stream_kernel<T, 1, W>
+                   : c.M <= 2 ? gated_stream_kernel<T, 2, W>
+                   : c.M <= 4 ? gated_stream_kernel<T, 4, W>
+                              : gated_stream_kernel<T, 8, W>;
+        };
+        auto kernel = w_wide ? pick(std::true_type{}) : pick(std::false_type{});
+        kernel<<<unsigned(blocks), RANK_THREADS, 0, c.stream>>>(w, X, Wg, c.ldwg, Wu, c.ldwu);
+        st = sgh::launched(kFewRows);
+    } else if constexpr (sizeof(T) == 4) {
+        auto kernel = c.M <= 16 ? gated_few_rows_kernel<1> : c.M <= 32 ? gated_few_rows_kernel<2> : gated_few_rows_kernel<4>;
+        const size_t smem = c.M <= 16 ? FewRows<1>::SMEM : c.M <= 32 ? FewRows<2>::SMEM : FewRows<4>::SMEM;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return sgh::cuda_fail(e);
+        kernel<<<unsigned(blocks), RANK_THREADS, smem, c.stream>>>(w, X, Wg, c.ldwg, Wu, c.ldwu, w_wide);
+        st = sgh::launched(kFewRows);
+    }
+    if (st != SGEMM_OK) return st;
+    const PairOut<T> to{static_cast<T *>(c.G), static_cast<T *>(c.U), static_cast<T *>(c.H), c.ldg, c.ldu, c.ldh, c.act};
+    st = finish<T, true>(c.M, c.N, w.ranges, w.partial, w.partial + one, c.N, (long long)c.M * c.N, to, c.stream);
+    return st == SGEMM_OK ? ws.release() : st;
+}
+
+template <class T>
+int forward(const Call &c) {
+    int sms, st;
+    cudaMemPool_t pool;
+    if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
+    constexpr int PARTS = Packed<T>::PARTS;
+    const PairOut<T> to{static_cast<T *>(c.G), static_cast<T *>(c.U), static_cast<T *>(c.H), c.ldg, c.ldu, c.ldh, c.act};
+    if (c.K == 0) return finish<T, true>(c.M, c.N, 0, nullptr, nullptr, c.N, 0, to, c.stream);
+    Packed<T> X(c.M, c.K, c.X, c.ldx), Wg(c.K, c.N, c.Wg, c.ldwg), Wu(c.K, c.N, c.Wu, c.ldwu);
+    const bool in_place = Wg.direct && Wu.direct;
+    if (c.M <= STREAM_ROWS && (PARTS == 3 || !in_place || c.M <= 2 || (long long)c.K * c.N < 4000000))
+        return forward_few_rows<T>(c, true, sms, pool);
+    if (PARTS == 3 && c.M <= MMA_ROWS) return forward_few_rows<T>(c, false, sms, pool);
+
+    const sgp::Split split = sgq::plan(sgq::GATE, c.M, c.N, c.K, PARTS == 3 ? 6 : 1, sms);
+    sgh::Workspace ws(pool, c.stream);
+    st = ws.allocate(X.bytes() + Wg.bytes() + Wu.bytes() + sgh::Workspace::piece(split.partial_floats * 4));
+    if (st != SGEMM_OK) return st;
+    X.place(ws);
+    Wg.place(ws);
+    Wu.place(ws);
+    float *partial = split.partial_floats ? ws.take<float>(split.partial_floats) : nullptr;
+    Packed<T> none(0, 0, nullptr, 8);
+    if ((st = pack(Wg, Wu, sms, c.stream)) != SGEMM_OK || (st = pack(X, none, sms, c.stream)) != SGEMM_OK) return st;
+    sgq::Product g{c.M, c.N, c.K, X.operand(), {Wg.operand(), Wu.operand()}};
+    const sgq::Output<T> out{to.out, to.out1, to.H, to.ldo, to.ldo1, to.ldh, to.act, nullptr, nullptr, nullptr};
+    if ((st = sgq::run<T, sgq::GATE>(g, out, split, partial, sms, c.stream)) != SGEMM_OK) return st;
+    if (partial) {
+        st = finish<T, true>(c.M, c.N, split.splits, partial, partial + c.N, 2LL * c.N, 2LL * c.M * c.N, to, c.stream);
+        if (st != SGEMM_OK) return st;
+    }
+    return ws.release();
+}
+
+// ------------------------------------------------------------------ backward
+template <class T>
+int backward(const Call &c) {
+    int sms, st;
+    cudaMemPool_t pool;
+    if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
+    constexpr int PARTS = Packed<T>::PARTS, PRODUCTS = PARTS == 3 ? 6 : 1;
+    const bool want_dx = c.dX != nullptr, want_dw = c.dWg != nullptr;
+    Packed<T> X(c.M, c.K, c.X, c.ldx), Wg(c.K, c.N, c.Wg, c.ldwg), Wu(c.K, c.N, c.Wu, c.ldwu), none(0, 0, nullptr, 8);
+    if (!want_dw) X.direct = true;                  // no parts of them are needed
+    if (!want_dx) Wg.direct = Wu.direct = true;
+    const sgp::Split sum = want_dx ? sgq::plan(sgq::SUM, c.M, c.K, c.N, PRODUCTS, sms) : sgp::Split{1, 256, 0};
+    const sgp::Split two = want_dw ? sgq::plan(sgq::TWO, c.K, c.N, c.M, PRODUCTS, sms) : sgp::Split{1, 256, 0};
+    const long long pitch = pitch8(c.N), plane = c.M * pitch;
+    const size_t d_elems = size_t(2) * PARTS * plane;
+    sgh::Workspace ws(pool, c.stream);
+    st = ws.allocate(sgh::Workspace::piece(d_elems * 2) + X.bytes() + Wg.bytes() + Wu.bytes() +
+                     sgh::Workspace::piece(sum.partial_floats * 4) + sgh::Workspace::piece(two.partial_floats * 4));
+    if (st != SGEMM_OK) return st;
+    bf16 *d = ws.take<bf16>(d_elems);
+    X.place(ws);
+    Wg.place(ws);
+    Wu.place(ws);
+    float *sum_partial = sum.partial_floats ? ws.take<float>(sum.partial_floats) : nullptr;
+    float *two_partial = two.partial_floats ? ws.take<float>(two.partial_floats) : nullptr;
+
+    SlopesJob<T> job{static_cast<const T *>(c.H), static_cast<const T *>(c.G), static_cast<const T *>(c.U), c.ldh, c.ldg, c.ldu,
+                     c.M, c.N, c.act, false, {d, pitch, plane}, {d + PARTS * plane, pitch, plane},
+                     Divisor::of(unsigned((c.N + 7LL) / 8))};
+    job.wide = wide_rows(job.dH, job.ldh) && wide_rows(job.G, job.ldg) && wide_rows(job.U, job.ldu);
+    const long long octets = (long long)c.M * job.per_row.d;
+    st = sgh::launch(nullptr, gated_slopes_kernel<T>, dim3(unsigned(std::min<long long>((octets + 255) / 256, 32LL * sms))), 256,
+                     0, c.stream, job);
+    if (st != SGEMM_OK || (st = pack(Wg, Wu, sms, c.stream)) != SGEMM_OK || (st = pack(X, none, sms, c.stream)) != SGEMM_OK)
+        return st;
+    const sgp::Operand dG{d, c.N, c.M, PARTS, pitch, plane}, dU{d + PARTS * plane, c.N, c.M, PARTS, pitch, plane};
+    if (want_dx) {
+        sgq::Product g{c.M, c.K, c.N, {d, c.N, c.M, 2 * PARTS, pitch, plane}, {Wg.operand(), Wu.operand()}};
+        const sgq::Output<T> out{static_cast<T *>(c.dX), nullptr, nullptr, c.lddx, 0, 0, 0, nullptr, nullptr, nullptr};
+        if ((st = sgq::run<T, sgq::SUM>(g, out, sum, sum_partial, sms, c.stream)) != SGEMM_OK) return st;
+        if (sum_partial) {
+            const sgp::Epilogue<T, false> epi{Adapters{}, nullptr, 0, {}, nullptr, 0.0f, out.out, out.ldo};
+            st = sgp::finish<T, false>(c.M, c.K, sum.splits, sum_partial, nullptr, epi, c.stream);
+            if (st != SGEMM_OK) return st;
+        }
+    }
+    if (want_dw) {
+        sgq::Product g{c.K, c.N, c.M, X.operand(), {dG, dU}};
+        const PairOut<T> to{static_cast<T *>(c.dWg), static_cast<T *>(c.dWu), nullptr, c.lddwg, c.lddwu, 0, 0};
+        const sgq::Output<T> out{to.out, to.out1, nullptr, to.ldo, to.ldo1, 0, 0, nullptr, nullptr, nullptr};
+        if ((st = sgq::run<T, sgq::TWO>(g, out, two, two_partial, sms, c.stream)) != SGEMM_OK) return st;
+        if (two_partial) {
+            st = finish<T, false>(c.K, c.N, two.splits, two_partial, two_partial + c.N, 2LL * c.N, 2LL * c.K * c.N, to,
+                                  c.stream);
+            if (st != SGEMM_OK) return st;
+        }
+    }
+    return ws.release();
+}
+
+}  // namespace
+
+cudaError_t sgh::gated_error_word(unsigned *v, bool clear) { return sgv::unit_error_word(v, clear); }
+
+SGEMM_API int sgemm_gated(int type, int M, int N, int K, const void *X, int ldx, const void *Wg, int ldwg, const void *Wu,
+                          int ldwu, int act, void *G, int ldg, void *U, int ldu, void *H, int ldh, sgemm_stream_t stream) {
+    const int st = sgh::check_sizes(type, {M, N, K});
+    if (st != SGEMM_OK) return st;
+    if (act < SGEMM_ACT_NONE || act > SGEMM_ACT_SILU) return SGEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return SGEMM_OK;
+    const size_t size = sgh::element_bytes(type);
+    if ((K > 0 && (sgh::bad_matrix(X, ldx, K, size) || sgh::bad_matrix(Wg, ldwg, N, size) || sgh::bad_matrix(Wu, ldwu, N, size))) ||
+        !G != !U || sgh::bad_optional(G, ldg, N, size) || sgh::bad_optional(U, ldu, N, size) || sgh::bad_matrix(H, ldh, N, size))
+        return SGEMM_ERR_INVALID_ARG;
+    Call c{};
+    c.type = type, c.M = M, c.N = N, c.K = K, c.act = act;
+    c.X = X, c.ldx = ldx, c.Wg = Wg, c.ldwg = ldwg, c.Wu = Wu, c.ldwu = ldwu;
+    c.G = G, c.ldg = ldg, c.U = U, c.ldu = ldu, c.H = H, c.ldh = ldh;
+    c.stream = reinterpret_cast<cudaStream_t>(stream);
+    return type == SGEMM_BF16 ? forward<bf16>(c) : forward<float>(c);
+}
+
+SGEMM_API int sgemm_gated_backward(int type, int M, int N, int K, int act, const void *dH, int lddh, const void *X, int ldx,
+                                   const void *G, int ldg, const void *U, int ldu, const void *Wg, int ldwg, const void *Wu,
+                                   int ldwu, void *dX, int lddx, void *dWg, int lddwg, void *dWu, int lddwu,
+                                   sgemm_stream_t stream) {
+    int st = sgh::check_sizes(type, {M, N, K});
+    if (st != SGEMM_OK) return st;
+    if (act < SGEMM_ACT_NONE || act > SGEMM_ACT_SILU) return SGEMM_ERR_INVALID_ARG;
+    const size_t size = sgh::element_bytes(type);
+    const bool want_dx = dX && M > 0 && K > 0, want_dw = (dWg || dWu) && K > 0 && N > 0;
+    if (want_dw && (!dWg || !dWu || sgh::bad_matrix(dWg, lddwg, N, size) || sgh::bad_matrix(dWu, lddwu, N, size)))
+        return SGEMM_ERR_INVALID_ARG;
+    if (want_dx && (sgh::bad_matrix(dX, lddx, K, size) ||
+                    (N > 0 && (sgh::bad_matrix(Wg, ldwg, N, size) || sgh::bad_matrix(Wu, ldwu, N, size)))))
+        return SGEMM_ERR_INVALID_ARG;
+    if ((want_dx || want_dw) && M > 0 && N > 0 &&
+        (sgh::bad_matrix(dH, lddh, N, size) || sgh::bad_matrix(G, ldg, N, size) || sgh::bad_matrix(U, ldu, N, size)))
+        return SGEMM_ERR_INVALID_ARG;
+    if (want_dw && M > 0 && sgh::bad_matrix(X, ldx, K, size)) return SGEMM_ERR_INVALID_ARG;
+    if (!want_dx && !want_dw) return SGEMM_OK;
+    Call c{};
+    c.type = type, c.M = M, c.N = N, c.K = K, c.act = act;
+    c.H = const_cast<void *>(dH), c.ldh = lddh, c.X = X, c.ldx = ldx;
+    c.G = const_cast<void *>(G), c.ldg = ldg, c.U = const_cast<void *>(U), c.ldu = ldu;
+    c.Wg = Wg, c.ldwg = ldwg, c.Wu = Wu, c.ldwu = ldwu;
+    c.dX = want_dx ? dX : nullptr, c.lddx = lddx;
+    c.dWg = want_dw ? dWg : nullptr, c.lddwg = lddwg, c.dWu = want_dw ? dWu : nullptr, c.lddwu = lddwu;
+    c.stream = reinterpret_cast<cudaStream_t>(stream);
+    if (M == 0 || N == 0) {   // sums of nothing
+        int sms;
+        cudaMemPool_t pool;
+        if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
+        if ((st = zero(c.dX, lddx, M, K, size, c.stream)) != SGEMM_OK || (st = zero(c.dWg, lddwg, K, N, size, c.stream)) != SGEMM_OK)
+            return st;
+        return zero(c.dWu, lddwu, K, N, size, c.stream);
+    }
+    return type == SGEMM_BF16 ? backward<bf16>(c) : backward<float>(c);
+}

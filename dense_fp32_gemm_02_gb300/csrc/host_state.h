@@ -37,6 +37,11 @@ cudaError_t act8_error_word(unsigned *v, bool clear);
 cudaError_t lora_error_word(unsigned *v, bool clear);
 cudaError_t parts_gemm_error_word(unsigned *v, bool clear);
 cudaError_t norm_error_word(unsigned *v, bool clear);
+cudaError_t pair_gemm_error_word(unsigned *v, bool clear);
+cudaError_t gated_error_word(unsigned *v, bool clear);
+cudaError_t linear8_error_word(unsigned *v, bool clear);
+
+inline bool aligned(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
 // Largest size that an entry point accepts.
 constexpr int kMaxDim = 0x7fffffff - 0xffff;

@@ -8,8 +8,6 @@
 
 namespace sgh {
 
-inline bool aligned(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
 // A matrix that an entry point refuses: none, not aligned to its elements, or with overlapping rows.
 inline bool bad_matrix(const void *p, int ld, int columns, size_t element) {
     return !p || !aligned(p, element) || ld < std::max(1, columns);

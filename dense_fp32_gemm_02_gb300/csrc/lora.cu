@@ -4,6 +4,7 @@
 
 #include "../../include/sgemm_layers.h"
 #include "host_state.h"
+#include "packed.cuh"
 #include "parts_gemm.h"
 #include "rank_products.cuh"
 #include "rows.cuh"
@@ -14,10 +15,10 @@
 namespace {
 
 using namespace sgl;
+using sgh::aligned;
 
 constexpr int kMaxRank = 128, kMaxAdapters = 1024;
 
-bool aligned(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 bool bad_matrix(const void *p, int ld, int columns, size_t element) {
     return !p || !aligned(p, element) || ld < std::max(1, columns);
 }
@@ -96,56 +97,14 @@ bool bad_stack(const void *p, int ld, long long stride, int L, int rows, int col
 }
 
 // ------------------------------------------------------------------ operands
-long long pitch8(long long cols) { return (cols + 7) / 8 * 8; }
-
-// A matrix that the TMA reads where it lies: bfloat16, 16-byte aligned rows.
-template <class T>
-bool in_place(const T *p, int ld) {
-    return sizeof(T) == 2 && aligned(p, 16) && ld % 8 == 0;
-}
-
 template <class T>
 Stack<const T> stack_of(const void *p, int ld, long long stride) {
     return {static_cast<const T *>(p), ld, stride};
 }
 template <class T>
-bool wide_rows(const T *p, long long ld) {
-    return aligned(p, 16) && ld % (16 / (long long)sizeof(T)) == 0;
-}
-template <class T>
 bool wide_stack(const Stack<T> &v, int L) {
     return wide_rows(v.p, v.ld) && (L <= 1 || v.stride % (16 / (long long)sizeof(T)) == 0);
 }
-
-// The parts of a rows x cols matrix as an operand: the matrix itself, or planes in the
-// workspace that parts_kernel fills.
-template <class T>
-struct Packed {
-    static constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
-    long long rows, cols, pitch;
-    bool direct;
-    const T *src;
-    int ld;
-    Parts parts{};
-
-    Packed(long long rows_, long long cols_, const void *p, int ld_)
-        : rows(rows_), cols(cols_), pitch(pitch8(cols_)), direct(in_place(static_cast<const T *>(p), ld_)),
-          src(static_cast<const T *>(p)), ld(ld_) {}
-
-    size_t elements() const { return direct ? 0 : size_t(PARTS) * rows * pitch; }
-    size_t bytes() const { return sgh::Workspace::piece(elements() * 2); }
-    void place(sgh::Workspace &ws) {
-        if (!direct) parts = Parts{ws.take<bf16>(elements()), pitch, rows * pitch};
-    }
-    PartsJob<Rows<T>> job() const {   // (no rows where the TMA reads the matrix itself)
-        return PartsJob<Rows<T>>(Rows<T>{src, ld}, direct ? 0 : int(rows), int(cols), wide_rows(src, ld), parts);
-    }
-    sgp::Operand operand() const {
-        if (direct)
-            return {reinterpret_cast<const bf16 *>(src), cols, rows, 1, ld, rows * (long long)ld};
-        return {parts.p, cols, rows, PARTS, pitch, rows * pitch};
-    }
-};
 
 // Raises a kernel's shared memory limit; on every launch, as it costs less than
 // remembering the devices it was done on.  `bytes` is the same in every call for a kernel.
@@ -401,23 +360,6 @@ StreamKernel<T> stream_kernel(int M) {
            : M <= 2 ? stream_rows_kernel<T, 2, WIDE>
            : M <= 4 ? stream_rows_kernel<T, 4, WIDE>
                     : stream_rows_kernel<T, 8, WIDE>;
-}
-
-// The split of K over the grid: the count of ranges (whole `step`s, none above `longest`)
-// whose waves of blocks take the fewest steps, with two for filling and emptying; partial
-// sums (8 bytes of traffic per row and column) of at most half of what W takes.
-void split_rows(RowsWork &w, int cols, int step, int longest, long long slots, size_t element) {
-    w.across = (w.N + cols - 1) / cols;
-    const long long steps = (w.K + step - 1LL) / step;
-    const long long fewest = (w.K + (long long)longest - 1) / longest;
-    const long long most = std::max(fewest, std::min(steps, (long long)w.K * (long long)element / (16LL * w.M)));
-    long long least = 0;
-    for (long long n = fewest; n <= std::min(most, fewest + 64); ++n) {
-        const long long per = (steps + n - 1) / n;
-        const long long cost = ((w.across * n + slots - 1) / slots) * (per + 2);
-        if (n == fewest || cost < least) least = cost, w.range = int(per * step);
-    }
-    w.ranges = int((w.K + (long long)w.range - 1) / w.range);
 }
 
 // Whether W goes through registers and FMAs.  Of up to 8 rows all do in float32 (8 x 8192 x

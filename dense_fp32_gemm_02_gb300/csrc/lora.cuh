@@ -347,6 +347,7 @@ constexpr size_t sort_smem(int L) {
 
 // Block 0 lays the planes out; block 1, where there is one, sorts the rows.  Bound by
 // latency: 6 us up to 8192 rows.
+namespace {   // (no template: a copy to each unit)
 __global__ void __launch_bounds__(SORT_THREADS, 1) group_rows_kernel(int M, Adapters ad, Groups g) {
     extern __shared__ int sm[];
     __shared__ int warp_sum[32];
@@ -360,6 +361,7 @@ __global__ void __launch_bounds__(SORT_THREADS, 1) group_rows_kernel(int M, Adap
     else
         sort_rows(M, ad, g, no_rank, sm, warp_sum);
 }
+}  // namespace
 
 // One side of the stack laid out for the tensor cores: the parts of the used adapters as
 // planes part * L + a of width x cols, zero past the adapter's rank.  `trans`: V_a is

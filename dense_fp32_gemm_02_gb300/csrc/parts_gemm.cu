@@ -15,17 +15,6 @@ namespace {
 
 using namespace sgp;
 
-int encode(CUtensorMap *map, const Operand &o, uint32_t box_inner, uint32_t box_outer) {
-    const cuuint64_t dims[3] = {cuuint64_t(o.inner), cuuint64_t(o.outer), cuuint64_t(o.planes)};
-    const cuuint64_t strides[2] = {cuuint64_t(o.pitch) * 2, cuuint64_t(o.plane_pitch) * 2};
-    const cuuint32_t box[3] = {box_inner, box_outer, 1}, steps[3] = {1, 1, 1};
-    const CUresult r = sgh::encode_tiled()(
-        map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16 *>(o.p), dims, strides, box, steps,
-        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? SGEMM_OK : sgh::driver_fail(int(r));
-}
-
 template <class T, Layout LAYOUT>
 struct Kernel {
     static constexpr bool F32 = sizeof(T) == 4, A_MN = LAYOUT == WEIGHT_GRAD, B_MN = LAYOUT != INPUT_GRAD;
@@ -50,6 +39,17 @@ struct RankKernel {
 };
 
 }  // namespace
+
+int sgp::encode(CUtensorMap *map, const Operand &o, uint32_t box_inner, uint32_t box_outer) {
+    const cuuint64_t dims[3] = {cuuint64_t(o.inner), cuuint64_t(o.outer), cuuint64_t(o.planes)};
+    const cuuint64_t strides[2] = {cuuint64_t(o.pitch) * 2, cuuint64_t(o.plane_pitch) * 2};
+    const cuuint32_t box[3] = {box_inner, box_outer, 1}, steps[3] = {1, 1, 1};
+    const CUresult r = sgh::encode_tiled()(
+        map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16 *>(o.p), dims, strides, box, steps,
+        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SGEMM_OK : sgh::driver_fail(int(r));
+}
 
 cudaError_t sgh::parts_gemm_error_word(unsigned *v, bool clear) { return sgv::unit_error_word(v, clear); }
 
@@ -87,9 +87,9 @@ int sgp::set_up() {
 // 89.1, 192: 84.1, 128: 128.8), the input gradient 3001 x 1024 x 1023 of 192 (75.4; 256:
 // 81.8).  120 float32 products of random sizes take 0.966 of the time that 256 columns
 // take, the best width of each 0.954.
-Split sgp::plan_split(int M, int N, int K, int products, int sms) {
+Split sgp::plan_split(int M, int N, int K, int products, int sms, Outputs outputs, int contractions) {
     const long long pairs = std::max(1, sms / 2);
-    const long long slabs = (K + BK - 1LL) / BK;
+    const long long slabs = contractions * ((K + BK - 1LL) / BK), columns = N * (outputs == ALONE ? 1LL : 2LL);
     const int parts = products == 1 ? 2 : products == 3 ? 4 : 6;   // that a slab loads
     auto slab_cost = [&](int width) {
         return width == TILE || products == 1 ? double(products)
@@ -97,8 +97,10 @@ Split sgp::plan_split(int M, int N, int K, int products, int sms) {
     };
     Split best{1, TILE, 0};
     double least = 0;
-    for (int width = TILE; width >= (products == 1 ? TILE : TILE / 2); width -= 32) {
-        const long long tiles = ((M + 255LL) / 256) * ((N + width - 1LL) / width);
+    for (int width = TILE; width >= (products == 1 ? TILE : TILE / 2);
+         width -= outputs == HALF_EACH ? 64 : 32) {
+        const long long across = outputs == ONE_BY_ONE ? 2 * ((N + width - 1LL) / width) : (columns + width - 1) / width;
+        const long long tiles = ((M + 255LL) / 256) * across;
         for (long long s = 1; s <= std::min(64LL, std::max(1LL, slabs)); ++s) {
             const long long per = (slabs + s - 1) / s;
             if ((slabs + per - 1) / per != s) continue;      // a range would be empty
@@ -107,10 +109,10 @@ Split sgp::plan_split(int M, int N, int K, int products, int sms) {
             const double last = rest == 0 ? 0.0 : halves && waves > 0 ? 0.5 : 1.0;
             const double slab = slab_cost(halves && waves == 0 ? TILE / 2 : width);
             const double cost = (double(waves) + last) * (double(per) * slab + 8.0) +
-                                (s > 1 ? 12.0 + double(s) * M * N * 8.0 / 5.0e6 / 0.27 : 0.0);
+                                (s > 1 ? 12.0 + double(s) * M * columns * 8.0 / 5.0e6 / 0.27 : 0.0);
             if (least == 0 || cost < least) {
                 least = cost;
-                best = Split{int(s), width, s > 1 ? size_t(s) * M * N : 0};
+                best = Split{int(s), width, s > 1 ? size_t(s) * M * size_t(columns) : 0};
             }
         }
     }

@@ -2,6 +2,7 @@
 // tensor cores (parts_gemm.cu), as the layer entry points call them.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "adapters.cuh"
@@ -68,7 +69,13 @@ struct Split {
     int splits, tile_n;   // tile_n: columns of a tile
     size_t partial_floats;
 };
-Split plan_split(int M, int N, int K, int products, int sms);
+// `outputs`: one matrix, or two of N columns each whose tiles are one list (ONE_BY_ONE) or hold
+// half their columns of either (HALF_EACH); `contractions` of K each.
+enum Outputs { ALONE, ONE_BY_ONE, HALF_EACH };
+Split plan_split(int M, int N, int K, int products, int sms, Outputs outputs = ALONE, int contractions = 1);
+
+// The tensor map of an operand with boxes of box_inner x box_outer elements of one plane.
+int encode(CUtensorMap *map, const Operand &o, uint32_t box_inner, uint32_t box_outer);
 
 // float: a of 3 parts (1 in WEIGHT_GRAD) and b of 3; bfloat16: one part each.
 // The kernel is launched early (host_state.h).  PARTIALS leaves the partial sums (of one

@@ -19,6 +19,8 @@
 // before it 23.6, because the product's blocks then wait for shared memory).
 #pragma once
 
+#include <algorithm>
+
 #include "rank_products.cuh"
 
 namespace sgl {
@@ -35,6 +37,24 @@ struct RowsWork {
     float *partial;        // ranges x M x N
     float *rank_partial;   // rank_ranges x M x R
 };
+
+// The split of K over the grid: the count of ranges (whole `step`s, none above `longest`)
+// whose waves of blocks take the fewest steps, with two for filling and emptying; partial
+// sums (8 bytes of traffic per row and column) of at most half of what W takes.  `matrices` like W
+// are multiplied together.
+inline void split_rows(RowsWork &w, int cols, int step, int longest, long long slots, size_t element, int matrices = 1) {
+    w.across = (w.N + cols - 1) / cols;
+    const long long steps = (w.K + step - 1LL) / step;
+    const long long fewest = (w.K + (long long)longest - 1) / longest;
+    const long long most = std::max(fewest, std::min(steps, (long long)w.K * (long long)element / (16LL * w.M)));
+    long long least = 0;
+    for (long long n = fewest; n <= std::min(most, fewest + 64); ++n) {
+        const long long per = (steps + n - 1) / n;
+        const long long cost = ((matrices * w.across * n + slots - 1) / slots) * (per + 2);
+        if (n == fewest || cost < least) least = cost, w.range = int(per * step);
+    }
+    w.ranges = int((w.K + (long long)w.range - 1) / w.range);
+}
 
 // The rank side of one row over one range.  Lanes along the rank, 16 bytes each, and in
 // groups along the range; a thread's sums, then its warp's groups, then the warps.
@@ -109,18 +129,20 @@ constexpr int STREAM_RANGE = 512, STREAM_DEPTH = 8;
 
 constexpr int stream_blocks(int rows) { return rows <= 4 ? 3 : 2; }   // to an SM
 
+template <class T, int MR>
+struct StreamRows {
+    static constexpr int COLS = 32 * 16 / int(sizeof(T)), WARPS = RANK_THREADS / 32;
+    static constexpr int XS = STREAM_RANGE * MR, RED = WARPS * COLS * (MR < 4 ? MR : 4);
+    static constexpr int FLOATS = XS > RED ? (XS > RANK_SUMS ? XS : RANK_SUMS) : (RED > RANK_SUMS ? RED : RANK_SUMS);
+};
+
+// Block `block` of the product; its sums go to partial[range][row][column].
 template <class T, int MR, bool WIDE>
-__global__ void __launch_bounds__(RANK_THREADS, stream_blocks(MR))
-    stream_rows_kernel(RowsWork w, Rows<T> X, const T *W, long long ldw, Stack<const T> V, Adapters ad) {
-    constexpr int PER = 16 / int(sizeof(T)), COLS = 32 * PER, WARPS = RANK_THREADS / 32;
-    constexpr int XS = STREAM_RANGE * MR, RED = WARPS * COLS * (MR < 4 ? MR : 4);
-    __shared__ __align__(16) float sm[XS > RED ? (XS > RANK_SUMS ? XS : RANK_SUMS) : (RED > RANK_SUMS ? RED : RANK_SUMS)];
-    sg::launch_dependents();
-    if (int(blockIdx.x) >= w.across * w.ranges) {
-        rank_of_row(w, int(blockIdx.x) - w.across * w.ranges, X, V, ad, sm);
-        return;
-    }
-    const int n0 = (int(blockIdx.x) % w.across) * COLS, q = int(blockIdx.x) / w.across;
+__device__ __forceinline__ void stream_rows(const RowsWork &w, int block, const Rows<T> &X, const T *W, long long ldw,
+                                            float *partial, float *sm) {
+    constexpr int PER = 16 / int(sizeof(T)), COLS = StreamRows<T, MR>::COLS, WARPS = StreamRows<T, MR>::WARPS;
+    [[maybe_unused]] constexpr int RED = StreamRows<T, MR>::RED;
+    const int n0 = (block % w.across) * COLS, q = block / w.across;
     const int k0 = q * w.range, kn = min(w.range, w.K - k0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (!SG_IN_RANGE(kn > 0 && kn <= STREAM_RANGE && k0 + kn <= w.K && n0 < w.N && q < w.ranges && w.M <= MR)) return;
@@ -163,7 +185,7 @@ __global__ void __launch_bounds__(RANK_THREADS, stream_blocks(MR))
             }
         }
     }
-    float *out = w.partial + (long long)q * w.M * w.N;
+    float *out = partial + (long long)q * w.M * w.N;
 #pragma unroll
     for (int m0 = 0; m0 < MR; m0 += 4) {
         __syncthreads();
@@ -183,6 +205,18 @@ __global__ void __launch_bounds__(RANK_THREADS, stream_blocks(MR))
             if (m < w.M && n0 + c < w.N && SG_IN_RANGE(((m - m0 + 1) * WARPS - 1) * COLS + c < RED)) out[(long long)m * w.N + n0 + c] = s;
         }
     }
+}
+
+template <class T, int MR, bool WIDE>
+__global__ void __launch_bounds__(RANK_THREADS, stream_blocks(MR))
+    stream_rows_kernel(RowsWork w, Rows<T> X, const T *W, long long ldw, Stack<const T> V, Adapters ad) {
+    __shared__ __align__(16) float sm[StreamRows<T, MR>::FLOATS];
+    sg::launch_dependents();
+    if (int(blockIdx.x) >= w.across * w.ranges) {
+        rank_of_row(w, int(blockIdx.x) - w.across * w.ranges, X, V, ad, sm);
+        return;
+    }
+    stream_rows<T, MR, WIDE>(w, int(blockIdx.x), X, W, ldw, w.partial, sm);
 }
 
 // ------------------------------------------------------------------ float32, up to 64 rows
@@ -240,17 +274,16 @@ __device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
+// Block `block` of the product, its sums to partial[range][row][column]; `smem` FewRows<MT>::SMEM bytes.
 template <int MT>
-__global__ void __launch_bounds__(RANK_THREADS, 2)
-    few_rows_kernel(RowsWork w, Rows<float> X, const float *W, long long ldw, bool w_wide) {
+__device__ __forceinline__ void few_rows(const RowsWork &w, int block, const Rows<float> &X, const float *W, long long ldw,
+                                         bool w_wide, float *partial, unsigned char *smem) {
     using Z = FewRows<MT>;
     constexpr int STAGES = Z::STAGES, WARPS = RANK_THREADS / 32, PIECES = WARPS / 4;   // of a slab's k
-    extern __shared__ __align__(16) unsigned char smem_rows[];
-    sg::launch_dependents();
-    float *ring = reinterpret_cast<float *>(smem_rows);
+    float *ring = reinterpret_cast<float *>(smem);
     float *raw = ring + STAGES * Z::W_ELEMS;                      // X's next slab
     bf16 *xs = reinterpret_cast<bf16 *>(raw + Z::X_ROWS * SLAB);   // this one's parts
-    const int n0 = (int(blockIdx.x) % w.across) * ROWS_COLS, q = int(blockIdx.x) / w.across;
+    const int n0 = (block % w.across) * ROWS_COLS, q = block / w.across;
     const int k_begin = q * w.range, k_end = min(w.K, k_begin + w.range);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp & 3, piece = warp >> 2;
     if (!SG_IN_RANGE(k_begin < k_end && n0 < w.N && q < w.ranges && w.M <= Z::X_ROWS)) return;
@@ -372,7 +405,7 @@ __global__ void __launch_bounds__(RANK_THREADS, 2)
     }
     __syncthreads();
     if (piece > 0) return;
-    float *out = w.partial + (long long)q * w.M * w.N;
+    float *out = partial + (long long)q * w.M * w.N;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -394,6 +427,14 @@ __global__ void __launch_bounds__(RANK_THREADS, 2)
                     if (j + t < w.N) out[(long long)i * w.N + j + t] = v[t];
             }
         }
+}
+
+template <int MT>
+__global__ void __launch_bounds__(RANK_THREADS, 2)
+    few_rows_kernel(RowsWork w, Rows<float> X, const float *W, long long ldw, bool w_wide) {
+    extern __shared__ __align__(16) unsigned char smem_rows[];
+    sg::launch_dependents();
+    few_rows<MT>(w, int(blockIdx.x), X, W, ldw, w_wide, w.partial, smem_rows);
 }
 
 // ------------------------------------------------------------------ the rest

@@ -1267,7 +1267,7 @@ int read_and_clear_error_word(cudaStream_t stream) {
         sgv::staged_variants().error_word, sgv::sweep_variants_a().error_word,
         sgv::sweep_variants_b().error_word, sgv::sweep_variants_c().error_word,
         sgv::tall_variants().error_word, &sgh::parts_gemm_error_word, &sgh::lora_error_word, &sgh::act8_error_word,
-        &sgh::norm_error_word};
+        &sgh::norm_error_word, &sgh::pair_gemm_error_word, &sgh::gated_error_word, &sgh::linear8_error_word};
     unsigned any = 0;
     for (auto word : units) {
         unsigned v = 0;

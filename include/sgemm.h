@@ -81,7 +81,8 @@ int sgemm(int M, int N, int K, float alpha,
 typedef enum {
     SGEMM_ACT_NONE = 0, /* identity */
     SGEMM_ACT_RELU = 1, /* max(z, 0) */
-    SGEMM_ACT_GELU = 2  /* z * Phi(z) = 0.5 z (1 + erf(z / sqrt 2)) */
+    SGEMM_ACT_GELU = 2, /* z * Phi(z) = 0.5 z (1 + erf(z / sqrt 2)) */
+    SGEMM_ACT_SILU = 3  /* z / (1 + exp(-z)); of the gated block alone (sgemm_layers.h) */
 } sgemm_act;
 
 /*

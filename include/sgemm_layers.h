@@ -2,8 +2,9 @@
  * sgemm_layers.h -- the linear layer of a language model around the GEMM of
  * sgemm.h: low-rank adapters of many requests beside a shared projection
  * (forward and backward), activation checkpoints in 8 bits with their use
- * in the backward pass, and the root-mean-square norm before such a layer, with an
- * output in 8 bits.  Part of libsgemm.so; statuses, streams, ownership,
+ * in the backward pass, the root-mean-square norm before such a layer, with an
+ * output in 8 bits and the projection that reads it, and the gated feed-forward
+ * block.  Part of libsgemm.so; statuses, streams, ownership,
  * workspaces and the device error word are those of sgemm.h.
  *
  * Conventions of every entry point here:
@@ -206,6 +207,74 @@ int sgemm_rmsnorm_backward(int type, int M, int K,
                            void *dX, int lddx,
                            void *dw,
                            sgemm_stream_t stream);
+
+/*
+ * sgemm_linear8 -- a projection of rows in 8 bits by a weight in 8 bits with a scale for each
+ * output column:
+ *
+ *   Y[i][j] = scale[i] * wscale[j] * (sum over k of q[i][k] * W[k][j]) + bias[j]     (M x N)
+ *
+ * The rows are given as (q, scale) with X == NULL, or as the matrix X (M x K, of `type`), which the
+ * call brings to rows of 8 bits itself.  W: K x N int8; wscale: N floats; bias: N elements of
+ * `type`, or NULL.  Every int8 value, -128 too, counts as it stands.  The sums are exact, so K is at
+ * most 131071 (SGEMM_ERR_TOO_LARGE); the rest is fp32, rounded once.  K == 0 gives bias, or 0.
+ */
+int sgemm_linear8(int type, int M, int N, int K,
+                  const void *X, int ldx,
+                  const signed char *q, int ldq, const float *scale,
+                  const signed char *W, int ldw, const float *wscale,
+                  const void *bias,
+                  void *Y, int ldy,
+                  sgemm_stream_t stream);
+
+/* ------------------------------------------------------------------ gated block
+ *
+ * Two projections of the same rows, an activation of the one and its product with the other: the
+ * feed-forward block of a language model up to its last projection.  `act`: sgemm_act of sgemm.h,
+ * SGEMM_ACT_SILU among them.  SILU and GELU are +inf at +inf and NaN at -inf, as their formulas
+ * are.
+ */
+
+/*
+ * sgemm_gated -- forward, for one token up to a long prefill:
+ *
+ *   G = X * Wg,  U = X * Wu,  H = act(G) * U                (M x N each)
+ *
+ * X: M x K; Wg, Wu: K x N.  G and U, NULL together, receive the projections for the backward pass;
+ * H is made of their fp32 sums, before they are rounded to `type`.  K == 0 gives zero sums.
+ */
+int sgemm_gated(int type, int M, int N, int K,
+                const void *X, int ldx,
+                const void *Wg, int ldwg,
+                const void *Wu, int ldwu,
+                int act,
+                void *G, int ldg,
+                void *U, int ldu,
+                void *H, int ldh,
+                sgemm_stream_t stream);
+
+/*
+ * sgemm_gated_backward -- the gradients of sgemm_gated for dH (M x N), given X, G and U:
+ *
+ *   dG = dH * U * act'(G),  dU = dH * act(G)
+ *   dX = dG * Wg^T + dU * Wu^T                              (M x K)
+ *   dWg = X^T * dG,  dWu = X^T * dU                         (K x N each)
+ *
+ * relu'(0) is 0.  In bfloat16 dG and dU are rounded to bfloat16 before the products that take them.
+ * dX may be NULL (Wg and Wu are then not read), and dWg and dWu together (X is then not read).
+ * M == 0 or N == 0 gives zeros.  The outputs must not overlap an input or each other.
+ */
+int sgemm_gated_backward(int type, int M, int N, int K, int act,
+                         const void *dH, int lddh,
+                         const void *X, int ldx,
+                         const void *G, int ldg,
+                         const void *U, int ldu,
+                         const void *Wg, int ldwg,
+                         const void *Wu, int ldwu,
+                         void *dX, int lddx,
+                         void *dWg, int lddwg,
+                         void *dWu, int lddwu,
+                         sgemm_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -70,3 +70,79 @@ def norm_backward_reference(dY, V, w, dS, eps):
     if dS is not None:
         dX, dmag = dX + dS.double(), dmag + dS.double().abs()
     return dX, (dY * n).sum(0), dmag, (dY * n).abs().sum(0)
+
+
+# ------------------------------------------------------------------ 8-bit product
+def linear8_reference(q, scale, W, wscale, bias):
+    """(y, magnitude) in 64 bits; the integer sums are exact there too."""
+    v = (q.double() @ W.double()) * scale.double().unsqueeze(1) * wscale.double()
+    mag = v.abs()
+    return (v, mag) if bias is None else (v + bias.double(), mag + bias.double().abs())
+
+
+# ------------------------------------------------------------------ gated block
+def act_reference(z, act):
+    """(act, act') in 64 bits."""
+    z = z.double()
+    if act == "none":
+        return z, torch.where(z == z, 1.0, z)
+    if act == "relu":
+        return torch.where(z < 0, 0.0, z), torch.where(z > 0, 1.0, torch.where(z <= 0, 0.0, z))
+    if act == "silu":
+        s = 1 / (1 + torch.exp(-z))
+        return z * s, s + z * s * (1 / (1 + torch.exp(z)))
+    cdf = 0.5 * torch.erfc(-z / math.sqrt(2.0))
+    return z * cdf, cdf + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+
+
+def act_slack(z, act):
+    """What fp32 makes of (act(z), act'(z)): SILU by an exponential (2 units in the last place of float32; by an
+    argument rounded at |z| in bfloat16), a quotient and products; GELU by a tail whose error is up to 1.5e-7 for
+    bfloat16, and the bell of the derivative by an exponential of z^2 / 2 as the checkpoints' gradient."""
+    z = z.double()
+    value, slope = act_reference(z, act)
+    if act in ("none", "relu"):
+        return torch.zeros_like(z), torch.zeros_like(z)
+    if act == "silu":
+        rel = (z.abs() + 16) * 2.0 ** -23
+        return rel * value.abs(), rel * (1 + value.abs())
+    return 2e-7 * z.abs() + 16 * 2.0 ** -24 * value.abs(), 3e-7 * (1 + z.abs()) + 16 * 2.0 ** -24 * slope.abs()
+
+
+def gated_reference(X, Wg, Wu, act):
+    """(H, G, U) in 64 bits and the fp32 errors that they may have: sums of K products, each of whose additions,
+    products and splittings is off by at most 2^-23 of the sum of magnitudes; H by those of G and U, the
+    slope of an activation being at most 1.13."""
+    X, Wg, Wu = X.double(), Wg.double(), Wu.double()
+    G, U = X @ Wg, X @ Wu
+    unit = (X.shape[1] + 16) * 2.0 ** -23
+    dg, du = unit * (X.abs() @ Wg.abs()), unit * (X.abs() @ Wu.abs())
+    value, _ = act_reference(G, act)
+    slack = 1.13 * dg * (U.abs() + du) + value.abs() * du + act_slack(G, act)[0] * U.abs() + 2.0 ** -23 * (value * U).abs()
+    return value * U, G, U, slack, dg, du
+
+
+def gated_backward_reference(dH, X, Wg, Wu, G, U, act):
+    """(dX, dWg, dWu) in 64 bits and the errors that they may have: those of dG and dU (in bfloat16 a rounding, 2^-8 of
+    the value at most, more than all fp32 ones) through sums of magnitudes, and the sums' own."""
+    half = 2.0 ** -8 if dH.dtype == torch.bfloat16 else 2.0 ** -23
+    dH, X, Wg, Wu, G, U = (t.double() for t in (dH, X, Wg, Wu, G, U))
+    (value, slope), (vs, ss) = act_reference(G, act), act_slack(G, act)
+    dG, dU = dH * U * slope, dH * value
+    eg = (half + 2.0 ** -22) * dG.abs() + ss * (dH * U).abs()
+    eu = (half + 2.0 ** -22) * dU.abs() + vs * dH.abs()
+    un, um = (2 * G.shape[1] + 32) * 2.0 ** -23, (G.shape[0] + 16) * 2.0 ** -23
+    dX = dG @ Wg.t() + dU @ Wu.t()
+    sX = (eg + un * dG.abs()) @ Wg.abs().t() + (eu + un * dU.abs()) @ Wu.abs().t()
+    sg, su = X.abs().t() @ (eg + um * dG.abs()), X.abs().t() @ (eu + um * dU.abs())
+    return dX, X.t() @ dG, X.t() @ dU, sX, sg, su
+
+
+def norm_close(got, ref, what, least=256):
+    """The 2-norm of the difference: the errors of many terms do not all lie on one side.  float32 2e-6 (sums of up to
+    512 terms that truncate, 2^-23 each, then fp32); bfloat16 the rms of two roundings, of the terms and of
+    the result, each at most 2^-8 / sqrt 3."""
+    if ref.numel() < least or float(ref.norm()) == 0:
+        return
+    rel = float((got.detach().cpu().double() - ref.cpu()).norm() / ref.norm())
+    assert rel <= (2.0 ** -8 * math.sqrt(2 / 3) if got.dtype == torch.bfloat16 else 2e-6), f"{what}: relative error {rel:.3e}"
