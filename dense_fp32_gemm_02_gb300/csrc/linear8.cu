@@ -1,5 +1,8 @@
 // linear8.cu -- entry point of the product of int8 matrices with scales for each row and column.
+#include <cstdlib>
+
 #include "layer_host.h"
+#include "byte_tiles.cuh"
 #include "linear8.cuh"
 #include "packed.cuh"
 #include "pair_gemm.h"
@@ -45,6 +48,49 @@ void split_bytes(ByteWork &w, long long slots) {
     w.ranges = int((w.K + (long long)w.range - 1) / w.range);
 }
 
+// The tiles of up to 256 rows and their ranges: the fewest us over the counts of ranges, with 0.19
+// us for each slab of W that an SM reads, 2 to fill and empty a block, and the ranges' sums
+// written and read once at 5 TB/s.
+TileWork tiles_of(const Call &c, int sms) {
+    TileWork w{};
+    w.M = c.M, w.N = c.N, w.K = c.K;
+    w.across = (c.N + TILE_COLS - 1) / TILE_COLS;
+    w.down = (c.M + 255) / 256;
+    w.rows = ((c.M + w.down - 1) / w.down + 15) / 16 * 16;
+    w.timeout_ns = sgh::wait_timeout_ns();
+    const int blocks = w.rows <= 64 ? 2 : 1, slabs = (c.K + TILE_K - 1) / TILE_K;
+    const long long fewest = (c.K + TILE_RANGE - 1LL) / TILE_RANGE, slots = (long long)blocks * sms;
+    double least = 0;
+    for (long long n = fewest; n <= std::min<long long>(slabs, fewest + 64); ++n) {
+        const long long per = (slabs + n - 1) / n;
+        if ((slabs + per - 1) / per != n) continue;   // a range would be empty
+        const long long items = (long long)w.across * w.down * n, waves = (items + slots - 1) / slots;
+        const double cost = double(waves) * (double(per) * 0.19 * blocks + 2.0) + (n > 1 ? 2.0 + double(n) * c.M * c.N * 8.0 / 5.0e6 : 0.0);
+        if (w.ranges == 0 || cost < least) least = cost, w.ranges = int(n), w.range = int(per * TILE_K);
+    }
+    return w;
+}
+
+template <class T, bool ALIGNED>
+int launch_tiles(const Call &c, const TileWork &w) {
+    const auto go = [&](auto of) {
+        constexpr int ROWS = decltype(of)::value;
+        using Z = ByteTile<ROWS, ALIGNED>;
+        const auto kernel = byte_tiles_kernel<T, ROWS, ALIGNED>;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Z::SMEM));
+        if (e != cudaSuccess) return sgh::cuda_fail(e);
+        const long long blocks = (long long)w.across * w.down * w.ranges;
+        if (blocks > 0x7fffffffLL) return int(SGEMM_ERR_TOO_LARGE);
+        return sgh::launch("int8 as float16, tcgen05, W converted on its way", kernel, dim3(unsigned(blocks)), TILE_THREADS, Z::SMEM,
+                           c.stream, w, c.q, c.ldq, c.W, (long long)c.ldw, c.scale, c.wscale, static_cast<const T *>(c.bias),
+                           static_cast<T *>(c.Y), (long long)c.ldy);
+    };
+    return w.rows <= 32   ? go(std::integral_constant<int, 32>{})
+           : w.rows <= 64 ? go(std::integral_constant<int, 64>{})
+           : w.rows <= 128 ? go(std::integral_constant<int, 128>{})
+                           : go(std::integral_constant<int, 256>{});
+}
+
 template <class T>
 int finish(const Call &c, int ranges, const int *partial) {
     return sgh::launch(nullptr, byte_finish_kernel<T>, dim3(unsigned((c.N + 255LL) / 256), unsigned(std::min(c.M, 65535))), 256, 0,
@@ -52,16 +98,21 @@ int finish(const Call &c, int ranges, const int *partial) {
                        static_cast<T *>(c.Y), (long long)c.ldy);
 }
 
+int few_rows_most() { const char *e = getenv("L8_FEW"); return e ? atoi(e) : BYTE_ROWS; }
+int tiles_most() { const char *e = getenv("L8_TILES"); return e ? atoi(e) : 512; }
+
 template <class T>
 int linear8(Call c) {
     int sms, st;
     cudaMemPool_t pool;
     if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
-    const bool own_rows = c.X != nullptr && c.K > 0, few = c.M <= BYTE_ROWS;
+    const bool own_rows = c.X != nullptr && c.K > 0, few = c.M <= few_rows_most(), tiles = !few && c.M <= tiles_most();
     const long long qpitch = (c.K + 15LL) / 16 * 16, xpitch = pitch8(c.K), wpitch = pitch8(c.N);
     const size_t q_bytes = own_rows ? size_t(c.M) * qpitch : 0, s_floats = own_rows ? c.M : 0;
-    const size_t x_elems = few ? 0 : size_t(c.M) * xpitch, w_elems = few ? 0 : size_t(c.K) * wpitch;
+    const bool pack = !few && !tiles;
+    const size_t x_elems = pack ? size_t(c.M) * xpitch : 0, w_elems = pack ? size_t(c.K) * wpitch : 0;
     ByteWork w{};
+    TileWork tw{};
     sgp::Split split{1, 256, 0};
     size_t p_ints = 0;
     if (c.K == 0) {
@@ -69,6 +120,9 @@ int linear8(Call c) {
         w.M = c.M, w.N = c.N, w.K = c.K;
         split_bytes(w, (c.M <= 4 ? 2LL : 1LL) * sms);
         p_ints = size_t(w.ranges) * c.M * c.N;
+    } else if (tiles) {
+        tw = tiles_of(c, sms);
+        p_ints = tw.ranges > 1 ? size_t(tw.ranges) * c.M * c.N : 0;
     } else {
         split = sgq::plan(sgq::BYTES, c.M, c.N, c.K, 1, sms);
         p_ints = split.partial_floats;
@@ -99,6 +153,11 @@ int linear8(Call c) {
         st = sgh::launch("int8, few rows, W read once", wide ? pick(std::true_type{}) : pick(std::false_type{}),
                          dim3(unsigned(blocks)), BYTE_THREADS, 0, c.stream, w, c.q, c.ldq, c.W, (long long)c.ldw);
         if (st == SGEMM_OK) st = finish<T>(c, w.ranges, partial);
+    } else if (tiles) {
+        tw.partial = partial;
+        const bool in_place = sgh::aligned(c.W, 16) && c.ldw % 16 == 0 && sgh::aligned(c.q, 16) && c.ldq % 16 == 0;
+        st = in_place ? launch_tiles<T, true>(c, tw) : launch_tiles<T, false>(c, tw);
+        if (st == SGEMM_OK && partial) st = finish<T>(c, tw.ranges, partial);
     } else {
         const PartsJob<ByteRows> a(ByteRows{c.q, c.ldq}, c.M, c.K, sgh::aligned(c.q, 8) && c.ldq % 8 == 0, xp);
         const PartsJob<ByteRows> b(ByteRows{c.W, c.ldw}, c.K, c.N, sgh::aligned(c.W, 8) && c.ldw % 8 == 0, wp);

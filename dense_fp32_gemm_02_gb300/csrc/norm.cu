@@ -18,6 +18,7 @@ template <class C>
 struct Form {
     Kernel<C> kernel;
     int threads, rows;
+    size_t smem = 0;
 };
 
 template <class T, int KIND, int THREADS, int CHUNKS, bool WIDE, bool LONG = false>
@@ -48,12 +49,13 @@ int forward(const NormCall<T> &c, int sms, cudaStream_t stream) {
 
 template <class T, int THREADS, int CHUNKS, bool WIDE, bool LONG = false>
 Form<NormBackCall<T>> back_form() {
-    return {&norm_backward_kernel<T, THREADS, CHUNKS, WIDE, LONG>, norm_block(THREADS), norm_block(THREADS) / THREADS};
+    return {&norm_backward_kernel<T, THREADS, CHUNKS, WIDE, LONG>, norm_block(THREADS), norm_block(THREADS) / THREADS,
+            NormRing<T, THREADS, CHUNKS, WIDE, LONG>::BYTES};
 }
 template <class T, bool WIDE>
 Form<NormBackCall<T>> backward_form(int K) {
     return K <= 256     ? back_form<T, 32, 1, WIDE>()
-           : K <= 1024  ? back_form<T, 32, 4, WIDE>()
+           : K <= 1024  ? back_form<T, 128, 1, WIDE>()
            : K <= 4096  ? back_form<T, 256, 2, WIDE>()
            : K <= 8192  ? back_form<T, 512, 2, WIDE>()
            : K <= 16384 ? back_form<T, 512, 4, WIDE>()
@@ -73,14 +75,15 @@ int backward(NormBackCall<T> c, T *dw, cudaStream_t stream) {
                       sgh::wide_rows(c.dS, c.ldds) && sgh::wide_rows(c.dX, c.lddx) && sgh::aligned(c.w, 16);
     const auto f = wide ? backward_form<T, true>(c.K) : backward_form<T, false>(c.K);
     int per_sm = 1;
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, f.kernel, f.threads, 0);
+    cudaError_t e = cudaFuncSetAttribute(f.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(f.smem));
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, f.kernel, f.threads, f.smem);
     if (e != cudaSuccess) return sgh::cuda_fail(e);
     const int blocks = int(std::min<long long>((c.M + f.rows - 1LL) / f.rows, (long long)sms * std::max(1, per_sm)));
     sgh::Workspace ws(pool, stream);
     const size_t floats = dw ? size_t(blocks) * c.K : 0;
     if ((st = ws.allocate(sgh::Workspace::piece(floats * 4))) != SGEMM_OK) return st;
     c.partial = dw ? ws.take<float>(floats) : nullptr;
-    f.kernel<<<unsigned(blocks), f.threads, 0, stream>>>(c);
+    f.kernel<<<unsigned(blocks), f.threads, f.smem, stream>>>(c);
     st = sgh::launched(wide ? "norm backward, rows read 16 bytes at a time" : "norm backward, any alignment");
     if (st != SGEMM_OK) return st;
     if (dw) {

@@ -6,8 +6,8 @@
 // q does not depend on rstd, so the row's sum of squares and its largest |p| are taken together in
 // one pass, and q is the exactly rounded quotient whatever order the sum is taken in: 127 p / max is
 // worked out in fp32 (at most 4 roundings, 3.1e-5 in q's units), and where that is within NEAR = 2^-14
-// of a tie the products are compared in 64 bits, where p (16 bits from bfloat16, 48 from float32) is
-// exact.  For this the maximum of float32 products is kept as a pair (value, remainder).
+// of a tie the products are compared exactly (p has 16 bits from bfloat16, 48 from float32, where
+// the maximum is kept as a pair, value and remainder, for it).
 //
 // A row goes to a group of threads (a warp or a block) that keeps it in registers between its
 // two uses, up to 16384 columns; longer rows are read twice (LONG).  Everything is read and
@@ -26,7 +26,7 @@ constexpr float LEAST_TOP = 0x1p-60f, MOST_TOP = 0x1p100f;
 // The range of a row's sum of squares in which no term has overflowed or counts for too little.
 constexpr float LEAST_SQUARES = 0x1p-80f, MOST_SQUARES = 0x1p120f;
 
-__host__ __device__ constexpr int norm_block(int threads) { return threads < 256 ? 256 : threads; }
+__host__ __device__ constexpr int norm_block(int threads) { return threads < 128 ? 256 : threads; }
 
 // Where eight elements `c` of thread `t` lie in a row: together (WIDE, rows that are 16-byte
 // aligned and of a multiple of 8 columns), or a group's width apart, next to the other threads'.
@@ -200,13 +200,23 @@ __device__ __noinline__ double rare_rows8(GroupSums &sm, V v, const T *w, signed
     return top;
 }
 
-// q of |p| near a tie: n or n + 1, n the whole part of the fp32 quotient.
-static __device__ __noinline__ float near_tie(float v, float w, float quotient, float top_hi, float top_lo) {
+// q of |p| near a tie: n or n + 1, n the whole part of the fp32 quotient, by the sign of 127 |p| - (n
+// + 1/2) top.  p of 24 bits (from bfloat16 16): the difference of the products in fp32 is exact, as it
+// is under 2^18 units of p's last place, and so is what (n + 1/2) top leaves.  (In bfloat16 ties are no
+// rare thing: a row whose largest value is 127 / 32 has 32 x for a quotient.)
+__device__ __forceinline__ float tie_exact(float p, float quotient, float top) {
+    const float n = floorf(fabsf(quotient)), h = n + 0.5f, t = h * top;
+    const float d = fmaf(127.0f, fabsf(p), -t) - fmaf(h, top, -t);
+    const bool odd = (int(n) & 1) != 0;
+    return copysignf(d > 0.0f || (d == 0.0f && odd) ? n + 1.0f : n, quotient);
+}
+// The same of a product of float32 values, in 64 bits.
+static __device__ __noinline__ float tie_wide(float v, float w, float quotient, float top_hi, float top_lo) {
     const double p = fabs(double(v) * w), top = double(top_hi) + top_lo;
     const float n = floorf(fabsf(quotient));
     const double d = fma(127.0, p, -(n + 0.5) * top);
-    const bool up = d > 0 || (d == 0 && fmodf(n, 2.0f) == 1.0f);
-    return copysignf(up ? n + 1.0f : n, quotient);
+    const bool odd = (int(n) & 1) != 0;
+    return copysignf(d > 0 || (d == 0 && odd) ? n + 1.0f : n, quotient);
 }
 
 // ------------------------------------------------------------------ forward
@@ -323,12 +333,13 @@ __global__ void __launch_bounds__(norm_block(THREADS))
                     out[e] = rintf(quotient);
                     off = fmaxf(off, fabsf(quotient - out[e]));
                 }
-                if (off > 0.5f - NEAR) {   // one of eight: 1 in 1000
+                if (off > 0.5f - NEAR) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float u = KIND == ROWS8 ? 1.0f : w[e], quotient = v[c][e] * u * times;
+                        const float p = KIND == ROWS8 ? v[c][e] : v[c][e] * w[e], quotient = p * times;
                         if (fabsf(quotient - out[e]) > 0.5f - NEAR)
-                            out[e] = near_tie(v[c][e], u, quotient, top.value(), top.lo);
+                            out[e] = WITH_LO ? tie_wide(v[c][e], w[e], quotient, top.value(), top.lo)
+                                             : tie_exact(p, quotient, top.value());
                     }
                 }
                 at.store_q(q, c, out);
@@ -356,24 +367,101 @@ struct NormBackCall {
     float eps;
 };
 
+// The rows to come stand in a ring of asynchronous copies, each thread's own elements in its own
+// slots, so that they need no barrier; bfloat16 rows that are not 16-byte aligned, and rows that
+// are too long for a ring of two, go from memory to registers.
 template <class T, int THREADS, int CHUNKS, bool WIDE, bool LONG>
-__global__ void __launch_bounds__(norm_block(THREADS))
+struct NormRing {
+    static constexpr size_t STAGE = size_t(3) * CHUNKS * 8 * sizeof(T) * norm_block(THREADS), MOST = 98304;
+    static constexpr bool ON = !LONG && (WIDE || sizeof(T) == 4) && STAGE <= MOST;
+    static constexpr int DEPTH = !ON ? 1 : STAGE * 4 <= MOST ? 4 : STAGE * 3 <= MOST ? 3 : 2;
+    static constexpr size_t BYTES = ON ? DEPTH * STAGE : 0;
+};
+template <int THREADS, int CHUNKS>
+constexpr int norm_blocks_per_sm = THREADS == 128 ? 6 : THREADS == 512 ? 1 : 2;
+
+template <class T, int THREADS, int CHUNKS, bool WIDE, bool LONG>
+__global__ void __launch_bounds__(norm_block(THREADS), norm_blocks_per_sm<THREADS, CHUNKS>)
     norm_backward_kernel(const NormBackCall<T> a) {
-    constexpr int GROUPS = norm_block(THREADS) / THREADS, SPAN = THREADS * 8 * CHUNKS;
+    constexpr int BLOCK = norm_block(THREADS), GROUPS = BLOCK / THREADS, SPAN = THREADS * 8 * CHUNKS;
+    using Ring = NormRing<T, THREADS, CHUNKS, WIDE, LONG>;
+    constexpr bool KEEP_W = !LONG && CHUNKS <= 2;
+    extern __shared__ __align__(16) unsigned char norm_ring[];
     __shared__ GroupSums sm;
     __shared__ float columns[GROUPS > 1 ? SPAN : 1];
     const int t = threadIdx.x % THREADS, group = threadIdx.x / THREADS;
     if (!SG_IN_RANGE(LONG || a.K <= SPAN)) return;
     float *partial = a.partial ? a.partial + (long long)blockIdx.x * a.K : nullptr;
-    float v[CHUNKS][8], dy[CHUNKS][8], dw[LONG ? 1 : CHUNKS][8] = {}, w[8];
-    int turn = 0;
+    const long long step = (long long)gridDim.x * GROUPS;
+    long long row = (long long)blockIdx.x * GROUPS + group;
+
+    // Element e of chunk c of matrix m: 16 bytes at a time, or one by one next to the other threads'.
+    auto slot = [&](int stage, int m, int c, int e) {
+        constexpr int PER = 16 / int(sizeof(T));
+        const int at = ((stage * 3 + m) * CHUNKS + c) * 8;
+        return reinterpret_cast<T *>(norm_ring) +
+               (WIDE ? (at + e / PER * PER) * BLOCK + int(threadIdx.x) * PER + e % PER : (at + e) * BLOCK + int(threadIdx.x));
+    };
+    auto issue = [&](int stage, long long r) {
+        if constexpr (Ring::ON) {
+            const Place<THREADS, WIDE> at{a.K, 0, t};
+            if (r < a.M)
+#pragma unroll
+                for (int m = 0; m < 3; ++m) {
+                    const T *p = m == 0 ? a.V + r * a.ldv : m == 1 ? a.dY + r * a.lddy : a.dS + r * a.ldds;
+                    if (m == 2 && !a.dS) break;
+#pragma unroll
+                    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+                        for (int e = 0; e < 8; e += WIDE ? 16 / int(sizeof(T)) : 1) {
+                            const uint32_t to = sg::smem_addr(slot(stage, m, c, e));
+                            const bool in = at.column(c, e) < a.K;
+                            const T *from = in ? p + at.column(c, e) : p;
+                            if constexpr (WIDE) sg::cp_async16(to, from, in ? 16u : 0u);
+                            else sg::cp_async4(to, from, in ? 4u : 0u);
+                        }
+                }
+            sg::cp_async_commit();
+        }
+    };
+    auto take = [&](int stage, int m, int c, float (&x)[8]) {
+        if constexpr (WIDE && sizeof(T) == 4) {
+            float lo[4], hi[4];
+            load4(slot(stage, m, c, 0), lo);
+            load4(slot(stage, m, c, 4), hi);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = lo[e], x[e + 4] = hi[e];
+        } else if constexpr (WIDE) {
+            load8(slot(stage, m, c, 0), x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = to_f32(*slot(stage, m, c, e));
+        }
+    };
+
+    float v[CHUNKS][8], dy[CHUNKS][8], dw[LONG ? 1 : CHUNKS][8] = {}, w[KEEP_W ? CHUNKS : 1][8];
+    auto weight = [&](const Place<THREADS, WIDE> &at, int c) -> float(&)[8] {
+        if (!KEEP_W) at.load(a.w, c, w[0]);
+        return w[KEEP_W ? c : 0];
+    };
+#pragma unroll
+    for (int c = 0; KEEP_W && c < CHUNKS; ++c) Place<THREADS, WIDE>{a.K, 0, t}.load(a.w, c, w[c]);
+#pragma unroll
+    for (int d = 0; Ring::ON && d < Ring::DEPTH; ++d) issue(d, row + d * step);
+    int turn = 0, stage = 0;
     bool first = true;
-    for (long long row = (long long)blockIdx.x * GROUPS + group; row < a.M; row += (long long)gridDim.x * GROUPS) {
+    for (; row < a.M; row += step) {
         const T *vr = a.V + row * a.ldv, *dyr = a.dY + row * a.lddy, *dsr = a.dS ? a.dS + row * a.ldds : nullptr;
         T *dxr = a.dX + row * a.lddx;
         auto read = [&](const Place<THREADS, WIDE> &at) {
+            if constexpr (Ring::ON) sg::cp_async_wait<Ring::DEPTH - 1>();
 #pragma unroll
-            for (int c = 0; c < CHUNKS; ++c) at.load(vr, c, v[c]), at.load(dyr, c, dy[c]);
+            for (int c = 0; c < CHUNKS; ++c) {
+                if constexpr (Ring::ON)
+                    take(stage, 0, c, v[c]), take(stage, 1, c, dy[c]);
+                else
+                    at.load(vr, c, v[c]), at.load(dyr, c, dy[c]);
+            }
         };
         float squares = 0.0f, gv = 0.0f;
         Top none{};
@@ -382,14 +470,14 @@ __global__ void __launch_bounds__(norm_block(THREADS))
             read(at);
 #pragma unroll
             for (int c = 0; c < CHUNKS; ++c) {
-                at.load(a.w, c, w);
+                const float(&u)[8] = weight(at, c);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     squares = fmaf(v[c][e], v[c][e], squares);
-                    gv = fmaf(dy[c][e] * w[e], v[c][e], gv);
+                    gv = fmaf(dy[c][e] * u[e], v[c][e], gv);
                 }
             }
-            }
+        }
         group_reduce<THREADS, true, false, false>(sm, turn, squares, gv, none);
         turn ^= 1;
         float rstd = 1.0f / sqrtf(squares / float(a.K) + a.eps), mean = gv * rstd / float(a.K);
@@ -403,20 +491,25 @@ __global__ void __launch_bounds__(norm_block(THREADS))
         for (int base = 0; base < (LONG ? a.K : 1); base += SPAN) {
             const Place<THREADS, WIDE> at{a.K, base, t};
             if (LONG) read(at);
+            float ds[CHUNKS][8];
 #pragma unroll
             for (int c = 0; c < CHUNKS; ++c) {
-                float out[8];
-                if (dsr) {
-                    at.load(dsr, c, out);
-                } else {
+                if (!dsr) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) out[e] = 0.0f;
+                    for (int e = 0; e < 8; ++e) ds[c][e] = 0.0f;
+                } else if constexpr (Ring::ON) {
+                    take(stage, 2, c, ds[c]);
+                } else {
+                    at.load(dsr, c, ds[c]);
                 }
-                at.load(a.w, c, w);
+            }
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) {
+                const float(&u)[8] = weight(at, c);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float n = v[c][e] * rstd;
-                    out[e] = fmaf(rstd, fmaf(-mean, n, dy[c][e] * w[e]), out[e]);
+                    ds[c][e] = fmaf(rstd, fmaf(-mean, n, dy[c][e] * u[e]), ds[c][e]);
                     if (!LONG) {
                         dw[c][e] = fmaf(dy[c][e], n, dw[c][e]);
                     } else if (partial && at.column(c, e) < a.K) {   // (this thread's own column)
@@ -424,11 +517,14 @@ __global__ void __launch_bounds__(norm_block(THREADS))
                         *p = fmaf(dy[c][e], n, first ? 0.0f : *p);
                     }
                 }
-                at.store(dxr, c, out);
+                at.store(dxr, c, ds[c]);
             }
-            }
+        }
+        issue(stage, row + Ring::DEPTH * step);
+        stage = stage + 1 == Ring::DEPTH ? 0 : stage + 1;
         first = false;
     }
+    if constexpr (Ring::ON) sg::cp_async_wait<0>();
     if (LONG || !partial) return;
     const Place<THREADS, WIDE> at{a.K, 0, t};
     for (int g = 0; g < GROUPS; ++g) {   // a block's warps in order
@@ -448,7 +544,7 @@ __global__ void __launch_bounds__(norm_block(THREADS))
     }
     if (GROUPS == 1) return;
     __syncthreads();
-    for (int j = threadIdx.x; j < a.K; j += norm_block(THREADS)) partial[j] = columns[j];
+    for (int j = threadIdx.x; j < a.K; j += BLOCK) partial[j] = columns[j];
 }
 
 // dw from the blocks' sums: 32 columns to a block, its warps' shares of the sums in order.

@@ -48,7 +48,7 @@ struct Params {
 };
 
 // Slabs of a chunk of the accumulation: see parts_gemm.cuh; BYTES 1024 k.
-__host__ __device__ constexpr int chunk_slabs(bool several, bool bytes) { return bytes ? 16 : several ? sgp::CHUNK : sgp::LONG_CHUNK; }
+__host__ __device__ constexpr int chunk_slabs(bool several, bool bytes) { return bytes ? 16 : several ? 4 : sgp::LONG_CHUNK; }
 
 // The work of a pair of CTAs, as sgp::Items; columns of an output are `cols` from col0, of which
 // this CTA loads `load` from load0 of matrix `which`.
