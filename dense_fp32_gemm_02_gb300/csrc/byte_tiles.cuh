@@ -1,20 +1,23 @@
 // byte_tiles.cuh -- the product of int8 matrices of up to 256 rows to a tile on the tensor cores, W brought
-// to float16 on its way into shared memory.
+// to float16 inside shared memory.
 //
 // Bound by reading W once.  The rows are the MMA's narrow side: a tile is 128 columns of W (the MMA's M) by
-// up to 256 rows of X (its N), and a block has one tile and one range of at most 1024 of the
-// contraction.  Every int8 is exactly a float16, a sum of 1024 products of two is at most 2^24, so
-// the fp32 accumulator holds it exactly; the ranges' sums are added as int32 (byte_finish_kernel).
+// up to 256 rows of X (its N), and a block has one tile and one range of the contraction.  The ranges of a
+// tile, up to 8, are a cluster, whose blocks add each other's sums as int32 and share the rows out.
+// Every int8 is exactly a float16 and a sum of 1024 products of two is at most 2^24, so an fp32
+// accumulator holds it exactly; every 1024 k it goes to int32 registers, while the next one fills.
 //
-// 288 threads.  Warps 0 to 7 copy 64 k at a time, several slabs ahead (16 bytes to a copy, each
-// thread its own bytes in its own slots, so that a copy is waited for without a barrier), turn
-// their bytes into float16 (a byte plus 128 under the exponent of 1024, less 1152: three
-// instructions for four) and store them where the MMA wants them (128-byte swizzle: W with its
-// columns, X with its k next to each other).  Warp 8 issues the MMAs.  At the end warps 0 to 7 take the
-// accumulator out, a lane to a column of W.
+// 576 threads.  Warp 16 copies slabs of 64 k of both matrices' bytes by TMA, several ahead.  Warps 0 to
+// 15 turn them into float16 (a byte plus 128 under the exponent of 1024, less 1152: five instructions
+// for four) and store them where the MMA wants them (128-byte swizzle: W with its columns, X with its k
+// next to each other), a thread 16 bytes at a time, in teams, a slab and a stage to each.  Warp 17
+// issues the MMAs.  At the end warps 0 to 15 take the accumulators out, a lane to a column of W.
 //
-// W's rows that are not 16-byte aligned take two copies, and their bytes are shifted into place in
-// registers.
+// Measured with parts left out: at 64 x 8192 x 8192 (30 us) the converting warps' steps, mostly
+// latency, set the pace (0.36 us a slab on an SM, of which loads, stores, conversion and MMAs each save under a
+// tenth); small calls are 5 us of launch, hand-overs and the cluster's sums.  Reading the bytes straight
+// into registers, with the freed memory for more stages, took 12.0 us for 11.9 at 64 x 4096 x 4096
+// and 24.9 for 20.0 at 256 rows.
 #pragma once
 
 #include "linear8.cuh"
@@ -22,28 +25,30 @@
 
 namespace sgl {
 
-constexpr int TILE_COLS = 128, TILE_K = 64, TILE_RANGE = 1024, TILE_THREADS = 288, TILE_COPIERS = 256;
+constexpr int TILE_COLS = 128, TILE_CHUNK = 1024, TILE_CONVERTERS = 512, TILE_THREADS = TILE_CONVERTERS + 64;
+constexpr int MOST_CLUSTER = 8;
 
 struct TileWork {
     int M, N, K;
-    int across, down, ranges, range;   // tiles of columns, of rows; range: a multiple of 64
+    int across, down, ranges, range;   // tiles of columns, of rows; range: a multiple of 128
     int rows;                          // of a tile: a multiple of 16
-    int *partial;                      // ranges x M x N; null (one range): Y
     unsigned long long timeout_ns;
 };
 
-// ROWS: of a tile at most.  ALIGNED: the rows of W and of q can be copied 16 bytes at a time.
-template <int ROWS, bool ALIGNED>
+// ROWS: of a tile at most.
+template <int ROWS>
 struct ByteTile {
-    static constexpr int BLOCKS = ROWS <= 64 ? 2 : 1;          // to an SM
-    static constexpr int W_UNITS = 2, X_UNITS = ROWS * 4 > TILE_COPIERS ? ROWS * 4 / TILE_COPIERS : 1;   // of 16 bytes, to a thread
-    static constexpr int UNIT = ALIGNED ? 1 : 2;               // copies to a unit
-    static constexpr int SLAB = (W_UNITS + X_UNITS) * UNIT * 16 * TILE_COPIERS;
-    static constexpr int DEPTH = ROWS == 256 && !ALIGNED ? 2 : ROWS == 128 && ALIGNED ? 6 : ALIGNED ? 4 : ROWS <= 64 ? 2 : 3;
-    static constexpr int W_BYTES = TILE_COLS * TILE_K * 2, X_BYTES = ROWS * TILE_K * 2, STAGE = W_BYTES + X_BYTES, STAGES = 2;
-    static constexpr size_t SMEM = size_t(STAGES) * STAGE + size_t(DEPTH) * SLAB + 1024 + 128;
-    static constexpr uint32_t TMEM = ROWS < 32 ? 32 : ROWS;
-    static_assert(SMEM * BLOCKS + 1024 * BLOCKS <= 228 * 1024, "shared memory of an SM");
+    static constexpr int STEP = 64;                                       // k of a slab
+    static constexpr int W_RAW = TILE_COLS * STEP, X_RAW = ROWS * STEP, RAW = W_RAW + X_RAW;
+    static constexpr int TEAMS = ROWS <= 128 ? 4 : 2, TEAM = TILE_CONVERTERS / TEAMS;
+    static constexpr int W_EACH = W_RAW / 16 / TEAM, X_EACH = X_RAW / 16 / TEAM;   // units of 16 bytes, to a thread
+    static constexpr int STAGES = TEAMS, STAGE = 2 * RAW;
+    static constexpr int DEPTH = ROWS == 32 ? 12 : ROWS == 64 ? 8 : ROWS == 128 ? 5 : 4;
+    static constexpr size_t SMEM = size_t(STAGES) * STAGE + size_t(DEPTH) * RAW + 1024 + 512;
+    static constexpr uint32_t TMEM = 2 * ROWS;                            // two accumulators
+    static constexpr int PER_CHUNK = TILE_CHUNK / STEP, GROUPS = ROWS > 64 ? ROWS / 64 : 1;
+    static_assert(SMEM <= 232448, "shared memory of a block");
+    static_assert(ROWS * TILE_COLS * 4 <= STAGES * STAGE + DEPTH * RAW, "the sums take their place");
 };
 
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
@@ -63,50 +68,60 @@ __device__ __forceinline__ uint2 halves_of(uint32_t w) {
     asm("sub.f16x2 %0, %1, %2;" : "=r"(out.y) : "r"(hi), "r"(0x64806480u));
     return out;
 }
-
-// Bytes from `shift` of the 32 in a and b.
-__device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int shift) {
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    if (shift & 8) {
-#pragma unroll
-        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-    }
-    if (shift & 4) {
-#pragma unroll
-        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-    }
-    const int bits = (shift & 3) * 8;
-    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+__device__ __forceinline__ uint4 lds_words(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts_words(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-template <class T, int ROWS, bool ALIGNED>
-__global__ void __launch_bounds__(TILE_THREADS, ByteTile<ROWS, ALIGNED>::BLOCKS)
-    byte_tiles_kernel(const TileWork w, const signed char *X, long long ldx, const signed char *W, long long ldw,
+template <class T, int ROWS>
+__global__ void __launch_bounds__(TILE_THREADS, 1)
+    byte_tiles_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mW, const TileWork w,
                       const float *scale, const float *wscale, const T *bias, T *Y, long long ldy) {
-    using Z = ByteTile<ROWS, ALIGNED>;
+    using Z = ByteTile<ROWS>;
     using namespace sg;
     using namespace sg::t3;
+    constexpr int WARPS = TILE_CONVERTERS / 32;
     extern __shared__ unsigned char smem_tiles[];
     const uintptr_t base = (reinterpret_cast<uintptr_t>(smem_tiles) + 1023) & ~uintptr_t(1023);
     const uint32_t stages = smem_addr(reinterpret_cast<void *>(base)), raw = stages + Z::STAGES * Z::STAGE;
-    uint64_t *full = reinterpret_cast<uint64_t *>(base + Z::STAGES * Z::STAGE + Z::DEPTH * Z::SLAB);
-    uint64_t *empty = full + Z::STAGES;
-    uint64_t *done = empty + Z::STAGES;
-    uint32_t *tmem_base = reinterpret_cast<uint32_t *>(done + 1);
+    uint64_t *full = reinterpret_cast<uint64_t *>(base + Z::STAGES * Z::STAGE + Z::DEPTH * Z::RAW);
+    uint64_t *empty = full + Z::STAGES;       // converters -> MMA and back
+    uint64_t *landed = empty + Z::STAGES;     // copies -> converters
+    uint64_t *taken = landed + Z::DEPTH;      // and back
+    uint64_t *acc_full = taken + Z::DEPTH;    // MMA -> converters, [2]
+    uint64_t *acc_empty = acc_full + 2;       // and back
+    uint64_t *drain = acc_empty + 2;
+    uint32_t *tmem_base = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_base + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < Z::STAGES; ++s) {
-            mbar_init(&full[s], TILE_COPIERS / 32);
+            mbar_init(&full[s], WARPS / Z::TEAMS);
             mbar_init(&empty[s], 1);
         }
-        mbar_init(done, 1);
+        for (int d = 0; d < Z::DEPTH; ++d) {
+            mbar_init(&landed[d], 1);
+            mbar_init(&taken[d], WARPS / Z::TEAMS);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&acc_full[a], 1);
+            mbar_init(&acc_empty[a], WARPS);
+        }
+        mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == TILE_COPIERS / 32) tmem_alloc(tmem_base, Z::TMEM);
+    if (warp == WARPS + 1) {
+        tmem_alloc(tmem_base, Z::TMEM);
+    } else if (warp == WARPS && lane == 0) {
+        tma_prefetch_desc(&mX);
+        tma_prefetch_desc(&mW);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -114,187 +129,229 @@ __global__ void __launch_bounds__(TILE_THREADS, ByteTile<ROWS, ALIGNED>::BLOCKS)
     launch_dependents();
     const uint32_t taddr = *tmem_base;
 
-    // blocks of the same columns and range are neighbours: their W comes from L2
-    int b = int(blockIdx.x);
-    const int tm = b % w.down;
-    b /= w.down;
-    const int n0 = (b % w.across) * TILE_COLS, q = b / w.across;
-    const int m0 = tm * w.rows, rows = min(w.rows, (w.M - m0 + 15) & ~15);   // of the MMA
-    const int k0 = q * w.range, kn = min(w.range, w.K - k0), slabs = (kn + TILE_K - 1) / TILE_K;
-    const bool sane = SG_IN_RANGE(kn > 0 && kn <= TILE_RANGE && n0 < w.N && m0 < w.M && q < w.ranges && rows <= ROWS);
-
-    bool ok = sane;
+    // a tile's ranges are neighbours (a cluster), then the tiles of the same columns, whose W comes from L2
+    const int q = int(blockIdx.x) % w.ranges, tile = int(blockIdx.x) / w.ranges;
+    const int m0 = (tile % w.down) * w.rows, n0 = (tile / w.down) * TILE_COLS;
+    const int rows = min(w.rows, (w.M - m0 + 15) & ~15);   // of the MMA
+    const int k0 = q * w.range, kn = min(w.range, w.K - k0);
+    const bool sane = SG_IN_RANGE(kn > 0 && n0 < w.N && m0 < w.M && rows <= ROWS && w.rows <= ROWS);
+    const int slabs = sane ? (kn + Z::STEP - 1) / Z::STEP : 0;
     auto give_up = [&](unsigned what) {
         atomicOr(&g_error_word, what);
         *abort_flag = 1;
-        ok = false;
     };
-    if (warp < TILE_COPIERS / 32) {
-        // ================================================================ copies and conversion
-        const int t = threadIdx.x;
-        // Unit i of W: 16 columns of row k of the slab; of X: 16 k of a row.
-        auto w_at = [&](int i, int &k, int &c) { k = (t + i * TILE_COPIERS) >> 3, c = (t & 7) * 16; };
-        auto x_at = [&](int i, int &m, int &k) { m = (t + i * TILE_COPIERS) >> 2, k = (t & 3) * 16; };
-        auto slot = [&](int depth, int unit, int part) {
-            return raw + uint32_t(depth * Z::SLAB + ((unit * Z::UNIT + part) * TILE_COPIERS + t) * 16);
-        };
-        // `n` bytes from p (at most 16, the rest zero; `first`: the matrix's first byte) to a unit's slots.
-        auto copy = [&](int depth, int unit, const signed char *p, int n, const signed char *first) {
-            n = max(0, min(16, n));
-            if constexpr (ALIGNED) {
-                cp_async16(slot(depth, unit, 0), n > 0 ? p : first, uint32_t(n));
-            } else {
-                const int shift = int(reinterpret_cast<uintptr_t>(p) & 15);
-                const signed char *from = p - shift;
-                if (from < first && n > 0) {   // (it would begin before the matrix)
-                    uint32_t word[8] = {};
+    const int col = n0 + lane * 4;   // of the output, a warp to a row
+    float of[4] = {}, add[4] = {}, row_scale = 0.0f;   // (lane i: of the warp's i-th row)
+    int sum[Z::GROUPS][16];          // the tile's: a lane's column, 16 rows of each 64
+
+    if (warp < WARPS) {
+        // ================================================================ bytes to float16
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (i < n) {
-                            const int at = shift + i;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (at >> 2 == j) word[j] |= (uint32_t(p[i]) & 0xffu) << (8 * (at & 3));
-                        }
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot(depth, unit, 0)), "r"(word[0]),
-                                 "r"(word[1]), "r"(word[2]), "r"(word[3]) : "memory");
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot(depth, unit, 1)), "r"(word[4]),
-                                 "r"(word[5]), "r"(word[6]), "r"(word[7]) : "memory");
-                } else {
-                    const int head = n > 0 ? min(16, shift + n) : 0, tail = n > 0 ? max(0, shift + n - 16) : 0;
-                    const signed char *some = reinterpret_cast<const signed char *>(reinterpret_cast<uintptr_t>(first) & ~uintptr_t(15));
-                    cp_async16(slot(depth, unit, 0), head ? from : some, uint32_t(head));
-                    cp_async16(slot(depth, unit, 1), tail ? from + 16 : some, uint32_t(tail));
-                }
-            }
-        };
-        auto issue = [&](int s) {
-            if (s < slabs) {
-                const int depth = s % Z::DEPTH, ks = s * TILE_K;
-#pragma unroll
-                for (int i = 0; i < Z::W_UNITS; ++i) {
-                    int k, c;
-                    w_at(i, k, c);
-                    copy(depth, i, W + (long long)(k0 + ks + k) * ldw + n0 + c, ks + k < kn ? w.N - n0 - c : 0, W);
-                }
-#pragma unroll
-                for (int i = 0; i < Z::X_UNITS; ++i) {
-                    int m, k;
-                    x_at(i, m, k);
-                    if (m < ROWS)
-                        copy(depth, Z::W_UNITS + i, X + (long long)(m0 + m) * ldx + k0 + ks + k,
-                             m < rows && m0 + m < w.M ? kn - ks - k : 0, X);
-                }
-            }
-            cp_async_commit();
-        };
-        auto take = [&](int depth, int unit, const signed char *p) {
-            auto load = [&](int part) {
-                uint4 v;
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(slot(depth, unit, part)) : "memory");
-                return v;
-            };
-            if constexpr (ALIGNED) return load(0);
-            return shifted(load(0), load(1), int(reinterpret_cast<uintptr_t>(p) & 15));
-        };
-        // 16 values to the halves of a 128-byte line: chunks `chunk` and the one after, swizzled
-        auto put = [&](uint32_t line, int chunk, int row, uint4 v) {
-            const uint2 a = halves_of(v.x), b = halves_of(v.y), c = halves_of(v.z), d = halves_of(v.w);
-            const uint32_t at = line + uint32_t((chunk ^ (row & 7)) << 4), at1 = line + uint32_t(((chunk + 1) ^ (row & 7)) << 4);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a.x), "r"(a.y), "r"(b.x), "r"(b.y) : "memory");
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at1), "r"(c.x), "r"(c.y), "r"(d.x), "r"(d.y) : "memory");
-        };
-        if (sane) {
-#pragma unroll 1
-            for (int s = 0; s < Z::DEPTH; ++s) issue(s);
+        for (int d = 0; d < 4; ++d) {   // (early: they are needed at the end)
+            if (col + d < w.N) of[d] = wscale[col + d];
+            if (bias && col + d < w.N) add[d] = to_f32(bias[col + d]);
         }
-        uint32_t phase = 0;
-        for (int s = 0; s < slabs && ok; ++s) {
-            const int stage = s % Z::STAGES, depth = s % Z::DEPTH, ks = s * TILE_K;
-            cp_async_wait<Z::DEPTH - 1>();
-            // first use of a stage: parity 1 counts as complete
-            if (*abort_flag || !mbar_wait(&empty[stage], phase ^ 1u, w.timeout_ns)) {
-                if (!*abort_flag) atomicOr(&g_error_word, ERR_EMPTY_WAIT);
-                *abort_flag = 1;
-                ok = false;
-            }
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            const uint32_t st = stages + uint32_t(stage * Z::STAGE);
+        const long long own = m0 + q + (warp + lane * WARPS) * (long long)w.ranges;
+        if (own < w.M) row_scale = scale[own];
+        // where a unit's 16 values go in the team's stage: two 16-byte chunks of a 128-byte line, swizzled
+        constexpr int TEAM = Z::TEAM;
+        const int team = int(threadIdx.x) / TEAM, t = int(threadIdx.x) % TEAM;
+        // W: 16 columns of a k, of two groups of 64 columns; X: 16 k of a row; units TEAM apart lie in the same place of
+        // other lines.  (Four threads to a line's bytes and the next four to the next line's: their chunks, all
+        // even ones, are swizzled to even and to odd places.)
+        const int wk = ((t >> 2) & 7) | (t >> 6) << 3, wg = (t >> 5) & 1, xm = t >> 2, c = t & 3;
+        const uint32_t stage = stages + uint32_t(team * Z::STAGE);
+        const uint32_t w_line = stage + uint32_t(wg * int(sgp::GROUP_BYTES) + wk * 128), x_line = stage + uint32_t(2 * Z::W_RAW + xm * 128);
+        const uint32_t w_to = w_line + uint32_t((2 * c ^ (wk & 7)) << 4), w_to1 = w_line + uint32_t(((2 * c + 1) ^ (wk & 7)) << 4);
+        const uint32_t x_to = x_line + uint32_t((2 * c ^ (xm & 7)) << 4), x_to1 = x_line + uint32_t(((2 * c + 1) ^ (xm & 7)) << 4);
+        const uint32_t w_from = uint32_t(wk * TILE_COLS + wg * 64 + c * 16), x_from = uint32_t(Z::W_RAW + xm * Z::STEP + c * 16);
+        const int x_rows = rows - xm;   // from here on
+        auto put = [&](uint32_t at, uint32_t at1, uint4 v) {
+            const uint2 a = halves_of(v.x), b = halves_of(v.y), d = halves_of(v.z), e = halves_of(v.w);
+            sts_words(at, a.x, a.y, b.x, b.y);
+            sts_words(at1, d.x, d.y, e.x, e.y);
+        };
+        const int quarter = warp & 3, group = warp >> 2;
+        auto take_out = [&](int chunk) {
+            bool ok = mbar_wait(&acc_full[chunk & 1], uint32_t(chunk >> 1) & 1u, w.timeout_ns);
+            if (!ok && !*abort_flag) give_up(ERR_FULL_WAIT);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+            tc_fence_after();
 #pragma unroll
-            for (int i = 0; i < Z::W_UNITS; ++i) {
-                int k, c;
-                w_at(i, k, c);
-                put(st + uint32_t((c >> 6) * sgp::GROUP_BYTES + k * 128), (c & 63) >> 3, k,
-                    take(depth, i, W + (long long)(k0 + ks + k) * ldw + n0 + c));
-            }
+            for (int g = 0; g < Z::GROUPS; ++g) {
+                const int c = group * 16 + g * 64;
+                if (c >= rows) break;
+                float v[16];
+                tmem_add16(taddr + uint32_t((chunk & 1) * ROWS + c) + (uint32_t(quarter * 32) << 16), v, false);
 #pragma unroll
-            for (int i = 0; i < Z::X_UNITS; ++i) {
-                int m, k;
-                x_at(i, m, k);
-                if (m < rows)
-                    put(st + uint32_t(Z::W_BYTES + m * 128), k >> 3, m,
-                        take(depth, Z::W_UNITS + i, X + (long long)(m0 + m) * ldx + k0 + ks + k));
+                for (int i = 0; i < 16; ++i) sum[g][i] = __float2int_rn(v[i]) + (chunk > 0 ? sum[g][i] : 0);
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMA reads them
+            tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&full[stage]);
-            issue(s + Z::DEPTH);
-            if (stage == Z::STAGES - 1) phase ^= 1u;
+            if (lane == 0) mbar_arrive(&acc_empty[chunk & 1]);
+            return true;
+        };
+        int taken_out = 0;
+        bool ok = true;
+        for (int s = team, use = 0; s < slabs; s += Z::TEAMS, ++use) {
+            // (first use of a stage: parity 1 counts as complete)
+            const int depth = s % Z::DEPTH;
+            ok = mbar_wait(&empty[team], (uint32_t(use) & 1u) ^ 1u, w.timeout_ns) &&
+                 mbar_wait(&landed[depth], uint32_t(s / Z::DEPTH) & 1u, w.timeout_ns);
+            if (!ok && !*abort_flag) give_up(ERR_FULL_WAIT);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            const uint32_t from = raw + uint32_t(depth * Z::RAW);
+            uint4 v[Z::W_EACH > Z::X_EACH ? Z::W_EACH : Z::X_EACH];
+#pragma unroll
+            for (int i = 0; i < Z::W_EACH; ++i) v[i] = lds_words(from + w_from + uint32_t(i * (TEAM / 8) * TILE_COLS));
+#pragma unroll
+            for (int i = 0; i < Z::W_EACH; ++i) put(w_to + uint32_t(i * (TEAM / 8) * 128), w_to1 + uint32_t(i * (TEAM / 8) * 128), v[i]);
+#pragma unroll
+            for (int i = 0; i < Z::X_EACH; ++i)
+                if (i * (TEAM / 4) < x_rows) v[i] = lds_words(from + x_from + uint32_t(i * (TEAM / 4) * Z::STEP));
+#pragma unroll
+            for (int i = 0; i < Z::X_EACH; ++i)
+                if (i * (TEAM / 4) < x_rows)
+                    put(x_to + uint32_t(i * (TEAM / 4) * 128), x_to1 + uint32_t(i * (TEAM / 4) * 128), v[i]);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMA reads what was written
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&full[team]);
+                mbar_arrive(&taken[depth]);
+            }
+            // a chunk that is done, while the MMAs of this one go on
+            if (taken_out < s / Z::PER_CHUNK && !(ok = take_out(taken_out++))) break;
         }
-        cp_async_wait<0>();
-    } else if (lane == 0) {
+        while (ok && taken_out * Z::PER_CHUNK < slabs) ok = take_out(taken_out++);
+    } else if (warp == WARPS) {
+        // ================================================================ copies
+        int depth = 0, issued = 0;
+        uint32_t phase = 0;
+        for (; issued < slabs; ++issued) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&taken[depth], phase ^ 1u, w.timeout_ns))) {
+                give_up(ERR_EMPTY_WAIT);
+                break;
+            }
+            const uint32_t to = raw + uint32_t(depth * Z::RAW), bar = smem_addr(&landed[depth]);
+            const int k = k0 + issued * Z::STEP;
+            if (elect_one()) {
+                mbar_arrive_expect_tx_at(bar, Z::RAW);
+                tma_load_2d_at(to, &mW, bar, n0, k);
+                tma_load_2d_at(to + Z::W_RAW, &mX, bar, k, m0);
+            }
+            __syncwarp();
+            if (++depth == Z::DEPTH) depth = 0, phase ^= 1u;
+        }
+        if (*abort_flag)   // what is in flight lands before the block ends
+            for (int i = max(0, issued - Z::DEPTH); i < issued; ++i)
+                if (!mbar_wait(&landed[i % Z::DEPTH], uint32_t(i / Z::DEPTH) & 1u, drain_limit_ns(w.timeout_ns))) {
+                    atomicOr(&g_error_word, ERR_DRAIN_WAIT);
+                    break;
+                }
+    } else {
         // ================================================================ MMA issuer
         const uint32_t idesc = (1u << 4) | (1u << 15) | (uint32_t(rows >> 3) << 17) | (uint32_t(TILE_COLS >> 4) << 24);
+        const uint64_t desc_w = sgp::part_desc<true>(stages, 0), desc_x = sgp::part_desc<false>(stages + 2 * Z::W_RAW, 0);
+        int stage = 0, s = 0;
         uint32_t phase = 0;
-        for (int s = 0; s < slabs && ok; ++s) {
-            const int stage = s % Z::STAGES;
-            if (*abort_flag || !mbar_wait(&full[stage], phase, w.timeout_ns)) {
-                give_up(*abort_flag ? 0u : ERR_FULL_WAIT);
+        for (; s < slabs; ++s) {
+            const int chunk = s / Z::PER_CHUNK;
+            const bool first = s % Z::PER_CHUNK == 0;
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, w.timeout_ns) &&
+                                             (!first || mbar_wait(&acc_empty[chunk & 1], (uint32_t(chunk >> 1) & 1u) ^ 1u, w.timeout_ns)))) {
+                give_up(ERR_FULL_WAIT);
                 break;
             }
             tc_fence_after();
-            const uint32_t st = stages + uint32_t(stage * Z::STAGE);
+            const uint32_t acc = taddr + uint32_t((chunk & 1) * ROWS);
+            const uint64_t da = desc_w + uint64_t(stage * (Z::STAGE >> 4)), db = desc_x + uint64_t(stage * (Z::STAGE >> 4));
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < TILE_K / 16; ++kk)
-                mma_f16(taddr, sgp::part_desc<true>(st, kk), sgp::part_desc<false>(st + Z::W_BYTES, kk), idesc, s > 0 || kk > 0);
-            mma_commit(&empty[stage]);
-            if (stage == Z::STAGES - 1) phase ^= 1u;
+                for (int kk = 0; kk < Z::STEP / 16; ++kk) mma_f16(acc, da + kk * (2048 >> 4), db + kk * (32 >> 4), idesc, !first || kk > 0);
+                mma_commit(&empty[stage]);
+                if (s % Z::PER_CHUNK == Z::PER_CHUNK - 1 || s == slabs - 1) mma_commit(&acc_full[chunk & 1]);
+            }
+            if (++stage == Z::STAGES) stage = 0, phase ^= 1u;
         }
-        mma_commit(done);   // of all that were issued
-        if (!mbar_wait(done, 0u, drain_limit_ns(w.timeout_ns))) give_up(ERR_DRAIN_WAIT);
+        if (s < slabs) {   // given up: no MMA may still run when the block ends
+            if (elect_one()) mma_commit(drain);
+            if (!mbar_wait(drain, 0u, drain_limit_ns(w.timeout_ns))) atomicOr(&g_error_word, ERR_DRAIN_WAIT);
+        }
     }
     __syncthreads();
-    if (sane && !*abort_flag && warp < TILE_COPIERS / 32) {
-        // ================================================================ the sums, a lane to a column
-        tc_fence_after();
-        const int quarter = warp & 3, col = n0 + quarter * 32 + lane;
-        const float of = !w.partial && col < w.N ? wscale[col] : 0.0f;
-        const float add = !w.partial && bias && col < w.N ? to_f32(bias[col]) : 0.0f;
-        for (int c = (warp >> 2) * 16; c < rows; c += 32) {
-            float v[16];
-            tmem_add16(taddr + (uint32_t(quarter * 32) << 16) + uint32_t(c), v, false);
-            if (col >= w.N) continue;
+    const bool good = sane && !*abort_flag;
+    const uint32_t sums = stages;   // rows x 128 int32 in the place of all that, which nothing reads any more
+    if (good && warp < WARPS) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const long long m = m0 + c + i;
-                if (m >= w.M || c + i >= rows) continue;
-                if (w.partial) {
-                    w.partial[((long long)q * w.M + m) * w.N + col] = __float2int_rn(v[i]);
-                } else {
-                    const float y = v[i] * (scale[m] * of);
-                    Y[m * ldy + col] = from_f32<T>(bias ? y + add : y);
-                }
+        for (int g = 0; g < Z::GROUPS; ++g) {
+            const int c = (warp >> 2) * 16 + g * 64;
+            if (c >= rows) break;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(sums + uint32_t((c + i) * TILE_COLS + (warp & 3) * 32 + lane) * 4),
+                             "r"(sum[g][i]) : "memory");
+        }
+    }
+    // ================================================================ the cluster's sums, a warp to a row
+    cluster_barrier();
+    if (good && warp < WARPS) {
+        const bool wide = (reinterpret_cast<uintptr_t>(Y) & (4 * sizeof(T) - 1)) == 0 && ldy % 4 == 0 && col + 4 <= w.N;
+        for (int r = q + warp * w.ranges, i = 0; r < rows; r += WARPS * w.ranges, ++i) {   // (i < 16)
+            const long long m = m0 + r;
+            if (m >= w.M) break;
+            const float of_row = __shfl_sync(0xffffffffu, row_scale, i);
+            int s[4] = {};
+#pragma unroll 4
+            for (int c = 0; c < w.ranges; ++c) {
+                uint32_t x[4];
+                asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                             : "r"(dsmem_map(sums + uint32_t(r * TILE_COLS + lane * 4) * 4, uint32_t(c))) : "memory");
+#pragma unroll
+                for (int d = 0; d < 4; ++d) s[d] += int(x[d]);
+            }
+            float y[4];
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {   // (without a bias nothing is added: it would turn -0 into 0)
+                y[d] = float(s[d]) * (of_row * of[d]);
+                y[d] = bias ? y[d] + add[d] : y[d];
+            }
+            T *out = Y + m * ldy + col;
+            if (wide) {
+                store4(out, y);
+            } else {
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    if (col + d < w.N) out[d] = from_f32<T>(y[d]);
             }
         }
-        tc_fence_before();
     }
-    __syncthreads();
+    cluster_barrier();   // this block's sums have been read
     tc_fence_after();
-    if (warp == TILE_COPIERS / 32) {
+    if (warp == WARPS + 1) {
         __syncwarp();
         tmem_dealloc(taddr, Z::TMEM);
+    }
+}
+
+// Rows of bytes at any pitch as rows that are 16-byte aligned (zeros behind them): a
+// thread to 16 bytes.
+static __global__ void __launch_bounds__(256)
+    byte_pitch_kernel(const signed char *p, long long ld, int rows, int cols, Divisor per_row, signed char *out, long long pitch) {
+    sg::wait_prerequisites();
+    sg::launch_dependents();
+    const long long total = (long long)rows * per_row.d, step = (long long)gridDim.x * 256;
+    const bool small = total <= 0x7fffffffll;
+    for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < total; t += step) {
+        const long long i = small ? (long long)per_row.quotient(unsigned(t)) : t / per_row.d;
+        const int c = int(t - i * per_row.d) * 16;
+        if (!SG_IN_RANGE(i < rows && c < cols && c + 16 <= pitch)) continue;
+        const signed char *from = p + i * ld + c;
+        uint32_t word[4] = {};
+#pragma unroll
+        for (int d = 0; d < 16; ++d)
+            if (c + d < cols) word[d / 4] |= (uint32_t(from[d]) & 0xffu) << (8 * (d % 4));
+        *reinterpret_cast<uint4 *>(out + i * pitch + c) = make_uint4(word[0], word[1], word[2], word[3]);
     }
 }
 

@@ -57,6 +57,13 @@ __device__ __forceinline__ void load4(const bf16 *p, float (&v)[4]) {
     v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
 }
 
+__device__ __forceinline__ void store4(float *p, const float (&v)[4]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(bf16 *p, const float (&v)[4]) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+}
+
 // Eight consecutive elements at a 16-byte aligned address.
 __device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
     const float4 a = *reinterpret_cast<const float4 *>(p);

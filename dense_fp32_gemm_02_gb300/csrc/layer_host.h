@@ -50,6 +50,26 @@ int launch(const char *text, void (*kernel)(P...), dim3 grid, unsigned threads, 
     return e == cudaSuccess ? launched(text) : cuda_fail(e);
 }
 
+// The same in clusters of `cluster` blocks.
+template <class... P, class... Args>
+int launch_cluster(const char *text, void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, int cluster, cudaStream_t stream,
+                   const Args &...args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cluster), attr[1].val.clusterDim.y = 1, attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+    return e == cudaSuccess ? launched(text) : cuda_fail(e);
+}
+
 // Rows in 8 bits, each with a scale (norm.cu): q and scale of the rows of X.
 int rows8(int type, int M, int K, const void *X, int ldx, signed char *q, long long ldq, float *scale, int sms,
           cudaStream_t stream);

@@ -1,6 +1,4 @@
 // linear8.cu -- entry point of the product of int8 matrices with scales for each row and column.
-#include <cstdlib>
-
 #include "layer_host.h"
 #include "byte_tiles.cuh"
 #include "linear8.cuh"
@@ -24,7 +22,7 @@ struct Call {
     long long ldq;
     const float *scale;
     const signed char *W;
-    int ldw;
+    long long ldw;
     const float *wscale;
     const void *bias;
     void *Y;
@@ -32,25 +30,8 @@ struct Call {
     cudaStream_t stream;
 };
 
-// The split of K over the grid for few rows: as split_rows (rows.cuh), with partial sums of at most
-// half of W's bytes.
-void split_bytes(ByteWork &w, long long slots) {
-    w.across = (w.N + BYTE_COLS - 1) / BYTE_COLS;
-    constexpr int step = BYTE_THREADS / 32 * 4 * BYTE_STEP;
-    const long long steps = (w.K + step - 1LL) / step, fewest = (w.K + BYTE_RANGE - 1LL) / BYTE_RANGE;
-    const long long most = std::max(fewest, std::min(steps, (long long)w.K / (16LL * w.M)));
-    long long least = 0;
-    for (long long n = fewest; n <= std::min(most, fewest + 64); ++n) {
-        const long long per = (steps + n - 1) / n;
-        const long long cost = ((w.across * n + slots - 1) / slots) * (per + 2);
-        if (n == fewest || cost < least) least = cost, w.range = int(per * step);
-    }
-    w.ranges = int((w.K + (long long)w.range - 1) / w.range);
-}
-
-// The tiles of up to 256 rows and their ranges: the fewest us over the counts of ranges, with 0.19
-// us for each slab of W that an SM reads, 2 to fill and empty a block, and the ranges' sums
-// written and read once at 5 TB/s.
+// The tiles of up to 256 rows and their ranges: the fewest us over the counts of ranges, with 0.35
+// us for each 128 k of a block and 4 to fill and empty it.
 TileWork tiles_of(const Call &c, int sms) {
     TileWork w{};
     w.M = c.M, w.N = c.N, w.K = c.K;
@@ -58,78 +39,99 @@ TileWork tiles_of(const Call &c, int sms) {
     w.down = (c.M + 255) / 256;
     w.rows = ((c.M + w.down - 1) / w.down + 15) / 16 * 16;
     w.timeout_ns = sgh::wait_timeout_ns();
-    const int blocks = w.rows <= 64 ? 2 : 1, slabs = (c.K + TILE_K - 1) / TILE_K;
-    const long long fewest = (c.K + TILE_RANGE - 1LL) / TILE_RANGE, slots = (long long)blocks * sms;
+    const int steps = (c.K + 127) / 128;
     double least = 0;
-    for (long long n = fewest; n <= std::min<long long>(slabs, fewest + 64); ++n) {
-        const long long per = (slabs + n - 1) / n;
-        if ((slabs + per - 1) / per != n) continue;   // a range would be empty
-        const long long items = (long long)w.across * w.down * n, waves = (items + slots - 1) / slots;
-        const double cost = double(waves) * (double(per) * 0.19 * blocks + 2.0) + (n > 1 ? 2.0 + double(n) * c.M * c.N * 8.0 / 5.0e6 : 0.0);
-        if (w.ranges == 0 || cost < least) least = cost, w.ranges = int(n), w.range = int(per * TILE_K);
+    for (int n = 1; n <= std::min(steps, MOST_CLUSTER); ++n) {
+        const int per = (steps + n - 1) / n;
+        if ((steps + per - 1) / per != n) continue;   // a range would be empty
+        const long long items = (long long)w.across * w.down * n, waves = (items + sms - 1) / sms;
+        const double cost = double(waves) * (per * 0.35 + 4.0) + 0.25 * n;
+        if (w.ranges == 0 || cost < least) least = cost, w.ranges = n, w.range = per * 128;
     }
     return w;
 }
 
-template <class T, bool ALIGNED>
+int encode_bytes(CUtensorMap *map, const signed char *p, long long inner, long long outer, long long pitch, uint32_t box_inner,
+                 uint32_t box_outer) {
+    const cuuint64_t dims[2] = {cuuint64_t(inner), cuuint64_t(outer)}, strides[1] = {cuuint64_t(pitch)};
+    const cuuint32_t box[2] = {box_inner, box_outer}, steps[2] = {1, 1};
+    const CUresult r = sgh::encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<signed char *>(p), dims, strides, box,
+                                           steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SGEMM_OK : sgh::driver_fail(int(r));
+}
+
+template <class T>
 int launch_tiles(const Call &c, const TileWork &w) {
     const auto go = [&](auto of) {
         constexpr int ROWS = decltype(of)::value;
-        using Z = ByteTile<ROWS, ALIGNED>;
-        const auto kernel = byte_tiles_kernel<T, ROWS, ALIGNED>;
+        using Z = ByteTile<ROWS>;
+        const auto kernel = byte_tiles_kernel<T, ROWS>;
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Z::SMEM));
         if (e != cudaSuccess) return sgh::cuda_fail(e);
+        CUtensorMap mX, mW;
+        int st = encode_bytes(&mX, c.q, c.K, c.M, c.ldq, Z::STEP, ROWS);
+        if (st == SGEMM_OK) st = encode_bytes(&mW, c.W, c.N, c.K, c.ldw, TILE_COLS, Z::STEP);
+        if (st != SGEMM_OK) return st;
         const long long blocks = (long long)w.across * w.down * w.ranges;
         if (blocks > 0x7fffffffLL) return int(SGEMM_ERR_TOO_LARGE);
-        return sgh::launch("int8 as float16, tcgen05, W converted on its way", kernel, dim3(unsigned(blocks)), TILE_THREADS, Z::SMEM,
-                           c.stream, w, c.q, c.ldq, c.W, (long long)c.ldw, c.scale, c.wscale, static_cast<const T *>(c.bias),
-                           static_cast<T *>(c.Y), (long long)c.ldy);
+        return sgh::launch_cluster("int8 as float16, tcgen05, W converted on its way", kernel, dim3(unsigned(blocks)), TILE_THREADS,
+                                   Z::SMEM, w.ranges, c.stream, mX, mW, w, c.scale, c.wscale,
+                                   static_cast<const T *>(c.bias), static_cast<T *>(c.Y), (long long)c.ldy);
     };
-    return w.rows <= 32   ? go(std::integral_constant<int, 32>{})
-           : w.rows <= 64 ? go(std::integral_constant<int, 64>{})
+    return w.rows <= 32    ? go(std::integral_constant<int, 32>{})
+           : w.rows <= 64  ? go(std::integral_constant<int, 64>{})
            : w.rows <= 128 ? go(std::integral_constant<int, 128>{})
                            : go(std::integral_constant<int, 256>{});
 }
 
+// Bytes whose rows are not 16-byte aligned, at a pitch where they are.
+int pitched(const signed char *p, long long ld, int rows, int cols, signed char *out, long long pitch, int sms, cudaStream_t stream) {
+    const Divisor per_row = Divisor::of(unsigned((cols + 15LL) / 16));
+    const long long units = (long long)rows * per_row.d;
+    return sgh::launch(nullptr, byte_pitch_kernel, dim3(unsigned(std::min<long long>((units + 255) / 256, 32LL * sms))), 256, 0, stream,
+                       p, ld, rows, cols, per_row, out, pitch);
+}
+
 template <class T>
 int finish(const Call &c, int ranges, const int *partial) {
-    return sgh::launch(nullptr, byte_finish_kernel<T>, dim3(unsigned((c.N + 255LL) / 256), unsigned(std::min(c.M, 65535))), 256, 0,
+    return sgh::launch(nullptr, byte_finish_kernel<T>, dim3(unsigned((c.N + 511LL) / 512), unsigned(std::min(c.M, 65535))), 128, 0,
                        c.stream, c.M, c.N, ranges, partial, c.scale, c.wscale, static_cast<const T *>(c.bias),
                        static_cast<T *>(c.Y), (long long)c.ldy);
 }
 
-int few_rows_most() { const char *e = getenv("L8_FEW"); return e ? atoi(e) : BYTE_ROWS; }
-int tiles_most() { const char *e = getenv("L8_TILES"); return e ? atoi(e) : 512; }
+bool aligned_rows(const signed char *p, long long ld) { return sgh::aligned(p, 16) && ld % 16 == 0; }
+
+// Up to so many rows W is brought to float16 on its way; more rows make it worth while to lay both
+// matrices out as bfloat16 first.  us at 4096 x 4096, on its way / laid out: 64 rows 10.6 / 27.6, 256 rows
+// 19.9 / 34.2, 512 rows 31.1 / 37.4, 1024 rows 57 / 43.5.
+constexpr int kTileRows = 512;
 
 template <class T>
 int linear8(Call c) {
     int sms, st;
     cudaMemPool_t pool;
     if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
-    const bool own_rows = c.X != nullptr && c.K > 0, few = c.M <= few_rows_most(), tiles = !few && c.M <= tiles_most();
-    const long long qpitch = (c.K + 15LL) / 16 * 16, xpitch = pitch8(c.K), wpitch = pitch8(c.N);
+    const bool own_rows = c.X != nullptr && c.K > 0, tiles = c.M <= kTileRows;
+    const long long qpitch = (c.K + 15LL) / 16 * 16, xpitch = pitch8(c.K), wpitch = pitch8(c.N), bpitch = (c.N + 15LL) / 16 * 16;
     const size_t q_bytes = own_rows ? size_t(c.M) * qpitch : 0, s_floats = own_rows ? c.M : 0;
-    const bool pack = !few && !tiles;
-    const size_t x_elems = pack ? size_t(c.M) * xpitch : 0, w_elems = pack ? size_t(c.K) * wpitch : 0;
-    ByteWork w{};
+    const size_t x_elems = tiles ? 0 : size_t(c.M) * xpitch, w_elems = tiles ? 0 : size_t(c.K) * wpitch;
     TileWork tw{};
     sgp::Split split{1, 256, 0};
-    size_t p_ints = 0;
+    size_t p_ints = 0, q_copy = 0, w_copy = 0;
     if (c.K == 0) {
-    } else if (few) {
-        w.M = c.M, w.N = c.N, w.K = c.K;
-        split_bytes(w, (c.M <= 4 ? 2LL : 1LL) * sms);
-        p_ints = size_t(w.ranges) * c.M * c.N;
     } else if (tiles) {
         tw = tiles_of(c, sms);
-        p_ints = tw.ranges > 1 ? size_t(tw.ranges) * c.M * c.N : 0;
+        if (!own_rows && !aligned_rows(c.q, c.ldq)) q_copy = size_t(c.M) * qpitch;
+        if (!aligned_rows(c.W, c.ldw)) w_copy = size_t(c.K) * bpitch;
     } else {
         split = sgq::plan(sgq::BYTES, c.M, c.N, c.K, 1, sms);
         p_ints = split.partial_floats;
     }
     sgh::Workspace ws(pool, c.stream);
     const auto piece = [](size_t n) { return sgh::Workspace::piece(n); };
-    st = ws.allocate(piece(q_bytes) + piece(s_floats * 4) + piece(x_elems * 2) + piece(w_elems * 2) + piece(p_ints * 4));
+    st = ws.allocate(piece(q_bytes) + piece(s_floats * 4) + piece(x_elems * 2) + piece(w_elems * 2) + piece(p_ints * 4) +
+                     piece(q_copy) + piece(w_copy));
     if (st != SGEMM_OK) return st;
     signed char *q = ws.take<signed char>(q_bytes);
     float *scale = ws.take<float>(s_floats);
@@ -141,23 +143,18 @@ int linear8(Call c) {
     }
     if (c.K == 0) {
         st = finish<T>(c, 0, nullptr);
-    } else if (few) {
-        w.partial = partial;
-        const bool wide = sgh::aligned(c.W, 16) && c.ldw % 16 == 0;
-        auto pick = [&](auto of) {
-            constexpr bool V = decltype(of)::value;
-            return c.M <= 1 ? byte_rows_kernel<1, V> : c.M <= 2 ? byte_rows_kernel<2, V> : c.M <= 4 ? byte_rows_kernel<4, V> : byte_rows_kernel<8, V>;
-        };
-        const long long blocks = (long long)w.across * w.ranges;
-        if (blocks > 0x7fffffffLL) return SGEMM_ERR_TOO_LARGE;
-        st = sgh::launch("int8, few rows, W read once", wide ? pick(std::true_type{}) : pick(std::false_type{}),
-                         dim3(unsigned(blocks)), BYTE_THREADS, 0, c.stream, w, c.q, c.ldq, c.W, (long long)c.ldw);
-        if (st == SGEMM_OK) st = finish<T>(c, w.ranges, partial);
     } else if (tiles) {
-        tw.partial = partial;
-        const bool in_place = sgh::aligned(c.W, 16) && c.ldw % 16 == 0 && sgh::aligned(c.q, 16) && c.ldq % 16 == 0;
-        st = in_place ? launch_tiles<T, true>(c, tw) : launch_tiles<T, false>(c, tw);
-        if (st == SGEMM_OK && partial) st = finish<T>(c, tw.ranges, partial);
+        if (q_copy) {
+            signed char *to = ws.take<signed char>(q_copy);
+            if ((st = pitched(c.q, c.ldq, c.M, c.K, to, qpitch, sms, c.stream)) != SGEMM_OK) return st;
+            c.q = to, c.ldq = qpitch;
+        }
+        if (w_copy) {
+            signed char *to = ws.take<signed char>(w_copy);
+            if ((st = pitched(c.W, c.ldw, c.K, c.N, to, bpitch, sms, c.stream)) != SGEMM_OK) return st;
+            c.W = to, c.ldw = bpitch;
+        }
+        st = launch_tiles<T>(c, tw);
     } else {
         const PartsJob<ByteRows> a(ByteRows{c.q, c.ldq}, c.M, c.K, sgh::aligned(c.q, 8) && c.ldq % 8 == 0, xp);
         const PartsJob<ByteRows> b(ByteRows{c.W, c.ldw}, c.K, c.N, sgh::aligned(c.W, 8) && c.ldw % 8 == 0, wp);

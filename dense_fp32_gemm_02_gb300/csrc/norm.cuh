@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(norm_block(THREADS))
     constexpr int GROUPS = norm_block(THREADS) / THREADS, SPAN = THREADS * 8 * CHUNKS;
     constexpr bool EIGHT = KIND != NORM, WITH_LO = EIGHT && KIND != ROWS8 && sizeof(T) == 4;
     __shared__ GroupSums sm;
+    if (KIND == ROWS8) sg::launch_dependents();   // (its call's first kernel, launched plainly: host_state.h)
     const int t = threadIdx.x % THREADS;
     const long long row = (long long)blockIdx.x * GROUPS + threadIdx.x / THREADS;
     if (row >= a.M || !SG_IN_RANGE(LONG || a.K <= SPAN)) return;

@@ -214,13 +214,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
     } else if (warp == 1) {
         // ================================================================ MMA issuer (CTA 0)
-        if (lane == 0 && rank == 0) {
+        // All lanes go through the loop, what they wait for decided together, and one, elected, issues: in a branch
+        // of one lane the operands are not in uniform registers.
+        if (rank == 0) {
             int stage = 0;
             uint32_t phase = 0;
             int chunk = 0, piece = 0;   // accumulator hand-overs of several parts; tiles (PIECES: chunks) so far
             bool ok = true;
             auto wait_acc = [&](int a, int use) {   // the epilogues are through with its use - 1
-                if (mbar_wait_cluster(&acc_empty[a], (uint32_t(use) & 1u) ^ 1u, p.timeout_ns)) {
+                if (__all_sync(0xffffffffu, mbar_wait_cluster(&acc_empty[a], (uint32_t(use) & 1u) ^ 1u, p.timeout_ns))) {
                     tc_fence_after();
                     return true;
                 }
@@ -239,7 +241,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     if (!(ok = SEVERAL ? wait_acc(1, piece) : wait_acc(a, piece >> 1))) break;
                     ++piece;
                     for (int s = begin; s < end; ++s) {
-                        if (*abort_flag || !mbar_wait_cluster(&full[stage], phase, p.timeout_ns)) {
+                        if (!__all_sync(0xffffffffu, !*abort_flag && mbar_wait_cluster(&full[stage], phase, p.timeout_ns))) {
                             if (!*abort_flag) atomicOr(&g_error_word, ERR_FULL_WAIT);
                             set_abort();
                             ok = false;
@@ -252,7 +254,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                             sgp::mma_bf16_pair(d, part_desc<A_MN>(sa + uint32_t(qa) * PART_BYTES, kk),
                                                part_desc<B_MN>(sb + uint32_t(qb) * PART_BYTES, kk), idesc, accumulate);
                         };
+                        const bool elected = elect_one();
                         if constexpr (SEVERAL) {
+                            if (elected)
 #pragma unroll
                             for (int kk = 0; kk < BK / 16; ++kk) {
                                 bool first = s == 0 && kk == 0;
@@ -271,23 +275,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                             }
                         }
                         const uint32_t main_acc = taddr + uint32_t(a) * ACC_COLUMNS;
+                        if (elected) {
 #pragma unroll
-                        for (int kk = 0; kk < BK / 16; ++kk)
-                            mma(main_acc, 0, 0, kk, SEVERAL ? (s % PER_CHUNK != 0 || kk > 0) : (s > begin || kk > 0));
-                        mma_commit_pair(&empty[stage]);   // both CTAs' stage free once read
+                            for (int kk = 0; kk < BK / 16; ++kk)
+                                mma(main_acc, 0, 0, kk, SEVERAL ? (s % PER_CHUNK != 0 || kk > 0) : (s > begin || kk > 0));
+                            mma_commit_pair(&empty[stage]);   // both CTAs' stage free once read
+                            if (SEVERAL && (s % PER_CHUNK == PER_CHUNK - 1 || s == it.slabs - 1)) mma_commit_pair(&acc_full[0]);
+                        }
                         if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1u;
                         }
-                        if (SEVERAL && (s % PER_CHUNK == PER_CHUNK - 1 || s == it.slabs - 1)) mma_commit_pair(&acc_full[0]);
                     }
-                    if (!SEVERAL && ok) mma_commit_pair(&acc_full[a]);
+                    if (!SEVERAL && ok && elect_one()) mma_commit_pair(&acc_full[a]);
                     begin = end;
                 } while (PIECES && ok && begin < it.slabs);
             }
             if (!ok) {
                 // no MMA may still run when either CTA frees its TMEM or exits
-                mma_commit_pair(drain);
+                if (elect_one()) mma_commit_pair(drain);
                 if (!mbar_wait(drain, 0u, drain_limit_ns(p.timeout_ns)))
                     atomicOr(&g_error_word, ERR_DRAIN_WAIT);
             }
