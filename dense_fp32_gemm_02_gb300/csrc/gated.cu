@@ -117,8 +117,10 @@ int forward(const Call &c) {
     if (c.K == 0) return finish<T, true>(c.M, c.N, 0, nullptr, nullptr, c.N, 0, to, c.stream);
     Packed<T> X(c.M, c.K, c.X, c.ldx), Wg(c.K, c.N, c.Wg, c.ldwg), Wu(c.K, c.N, c.Wu, c.ldwu);
     const bool in_place = Wg.direct && Wu.direct;
-    if (c.M <= STREAM_ROWS && (PARTS == 3 || !in_place || c.M <= 2 || (long long)c.K * c.N < 4000000))
-        return forward_few_rows<T>(c, true, sms, pool);
+    // Up to 8 rows by FMAs, W through registers once; bfloat16 that the TMA reads where it lies only up to 2.  us,
+    // by FMAs / by the tensor cores: 1 row of 1024 x 1024 6.0 / 8.4, of 4096 x 4096 15.9 / 18.1; 4 rows 7.8 / 8.8
+    // and 27.8 / 18.4; 8 rows 8.5 / 9.0 and 28.4 / 18.6.
+    if (c.M <= STREAM_ROWS && (PARTS == 3 || !in_place || c.M <= 2)) return forward_few_rows<T>(c, true, sms, pool);
     if (PARTS == 3 && c.M <= MMA_ROWS) return forward_few_rows<T>(c, false, sms, pool);
 
     const sgp::Split split = sgq::plan(sgq::GATE, c.M, c.N, c.K, PARTS == 3 ? 6 : 1, sms);

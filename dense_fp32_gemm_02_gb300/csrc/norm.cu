@@ -87,7 +87,7 @@ int backward(NormBackCall<T> c, T *dw, cudaStream_t stream) {
     st = sgh::launched(wide ? "norm backward, rows read 16 bytes at a time" : "norm backward, any alignment");
     if (st != SGEMM_OK) return st;
     if (dw) {
-        st = sgh::launch(nullptr, norm_weight_kernel<T>, dim3(unsigned((c.K + 31LL) / 32)), 256, 0, stream, c.K, blocks,
+        st = sgh::launch(nullptr, norm_weight_kernel<T>, dim3(unsigned((c.K + 31LL) / 32)), 1024, 0, stream, c.K, blocks,
                          (const float *)c.partial, dw);
         if (st != SGEMM_OK) return st;
     }

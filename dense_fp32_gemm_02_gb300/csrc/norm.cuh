@@ -28,48 +28,61 @@ constexpr float LEAST_SQUARES = 0x1p-80f, MOST_SQUARES = 0x1p120f;
 
 __host__ __device__ constexpr int norm_block(int threads) { return threads < 128 ? 256 : threads; }
 
-// Where eight elements `c` of thread `t` lie in a row: together (WIDE, rows that are 16-byte
-// aligned and of a multiple of 8 columns), or a group's width apart, next to the other threads'.
-template <int THREADS, bool WIDE>
+// Where eight elements `c` of thread `t` lie in a row: 16 bytes together, next to the other threads'
+// (WIDE, rows that are 16-byte aligned and of a multiple of 8 columns; float32: in two such pieces), or
+// one by one, a group's width apart.
+template <class T, int THREADS, bool WIDE>
 struct Place {
+    static constexpr int PER = WIDE ? 16 / int(sizeof(T)) : 1;   // together
     int K, base, t;
 
-    __device__ int column(int c, int e) const {
-        return base + (WIDE ? (c * THREADS + t) * 8 + e : (c * 8 + e) * THREADS + t);
-    }
-    template <class T>
+    __device__ int column(int c, int e) const { return base + ((c * (8 / PER) + e / PER) * THREADS + t) * PER + e % PER; }
     __device__ void load(const T *row, int c, float (&v)[8]) const {
-        if (WIDE) {
-            if (column(c, 0) < K) {
-                load8(row + column(c, 0), v);
-                return;
+#pragma unroll
+        for (int e = 0; e < 8; e += PER) {
+            const int j = column(c, e);
+            if constexpr (PER == 8) {
+                if (j < K) load8(row + j, v);
+            } else if constexpr (PER == 4) {
+                float x[4];
+                if (j < K) load4(row + j, x);
+#pragma unroll
+                for (int d = 0; d < 4; ++d) v[e + d] = j < K ? x[d] : 0.0f;
+            } else {
+                v[e] = j < K ? to_f32(row[j]) : 0.0f;
             }
+            if (PER == 8 && j >= K)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = column(c, e) < K ? to_f32(row[column(c, e)]) : 0.0f;
+                for (int d = 0; d < 8; ++d) v[d] = 0.0f;
         }
     }
-    template <class T>
     __device__ void store(T *row, int c, const float (&v)[8]) const {
-        if (WIDE) {
-            if (column(c, 0) < K) store8(row + column(c, 0), v);
-        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (column(c, e) < K) row[column(c, e)] = from_f32<T>(v[e]);
+        for (int e = 0; e < 8; e += PER) {
+            const int j = column(c, e);
+            if (j >= K) continue;
+            if constexpr (PER == 8) {
+                store8(row + j, v);
+            } else if constexpr (PER == 4) {
+                const float x[4] = {v[e], v[e + 1], v[e + 2], v[e + 3]};
+                store4(row + j, x);
+            } else {
+                row[j] = from_f32<T>(v[e]);
+            }
         }
     }
     // Eight integers of at most 127 in magnitude, given as floats.
     __device__ void store_q(signed char *row, int c, const float (&r)[8]) const {
-        if (WIDE) {
-            if (column(c, 0) < K)
-                *reinterpret_cast<uint2 *>(row + column(c, 0)) = make_uint2(pack_s8(r, 1.0f), pack_s8(r + 4, 1.0f));
-        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (column(c, e) < K) row[column(c, e)] = static_cast<signed char>(__float2int_rn(r[e]));
+        for (int e = 0; e < 8; e += PER) {
+            const int j = column(c, e);
+            if (j >= K) continue;
+            if constexpr (PER == 8)
+                *reinterpret_cast<uint2 *>(row + j) = make_uint2(pack_s8(r, 1.0f), pack_s8(r + 4, 1.0f));
+            else if constexpr (PER == 4)
+                *reinterpret_cast<uint32_t *>(row + j) = pack_s8(r + e, 1.0f);
+            else
+                row[j] = static_cast<signed char>(__float2int_rn(r[e]));
         }
     }
 };
@@ -248,7 +261,7 @@ __global__ void __launch_bounds__(norm_block(THREADS))
     signed char *q = EIGHT ? a.q + row * a.ldq : nullptr;
 
     float v[CHUNKS][8], w[8];
-    auto read = [&](const Place<THREADS, WIDE> &at, bool again) {
+    auto read = [&](const Place<T, THREADS, WIDE> &at, bool again) {
         const T *from = again && s ? s : x;
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) at.load(from, c, v[c]);
@@ -267,7 +280,7 @@ __global__ void __launch_bounds__(norm_block(THREADS))
     float squares = 0.0f, none = 0.0f;
     Top top{0, 0.0f};
     for (int base = 0; base < (LONG ? a.K : 1); base += SPAN) {
-        const Place<THREADS, WIDE> at{a.K, base, t};
+        const Place<T, THREADS, WIDE> at{a.K, base, t};
         read(at, false);
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
@@ -320,7 +333,7 @@ __global__ void __launch_bounds__(norm_block(THREADS))
     }
 
     for (int base = 0; base < (LONG ? a.K : 1); base += SPAN) {
-        const Place<THREADS, WIDE> at{a.K, base, t};
+        const Place<T, THREADS, WIDE> at{a.K, base, t};
         if (LONG) read(at, true);
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
@@ -405,7 +418,7 @@ __global__ void __launch_bounds__(norm_block(THREADS), norm_blocks_per_sm<THREAD
     };
     auto issue = [&](int stage, long long r) {
         if constexpr (Ring::ON) {
-            const Place<THREADS, WIDE> at{a.K, 0, t};
+            const Place<T, THREADS, WIDE> at{a.K, 0, t};
             if (r < a.M)
 #pragma unroll
                 for (int m = 0; m < 3; ++m) {
@@ -441,12 +454,12 @@ __global__ void __launch_bounds__(norm_block(THREADS), norm_blocks_per_sm<THREAD
     };
 
     float v[CHUNKS][8], dy[CHUNKS][8], dw[LONG ? 1 : CHUNKS][8] = {}, w[KEEP_W ? CHUNKS : 1][8];
-    auto weight = [&](const Place<THREADS, WIDE> &at, int c) -> float(&)[8] {
+    auto weight = [&](const Place<T, THREADS, WIDE> &at, int c) -> float(&)[8] {
         if (!KEEP_W) at.load(a.w, c, w[0]);
         return w[KEEP_W ? c : 0];
     };
 #pragma unroll
-    for (int c = 0; KEEP_W && c < CHUNKS; ++c) Place<THREADS, WIDE>{a.K, 0, t}.load(a.w, c, w[c]);
+    for (int c = 0; KEEP_W && c < CHUNKS; ++c) Place<T, THREADS, WIDE>{a.K, 0, t}.load(a.w, c, w[c]);
 #pragma unroll
     for (int d = 0; Ring::ON && d < Ring::DEPTH; ++d) issue(d, row + d * step);
     int turn = 0, stage = 0;
@@ -454,7 +467,7 @@ __global__ void __launch_bounds__(norm_block(THREADS), norm_blocks_per_sm<THREAD
     for (; row < a.M; row += step) {
         const T *vr = a.V + row * a.ldv, *dyr = a.dY + row * a.lddy, *dsr = a.dS ? a.dS + row * a.ldds : nullptr;
         T *dxr = a.dX + row * a.lddx;
-        auto read = [&](const Place<THREADS, WIDE> &at) {
+        auto read = [&](const Place<T, THREADS, WIDE> &at) {
             if constexpr (Ring::ON) sg::cp_async_wait<Ring::DEPTH - 1>();
 #pragma unroll
             for (int c = 0; c < CHUNKS; ++c) {
@@ -467,7 +480,7 @@ __global__ void __launch_bounds__(norm_block(THREADS), norm_blocks_per_sm<THREAD
         float squares = 0.0f, gv = 0.0f;
         Top none{};
         for (int base = 0; base < (LONG ? a.K : 1); base += SPAN) {
-            const Place<THREADS, WIDE> at{a.K, base, t};
+            const Place<T, THREADS, WIDE> at{a.K, base, t};
             read(at);
 #pragma unroll
             for (int c = 0; c < CHUNKS; ++c) {
@@ -490,7 +503,7 @@ __global__ void __launch_bounds__(norm_block(THREADS), norm_blocks_per_sm<THREAD
             if (THREADS > 32) __syncthreads();   // dX, written below, may be dY
         }
         for (int base = 0; base < (LONG ? a.K : 1); base += SPAN) {
-            const Place<THREADS, WIDE> at{a.K, base, t};
+            const Place<T, THREADS, WIDE> at{a.K, base, t};
             if (LONG) read(at);
             float ds[CHUNKS][8];
 #pragma unroll
@@ -527,7 +540,7 @@ __global__ void __launch_bounds__(norm_block(THREADS), norm_blocks_per_sm<THREAD
     }
     if constexpr (Ring::ON) sg::cp_async_wait<0>();
     if (LONG || !partial) return;
-    const Place<THREADS, WIDE> at{a.K, 0, t};
+    const Place<T, THREADS, WIDE> at{a.K, 0, t};
     for (int g = 0; g < GROUPS; ++g) {   // a block's warps in order
         if (GROUPS > 1) __syncthreads();
         if (group != g) continue;
@@ -548,13 +561,13 @@ __global__ void __launch_bounds__(norm_block(THREADS), norm_blocks_per_sm<THREAD
     for (int j = threadIdx.x; j < a.K; j += BLOCK) partial[j] = columns[j];
 }
 
-// dw from the blocks' sums: 32 columns to a block, its warps' shares of the sums in order.
+// dw from the blocks' sums: 32 columns to a block, its 32 warps' shares of the sums in order.
 template <class T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
     norm_weight_kernel(int K, int sums, const float *__restrict__ partial, T *dw) {
-    __shared__ float part[8][32];
+    __shared__ float part[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = blockIdx.x * 32 + lane;
-    const int per = (sums + 7) / 8, last = min(sums, (warp + 1) * per);
+    const int per = (sums + 31) / 32, last = min(sums, (warp + 1) * per);
     sg::wait_prerequisites();
     float s = 0.0f;
     if (j < K && SG_IN_RANGE(sums > 0)) {
@@ -563,11 +576,10 @@ __global__ void __launch_bounds__(256)
     }
     part[warp][lane] = s;
     __syncthreads();
-    if (warp != 0 || j >= K) return;
-    float all = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) all += part[k][lane];
-    dw[j] = from_f32<T>(all);
+    // a warp to a column: the shares by a tree
+    const float all = warp_sum(part[lane][warp]);
+    const int column = blockIdx.x * 32 + warp;
+    if (lane == 0 && column < K) dw[column] = from_f32<T>(all);
 }
 
 }  // namespace sgl

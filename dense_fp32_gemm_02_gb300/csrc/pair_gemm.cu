@@ -54,9 +54,12 @@ int sgq::run(const Product &g, const Output<T> &out, sgp::Split split, float *pa
     const auto kernel = p.per_split > sgp::LONG_CHUNK ? K::chunks : K::main;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM_BYTES));
     if (e != cudaSuccess) return sgh::cuda_fail(e);
+    // (a CTA's rows of A, the last ones of few left as they are in shared memory: they reach no output)
+    const uint32_t a_rows = K::A_MN ? BK : uint32_t(std::min(ROWS, (g.M + 7) / 8 * 8));
+    p.slab_bytes = uint32_t(K::PARTS) * (K::A_MN ? PART_BYTES : a_rows * BK * 2) + K::PARTS * PART_BYTES;
     CUtensorMap mA, mB0, mB1;
     int st;
-    if ((st = sgp::encode(&mA, g.a, BK, K::A_MN ? BK : ROWS)) != SGEMM_OK ||
+    if ((st = sgp::encode(&mA, g.a, BK, a_rows)) != SGEMM_OK ||
         (st = sgp::encode(&mB0, g.b[0], BK, K::B_MN ? BK : ROWS)) != SGEMM_OK)
         return st;
     mB1 = mB0;

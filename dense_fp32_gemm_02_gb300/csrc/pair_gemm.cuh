@@ -43,6 +43,7 @@ struct Params {
     int out_tiles;          // TWO: tiles_n of the first output
     int slabs, first_slabs; // of 64 k; SUM: of the first pair
     int splits, per_split;
+    uint32_t slab_bytes;    // that a CTA loads of a slab
     float *partial;
     unsigned long long timeout_ns;
 };
@@ -182,7 +183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     }
                     const uint32_t st = ring + uint32_t(stage) * STAGE;
                     const uint32_t fb = dsmem_map(smem_addr(&full[stage]), 0u);
-                    mbar_arrive_expect_tx_cluster(fb, STAGE);
+                    mbar_arrive_expect_tx_cluster(fb, p.slab_bytes);
                     const int slab = SG_IN_RANGE(it.slab0 + s < p.slabs && it.tm < p.tiles_m && stage < STAGES) ? it.slab0 + s : 0;
                     const int second = MODE == SUM && slab >= p.first_slabs ? 1 : 0;
                     const int k = (slab - second * p.first_slabs) * BK;
@@ -301,7 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     } else {
         // ================================================================ epilogue (both CTAs)
         const int quarter = warp & 3, half = (warp - 2) >> 2;
-        float *buf = stage_out + (warp - 2) * (32 * 33);
+        float *buf = stage_out + (warp - 2) * (32 * (CHUNKED ? 33 : 32));
         const uint32_t lanes = taddr + (uint32_t(quarter * 32) << 16);
         int turn = 0;
         bool ok = true;
@@ -329,22 +330,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const int row0 = it.tm * TILE + int(rank) * ROWS + quarter * 32, rows = min(32, p.M - row0);
             const int col0 = it.col0 + half * first_half;
 
-            // A lane's row of 32 columns from `col`, given two at a time, written with a lane to a column.
+            // A lane's row of 32 columns from `col`, given two at a time, written a column to a lane; where the sums
+            // leave registers for it (64 x 8192 x 4096 bfloat16 weight gradients 82 -> 55 us; beside 128 sums it
+            // spilled, and 79 us of float32 became 86) and rows are aligned, four columns to a lane.
             auto write = [&](auto *out, long long ld, int col, auto &&value) {
+                using E = std::remove_reference_t<decltype(*out)>;
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
+                for (int i = 0; i < 32; i += CHUNKED ? 2 : 4) {
                     const float2 v = value(i);
-                    buf[lane * 33 + i] = v.x, buf[lane * 33 + i + 1] = v.y;
+                    if constexpr (CHUNKED) {
+                        buf[lane * 33 + i] = v.x, buf[lane * 33 + i + 1] = v.y;
+                    } else {   // rows 128 bytes apart, their 16-byte pieces swizzled
+                        const float2 u = value(i + 2);
+                        *reinterpret_cast<float4 *>(buf + lane * 32 + ((i / 4) ^ (lane & 7)) * 4) = make_float4(v.x, v.y, u.x, u.y);
+                    }
                 }
                 __syncwarp();
+                if constexpr (!CHUNKED) {
+                    if (!SG_IN_RANGE(col + 32 <= it.col0 + it.cols && row0 + rows <= (it.tm + 1) * TILE)) return;
+                    if (col + 32 <= p.N && ld % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (4 * sizeof(E) - 1)) == 0) {
+                        E *at = out + (long long)(row0 + (lane >> 3)) * ld + col + (lane & 7) * 4;
+                        const float *from = buf + lane / 8 * 32;
+#pragma unroll 8
+                        for (int r = lane >> 3; r < rows; r += 4, at += 4 * ld, from += 4 * 32) {
+                            float v[4];
+                            sgl::load4(from + ((lane & 7) ^ (r & 7)) * 4, v);
+                            sgl::store4(at, v);
+                        }
+                        return;
+                    }
+                }
                 const int c = col + lane;
                 if (c >= p.N) return;
                 if (!SG_IN_RANGE(c < it.col0 + it.cols && row0 + rows <= (it.tm + 1) * TILE && it.split < p.splits)) return;
-                using E = std::remove_reference_t<decltype(*out)>;
                 E *at = out + (long long)row0 * ld + c;
 #pragma unroll 8
-                for (int r = 0; r < rows; ++r) at[(long long)r * ld] = sgl::from_f32<E>(buf[r * 33 + lane]);
+                for (int r = 0; r < rows; ++r)
+                    at[(long long)r * ld] =
+                        sgl::from_f32<E>(CHUNKED ? buf[r * 33 + lane] : buf[r * 32 + ((lane >> 2) ^ (r & 7)) * 4 + (lane & 3)]);
             };
             // 32 columns of the tile's sums: x (and GATE: y, the same columns of U)
             auto finish = [&](int c, const float (&x)[32], const float (&y)[32]) {
