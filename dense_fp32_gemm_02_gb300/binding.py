@@ -420,8 +420,11 @@ def _matrix(name, t, rows, cols):
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must be {(rows, cols)}, got {tuple(t.shape)}")
     row_stride, col_stride = t.stride()
-    if col_stride == 1 and 0 < cols <= row_stride <= _INT_MAX and 1 < rows <= _INT_MAX:   # (what _pitch would say)
-        return t.data_ptr(), row_stride
+    if col_stride == 1 and 0 < cols <= _INT_MAX:   # (what _pitch would say)
+        if rows == 1:
+            return t.data_ptr(), cols
+        if cols <= row_stride <= _INT_MAX and 1 < rows <= _INT_MAX:
+            return t.data_ptr(), row_stride
     return t.data_ptr(), _pitch(name, rows, cols, row_stride, col_stride)
 
 

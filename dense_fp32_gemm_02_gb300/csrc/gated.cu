@@ -134,7 +134,7 @@ int forward(const Call &c) {
     Packed<T> none(0, 0, nullptr, 8);
     if ((st = pack(Wg, Wu, sms, c.stream)) != SGEMM_OK || (st = pack(X, none, sms, c.stream)) != SGEMM_OK) return st;
     sgq::Product g{c.M, c.N, c.K, X.operand(), {Wg.operand(), Wu.operand()}};
-    const sgq::Output<T> out{to.out, to.out1, to.H, to.ldo, to.ldo1, to.ldh, to.act, nullptr, nullptr, nullptr};
+    const sgq::Output<T> out{to.out, to.out1, to.H, to.ldo, to.ldo1, to.ldh, to.act, nullptr, nullptr, nullptr, nullptr};
     if ((st = sgq::run<T, sgq::GATE>(g, out, split, partial, sms, c.stream)) != SGEMM_OK) return st;
     if (partial) {
         st = finish<T, true>(c.M, c.N, split.splits, partial, partial + c.N, 2LL * c.N, 2LL * c.M * c.N, to, c.stream);
@@ -181,7 +181,7 @@ int backward(const Call &c) {
     const sgp::Operand dG{d, c.N, c.M, PARTS, pitch, plane}, dU{d + PARTS * plane, c.N, c.M, PARTS, pitch, plane};
     if (want_dx) {
         sgq::Product g{c.M, c.K, c.N, {d, c.N, c.M, 2 * PARTS, pitch, plane}, {Wg.operand(), Wu.operand()}};
-        const sgq::Output<T> out{static_cast<T *>(c.dX), nullptr, nullptr, c.lddx, 0, 0, 0, nullptr, nullptr, nullptr};
+        const sgq::Output<T> out{static_cast<T *>(c.dX), nullptr, nullptr, c.lddx, 0, 0, 0, nullptr, nullptr, nullptr, nullptr};
         if ((st = sgq::run<T, sgq::SUM>(g, out, sum, sum_partial, sms, c.stream)) != SGEMM_OK) return st;
         if (sum_partial) {
             const sgp::Epilogue<T, false> epi{Adapters{}, nullptr, 0, {}, nullptr, 0.0f, out.out, out.ldo};
@@ -192,7 +192,7 @@ int backward(const Call &c) {
     if (want_dw) {
         sgq::Product g{c.K, c.N, c.M, X.operand(), {dG, dU}};
         const PairOut<T> to{static_cast<T *>(c.dWg), static_cast<T *>(c.dWu), nullptr, c.lddwg, c.lddwu, 0, 0};
-        const sgq::Output<T> out{to.out, to.out1, nullptr, to.ldo, to.ldo1, 0, 0, nullptr, nullptr, nullptr};
+        const sgq::Output<T> out{to.out, to.out1, nullptr, to.ldo, to.ldo1, 0, 0, nullptr, nullptr, nullptr, nullptr};
         if ((st = sgq::run<T, sgq::TWO>(g, out, two, two_partial, sms, c.stream)) != SGEMM_OK) return st;
         if (two_partial) {
             st = finish<T, false>(c.K, c.N, two.splits, two_partial, two_partial + c.N, 2LL * c.N, 2LL * c.K * c.N, to,

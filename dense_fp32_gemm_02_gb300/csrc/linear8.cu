@@ -100,7 +100,7 @@ int finish(const Call &c, int ranges, const int *partial) {
                        static_cast<T *>(c.Y), (long long)c.ldy);
 }
 
-bool aligned_rows(const signed char *p, long long ld) { return sgh::aligned(p, 16) && ld % 16 == 0; }
+bool aligned_rows(const signed char *p, long long ld, int to = 16) { return sgh::aligned(p, size_t(to)) && ld % to == 0; }
 
 // Up to so many rows W is brought to float16 on its way; more rows make it worth while to lay both
 // matrices out as bfloat16 first.  us at 4096 x 4096, on its way / laid out: 64 rows 10.6 / 27.6, 256 rows
@@ -131,12 +131,12 @@ int linear8(Call c) {
     sgh::Workspace ws(pool, c.stream);
     const auto piece = [](size_t n) { return sgh::Workspace::piece(n); };
     st = ws.allocate(piece(q_bytes) + piece(s_floats * 4) + piece(x_elems * 2) + piece(w_elems * 2) + piece(p_ints * 4) +
-                     piece(q_copy) + piece(w_copy));
+                     piece(q_copy) + piece(w_copy) + piece(sizeof(int)));
     if (st != SGEMM_OK) return st;
     signed char *q = ws.take<signed char>(q_bytes);
     float *scale = ws.take<float>(s_floats);
     const Parts xp{ws.take<bf16>(x_elems), xpitch, c.M * xpitch}, wp{ws.take<bf16>(w_elems), wpitch, c.K * wpitch};
-    int *partial = p_ints ? ws.take<int>(p_ints) : nullptr;
+    int *partial = p_ints ? ws.take<int>(p_ints) : nullptr, *large = ws.take<int>(1);
     if (own_rows) {
         if ((st = sgh::rows8(c.type, c.M, c.K, c.X, c.ldx, q, qpitch, scale, sms, c.stream)) != SGEMM_OK) return st;
         c.q = q, c.ldq = qpitch, c.scale = scale;
@@ -156,13 +156,16 @@ int linear8(Call c) {
         }
         st = launch_tiles<T>(c, tw);
     } else {
-        const PartsJob<ByteRows> a(ByteRows{c.q, c.ldq}, c.M, c.K, sgh::aligned(c.q, 8) && c.ldq % 8 == 0, xp);
-        const PartsJob<ByteRows> b(ByteRows{c.W, c.ldw}, c.K, c.N, sgh::aligned(c.W, 8) && c.ldw % 8 == 0, wp);
-        const unsigned blocks = unsigned(std::min<long long>((a.octets() + b.octets() + 255) / 256, 32LL * sms));
-        st = sgh::launch(nullptr, parts_kernel<1, 1, ByteRows, ByteRows>, dim3(blocks), 256, 0, c.stream, a, b, false);
+        const auto expand = [&](auto kernel, const ByteJob &job) {
+            const unsigned blocks = unsigned(std::min<long long>((job.items() + 7) / 8, 32LL * sms));
+            return sgh::launch(nullptr, kernel, dim3(blocks), 256, 0, c.stream, job, large);
+        };
+        st = expand(byte_expand_kernel<false>, ByteJob{c.W, c.ldw, c.K, c.N, wp, aligned_rows(c.W, c.ldw, 8)});
+        if (st == SGEMM_OK) st = expand(byte_expand_kernel<true>, ByteJob{c.q, c.ldq, c.M, c.K, xp, aligned_rows(c.q, c.ldq, 8)});
         if (st != SGEMM_OK) return st;
         sgq::Product g{c.M, c.N, c.K, {xp.p, c.K, c.M, 1, xpitch, c.M * xpitch}, {{wp.p, c.N, c.K, 1, wpitch, c.K * wpitch}, {}}};
-        const sgq::Output<T> out{static_cast<T *>(c.Y), nullptr, nullptr, c.ldy, 0, 0, 0, c.scale, c.wscale, static_cast<const T *>(c.bias)};
+        const sgq::Output<T> out{static_cast<T *>(c.Y), nullptr, nullptr, c.ldy, 0, 0, 0, c.scale, c.wscale, static_cast<const T *>(c.bias),
+                                 partial ? nullptr : large};   // (with one range chunks begin at multiples of 2048)
         st = sgq::run<T, sgq::BYTES>(g, out, split, reinterpret_cast<float *>(partial), sms, c.stream);
         if (st == SGEMM_OK && partial) st = finish<T>(c, split.splits, partial);
     }

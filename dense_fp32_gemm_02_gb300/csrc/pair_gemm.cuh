@@ -10,8 +10,9 @@
 //   SUM    the contraction runs over both pairs of operands, one after the other.
 //   TWO    the tiles of both outputs are one list.
 //   BYTES  an int8 is exactly a bfloat16, and sums of 1024 products of two are at most 2^24: exact
-//          in the fp32 accumulator.  Every 1024 k it is taken to int32 registers.  (The integer MMA
-//          of this GPU runs at a tenth of the bfloat16 one's rate.)
+//          in the fp32 accumulator.  Every 1024 k it is taken to int32 registers, or every 2048 where
+//          the rows' magnitudes keep such sums within 2^24 too (8192 x 4096 x 4096: 175 us for 199).
+//          (The integer MMA of this GPU runs at a tenth of the bfloat16 one's rate.)
 #pragma once
 
 #include "gate.cuh"
@@ -108,7 +109,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // the accumulator goes to registers by chunks: of several parts inside the loop over slabs, of
     // one as pieces of the tile with an accumulator each
     constexpr bool CHUNKED = SEVERAL || CHUNKS, PIECES = CHUNKS && !SEVERAL;
-    constexpr int PER_CHUNK = chunk_slabs(SEVERAL, BYTES_MODE);
     constexpr uint32_t STAGE = 2 * PARTS * PART_BYTES;
     constexpr int STAGES = int(SMEM_RING / STAGE);
     constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(A_MN) << 15) | (uint32_t(B_MN) << 16) |
@@ -155,6 +155,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         st_cluster_flag(peer_abort, 1);
     };
 
+    const int PER_CHUNK = chunk_slabs(SEVERAL, BYTES_MODE) * (BYTES_MODE && to.large && *to.large == 0 ? 2 : 1);
     Work<MODE> work;
     using Item = typename Work<MODE>::Item;
     work.init(p);

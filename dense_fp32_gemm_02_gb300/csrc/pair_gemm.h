@@ -24,6 +24,7 @@ struct Output {
     int act;
     const float *scale, *wscale;
     const T *bias;
+    const int *large;           // BYTES: whether sums of 2048 products may leave 2^24 (null: they may)
 };
 
 // Operands as in parts_gemm.h; SUM: the planes of `a` are A0's parts and then A1's; TWO: the

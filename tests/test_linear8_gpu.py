@@ -75,7 +75,22 @@ def test_rows_of_the_type(M, N, K, dtype):
     assert bool(torch.isnan(Y[0]).all()) and (M == 1 or bool(torch.isfinite(Y[1:]).all()))
 
 
-@pytest.mark.parametrize("M", [1, 8, 40, 300])
+@pytest.mark.parametrize("fill", [63, 64, 65, 127, -128])
+def test_many_rows_with_magnitudes_at_the_bound(fill):
+    """Rows whose 2048 magnitudes add up to just under, to and past 2^17, in one row of many: sums that fp32 holds
+    exactly every 2048 terms, or every 1024 only."""
+    b = binding()
+    M, N, K = 2600, 4096, 4500
+    q, W = bytes_of(M, K, 31, -20) // 7, bytes_of(K, N, 32)
+    q[1234, 2048:4096] = fill
+    W[:, ::2] = 127
+    W[:, 1::4] = -128
+    one, ones, Y = torch.ones(M, device="cuda"), torch.ones(N, device="cuda"), torch.empty(M, N, device="cuda")
+    b.linear8_into((q.cuda(), one), W.cuda(), ones, Y)
+    assert torch.equal(Y, (q.cuda().double() @ W.cuda().double()).float())
+
+
+@pytest.mark.parametrize("M", [1, 8, 40, 300, 700])
 @pytest.mark.parametrize("K", [1024, 5000, 131071])
 def test_the_largest_sums_are_exact(M, K):
     """All values at their limits: sums up to 2^31, to the last integer."""
