@@ -51,15 +51,18 @@ int finish(int M, int N, int ranges, const float *x, const float *y, long long p
                        128, 0, stream, M, N, ranges, x, y, pitch, plane, wide, to);
 }
 
-// The operands that the TMA does not read where they lie, as parts.
+// The operands that the TMA does not read where they lie, as parts.  `beside`: not the call's first kernel, it
+// runs beside the one before it (host_state.h); true from here on.
 template <class T>
-int pack(const Packed<T> &p, const Packed<T> &q, int sms, cudaStream_t stream) {
+int pack(const Packed<T> &p, const Packed<T> &q, bool &beside, int sms, cudaStream_t stream) {
     const auto a = p.job(), b = q.job();
     const long long octets = a.octets() + b.octets();
     if (octets == 0) return SGEMM_OK;
     const unsigned blocks = unsigned(std::min<long long>((octets + 255) / 256, 32LL * sms));
     constexpr int PARTS = Packed<T>::PARTS;
-    return sgh::launch(nullptr, parts_kernel<PARTS, PARTS, Rows<T>, Rows<T>>, dim3(blocks), 256, 0, stream, a, b, false);
+    const int st = sgh::launch(nullptr, parts_kernel<PARTS, PARTS, Rows<T>, Rows<T>>, dim3(blocks), 256, 0, stream, a, b, beside);
+    beside = true;
+    return st;
 }
 
 // ------------------------------------------------------------------ forward
@@ -132,7 +135,8 @@ int forward(const Call &c) {
     Wu.place(ws);
     float *partial = split.partial_floats ? ws.take<float>(split.partial_floats) : nullptr;
     Packed<T> none(0, 0, nullptr, 8);
-    if ((st = pack(Wg, Wu, sms, c.stream)) != SGEMM_OK || (st = pack(X, none, sms, c.stream)) != SGEMM_OK) return st;
+    bool beside = false;
+    if ((st = pack(Wg, Wu, beside, sms, c.stream)) != SGEMM_OK || (st = pack(X, none, beside, sms, c.stream)) != SGEMM_OK) return st;
     sgq::Product g{c.M, c.N, c.K, X.operand(), {Wg.operand(), Wu.operand()}};
     const sgq::Output<T> out{to.out, to.out1, to.H, to.ldo, to.ldo1, to.ldh, to.act, nullptr, nullptr, nullptr, nullptr};
     if ((st = sgq::run<T, sgq::GATE>(g, out, split, partial, sms, c.stream)) != SGEMM_OK) return st;
@@ -176,7 +180,8 @@ int backward(const Call &c) {
     const long long octets = (long long)c.M * job.per_row.d;
     st = sgh::launch(nullptr, gated_slopes_kernel<T>, dim3(unsigned(std::min<long long>((octets + 255) / 256, 32LL * sms))), 256,
                      0, c.stream, job);
-    if (st != SGEMM_OK || (st = pack(Wg, Wu, sms, c.stream)) != SGEMM_OK || (st = pack(X, none, sms, c.stream)) != SGEMM_OK)
+    bool beside = true;
+    if (st != SGEMM_OK || (st = pack(Wg, Wu, beside, sms, c.stream)) != SGEMM_OK || (st = pack(X, none, beside, sms, c.stream)) != SGEMM_OK)
         return st;
     const sgp::Operand dG{d, c.N, c.M, PARTS, pitch, plane}, dU{d + PARTS * plane, c.N, c.M, PARTS, pitch, plane};
     if (want_dx) {
