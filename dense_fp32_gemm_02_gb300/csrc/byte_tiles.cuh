@@ -242,12 +242,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             __syncwarp();
             if (++depth == Z::DEPTH) depth = 0, phase ^= 1u;
         }
-        if (*abort_flag)   // what is in flight lands before the block ends
-            for (int i = max(0, issued - Z::DEPTH); i < issued; ++i)
-                if (!mbar_wait(&landed[i % Z::DEPTH], uint32_t(i / Z::DEPTH) & 1u, drain_limit_ns(w.timeout_ns))) {
-                    atomicOr(&g_error_word, ERR_DRAIN_WAIT);
-                    break;
-                }
+        for (int i = max(0, issued - Z::DEPTH); i < issued; ++i)   // what is in flight lands before the block ends
+            if (!mbar_wait(&landed[i % Z::DEPTH], uint32_t(i / Z::DEPTH) & 1u, drain_limit_ns(w.timeout_ns))) {
+                atomicOr(&g_error_word, ERR_DRAIN_WAIT);
+                break;
+            }
     } else {
         // ================================================================ MMA issuer
         const uint32_t idesc = (1u << 4) | (1u << 15) | (uint32_t(rows >> 3) << 17) | (uint32_t(TILE_COLS >> 4) << 24);
@@ -334,24 +333,49 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     }
 }
 
-// Rows of bytes at any pitch as rows that are 16-byte aligned (zeros behind them): a
-// thread to 16 bytes.
+// Bytes from `shift` of the 32 in a and b.
+__device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int shift) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (shift & 8) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (shift & 4) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    const int bits = (shift & 3) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+// Rows of bytes at any pitch as rows that are 16-byte aligned (what lies behind a row in its last 16
+// is never read as the matrix's): a thread to 16 bytes, two aligned loads shifted into place, or, where those
+// would leave the matrix, byte by byte.
 static __global__ void __launch_bounds__(256)
     byte_pitch_kernel(const signed char *p, long long ld, int rows, int cols, Divisor per_row, signed char *out, long long pitch) {
     sg::wait_prerequisites();
     sg::launch_dependents();
     const long long total = (long long)rows * per_row.d, step = (long long)gridDim.x * 256;
     const bool small = total <= 0x7fffffffll;
+    const signed char *end = p + (rows - 1) * ld + cols;
     for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < total; t += step) {
         const long long i = small ? (long long)per_row.quotient(unsigned(t)) : t / per_row.d;
         const int c = int(t - i * per_row.d) * 16;
         if (!SG_IN_RANGE(i < rows && c < cols && c + 16 <= pitch)) continue;
         const signed char *from = p + i * ld + c;
-        uint32_t word[4] = {};
+        const int shift = int(reinterpret_cast<uintptr_t>(from) & 15);
+        uint4 v;
+        if (from - shift >= p && from - shift + 32 <= end) {
+            const uint4 *at = reinterpret_cast<const uint4 *>(from - shift);
+            v = shifted(at[0], at[1], shift);
+        } else {
+            alignas(16) signed char x[16];
 #pragma unroll
-        for (int d = 0; d < 16; ++d)
-            if (c + d < cols) word[d / 4] |= (uint32_t(from[d]) & 0xffu) << (8 * (d % 4));
-        *reinterpret_cast<uint4 *>(out + i * pitch + c) = make_uint4(word[0], word[1], word[2], word[3]);
+            for (int d = 0; d < 16; ++d) x[d] = c + d < cols ? from[d] : static_cast<signed char>(0);
+            v = *reinterpret_cast<const uint4 *>(x);
+        }
+        *reinterpret_cast<uint4 *>(out + i * pitch + c) = v;
     }
 }
 

@@ -155,6 +155,11 @@ __device__ __forceinline__ void group_reduce(GroupSums &sm, int turn, float &a, 
     }
 }
 template <int THREADS>
+__device__ __forceinline__ void group_sync() {
+    if (THREADS == 32) __syncwarp();
+    else __syncthreads();
+}
+template <int THREADS>
 __device__ __forceinline__ double group_sum(GroupSums &sm, double v) {
     v = warp_sum(v);
     if (THREADS == 32) return v;
@@ -305,17 +310,17 @@ __global__ void __launch_bounds__(norm_block(THREADS))
     }
     group_reduce<THREADS, false, EIGHT, WITH_LO>(sm, 0, squares, none, top);
 
+    if (THREADS == 32) __syncwarp();   // (else group_reduce's barrier)
     auto held = [&](int j) {   // v, from what any thread may have written of it above
         if (KIND == ROWS8) return to_f32(x[j]);
         return s ? to_f32(s[j]) : r ? to_f32(from_f32<T>(to_f32(x[j]) + to_f32(r[j]))) : to_f32(x[j]);
     };
-    if (THREADS == 32) __syncwarp();
     float rstd = 1.0f;
     if (KIND != ROWS8) {
         rstd = 1.0f / sqrtf(squares / float(a.K) + a.eps);
         if (!(squares <= MOST_SQUARES) || (squares < LEAST_SQUARES && a.eps < 1e-10f)) {
             rstd = rare_rstd<THREADS>(sm, held, a.K, a.eps, t);
-            if (THREADS > 32) __syncthreads();   // Y, written below, may be X
+            group_sync<THREADS>();   // Y, written below, may be X
         }
     }
     float times = 0.0f;    // 127 / max|p|; 0: q is there already
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(norm_block(THREADS))
         } else {
             const double all = rare_rows8<T, THREADS, KIND != ROWS8>(sm, held, a.w, q, a.K, t);
             scale = all <= 1.7e308 ? float(all * rstd / 127.0) : __uint_as_float(0x7fc00000u);
-            if (THREADS > 32) __syncthreads();   // Y, written below, may be X
+            group_sync<THREADS>();   // Y, written below, may be X
         }
         if (t == 0) a.scale[row] = scale;
     }
@@ -344,7 +349,7 @@ __global__ void __launch_bounds__(norm_block(THREADS))
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float quotient = (KIND == ROWS8 ? v[c][e] : v[c][e] * w[e]) * times;
-                    out[e] = rintf(quotient);
+                    out[e] = (quotient + 12582912.0f) - 12582912.0f;   // to an integer: 1.5 * 2^23 leaves no fraction
                     off = fmaxf(off, fabsf(quotient - out[e]));
                 }
                 if (off > 0.5f - NEAR) {
@@ -500,7 +505,7 @@ __global__ void __launch_bounds__(norm_block(THREADS), norm_blocks_per_sm<THREAD
             for (int j = t; j < a.K; j += THREADS) sum += double(to_f32(dyr[j])) * to_f32(a.w[j]) * to_f32(vr[j]);
             rstd = rare_rstd<THREADS>(sm, [&](int j) { return to_f32(vr[j]); }, a.K, a.eps, t);
             mean = float(group_sum<THREADS>(sm, sum) * rstd / a.K);
-            if (THREADS > 32) __syncthreads();   // dX, written below, may be dY
+            group_sync<THREADS>();   // dX, written below, may be dY
         }
         for (int base = 0; base < (LONG ? a.K : 1); base += SPAN) {
             const Place<T, THREADS, WIDE> at{a.K, base, t};

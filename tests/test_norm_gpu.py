@@ -152,6 +152,27 @@ def test_values_out_of_range(K, dtype):
     assert b.device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("K", [200, 900, 3000, 17000])
+def test_values_out_of_range_in_place(K, dtype):
+    """The rows that are read again, with the outputs in the inputs' place."""
+    b = binding()
+    X, R, w = normal(40, K, dtype, 8) * 1e30, normal(40, K, dtype, 9) * 1e30, weight(K, dtype) * 1e-25
+    X, R, w = X.cuda(), R.cuda(), w.cuda()
+    S, Y, q, scale = torch.empty_like(X), torch.empty_like(X), torch.empty(40, K, dtype=torch.int8, device="cuda"), torch.empty(40, device="cuda")
+    b.rmsnorm_into(X, w, Y=Y, q=q, scale=scale, R=R, S=S, eps=0.0)
+    for s_of, y_of in (("X", "R"), ("R", "X"), (None, "X"), (None, "R")):
+        x, r, q2, s2 = X.clone(), R.clone(), torch.empty_like(q), torch.empty_like(scale)
+        at = {"X": x, "R": r, None: None}
+        b.rmsnorm_into(x, w, Y=at[y_of], q=q2, scale=s2, R=r, S=at[s_of], eps=0.0)
+        assert torch.equal(at[y_of], Y) and torch.equal(q2, q) and torch.equal(s2, scale)
+    dY, dS = normal(40, K, dtype, 10).cuda(), normal(40, K, dtype, 11).cuda()
+    dX = b.rmsnorm_backward_into(dY, S, w, torch.empty_like(S), dS=dS, eps=0.0)[0]
+    for into in range(3):
+        given = [dY.clone(), S.clone(), dS.clone()]
+        assert torch.equal(b.rmsnorm_backward_into(given[0], given[1], w, given[into], dS=given[2], eps=0.0)[0], dX)
+
+
 def test_ties_are_rounded_to_even():
     """Rows whose quotients lie on and next to the ties."""
     b = binding()
