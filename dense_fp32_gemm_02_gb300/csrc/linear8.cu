@@ -30,8 +30,8 @@ struct Call {
     cudaStream_t stream;
 };
 
-// The tiles of up to 256 rows and their ranges: the fewest us over the counts of ranges, with 0.35
-// us for each 128 k of a block and 4 to fill and empty it.
+// The tiles of up to 256 rows and their ranges: the fewest us over the counts of ranges, with so
+// many for each 128 k of a block, by its rows, and 5.5 to fill and empty it.
 TileWork tiles_of(const Call &c, int sms) {
     TileWork w{};
     w.M = c.M, w.N = c.N, w.K = c.K;
@@ -40,16 +40,22 @@ TileWork tiles_of(const Call &c, int sms) {
     w.rows = ((c.M + w.down - 1) / w.down + 15) / 16 * 16;
     w.timeout_ns = sgh::wait_timeout_ns();
     const int steps = (c.K + 127) / 128;
+    const double slab = w.rows <= 32 ? 0.45 : w.rows <= 64 ? 0.6 : w.rows <= 128 ? 0.85 : 1.75;
     double least = 0;
     for (int n = 1; n <= std::min(steps, MOST_CLUSTER); ++n) {
         const int per = (steps + n - 1) / n;
         if ((steps + per - 1) / per != n) continue;   // a range would be empty
         const long long items = (long long)w.across * w.down * n, waves = (items + sms - 1) / sms;
-        const double cost = double(waves) * (per * 0.35 + 4.0) + 0.25 * n;
-        if (w.ranges == 0 || cost < least) least = cost, w.ranges = n, w.range = per * 128;
+        const double of = double(waves) * (per * slab + 5.5) + 0.25 * n;
+        if (w.ranges == 0 || of < least) least = of, w.ranges = n, w.range = per * 128;
     }
     return w;
 }
+
+// Up to so many rows W is brought to float16 on its way (byte_tiles.cuh); more rows make it worth while to
+// lay both matrices out as bfloat16 first.  us at 4096 x 4096, on its way / laid out: 64 rows 10.6 / 27.6,
+// 256 rows 19.9 / 34.2, 512 rows 32 / 37, 1024 rows 57 / 38; 753 x 678 x 4443 36.8 / 22.
+constexpr int kTileRows = 512;
 
 int encode_bytes(CUtensorMap *map, const signed char *p, long long inner, long long outer, long long pitch, uint32_t box_inner,
                  uint32_t box_outer) {
@@ -101,11 +107,6 @@ int finish(const Call &c, int ranges, const int *partial) {
 }
 
 bool aligned_rows(const signed char *p, long long ld, int to = 16) { return sgh::aligned(p, size_t(to)) && ld % to == 0; }
-
-// Up to so many rows W is brought to float16 on its way; more rows make it worth while to lay both
-// matrices out as bfloat16 first.  us at 4096 x 4096, on its way / laid out: 64 rows 10.6 / 27.6, 256 rows
-// 19.9 / 34.2, 512 rows 31.1 / 37.4, 1024 rows 57 / 43.5.
-constexpr int kTileRows = 512;
 
 template <class T>
 int linear8(Call c) {

@@ -18,9 +18,9 @@ template <class T, Mode MODE>
 struct Kernels {
     static constexpr bool A_MN = MODE == TWO, B_MN = MODE != SUM, BYTES_MODE = MODE == BYTES;
     static constexpr int PARTS = sizeof(T) == 4 && !BYTES_MODE ? 3 : 1;
-    static constexpr auto *main = &pair_gemm_kernel<T, PARTS, A_MN, B_MN, MODE, BYTES_MODE>;
-    // (of several parts, and of bytes, the one kernel is for any length)
-    static constexpr auto *chunks = &pair_gemm_kernel<T, PARTS, A_MN, B_MN, MODE, BYTES_MODE || PARTS == 1>;
+    static constexpr auto *main = &pair_gemm_kernel<T, PARTS, A_MN, B_MN, MODE, false>;
+    // (of several parts the one kernel is for any length)
+    static constexpr auto *chunks = &pair_gemm_kernel<T, PARTS, A_MN, B_MN, MODE, PARTS == 1>;
 };
 
 }  // namespace
@@ -51,7 +51,7 @@ int sgq::run(const Product &g, const Output<T> &out, sgp::Split split, float *pa
     p.per_split = (p.slabs + split.splits - 1) / split.splits;
     p.partial = partial;
     p.timeout_ns = sgh::wait_timeout_ns();
-    const auto kernel = p.per_split > sgp::LONG_CHUNK ? K::chunks : K::main;
+    const auto kernel = p.per_split > chunk_slabs(K::PARTS > 1, MODE == BYTES) ? K::chunks : K::main;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(SMEM_BYTES));
     if (e != cudaSuccess) return sgh::cuda_fail(e);
     // (a CTA's rows of A, the last ones of few left as they are in shared memory: they reach no output)

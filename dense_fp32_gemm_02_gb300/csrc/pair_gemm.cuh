@@ -52,6 +52,10 @@ struct Params {
 // Slabs of a chunk of the accumulation: see parts_gemm.cuh; BYTES 1024 k.
 __host__ __device__ constexpr int chunk_slabs(bool several, bool bytes) { return bytes ? 16 : several ? 4 : sgp::LONG_CHUNK; }
 
+__device__ __forceinline__ void sts_float(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
 // The work of a pair of CTAs, as sgp::Items; columns of an output are `cols` from col0, of which
 // this CTA loads `load` from load0 of matrix `which`.
 template <Mode MODE>
@@ -303,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     } else {
         // ================================================================ epilogue (both CTAs)
         const int quarter = warp & 3, half = (warp - 2) >> 2;
-        float *buf = stage_out + (warp - 2) * (32 * (CHUNKED ? 33 : 32));
+        const uint32_t buf = smem_addr(stage_out + (warp - 2) * (32 * (CHUNKED ? 33 : 32)));
         const uint32_t lanes = taddr + (uint32_t(quarter * 32) << 16);
         int turn = 0;
         bool ok = true;
@@ -333,72 +337,111 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
             // A lane's row of 32 columns from `col`, given two at a time, written a column to a lane; where the sums
             // leave registers for it (64 x 8192 x 4096 bfloat16 weight gradients 82 -> 55 us; beside 128 sums it
-            // spilled, and 79 us of float32 became 86) and rows are aligned, four columns to a lane.
-            auto write = [&](auto *out, long long ld, int col, auto &&value) {
+            // spilled, and 79 us of float32 became 86) and rows are aligned, four columns to a lane.  SCALED: by the
+            // rows' and columns' scales, and the bias (not added where there is none: it would turn -0 into 0).
+            const float scale = BYTES_MODE && !p.partial && row0 + lane < p.M ? to.scale[row0 + lane] : 0.0f;   // of this lane's row
+            auto write = [&](auto *out, long long ld, int col, auto scaled, auto &&value) {
                 using E = std::remove_reference_t<decltype(*out)>;
+                constexpr bool SCALED = decltype(scaled)::value;
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 32; i += CHUNKED ? 2 : 4) {
                     const float2 v = value(i);
                     if constexpr (CHUNKED) {
-                        buf[lane * 33 + i] = v.x, buf[lane * 33 + i + 1] = v.y;
+                        sts_float(buf + uint32_t(lane * 33 + i) * 4, v.x);
+                        sts_float(buf + uint32_t(lane * 33 + i + 1) * 4, v.y);
                     } else {   // rows 128 bytes apart, their 16-byte pieces swizzled
                         const float2 u = value(i + 2);
-                        *reinterpret_cast<float4 *>(buf + lane * 32 + ((i / 4) ^ (lane & 7)) * 4) = make_float4(v.x, v.y, u.x, u.y);
+                        sts128(buf + uint32_t(lane * 128 + ((i / 4) ^ (lane & 7)) * 16), make_float4(v.x, v.y, u.x, u.y));
                     }
                 }
                 __syncwarp();
+                if (!SG_IN_RANGE(col + 32 <= it.col0 + it.cols && row0 + rows <= (it.tm + 1) * TILE && it.split < p.splits)) return;
+                const bool biased = SCALED && to.bias;
+                auto finished = [&](float v, float of_row, float of, float bias) {
+                    if (!SCALED) return v;
+                    v *= of_row * of;
+                    return biased ? v + bias : v;
+                };
                 if constexpr (!CHUNKED) {
-                    if (!SG_IN_RANGE(col + 32 <= it.col0 + it.cols && row0 + rows <= (it.tm + 1) * TILE)) return;
                     if (col + 32 <= p.N && ld % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (4 * sizeof(E) - 1)) == 0) {
-                        E *at = out + (long long)(row0 + (lane >> 3)) * ld + col + (lane & 7) * 4;
-                        const float *from = buf + lane / 8 * 32;
-#pragma unroll 8
-                        for (int r = lane >> 3; r < rows; r += 4, at += 4 * ld, from += 4 * 32) {
-                            float v[4];
-                            sgl::load4(from + ((lane & 7) ^ (r & 7)) * 4, v);
-                            sgl::store4(at, v);
+                        const int c = col + (lane & 7) * 4, r0 = lane >> 3;
+                        float of[4], bias[4];
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) {
+                            of[d] = SCALED ? to.wscale[c + d] : 0.0f;
+                            bias[d] = biased ? sgl::to_f32(to.bias[c + d]) : 0.0f;
+                        }
+                        E *at = out + (long long)(row0 + r0) * ld + c;
+                        // (rows r0, r0 + 8, ... and r0 + 4, r0 + 12, ... have their piece in the same place of the 128 bytes)
+                        const uint32_t even = buf + uint32_t(r0 * 128 + ((lane & 7) ^ r0) * 16);
+                        const uint32_t odd = buf + uint32_t(r0 * 128 + ((lane & 7) ^ (r0 + 4)) * 16);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j, at += 4 * ld) {
+                            const float of_row = SCALED ? __shfl_sync(0xffffffffu, scale, 4 * j + r0) : 0.0f;
+                            const float4 x = lds128((j & 1 ? odd : even) + uint32_t(j * 512));
+                            const float v[4] = {finished(x.x, of_row, of[0], bias[0]), finished(x.y, of_row, of[1], bias[1]),
+                                                finished(x.z, of_row, of[2], bias[2]), finished(x.w, of_row, of[3], bias[3])};
+                            if (4 * j + r0 < rows) sgl::store4(at, v);
                         }
                         return;
                     }
                 }
                 const int c = col + lane;
-                if (c >= p.N) return;
-                if (!SG_IN_RANGE(c < it.col0 + it.cols && row0 + rows <= (it.tm + 1) * TILE && it.split < p.splits)) return;
+                const bool in = c < p.N;
+                if (!SCALED && !in) return;
+                const float of = SCALED && in ? to.wscale[c] : 0.0f, bias = biased && in ? sgl::to_f32(to.bias[c]) : 0.0f;
                 E *at = out + (long long)row0 * ld + c;
-#pragma unroll 8
-                for (int r = 0; r < rows; ++r)
-                    at[(long long)r * ld] =
-                        sgl::from_f32<E>(CHUNKED ? buf[r * 33 + lane] : buf[r * 32 + ((lane >> 2) ^ (r & 7)) * 4 + (lane & 3)]);
+                uint32_t from[8];   // of rows 0 to 7, and 8 further on each time
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    from[r] = buf + (CHUNKED ? uint32_t(r * 33 + lane) * 4
+                                             : uint32_t(r * 128 + ((lane >> 2) ^ r) * 16 + (lane & 3) * 4));
+                for (int r = 0; r < rows; r += 8) {   // (rows: of the whole warp)
+#pragma unroll
+                    for (int d = 0; d < 8; ++d, at += ld) {
+                        const float of_row = SCALED ? __shfl_sync(0xffffffffu, scale, r + d) : 0.0f;
+                        const float v = finished(lds32(from[d] + uint32_t(r * (CHUNKED ? 132 : 128))), of_row, of, bias);
+                        if (r + d < rows && (!SCALED || in)) *at = sgl::from_f32<E>(v);
+                    }
+                }
             };
+            constexpr std::false_type AS_IT_IS{};
             // 32 columns of the tile's sums: x (and GATE: y, the same columns of U)
             auto finish = [&](int c, const float (&x)[32], const float (&y)[32]) {
                 const int col = col0 + c * 32;
                 auto xs = [&](int i) { return make_float2(x[i], x[i + 1]); };
                 auto ys = [&](int i) { return make_float2(y[i], y[i + 1]); };
-                if (p.partial) {
+                if constexpr (BYTES_MODE) {   // (a range's sums are up to 2^24 here, and stay whole)
+                    if (p.partial)
+                        write(p.partial + (long long)it.split * p.M * p.N, (long long)p.N, col, AS_IT_IS, [&](int i) {
+                            return make_float2(__int_as_float(__float2int_rn(x[i])), __int_as_float(__float2int_rn(x[i + 1])));
+                        });
+                    else
+                        write(to.out, to.ldo, col, std::true_type{}, xs);
+                } else if (p.partial) {
                     constexpr int OUTPUTS = MODE == GATE || MODE == TWO ? 2 : 1;
                     const long long ld = (long long)OUTPUTS * p.N;
                     float *out = p.partial + (long long)it.split * p.M * ld + (long long)it.which * p.N;
-                    write(out, ld, col, xs);
-                    if (MODE == GATE) write(out + p.N, ld, col, ys);
+                    write(out, ld, col, AS_IT_IS, xs);
+                    if (MODE == GATE) write(out + p.N, ld, col, AS_IT_IS, ys);
                 } else if constexpr (MODE == GATE) {
                     if (to.out) {
-                        write(to.out, to.ldo, col, xs);
-                        write(to.out1, to.ldo1, col, ys);
+                        write(to.out, to.ldo, col, AS_IT_IS, xs);
+                        write(to.out1, to.ldo1, col, AS_IT_IS, ys);
                     }
                     sgl::with_act(to.act, [&](auto act) {
-                        write(to.H, to.ldh, col, [&](int i) {
+                        write(to.H, to.ldh, col, AS_IT_IS, [&](int i) {
                             const float2 v = sgl::gate_value<T, decltype(act)::value>(xs(i));
                             return make_float2(v.x * y[i], v.y * y[i + 1]);
                         });
                     });
                 } else {
-                    write(it.which ? to.out1 : to.out, it.which ? to.ldo1 : to.ldo, col, xs);
+                    write(it.which ? to.out1 : to.out, it.which ? to.ldo1 : to.ldo, col, AS_IT_IS, xs);
                 }
             };
 
-            if constexpr (BYTES_MODE) {
+            if constexpr (BYTES_MODE && CHUNKED) {
                 int sum[4][32];
                 for (int s = 0; s < it.slabs && ok; s += PER_CHUNK, ++turn) {
                     if (!(ok = wait_full(turn & 1, turn >> 1))) break;
@@ -416,28 +459,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     hand_back(turn & 1);
                 }
                 if (!ok) break;
-                const float scale = row0 + lane < p.M ? to.scale[row0 + lane] : 0.0f;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     if (c * 32 >= width) break;
-                    const int col = col0 + c * 32, own = col + lane;
-                    if (p.partial) {   // (they stay whole)
-                        write(p.partial + (long long)it.split * p.M * p.N, (long long)p.N, col, [&](int i) {
+                    const int col = col0 + c * 32;
+                    if (p.partial)   // (they stay whole)
+                        write(p.partial + (long long)it.split * p.M * p.N, (long long)p.N, col, AS_IT_IS, [&](int i) {
                             return make_float2(__int_as_float(sum[c][i]), __int_as_float(sum[c][i + 1]));
                         });
-                        continue;
-                    }
-                    const float w = own < p.N ? to.wscale[own] : 0.0f, b = to.bias && own < p.N ? sgl::to_f32(to.bias[own]) : 0.0f;
-                    write(to.out, to.ldo, col, [&](int i) {
-                        float2 v;
-                        v.x = float(sum[c][i]) * (scale * __shfl_sync(0xffffffffu, w, i));
-                        v.y = float(sum[c][i + 1]) * (scale * __shfl_sync(0xffffffffu, w, i + 1));
-                        if (to.bias) {   // (without one nothing is added: it would turn -0 into 0)
-                            v.x += __shfl_sync(0xffffffffu, b, i);
-                            v.y += __shfl_sync(0xffffffffu, b, i + 1);
-                        }
-                        return v;
-                    });
+                    else
+                        write(to.out, to.ldo, col, std::true_type{},
+                              [&](int i) { return make_float2(float(sum[c][i]), float(sum[c][i + 1])); });
                 }
             } else if constexpr (CHUNKED) {
                 float sum[4][32];   // GATE: two of G, two of U
