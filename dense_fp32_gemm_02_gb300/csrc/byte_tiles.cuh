@@ -333,22 +333,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     }
 }
 
-// Bytes from `shift` of the 32 in a and b.
-__device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int shift) {
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    if (shift & 8) {
-#pragma unroll
-        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-    }
-    if (shift & 4) {
-#pragma unroll
-        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-    }
-    const int bits = (shift & 3) * 8;
-    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
-}
-
 // Rows of bytes at any pitch as rows that are 16-byte aligned (what lies behind a row in its last 16
 // is never read as the matrix's): a thread to 16 bytes, two aligned loads shifted into place, or, where those
 // would leave the matrix, byte by byte.
@@ -365,17 +349,19 @@ static __global__ void __launch_bounds__(256)
         if (!SG_IN_RANGE(i < rows && c < cols && c + 16 <= pitch)) continue;
         const signed char *from = p + i * ld + c;
         const int shift = int(reinterpret_cast<uintptr_t>(from) & 15);
-        uint4 v;
+        uint32_t v[4];
         if (from - shift >= p && from - shift + 32 <= end) {
-            const uint4 *at = reinterpret_cast<const uint4 *>(from - shift);
-            v = shifted(at[0], at[1], shift);
+            const uint4 at[2] = {reinterpret_cast<const uint4 *>(from - shift)[0], reinterpret_cast<const uint4 *>(from - shift)[1]};
+            uint32_t both[8];
+            memcpy(both, at, 32);
+            shift_bytes(both, shift, v);
         } else {
             alignas(16) signed char x[16];
 #pragma unroll
             for (int d = 0; d < 16; ++d) x[d] = c + d < cols ? from[d] : static_cast<signed char>(0);
-            v = *reinterpret_cast<const uint4 *>(x);
+            memcpy(v, x, 16);
         }
-        *reinterpret_cast<uint4 *>(out + i * pitch + c) = v;
+        *reinterpret_cast<uint4 *>(out + i * pitch + c) = make_uint4(v[0], v[1], v[2], v[3]);
     }
 }
 

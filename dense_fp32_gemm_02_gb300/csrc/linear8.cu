@@ -1,5 +1,6 @@
 // linear8.cu -- entry point of the product of int8 matrices with scales for each row and column.
 #include "layer_host.h"
+#include "byte_rows.cuh"
 #include "byte_tiles.cuh"
 #include "linear8.cuh"
 #include "packed.cuh"
@@ -108,11 +109,51 @@ int finish(const Call &c, int ranges, const int *partial) {
 
 bool aligned_rows(const signed char *p, long long ld, int to = 16) { return sgh::aligned(p, size_t(to)) && ld % to == 0; }
 
+// One to four rows, unless their range of q in shared memory would be too long (byte_rows.cuh).  us so / by
+// tiles, rows of bfloat16: at 4096 x 4096 one row 7.1 / 12.4, two 7.9 / 12.5, four 9.1 / 12.6; four at 8192 x 8192
+// 23 / 25, at 65536 x 1024 72 / 45, at 8191 x 8191 35 / 46.
+constexpr int kStreamedRows = 4;
+bool streamed(const Call &c) {
+    return c.M <= kStreamedRows && c.K > 0 && (long long)c.M * c.K <= MOST_CLUSTER * ROWS_RANGE;
+}
+
+// The ranges: the least of waves of two blocks to an SM times the steps of a block, with 3 to begin and end it.
+template <class T, int ROWS, int TILE>
+int stream(const Call &c, int sms) {
+    constexpr int STEP = rows_step(TILE);
+    const int across = (c.N + TILE - 1) / TILE, steps = (c.K + STEP - 1) / STEP;
+    ByteRows<T> a{c.M, c.N, c.K, 0, 0, static_cast<const T *>(c.X), c.q, c.W, c.scale, c.wscale, static_cast<const T *>(c.bias),
+                  static_cast<T *>(c.Y), c.ldx, c.ldq, c.ldw, c.ldy};
+    long long least = 0;
+    for (int n = 1; n <= std::min(steps, MOST_CLUSTER); ++n) {
+        const int per = (steps + n - 1) / n;
+        if ((steps + per - 1) / per != n || per * STEP > ROWS_RANGE) continue;   // a range would be empty, or too long
+        const long long cost = ((long long)across * n + 2 * sms - 1) / (2 * sms) * (per + 3);
+        if (a.ranges == 0 || cost < least) least = cost, a.ranges = n, a.range = per * STEP;
+    }
+    const auto kernel = aligned_rows(c.W, c.ldw, ROWS == 4 ? 4 : 8) ? byte_rows_kernel<T, ROWS, TILE, true> : byte_rows_kernel<T, ROWS, TILE, false>;
+    const size_t smem = byte_rows_smem<ROWS, TILE>(a.range);
+    if (smem > 40960) {   // (with what the kernel declares itself, over the 48 KB that need no leave)
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return sgh::cuda_fail(e);
+    }
+    return sgh::launch_cluster("int8, W streamed to few rows", kernel, dim3(unsigned(across * a.ranges)), ROWS_THREADS, smem, a.ranges,
+                               c.stream, a);
+}
+
 template <class T>
 int linear8(Call c) {
     int sms, st;
     cudaMemPool_t pool;
     if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
+    if (streamed(c)) {
+        // (columns whose tiles of 128 would leave SMs without a block; 16384 x 1024, tiles of 64 / 128: 7.2 / 10.5 us)
+        const bool narrow = (long long)(c.N + 127) / 128 * MOST_CLUSTER <= sms;
+        return c.M > 2    ? stream<T, 4, 128>(c, sms)
+               : c.M == 2 ? stream<T, 2, 128>(c, sms)
+               : narrow   ? stream<T, 1, 64>(c, sms)
+                          : stream<T, 1, 128>(c, sms);
+    }
     const bool own_rows = c.X != nullptr && c.K > 0, tiles = c.M <= kTileRows;
     const long long qpitch = (c.K + 15LL) / 16 * 16, xpitch = pitch8(c.K), wpitch = pitch8(c.N), bpitch = (c.N + 15LL) / 16 * 16;
     const size_t q_bytes = own_rows ? size_t(c.M) * qpitch : 0, s_floats = own_rows ? c.M : 0;

@@ -4,25 +4,20 @@
 //   8 bits: scale = max|y| / 127,  q_j = rint(y_j / scale) = rint(127 p_j / max|p|),  p = v w
 //
 // q does not depend on rstd, so the row's sum of squares and its largest |p| are taken together in
-// one pass, and q is the exactly rounded quotient whatever order the sum is taken in: 127 p / max is
-// worked out in fp32 (at most 4 roundings, 3.1e-5 in q's units), and where that is within NEAR = 2^-14
-// of a tie the products are compared exactly (p has 16 bits from bfloat16, 48 from float32, where
-// the maximum is kept as a pair, value and remainder, for it).
+// one pass, and q is the exactly rounded quotient whatever order the sum is taken in (rows8.cuh; p has
+// 16 bits from bfloat16, 48 from float32, where the maximum is kept as a pair, value and remainder,
+// for the comparison near a tie).
 //
 // A row goes to a group of threads (a warp or a block) that keeps it in registers between its
 // two uses, up to 16384 columns; longer rows are read twice (LONG).  Everything is read and
 // written once, and the kernels are bound by that.
 #pragma once
 
-#include "act8.cuh"
 #include "kernels.cuh"
+#include "rows8.cuh"
 
 namespace sgl {
 
-constexpr float NEAR = 0x1p-14f;
-// The range of the largest |p| in which fp32 products and 127 / max lose nothing; rows outside it
-// are quantised in 64 bits.
-constexpr float LEAST_TOP = 0x1p-60f, MOST_TOP = 0x1p100f;
 // The range of a row's sum of squares in which no term has overflowed or counts for too little.
 constexpr float LEAST_SQUARES = 0x1p-80f, MOST_SQUARES = 0x1p120f;
 
@@ -218,17 +213,7 @@ __device__ __noinline__ double rare_rows8(GroupSums &sm, V v, const T *w, signed
     return top;
 }
 
-// q of |p| near a tie: n or n + 1, n the whole part of the fp32 quotient, by the sign of 127 |p| - (n
-// + 1/2) top.  p of 24 bits (from bfloat16 16): the difference of the products in fp32 is exact, as it
-// is under 2^18 units of p's last place, and so is what (n + 1/2) top leaves.  (In bfloat16 ties are no
-// rare thing: a row whose largest value is 127 / 32 has 32 x for a quotient.)
-__device__ __forceinline__ float tie_exact(float p, float quotient, float top) {
-    const float n = floorf(fabsf(quotient)), h = n + 0.5f, t = h * top;
-    const float d = fmaf(127.0f, fabsf(p), -t) - fmaf(h, top, -t);
-    const bool odd = (int(n) & 1) != 0;
-    return copysignf(d > 0.0f || (d == 0.0f && odd) ? n + 1.0f : n, quotient);
-}
-// The same of a product of float32 values, in 64 bits.
+// tie_exact (rows8.cuh) of a product of float32 values, in 64 bits.
 static __device__ __noinline__ float tie_wide(float v, float w, float quotient, float top_hi, float top_lo) {
     const double p = fabs(double(v) * w), top = double(top_hi) + top_lo;
     const float n = floorf(fabsf(quotient));
@@ -349,7 +334,7 @@ __global__ void __launch_bounds__(norm_block(THREADS))
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float quotient = (KIND == ROWS8 ? v[c][e] : v[c][e] * w[e]) * times;
-                    out[e] = (quotient + 12582912.0f) - 12582912.0f;   // to an integer: 1.5 * 2^23 leaves no fraction
+                    out[e] = whole(quotient);
                     off = fmaxf(off, fabsf(quotient - out[e]));
                 }
                 if (off > 0.5f - NEAR) {

@@ -217,7 +217,8 @@ int sgemm_rmsnorm_backward(int type, int M, int K,
  * The rows are given as (q, scale) with X == NULL, or as the matrix X (M x K, of `type`), which the
  * call brings to rows of 8 bits itself.  W: K x N int8; wscale: N floats; bias: N elements of
  * `type`, or NULL.  Every int8 value, -128 too, counts as it stands.  The sums are exact, so K is at
- * most 131071 (SGEMM_ERR_TOO_LARGE); the rest is fp32, rounded once.  K == 0 gives bias, or 0.
+ * most 131071 (SGEMM_ERR_TOO_LARGE); the rest is fp32, rounded once.  K == 0 gives bias, or 0.  Y
+ * must not overlap an input.
  */
 int sgemm_linear8(int type, int M, int N, int K,
                   const void *X, int ldx,
@@ -242,6 +243,7 @@ int sgemm_linear8(int type, int M, int N, int K,
  *
  * X: M x K; Wg, Wu: K x N.  G and U, NULL together, receive the projections for the backward pass;
  * H is made of their fp32 sums, before they are rounded to `type`.  K == 0 gives zero sums.
+ * The outputs must not overlap an input or each other.
  */
 int sgemm_gated(int type, int M, int N, int K,
                 const void *X, int ldx,

@@ -75,6 +75,49 @@ def test_rows_of_the_type(M, N, K, dtype):
     assert bool(torch.isnan(Y[0]).all()) and (M == 1 or bool(torch.isfinite(Y[1:]).all()))
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("N,K", [(1, 1), (63, 3), (65, 5), (128, 256), (129, 257), (2432, 511), (2433, 513), (70, 2049), (64, 16385),
+                                 (9, 65536), (7, 65537), (20000, 40)])
+def test_few_rows(M, N, K, dtype):
+    """Rows given in 8 bits and rows of the type, from aligned and from odd places, with the same sums."""
+    b = binding()
+    g = torch.Generator()
+    g.manual_seed(M * 100003 + N * 101 + K)
+    X = (torch.randn(M, K, generator=g) * 5).to(dtype)
+    W, wscale, bias = bytes_of(K, N, 41), floats(N, 42), floats(N, 43, dtype)
+    q, scale = rows8_reference(X)
+    scale = scale.float()
+    flat = torch.full((K * N + 64,), 99, dtype=torch.int8, device="cuda")
+    for offset in (0, 1, 4, 8):
+        view = flat[offset:offset + K * N].view(K, N)
+        view.copy_(W)
+        Y, Z = (torch.full((M, N + 1), 3.0, dtype=dtype, device="cuda")[:, :N] for _ in range(2))
+        b.linear8_into((q.cuda(), scale.cuda()), view, wscale.cuda(), Y, bias=bias.cuda())
+        check(Y, q, scale, W, wscale, bias, "Y")
+        b.linear8_into(device_matrix(X, offset, offset // 4), view, wscale.cuda(), Z, bias=bias.cuda())
+        ref, mag = linear8_reference(q, rows8_reference(X)[1], W, wscale, bias)
+        rounded(Z, ref, 5 * 2.0 ** -24 * mag, "rows of the type")
+    assert b.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("M", [1, 2, 4])
+def test_few_rows_out_of_range(M, dtype):
+    """Rows of the smallest and the largest values, of ties, of zeros, with an infinity and a NaN: as in many rows."""
+    b = binding()
+    K, N = 1000, 200
+    x = torch.arange(K).float() % 255 - 127.0
+    rows = [x * 0.5, x * 2.0 ** -133, x * 2.0 ** -120, x * 2.0 ** 120, x * 2.0 ** 115, x * 0.0, x + 0.0, x * 1.5, x.clone()]
+    rows[6][17], rows[7][999], rows[8][0] = float("inf"), float("-inf"), float("nan")
+    W, wscale = bytes_of(K, N, 44), floats(N, 45)
+    many = torch.stack(rows + [x * 0.75] * 8).to(dtype).cuda()
+    all_rows = b.linear8_into(many, W.cuda(), wscale.cuda(), torch.empty(len(many), N, dtype=dtype, device="cuda"))
+    for r in range(len(rows)):
+        Y = b.linear8_into(many[r:r + M].contiguous(), W.cuda(), wscale.cuda(), torch.empty(M, N, dtype=dtype, device="cuda"))
+        assert torch.equal(torch.nan_to_num(Y, 3.0), torch.nan_to_num(all_rows[r:r + M], 3.0)), r
+
+
 @pytest.mark.parametrize("fill", [63, 64, 65, 127, -128])
 def test_many_rows_with_magnitudes_at_the_bound(fill):
     """Rows whose 2048 magnitudes add up to just under, to and past 2^17, in one row of many: sums that fp32 holds
