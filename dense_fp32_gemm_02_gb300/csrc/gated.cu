@@ -52,17 +52,14 @@ int finish(int M, int N, int ranges, const float *x, const float *y, long long p
 }
 
 // The operands that the TMA does not read where they lie, as parts.  `beside`: not the call's first kernel, it
-// runs beside the one before it (host_state.h); true from here on.
+// runs beside the one before it (host_state.h).
 template <class T>
-int pack(const Packed<T> &p, const Packed<T> &q, bool &beside, int sms, cudaStream_t stream) {
-    const auto a = p.job(), b = q.job();
-    const long long octets = a.octets() + b.octets();
+int pack(const Packed<T> &Wg, const Packed<T> &Wu, const Packed<T> &X, bool beside, int sms, cudaStream_t stream) {
+    const auto g = Wg.job(), u = Wu.job(), x = X.job();
+    const long long octets = g.octets() + u.octets() + x.octets();
     if (octets == 0) return SGEMM_OK;
     const unsigned blocks = unsigned(std::min<long long>((octets + 255) / 256, 32LL * sms));
-    constexpr int PARTS = Packed<T>::PARTS;
-    const int st = sgh::launch(nullptr, parts_kernel<PARTS, PARTS, Rows<T>, Rows<T>>, dim3(blocks), 256, 0, stream, a, b, beside);
-    beside = true;
-    return st;
+    return sgh::launch(nullptr, gated_parts_kernel<T>, dim3(blocks), 256, 0, stream, g, u, x, beside);
 }
 
 // ------------------------------------------------------------------ forward
@@ -134,9 +131,7 @@ int forward(const Call &c) {
     Wg.place(ws);
     Wu.place(ws);
     float *partial = split.partial_floats ? ws.take<float>(split.partial_floats) : nullptr;
-    Packed<T> none(0, 0, nullptr, 8);
-    bool beside = false;
-    if ((st = pack(Wg, Wu, beside, sms, c.stream)) != SGEMM_OK || (st = pack(X, none, beside, sms, c.stream)) != SGEMM_OK) return st;
+    if ((st = pack(Wg, Wu, X, false, sms, c.stream)) != SGEMM_OK) return st;
     sgq::Product g{c.M, c.N, c.K, X.operand(), {Wg.operand(), Wu.operand()}};
     const sgq::Output<T> out{to.out, to.out1, to.H, to.ldo, to.ldo1, to.ldh, to.act, nullptr, nullptr, nullptr, nullptr};
     if ((st = sgq::run<T, sgq::GATE>(g, out, split, partial, sms, c.stream)) != SGEMM_OK) return st;
@@ -155,7 +150,7 @@ int backward(const Call &c) {
     if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
     constexpr int PARTS = Packed<T>::PARTS, PRODUCTS = PARTS == 3 ? 6 : 1;
     const bool want_dx = c.dX != nullptr, want_dw = c.dWg != nullptr;
-    Packed<T> X(c.M, c.K, c.X, c.ldx), Wg(c.K, c.N, c.Wg, c.ldwg), Wu(c.K, c.N, c.Wu, c.ldwu), none(0, 0, nullptr, 8);
+    Packed<T> X(c.M, c.K, c.X, c.ldx), Wg(c.K, c.N, c.Wg, c.ldwg), Wu(c.K, c.N, c.Wu, c.ldwu);
     if (!want_dw) X.direct = true;                  // no parts of them are needed
     if (!want_dx) Wg.direct = Wu.direct = true;
     const sgp::Split sum = want_dx ? sgq::plan(sgq::SUM, c.M, c.K, c.N, PRODUCTS, sms) : sgp::Split{1, 256, 0};
@@ -180,9 +175,7 @@ int backward(const Call &c) {
     const long long octets = (long long)c.M * job.per_row.d;
     st = sgh::launch(nullptr, gated_slopes_kernel<T>, dim3(unsigned(std::min<long long>((octets + 255) / 256, 32LL * sms))), 256,
                      0, c.stream, job);
-    bool beside = true;
-    if (st != SGEMM_OK || (st = pack(Wg, Wu, beside, sms, c.stream)) != SGEMM_OK || (st = pack(X, none, beside, sms, c.stream)) != SGEMM_OK)
-        return st;
+    if (st != SGEMM_OK || (st = pack(Wg, Wu, X, true, sms, c.stream)) != SGEMM_OK) return st;
     const sgp::Operand dG{d, c.N, c.M, PARTS, pitch, plane}, dU{d + PARTS * plane, c.N, c.M, PARTS, pitch, plane};
     if (want_dx) {
         sgq::Product g{c.M, c.K, c.N, {d, c.N, c.M, 2 * PARTS, pitch, plane}, {Wg.operand(), Wu.operand()}};

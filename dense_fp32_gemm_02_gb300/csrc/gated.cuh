@@ -152,4 +152,20 @@ __global__ void __launch_bounds__(256) gated_slopes_kernel(SlopesJob<T> a) {
     with_act(a.act, [&](auto act) { take_slopes<T, decltype(act)::value>(a); });
 }
 
+// ------------------------------------------------------------------ operands
+// The parts of the operands that the TMA cannot read where they lie, in one launch (1025 x 1023 x 3001 in
+// bfloat16 24.3 us, with X's in a launch of its own 25.9).  `beside`: not the call's first kernel, it runs beside the one before it.
+template <class T>
+__global__ void __launch_bounds__(256)
+    gated_parts_kernel(PartsJob<Rows<T>> g, PartsJob<Rows<T>> u, PartsJob<Rows<T>> x, bool beside) {
+    constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
+    if (!beside) sg::wait_prerequisites();
+    sg::launch_dependents();
+    const long long t = (long long)blockIdx.x * 256 + threadIdx.x, step = (long long)gridDim.x * 256;
+    take_parts<PARTS>(g, t, step);
+    take_parts<PARTS>(u, t, step);
+    take_parts<PARTS>(x, t, step);
+    if (beside && blockIdx.x == 0) sg::wait_prerequisites();
+}
+
 }  // namespace sgl
