@@ -21,7 +21,7 @@
 #pragma once
 
 #include "linear8.cuh"
-#include "parts_gemm.cuh"
+#include "tiles.cuh"
 
 namespace sgl {
 
@@ -51,14 +51,6 @@ struct ByteTile {
     static_assert(ROWS * TILE_COLS * 4 <= STAGES * STAGE + DEPTH * RAW, "the sums take their place");
 };
 
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
-        : "memory");
-}
-
 // Four int8 as two words of float16.
 __device__ __forceinline__ uint2 halves_of(uint32_t w) {
     w ^= 0x80808080u;
@@ -68,15 +60,6 @@ __device__ __forceinline__ uint2 halves_of(uint32_t w) {
     asm("sub.f16x2 %0, %1, %2;" : "=r"(out.y) : "r"(hi), "r"(0x64806480u));
     return out;
 }
-__device__ __forceinline__ uint4 lds_words(uint32_t at) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-    return v;
-}
-__device__ __forceinline__ void sts_words(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-
 template <class T, int ROWS>
 __global__ void __launch_bounds__(TILE_THREADS, 1)
     byte_tiles_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mW, const TileWork w,
@@ -266,7 +249,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             const uint64_t da = desc_w + uint64_t(stage * (Z::STAGE >> 4)), db = desc_x + uint64_t(stage * (Z::STAGE >> 4));
             if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < Z::STEP / 16; ++kk) mma_f16(acc, da + kk * (2048 >> 4), db + kk * (32 >> 4), idesc, !first || kk > 0);
+                for (int kk = 0; kk < Z::STEP / 16; ++kk) mma_half(acc, da + kk * (2048 >> 4), db + kk * (32 >> 4), idesc, !first || kk > 0);
                 mma_commit(&empty[stage]);
                 if (s % Z::PER_CHUNK == Z::PER_CHUNK - 1 || s == slabs - 1) mma_commit(&acc_full[chunk & 1]);
             }

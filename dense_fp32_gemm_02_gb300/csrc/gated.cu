@@ -3,6 +3,7 @@
 #include "layer_host.h"
 #include "packed.cuh"
 #include "pair_gemm.h"
+#include "split_tiles.cuh"
 #include "variant.cuh"
 
 #define SGEMM_API extern "C" __attribute__((visibility("default")))
@@ -94,8 +95,8 @@ int forward_few_rows(const Call &c, bool stream_rows, int sms, cudaMemPool_t poo
         kernel<<<unsigned(blocks), RANK_THREADS, 0, c.stream>>>(w, X, Wg, c.ldwg, Wu, c.ldwu);
         st = sgh::launched(kFewRows);
     } else if constexpr (sizeof(T) == 4) {
-        auto kernel = c.M <= 16 ? gated_few_rows_kernel<1> : c.M <= 32 ? gated_few_rows_kernel<2> : gated_few_rows_kernel<4>;
-        const size_t smem = c.M <= 16 ? FewRows<1>::SMEM : c.M <= 32 ? FewRows<2>::SMEM : FewRows<4>::SMEM;
+        const auto kernel = gated_few_rows_kernel;
+        const size_t smem = FewRows<1>::SMEM;
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return sgh::cuda_fail(e);
         kernel<<<unsigned(blocks), RANK_THREADS, smem, c.stream>>>(w, X, Wg, c.ldwg, Wu, c.ldwu, w_wide);
@@ -106,6 +107,65 @@ int forward_few_rows(const Call &c, bool stream_rows, int sms, cudaMemPool_t poo
     st = finish<T, true>(c.M, c.N, w.ranges, w.partial, w.partial + one, c.N, (long long)c.M * c.N, to, c.stream);
     return st == SGEMM_OK ? ws.release() : st;
 }
+
+// Few float32 rows, W split on its way (split_tiles.cuh).
+int encode_floats(CUtensorMap *map, const float *p, long long inner, long long outer, long long pitch) {
+    const cuuint64_t dims[2] = {cuuint64_t(inner), cuuint64_t(outer)}, strides[1] = {cuuint64_t(pitch) * 4};
+    const cuuint32_t box[2] = {SPLIT_COLS, SPLIT_STEP}, steps[2] = {1, 1};
+    const CUresult r = sgh::encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float *>(p), dims, strides, box,
+                                           steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SGEMM_OK : sgh::driver_fail(int(r));
+}
+
+int forward_split(const Call &c, bool wide, int sms, cudaMemPool_t pool) {
+    SplitWork w{};
+    w.M = c.M, w.N = c.N, w.K = c.K;
+    w.across = (c.N + SPLIT_COLS - 1) / SPLIT_COLS;
+    w.down = (c.M + SPLIT_ROWS - 1) / SPLIT_ROWS;
+    w.rows = ((c.M + w.down - 1) / w.down + 15) / 16 * 16;
+    w.timeout_ns = sgh::wait_timeout_ns();
+    const int steps = (c.K + SPLIT_STEP - 1) / SPLIT_STEP;
+    const long long tiles = 2LL * w.across * w.down, one = (long long)c.M * c.N;
+    double least = 0;
+    for (int n = 1; n <= std::min(steps, 64); ++n) {   // us: a slab, filling and emptying a block, the ranges' sums
+        const int per = (steps + n - 1) / n;
+        if ((steps + per - 1) / per != n) continue;   // a range would be empty
+        const double cost = double((tiles * n + sms - 1) / sms) * (per * 1.0 + 6.0) + n * double(one) * 16 / 5.0e6;
+        if (w.ranges == 0 || cost < least) least = cost, w.ranges = n, w.range = per * SPLIT_STEP;
+    }
+    if (tiles * w.ranges > 0x7fffffffLL) return SGEMM_ERR_TOO_LARGE;
+    Packed<float> X(c.M, c.K, c.X, c.ldx), none(0, 0, nullptr, 8);
+    sgh::Workspace ws(pool, c.stream);
+    int st = ws.allocate(X.bytes() + sgh::Workspace::piece(size_t(one) * w.ranges * 8));
+    if (st != SGEMM_OK) return st;
+    X.place(ws);
+    w.partial = ws.take<float>(size_t(one) * w.ranges * 2);
+    if ((st = pack(none, none, X, false, sms, c.stream)) != SGEMM_OK) return st;
+    const SplitWeights weights{{static_cast<const float *>(c.Wg), static_cast<const float *>(c.Wu)}, {c.ldwg, c.ldwu}};
+    CUtensorMap mX, mG, mU;
+    if ((st = sgp::encode(&mX, X.operand(), SPLIT_STEP, unsigned(w.rows))) != SGEMM_OK) return st;
+    mG = mU = mX;
+    if (wide && ((st = encode_floats(&mG, weights.p[0], c.N, c.K, c.ldwg)) != SGEMM_OK ||
+                 (st = encode_floats(&mU, weights.p[1], c.N, c.K, c.ldwu)) != SGEMM_OK))
+        return st;
+    const auto kernel = wide ? split_tiles_kernel<true> : split_tiles_kernel<false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(SPLIT_SMEM));
+    if (e != cudaSuccess) return sgh::cuda_fail(e);
+    st = sgh::launch("gated, W split into bf16 parts on its way, tcgen05", kernel, dim3(unsigned(tiles * w.ranges)), SPLIT_THREADS,
+                     SPLIT_SMEM, c.stream, mX, mG, mU, weights, w);
+    if (st != SGEMM_OK) return st;
+    const PairOut<float> to{static_cast<float *>(c.G), static_cast<float *>(c.U), static_cast<float *>(c.H), c.ldg, c.ldu, c.ldh, c.act};
+    st = finish<float, true>(c.M, c.N, w.ranges, w.partial, w.partial + one * w.ranges, c.N, one, to, c.stream);
+    return st == SGEMM_OK ? ws.release() : st;
+}
+
+// Float32 rows up to which W is read by warp-level MMAs (rows.cuh), and split on its way to the tensor cores, W's
+// rows 16-byte aligned or not; more have its parts laid out first.  us, 16 rows of 4096 x 4096 40.8 by
+// warps / 40.7 split, of 704 x 1504 8.0 / 9.7; 192 rows of 4096 x 4096 110 split / 130 laid out, 256 rows 137 / 137 (4096 x
+// 8192: 254 / 222).  Not aligned: 17 rows of 2048 x 2047 23.0 by warps / 22.5, 64 rows 37.6 / 25.3, 128 rows 43.3
+// laid out / 37.2, 256 rows of 1023 x 3001 36.4 / 65.
+constexpr int kWarpRows = 16, kSplitRows = 192, kSplitUnaligned = 128;
 
 template <class T>
 int forward(const Call &c) {
@@ -121,7 +181,11 @@ int forward(const Call &c) {
     // by FMAs / by the tensor cores: 1 row of 1024 x 1024 6.0 / 8.4, of 4096 x 4096 15.9 / 18.1; 4 rows 7.8 / 8.8
     // and 27.8 / 18.4; 8 rows 8.5 / 9.0 and 28.4 / 18.6.
     if (c.M <= STREAM_ROWS && (PARTS == 3 || !in_place || c.M <= 2)) return forward_few_rows<T>(c, true, sms, pool);
-    if (PARTS == 3 && c.M <= MMA_ROWS) return forward_few_rows<T>(c, false, sms, pool);
+    if constexpr (PARTS == 3) {
+        if (c.M <= kWarpRows) return forward_few_rows<T>(c, false, sms, pool);
+        const bool wide = wide_rows(static_cast<const T *>(c.Wg), c.ldwg) && wide_rows(static_cast<const T *>(c.Wu), c.ldwu);
+        if (c.M <= (wide ? kSplitRows : kSplitUnaligned)) return forward_split(c, wide, sms, pool);
+    }
 
     const sgp::Split split = sgq::plan(sgq::GATE, c.M, c.N, c.K, PARTS == 3 ? 6 : 1, sms);
     sgh::Workspace ws(pool, c.stream);

@@ -23,15 +23,14 @@ __global__ void __launch_bounds__(RANK_THREADS, stream_blocks(MR))
                              w.partial + second * (long long)w.ranges * w.M * w.N, sm);
 }
 
-template <int MT>
-__global__ void __launch_bounds__(RANK_THREADS, 2)
+static __global__ void __launch_bounds__(RANK_THREADS, 2)
     gated_few_rows_kernel(RowsWork w, Rows<float> X, const float *Wg, long long ldg, const float *Wu, long long ldu,
                           bool w_wide) {
     extern __shared__ __align__(16) unsigned char smem_rows[];
     sg::launch_dependents();
     const int n = w.across * w.ranges, second = int(blockIdx.x) >= n;
     if (!SG_IN_RANGE(int(blockIdx.x) < 2 * n)) return;
-    few_rows<MT>(w, int(blockIdx.x) - second * n, X, second ? Wu : Wg, second ? ldu : ldg, w_wide,
+    few_rows<1>(w, int(blockIdx.x) - second * n, X, second ? Wu : Wg, second ? ldu : ldg, w_wide,
                  w.partial + second * (long long)w.ranges * w.M * w.N, smem_rows);
 }
 

@@ -149,6 +149,14 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// All copies of this thread.
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Arrives on an mbarrier when this thread's copies so far are there; the barrier's count has
+// a place for each thread that does so.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // ---------------------------------------------------------------- TMA
 // Bring the 128-byte line that holds `ptr` into L2 (no register result).
 __device__ __forceinline__ void prefetch_l2(const void *ptr) {

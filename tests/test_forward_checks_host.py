@@ -7,7 +7,7 @@ import pytest
 
 import test_layers_checks_host as layers
 
-FILES = ["norm.cuh", "gated.cuh", "linear8.cuh", "byte_tiles.cuh", "byte_rows.cuh", "pair_gemm.cuh"]
+FILES = ["norm.cuh", "gated.cuh", "linear8.cuh", "byte_tiles.cuh", "byte_rows.cuh", "split_tiles.cuh", "pair_gemm.cuh"]
 
 
 def functions():
@@ -39,7 +39,7 @@ def checks(name, seen=()):
 def test_the_kernels_are_found():
     assert {"norm_kernel", "norm_backward_kernel", "norm_weight_kernel", "gated_stream_kernel", "gated_few_rows_kernel",
             "pair_finish_kernel", "gated_slopes_kernel", "byte_finish_kernel", "byte_expand_kernel", "byte_tiles_kernel", "byte_pitch_kernel",
-            "pair_gemm_kernel", "byte_rows_kernel", "gated_parts_kernel"} == set(KERNELS)
+            "pair_gemm_kernel", "byte_rows_kernel", "gated_parts_kernel", "split_tiles_kernel"} == set(KERNELS)
 
 
 @pytest.mark.parametrize("kernel", KERNELS)
@@ -51,7 +51,8 @@ def test_early_kernels_wait_before_they_let_the_next_one_start():
     """As for the layers' kernels: what lets the next kernel start at its beginning is launched plainly, so that
     all earlier work has ended by then."""
     plain = {"gated_stream_kernel", "gated_few_rows_kernel", "norm_kernel"}
-    never_first = {"byte_expand_kernel"}      # X's form; W's, the call's first, waits
+    never_first = {"byte_expand_kernel",      # X's form; W's, the call's first, waits
+                   "split_tiles_kernel"}      # its parts of X are laid out first, by a kernel that waits
     for name in KERNELS:
         body = FUNCTIONS[name][1]
         wait, let = body.find("wait_prerequisites()"), body.find("launch_dependents()")

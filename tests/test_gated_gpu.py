@@ -60,6 +60,48 @@ def test_forward(M, N, K, dtype):
     assert b.device_status() == 0
 
 
+@pytest.mark.parametrize("pad", [0, 4, 3])
+@pytest.mark.parametrize("M,N,K", [(17, 4, 1), (17, 128, 64), (31, 132, 63), (48, 260, 65), (64, 516, 257), (65, 128, 1000), (100, 96, 515),
+                                   (128, 1000, 130), (129, 64, 260), (192, 388, 300), (193, 130, 70), (40, 64, 4100)])
+def test_forward_between_few_and_many_rows(M, N, K, pad):
+    """Float32 weights at pitches that the TMA reads and at others, over tiles and ranges that end inside one another."""
+    b = binding()
+    X, (Wg, Wu) = normal(M, K, torch.float32, 71), weights(K, N, torch.float32, 72)
+    pg, pu = device_matrix(Wg.cpu(), pad, 4), device_matrix(Wu.cpu(), 0 if pad != 4 else 8, 0)
+    flat = [torch.full((M + 2, N), 5.0, device="cuda") for _ in range(3)]
+    H, G, U = (f[1:1 + M] for f in flat)
+    b.gated_into(device_matrix(X.cpu(), 1, 1), pg, pu, H, G=G, U=U)
+    check_forward(X, Wg, Wu, "silu", H, G, U)
+    assert all(bool((f[0] == 5).all()) and bool((f[-1] == 5).all()) for f in flat)
+    assert torch.equal(b.gated_into(X, pg, pu, torch.empty_like(H)), H)
+    assert b.device_status() == 0
+
+
+@pytest.mark.parametrize("pad", [0, 3])
+def test_values_of_every_size_between_few_and_many_rows(pad):
+    """Float32 that needs all of its three parts, from 2^-100 to 2^60, each against the sum's own magnitudes; infinities reach
+    their own rows and columns alone."""
+    b = binding()
+    M, N, K = 50, 200, 300
+    g = torch.Generator()
+    g.manual_seed(73)
+    size = lambda *s: torch.exp2(torch.randint(-100, 61, s, generator=g).float())   # noqa: E731
+    X, Wg = torch.randn(M, K, generator=g) * size(M, 1), torch.randn(K, N, generator=g) * size(1, N)
+    Wu = torch.randn(K, N, generator=g)
+    X[3, 5], Wg[7, 11], Wu[9, 13] = float("inf"), float("-inf"), float("nan")
+    H, G, U = (torch.empty(M, N, device="cuda") for _ in range(3))
+    b.gated_into(X.cuda(), device_matrix(Wg, pad), device_matrix(Wu, pad), H, act="relu", G=G, U=U)
+    for got, W in ((G, Wg), (U, Wu)):
+        ref, mag = X.double() @ W.double(), X.double().abs() @ W.double().abs()
+        fine = torch.isfinite(ref) & (ref.abs() < 1e38)
+        assert bool(torch.isfinite(got.cpu()[fine]).all())
+        # the six pairs leave 2^-23.4 of a product, sums and their chunks (16 truncating additions of 2^-23, 3 chunks) the rest
+        over = (got.cpu().double() - ref).abs()[fine] > (24 * 2.0 ** -23) * mag[fine] + 1e-37
+        assert not bool(over.any())
+        odd = ~torch.isfinite(ref)
+        assert not bool(torch.isfinite(got.cpu()[odd]).any())
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
 @pytest.mark.parametrize("M", [2, 40, 300])
 @pytest.mark.parametrize("act", ["none", "relu"])
