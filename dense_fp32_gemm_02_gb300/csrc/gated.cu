@@ -92,15 +92,15 @@ int forward_few_rows(const Call &c, bool stream_rows, int sms, cudaMemPool_t poo
                               : gated_stream_kernel<T, 8, W>;
         };
         auto kernel = w_wide ? pick(std::true_type{}) : pick(std::false_type{});
-        kernel<<<unsigned(blocks), RANK_THREADS, 0, c.stream>>>(w, X, Wg, c.ldwg, Wu, c.ldwu);
-        st = sgh::launched(kFewRows);
+        st = sgh::launch(kFewRows, kernel, dim3(unsigned(blocks)), RANK_THREADS, 0, c.stream, w, X, Wg, (long long)c.ldwg, Wu,
+                         (long long)c.ldwu);
     } else if constexpr (sizeof(T) == 4) {
         const auto kernel = gated_few_rows_kernel;
         const size_t smem = FewRows<1>::SMEM;
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return sgh::cuda_fail(e);
-        kernel<<<unsigned(blocks), RANK_THREADS, smem, c.stream>>>(w, X, Wg, c.ldwg, Wu, c.ldwu, w_wide);
-        st = sgh::launched(kFewRows);
+        st = sgh::launch(kFewRows, kernel, dim3(unsigned(blocks)), RANK_THREADS, smem, c.stream, w, X, Wg, (long long)c.ldwg, Wu,
+                         (long long)c.ldwu, w_wide);
     }
     if (st != SGEMM_OK) return st;
     const PairOut<T> to{static_cast<T *>(c.G), static_cast<T *>(c.U), static_cast<T *>(c.H), c.ldg, c.ldu, c.ldh, c.act};

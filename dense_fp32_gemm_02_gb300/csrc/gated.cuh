@@ -16,6 +16,7 @@ template <class T, int MR, bool WIDE>
 __global__ void __launch_bounds__(RANK_THREADS, stream_blocks(MR))
     gated_stream_kernel(RowsWork w, Rows<T> X, const T *Wg, long long ldg, const T *Wu, long long ldu) {
     __shared__ __align__(16) float sm[StreamRows<T, MR>::FLOATS];
+    sg::wait_prerequisites();
     sg::launch_dependents();
     const int n = w.across * w.ranges, second = int(blockIdx.x) >= n;
     if (!SG_IN_RANGE(int(blockIdx.x) < 2 * n)) return;
@@ -27,6 +28,7 @@ static __global__ void __launch_bounds__(RANK_THREADS, 2)
     gated_few_rows_kernel(RowsWork w, Rows<float> X, const float *Wg, long long ldg, const float *Wu, long long ldu,
                           bool w_wide) {
     extern __shared__ __align__(16) unsigned char smem_rows[];
+    sg::wait_prerequisites();
     sg::launch_dependents();
     const int n = w.across * w.ranges, second = int(blockIdx.x) >= n;
     if (!SG_IN_RANGE(int(blockIdx.x) < 2 * n)) return;

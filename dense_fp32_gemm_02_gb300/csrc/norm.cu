@@ -51,8 +51,8 @@ int forward(const NormCall<T> &c, int sms, cudaStream_t stream) {
                       sgh::wide_rows(c.S, c.lds) && sgh::wide_rows(c.Y, c.ldy) && sgh::aligned(c.w, 16) &&
                       sgh::aligned(c.q, 8) && c.ldq % 8 == 0;
     const auto f = wide ? forward_form<T, KIND, true>(c.M, c.K, sms) : forward_form<T, KIND, false>(c.M, c.K, sms);
-    f.kernel<<<unsigned((c.M + f.rows - 1LL) / f.rows), f.threads, 0, stream>>>(c);
-    return sgh::launched(wide ? "norm, rows read 16 bytes at a time" : "norm, any alignment");
+    return sgh::launch(wide ? "norm, rows read 16 bytes at a time" : "norm, any alignment", f.kernel,
+                       dim3(unsigned((c.M + f.rows - 1LL) / f.rows)), unsigned(f.threads), 0, stream, c);
 }
 
 template <class T, int THREADS, int CHUNKS, bool WIDE, bool LONG = false>
@@ -91,8 +91,8 @@ int backward(NormBackCall<T> c, T *dw, cudaStream_t stream) {
     const size_t floats = dw ? size_t(blocks) * c.K : 0;
     if ((st = ws.allocate(sgh::Workspace::piece(floats * 4))) != SGEMM_OK) return st;
     c.partial = dw ? ws.take<float>(floats) : nullptr;
-    f.kernel<<<unsigned(blocks), f.threads, f.smem, stream>>>(c);
-    st = sgh::launched(wide ? "norm backward, rows read 16 bytes at a time" : "norm backward, any alignment");
+    st = sgh::launch(wide ? "norm backward, rows read 16 bytes at a time" : "norm backward, any alignment", f.kernel,
+                     dim3(unsigned(blocks)), unsigned(f.threads), f.smem, stream, c);
     if (st != SGEMM_OK) return st;
     if (dw) {
         st = sgh::launch(nullptr, norm_weight_kernel<T>, dim3(unsigned((c.K + 31LL) / 32)), 1024, 0, stream, c.K, blocks,

@@ -242,7 +242,8 @@ __global__ void __launch_bounds__(norm_block(THREADS))
     constexpr int GROUPS = norm_block(THREADS) / THREADS, SPAN = THREADS * 8 * CHUNKS;
     constexpr bool EIGHT = KIND != NORM, WITH_LO = EIGHT && KIND != ROWS8 && sizeof(T) == 4;
     __shared__ GroupSums sm;
-    if (KIND == ROWS8) sg::launch_dependents();   // (its call's first kernel, launched plainly: host_state.h)
+    sg::wait_prerequisites();
+    sg::launch_dependents();
     const int t = threadIdx.x % THREADS;
     const long long row = (long long)blockIdx.x * GROUPS + threadIdx.x / THREADS;
     if (row >= a.M || !SG_IN_RANGE(LONG || a.K <= SPAN)) return;
@@ -392,6 +393,8 @@ __global__ void __launch_bounds__(norm_block(THREADS), norm_blocks_per_sm<THREAD
     constexpr bool KEEP_W = !LONG && CHUNKS <= 2;
     extern __shared__ __align__(16) unsigned char norm_ring[];
     __shared__ GroupSums sm;
+    sg::wait_prerequisites();
+    sg::launch_dependents();
     __shared__ float columns[GROUPS > 1 ? SPAN : 1];
     const int t = threadIdx.x % THREADS, group = threadIdx.x / THREADS;
     if (!SG_IN_RANGE(LONG || a.K <= SPAN)) return;

@@ -48,19 +48,15 @@ def test_every_kernel_checks_its_indices(kernel):
 
 
 def test_early_kernels_wait_before_they_let_the_next_one_start():
-    """As for the layers' kernels: what lets the next kernel start at its beginning is launched plainly, so that
-    all earlier work has ended by then."""
-    plain = {"gated_stream_kernel", "gated_few_rows_kernel", "norm_kernel"}
+    """As for the layers' kernels; here a call's first kernel is launched early as well, and waits before it lets the
+    second one start, so that all earlier work has ended by then."""
     never_first = {"byte_expand_kernel",      # X's form; W's, the call's first, waits
                    "split_tiles_kernel"}      # its parts of X are laid out first, by a kernel that waits
     for name in KERNELS:
         body = FUNCTIONS[name][1]
         wait, let = body.find("wait_prerequisites()"), body.find("launch_dependents()")
-        if let >= 0 and name not in plain | never_first:
+        if let >= 0 and name not in never_first:
             assert 0 <= wait < let, name
-    with open(os.path.join(layers.CSRC, "gated.cu")) as f:
-        gated = f.read()
-    with open(os.path.join(layers.CSRC, "norm.cu")) as f:
-        norm = f.read()
-    assert gated.count("kernel<<<") == 2 and "launch(kFewRows" not in gated      # both few-row kernels
-    assert norm.count("f.kernel<<<") == 2 and "f.kernel," not in norm.replace("(f.kernel, cuda", "").replace("(&per_sm, f.kernel,", "")
+    for unit in ("norm.cu", "linear8.cu", "gated.cu", "pair_gemm.cu"):
+        with open(os.path.join(layers.CSRC, unit)) as f:
+            assert "<<<" not in f.read(), unit
