@@ -68,7 +68,7 @@ __device__ __forceinline__ void take_columns(const signed char *p, long long ld,
             } else {
                 uint32_t both[2 * WORDS];
                 memcpy(both, v[i], 2 * BYTES);
-                shift_bytes(both, int(reinterpret_cast<uintptr_t>(p + i * ld) & (BYTES - 1)), w[i]);
+                shift_bytes<1>(both, int(reinterpret_cast<uintptr_t>(p + i * ld) & (BYTES - 1)), w[i]);
             }
         }
     } else {

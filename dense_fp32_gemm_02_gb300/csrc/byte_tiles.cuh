@@ -337,7 +337,7 @@ static __global__ void __launch_bounds__(256)
             const uint4 at[2] = {reinterpret_cast<const uint4 *>(from - shift)[0], reinterpret_cast<const uint4 *>(from - shift)[1]};
             uint32_t both[8];
             memcpy(both, at, 32);
-            shift_bytes(both, shift, v);
+            shift_bytes<1>(both, shift, v);
         } else {
             alignas(16) signed char x[16];
 #pragma unroll

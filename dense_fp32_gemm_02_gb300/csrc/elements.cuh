@@ -85,4 +85,41 @@ __device__ __forceinline__ void store8(bf16 *p, const float (&v)[8]) {
                                                pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
+// The 4 N bytes from `shift` on of the 4 M in w, `shift` a multiple of GRAIN and at most 4 (M - N) - 1.
+template <int GRAIN, int M, int N>
+__device__ __forceinline__ void shift_bytes(uint32_t (&w)[M], int shift, uint32_t (&out)[N]) {
+    static_assert(M == N + 1 || M == N + 2 || M == N + 4, "up to 3, 7 or 15 bytes");
+    if (M == N + 4 && (shift & 8)) {
+#pragma unroll
+        for (int i = 0; i < N + 2; ++i) w[i] = w[i + 2];
+    }
+    if (M >= N + 2 && (shift & 4)) {
+#pragma unroll
+        for (int i = 0; i < (GRAIN == 4 ? N : N + 1); ++i) w[i] = w[i + 1];
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = GRAIN == 4 ? w[i] : __funnelshift_r(w[i], w[i + 1], (shift & 3) * 8);
+}
+
+// Eight consecutive elements at any address, of a matrix from `begin` to `end`: the aligned 16 bytes that hold them,
+// shifted into place (one by one they are eight accesses, of few bytes or 32 apart); false where those would leave the
+// matrix.
+template <class T>
+__device__ __forceinline__ bool load8_shifted(const T *p, const T *begin, const T *end, float (&v)[8]) {
+    constexpr int N = 2 * int(sizeof(T));
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p) & ~uintptr_t(15);
+    if (at < reinterpret_cast<uintptr_t>(begin) || at + 4 * N + 16 > reinterpret_cast<uintptr_t>(end)) return false;
+    uint32_t w[N + 4], x[N];
+#pragma unroll
+    for (int i = 0; i < N + 4; i += 4) {
+        const uint4 q = reinterpret_cast<const uint4 *>(at)[i / 4];
+        w[i] = q.x, w[i + 1] = q.y, w[i + 2] = q.z, w[i + 3] = q.w;
+    }
+    shift_bytes<int(sizeof(T))>(w, int(reinterpret_cast<uintptr_t>(p) & 15), x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = sizeof(T) == 4 ? __uint_as_float(x[i * N / 8]) : i & 1 ? bf16_hi(x[i / 2]) : bf16_lo(x[i / 2]);
+    return true;
+}
+
 }  // namespace sgl

@@ -128,7 +128,9 @@ __device__ __forceinline__ void take_slopes(const SlopesJob<T> &a) {
             load8(ph, dh);
             load8(pg, g);
             load8(pu, u);
-        } else {
+        } else if (c + 8 > a.N || !load8_shifted(ph, a.dH, a.dH + (a.M - 1) * a.ldh + a.N, dh) ||
+                   !load8_shifted(pg, a.G, a.G + (a.M - 1) * a.ldg + a.N, g) ||
+                   !load8_shifted(pu, a.U, a.U + (a.M - 1) * a.ldu + a.N, u)) {
 #pragma unroll
             for (int d = 0; d < 8; ++d) {
                 const bool in = c + d < a.N;

@@ -87,22 +87,6 @@ __global__ void __launch_bounds__(256) byte_expand_kernel(ByteJob job, int *larg
     if (over && (threadIdx.x & 31) == 0) atomicExch(large, 1);
 }
 
-// The 4 N bytes from `shift` < 4 N of the 8 N in w.
-template <int N>
-__device__ __forceinline__ void shift_bytes(uint32_t (&w)[2 * N], int shift, uint32_t (&out)[N]) {
-    static_assert(N == 1 || N == 2 || N == 4, "4, 8 or 16 bytes");
-    if (N == 4 && (shift & 8)) {
-#pragma unroll
-        for (int i = 0; i < 2 * N - 2; ++i) w[i] = w[i + 2];
-    }
-    if (N > 1 && (shift & 4)) {
-#pragma unroll
-        for (int i = 0; i < N + 1; ++i) w[i] = w[i + 1];
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) out[i] = __funnelshift_r(w[i], w[i + 1], (shift & 3) * 8);
-}
-
 // ------------------------------------------------------------------ sums of ranges
 // A thread to four columns of a row, the ranges' sums and the scales (no range, K = 0: the bias, or 0).
 template <class T>

@@ -15,6 +15,10 @@ struct Rows {
     long long ld;
     __device__ float at(long long i, long long j) const { return to_f32(p[i * ld + j]); }
     __device__ void at8(long long i, long long j, float (&v)[8]) const { load8(p + i * ld + j, v); }
+    // Of a rows x cols matrix at any pitch; false where it is not done.
+    __device__ bool shifted8(long long i, long long j, int rows, int cols, float (&v)[8]) const {
+        return load8_shifted(p + i * ld + j, p, p + (rows - 1) * ld + cols, v);
+    }
 };
 struct Act8Rows {
     const signed char *q, *e;
@@ -30,6 +34,7 @@ struct Act8Rows {
 #pragma unroll
         for (int d = 0; d < 8; ++d) v[d] *= step;
     }
+    __device__ bool shifted8(long long, long long, int, int, float (&)[8]) const { return false; }
 };
 
 // ------------------------------------------------------------------ parts
@@ -112,7 +117,7 @@ __device__ __forceinline__ void take_parts(const PartsJob<X> &job, long long t, 
         float v[8];
         if (job.wide && c + 8 <= job.cols) {
             job.x.at8(i, c, v);
-        } else {
+        } else if (c + 8 > job.cols || !job.x.shifted8(i, c, job.rows, job.cols, v)) {
 #pragma unroll
             for (int d = 0; d < 8; ++d) v[d] = c + d < job.cols ? job.x.at(i, c + d) : 0.0f;
         }
