@@ -1,5 +1,5 @@
 // gated.cu -- entry points of the gated block, forward and backward.
-#include "gated.cuh"
+#include "gated_tiles.cuh"
 #include "layer_host.h"
 #include "packed.cuh"
 #include "pair_gemm.h"
@@ -64,19 +64,19 @@ int pack(const Packed<T> &Wg, const Packed<T> &Wu, const Packed<T> &X, bool besi
 }
 
 // ------------------------------------------------------------------ forward
-template <class T>
-int forward_few_rows(const Call &c, bool stream_rows, int sms, cudaMemPool_t pool) {
-    const T *Wg = static_cast<const T *>(c.Wg), *Wu = static_cast<const T *>(c.Wu);
-    const bool w_wide = wide_rows(Wg, c.ldwg) && wide_rows(Wu, c.ldwu);
-    const Rows<T> X{static_cast<const T *>(c.X), c.ldx};
+// Up to 16 float32 rows: by FMAs to 8 (W through registers once), by warp-level MMAs to 16 (rows.cuh).
+int forward_few_rows(const Call &c, int sms, cudaMemPool_t pool) {
+    const float *Wg = static_cast<const float *>(c.Wg), *Wu = static_cast<const float *>(c.Wu);
+    const bool w_wide = wide_rows(Wg, c.ldwg) && wide_rows(Wu, c.ldwu), stream_rows = c.M <= STREAM_ROWS;
+    const Rows<float> X{static_cast<const float *>(c.X), c.ldx};
     RowsWork w{};
     w.M = c.M, w.N = c.N, w.K = c.K;
-    w.x_wide = sgh::aligned(c.X, 4 * sizeof(T)) && c.ldx % 4 == 0;
+    w.x_wide = sgh::aligned(c.X, 4 * sizeof(float)) && c.ldx % 4 == 0;
     if (stream_rows)
-        split_rows(w, 32 * 16 / int(sizeof(T)), RANK_THREADS / 32 * STREAM_DEPTH, STREAM_RANGE,
-                   (long long)sms * stream_blocks(c.M), sizeof(T), 2);
+        split_rows(w, 32 * 16 / int(sizeof(float)), RANK_THREADS / 32 * STREAM_DEPTH, STREAM_RANGE,
+                   (long long)sms * stream_blocks(c.M), sizeof(float), 2);
     else
-        split_rows(w, ROWS_COLS, SLAB, sgh::kMaxDim, 2LL * sms, sizeof(T), 2);
+        split_rows(w, ROWS_COLS, SLAB, sgh::kMaxDim, 2LL * sms, sizeof(float), 2);
     const long long blocks = 2LL * w.across * w.ranges, one = (long long)w.ranges * c.M * c.N;
     if (blocks > 0x7fffffffLL) return SGEMM_ERR_TOO_LARGE;
     sgh::Workspace ws(pool, c.stream);
@@ -86,25 +86,24 @@ int forward_few_rows(const Call &c, bool stream_rows, int sms, cudaMemPool_t poo
     if (stream_rows) {
         auto pick = [&](auto wide) {
             constexpr bool W = decltype(wide)::value;
-            return c.M <= 1   ? gated_stream_kernel<T, 1, W>
-                   : c.M <= 2 ? gated_stream_kernel<T, 2, W>
-                   : c.M <= 4 ? gated_stream_kernel<T, 4, W>
-                              : gated_stream_kernel<T, 8, W>;
+            return c.M <= 1   ? gated_stream_kernel<1, W>
+                   : c.M <= 2 ? gated_stream_kernel<2, W>
+                   : c.M <= 4 ? gated_stream_kernel<4, W>
+                              : gated_stream_kernel<8, W>;
         };
         auto kernel = w_wide ? pick(std::true_type{}) : pick(std::false_type{});
         st = sgh::launch(kFewRows, kernel, dim3(unsigned(blocks)), RANK_THREADS, 0, c.stream, w, X, Wg, (long long)c.ldwg, Wu,
                          (long long)c.ldwu);
-    } else if constexpr (sizeof(T) == 4) {
-        const auto kernel = gated_few_rows_kernel;
+    } else {
         const size_t smem = FewRows<1>::SMEM;
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        const cudaError_t e = cudaFuncSetAttribute(gated_few_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return sgh::cuda_fail(e);
-        st = sgh::launch(kFewRows, kernel, dim3(unsigned(blocks)), RANK_THREADS, smem, c.stream, w, X, Wg, (long long)c.ldwg, Wu,
-                         (long long)c.ldwu, w_wide);
+        st = sgh::launch(kFewRows, gated_few_rows_kernel, dim3(unsigned(blocks)), RANK_THREADS, smem, c.stream, w, X, Wg,
+                         (long long)c.ldwg, Wu, (long long)c.ldwu, w_wide);
     }
     if (st != SGEMM_OK) return st;
-    const PairOut<T> to{static_cast<T *>(c.G), static_cast<T *>(c.U), static_cast<T *>(c.H), c.ldg, c.ldu, c.ldh, c.act};
-    st = finish<T, true>(c.M, c.N, w.ranges, w.partial, w.partial + one, c.N, (long long)c.M * c.N, to, c.stream);
+    const PairOut<float> to{static_cast<float *>(c.G), static_cast<float *>(c.U), static_cast<float *>(c.H), c.ldg, c.ldu, c.ldh, c.act};
+    st = finish<float, true>(c.M, c.N, w.ranges, w.partial, w.partial + one, c.N, (long long)c.M * c.N, to, c.stream);
     return st == SGEMM_OK ? ws.release() : st;
 }
 
@@ -166,6 +165,58 @@ int forward_split(const Call &c, bool wide, int sms, cudaMemPool_t pool) {
 // 8192: 254 / 222).  Not aligned: 17 rows of 2048 x 2047 23.0 by warps / 22.5, 64 rows 37.6 / 25.3, 128 rows 43.3
 // laid out / 37.2, 256 rows of 1023 x 3001 36.4 / 65.
 constexpr int kWarpRows = 16, kSplitRows = 192, kSplitUnaligned = 128;
+// bfloat16 rows whose ranges' sums meet in clusters (gated_tiles.cuh), and not in memory after the pair product.  us, so /
+// by the pair product (below three rows: by FMAs): 1 row of 1024 x 1024 4.1 / 6.0, of 4096 x 8192 22.2 / 26.9; 8 rows 4.3 / 8.5
+// and 22.7 / 26.5; 64 rows 6.1 / 7.9 and 26.3 / 27.0.  W laid out first: 1 row of 1023 x 3001 11.4 / 12.8 by FMAs, 8 rows
+// 11.5 / 17.1, 64 rows 13.6 / 15.6.
+constexpr int kTileRows = 64;
+
+// Few bfloat16 rows in one launch (gated_tiles.cuh), after the layout of what the TMA does not read.
+int forward_tiles(const Call &c, int sms, cudaMemPool_t pool) {
+    GatedTileWork w{};
+    w.M = c.M, w.N = c.N, w.K = c.K;
+    w.across = (c.N + GATED_COLS - 1) / GATED_COLS;
+    w.rows = (c.M + 15) / 16 * 16;
+    w.timeout_ns = sgh::wait_timeout_ns();
+    const int steps = (c.K + GATED_STEP - 1) / GATED_STEP;
+    double least = 0;
+    for (int n = 1; n <= std::min(steps, GATED_CLUSTER); ++n) {   // us: a slab, filling and emptying a block, the cluster
+        const int per = (steps + n - 1) / n;
+        if ((steps + per - 1) / per != n || per * GATED_STEP > GATED_RANGE) continue;   // a range would be empty, or too long
+        const double cost = double(((long long)w.across * n + 2 * sms - 1) / (2 * sms)) * (per * 0.5 + 4.0) + 0.25 * n;
+        if (w.ranges == 0 || cost < least) least = cost, w.ranges = n, w.range = per * GATED_STEP;
+    }
+    Packed<bf16> X(c.M, c.K, c.X, c.ldx), Wg(c.K, c.N, c.Wg, c.ldwg), Wu(c.K, c.N, c.Wu, c.ldwu);
+    sgh::Workspace ws(pool, c.stream);
+    int st;
+    if (const size_t bytes = X.bytes() + Wg.bytes() + Wu.bytes()) {
+        if ((st = ws.allocate(bytes)) != SGEMM_OK) return st;
+        X.place(ws);
+        Wg.place(ws);
+        Wu.place(ws);
+        if ((st = pack(Wg, Wu, X, false, sms, c.stream)) != SGEMM_OK) return st;
+    }
+    CUtensorMap mX, mG, mU;
+    if ((st = sgp::encode(&mX, X.operand(), GATED_STEP, unsigned(w.rows))) != SGEMM_OK ||
+        (st = sgp::encode(&mG, Wg.operand(), GATED_STEP, GATED_STEP)) != SGEMM_OK ||
+        (st = sgp::encode(&mU, Wu.operand(), GATED_STEP, GATED_STEP)) != SGEMM_OK)
+        return st;
+    const PairOut<bf16> to{static_cast<bf16 *>(c.G), static_cast<bf16 *>(c.U), static_cast<bf16 *>(c.H), c.ldg, c.ldu, c.ldh, c.act};
+    const auto go = [&](auto rows) {
+        constexpr int ROWS = decltype(rows)::value;
+        const auto kernel = gated_tiles_kernel<ROWS>;
+        constexpr size_t smem = GatedTile<ROWS>::SMEM;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return sgh::cuda_fail(e);
+        const long long blocks = (long long)w.across * w.ranges;
+        return sgh::launch_cluster("gated, few rows, tcgen05, sums in clusters", kernel, dim3(unsigned(blocks)), GATED_THREADS, smem, w.ranges,
+                                   c.stream, mX, mG, mU, w, to);
+    };
+    st = w.rows <= 16   ? go(std::integral_constant<int, 16>{})
+         : w.rows <= 32 ? go(std::integral_constant<int, 32>{})
+                        : go(std::integral_constant<int, 64>{});
+    return st == SGEMM_OK ? ws.release() : st;
+}
 
 template <class T>
 int forward(const Call &c) {
@@ -175,18 +226,14 @@ int forward(const Call &c) {
     constexpr int PARTS = Packed<T>::PARTS;
     const PairOut<T> to{static_cast<T *>(c.G), static_cast<T *>(c.U), static_cast<T *>(c.H), c.ldg, c.ldu, c.ldh, c.act};
     if (c.K == 0) return finish<T, true>(c.M, c.N, 0, nullptr, nullptr, c.N, 0, to, c.stream);
-    Packed<T> X(c.M, c.K, c.X, c.ldx), Wg(c.K, c.N, c.Wg, c.ldwg), Wu(c.K, c.N, c.Wu, c.ldwu);
-    const bool in_place = Wg.direct && Wu.direct;
-    // Up to 8 rows by FMAs, W through registers once; bfloat16 that the TMA reads where it lies only up to 2.  us,
-    // by FMAs / by the tensor cores: 1 row of 1024 x 1024 6.0 / 8.4, of 4096 x 4096 15.9 / 18.1; 4 rows 7.8 / 8.8
-    // and 27.8 / 18.4; 8 rows 8.5 / 9.0 and 28.4 / 18.6.
-    if (c.M <= STREAM_ROWS && (PARTS == 3 || !in_place || c.M <= 2)) return forward_few_rows<T>(c, true, sms, pool);
     if constexpr (PARTS == 3) {
-        if (c.M <= kWarpRows) return forward_few_rows<T>(c, false, sms, pool);
+        if (c.M <= kWarpRows) return forward_few_rows(c, sms, pool);
         const bool wide = wide_rows(static_cast<const T *>(c.Wg), c.ldwg) && wide_rows(static_cast<const T *>(c.Wu), c.ldwu);
         if (c.M <= (wide ? kSplitRows : kSplitUnaligned)) return forward_split(c, wide, sms, pool);
+    } else {
+        if (c.M <= kTileRows && c.K <= GATED_CLUSTER * GATED_RANGE) return forward_tiles(c, sms, pool);
     }
-
+    Packed<T> X(c.M, c.K, c.X, c.ldx), Wg(c.K, c.N, c.Wg, c.ldwg), Wu(c.K, c.N, c.Wu, c.ldwu);
     const sgp::Split split = sgq::plan(sgq::GATE, c.M, c.N, c.K, PARTS == 3 ? 6 : 1, sms);
     sgh::Workspace ws(pool, c.stream);
     st = ws.allocate(X.bytes() + Wg.bytes() + Wu.bytes() + sgh::Workspace::piece(split.partial_floats * 4));

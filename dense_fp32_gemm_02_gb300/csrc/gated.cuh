@@ -9,18 +9,18 @@
 
 namespace sgl {
 
-// ------------------------------------------------------------------ few rows
+// ------------------------------------------------------------------ few rows of float32
 // Bound by reading both matrices once.  The products of rows.cuh, the blocks of Wg's and then of
 // Wu's in one launch; their sums over each range go to partial[range][row][column], U's behind G's.
-template <class T, int MR, bool WIDE>
+template <int MR, bool WIDE>
 __global__ void __launch_bounds__(RANK_THREADS, stream_blocks(MR))
-    gated_stream_kernel(RowsWork w, Rows<T> X, const T *Wg, long long ldg, const T *Wu, long long ldu) {
-    __shared__ __align__(16) float sm[StreamRows<T, MR>::FLOATS];
+    gated_stream_kernel(RowsWork w, Rows<float> X, const float *Wg, long long ldg, const float *Wu, long long ldu) {
+    __shared__ __align__(16) float sm[StreamRows<float, MR>::FLOATS];
     sg::wait_prerequisites();
     sg::launch_dependents();
     const int n = w.across * w.ranges, second = int(blockIdx.x) >= n;
     if (!SG_IN_RANGE(int(blockIdx.x) < 2 * n)) return;
-    stream_rows<T, MR, WIDE>(w, int(blockIdx.x) - second * n, X, second ? Wu : Wg, second ? ldu : ldg,
+    stream_rows<float, MR, WIDE>(w, int(blockIdx.x) - second * n, X, second ? Wu : Wg, second ? ldu : ldg,
                              w.partial + second * (long long)w.ranges * w.M * w.N, sm);
 }
 

@@ -7,7 +7,7 @@ import pytest
 
 import test_layers_checks_host as layers
 
-FILES = ["norm.cuh", "gated.cuh", "linear8.cuh", "byte_tiles.cuh", "byte_rows.cuh", "split_tiles.cuh", "pair_gemm.cuh"]
+FILES = ["norm.cuh", "gated.cuh", "linear8.cuh", "byte_tiles.cuh", "byte_rows.cuh", "split_tiles.cuh", "gated_tiles.cuh", "pair_gemm.cuh"]
 
 
 def functions():
@@ -39,7 +39,8 @@ def checks(name, seen=()):
 def test_the_kernels_are_found():
     assert {"norm_kernel", "norm_backward_kernel", "norm_weight_kernel", "gated_stream_kernel", "gated_few_rows_kernel",
             "pair_finish_kernel", "gated_slopes_kernel", "byte_finish_kernel", "byte_expand_kernel", "byte_tiles_kernel", "byte_pitch_kernel",
-            "pair_gemm_kernel", "byte_rows_kernel", "gated_parts_kernel", "split_tiles_kernel"} == set(KERNELS)
+            "pair_gemm_kernel", "byte_rows_kernel", "gated_parts_kernel", "split_tiles_kernel",
+            "gated_tiles_kernel"} == set(KERNELS)
 
 
 @pytest.mark.parametrize("kernel", KERNELS)

@@ -77,6 +77,29 @@ def test_forward_between_few_and_many_rows(M, N, K, pad):
     assert b.device_status() == 0
 
 
+@pytest.mark.parametrize("pad", [0, 8, 3])
+@pytest.mark.parametrize("M,N,K", [(1, 8, 1), (1, 128, 8200), (2, 136, 63), (7, 64, 65), (15, 200, 513), (16, 65, 1000), (17, 1031, 64),
+                                   (32, 256, 2048), (33, 8, 300), (48, 129, 129), (63, 264, 70), (64, 1000, 520), (3, 72, 65536),
+                                   (3, 72, 65537), (64, 40, 8193)])
+def test_forward_of_few_bfloat16_rows(M, N, K, pad):
+    """Tiles, ranges and rows that end inside one another, the projections kept or not; what lies around the outputs is
+    left alone."""
+    b = binding()
+    X, (Wg, Wu) = normal(M, K, torch.bfloat16, 75), weights(K, N, torch.bfloat16, 76)
+    pg, pu = device_matrix(Wg.cpu(), pad, pad), device_matrix(Wu.cpu(), 0, 0)
+    flat = [torch.full((M + 2, N + 2), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    H, G, U = (f[1:1 + M, 1:1 + N] for f in flat)
+    b.gated_into(device_matrix(X.cpu(), pad, 0), pg, pu, H, G=G, U=U, act="gelu")
+    check_forward(X, Wg, Wu, "gelu", H, G, U)
+    for f in flat:
+        f[1:1 + M, 1:1 + N] = 5
+    assert all(bool((f == 5).all()) for f in flat)
+    alone = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    b.gated_into(X, pg, pu, alone, act="silu")
+    check_forward(X, Wg, Wu, "silu", alone)
+    assert b.device_status() == 0
+
+
 @pytest.mark.parametrize("pad", [0, 3])
 def test_values_of_every_size_between_few_and_many_rows(pad):
     """Float32 that needs all of its three parts, from 2^-100 to 2^60, each against the sum's own magnitudes; infinities reach
