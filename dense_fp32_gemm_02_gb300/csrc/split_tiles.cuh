@@ -9,9 +9,10 @@
 // small pairs to one of their own.
 //
 // 608 threads.  Warp 16 copies slabs of 64 k of W by TMA, two ahead (W whose rows are not 16-byte aligned: each
-// team its own, four bytes at a time); warp 18 the same of X's parts, straight to where the MMA wants them.  Warps 0 to 15 split W, in two teams, a slab and a stage to each, a thread eight columns
-// at a time, and store them with the columns next to each other (128-byte swizzle).  Warp 17 issues the MMAs.  At
-// the end warps 0 to 15 take the sums out, a lane to a column of W.
+// team its own, four bytes at a time); warp 18 the same of X's parts, straight to where the MMA wants them.
+// Warps 0 to 15 split W, in two teams, a slab and a stage to each, a thread eight columns at a time, and store them
+// with the columns next to each other (128-byte swizzle).  Warp 17 issues the MMAs.  At the end warps 0 to 15 take
+// the sums out, a lane to a column of W.
 //
 // us, whole call: 64 rows of 4096 x 4096 41.7 (3.2 TB/s; by warp-level MMAs that split what they read 95.9, by
 // parts laid out first 114), 16 rows 40.7, 128 rows 70.7 (116); 64 rows of 4096 x 8192 72.6 (182), of
