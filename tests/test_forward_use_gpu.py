@@ -352,3 +352,49 @@ def test_rows_past_2_31_elements():
     few = b.linear8_into((q[-300:], s[-300:]), W8, ws, torch.empty(300, N, dtype=torch.bfloat16, device="cuda"))
     assert torch.equal(H[-300:], few)
     assert b.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("M", [1, 4, 33, 64, 65, 150, 300])
+def test_calls_close_behind_one_another(M, dtype):
+    """Each call reads what the one before it writes, and writes what an earlier one still reads: the same bits as with the
+    device waited for after every call, in a stream and in a graph, where kernels start before the last one's end."""
+    b, D, F = binding(), 520, 1000
+    layers = [dict(w=(1 + 0.1 * rnd(D, seed=20 + i)).to(dtype), Wg=rnd(D, F, dtype=dtype, seed=30 + i) * 0.05,
+                   Wu=rnd(D, F, dtype=dtype, seed=40 + i) * 0.05, Wd=bytes_of(F, D, 50 + i), Wq=bytes_of(D, D, 60 + i),
+                   s=torch.rand(D, device="cuda") * 1e-3) for i in range(3)]
+    X = rnd(M, D, dtype=dtype, seed=70)
+
+    def e(*shape, t=dtype):
+        return torch.empty(*shape, dtype=t, device="cuda")
+    S, Y, A, O, dX, dV, H, G, U = (*(e(M, D) for _ in range(6)), *(e(M, F) for _ in range(3)))
+    q, scale, dw, dWg, dWu = e(M, D, t=torch.int8), e(M, t=torch.float32), e(D), e(D, F), e(D, F)
+
+    def chain(wait):
+        S.copy_(X)
+        O.zero_()
+        for p in layers:
+            for step in (lambda: b.rmsnorm_into(S, p["w"], q=q, scale=scale, R=O, S=S),
+                         lambda: b.linear8_into((q, scale), p["Wq"], p["s"], A),
+                         lambda: b.rmsnorm_into(A, p["w"], Y=Y, R=S, S=S),
+                         lambda: b.gated_into(Y, p["Wg"], p["Wu"], H, G=G, U=U),
+                         lambda: b.linear8_into(H, p["Wd"], p["s"], O),
+                         lambda: b.gated_backward_into(H, Y, p["Wg"], p["Wu"], G, U, dX=dX, dWg=dWg, dWu=dWu),
+                         lambda: b.rmsnorm_backward_into(dX, S, p["w"], dV, dw=dw, dS=O),
+                         lambda: b.gated_into(dV, p["Wg"], p["Wu"], H)):
+                step()
+                if wait:
+                    torch.cuda.synchronize()
+        return [t.clone() for t in (S, O, H, dV, dw, dWg, dWu, A)]
+    ref = chain(True)
+    assert all(bool(torch.isfinite(t).all()) for t in ref)
+    for _ in range(6):
+        assert all(torch.equal(x, y) for x, y in zip(chain(False), ref))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(False)
+    for _ in range(4):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, ref))
+    assert b.device_status() == 0
