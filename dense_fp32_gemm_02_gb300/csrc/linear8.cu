@@ -133,8 +133,11 @@ int stream(const Call &c, int sms) {
     }
     const auto kernel = aligned_rows(c.W, c.ldw, ROWS == 4 ? 4 : 8) ? byte_rows_kernel<T, ROWS, TILE, true> : byte_rows_kernel<T, ROWS, TILE, false>;
     const size_t smem = byte_rows_smem<ROWS, TILE>(a.range);
-    if (smem > 40960) {   // (with what the kernel declares itself, over the 48 KB that need no leave)
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    // Over the 48 KB that need no leave, with what the kernel declares itself.  The leave is for the most that any call
+    // takes: threads share it, and a call's own size would take another thread's launch its leave away.
+    if (smem > 40960) {
+        constexpr size_t most = byte_rows_smem<ROWS, TILE>(ROWS_RANGE);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most));
         if (e != cudaSuccess) return sgh::cuda_fail(e);
     }
     return sgh::launch_cluster("int8, W streamed to few rows", kernel, dim3(unsigned(across * a.ranges)), ROWS_THREADS, smem, a.ranges,
