@@ -35,19 +35,18 @@ bool wide_rows(const T *p, long long ld) {
     return !p || (aligned(p, 16) && ld % (16 / (long long)sizeof(T)) == 0);
 }
 
-// Counts a launch just made and returns its error.
-inline int launched(const char *main_kernel = nullptr) {
+// Counts a launch that returned `e`, where it was made, and returns its status.
+inline int launched(cudaError_t e, const char *main_kernel) {
+    if (e != cudaSuccess) return cuda_fail(e);
     count_launch(main_kernel);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? SGEMM_OK : cuda_fail(e);
+    return SGEMM_OK;
 }
 
 // An early launch (host_state.h), counted.
 template <class... P, class... Args>
 int launch(const char *text, void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
            const Args &...args) {
-    const cudaError_t e = launch_early(kernel, grid, threads, smem, stream, args...);
-    return e == cudaSuccess ? launched(text) : cuda_fail(e);
+    return launched(launch_early(kernel, grid, threads, smem, stream, args...), text);
 }
 
 // The same in clusters of `cluster` blocks.
@@ -66,8 +65,7 @@ int launch_cluster(const char *text, void (*kernel)(P...), dim3 grid, unsigned t
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-    return e == cudaSuccess ? launched(text) : cuda_fail(e);
+    return launched(cudaLaunchKernelEx(&cfg, kernel, P(args)...), text);
 }
 
 // Rows in 8 bits, each with a scale (norm.cu): q and scale of the rows of X.

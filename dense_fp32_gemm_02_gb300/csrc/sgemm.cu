@@ -265,6 +265,7 @@ struct ProfCall {
 // ------------------------------------------------------------------ helpers
 int cuda_fail(cudaError_t e) {
     t_last_cuda_error = int(e);
+    cudaGetLastError();   // (the runtime keeps it until it is read, and the next launch would be taken for a failed one)
     return (e == cudaErrorMemoryAllocation) ? SGEMM_ERR_ALLOC : SGEMM_ERR_CUDA;
 }
 

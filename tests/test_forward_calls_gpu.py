@@ -72,3 +72,53 @@ def test_streamed_products_of_several_lengths_at_once(tmp_path):
     assert [c.refused for c in calls] == [0] * len(shapes)
     assert all(torch.equal(Y, want) for Y, want, _ in work)
     assert b.device_status() == 0
+
+
+# ------------------------------------------------------------------ after a refused call
+def refuse(call):
+    """Makes `call(stream)` in a capture that has been invalidated, where CUDA refuses its launch."""
+    driver = ctypes.CDLL("libcuda.so.1")
+    stream = torch.cuda.Stream()
+    handle, graph = ctypes.c_void_p(stream.cuda_stream), ctypes.c_void_p()
+    assert driver.cuStreamBeginCapture_v2(handle, 1) == 0      # (thread-local mode)
+    try:
+        assert driver.cuStreamSynchronize(handle) != 0         # not permitted in a capture: invalidates it
+        call(stream)
+    finally:
+        driver.cuStreamEndCapture(handle, ctypes.byref(graph))
+
+
+def normal(rows, cols, seed, scale=1.0):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return torch.randn(rows, cols, generator=g) * scale
+
+
+def test_a_call_after_one_that_was_refused():
+    """A launch that CUDA refuses fails its own call alone: the next one, of one kernel or of several, does its work."""
+    b = binding()
+    X, w = normal(40, 512, 1).cuda(), torch.ones(512, device="cuda")
+    Wg, Wu = normal(512, 300, 2, 0.05).cuda(), normal(512, 300, 3, 0.05).cuda()
+    e = torch.empty
+    q8, e8 = e(40, 512, dtype=torch.int8, device="cuda"), e(40, 16, dtype=torch.int8, device="cuda")
+    q, s, W8 = e(40, 512, dtype=torch.int8, device="cuda"), e(40, device="cuda"), torch.ones(512, 300, dtype=torch.int8, device="cuda")
+    rows8, ones = b.rmsnorm_into(X, w, q=q, scale=s)[2:], torch.ones(300, device="cuda")
+    calls = {
+        "norm": ([e(40, 512, device="cuda")], lambda out, stream: b.rmsnorm_into(X, w, Y=out[0], stream=stream)),
+        "gated": ([e(40, 300, device="cuda")], lambda out, stream: b.gated_into(X, Wg, Wu, out[0], stream=stream)),
+        "linear8": ([e(40, 300, device="cuda")], lambda out, stream: b.linear8_into(rows8, W8, ones, out[0], stream=stream)),
+        "sgemm": ([e(40, 300, device="cuda")], lambda out, stream: b.sgemm_into(X, Wg, out[0], stream=stream)),
+        "act8": ([q8, e8], lambda out, stream: b.act8_store_into(X, out[0], out[1], stream=stream)),
+    }
+    for name, (out, call) in calls.items():
+        call(out, None)
+        want = [t.clone() for t in out]
+        for refused in calls:
+            with pytest.raises(b.SgemmError):
+                refuse(lambda stream: calls[refused][1](calls[refused][0], stream))
+            for t in out:
+                t.fill_(55)
+            call(out, None)               # raises nothing
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(out, want)), (name, refused)
+    assert b.device_status() == 0
