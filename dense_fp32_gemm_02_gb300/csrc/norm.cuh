@@ -208,6 +208,16 @@ __device__ __noinline__ float rare_rstd(GroupSums &sm, V v, int K, float eps, in
     return float(1.0 / sqrt(group_sum<THREADS>(sm, ss) / K + eps));
 }
 
+// tie_exact (rows8.cuh) of a product p of float32 values, of 48 bits as `top` is, in 64: (n + 1/2) top has 56, so the
+// comparison takes what its rounding leaves into account.  Near a tie 127 |p| - t is under 2^-13 top and a whole number
+// of the smaller of the two products' last places, which then is under 2^44 of them: both differences are exact.
+static __device__ __noinline__ float tie_wide(double p, double quotient, double top) {
+    const double n = floor(fabs(quotient)), h = n + 0.5, t = h * top;
+    const double d = fma(127.0, fabs(p), -t) - fma(h, top, -t);
+    const bool odd = (int(n) & 1) != 0;
+    return float(copysign(d > 0 || (d == 0 && odd) ? n + 1.0 : n, quotient));
+}
+
 // A row's q and the largest |p| in 64 bits, where products leave fp32's range.
 template <class T, int THREADS, bool WEIGHED, class V>
 __device__ __noinline__ double rare_rows8(GroupSums &sm, V v, const T *w, signed char *q, int K, int t) {
@@ -224,19 +234,11 @@ __device__ __noinline__ double rare_rows8(GroupSums &sm, V v, const T *w, signed
     if (any) top = group_max<THREADS>(sm, top);
     const bool keep = any && top > 0 && top <= 1.7e308;   // not zeros, an infinity or a NaN
     for (int j = t; j < K; j += THREADS) {
-        const double p = keep ? double(v(j)) * (WEIGHED ? to_f32(w[j]) : 1.0f) : 0.0;
-        q[j] = static_cast<signed char>(keep ? __double2int_rn(127.0 * p / top) : 0);
+        const double p = keep ? double(v(j)) * (WEIGHED ? to_f32(w[j]) : 1.0f) : 0.0, quotient = keep ? 127.0 * p / top : 0.0;
+        const double near = rint(quotient);   // (a quotient of 64 bits is within 2^-45)
+        q[j] = static_cast<signed char>(fabs(quotient - near) > 0.5 - 0x1p-40 ? tie_wide(p, quotient, top) : near);
     }
     return top;
-}
-
-// tie_exact (rows8.cuh) of a product of float32 values, in 64 bits.
-static __device__ __noinline__ float tie_wide(float v, float w, float quotient, float top_hi, float top_lo) {
-    const double p = fabs(double(v) * w), top = double(top_hi) + top_lo;
-    const float n = floorf(fabsf(quotient));
-    const double d = fma(127.0, p, -(n + 0.5) * top);
-    const bool odd = (int(n) & 1) != 0;
-    return copysignf(d > 0 || (d == 0 && odd) ? n + 1.0f : n, quotient);
 }
 
 // ------------------------------------------------------------------ forward
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(norm_block(THREADS))
                     for (int e = 0; e < 8; ++e) {
                         const float p = KIND == ROWS8 ? v[c][e] : v[c][e] * w[e], quotient = p * times;
                         if (fabsf(quotient - out[e]) > 0.5f - NEAR)
-                            out[e] = WITH_LO ? tie_wide(v[c][e], w[e], quotient, top.value(), top.lo)
+                            out[e] = WITH_LO ? tie_wide(double(v[c][e]) * w[e], quotient, double(top.value()) + top.lo)
                                              : tie_exact(p, quotient, top.value());
                     }
                 }
