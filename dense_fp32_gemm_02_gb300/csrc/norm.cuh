@@ -198,29 +198,25 @@ __device__ __forceinline__ double group_max(GroupSums &sm, double v) {   // of m
     return all;
 }
 
-// ------------------------------------------------------------------ rows out of fp32's range
-// 1 / sqrt(mean(v^2) + eps) in 64 bits, where squares leave fp32's range.  An infinity in v
-// gives 0, a NaN a NaN.
-template <int THREADS, class V>
-__device__ __noinline__ float rare_rstd(GroupSums &sm, V v, int K, float eps, int t) {
-    double ss = 0;
-    for (int j = t; j < K; j += THREADS) ss += double(v(j)) * v(j);
-    return float(1.0 / sqrt(group_sum<THREADS>(sm, ss) / K + eps));
-}
+enum NormKind { NORM, NORM8, ROWS8 };   // y alone; q and, where Y is given, y; q of x itself
 
+// ------------------------------------------------------------------ rows out of fp32's range
 // tie_exact (rows8.cuh) of a product p of float32 values, of 48 bits as `top` is, in 64: (n + 1/2) top has 56, so the
 // comparison takes what its rounding leaves into account.  Near a tie 127 |p| - t is under 2^-13 top and a whole number
 // of the smaller of the two products' last places, which then is under 2^44 of them: both differences are exact.
-static __device__ __noinline__ float tie_wide(double p, double quotient, double top) {
+__device__ __forceinline__ double tie_of(double p, double quotient, double top) {
     const double n = floor(fabs(quotient)), h = n + 0.5, t = h * top;
     const double d = fma(127.0, fabs(p), -t) - fma(h, top, -t);
     const bool odd = (int(n) & 1) != 0;
-    return float(copysign(d > 0 || (d == 0 && odd) ? n + 1.0 : n, quotient));
+    return copysign(d > 0 || (d == 0 && odd) ? n + 1.0 : n, quotient);
+}
+static __device__ __noinline__ float tie_wide(float v, float w, float quotient, float top_hi, float top_lo) {
+    return float(tie_of(double(v) * w, quotient, double(top_hi) + top_lo));
 }
 
 // A row's q and the largest |p| in 64 bits, where products leave fp32's range.
 template <class T, int THREADS, bool WEIGHED, class V>
-__device__ __noinline__ double rare_rows8(GroupSums &sm, V v, const T *w, signed char *q, int K, int t) {
+__device__ __forceinline__ double rare_rows8(GroupSums &sm, V v, const T *w, signed char *q, int K, int t) {
     double top = 0;
     bool any = false;   // rows of zeros, padding, need no more than this pass
     for (int j = t; j < K; j += THREADS) {
@@ -232,18 +228,49 @@ __device__ __noinline__ double rare_rows8(GroupSums &sm, V v, const T *w, signed
     }
     any = THREADS == 32 ? __any_sync(0xffffffffu, any) : __syncthreads_or(any);
     if (any) top = group_max<THREADS>(sm, top);
-    const bool keep = any && top > 0 && top <= 1.7e308;   // not zeros, an infinity or a NaN
+    if (!any || !(top > 0 && top <= 1.7e308)) {   // zeros, an infinity or a NaN
+        for (int j = t; j < K; j += THREADS) q[j] = 0;
+        return top;
+    }
     for (int j = t; j < K; j += THREADS) {
-        const double p = keep ? double(v(j)) * (WEIGHED ? to_f32(w[j]) : 1.0f) : 0.0, quotient = keep ? 127.0 * p / top : 0.0;
-        const double near = rint(quotient);   // (a quotient of 64 bits is within 2^-45)
-        q[j] = static_cast<signed char>(fabs(quotient - near) > 0.5 - 0x1p-40 ? tie_wide(p, quotient, top) : near);
+        const double p = double(v(j)) * (WEIGHED ? to_f32(w[j]) : 1.0f), quotient = 127.0 * p / top;
+        const float near = whole(float(quotient));
+        q[j] = static_cast<signed char>(fabsf(float(quotient) - near) > 0.5f - NEAR ? tie_of(p, quotient, top) : near);
     }
     return top;
 }
 
-// ------------------------------------------------------------------ forward
-enum NormKind { NORM, NORM8, ROWS8 };   // y alone; q and, where Y is given, y; q of x itself
+// 1 / sqrt(mean(v^2) + eps) where the squares leave fp32's range, and rstd with them: it is up to 2^165 where v is
+// subnormal and eps is 0.  As r * s, s a power of two, r a normal number: v s r is rounded once, as v rstd is in other
+// rows.  An infinity in v makes it 0, a NaN a NaN.
+struct RareRstd {
+    float r, s;
+};
+template <int THREADS, class V>
+__device__ __forceinline__ RareRstd rare_rstd(GroupSums &sm, V v, int K, float eps, int t) {
+    double ss = 0;
+    for (int j = t; j < K; j += THREADS) ss += double(v(j)) * v(j);
+    const double rstd = 1.0 / sqrt(group_sum<THREADS>(sm, ss) / K + eps);
+    const float s = rstd > 0x1p64 ? 0x1p64f : rstd < 0x1p-64 ? 0x1p-64f : 1.0f;
+    return {float(rstd / s), s};
+}
 
+// A row whose squares (`far`) or products leave fp32's range, all that is left of it.  (Nothing of the row is needed after
+// this call, so that the registers that it takes cost other rows none.)
+template <class T, int KIND, int THREADS, class V>
+__device__ __noinline__ void rare_row(GroupSums &sm, V v, const T *w, T *y, signed char *q, float *scale, int K, float eps, int t,
+                                      bool far, float rstd) {
+    RareRstd at{rstd, 1.0f};
+    if (KIND != ROWS8 && far) at = rare_rstd<THREADS>(sm, v, K, eps, t);
+    if (KIND != NORM) {
+        const double top = rare_rows8<T, THREADS, KIND != ROWS8>(sm, v, w, q, K, t);
+        if (t == 0) *scale = top <= 1.7e308 ? float(top * at.s * at.r / 127.0) : __uint_as_float(0x7fc00000u);
+    }
+    if (KIND != ROWS8 && y)   // (y may be X: an element's own reads are done)
+        for (int j = t; j < K; j += THREADS) y[j] = from_f32<T>(v(j) * at.s * at.r * to_f32(w[j]));
+}
+
+// ------------------------------------------------------------------ forward
 template <class T>
 struct NormCall {
     int M, K;
@@ -320,26 +347,19 @@ __global__ void __launch_bounds__(norm_block(THREADS))
         if (KIND == ROWS8) return to_f32(x[j]);
         return s ? to_f32(s[j]) : r ? to_f32(from_f32<T>(to_f32(x[j]) + to_f32(r[j]))) : to_f32(x[j]);
     };
-    float rstd = 1.0f;
+    float rstd = 1.0f, times = 0.0f;   // times: 127 / max|p|
+    bool far = false;
     if (KIND != ROWS8) {
         rstd = 1.0f / sqrtf(squares / float(a.K) + a.eps);
-        if (!(squares <= MOST_SQUARES) || (squares < LEAST_SQUARES && a.eps < 1e-10f)) {
-            rstd = rare_rstd<THREADS>(sm, held, a.K, a.eps, t);
-            group_sync<THREADS>();   // Y, written below, may be X
-        }
+        far = !(squares <= MOST_SQUARES) || (squares < LEAST_SQUARES && a.eps < 1e-10f);
     }
-    float times = 0.0f;    // 127 / max|p|; 0: q is there already
+    if (far || (EIGHT && !(top.value() >= LEAST_TOP && top.value() <= MOST_TOP))) {
+        rare_row<T, KIND, THREADS>(sm, held, a.w, y, q, EIGHT ? a.scale + row : nullptr, a.K, a.eps, t, far, rstd);
+        return;
+    }
     if (EIGHT) {
-        float scale;
-        if (top.value() >= LEAST_TOP && top.value() <= MOST_TOP) {
-            times = 127.0f / top.value();
-            scale = (KIND == ROWS8 ? top.value() : top.value() * rstd) / 127.0f;
-        } else {
-            const double all = rare_rows8<T, THREADS, KIND != ROWS8>(sm, held, a.w, q, a.K, t);
-            scale = all <= 1.7e308 ? float(all * rstd / 127.0) : __uint_as_float(0x7fc00000u);
-            group_sync<THREADS>();   // Y, written below, may be X
-        }
-        if (t == 0) a.scale[row] = scale;
+        times = 127.0f / top.value();
+        if (t == 0) a.scale[row] = (KIND == ROWS8 ? top.value() : top.value() * rstd) / 127.0f;
     }
 
     for (int base = 0; base < (LONG ? a.K : 1); base += SPAN) {
@@ -349,7 +369,7 @@ __global__ void __launch_bounds__(norm_block(THREADS))
         for (int c = 0; c < CHUNKS; ++c) {
             float out[8];
             if (KIND != ROWS8) at.load(a.w, c, w);
-            if (EIGHT && times != 0.0f) {
+            if (EIGHT) {
                 float off = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -362,7 +382,7 @@ __global__ void __launch_bounds__(norm_block(THREADS))
                     for (int e = 0; e < 8; ++e) {
                         const float p = KIND == ROWS8 ? v[c][e] : v[c][e] * w[e], quotient = p * times;
                         if (fabsf(quotient - out[e]) > 0.5f - NEAR)
-                            out[e] = WITH_LO ? tie_wide(double(v[c][e]) * w[e], quotient, double(top.value()) + top.lo)
+                            out[e] = WITH_LO ? tie_wide(v[c][e], w[e], quotient, top.value(), top.lo)
                                              : tie_exact(p, quotient, top.value());
                     }
                 }
@@ -390,6 +410,12 @@ struct NormBackCall {
     long long lddy, ldv, ldds, lddx;
     float eps;
 };
+
+// The same of the backward pass, where the row's work goes on.
+template <class T, int THREADS>
+__device__ __noinline__ RareRstd rare_row_rstd(GroupSums &sm, const T *v, int K, float eps, int t) {
+    return rare_rstd<THREADS>(sm, [&](int j) { return to_f32(v[j]); }, K, eps, t);
+}
 
 // The rows to come stand in a ring of asynchronous copies, each thread's own elements in its own
 // slots, so that they need no barrier; bfloat16 rows that are not 16-byte aligned, and rows that
@@ -489,6 +515,12 @@ __global__ void __launch_bounds__(norm_block(THREADS), norm_blocks_per_sm<THREAD
                     at.load(vr, c, v[c]), at.load(dyr, c, dy[c]);
             }
         };
+        auto scale_v = [&](float by) {
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[c][e] *= by;
+        };
         float squares = 0.0f, gv = 0.0f;
         Top none{};
         for (int base = 0; base < (LONG ? a.K : 1); base += SPAN) {
@@ -506,17 +538,22 @@ __global__ void __launch_bounds__(norm_block(THREADS), norm_blocks_per_sm<THREAD
         }
         group_reduce<THREADS, true, false, false>(sm, turn, squares, gv, none);
         turn ^= 1;
-        float rstd = 1.0f / sqrtf(squares / float(a.K) + a.eps), mean = gv * rstd / float(a.K);
+        float rstd = 1.0f / sqrtf(squares / float(a.K) + a.eps), mean = gv * rstd / float(a.K), shift = 1.0f;
         if (!(squares <= MOST_SQUARES) || (squares < LEAST_SQUARES && a.eps < 1e-10f)) {
             double sum = 0;
             for (int j = t; j < a.K; j += THREADS) sum += double(to_f32(dyr[j])) * to_f32(a.w[j]) * to_f32(vr[j]);
-            rstd = rare_rstd<THREADS>(sm, [&](int j) { return to_f32(vr[j]); }, a.K, a.eps, t);
-            mean = float(group_sum<THREADS>(sm, sum) * rstd / a.K);
+            const RareRstd of = rare_row_rstd<T, THREADS>(sm, vr, a.K, a.eps, t);
+            rstd = of.r, shift = of.s;
+            mean = float(group_sum<THREADS>(sm, sum) * shift * rstd / a.K);
             group_sync<THREADS>();   // dX, written below, may be dY
+            if (!LONG) scale_v(shift);
         }
         for (int base = 0; base < (LONG ? a.K : 1); base += SPAN) {
             const Place<T, THREADS, WIDE> at{a.K, base, t};
-            if (LONG) read(at);
+            if (LONG) {
+                read(at);
+                if (shift != 1.0f) scale_v(shift);
+            }
             float ds[CHUNKS][8];
 #pragma unroll
             for (int c = 0; c < CHUNKS; ++c) {
@@ -534,8 +571,8 @@ __global__ void __launch_bounds__(norm_block(THREADS), norm_blocks_per_sm<THREAD
                 const float(&u)[8] = weight(at, c);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float n = v[c][e] * rstd;
-                    ds[c][e] = fmaf(rstd, fmaf(-mean, n, dy[c][e] * u[e]), ds[c][e]);
+                    const float n = v[c][e] * rstd;   // (shift: 1 but for rows out of range, whose v holds it too)
+                    ds[c][e] = fmaf(rstd, fmaf(-mean, n, dy[c][e] * u[e]) * shift, ds[c][e]);
                     if (!LONG) {
                         dw[c][e] = fmaf(dy[c][e], n, dw[c][e]);
                     } else if (partial && at.column(c, e) < a.K) {   // (this thread's own column)

@@ -1,8 +1,12 @@
-"""The norm and its 8-bit rows where their arithmetic is at its limits: products a hair beside a tie."""
+"""The norm, its 8-bit rows and its backward pass where their arithmetic is at its limits: products a hair beside a
+tie, rows at the ends of float32's range."""
 import pytest
 import torch
 
+from _forward import norm_backward_reference, norm_reference, norm_slack, rounded, rows8_reference
+
 pytestmark = pytest.mark.gpu
+TYPES = [torch.float32, torch.bfloat16]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -13,6 +17,12 @@ def _gpu(cuda_device):
 def binding():
     from dense_fp32_gemm_02_gb300 import binding
     return binding
+
+
+def normal(rows, cols, seed, scale=1.0):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return torch.randn(rows, cols, generator=g) * scale
 
 
 # ------------------------------------------------------------------ ties
@@ -54,3 +64,57 @@ def test_products_beside_a_tie(v_scale, w_scale, K):
         n = nearest(c * d, a * x)
         want += [127, -n, -127, n]
     assert got == want
+
+
+# ------------------------------------------------------------------ the ends of float32's range
+ENDS = [1e-44, 1e-41, 1e-39, 3e-38, 1e37, 8e37]
+
+
+def rows_at_the_ends(K, dtype):
+    """A row for each of ENDS; values of order 1 (none above 4) times it, as the type holds them."""
+    x = normal(len(ENDS), K, 5).clamp(-4, 4)
+    x[:, 0] = 2.0
+    return (x.double() * torch.tensor(ENDS).double().unsqueeze(1)).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("K", [40, 257, 1000, 2048, 5000, 16384, 16390, 40000])
+def test_rows_at_the_ends_of_the_range(K, dtype):
+    """eps = 0: y is of order 1 whatever the row's size, down to the smallest values that the types hold."""
+    b = binding()
+    X, w = rows_at_the_ends(K, dtype), (1.0 + 0.3 * normal(1, K, 6)[0]).to(dtype)
+    M = len(ENDS)
+    Y, q, scale = torch.empty(M, K, dtype=dtype, device="cuda"), torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    S = torch.empty_like(Y)
+    b.rmsnorm_into(X.cuda(), w.cuda(), Y=Y, q=q, scale=scale, S=S, eps=0.0)
+    y = norm_reference(X, w, 0.0)
+    assert torch.equal(S.cpu(), X)
+    some = (X != 0).any(1)            # (1e-44 is 0 in bfloat16, whose norm is 0 / 0)
+    rounded(Y[some.cuda()], y[some], norm_slack(X, y)[some], "Y")
+    assert torch.equal(q.cpu()[some], rows8_reference(X.double() * w.double())[0][some])
+    ref = y.abs().amax(1) / 127.0
+    rounded(scale[some.cuda()], ref[some], norm_slack(X, ref)[some] + 3 * 2.0 ** -24 * ref[some], "scale")
+    x = X.cuda()                      # in the input's place, and without the 8 bits
+    b.rmsnorm_into(x, w.cuda(), Y=x, q=q, scale=scale, eps=0.0)
+    assert torch.equal(x[some.cuda()], Y[some.cuda()])
+    x = X.cuda()
+    b.rmsnorm_into(x, w.cuda(), Y=x, eps=0.0)
+    assert torch.equal(x[some.cuda()], Y[some.cuda()])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("K", [40, 257, 1000, 2048, 5000, 16384, 16390, 40000])
+def test_gradients_at_the_ends_of_the_range(K, dtype):
+    """The same of the backward pass, dX in dY's or V's place too."""
+    b = binding()
+    V, w = rows_at_the_ends(K, dtype), (1.0 + 0.3 * normal(1, K, 6)[0]).to(dtype)
+    V = V[(V != 0).any(1)]
+    sizes = V.double().square().mean(1).sqrt()
+    dY = (normal(len(V), K, 7).double() * sizes.clamp(1e-30, 1e30).unsqueeze(1)).to(dtype)   # (dX stays in range)
+    ref, ref_w, mag, mag_w = norm_backward_reference(dY, V, w, None, 0.0)
+    for into in ("other", "dY", "V"):
+        given = dict(dY=dY.cuda(), V=V.cuda())
+        dX, dw = given.get(into, torch.empty(len(V), K, dtype=dtype, device="cuda")), torch.empty(K, dtype=dtype, device="cuda")
+        b.rmsnorm_backward_into(given["dY"], given["V"], w.cuda(), dX, dw=dw, eps=0.0)
+        rounded(dX, ref, (2 * (K / 512 + 72) + 16) * 2.0 ** -24 * mag, "dX")
+        rounded(dw, ref_w, (0.5 * (K / 512 + 72) + 20 + len(V)) * 2.0 ** -24 * mag_w, "dw")
