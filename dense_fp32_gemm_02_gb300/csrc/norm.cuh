@@ -539,7 +539,8 @@ __global__ void __launch_bounds__(norm_block(THREADS), norm_blocks_per_sm<THREAD
         group_reduce<THREADS, true, false, false>(sm, turn, squares, gv, none);
         turn ^= 1;
         float rstd = 1.0f / sqrtf(squares / float(a.K) + a.eps), mean = gv * rstd / float(a.K), shift = 1.0f;
-        if (!(squares <= MOST_SQUARES) || (squares < LEAST_SQUARES && a.eps < 1e-10f)) {
+        // (the products' sum may leave the range where the squares do not; a NaN comes through in either way)
+        if (!(squares <= MOST_SQUARES) || (squares < LEAST_SQUARES && a.eps < 1e-10f) || !(fabsf(mean) <= 0x1.fffffep127f)) {
             double sum = 0;
             for (int j = t; j < a.K; j += THREADS) sum += double(to_f32(dyr[j])) * to_f32(a.w[j]) * to_f32(vr[j]);
             const RareRstd of = rare_row_rstd<T, THREADS>(sm, vr, a.K, a.eps, t);

@@ -118,3 +118,22 @@ def test_gradients_at_the_ends_of_the_range(K, dtype):
         b.rmsnorm_backward_into(given["dY"], given["V"], w.cuda(), dX, dw=dw, eps=0.0)
         rounded(dX, ref, (2 * (K / 512 + 72) + 16) * 2.0 ** -24 * mag, "dX")
         rounded(dw, ref_w, (0.5 * (K / 512 + 72) + 20 + len(V)) * 2.0 ** -24 * mag_w, "dw")
+
+
+@pytest.mark.parametrize("K", [40, 257, 1000, 5000, 20000])
+def test_sums_of_the_gradient_past_float32(K):
+    """Rows and gradients whose products, or their sum, leave fp32's range where the gradient itself does not."""
+    b = binding()
+    V, dY, w = normal(4, K, 8), normal(4, K, 9), 1.0 + 0.3 * normal(1, K, 10)[0]
+    dY += 0.3 * V                      # (mean(g n) is of g's order)
+    V[0] *= 1e14
+    dY[0] *= 1e27
+    V[1] *= 1e-5
+    dY[1] *= 1e33
+    V[2] *= 1e10
+    dY[2] *= 1e36
+    dX, dw = torch.empty(4, K, device="cuda"), torch.empty(K, device="cuda")
+    b.rmsnorm_backward_into(dY.cuda(), V.cuda(), w.cuda(), dX, dw=dw)
+    ref, ref_w, mag, mag_w = norm_backward_reference(dY, V, w, None, 1e-6)
+    rounded(dX, ref, (2 * (K / 512 + 72) + 16) * 2.0 ** -24 * mag, "dX")
+    rounded(dw, ref_w, (0.5 * (K / 512 + 72) + 24) * 2.0 ** -24 * mag_w, "dw")
