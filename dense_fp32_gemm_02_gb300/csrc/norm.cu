@@ -133,6 +133,17 @@ NormBackCall<T> back_call_of(int M, int K, const void *dY, int lddy, const void 
     return c;
 }
 
+// Rows of no columns: their scales alone are to be written, zeros.
+int no_columns(int M, float *scale, cudaStream_t stream) {
+    if (!scale) return SGEMM_OK;
+    if (!sgh::aligned(scale, 4)) return SGEMM_ERR_INVALID_ARG;
+    int sms, st;
+    cudaMemPool_t pool;
+    if ((st = sgh::current_device(&sms, &pool)) != SGEMM_OK) return st;
+    const cudaError_t e = cudaMemsetAsync(scale, 0, size_t(M) * sizeof(float), stream);
+    return e == cudaSuccess ? SGEMM_OK : sgh::cuda_fail(e);
+}
+
 }  // namespace
 
 cudaError_t sgh::norm_error_word(unsigned *v, bool clear) { return sgv::unit_error_word(v, clear); }
@@ -151,7 +162,8 @@ SGEMM_API int sgemm_rmsnorm(int type, int M, int K, const void *X, int ldx, cons
     const int st = sgh::check_sizes(type, {M, K});
     if (st != SGEMM_OK) return st;
     if (!(eps >= 0.0f && eps <= 3.0e38f)) return SGEMM_ERR_INVALID_ARG;
-    if (M == 0 || K == 0) return SGEMM_OK;
+    if (M == 0) return SGEMM_OK;
+    if (K == 0) return no_columns(M, scale, reinterpret_cast<cudaStream_t>(stream));
     if ((!S && !Y && !q) || !q != !scale) return SGEMM_ERR_INVALID_ARG;
     const size_t size = sgh::element_bytes(type);
     if (sgh::bad_matrix(X, ldx, K, size) || sgh::bad_vector(w, size) || sgh::bad_optional(R, ldr, K, size) ||

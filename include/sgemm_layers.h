@@ -163,8 +163,9 @@ int sgemm_act8_weight_grad(int type, int M, int N, int K,
  *
  * A matrix (M x K) in rows of 8 bits: q, M x K int8, and scale, M floats; row i stands for
  * scale[i] * q[i].  With t the largest magnitude of a row, scale = t / 127 and q = x / scale rounded to
- * the nearest integer, ties to even, of the exact quotient.  A row of zeros has scale 0; a row with an
- * infinity or a NaN is kept as q = 0, scale NaN and stands for NaN throughout.
+ * the nearest integer, ties to even, of the exact quotient.  A row of zeros has scale 0, one of no
+ * columns too; a row with an infinity or a NaN is kept as q = 0, scale NaN and stands for NaN
+ * throughout.
  */
 
 /*

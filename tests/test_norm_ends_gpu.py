@@ -137,3 +137,14 @@ def test_sums_of_the_gradient_past_float32(K):
     ref, ref_w, mag, mag_w = norm_backward_reference(dY, V, w, None, 1e-6)
     rounded(dX, ref, (2 * (K / 512 + 72) + 16) * 2.0 ** -24 * mag, "dX")
     rounded(dw, ref_w, (0.5 * (K / 512 + 72) + 24) * 2.0 ** -24 * mag_w, "dw")
+
+
+# ------------------------------------------------------------------ no columns
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_rows_of_no_columns_have_scales_of_zero(dtype):
+    """A row of zeros has scale 0, one of no columns too; nothing beside the scales is written."""
+    b = binding()
+    X, w = torch.empty(5, 0, dtype=dtype, device="cuda"), torch.empty(0, dtype=dtype, device="cuda")
+    scale = torch.full((7,), 55.0, device="cuda")
+    b.rmsnorm_into(X, w, q=torch.empty(5, 0, dtype=torch.int8, device="cuda"), scale=scale[1:6])
+    assert scale.tolist() == [55.0, 0.0, 0.0, 0.0, 0.0, 0.0, 55.0]
