@@ -59,7 +59,10 @@ constexpr int kMaxDim = 0x7fffffff - 0xffff;
 //  3. A kernel whose blocks do not all wait has its first block wait at the end: its own end then
 //     says that the kernels before it have ended, which is what the next one's wait relies on.
 // Kernels that make use of 1: parts_kernel beside the grouping, few_rows_rank_kernel beside the
-// product, and few_rows_finish_kernel, which reads ids, B and bias before its wait.
+// product, and few_rows_finish_kernel, which reads ids, B and bias before its wait;
+// byte_expand_kernel's form for X beside the one for W, byte_finish_kernel, which reads the scales and
+// the bias before its wait, gated_parts_kernel beside gated_slopes_kernel, and split_tiles_kernel,
+// whose W is on its way while X's parts are laid out.
 template <class... P, class... Args>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
                          const Args &...args) {
