@@ -25,10 +25,10 @@ template <class T, int KIND, int THREADS, int CHUNKS, bool WIDE, bool LONG = fal
 Form<NormCall<T>> form() {
     return {&norm_kernel<T, KIND, THREADS, CHUNKS, WIDE, LONG>, norm_block(THREADS), norm_block(THREADS) / THREADS};
 }
-// us, a warp to a row / four warps: y from 8192 x 1024 bfloat16 8.0 / 9.8, in 8 bits with residual 17.4 /
-// 18.5; float32 12.5 / 12.5 and 24.1 / 20.9; 4097 x 1023 (one element at a time) 8.7 / 8.0 and 23.1 / 13.3.
-// 8192 x 2048 bfloat16 in 8 bits, 256 threads of two pieces / one 45.5 / 39.7; of 4096 columns two pieces 52.8,
-// 512 threads of one 88.8.
+// us, a warp to a row / four warps: y from 8192 x 1024 bfloat16 7.4 / 9.1, in 8 bits with residual 14.7 /
+// 17.6; float32 12.1 / 11.4 and 22.0 / 20.1; 4097 x 1023 (one element at a time) 8.7 / 7.8 and 21.5 / 12.9.
+// 8192 x 2048 bfloat16 in 8 bits with residual, 256 threads of two pieces / one 44.5 / 34.9; of 4096 columns two pieces
+// 51.5, 512 threads of one 78.8.
 template <class T, int KIND, bool WIDE>
 Form<NormCall<T>> forward_form(int M, int K, int sms) {
     if (K <= 256) return form<T, KIND, 32, 1, WIDE>();
